@@ -11,6 +11,12 @@ in this package's CUDA kernels.  The functions keep the C entry points' names:
 * :func:`gdn_fused_decode`     -- conv update + gates from raw logits + recurrent step,
   one call
 
+* :func:`gdn_linear_prefill`, :func:`gdn_linear_decode` -- linear attention with a plain
+  decay for each head, over packed prompts and one token at a time
+* :func:`gdn_kv_append`, :func:`gdn_kv_read`, :func:`gdn_kv_attention` -- a paged
+  key/value cache held in 4 bits: rotate and store, read back, attend
+  (:func:`gdn_kv_cache` allocates one)
+
 plus :func:`gdn_layer_prefill` / :func:`gdn_layer_decode`, which chain the conv and the
 scan over the packed q||k||v channels (q, k, v are strided views of the conv output;
 nothing is copied).
@@ -36,14 +42,18 @@ import os
 import torch
 
 from . import _lib
-from ._lib import (GDN_CHECK_INPUTS, GDN_LAYER_FUSED_VCONV, GDN_PREFILL_SIMT,  # noqa: F401
-                   GDN_PREFILL_TILES2, GDN_PREFILL_TILES3, GDN_QK_L2NORM, GdnError)
+from ._lib import (GDN_CHECK_INPUTS, GDN_KV_INTERLEAVED, GDN_LAYER_FUSED_VCONV,  # noqa: F401
+                   GDN_PREFILL_SIMT, GDN_PREFILL_TILES2, GDN_PREFILL_TILES3, GDN_QK_L2NORM,
+                   GdnError)
 
 __all__ = ["gdn_conv1d_fwd", "gdn_conv1d_update", "gdn_chunk_prefill",
            "gdn_chunk_prefill_noalloc", "gdn_chunk_prefill_cp",
            "gdn_chunk_prefill_cp_workspace_size", "gdn_chunk_prefill_cp_range_hint",
            "gdn_recurrent_decode", "gdn_fused_decode", "gdn_chunk_prefill_workspace_size",
-           "gdn_layer_prefill", "gdn_layer_decode", "GdnError", "load"]
+           "gdn_layer_prefill", "gdn_layer_decode", "gdn_linear_prefill",
+           "gdn_linear_prefill_workspace_size", "gdn_linear_decode", "gdn_kv_cache",
+           "gdn_kv_append", "gdn_kv_read", "gdn_kv_attention",
+           "gdn_kv_attention_workspace_size", "GdnError", "load"]
 
 _DT = {torch.bfloat16: _lib.GDN_BF16, torch.float32: _lib.GDN_F32}
 
@@ -402,6 +412,248 @@ def gdn_layer_decode(x_qkv, conv_w, conv_bias, g, beta, conv_state, state, Hk, H
     q, k, v = split_qkv(y, Hk, Hv, dk, dv)
     return gdn_recurrent_decode(q, k, v, g, beta, state, state_idx, scale, l2norm, o,
                                 status)
+
+
+def _gates(g, T, Hv):
+    """(contiguous fp32 log decays, per-token flag) of g [Hv] or [T, Hv]."""
+    if g.dtype != torch.float32:
+        raise TypeError("g must be fp32, got %s" % g.dtype)
+    if g.dim() == 1 and g.shape[0] == Hv:
+        return g.contiguous(), 0
+    if g.dim() >= 2 and tuple(g.shape[-2:]) == (T, Hv) and g.numel() == T * Hv:
+        return g.contiguous(), 1
+    raise ValueError("g must be [Hv] or [T, Hv] = [%d, %d], got %s" % (T, Hv, tuple(g.shape)))
+
+
+def _states(name, t, shape):
+    if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or
+                          tuple(t.shape) != tuple(shape)):
+        raise ValueError("%s must be a contiguous fp32 tensor of shape %s" % (name, tuple(shape)))
+
+
+def gdn_linear_prefill_workspace_size(cu_seqlens_host, T, Hk, Hv, D, dtype=torch.bfloat16,
+                                      simt=False):
+    """Workspace bytes of gdn_linear_prefill."""
+    lib = _lib.load()
+    cu_h = cu_seqlens_host.to(torch.int32).contiguous()
+    return int(lib.gdn_linear_prefill_workspace_size(
+        ctypes.c_void_p(cu_h.data_ptr()), cu_h.numel() - 1, T, Hk, Hv, D, _DT[dtype],
+        GDN_PREFILL_SIMT if simt else 0))
+
+
+def gdn_linear_prefill(q, k, v, g, cu_seqlens, scale=1.0, initial_state=None,
+                       output_final_state=True, o=None, final_state=None, simt=False,
+                       cu_seqlens_host=None, workspace=None, status=None):
+    """Linear attention with a decay for each head over packed sequences,
+    S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.  Returns (o, final_state).
+
+    q, k [T, Hk, D]; v [T, Hv, D], all bf16 or all fp32 (token-major views); g fp32 log
+    decays, [Hv] or [T, Hv]; cu_seqlens [N+1]; initial_state [N, Hv, D, D] fp32 or None.
+    """
+    _forced("gdn_linear_prefill")
+    lib = _lib.load()
+    _need_cuda(q, k, v, g, initial_state, o, final_state, workspace, status)
+    cu, cu_h = _seqlens(cu_seqlens, cu_seqlens_host)
+    N = cu_h.numel() - 1
+    T, Hk, D = q.shape[-3:]
+    Hv = v.shape[-2]
+    g, per_token = _gates(g, T, Hv)
+    _states("initial_state", initial_state, (N, Hv, D, D))
+    _states("final_state", final_state, (N, Hv, D, D))
+    if o is None:
+        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    if final_state is None and output_final_state:
+        final_state = torch.empty((N, Hv, D, D), dtype=torch.float32, device=q.device)
+    flags = (GDN_PREFILL_SIMT if simt else 0) | _debug_flags()
+    dq, dk_, dv_, do = _desc(q), _desc(k), _desc(v), _desc(o)
+    ws_bytes = int(lib.gdn_linear_prefill_workspace_size(
+        ctypes.c_void_p(cu_h.data_ptr()), N, T, Hk, Hv, D, dv_.dtype, flags))
+    if ws_bytes and (workspace is None or workspace.numel() * workspace.element_size() < ws_bytes):
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    rc = lib.gdn_linear_prefill(
+        ctypes.byref(dq), ctypes.byref(dk_), ctypes.byref(dv_), _vp(g), per_token, _vp(cu),
+        ctypes.c_void_p(cu_h.data_ptr()), N, float(scale), flags, _vp(initial_state),
+        ctypes.byref(do), _vp(final_state), _vp(workspace), ws_bytes, _vp(status), _stream())
+    _lib.check(rc, "gdn_linear_prefill")
+    return o, final_state
+
+
+def gdn_linear_decode(q, k, v, g, state, state_idx=None, scale=1.0, o=None, status=None):
+    """One token per sequence of gdn_linear_prefill's recurrence; state [P, Hv, D, D] fp32
+    updated in place.  g [Hv] or [N, Hv].  Returns o."""
+    _forced("gdn_linear_decode")
+    lib = _lib.load()
+    _need_cuda(q, k, v, g, state, state_idx, o, status)
+    N, _, D = q.shape[-3:]
+    Hv = v.shape[-2]
+    g, per_token = _gates(g, N, Hv)
+    _states("state", state, (state.shape[0], Hv, D, D))
+    state_idx = _int32("state_idx", state_idx, (N,))
+    if o is None:
+        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    dq, dk_, dv_, do = _desc(q), _desc(k), _desc(v), _desc(o)
+    rc = lib.gdn_linear_decode(
+        ctypes.byref(dq), ctypes.byref(dk_), ctypes.byref(dv_), _vp(g), per_token, _vp(state),
+        state.shape[0], _vp(state_idx), float(scale), _debug_flags(), ctypes.byref(do),
+        _vp(status), _stream())
+    _lib.check(rc, "gdn_linear_decode")
+    return o
+
+
+def gdn_kv_cache(pages, page_size, Hkv, head_dim, device="cuda"):
+    """A zeroed paged 4-bit cache: uint8 [pages, 2, Hkv, page_size, record bytes] (the
+    layout is described in include/gdn.h)."""
+    rec = int(_lib.load().gdn_kv_record_bytes(head_dim))
+    if rec == 0:
+        raise GdnError(6, "gdn_kv_cache (head_dim %d)" % head_dim)
+    return torch.zeros((pages, 2, Hkv, page_size, rec), dtype=torch.uint8, device=device)
+
+
+def _int32(name, t, shape):
+    if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or
+                          tuple(t.shape) != tuple(shape)):
+        raise ValueError("%s must be a contiguous int32 tensor of shape %s" % (name, tuple(shape)))
+    return t
+
+
+def _kv_cache(cache, block_table, kv_lens, head_dim):
+    """The C descriptor of a cache tensor with its table and lengths."""
+    if cache.dtype != torch.uint8 or cache.dim() != 5 or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous uint8 tensor of five dimensions")
+    if cache.shape[1] != 2 or cache.shape[4] != _lib.load().gdn_kv_record_bytes(head_dim):
+        raise ValueError("cache of shape %s does not hold keys and values of head_dim %d"
+                         % (tuple(cache.shape), head_dim))
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [N, pages of a sequence]")
+    N = block_table.shape[0]
+    _int32("block_table", block_table, (N, block_table.shape[1]))
+    _int32("kv_lens", kv_lens, (N,))
+    c = _lib.GdnKvCache()
+    c.data, c.block_table, c.kv_lens = cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr()
+    c.pages, c.Hkv, c.page_size = cache.shape[0], cache.shape[2], cache.shape[3]
+    c.head_dim, c.table_width, c.N = head_dim, block_table.shape[1], N
+    return c
+
+
+def _kv_offsets(cu_seqlens, cu_seqlens_host, T, N):
+    """Device and host offsets of the new tokens as pointers (None: one per sequence)."""
+    if cu_seqlens is None:
+        if T != N:
+            raise ValueError("%d new tokens for %d sequences need cu_seqlens" % (T, N))
+        return None, None, None, None
+    cu, cu_h = _seqlens(cu_seqlens, cu_seqlens_host)
+    if cu_h.numel() != N + 1 or cu.numel() != N + 1:
+        raise ValueError("cu_seqlens must have %d entries" % (N + 1))
+    return cu, cu_h, _vp(cu), ctypes.c_void_p(cu_h.data_ptr())
+
+
+def gdn_kv_append(k, v, cache, block_table, kv_lens, cu_seqlens=None, cos=None, sin=None,
+                  q=None, q_out=None, interleaved=False, cu_seqlens_host=None, status=None):
+    """Store new tokens' keys (rotated) and values in a paged 4-bit cache; with ``q``,
+    return q rotated.
+
+    k, v [T, Hkv, D] and q [T, Hq, D], bf16 or fp32 views; cache as gdn_kv_cache gives it;
+    block_table int32 [N, W]; kv_lens int32 [N], the new tokens included; cu_seqlens [N+1]
+    offsets of the new tokens, or None for one per sequence; cos, sin fp32
+    [positions, rot / 2] or None for no rotation (rot = twice their width).
+    """
+    _forced("gdn_kv_append")
+    lib = _lib.load()
+    _need_cuda(k, v, cache, block_table, kv_lens, cos, sin, q, q_out, status)
+    T, Hkv, D = k.shape[-3:]
+    c = _kv_cache(cache, block_table, kv_lens, D)
+    cu, cu_h, cu_p, cu_hp = _kv_offsets(cu_seqlens, cu_seqlens_host, T, c.N)
+    rows = rot = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    if cos is not None:
+        for t in (cos, sin):
+            if t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous() or \
+                    t.shape != cos.shape:
+                raise ValueError("cos and sin must be contiguous fp32 [positions, rot / 2]")
+        rows, rot = cos.shape[0], 2 * cos.shape[1]
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    dk_, dv_ = _desc(k), _desc(v)
+    dq, do = (None, None) if q is None else (_desc(q), _desc(q_out))
+    rc = lib.gdn_kv_append(
+        ctypes.byref(c), cu_p, cu_hp, ctypes.byref(dk_), ctypes.byref(dv_),
+        None if dq is None else ctypes.byref(dq), None if do is None else ctypes.byref(do),
+        _vp(cos), _vp(sin), rows, rot,
+        (GDN_KV_INTERLEAVED if interleaved else 0) | _debug_flags(), _vp(status), _stream())
+    _lib.check(rc, "gdn_kv_append")
+    return q_out
+
+
+def gdn_kv_read(cache, block_table, kv_lens, cu_seqlens=None, head_dim=128,
+                dtype=torch.bfloat16, k=None, v=None, cu_seqlens_host=None, status=None):
+    """The last tokens' keys and values (as many per sequence as cu_seqlens says; None:
+    one) of a paged 4-bit cache, as values.  Returns (k, v), each [T, Hkv, head_dim]."""
+    _forced("gdn_kv_read")
+    lib = _lib.load()
+    _need_cuda(cache, block_table, kv_lens, k, v, status)
+    c = _kv_cache(cache, block_table, kv_lens, head_dim)
+    if cu_seqlens is None:
+        T, cu, cu_h, cu_p, cu_hp = c.N, None, None, None, None
+    else:
+        cu, cu_h, cu_p, cu_hp = _kv_offsets(cu_seqlens, cu_seqlens_host, None, c.N)
+        T = int(cu_h[-1])
+    if k is None:
+        k = torch.empty((T, c.Hkv, head_dim), dtype=dtype, device=cache.device)
+    if v is None:
+        v = torch.empty((T, c.Hkv, head_dim), dtype=k.dtype, device=cache.device)
+    dk_, dv_ = _desc(k), _desc(v)
+    rc = lib.gdn_kv_read(ctypes.byref(c), cu_p, cu_hp, ctypes.byref(dk_), ctypes.byref(dv_),
+                         _debug_flags(), _vp(status), _stream())
+    _lib.check(rc, "gdn_kv_read")
+    return k, v
+
+
+def gdn_kv_attention_workspace_size(head_dim, Hq, Hkv, T, N, max_q_len, max_kv_len,
+                                    dtype=torch.bfloat16, simt=False):
+    """Workspace bytes of gdn_kv_attention for T new tokens of N sequences."""
+    return int(_lib.load().gdn_kv_attention_workspace_size(
+        head_dim, Hq, Hkv, T, N, max_q_len, max_kv_len, _DT[dtype],
+        GDN_PREFILL_SIMT if simt else 0))
+
+
+def gdn_kv_attention(q, cache, block_table, kv_lens, cu_seqlens=None, max_kv_len=None,
+                     scale=None, o=None, lse=None, simt=False, cu_seqlens_host=None,
+                     workspace=None, status=None):
+    """Softmax attention of the new tokens over a paged 4-bit cache that already holds
+    them: the row at position p sees keys 0 .. p.  Returns o [T, Hq, D].
+
+    q [T, Hq, D] bf16 or fp32, Hq a multiple of the cache's Hkv; cu_seqlens [N+1], or None
+    for one new token per sequence; max_kv_len: an upper bound of kv_lens (default: what
+    block_table can hold; a tighter one means a smaller grid and workspace); scale
+    defaults to D^-1/2; lse: an fp32 [T, Hq] tensor that receives the log-sum-exp.
+    """
+    _forced("gdn_kv_attention")
+    lib = _lib.load()
+    _need_cuda(q, cache, block_table, kv_lens, o, lse, workspace, status)
+    T, Hq, D = q.shape[-3:]
+    c = _kv_cache(cache, block_table, kv_lens, D)
+    cu, cu_h, cu_p, cu_hp = _kv_offsets(cu_seqlens, cu_seqlens_host, T, c.N)
+    if max_kv_len is None:
+        max_kv_len = min(c.table_width * c.page_size, 0x7fffffff)
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or
+                            tuple(lse.shape) != (T, Hq)):
+        raise ValueError("lse must be a contiguous fp32 tensor of shape [T, Hq]")
+    if o is None:
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    flags = (GDN_PREFILL_SIMT if simt else 0) | _debug_flags()
+    dq, do = _desc(q), _desc(o)
+    max_q = 1 if cu_h is None else int((cu_h[1:] - cu_h[:-1]).max()) if c.N else 0
+    ws_bytes = int(lib.gdn_kv_attention_workspace_size(D, Hq, c.Hkv, T, c.N, max_q, max_kv_len,
+                                                       dq.dtype, flags))
+    if ws_bytes and (workspace is None or workspace.numel() * workspace.element_size() < ws_bytes):
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    rc = lib.gdn_kv_attention(
+        ctypes.byref(c), cu_p, cu_hp, int(max_kv_len), ctypes.byref(dq),
+        float(D ** -0.5 if scale is None else scale), flags, ctypes.byref(do), _vp(lse),
+        _vp(workspace), ws_bytes, _vp(status), _stream())
+    _lib.check(rc, "gdn_kv_attention")
+    return o
 
 
 def gdn_selftest_bounded_wait(status=None):

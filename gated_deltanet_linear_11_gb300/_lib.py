@@ -16,6 +16,7 @@ GDN_PREFILL_TILES2 = 0x200
 GDN_PREFILL_TILES3 = 0x400
 GDN_LAYER_FUSED_VCONV = 0x800
 GDN_CHECK_INPUTS = 0x1000
+GDN_KV_INTERLEAVED = 0x2000
 
 STATUS = {
     0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_LAYOUT",
@@ -29,7 +30,10 @@ EXPORTS = ("gdn_status_string", "gdn_version", "gdn_conv1d_fwd", "gdn_conv1d_upd
            "gdn_chunk_prefill_noalloc", "gdn_chunk_prefill_cp_workspace_size",
            "gdn_chunk_prefill_cp", "gdn_chunk_prefill_cp_range_hint",
            "gdn_chunk_prefill_cp_range_hint_for", "gdn_recurrent_decode", "gdn_fused_decode",
-           "gdn_layer_prefill", "gdn_selftest_bounded_wait")
+           "gdn_layer_prefill", "gdn_linear_prefill_workspace_size", "gdn_linear_prefill",
+           "gdn_linear_decode", "gdn_kv_record_bytes", "gdn_kv_append", "gdn_kv_read",
+           "gdn_kv_attention_workspace_size", "gdn_kv_attention",
+           "gdn_selftest_bounded_wait")
 
 NOALLOC_SCRATCH_BYTES = 128 << 20
 
@@ -38,6 +42,14 @@ class GdnTensor(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("ndim", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("shape", ctypes.c_int64 * 4),
                 ("stride", ctypes.c_int64 * 4)]
+
+
+class GdnKvCache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("kv_lens", ctypes.c_void_p), ("pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("table_width", ctypes.c_int32),
+                ("N", ctypes.c_int32)]
 
 
 class GdnError(RuntimeError):
@@ -61,6 +73,8 @@ def load(path: str = LIB_PATH):
     vp, i32, i64, u32, f32 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                               ctypes.c_uint32, ctypes.c_float)
     tp = ctypes.POINTER(GdnTensor)
+    cp = ctypes.POINTER(GdnKvCache)
+    size = ctypes.c_size_t
     sig = {
         "gdn_status_string": ([i32], ctypes.c_char_p),
         "gdn_version": ([], i32),
@@ -85,6 +99,16 @@ def load(path: str = LIB_PATH):
         "gdn_layer_prefill": ([vp, i64, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp, vp, vp,
                                vp, vp, f32, u32, vp, vp, vp, vp, ctypes.c_size_t, vp, vp,
                                vp], i32),
+        "gdn_linear_prefill_workspace_size": ([vp, i32, i64, i32, i32, i32, i32, u32], size),
+        "gdn_linear_prefill": ([tp, tp, tp, vp, i32, vp, vp, i32, f32, u32, vp, tp, vp, vp,
+                                size, vp, vp], i32),
+        "gdn_linear_decode": ([tp, tp, tp, vp, i32, vp, i32, vp, f32, u32, tp, vp, vp], i32),
+        "gdn_kv_record_bytes": ([i32], size),
+        "gdn_kv_append": ([cp, vp, vp, tp, tp, tp, tp, vp, vp, i32, i32, u32, vp, vp], i32),
+        "gdn_kv_read": ([cp, vp, vp, tp, tp, u32, vp, vp], i32),
+        "gdn_kv_attention_workspace_size": ([i32, i32, i32, i64, i32, i32, i32, i32, u32],
+                                            size),
+        "gdn_kv_attention": ([cp, vp, vp, i32, tp, f32, u32, tp, vp, vp, size, vp, vp], i32),
         "gdn_selftest_bounded_wait": ([vp, vp], i32),
     }
     for name, (args, res) in sig.items():

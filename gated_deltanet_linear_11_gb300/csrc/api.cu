@@ -8,6 +8,8 @@
 #include <vector>
 
 #include "common.cuh"
+#include "kv_format.cuh"
+#include "linear.cuh"
 
 namespace {
 
@@ -498,6 +500,276 @@ gdn_status_t gdn_layer_prefill(const void *x, int64_t T, int32_t Hk, int32_t Hv,
     cudaEventDestroy(fork);
     cudaEventDestroy(v_ready);
     return s;
+}
+
+}  // extern "C"
+
+// ----------------------------------------------- linear attention, paged 4-bit cache
+
+namespace {
+
+// One log decay per head (g_rows = 0) or per token and head.
+gdn_status_t linear_args(const gdn_tensor_t *q, const gdn_tensor_t *k, const gdn_tensor_t *v,
+                         const float *g, int32_t per_token, const gdn_tensor_t *o,
+                         gdn_host::LinearArgs &a) {
+    View Q, K, V, O;
+    gdn_status_t s;
+    if ((s = view_of(q, Q)) != GDN_OK) return s;
+    if ((s = view_of(k, K)) != GDN_OK) return s;
+    if ((s = view_of(v, V)) != GDN_OK) return s;
+    if ((s = view_of(o, O)) != GDN_OK) return s;
+    if (Q.T > 0 && !g) return GDN_ERR_NULL;
+    if (K.T != Q.T || V.T != Q.T || O.T != Q.T || K.H != Q.H || K.D != Q.D || O.H != V.H ||
+        O.D != V.D || Q.T > 0x7fffffff || V.H > 65535)
+        return GDN_ERR_SHAPE;
+    if (V.H % Q.H != 0) return GDN_ERR_SHAPE;
+    if (Q.dtype != K.dtype || Q.dtype != V.dtype || O.dtype != V.dtype) return GDN_ERR_DTYPE;
+    if (Q.D != V.D || !gdn_host::linear_supported(Q.D)) return GDN_ERR_UNSUPPORTED;
+    memset(&a, 0, sizeof(a));
+    a.q = Q.ptr; a.k = K.ptr; a.v = V.ptr; a.o = O.ptr;
+    a.q_tok = Q.tok; a.k_tok = K.tok; a.v_tok = V.tok; a.o_tok = O.tok;
+    a.g = g;
+    a.g_tok = per_token ? V.H : 0;
+    a.T = Q.T;
+    a.Hk = (int32_t)Q.H; a.Hv = (int32_t)V.H; a.D = (int32_t)Q.D;
+    a.in_f32 = Q.dtype == GDN_F32;
+    return GDN_OK;
+}
+
+gdn_status_t check_gates(const gdn_host::LinearArgs &a, cudaStream_t st) {
+    const size_t n = a.g_tok ? (size_t)a.T * a.Hv : (size_t)a.Hv;
+    return check_finite(a.g, a.g, n, st);
+}
+
+// The cache's own fields, and the new tokens' offsets (cu_host may be NULL: one each).
+gdn_status_t kv_args(const gdn_kv_cache_t *c, const int32_t *cu_dev, const int32_t *cu_host,
+                     int64_t T, gdn_host::KvArgs &a) {
+    if (!c) return GDN_ERR_NULL;
+    if (c->N < 0 || c->pages < 0 || c->Hkv <= 0 || c->Hkv > 65535 || c->table_width < 0)
+        return GDN_ERR_SHAPE;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return GDN_ERR_UNSUPPORTED;
+    if (c->page_size < 16 || c->page_size > 65536 || (c->page_size & (c->page_size - 1)))
+        return GDN_ERR_UNSUPPORTED;
+    if (T > 0x7fffffff) return GDN_ERR_SHAPE;
+    if (!cu_host != !cu_dev) return GDN_ERR_NULL;
+    memset(&a, 0, sizeof(a));
+    a.max_q_len = T > 0 ? 1 : 0;
+    if (cu_host) {
+        const gdn_status_t s = check_seqlens(cu_host, c->N, T, &a.max_q_len);
+        if (s != GDN_OK) return s;
+    } else if (T != c->N) {
+        return GDN_ERR_SEQLENS;
+    }
+    if (T > 0) {
+        if (!c->data || !c->block_table || !c->kv_lens) return GDN_ERR_NULL;
+        if (!aligned16(c->data)) return GDN_ERR_LAYOUT;
+    }
+    a.kv.data = (uint8_t *)c->data;
+    a.kv.table = c->block_table;
+    a.kv.kv_lens = c->kv_lens;
+    a.kv.cu = cu_dev;
+    a.kv.pages = c->pages;
+    a.kv.page_log2 = 0;
+    while ((1 << a.kv.page_log2) < c->page_size) ++a.kv.page_log2;
+    a.kv.Hkv = c->Hkv;
+    a.kv.table_width = c->table_width;
+    a.kv.N = c->N;
+    a.T = T;
+    a.D = c->head_dim;
+    return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_linear_prefill_workspace_size(const int32_t *cu_seqlens_host, int32_t N, int64_t T,
+                                         int32_t Hk, int32_t Hv, int32_t D, int32_t dtype,
+                                         uint32_t flags) {
+    (void)cu_seqlens_host; (void)N; (void)T; (void)Hk; (void)Hv; (void)D; (void)dtype; (void)flags;
+    return 0;
+}
+
+gdn_status_t gdn_linear_prefill(const gdn_tensor_t *q, const gdn_tensor_t *k,
+                                const gdn_tensor_t *v, const float *g, int32_t g_per_token,
+                                const int32_t *cu_seqlens_dev, const int32_t *cu_seqlens_host,
+                                int32_t N, float scale, uint32_t flags,
+                                const float *initial_state, const gdn_tensor_t *o,
+                                float *final_state, void *workspace, size_t workspace_bytes,
+                                int32_t *status_dev, void *stream) {
+    gdn_host::CallRange nvtx_range("gdn_linear_prefill");
+    gdn_host::LinearArgs a;
+    gdn_status_t s = linear_args(q, k, v, g, g_per_token, o, a);
+    if (s != GDN_OK) return s;
+    if (!cu_seqlens_dev || !cu_seqlens_host) return GDN_ERR_NULL;
+    if (N < 0 || N > 65535) return GDN_ERR_SHAPE;
+    if (!aligned16(initial_state) || !aligned16(final_state)) return GDN_ERR_LAYOUT;
+    if ((s = check_seqlens(cu_seqlens_host, N, a.T, &a.max_len)) != GDN_OK) return s;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (N == 0) return GDN_OK;
+    if ((flags & GDN_CHECK_INPUTS) &&
+        ((a.T > 0 && (s = check_gates(a, st)) != GDN_OK) ||
+         (s = check_seqlens_copy(cu_seqlens_dev, cu_seqlens_host, N, st)) != GDN_OK))
+        return s;
+    a.cu = cu_seqlens_dev;
+    a.cu_host = cu_seqlens_host;
+    a.h0 = initial_state;
+    a.hT = final_state;
+    a.N = N;
+    a.scale = scale;
+    a.flags = flags;
+    a.status = status_dev;
+    a.ws = workspace;
+    a.ws_bytes = workspace_bytes;
+    return gdn_host::launch_linear_scan(a, st);
+}
+
+gdn_status_t gdn_linear_decode(const gdn_tensor_t *q, const gdn_tensor_t *k,
+                               const gdn_tensor_t *v, const float *g, int32_t g_per_token,
+                               float *state, int32_t P, const int32_t *state_idx, float scale,
+                               uint32_t flags, const gdn_tensor_t *o, int32_t *status_dev,
+                               void *stream) {
+    gdn_host::CallRange nvtx_range("gdn_linear_decode");
+    gdn_host::LinearArgs a;
+    gdn_status_t s = linear_args(q, k, v, g, g_per_token, o, a);
+    if (s != GDN_OK) return s;
+    if (P < 0 || a.T > 65535) return GDN_ERR_SHAPE;
+    if (a.T == 0) return GDN_OK;
+    if (!state) return GDN_ERR_NULL;
+    if (!state_idx && P < a.T) return GDN_ERR_SHAPE;
+    if (!aligned16(state)) return GDN_ERR_LAYOUT;
+    if ((flags & GDN_CHECK_INPUTS) && (s = check_gates(a, (cudaStream_t)stream)) != GDN_OK)
+        return s;
+    a.state = state;
+    a.P = P;
+    a.idx = state_idx;
+    a.N = (int32_t)a.T;
+    a.scale = scale;
+    a.flags = flags;
+    a.status = status_dev;
+    return gdn_host::launch_linear_decode(a, (cudaStream_t)stream);
+}
+
+size_t gdn_kv_record_bytes(int32_t head_dim) {
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+    return (size_t)(head_dim / 2 + head_dim / 8);
+}
+
+gdn_status_t gdn_kv_append(const gdn_kv_cache_t *cache, const int32_t *cu_seqlens_dev,
+                           const int32_t *cu_seqlens_host, const gdn_tensor_t *k,
+                           const gdn_tensor_t *v, const gdn_tensor_t *q,
+                           const gdn_tensor_t *q_out, const float *cos_table,
+                           const float *sin_table, int32_t table_rows, int32_t rot,
+                           uint32_t flags, int32_t *status_dev, void *stream) {
+    gdn_host::CallRange nvtx_range("gdn_kv_append");
+    View K, V, Q, O;
+    gdn_status_t s;
+    if ((s = view_of(k, K)) != GDN_OK) return s;
+    if ((s = view_of(v, V)) != GDN_OK) return s;
+    if (!q != !q_out) return GDN_ERR_NULL;
+    gdn_host::KvArgs a;
+    if ((s = kv_args(cache, cu_seqlens_dev, cu_seqlens_host, K.T, a)) != GDN_OK) return s;
+    if (V.T != K.T || V.H != K.H || V.D != K.D || K.H != a.kv.Hkv || K.D != a.D)
+        return GDN_ERR_SHAPE;
+    if (K.dtype != V.dtype) return GDN_ERR_DTYPE;
+    if (q) {
+        if ((s = view_of(q, Q)) != GDN_OK) return s;
+        if ((s = view_of(q_out, O)) != GDN_OK) return s;
+        if (Q.T != K.T || Q.D != K.D || O.T != Q.T || O.H != Q.H || O.D != Q.D)
+            return GDN_ERR_SHAPE;
+        if (Q.dtype != K.dtype || O.dtype != K.dtype) return GDN_ERR_DTYPE;
+        // a lane of the rotation reads elements that another lane may already have stored
+        if (K.T > 0 && Q.ptr == O.ptr) return GDN_ERR_LAYOUT;
+        a.q = Q.ptr; a.q_out = O.ptr; a.q_tok = Q.tok; a.o_tok = O.tok;
+        a.Hq = (int32_t)Q.H;
+    }
+    if (!cos_table != !sin_table) return GDN_ERR_NULL;
+    if (cos_table) {
+        if (rot < 16 || rot > a.D || rot % 16 != 0) return GDN_ERR_UNSUPPORTED;
+        if (table_rows <= 0) return GDN_ERR_SHAPE;
+        if (!aligned16(cos_table) || !aligned16(sin_table)) return GDN_ERR_LAYOUT;
+    }
+    if (K.T == 0) return GDN_OK;
+    cudaStream_t st = (cudaStream_t)stream;
+    if ((flags & GDN_CHECK_INPUTS) && cu_seqlens_host &&
+        (s = check_seqlens_copy(cu_seqlens_dev, cu_seqlens_host, a.kv.N, st)) != GDN_OK)
+        return s;
+    a.k = K.ptr; a.v = V.ptr; a.k_tok = K.tok; a.v_tok = V.tok;
+    a.cos_tab = cos_table; a.sin_tab = sin_table; a.tab_rows = table_rows; a.rot = rot;
+    a.interleaved = (flags & GDN_KV_INTERLEAVED) ? 1 : 0;
+    a.in_f32 = K.dtype == GDN_F32;
+    a.status = status_dev;
+    return gdn_host::launch_kv_append(a, st);
+}
+
+gdn_status_t gdn_kv_read(const gdn_kv_cache_t *cache, const int32_t *cu_seqlens_dev,
+                         const int32_t *cu_seqlens_host, const gdn_tensor_t *k_out,
+                         const gdn_tensor_t *v_out, uint32_t flags, int32_t *status_dev,
+                         void *stream) {
+    gdn_host::CallRange nvtx_range("gdn_kv_read");
+    View K, V;
+    gdn_status_t s;
+    if ((s = view_of(k_out, K)) != GDN_OK) return s;
+    if ((s = view_of(v_out, V)) != GDN_OK) return s;
+    gdn_host::KvArgs a;
+    if ((s = kv_args(cache, cu_seqlens_dev, cu_seqlens_host, K.T, a)) != GDN_OK) return s;
+    if (V.T != K.T || V.H != K.H || V.D != K.D || K.H != a.kv.Hkv || K.D != a.D)
+        return GDN_ERR_SHAPE;
+    if (K.dtype != V.dtype) return GDN_ERR_DTYPE;
+    if (K.T == 0) return GDN_OK;
+    cudaStream_t st = (cudaStream_t)stream;
+    if ((flags & GDN_CHECK_INPUTS) && cu_seqlens_host &&
+        (s = check_seqlens_copy(cu_seqlens_dev, cu_seqlens_host, a.kv.N, st)) != GDN_OK)
+        return s;
+    a.k = K.ptr; a.v = V.ptr; a.k_tok = K.tok; a.v_tok = V.tok;
+    a.in_f32 = K.dtype == GDN_F32;
+    a.status = status_dev;
+    return gdn_host::launch_kv_read(a, st);
+}
+
+size_t gdn_kv_attention_workspace_size(int32_t head_dim, int32_t Hq, int32_t Hkv, int64_t T,
+                                       int32_t N, int32_t max_q_len, int32_t max_kv_len,
+                                       int32_t dtype, uint32_t flags) {
+    return gdn_host::kv_attention_workspace(head_dim, Hq, Hkv, T, N, max_q_len, max_kv_len,
+                                            dtype == GDN_F32, flags);
+}
+
+gdn_status_t gdn_kv_attention(const gdn_kv_cache_t *cache, const int32_t *cu_seqlens_dev,
+                              const int32_t *cu_seqlens_host, int32_t max_kv_len,
+                              const gdn_tensor_t *q, float scale, uint32_t flags,
+                              const gdn_tensor_t *o, float *lse, void *workspace,
+                              size_t workspace_bytes, int32_t *status_dev, void *stream) {
+    gdn_host::CallRange nvtx_range("gdn_kv_attention");
+    View Q, O;
+    gdn_status_t s;
+    if ((s = view_of(q, Q)) != GDN_OK) return s;
+    if ((s = view_of(o, O)) != GDN_OK) return s;
+    gdn_host::KvArgs a;
+    if ((s = kv_args(cache, cu_seqlens_dev, cu_seqlens_host, Q.T, a)) != GDN_OK) return s;
+    if (O.T != Q.T || O.H != Q.H || O.D != Q.D || Q.D != a.D || Q.H % a.kv.Hkv != 0 ||
+        Q.H > 65535 || max_kv_len < 0)
+        return GDN_ERR_SHAPE;
+    if (Q.dtype != O.dtype) return GDN_ERR_DTYPE;
+    if (Q.T == 0) return GDN_OK;
+    cudaStream_t st = (cudaStream_t)stream;
+    if ((flags & GDN_CHECK_INPUTS) && cu_seqlens_host &&
+        (s = check_seqlens_copy(cu_seqlens_dev, cu_seqlens_host, a.kv.N, st)) != GDN_OK)
+        return s;
+    a.q = Q.ptr; a.q_out = O.ptr; a.q_tok = Q.tok; a.o_tok = O.tok;
+    a.Hq = (int32_t)Q.H;
+    a.max_kv_len = max_kv_len;
+    a.scale = scale;
+    a.flags = flags;
+    a.lse = lse;
+    a.in_f32 = Q.dtype == GDN_F32;
+    a.status = status_dev;
+    a.ws = workspace;
+    a.ws_bytes = workspace_bytes;
+    const size_t need = gdn_host::kv_attention_workspace(a.D, a.Hq, a.kv.Hkv, a.T, a.kv.N, a.max_q_len,
+                                                         max_kv_len, a.in_f32, flags);
+    if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)))
+        return GDN_ERR_WORKSPACE;
+    return gdn_host::launch_kv_attention(a, st);
 }
 
 gdn_status_t gdn_selftest_bounded_wait(int32_t *status_dev, void *stream) {

@@ -1,0 +1,245 @@
+// linear.cu -- linear attention with a decay for each head, on the CUDA cores: the
+// recurrence over packed sequences (any D in {16, 32, 64, 128}, fp32 or bf16), and the
+// one-token step on a pool of states.
+//
+//     S_t = e^{g_t} S_{t-1} + k_t v_t^T      (S: D x D, fp32)
+//     o_t = scale * S_t^T q_t
+//
+// It is the gated delta rule without its correction term, so the state's columns do not
+// interact: column j of S needs v_j only.
+#include "linear.cuh"
+
+namespace gdn {
+
+// ------------------------------------------------------------------ prompts, CUDA cores
+// The decay factor as a sum hi + lo of two floats.  A slow decay multiplies the state
+// hundreds of times, so e^g rounded to 24 bits would leave a relative error of that many
+// half-ulps; 1 + expm1(g) keeps it to about |g| 2^-24 a step.
+__device__ __forceinline__ float2 decay_pair(float g) {
+    const float e = expm1f(g), hi = 1.f + e;
+    return make_float2(hi, e - (hi - 1.f));
+}
+
+// One CTA per (sequence, v-head, tile of columns), walking the tokens.  A lane holds two
+// columns of D / RG rows: lanes with equal column pairs split the rows in groups of four
+// (rows 4 rg + 4 RG x ..+3), so a float4 of k or q is read by all lanes of a warp without
+// bank conflicts, and o is summed over the RG lanes by shuffles in a fixed order.
+template <int D> struct LinShape {
+    static constexpr int RG = D / 4 < 8 ? D / 4 : 8;     // lanes that split the rows
+    static constexpr int CW = (32 / RG) * 2;             // columns per warp
+    static constexpr int WARPS = D / CW < 4 ? D / CW : 4;
+    static constexpr int COLS = CW * WARPS;              // columns per CTA
+    static constexpr int RX = D / (4 * RG);              // groups of four rows per lane
+    static constexpr int TB = 32;                        // tokens staged at a time
+    static constexpr int FIX = 8;                        // tokens per correction of the decay
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(LinShape<D>::WARPS * 32)
+linear_scan_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                   T *__restrict__ o, int64_t q_tok, int64_t k_tok, int64_t v_tok,
+                   int64_t o_tok, const float *__restrict__ g, int64_t g_tok,
+                   const int32_t *__restrict__ cu, const float *__restrict__ h0, float *hT,
+                   int Hk, int Hv, float scale) {
+    using L = LinShape<D>;
+    constexpr int THREADS = L::WARPS * 32;
+    __shared__ float4 sq[L::TB][D / 4], sk[L::TB][D / 4];
+    __shared__ float2 sv[L::TB][L::COLS / 2];
+    __shared__ float sa[L::TB], slo[L::TB];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rg = lane % L::RG, cp = warp * (L::CW / 2) + lane / L::RG;
+    const int j0 = blockIdx.x * L::COLS, hv = blockIdx.y, n = blockIdx.z;
+    const int hk = hv / (Hv / Hk);
+    const int t0 = cu[n], len = cu[n + 1] - t0;
+    const size_t st0 = ((size_t)n * Hv + hv) * D * D + j0 + 2 * cp;
+
+    float2 S[L::RX][4];
+#pragma unroll
+    for (int x = 0; x < L::RX; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            S[x][e] = h0 ? *reinterpret_cast<const float2 *>(
+                               h0 + st0 + (size_t)(4 * rg + 4 * L::RG * x + e) * D)
+                         : make_float2(0.f, 0.f);
+
+    for (int b = 0; b < len; b += L::TB) {
+        const int m = min(L::TB, len - b);
+        __syncthreads();
+        for (int i = tid; i < m * D; i += THREADS) {
+            const int t = i / D, d = i % D;
+            const int64_t row = t0 + b + t;
+            reinterpret_cast<float *>(sq[t])[d] = to_f32(q[row * q_tok + (int64_t)hk * D + d]);
+            reinterpret_cast<float *>(sk[t])[d] = to_f32(k[row * k_tok + (int64_t)hk * D + d]);
+        }
+        for (int i = tid; i < m * L::COLS; i += THREADS) {
+            const int t = i / L::COLS, j = i % L::COLS;
+            reinterpret_cast<float *>(sv[t])[j] =
+                to_f32(v[(t0 + b + t) * v_tok + (int64_t)hv * D + j0 + j]);
+        }
+        if (tid < m) {
+            const float2 a = decay_pair(g[(t0 + b + tid) * g_tok + hv]);
+            sa[tid] = a.x;
+            slo[tid] = a.x > 0.f ? a.y / a.x : 0.f;
+        }
+        __syncthreads();
+#pragma unroll 2
+        for (int t = 0; t < m; ++t) {
+            const float a = sa[t];
+            const float2 vv = sv[t][cp];
+            float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int x = 0; x < L::RX; ++x) {
+                const float4 k4 = sk[t][rg + L::RG * x], q4 = sq[t][rg + L::RG * x];
+                const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    S[x][e].x = fmaf(S[x][e].x, a, kk[e] * vv.x);
+                    S[x][e].y = fmaf(S[x][e].y, a, kk[e] * vv.y);
+                    acc.x = fmaf(qq[e], S[x][e].x, acc.x);
+                    acc.y = fmaf(qq[e], S[x][e].y, acc.y);
+                }
+            }
+#pragma unroll
+            for (int off = 1; off < L::RG; off <<= 1) {
+                acc.x += __shfl_xor_sync(0xffffffffu, acc.x, off);
+                acc.y += __shfl_xor_sync(0xffffffffu, acc.y, off);
+            }
+            if (rg == 0) {
+                T *dst = o + (t0 + b + t) * o_tok + (int64_t)hv * D + j0 + 2 * cp;
+                dst[0] = from_f32<T>(scale * acc.x);
+                dst[1] = from_f32<T>(scale * acc.y);
+            }
+            // the low parts of the last FIX decays at once (the sum is at most about 2^-21)
+            if (t % L::FIX == L::FIX - 1) {
+                float fix = 0.f;
+#pragma unroll
+                for (int e = 0; e < L::FIX; ++e) fix += slo[t - e];
+#pragma unroll
+                for (int x = 0; x < L::RX; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        S[x][e].x = fmaf(S[x][e].x, fix, S[x][e].x);
+                        S[x][e].y = fmaf(S[x][e].y, fix, S[x][e].y);
+                    }
+            }
+        }
+    }
+    if (hT) {
+#pragma unroll
+        for (int x = 0; x < L::RX; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<float2 *>(hT + st0 + (size_t)(4 * rg + 4 * L::RG * x + e) * D) =
+                    S[x][e];
+    }
+}
+
+// --------------------------------------------------------------------- one-token step
+// One CTA per (sequence, v-head): the state tile goes through registers once, as float4
+// of four columns, so a warp's load is a contiguous 512 bytes; o is summed over the row
+// groups in shared memory in a fixed order.
+template <int D> struct LinDecShape {
+    static constexpr int THREADS = D * D / 4 < 256 ? D * D / 4 : 256;
+    static constexpr int RG = THREADS / (D / 4);   // row groups
+    static constexpr int ROWS = D / RG;            // rows per thread
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(LinDecShape<D>::THREADS)
+linear_decode_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                     T *__restrict__ o, int64_t q_tok, int64_t k_tok, int64_t v_tok,
+                     int64_t o_tok, const float *__restrict__ g, int64_t g_tok,
+                     float *__restrict__ state, int P, const int32_t *__restrict__ idx, int Hk,
+                     int Hv, float scale, int32_t *status) {
+    using L = LinDecShape<D>;
+    __shared__ float sq[D], sk[D];
+    __shared__ __align__(16) float red[L::RG][D];
+    const int hv = blockIdx.x, n = blockIdx.y, tid = threadIdx.x;
+    const int slot = idx ? idx[n] : n;
+    if (slot < 0 || slot >= P) {
+        if (tid == 0) report(status, GDN_ERR_INDEX);
+        return;
+    }
+    const int hk = hv / (Hv / Hk);
+    const int c4 = tid % (D / 4), rg = tid / (D / 4);
+    float4 *tile = reinterpret_cast<float4 *>(state + ((size_t)slot * Hv + hv) * D * D);
+    float4 H[L::ROWS];
+#pragma unroll
+    for (int r = 0; r < L::ROWS; ++r) H[r] = tile[(size_t)(rg + L::RG * r) * (D / 4) + c4];
+    const float2 a = decay_pair(g[n * g_tok + hv]);
+    const T *vr = v + n * v_tok + (int64_t)hv * D + 4 * c4;
+    const float4 vv = make_float4(to_f32(vr[0]), to_f32(vr[1]), to_f32(vr[2]), to_f32(vr[3]));
+    for (int i = tid; i < D; i += L::THREADS) {
+        sq[i] = to_f32(q[n * q_tok + (int64_t)hk * D + i]);
+        sk[i] = to_f32(k[n * k_tok + (int64_t)hk * D + i]);
+    }
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < L::ROWS; ++r) {
+        const int i = rg + L::RG * r;
+        const float ki = sk[i], qi = sq[i];
+        float4 h = H[r];
+        h.x = fmaf(a.x, h.x, fmaf(a.y, h.x, ki * vv.x)); acc.x = fmaf(qi, h.x, acc.x);
+        h.y = fmaf(a.x, h.y, fmaf(a.y, h.y, ki * vv.y)); acc.y = fmaf(qi, h.y, acc.y);
+        h.z = fmaf(a.x, h.z, fmaf(a.y, h.z, ki * vv.z)); acc.z = fmaf(qi, h.z, acc.z);
+        h.w = fmaf(a.x, h.w, fmaf(a.y, h.w, ki * vv.w)); acc.w = fmaf(qi, h.w, acc.w);
+        tile[(size_t)i * (D / 4) + c4] = h;
+    }
+    reinterpret_cast<float4 *>(red[rg])[c4] = acc;
+    __syncthreads();
+    for (int j = tid; j < D; j += L::THREADS) {
+        float s = 0.f;
+#pragma unroll
+        for (int r = 0; r < L::RG; ++r) s += red[r][j];
+        o[n * o_tok + (int64_t)hv * D + j] = from_f32<T>(scale * s);
+    }
+}
+
+}  // namespace gdn
+
+namespace gdn_host {
+
+namespace {
+
+template <typename T, int D>
+gdn_status_t scan_launch(const LinearArgs &a, cudaStream_t st) {
+    using L = gdn::LinShape<D>;
+    gdn::linear_scan_kernel<T, D><<<dim3(D / L::COLS, a.Hv, a.N), L::WARPS * 32, 0, st>>>(
+        (const T *)a.q, (const T *)a.k, (const T *)a.v, (T *)a.o, a.q_tok, a.k_tok, a.v_tok,
+        a.o_tok, a.g, a.g_tok, a.cu, a.h0, a.hT, a.Hk, a.Hv, a.scale);
+    return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+template <typename T, int D>
+gdn_status_t decode_launch(const LinearArgs &a, cudaStream_t st) {
+    gdn::linear_decode_kernel<T, D>
+        <<<dim3(a.Hv, a.N), gdn::LinDecShape<D>::THREADS, 0, st>>>(
+            (const T *)a.q, (const T *)a.k, (const T *)a.v, (T *)a.o, a.q_tok, a.k_tok,
+            a.v_tok, a.o_tok, a.g, a.g_tok, a.state, a.P, a.idx, a.Hk, a.Hv, a.scale,
+            a.status);
+    return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // namespace
+
+#define GDN_LIN_DISPATCH(fn, a, st)                                          \
+    switch ((a).D) {                                                         \
+    case 16: return (a).in_f32 ? fn<float, 16>(a, st) : fn<gdn::bf16, 16>(a, st);    \
+    case 32: return (a).in_f32 ? fn<float, 32>(a, st) : fn<gdn::bf16, 32>(a, st);    \
+    case 64: return (a).in_f32 ? fn<float, 64>(a, st) : fn<gdn::bf16, 64>(a, st);    \
+    case 128: return (a).in_f32 ? fn<float, 128>(a, st) : fn<gdn::bf16, 128>(a, st); \
+    }                                                                        \
+    return GDN_ERR_UNSUPPORTED
+
+bool linear_supported(int64_t D) { return D == 16 || D == 32 || D == 64 || D == 128; }
+
+gdn_status_t launch_linear_scan(const LinearArgs &a, cudaStream_t st) {
+    GDN_LIN_DISPATCH(scan_launch, a, st);
+}
+
+gdn_status_t launch_linear_decode(const LinearArgs &a, cudaStream_t st) {
+    GDN_LIN_DISPATCH(decode_launch, a, st);
+}
+
+}  // namespace gdn_host

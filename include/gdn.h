@@ -357,6 +357,139 @@ gdn_status_t gdn_fused_decode(const void *x, int32_t N, int32_t Hk, int32_t Hv, 
                               float *state, int32_t P, const int32_t *state_idx, float scale,
                               uint32_t flags, void *o, int32_t *status_dev, void *stream);
 
+/*
+ * Linear attention with a decay for each head: the gated delta rule without its
+ * correction term,
+ *
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T   (dk x dv, fp32),    o_t = scale * S_t^T q_t
+ *
+ * over the same views, states and offsets as the entries above: q, k [T, Hk, D];
+ * v, o [T, Hv, D]; v-head h reads q/k head h / (Hv / Hk); states [.., Hv, D, D] fp32 with
+ * element [i][j] multiplying k_i and v_j.  g holds log decays (fp32): [Hv], one per head,
+ * when g_per_token is 0, else [T, Hv] (contiguous).  g = -inf clears the state; a NaN
+ * makes its head's later outputs NaN.  D in {16, 32, 64, 128}; all four views bf16 or all
+ * fp32; D = 128 in bf16 runs on the tensor cores.
+ */
+
+/*
+ * gdn_linear_prefill -- packed prompts.  Arguments as gdn_chunk_prefill's: cu_seqlens
+ * int32 [N+1] on device and host, initial_state [N, Hv, D, D] or NULL (zeros), final_state
+ * likewise or NULL (not written; may equal initial_state).  Every sequence's results are
+ * bit-identical alone and in any batch on one device.  workspace: device scratch of
+ * gdn_linear_prefill_workspace_size() bytes, 256-byte aligned (may be NULL when 0).
+ * flags: GDN_PREFILL_SIMT forces the CUDA-core kernel, GDN_CHECK_INPUTS as above.
+ */
+size_t gdn_linear_prefill_workspace_size(const int32_t *cu_seqlens_host, int32_t N, int64_t T,
+                                         int32_t Hk, int32_t Hv, int32_t D, int32_t dtype,
+                                         uint32_t flags);
+
+gdn_status_t gdn_linear_prefill(const gdn_tensor_t *q, const gdn_tensor_t *k,
+                                const gdn_tensor_t *v, const float *g, int32_t g_per_token,
+                                const int32_t *cu_seqlens_dev, const int32_t *cu_seqlens_host,
+                                int32_t N, float scale, uint32_t flags,
+                                const float *initial_state, const gdn_tensor_t *o,
+                                float *final_state, void *workspace, size_t workspace_bytes,
+                                int32_t *status_dev, void *stream);
+
+/*
+ * gdn_linear_decode -- one token per sequence on a pool of states, in place: arguments as
+ * gdn_recurrent_decode's (state [P, Hv, D, D]; state_idx [N] or NULL for identity; indices
+ * outside [0, P) set *status_dev = GDN_ERR_INDEX and skip that sequence).
+ */
+gdn_status_t gdn_linear_decode(const gdn_tensor_t *q, const gdn_tensor_t *k,
+                               const gdn_tensor_t *v, const float *g, int32_t g_per_token,
+                               float *state, int32_t P, const int32_t *state_idx, float scale,
+                               uint32_t flags, const gdn_tensor_t *o, int32_t *status_dev,
+                               void *stream);
+
+/*
+ * A paged key/value cache held in 4 bits, for the softmax-attention layers that hybrid
+ * models put between linear ones.
+ *
+ * data: uint8 [pages, 2, Hkv, page_size, gdn_kv_record_bytes(head_dim)], keys at index 0
+ * of the second dimension and values at 1; 16-byte aligned.  A record holds one token of
+ * one head: head_dim / 2 bytes of 4-bit codes, then per 32 consecutive elements an fp16
+ * pair (scale, minimum); element d stands for minimum + scale * code.  Nibble i (low
+ * first) of the record's 32-bit word W holds, with G = head_dim / 32,
+ *     keys:   d = 32 (W mod G) + 8 (W div G) + i
+ *     values: d = 64 (W div 8) + 32 (i div 4) + 4 (W mod 8) + (i mod 4).
+ * Per group, x clamped to +-65504: minimum = fp16(min x), scale = fp16((max x - minimum)/15),
+ * code = (x - minimum)/scale rounded to the nearest of 0..15 (ties to even).  A group with
+ * a NaN is stored with minimum = NaN.
+ * block_table [N, table_width] int32 (device): position p of sequence n is slot
+ * p mod page_size of page block_table[n][p div page_size].
+ * kv_lens [N] int32 (device): tokens of each sequence, the new ones of the call included.
+ * head_dim in {64, 128, 256}; page_size a power of two from 16 to 65536.
+ *
+ * New tokens are packed: sequence n's are rows cu_seqlens[n] .. cu_seqlens[n+1]-1 (int32
+ * [N+1] on device and host); with both NULL each sequence has one.  Row i of a sequence's m
+ * new rows has position kv_lens[n] - m + i.
+ */
+typedef struct {
+    void *data;
+    const int32_t *block_table;
+    const int32_t *kv_lens;
+    int32_t pages, page_size, Hkv, head_dim, table_width, N;
+} gdn_kv_cache_t;
+
+/* Bytes of one record: head_dim / 2 + head_dim / 8 (0 for a head_dim without a kernel). */
+size_t gdn_kv_record_bytes(int32_t head_dim);
+
+/*
+ * gdn_kv_append -- rotates the new tokens' k and stores k and v in the cache; with q,
+ * also writes the rotated q to q_out (which must not be q).
+ * k, v [T, Hkv, D]; q, q_out [T, Hq, D] or both NULL; one element type.  cos_table,
+ * sin_table fp32 [table_rows, rot / 2], 16-byte aligned, row = position, or both NULL (no
+ * rotation); rot a multiple of 16, at most D: the first rot elements turn in pairs
+ * (e, e + rot/2), or (2e, 2e + 1) with GDN_KV_INTERLEAVED.  The rotation is fp32, products
+ * and sums rounded separately, and k is not rounded to its type before it is stored.
+ * A position outside the block table or the angle tables, or a page outside [0, pages),
+ * sets *status_dev = GDN_ERR_INDEX and skips the row.  Two new tokens must not share a
+ * slot.
+ */
+#define GDN_KV_INTERLEAVED 0x2000u
+
+gdn_status_t gdn_kv_append(const gdn_kv_cache_t *cache, const int32_t *cu_seqlens_dev,
+                           const int32_t *cu_seqlens_host, const gdn_tensor_t *k,
+                           const gdn_tensor_t *v, const gdn_tensor_t *q,
+                           const gdn_tensor_t *q_out, const float *cos_table,
+                           const float *sin_table, int32_t table_rows, int32_t rot,
+                           uint32_t flags, int32_t *status_dev, void *stream);
+
+/*
+ * gdn_kv_read -- the rows of the given tokens (positions as above) as values:
+ * k_out, v_out [T, Hkv, D], minimum + scale * code rounded once to the views' type.
+ * Errors as gdn_kv_append's; skipped rows are not written.
+ */
+gdn_status_t gdn_kv_read(const gdn_kv_cache_t *cache, const int32_t *cu_seqlens_dev,
+                         const int32_t *cu_seqlens_host, const gdn_tensor_t *k_out,
+                         const gdn_tensor_t *v_out, uint32_t flags, int32_t *status_dev,
+                         void *stream);
+
+/*
+ * gdn_kv_attention -- softmax attention of the new tokens over the cache (which already
+ * holds them): q head h reads kv head h / (Hq / Hkv); the row at position p sees keys
+ * 0..p, weighted by exp(scale q.k).  A row that sees no key (kv_lens[n] smaller than its
+ * sequence's new rows) gives zeros, and -inf in lse.
+ * q, o [T, Hq, D], one type; lse fp32 [T, Hq] (natural logarithm of the weights' sum) or
+ * NULL.  max_kv_len: an upper bound of kv_lens (sizes the grid); a sequence with a length
+ * above it, above the block table's reach or negative sets *status_dev = GDN_ERR_SEQLENS
+ * and its rows are not written.  Keys in a page outside [0, pages) are left out and set
+ * GDN_ERR_INDEX.  What lies past kv_lens in a page is never used, whatever it holds.
+ * workspace: device scratch of gdn_kv_attention_workspace_size() bytes, 256-byte aligned
+ * (may be NULL when 0).  A sequence's results are bit-identical alone and in any batch
+ * called with the same number of new rows.
+ */
+size_t gdn_kv_attention_workspace_size(int32_t head_dim, int32_t Hq, int32_t Hkv, int64_t T,
+                                       int32_t N, int32_t max_q_len, int32_t max_kv_len,
+                                       int32_t dtype, uint32_t flags);
+
+gdn_status_t gdn_kv_attention(const gdn_kv_cache_t *cache, const int32_t *cu_seqlens_dev,
+                              const int32_t *cu_seqlens_host, int32_t max_kv_len,
+                              const gdn_tensor_t *q, float scale, uint32_t flags,
+                              const gdn_tensor_t *o, float *lse, void *workspace,
+                              size_t workspace_bytes, int32_t *status_dev, void *stream);
+
 /* gdn_selftest_bounded_wait -- checks the failure path of the bounded waits.  Every wait
  * of the tensor-core kernels on an mbarrier (a TMA copy or an MMA completing) gives up
  * after 2 s; the CTA then records GDN_ERR_TIMEOUT in the status word, stops issuing work,
