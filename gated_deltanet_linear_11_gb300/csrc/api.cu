@@ -553,10 +553,15 @@ gdn_status_t kv_args(const gdn_kv_cache_t *c, const int32_t *cu_dev, const int32
     if (T > 0x7fffffff) return GDN_ERR_SHAPE;
     if (!cu_host != !cu_dev) return GDN_ERR_NULL;
     memset(&a, 0, sizeof(a));
-    a.max_q_len = T > 0 ? 1 : 0;
+    a.max_q_len = a.min_q_len = T > 0 ? 1 : 0;
     if (cu_host) {
         const gdn_status_t s = check_seqlens(cu_host, c->N, T, &a.max_q_len);
         if (s != GDN_OK) return s;
+        a.min_q_len = a.max_q_len;
+        for (int32_t n = 0; n < c->N; ++n) {
+            const int32_t m = cu_host[n + 1] - cu_host[n];
+            if (m > 0 && m < a.min_q_len) a.min_q_len = m;
+        }
     } else if (T != c->N) {
         return GDN_ERR_SEQLENS;
     }

@@ -4,6 +4,10 @@
 // for token i of the m new tokens of a sequence with kv_len tokens (the new ones
 // included, already in the cache).  A row that sees no key (kv_len < m - i) gives zeros,
 // and a log-sum-exp of -inf.
+#include <algorithm>
+#include <atomic>
+
+#include "bulk_ptx.cuh"
 #include "kv_format.cuh"
 
 namespace gdn {
@@ -128,6 +132,590 @@ kv_attention_simt_kernel(KvView kv, const T *__restrict__ q, T *__restrict__ o, 
     if (lse && tid == 0) lse[t * Hq + hq] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
+// ------------------------------------------------------------------ tensor-core form
+// bf16 activations.  The rows of one kv-head (G query heads x m tokens, token-major) are
+// cut into tiles of 8 NT; one CTA takes one row tile and one split of the keys, its four
+// warps taking every fourth block of 32 keys with a softmax state of their own, joined at
+// the end.  All products run as m16n8k16 on fp16 with keys (then elements) as the 16 rows
+// and query rows as the 8 columns, so that few rows waste little of an instruction and
+// each stored code is unpacked once per warp however many rows use it:
+//     S^T = K Q^T      O^T = V^T P^T
+//
+// A code u enters as the fp16 bit pattern u or u << 4, i.e. the subnormal u 2^-24 or
+// u 2^-20: one AND per pair of codes, no conversion, and exact.  Scale and minimum stay
+// outside: with q', p' the rows as the fragments hold them and g the groups of 32,
+//     q.k = sum_g scale_kg (q'.u)_g + sum_g min_kg (sum of q' over g)
+//     o_d = sum_k (p_k scale_kg) u_kd + sum_k p_k min_kg
+// the first scales applied to the fp32 products, the second to p in fp16, and both terms
+// in the minima as one small product more (the sums of q' as an fp16 pair hi + lo).
+//
+// Fewer bits than fp32: q is scaled by a power of two per row so that its largest element
+// lies in [2^11, 2^12), where fp16 holds a bf16 exactly (down to 2^-26 of the largest);
+// p is rounded to fp16 (2^-11), at 4 times its value so that small weights keep more bits
+// while 4 * scale stays in the fp16 range.  p scale goes in as an fp16 pair (product and
+// what its rounding left out): scale * code and minimum cancel to a value several times
+// smaller than either, so one fp16 product would show where few keys carry a row.  Scores,
+// sums, maxima and outputs are fp32.
+//
+// Keys come in blocks of 16 records of a page (pages hold a multiple of 16) by bulk copies
+// into a ring that each warp runs for itself: no barrier of the CTA inside the loop.
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kAttnBlock = 32;      // keys per step of a warp
+
+template <int D, int NT> struct AttnShape {
+    using R = KvRec<D>;
+    static constexpr int ROWS = 8 * NT;
+    static constexpr int STAGE = 2 * kAttnBlock * R::BYTES;
+    static constexpr int STAGES = D == 256 ? 2 : 3;
+    static constexpr int RING = kAttnWarps * STAGES * STAGE;
+    static constexpr int JOIN = kAttnWarps * ROWS * D * 4;      // reuses the ring
+    static constexpr int BUF = RING > JOIN ? RING : JOIN;
+    static constexpr int QF = NT * R::NG * 32 * 16;             // q fragments
+    static constexpr int QM = NT * 32 * 8;                      // group sums of q
+    static constexpr int TAIL = ROWS * (4 + 4) + kAttnWarps * ROWS * 8 + 8 * kAttnWarps * STAGES +
+                                4 * kAttnWarps * STAGES;
+    static constexpr int SMEM = BUF + QF + QM + TAIL;
+};
+
+// Keys per split of a context of len keys with m new rows: 128 up to 1024 keys, doubling
+// with every fourfold length, so that both the number of splits and their length grow with
+// the context; and doubling with m, whose row tiles are work to spread by themselves (from
+// 256 rows on nothing is split).  It depends on the sequence's own lengths only.
+constexpr int kSplitMaxRows = 256;
+__host__ __device__ __forceinline__ int kv_split_len(int len, int m) {
+    if (m >= kSplitMaxRows) return 1 << 30;
+    int s = 128;
+    for (int64_t top = 1024; top < len; top *= 4) s *= 2;
+    for (int x = 1; 2 * x <= m; x *= 2) s *= 2;
+    return s;
+}
+
+// Splits a row of a context of len keys has room for.
+__device__ __forceinline__ int splits_of(int len, int split_len) { return (len + split_len - 1) / split_len; }
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// What rounding the product ab = a b left out.
+__device__ __forceinline__ uint32_t mul_rest(uint32_t a, uint32_t b, uint32_t ab) {
+    const __half2 h = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b),
+                              __hneg2(*reinterpret_cast<const __half2 *>(&ab)));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 4 x K contiguous 32-bit words, as wide loads.
+template <int K>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[K]) {
+    if constexpr (K == 2) {
+        const uint2 t = *reinterpret_cast<const uint2 *>(p);
+        w[0] = t.x; w[1] = t.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < K / 4; ++i) {
+            const uint4 t = reinterpret_cast<const uint4 *>(p)[i];
+            w[4 * i] = t.x; w[4 * i + 1] = t.y; w[4 * i + 2] = t.z; w[4 * i + 3] = t.w;
+        }
+    }
+}
+__device__ __forceinline__ bool half_pair_nonfinite(uint32_t w) {
+    return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+}
+
+constexpr uint32_t kNib0 = 0x000F000Fu, kNib1 = 0x00F000F0u;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads)
+kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__ o,
+                        float *__restrict__ lse, float *__restrict__ part_o,
+                        float2 *__restrict__ part_ml, int64_t q_tok, int64_t o_tok, int Hq,
+                        int row_tiles, int64_t slab, int max_kv_len, float scale,
+                        int32_t *status) {
+    using R = KvRec<D>;
+    using A = AttnShape<D, NT>;
+    constexpr int NG = R::NG, NP = D / 64, REC = R::BYTES;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t *ring = smem;
+    uint4 *qf = reinterpret_cast<uint4 *>(smem + A::BUF);
+    uint2 *qm = reinterpret_cast<uint2 *>(smem + A::BUF + A::QF);
+    float *sfac = reinterpret_cast<float *>(smem + A::BUF + A::QF + A::QM);
+    uint32_t *snan = reinterpret_cast<uint32_t *>(sfac + A::ROWS);
+    float2 *sml = reinterpret_cast<float2 *>(snan + A::ROWS);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sml + kAttnWarps * A::ROWS);
+    uint32_t *spages = reinterpret_cast<uint32_t *>(bars + kAttnWarps * A::STAGES);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+    const int split = blockIdx.x / row_tiles, rt = blockIdx.x % row_tiles;
+    const int hkv = blockIdx.y, n = blockIdx.z;
+    const int t0 = kv.cu ? kv.cu[n] : n, m = kv.cu ? kv.cu[n + 1] - t0 : 1;
+    const int len = kv.kv_lens[n];
+    const int G = Hq / kv.Hkv, rows = G * m, row0 = rt * A::ROWS;
+    if (row0 >= rows) return;
+    if (len < 0 || len > max_kv_len || len > kv.capacity()) {
+        if (tid == 0) report(status, GDN_ERR_SEQLENS);
+        return;
+    }
+    // keys seen by the tile's first and last row
+    const int see_first = len - m + row0 / G + 1;
+    const int see_last = len - m + (min(row0 + A::ROWS, rows) - 1) / G + 1;
+    const int split_len = kv_split_len(len, m);
+    const int k0 = split * split_len, k1 = min(k0 + split_len, see_last);
+    if (k0 >= k1 && split > 0) return;
+    const int splits = (see_last + split_len - 1) / split_len;   // <= 0: no key at all
+
+    // ---- the warp's ring: block b holds keys k0 + 32 (warp + 4 b) ..
+    uint64_t *bar = bars + warp * A::STAGES;
+    uint32_t *pg = spages + warp * A::STAGES;
+    uint8_t *wring = ring + warp * A::STAGES * A::STAGE;
+    const int first = k0 + kAttnBlock * warp;
+    const int blocks = k1 > first ? (k1 - first + kAttnBlock * kAttnWarps - 1) / (kAttnBlock * kAttnWarps) : 0;
+    // Lanes 0..3 copy (keys, values) x (first, second 16 records); a page outside the cache
+    // is left out and marked.  The page of the block after is looked up one fetch ahead.
+    const int sub_l = lane & 1, which = (lane >> 1) & 1;
+    auto lookup = [&](int b) {
+        const int j = first + b * kAttnBlock * kAttnWarps + 16 * sub_l;
+        return lane < 4 && j < k1 ? kv.table[(int64_t)n * kv.table_width + (j >> kv.page_log2)] : -2;
+    };
+    int page_next = lookup(0);
+    auto fetch = [&](int b) {
+        const int s = b % A::STAGES;
+        const int j = first + b * kAttnBlock * kAttnWarps + 16 * sub_l;
+        const int page = page_next;
+        page_next = lookup(b + 1);
+        const bool want = page >= 0 && page < kv.pages;
+        if (!want && page != -2) report(status, GDN_ERR_INDEX);
+        const uint32_t ok = __ballot_sync(0xffffffffu, want);
+        if (lane == 0) {
+            pg[s] = ok & 3u;
+            tc::mbar_expect_tx(bar + s, __popc(ok) * 16 * REC);
+        }
+        __syncwarp();
+        if (want)
+            bulk_load(wring + s * A::STAGE + (2 * which + sub_l) * 16 * REC,
+                      kv.block(page, which, hkv, REC) + (int64_t)(j & ((1 << kv.page_log2) - 1)) * REC,
+                      16 * REC, bar + s);
+    };
+    if (lane == 0) {
+        for (int s = 0; s < A::STAGES; ++s) tc::mbar_init(bar + s, 1);
+        tc::mbar_fence_init();
+    }
+    __syncwarp();
+    for (int b = 0; b < A::STAGES - 1 && b < blocks; ++b) fetch(b);
+
+    // ---- q as fragments: lane (r, c) of a tile's warp holds elements 32 g + 8 c .. +7 of
+    // row r, scaled; odd elements also by 1/16 (their codes come as u << 4)
+    for (int nt = warp; nt < NT; nt += kAttnWarps) {
+        const int row = row0 + 8 * nt + r;
+        float x[NG][8];
+        float mx = 0.f;
+        const bf16 *src = q + (int64_t)(t0 + (row < rows ? row / G : 0)) * q_tok +
+                          (int64_t)(hkv * G + (row < rows ? row % G : 0)) * D + 8 * c;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            if (row < rows) {
+                unpack8(*reinterpret_cast<const uint4 *>(src + 32 * g), x[g]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[g][e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[g][e]));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int ex = mx > 0.f && mx < INFINITY ? 11 - ilogbf(mx) : 0;
+        float sums[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            float sum = 0.f;
+            __half h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                h[e] = __float2half_rn(scalbnf(x[g][e], ex));
+                sum += __half2float(h[e]);
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            sums[g] = sum;
+            const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f);
+            const __half2 f0 = __halves2half2(h[0], h[4]), f1 = __hmul2(__halves2half2(h[1], h[5]), sixteenth);
+            const __half2 f2 = __halves2half2(h[2], h[6]), f3 = __hmul2(__halves2half2(h[3], h[7]), sixteenth);
+            qf[(nt * NG + g) * 32 + lane] =
+                make_uint4(*reinterpret_cast<const uint32_t *>(&f0), *reinterpret_cast<const uint32_t *>(&f1),
+                           *reinterpret_cast<const uint32_t *>(&f2), *reinterpret_cast<const uint32_t *>(&f3));
+        }
+        // group sums times 2^-12 as hi + lo: lane c has group c (and c + 4)
+        uint32_t mw[2] = {0u, 0u};
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const float v = sums[g] * 0.000244140625f;
+            const float hi = __half2float(__float2half_rn(v));
+            if ((g & 3) == c) mw[g >> 2] = pack_half2(hi, v - hi);
+        }
+        qm[nt * 32 + lane] = make_uint2(mw[0], mw[1]);
+        // a score is (sum of products) 2^24 2^-ex scale; its log2 weight times log2 e
+        if (c == 0) {
+            sfac[8 * nt + r] = scalbnf(scale * 1.4426950408889634f, 24 - ex);
+            snan[8 * nt + r] = 0;
+        }
+    }
+    __syncthreads();
+
+    float O[NT][2 * NG][4], Om[NT][4], mrun[NT][2], lrun[NT][2], fac[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int x = 0; x < 2 * NG; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) O[nt][x][e] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) Om[nt][e] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            mrun[nt][e] = -INFINITY;
+            lrun[nt][e] = 0.f;
+            fac[nt][e] = sfac[8 * nt + 2 * c + e];
+        }
+    }
+
+    int gave_up = -1;
+    for (int b = 0; b < blocks; ++b) {
+        const int s = b % A::STAGES;
+        if (b + A::STAGES - 1 < blocks) fetch(b + A::STAGES - 1);
+        if (!wait_bounded(bar + s, (b / A::STAGES) & 1)) {
+            gave_up = b;
+            break;
+        }
+        const uint8_t *st = wring + s * A::STAGE;
+        const int j0 = first + b * kAttnBlock * kAttnWarps;
+        const uint32_t have = pg[s];
+        // every key of the block is in the cache and seen by every row
+        const bool full = have == 3u && j0 + kAttnBlock <= min(k1, see_first);
+
+        // ---- scores
+        float S[2][NT][4];
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+            const uint8_t *rec0 = st + (16 * sub + r) * REC, *rec1 = rec0 + 8 * REC;
+            uint32_t w0[NG], w1[NG], s0[NG], s1[NG];
+            load_words<NG>(rec0 + c * 4 * NG, w0);
+            load_words<NG>(rec1 + c * 4 * NG, w1);
+            load_words<NG>(rec0 + R::CODES, s0);
+            load_words<NG>(rec1 + R::CODES, s1);
+            // minima: k slots (2c, 2c+1) take group c against the pair (hi, lo)
+            uint32_t am[4] = {0u, 0u, 0u, 0u};
+            if (NG >= 4 || c < NG) {
+                am[0] = __byte_perm(reinterpret_cast<const uint32_t *>(rec0 + R::CODES)[c], 0u, 0x3232);
+                am[1] = __byte_perm(reinterpret_cast<const uint32_t *>(rec1 + R::CODES)[c], 0u, 0x3232);
+            }
+            if (NG == 8) {
+                am[2] = __byte_perm(reinterpret_cast<const uint32_t *>(rec0 + R::CODES)[c + 4], 0u, 0x3232);
+                am[3] = __byte_perm(reinterpret_cast<const uint32_t *>(rec1 + R::CODES)[c + 4], 0u, 0x3232);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint2 bm = qm[nt * 32 + lane];
+                mma16816(t, am[0], am[1], am[2], am[3], bm.x, bm.y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[sub][nt][e] = t[e] * 0.000244140625f;
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float f0 = __low2float(*reinterpret_cast<const __half2 *>(&s0[g]));
+                const float f1 = __low2float(*reinterpret_cast<const __half2 *>(&s1[g]));
+                const uint32_t h0 = w0[g] >> 8, h1 = w1[g] >> 8;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint4 bq = qf[(nt * NG + g) * 32 + lane];
+                    float t[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma16816(t, w0[g] & kNib0, w1[g] & kNib0, w0[g] & kNib1, w1[g] & kNib1, bq.x, bq.y);
+                    mma16816(t, h0 & kNib0, h1 & kNib0, h0 & kNib1, h1 & kNib1, bq.z, bq.w);
+                    S[sub][nt][0] = fmaf(f0, t[0], S[sub][nt][0]);
+                    S[sub][nt][1] = fmaf(f0, t[1], S[sub][nt][1]);
+                    S[sub][nt][2] = fmaf(f1, t[2], S[sub][nt][2]);
+                    S[sub][nt][3] = fmaf(f1, t[3], S[sub][nt][3]);
+                }
+            }
+        }
+
+        // ---- softmax step: columns 2c, 2c+1 of each tile; keys r, r+8, r+16, r+24
+        uint32_t P[2][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float bm[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = S[sub][nt][e] * fac[nt][e & 1];
+                    if (!full) {
+                        const int row = min(row0 + 8 * nt + 2 * c + (e & 1), rows - 1);
+                        const int j = j0 + 16 * sub + r + 8 * (e >> 1);
+                        if (j >= min(k1, len - m + row / G + 1) || !((have >> sub) & 1u)) x = -INFINITY;
+                    }
+                    S[sub][nt][e] = x;
+                    bm[e & 1] = fmaxf(bm[e & 1], x);
+                }
+            float mnew[2], msub[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 4));
+                bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 8));
+                bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 16));
+                mnew[e] = fmaxf(mrun[nt][e], bm[e]);
+                msub[e] = mnew[e] == -INFINITY ? 0.f : mnew[e] - 2.f;   // p at 4 times its value
+            }
+            if (__any_sync(0xffffffffu, mnew[0] > mrun[nt][0] || mnew[1] > mrun[nt][1])) {
+                float keep[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    keep[e] = mnew[e] == mrun[nt][e] ? 1.f : exp2_approx(mrun[nt][e] - mnew[e]);
+                    mrun[nt][e] = mnew[e];
+                    lrun[nt][e] *= keep[e];
+                }
+#pragma unroll
+                for (int x = 0; x < 2 * NG; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) O[nt][x][e] *= keep[e & 1];
+                Om[nt][0] *= keep[0];
+                Om[nt][1] *= keep[1];
+            }
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = exp2_approx(S[sub][nt][e] - msub[e & 1]);
+                    lrun[nt][e & 1] += p[e];
+                }
+                P[sub][nt][0] = transpose8x8(pack_half2(p[0], p[1]));
+                P[sub][nt][1] = transpose8x8(pack_half2(p[2], p[3]));
+            }
+        }
+
+        // ---- values: k slots 2c, 2c+1, 2c+8, 2c+9 are the keys of the same number
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+            const uint8_t *v0 = st + (32 + 16 * sub + 2 * c) * REC;
+            const uint8_t *vk[4] = {v0, v0 + REC, v0 + 8 * REC, v0 + 9 * REC};
+            uint32_t pr[4][NG], mr[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                load_words<NG>(vk[x] + R::CODES, pr[x]);
+                mr[x] = r < NG ? reinterpret_cast<const uint32_t *>(vk[x] + R::CODES)[r] : 0u;
+            }
+            if (!full) {
+                // records no row of this tile sees are taken as zero; so are non-finite
+                // pairs, whose group becomes NaN in just the rows that see the key
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int j = j0 + 16 * sub + 2 * c + (x & 1) + 8 * (x >> 1);
+                    const bool in = j < k1 && ((have >> sub) & 1u);
+                    if (!in || half_pair_nonfinite(mr[x])) mr[x] = 0u;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        if (in && r == 0 && half_pair_nonfinite(pr[x][g])) {
+                            for (int y = 0; y < A::ROWS && row0 + y < rows; ++y)
+                                if (j < len - m + (row0 + y) / G + 1) atomicOr(snan + y, 1u << g);
+                        }
+                        if (!in || half_pair_nonfinite(pr[x][g])) pr[x][g] = 0u;
+                    }
+                }
+            }
+            const uint32_t a0 = __byte_perm(mr[0], mr[1], 0x7632), a2 = __byte_perm(mr[2], mr[3], 0x7632);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(Om[nt], a0, 0u, a2, 0u, P[sub][nt][0], P[sub][nt][1]);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                uint32_t w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) w[x] = reinterpret_cast<const uint32_t *>(vk[x])[8 * p + r];
+#pragma unroll
+                for (int hgrp = 0; hgrp < 2; ++hgrp) {
+                    const int g = 2 * p + hgrp;
+                    const uint32_t sel = hgrp ? 0x7632 : 0x5410;
+                    const uint32_t x1 = __byte_perm(w[0], w[1], sel), x2 = __byte_perm(w[2], w[3], sel);
+                    const uint32_t y1 = x1 >> 8, y2 = x2 >> 8;
+                    const uint32_t sc1 = __byte_perm(pr[0][g], pr[1][g], 0x5410);
+                    const uint32_t sc2 = __byte_perm(pr[2][g], pr[3][g], 0x5410);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint32_t b0 = mul_half2(P[sub][nt][0], sc1);
+                        const uint32_t b1 = mul_half2(P[sub][nt][1], sc2);
+                        const uint32_t e0 = mul_rest(P[sub][nt][0], sc1, b0);
+                        const uint32_t e1 = mul_rest(P[sub][nt][1], sc2, b1);
+                        mma16816(O[nt][2 * g], x1 & kNib0, x1 & kNib1, x2 & kNib0, x2 & kNib1, b0, b1);
+                        mma16816(O[nt][2 * g + 1], y1 & kNib0, y1 & kNib1, y2 & kNib0, y2 & kNib1, b0, b1);
+                        mma16816(O[nt][2 * g], x1 & kNib0, x1 & kNib1, x2 & kNib0, x2 & kNib1, e0, e1);
+                        mma16816(O[nt][2 * g + 1], y1 & kNib0, y1 & kNib1, y2 & kNib0, y2 & kNib1, e0, e1);
+                    }
+                }
+            }
+        }
+        __syncwarp();   // the stage is free for the fetch after the next
+    }
+    if (gave_up >= 0) {
+        // a copy never signalled: report, and let what is in flight land (bounded too)
+        if (lane == 0) report(status, GDN_ERR_TIMEOUT);
+        for (int b = gave_up; b < blocks && b < gave_up + A::STAGES; ++b)
+            wait_bounded(bar + b % A::STAGES, (b / A::STAGES) & 1);
+    }
+
+    // ---- join the warps: maxima and sums, then outputs through shared memory
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float l = lrun[nt][e];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            lrun[nt][e] = l;
+            if (r == 0) sml[warp * A::ROWS + 8 * nt + 2 * c + e] = make_float2(mrun[nt][e], l);
+        }
+    __syncthreads();     // every warp is done with its ring
+    float *join = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float wgt[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float mall = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) mall = fmaxf(mall, sml[w * A::ROWS + 8 * nt + 2 * c + e].x);
+            wgt[e] = mrun[nt][e] == -INFINITY ? 0.f : exp2_approx(mrun[nt][e] - mall);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const float m0 = __shfl_sync(0xffffffffu, Om[nt][0], 4 * g + c);
+            const float m1 = __shfl_sync(0xffffffffu, Om[nt][1], 4 * g + c);
+            const float up = 16777216.f, up16 = 1048576.f;   // 2^24; 2^20 where u came as u << 4
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float mm = e ? m1 : m0;
+                float4 v;
+                v.x = wgt[e] * fmaf(O[nt][2 * g][e], up, mm);
+                v.y = wgt[e] * fmaf(O[nt][2 * g][2 + e], up16, mm);
+                v.z = wgt[e] * fmaf(O[nt][2 * g + 1][e], up, mm);
+                v.w = wgt[e] * fmaf(O[nt][2 * g + 1][2 + e], up16, mm);
+                reinterpret_cast<float4 *>(join + (size_t)(warp * A::ROWS + 8 * nt + 2 * c + e) * D)[8 * g + r] = v;
+            }
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < A::ROWS * (D / 4); i += kAttnThreads) {
+        const int y = i / (D / 4), d4 = i % (D / 4), row = row0 + y;
+        if (row >= rows) continue;
+        float mall = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) mall = fmaxf(mall, sml[w * A::ROWS + y].x);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+            const float2 ml = sml[w * A::ROWS + y];
+            if (ml.x != -INFINITY || ml.y != ml.y) l += ml.y * (ml.x == -INFINITY ? 1.f : exp2_approx(ml.x - mall));
+            const float4 t = reinterpret_cast<const float4 *>(join + (size_t)(w * A::ROWS + y) * D)[d4];
+            v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+        }
+        if ((snan[y] >> (d4 >> 3)) & 1u) v.x = v.y = v.z = v.w = __int_as_float(0x7fffffff);
+        const int64_t t = t0 + row / G;
+        const int hq = hkv * G + row % G;
+        if (splits > 1) {
+            const int64_t at = n * slab + ((t - t0) * Hq + hq) * splits_of(len, split_len) + split;
+            reinterpret_cast<float4 *>(part_o + at * D)[d4] = v;
+            if (d4 == 0) part_ml[at] = make_float2(mall, l);
+        } else {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            uint2 u;
+            u.x = pack_bf2(v.x * inv, v.y * inv);
+            u.y = pack_bf2(v.z * inv, v.w * inv);
+            if (l != l) u.x = u.y = 0x7fff7fffu;
+            reinterpret_cast<uint2 *>(o + t * o_tok + (int64_t)hq * D)[d4] = u;
+            // p was 4 times its value
+            if (lse && d4 == 0) lse[t * Hq + hq] = l == 0.f ? -INFINITY : (mall + log2f(l) - 2.f) * 0.6931471805599453f;
+        }
+    }
+}
+
+// Joins the splits of a row: one warp per row, the weights 2^(m_s - max) in the order of
+// the splits.  Rows of one split were written by the kernel above.
+template <int D>
+__global__ void __launch_bounds__(128)
+kv_attention_join_kernel(KvView kv, bf16 *__restrict__ o, float *__restrict__ lse,
+                         const float *__restrict__ part_o, const float2 *__restrict__ part_ml,
+                         int64_t o_tok, int Hq, int64_t T, int tile_rows, int64_t slab,
+                         int max_kv_len) {
+    const int lane = threadIdx.x & 31;
+    const int64_t out = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    grid_dependency_wait();
+    if (out >= T * Hq) return;
+    const int64_t t = out / Hq;
+    const int hq = (int)(out - t * Hq);
+    const int n = kv.cu ? sequence_of(kv.cu, kv.N, (int)t) : (int)t;
+    const int t0 = kv.cu ? kv.cu[n] : n, m = kv.cu ? kv.cu[n + 1] - t0 : 1;
+    const int len = kv.kv_lens[n];
+    if (len < 0 || len > max_kv_len || len > kv.capacity()) return;
+    const int G = Hq / kv.Hkv, rows = G * m, row = (int)(t - t0) * G + hq % G;
+    const int last = min((row / tile_rows + 1) * tile_rows, rows) - 1;
+    const int see_last = len - m + last / G + 1;
+    const int split_len = kv_split_len(len, m);
+    const int splits = (see_last + split_len - 1) / split_len;
+    if (splits <= 1) return;
+    const int64_t at = n * slab + ((t - t0) * Hq + hq) * splits_of(len, split_len);
+    const float2 *ml = part_ml + at;
+    float mall = -INFINITY;
+    for (int s = lane; s < splits; s += 32) mall = fmaxf(mall, ml[s].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mall = fmaxf(mall, __shfl_xor_sync(0xffffffffu, mall, off));
+    constexpr int E = D / 32;
+    float acc[E] = {}, l = 0.f;
+    const float *po = part_o + at * D + E * lane;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+        const float2 x = ml[s];
+        const float w = x.x == -INFINITY ? (x.y == x.y ? 0.f : x.y) : exp2_approx(x.x - mall);
+        l = fmaf(w, x.y, l);
+        float v[E];
+        if constexpr (E == 2) {
+            *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(po + (int64_t)s * D);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E / 4; ++e)
+                reinterpret_cast<float4 *>(v)[e] = reinterpret_cast<const float4 *>(po + (int64_t)s * D)[e];
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    bf16 *dst = o + t * o_tok + (int64_t)hq * D + E * lane;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t *>(dst + e) = pack_bf2(acc[e] * inv, acc[e + 1] * inv);
+    if (lse && lane == 0) lse[out] = l == 0.f ? -INFINITY : (mall + log2f(l) - 2.f) * 0.6931471805599453f;
+}
+
 }  // namespace gdn
 
 namespace gdn_host {
@@ -155,13 +743,99 @@ gdn_status_t launch_kv_attention_simt(const KvArgs &a, cudaStream_t st) {
     return GDN_ERR_UNSUPPORTED;
 }
 
+namespace {
+
+int attn_max_nt(int D) { return D == 64 ? 8 : D == 128 ? 4 : 2; }
+
+// n-tiles per CTA: the fewest of 1, 2, 4 (8) that take every row of a kv-head, at most as
+// many as the accumulators' registers allow.
+int attn_nt(int D, int64_t rows) {
+    int nt = 1;
+    while (8 * nt < rows && nt < attn_max_nt(D)) nt *= 2;
+    return nt;
+}
+
+// The most splits that a context of at most max_len keys with m new rows has.
+int attn_max_splits(int max_len, int m) {
+    int most = 1;
+    for (int64_t top = 1024;; top *= 4) {
+        const int len = (int)std::min<int64_t>(top, max_len);
+        const int s = gdn::kv_split_len(len, m);
+        most = std::max(most, (int)(((int64_t)len + s - 1) / s));
+        if (top >= max_len) return most;
+    }
+}
+
+// Partial results of one sequence, in rows: Hq m rows of S(m) splits, where S(m) is at most
+// S(1) / 2^floor(log2 m) + 1, so m S(m) <= 2 S(1) + m, and nothing is split from
+// kSplitMaxRows rows on.
+int64_t attn_slab(int Hq, int64_t T, int N, int max_q_len, int max_len) {
+    const int64_t one = attn_max_splits(max_len, 1);
+    if (one <= 1) return 0;
+    if (N == 1) {
+        const int s = attn_max_splits(max_len, (int)std::min<int64_t>(T, gdn::kSplitMaxRows));
+        return s > 1 ? T * Hq * s : 0;
+    }
+    return max_q_len == 1 ? Hq * one : Hq * (2 * one + gdn::kSplitMaxRows);
+}
+
+size_t part_ml_bytes(int64_t rows) { return ((size_t)rows * 8 + 255) / 256 * 256; }
+
+template <int D, int NT>
+gdn_status_t mma_launch(const KvArgs &a, int row_tiles, int splits, cudaStream_t st) {
+    using A = gdn::AttnShape<D, NT>;
+    auto kern = gdn::kv_attention_mma_kernel<D, NT>;
+    static std::atomic<uint64_t> ready{0};   // one bit per device (beyond 63: set every time)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+    if (dev > 63 || !((ready.load() >> dev) & 1u)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM) != cudaSuccess)
+            return GDN_ERR_CUDA;
+        if (dev <= 63) ready.fetch_or(1ull << dev);
+    }
+    const int64_t slab = attn_slab(a.Hq, a.T, a.kv.N, a.max_q_len, a.max_kv_len);
+    float2 *ml = (float2 *)a.ws;
+    float *po = slab ? (float *)((uint8_t *)a.ws + part_ml_bytes(slab * a.kv.N)) : nullptr;
+    kern<<<dim3((unsigned)((int64_t)splits * row_tiles), a.kv.Hkv, a.kv.N), gdn::kAttnThreads, A::SMEM, st>>>(
+        a.kv, (const gdn::bf16 *)a.q, (gdn::bf16 *)a.q_out, a.lse, po, ml, a.q_tok, a.o_tok, a.Hq,
+        row_tiles, slab, a.max_kv_len, a.scale, a.status);
+    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+    if (splits > 1 &&
+        launch_dependent(gdn::kv_attention_join_kernel<D>, dim3((unsigned)((a.T * a.Hq + 3) / 4)), dim3(128), 0, st,
+                         a.kv, (gdn::bf16 *)a.q_out, a.lse, po, ml, a.o_tok, a.Hq, a.T, 8 * NT, slab,
+                         a.max_kv_len) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    return GDN_OK;
+}
+
+}  // namespace
+
 size_t kv_attention_workspace(int32_t D, int32_t Hq, int32_t Hkv, int64_t T, int32_t N,
                               int32_t max_q_len, int32_t max_kv_len, int in_f32, uint32_t flags) {
-    return 0;
+    if (in_f32 || (flags & GDN_PREFILL_SIMT) || T <= 0 || Hq <= 0 || Hkv <= 0) return 0;
+    const int64_t slab = attn_slab(Hq, T, N, max_q_len, max_kv_len);
+    return slab ? part_ml_bytes(slab * N) + (size_t)slab * N * D * sizeof(float) : 0;
 }
 
 gdn_status_t launch_kv_attention(const KvArgs &a, cudaStream_t st) {
-    return launch_kv_attention_simt(a, st);
+    if (a.in_f32 || (a.flags & GDN_PREFILL_SIMT)) return launch_kv_attention_simt(a, st);
+    const int64_t rows = (int64_t)(a.Hq / a.kv.Hkv) * a.max_q_len;
+    const int nt = attn_nt(a.D, rows);
+    const int64_t tiles = (rows + 8 * nt - 1) / (8 * nt);
+    const int splits = attn_max_splits(a.max_kv_len, a.min_q_len);
+    if (tiles * splits > 0x7fffffff || a.kv.N > 65535) return GDN_ERR_SHAPE;
+    switch (a.D * 10 + nt) {
+    case 641: return mma_launch<64, 1>(a, (int)tiles, splits, st);
+    case 642: return mma_launch<64, 2>(a, (int)tiles, splits, st);
+    case 644: return mma_launch<64, 4>(a, (int)tiles, splits, st);
+    case 648: return mma_launch<64, 8>(a, (int)tiles, splits, st);
+    case 1281: return mma_launch<128, 1>(a, (int)tiles, splits, st);
+    case 1282: return mma_launch<128, 2>(a, (int)tiles, splits, st);
+    case 1284: return mma_launch<128, 4>(a, (int)tiles, splits, st);
+    case 2561: return mma_launch<256, 1>(a, (int)tiles, splits, st);
+    case 2562: return mma_launch<256, 2>(a, (int)tiles, splits, st);
+    }
+    return GDN_ERR_UNSUPPORTED;
 }
 
 }  // namespace gdn_host

@@ -82,7 +82,7 @@ struct KvArgs {
     int32_t tab_rows, rot, interleaved;
     float *lse;
     int64_t T;
-    int32_t D, Hq, max_q_len, max_kv_len;
+    int32_t D, Hq, max_q_len, min_q_len, max_kv_len;   // min_q_len: over sequences with rows
     float scale;
     uint32_t flags;
     int in_f32;
