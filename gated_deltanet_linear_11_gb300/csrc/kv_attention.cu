@@ -151,11 +151,11 @@ kv_attention_simt_kernel(KvView kv, const T *__restrict__ q, T *__restrict__ o, 
 //
 // Fewer bits than fp32: q is scaled by a power of two per row so that its largest element
 // lies in [2^11, 2^12), where fp16 holds a bf16 exactly (down to 2^-26 of the largest);
-// p is rounded to fp16 (2^-11), at 4 times its value so that small weights keep more bits
-// while 4 * scale stays in the fp16 range.  p scale goes in as an fp16 pair (product and
-// what its rounding left out): scale * code and minimum cancel to a value several times
-// smaller than either, so one fp16 product would show where few keys carry a row.  Scores,
-// sums, maxima and outputs are fp32.
+// p is rounded to fp16 (2^-11); it is taken against a reference within 2 (in powers of two)
+// of the running maximum, so p < 4 and p scale stays in the fp16 range.  p scale goes in as
+// an fp16 pair (product and what its rounding left out): scale * code and minimum cancel to
+// a value several times smaller than either, so one fp16 product would show where few keys
+// carry a row.  Scores, sums, maxima and outputs are fp32.
 //
 // Keys come in blocks of 16 records of a page (pages hold a multiple of 16) by bulk copies
 // into a ring that each warp runs for itself: no barrier of the CTA inside the loop.
@@ -167,7 +167,7 @@ template <int D, int NT> struct AttnShape {
     using R = KvRec<D>;
     static constexpr int ROWS = 8 * NT;
     static constexpr int STAGE = 2 * kAttnBlock * R::BYTES;
-    static constexpr int STAGES = D == 256 ? 2 : 3;
+    static constexpr int STAGES = 2;
     static constexpr int RING = kAttnWarps * STAGES * STAGE;
     static constexpr int JOIN = kAttnWarps * ROWS * D * 4;      // reuses the ring
     static constexpr int BUF = RING > JOIN ? RING : JOIN;
@@ -176,6 +176,8 @@ template <int D, int NT> struct AttnShape {
     static constexpr int TAIL = ROWS * (4 + 4) + kAttnWarps * ROWS * 8 + 8 * kAttnWarps * STAGES +
                                 4 * kAttnWarps * STAGES;
     static constexpr int SMEM = BUF + QF + QM + TAIL;
+    // CTAs per SM that registers allow without spilling the accumulators (D NT / 4 a thread)
+    static constexpr int CTAS = D * NT <= 128 ? 4 : D * NT <= 256 ? 2 : 1;
 };
 
 // Keys per split of a context of len keys with m new rows: 128 up to 1024 keys, doubling
@@ -194,12 +196,20 @@ __host__ __device__ __forceinline__ int kv_split_len(int len, int m) {
 // Splits a row of a context of len keys has room for.
 __device__ __forceinline__ int splits_of(int len, int split_len) { return (len + split_len - 1) / split_len; }
 
+// d = a b + c on 16 x 8 x 16, fp16 in, fp32 out.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
-                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+        "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+        "{%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
@@ -246,7 +256,7 @@ __device__ __forceinline__ bool half_pair_nonfinite(uint32_t w) {
 constexpr uint32_t kNib0 = 0x000F000Fu, kNib1 = 0x00F000F0u;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads)
+__global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::CTAS)
 kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__ o,
                         float *__restrict__ lse, float *__restrict__ part_o,
                         float2 *__restrict__ part_ml, int64_t q_tok, int64_t o_tok, int Hq,
@@ -293,16 +303,17 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     // Lanes 0..3 copy (keys, values) x (first, second 16 records); a page outside the cache
     // is left out and marked.  The page of the block after is looked up one fetch ahead.
     const int sub_l = lane & 1, which = (lane >> 1) & 1;
-    auto lookup = [&](int b) {
-        const int j = first + b * kAttnBlock * kAttnWarps + 16 * sub_l;
-        return lane < 4 && j < k1 ? kv.table[(int64_t)n * kv.table_width + (j >> kv.page_log2)] : -2;
-    };
-    int page_next = lookup(0);
+    const int32_t *table = kv.table + (int64_t)n * kv.table_width;
+    const int64_t page_bytes = (int64_t)(2 * kv.Hkv * REC) << kv.page_log2;
+    const uint8_t *base = kv.block(0, which, hkv, REC);
+    const int slot_mask = (1 << kv.page_log2) - 1;
+    int jf = lane < 4 ? first + 16 * sub_l : 0x40000000;   // the next fetch's first key
+    int page_next = jf < k1 ? table[jf >> kv.page_log2] : -2;
     auto fetch = [&](int b) {
         const int s = b % A::STAGES;
-        const int j = first + b * kAttnBlock * kAttnWarps + 16 * sub_l;
-        const int page = page_next;
-        page_next = lookup(b + 1);
+        const int j = jf, page = page_next;
+        jf += kAttnBlock * kAttnWarps;
+        page_next = jf < k1 ? table[jf >> kv.page_log2] : -2;
         const bool want = page >= 0 && page < kv.pages;
         if (!want && page != -2) report(status, GDN_ERR_INDEX);
         const uint32_t ok = __ballot_sync(0xffffffffu, want);
@@ -313,8 +324,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         __syncwarp();
         if (want)
             bulk_load(wring + s * A::STAGE + (2 * which + sub_l) * 16 * REC,
-                      kv.block(page, which, hkv, REC) + (int64_t)(j & ((1 << kv.page_log2) - 1)) * REC,
-                      16 * REC, bar + s);
+                      base + page * page_bytes + (j & slot_mask) * REC, 16 * REC, bar + s);
     };
     if (lane == 0) {
         for (int s = 0; s < A::STAGES; ++s) tc::mbar_init(bar + s, 1);
@@ -344,7 +354,9 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int ex = mx > 0.f && mx < INFINITY ? 11 - ilogbf(mx) : 0;
+        // 2^ex brings the largest element into [2^11, 2^12) (rows below 2^-109 stay smaller)
+        const int ex = mx < INFINITY ? min(11 + 127 - (int)(__float_as_uint(mx) >> 23), 120) : 0;
+        const float up = __int_as_float((127 + ex) << 23), down = __int_as_float((127 - ex) << 23);
         float sums[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -352,7 +364,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
             __half h[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                h[e] = __float2half_rn(scalbnf(x[g][e], ex));
+                h[e] = __float2half_rn(x[g][e] * up);
                 sum += __half2float(h[e]);
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
@@ -376,7 +388,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         qm[nt * 32 + lane] = make_uint2(mw[0], mw[1]);
         // a score is (sum of products) 2^24 2^-ex scale; its log2 weight times log2 e
         if (c == 0) {
-            sfac[8 * nt + r] = scalbnf(scale * 1.4426950408889634f, 24 - ex);
+            sfac[8 * nt + r] = scale * (1.4426950408889634f * 16777216.f) * down;
             snan[8 * nt + r] = 0;
         }
     }
@@ -424,20 +436,19 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
             load_words<NG>(rec0 + R::CODES, s0);
             load_words<NG>(rec1 + R::CODES, s1);
             // minima: k slots (2c, 2c+1) take group c against the pair (hi, lo)
+            // (with two groups, lanes 2 and 3 repeat them against zeros)
             uint32_t am[4] = {0u, 0u, 0u, 0u};
-            if (NG >= 4 || c < NG) {
-                am[0] = __byte_perm(reinterpret_cast<const uint32_t *>(rec0 + R::CODES)[c], 0u, 0x3232);
-                am[1] = __byte_perm(reinterpret_cast<const uint32_t *>(rec1 + R::CODES)[c], 0u, 0x3232);
-            }
+            am[0] = __byte_perm(reinterpret_cast<const uint32_t *>(rec0 + R::CODES)[c % NG], 0u, 0x3232);
+            am[1] = __byte_perm(reinterpret_cast<const uint32_t *>(rec1 + R::CODES)[c % NG], 0u, 0x3232);
             if (NG == 8) {
                 am[2] = __byte_perm(reinterpret_cast<const uint32_t *>(rec0 + R::CODES)[c + 4], 0u, 0x3232);
                 am[3] = __byte_perm(reinterpret_cast<const uint32_t *>(rec1 + R::CODES)[c + 4], 0u, 0x3232);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                float t[4];
                 const uint2 bm = qm[nt * 32 + lane];
-                mma16816(t, am[0], am[1], am[2], am[3], bm.x, bm.y);
+                mma16816_first(t, am[0], am[1], am[2], am[3], bm.x, bm.y);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) S[sub][nt][e] = t[e] * 0.000244140625f;
             }
@@ -449,8 +460,8 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const uint4 bq = qf[(nt * NG + g) * 32 + lane];
-                    float t[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma16816(t, w0[g] & kNib0, w1[g] & kNib0, w0[g] & kNib1, w1[g] & kNib1, bq.x, bq.y);
+                    float t[4];
+                    mma16816_first(t, w0[g] & kNib0, w1[g] & kNib0, w0[g] & kNib1, w1[g] & kNib1, bq.x, bq.y);
                     mma16816(t, h0 & kNib0, h1 & kNib0, h0 & kNib1, h1 & kNib1, bq.z, bq.w);
                     S[sub][nt][0] = fmaf(f0, t[0], S[sub][nt][0]);
                     S[sub][nt][1] = fmaf(f0, t[1], S[sub][nt][1]);
@@ -478,21 +489,22 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                     S[sub][nt][e] = x;
                     bm[e & 1] = fmaxf(bm[e & 1], x);
                 }
-            float mnew[2], msub[2];
+            // the reference moves only when a score passes it by 2, so p stays below 4
+            float msub[2];
+            bool move[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 4));
                 bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 8));
                 bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 16));
-                mnew[e] = fmaxf(mrun[nt][e], bm[e]);
-                msub[e] = mnew[e] == -INFINITY ? 0.f : mnew[e] - 2.f;   // p at 4 times its value
+                move[e] = bm[e] > mrun[nt][e] + 2.f;
             }
-            if (__any_sync(0xffffffffu, mnew[0] > mrun[nt][0] || mnew[1] > mrun[nt][1])) {
+            if (__any_sync(0xffffffffu, move[0] || move[1])) {
                 float keep[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    keep[e] = mnew[e] == mrun[nt][e] ? 1.f : exp2_approx(mrun[nt][e] - mnew[e]);
-                    mrun[nt][e] = mnew[e];
+                    keep[e] = move[e] ? exp2_approx(mrun[nt][e] - bm[e]) : 1.f;
+                    mrun[nt][e] = move[e] ? bm[e] : mrun[nt][e];
                     lrun[nt][e] *= keep[e];
                 }
 #pragma unroll
@@ -502,6 +514,8 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                 Om[nt][0] *= keep[0];
                 Om[nt][1] *= keep[1];
             }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) msub[e] = mrun[nt][e] == -INFINITY ? 0.f : mrun[nt][e];
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
                 float p[4];
@@ -524,7 +538,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 load_words<NG>(vk[x] + R::CODES, pr[x]);
-                mr[x] = r < NG ? reinterpret_cast<const uint32_t *>(vk[x] + R::CODES)[r] : 0u;
+                mr[x] = reinterpret_cast<const uint32_t *>(vk[x] + R::CODES)[r % NG];   // rows past NG are not read
             }
             if (!full) {
                 // records no row of this tile sees are taken as zero; so are non-finite
@@ -653,26 +667,24 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
             u.y = pack_bf2(v.z * inv, v.w * inv);
             if (l != l) u.x = u.y = 0x7fff7fffu;
             reinterpret_cast<uint2 *>(o + t * o_tok + (int64_t)hq * D)[d4] = u;
-            // p was 4 times its value
-            if (lse && d4 == 0) lse[t * Hq + hq] = l == 0.f ? -INFINITY : (mall + log2f(l) - 2.f) * 0.6931471805599453f;
+            if (lse && d4 == 0) lse[t * Hq + hq] = l == 0.f ? -INFINITY : (mall + log2f(l)) * 0.6931471805599453f;
         }
     }
 }
 
-// Joins the splits of a row: one warp per row, the weights 2^(m_s - max) in the order of
-// the splits.  Rows of one split were written by the kernel above.
+// Joins the splits of a row: one CTA per row, warp w taking splits w, w + 4, ..., with
+// weights 2^(m_s - max); then the warps in order.  Rows of one split were written by the
+// kernel above.
 template <int D>
 __global__ void __launch_bounds__(128)
 kv_attention_join_kernel(KvView kv, bf16 *__restrict__ o, float *__restrict__ lse,
                          const float *__restrict__ part_o, const float2 *__restrict__ part_ml,
-                         int64_t o_tok, int Hq, int64_t T, int tile_rows, int64_t slab,
-                         int max_kv_len) {
-    const int lane = threadIdx.x & 31;
-    const int64_t out = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    grid_dependency_wait();
-    if (out >= T * Hq) return;
-    const int64_t t = out / Hq;
-    const int hq = (int)(out - t * Hq);
+                         int64_t o_tok, int Hq, int tile_rows, int64_t slab, int max_kv_len) {
+    __shared__ __align__(16) float sacc[4][D];
+    __shared__ float sl[4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t t = blockIdx.x;
+    const int hq = blockIdx.y;
     const int n = kv.cu ? sequence_of(kv.cu, kv.N, (int)t) : (int)t;
     const int t0 = kv.cu ? kv.cu[n] : n, m = kv.cu ? kv.cu[n + 1] - t0 : 1;
     const int len = kv.kv_lens[n];
@@ -685,6 +697,7 @@ kv_attention_join_kernel(KvView kv, bf16 *__restrict__ o, float *__restrict__ ls
     if (splits <= 1) return;
     const int64_t at = n * slab + ((t - t0) * Hq + hq) * splits_of(len, split_len);
     const float2 *ml = part_ml + at;
+    grid_dependency_wait();
     float mall = -INFINITY;
     for (int s = lane; s < splits; s += 32) mall = fmaxf(mall, ml[s].x);
 #pragma unroll
@@ -692,28 +705,46 @@ kv_attention_join_kernel(KvView kv, bf16 *__restrict__ o, float *__restrict__ ls
     constexpr int E = D / 32;
     float acc[E] = {}, l = 0.f;
     const float *po = part_o + at * D + E * lane;
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-        const float2 x = ml[s];
-        const float w = x.x == -INFINITY ? (x.y == x.y ? 0.f : x.y) : exp2_approx(x.x - mall);
-        l = fmaf(w, x.y, l);
-        float v[E];
-        if constexpr (E == 2) {
-            *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(po + (int64_t)s * D);
-        } else {
-#pragma unroll
-            for (int e = 0; e < E / 4; ++e)
-                reinterpret_cast<float4 *>(v)[e] = reinterpret_cast<const float4 *>(po + (int64_t)s * D)[e];
+    for (int s0 = warp; s0 < splits; s0 += 4 * 32) {
+        // lane i holds the weight of split s0 + 4 i; a lane past the end holds zero
+        const int mine = s0 + 4 * lane;
+        float w = 0.f;
+        if (mine < splits) {
+            const float2 x = ml[mine];
+            w = x.x == -INFINITY ? (x.y == x.y ? 0.f : x.y) : exp2_approx(x.x - mall);
+            l = fmaf(w, x.y, l);
         }
+        const int cnt = min(32, (splits - s0 + 3) / 4);
+#pragma unroll 8
+        for (int i = 0; i < cnt; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            float v[E];
+            if constexpr (E == 2) {
+                *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(po + (int64_t)(s0 + 4 * i) * D);
+            } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[e], acc[e]);
+                for (int e = 0; e < E / 4; ++e)
+                    reinterpret_cast<float4 *>(v)[e] =
+                        reinterpret_cast<const float4 *>(po + (int64_t)(s0 + 4 * i) * D)[e];
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, v[e], acc[e]);
+        }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    bf16 *dst = o + t * o_tok + (int64_t)hq * D + E * lane;
 #pragma unroll
-    for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t *>(dst + e) = pack_bf2(acc[e] * inv, acc[e + 1] * inv);
-    if (lse && lane == 0) lse[out] = l == 0.f ? -INFINITY : (mall + log2f(l) - 2.f) * 0.6931471805599453f;
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    if (lane == 0) sl[warp] = l;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sacc[warp][E * lane + e] = acc[e];
+    __syncthreads();
+    l = sl[0] + sl[1] + sl[2] + sl[3];
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    for (int d = 2 * tid; d < D; d += 256) {
+        const float a = sacc[0][d] + sacc[1][d] + sacc[2][d] + sacc[3][d];
+        const float b = sacc[0][d + 1] + sacc[1][d + 1] + sacc[2][d + 1] + sacc[3][d + 1];
+        *reinterpret_cast<uint32_t *>(o + t * o_tok + (int64_t)hq * D + d) = pack_bf2(a * inv, b * inv);
+    }
+    if (lse && tid == 0) lse[t * Hq + hq] = l == 0.f ? -INFINITY : (mall + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace gdn
@@ -801,9 +832,8 @@ gdn_status_t mma_launch(const KvArgs &a, int row_tiles, int splits, cudaStream_t
         row_tiles, slab, a.max_kv_len, a.scale, a.status);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
     if (splits > 1 &&
-        launch_dependent(gdn::kv_attention_join_kernel<D>, dim3((unsigned)((a.T * a.Hq + 3) / 4)), dim3(128), 0, st,
-                         a.kv, (gdn::bf16 *)a.q_out, a.lse, po, ml, a.o_tok, a.Hq, a.T, 8 * NT, slab,
-                         a.max_kv_len) != cudaSuccess)
+        launch_dependent(gdn::kv_attention_join_kernel<D>, dim3((unsigned)a.T, a.Hq), dim3(128), 0, st, a.kv,
+                         (gdn::bf16 *)a.q_out, a.lse, po, ml, a.o_tok, a.Hq, 8 * NT, slab, a.max_kv_len) != cudaSuccess)
         return GDN_ERR_CUDA;
     return GDN_OK;
 }
