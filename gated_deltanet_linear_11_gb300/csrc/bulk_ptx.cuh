@@ -16,7 +16,7 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 constexpr uint64_t kCopyWaitNs = 2000000000ull;   // 2 s bound on any single wait
 
 // Wait for an mbarrier phase; false when it has not completed within the bound.
-__device__ __forceinline__ bool wait_bounded(uint64_t *bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_copy(uint64_t *bar, uint32_t parity) {
     if (tc::mbar_try_wait(bar, parity)) return true;
     uint64_t t0, t;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));

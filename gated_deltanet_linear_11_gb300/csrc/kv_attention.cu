@@ -415,7 +415,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     for (int b = 0; b < blocks; ++b) {
         const int s = b % A::STAGES;
         if (b + A::STAGES - 1 < blocks) fetch(b + A::STAGES - 1);
-        if (!wait_bounded(bar + s, (b / A::STAGES) & 1)) {
+        if (!wait_copy(bar + s, (b / A::STAGES) & 1)) {
             gave_up = b;
             break;
         }
@@ -594,7 +594,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         // a copy never signalled: report, and let what is in flight land (bounded too)
         if (lane == 0) report(status, GDN_ERR_TIMEOUT);
         for (int b = gave_up; b < blocks && b < gave_up + A::STAGES; ++b)
-            wait_bounded(bar + b % A::STAGES, (b / A::STAGES) & 1);
+            wait_copy(bar + b % A::STAGES, (b / A::STAGES) & 1);
     }
 
     // ---- join the warps: maxima and sums, then outputs through shared memory
