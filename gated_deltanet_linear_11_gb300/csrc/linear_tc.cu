@@ -16,7 +16,7 @@
 // output: P, and S where it multiplies Q.  The state itself never goes through them.
 //
 // linear_out_kernel: one CTA per (sequence range, v-head) walks its chunks with the state
-// in registers (64 floats a thread).  Warps 0-7 do the elementwise work, a thread holding
+// in registers (32 floats a thread).  Warps 0-7 do the elementwise work, a thread holding
 // one TMEM lane and half the columns: weighted keys (A), P (B), state (C), output (D);
 // warp 8 issues the products, warp 9 the tile loads, warp 10 the sums of the gates.  Seven
 // 32 KB tiles (Q, K, V, hi, lo, S, P) leave room for one buffer each; the order A B C D
@@ -44,7 +44,7 @@ namespace gdn {
 constexpr int kLinC = 128;                 // tokens per chunk
 constexpr uint32_t kTile = 32768;          // one 128 x 128 bf16 tile: two 64-column blocks
 constexpr uint32_t kBlk = 16384;
-constexpr int kLinWarps = 8;               // warps that do elementwise work
+constexpr int kLinWarps = 16;              // warps that do elementwise work
 constexpr int kLinThreads = 32 * (kLinWarps + 3);
 constexpr int kMinSplitChunks = 12;        // shorter sequences are one range
 constexpr int kMinRangeChunks = 4;
@@ -90,10 +90,10 @@ __device__ __forceinline__ int64_t range_slot0(const LinParams &p, int n, int t0
 // ------------------------------------------------------------------------ shared memory
 
 struct LinBars {
-    uint64_t q, k, v[2];                 // tiles loaded
+    uint64_t q, k[3], v[2];              // tiles loaded
     uint64_t qk, qs, kv[2], pv;          // products done
     uint64_t gates;                      // this chunk's gate arrays are written
-    uint64_t r_kt[2], r_p, r_s, r_o, r_arr;   // eight warps: operands written, arrays read
+    uint64_t r_kt[2], r_p, r_s, r_o, r_arr;   // every elementwise warp: operands written, arrays read
     uint64_t fin;
 };
 struct LinSmem {
@@ -120,6 +120,25 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(tc::smem_u32(bar)) : "memory");
+}
+
+// Two fp32 operations in one instruction, rounded like the single ones.
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<unsigned long long *>(&d))
+        : "l"(*reinterpret_cast<const unsigned long long *>(&a)),
+          "l"(*reinterpret_cast<const unsigned long long *>(&b)));
+    return d;
+}
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(*reinterpret_cast<unsigned long long *>(&d))
+        : "l"(*reinterpret_cast<const unsigned long long *>(&a)),
+          "l"(*reinterpret_cast<const unsigned long long *>(&b)),
+          "l"(*reinterpret_cast<const unsigned long long *>(&c)));
+    return d;
 }
 
 // Bounded wait on an mbarrier phase.  Gives up when the bound has passed or another thread
@@ -214,15 +233,16 @@ __device__ __forceinline__ float lanes_above(float x) {
 }
 
 // --------------------------------------------------------------- weighted keys (phase A)
-// hi, lo <- bf16 pair of w_j k_j for rows j < L, zero rows after.  A quarter warp takes the
-// eight 16-byte chunks of a row.
+// hi, lo <- bf16 pair of w_j k_j for rows j < L, zero rows after (hi may be k).  A quarter
+// warp takes the eight 16-byte chunks of a row.
 __device__ __forceinline__ void weigh_keys(const uint8_t *k, uint8_t *hi, uint8_t *lo, const float *w,
                                            int L) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = lane & 7;
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int row = 32 * it + 4 * warp + (lane >> 3);
+    for (int it = 0; it < 128 / (4 * kLinWarps); ++it) {
+        const int row = 4 * kLinWarps * it + 4 * warp + (lane >> 3);
         const float wj = w[row];
+        const float2 w2 = make_float2(wj, wj), m1 = make_float2(-1.f, -1.f);
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
             const uint32_t at = kb * kBlk + tc::swz(row, ch);
@@ -231,11 +251,16 @@ __device__ __forceinline__ void weigh_keys(const uint8_t *k, uint8_t *hi, uint8_
             uint32_t h[4], r[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float a = __uint_as_float(uw[e] << 16) * wj;
-                const float b = __uint_as_float(uw[e] & 0xffff0000u) * wj;
-                h[e] = pack_bf2(a, b);
-                r[e] = pack_bf2(a - __uint_as_float(h[e] << 16), b - __uint_as_float(h[e] & 0xffff0000u));
-                if (row >= L) h[e] = r[e] = 0u;
+                const float2 x = mul_f32x2(
+                    make_float2(__uint_as_float(uw[e] << 16), __uint_as_float(uw[e] & 0xffff0000u)), w2);
+                h[e] = pack_bf2(x.x, x.y);
+                const float2 d = fma_f32x2(
+                    make_float2(__uint_as_float(h[e] << 16), __uint_as_float(h[e] & 0xffff0000u)), m1, x);
+                r[e] = pack_bf2(d.x, d.y);
+            }
+            if (L < kLinC && row >= L) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[e] = r[e] = 0u;
             }
             *reinterpret_cast<uint4 *>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
             *reinterpret_cast<uint4 *>(lo + at) = make_uint4(r[0], r[1], r[2], r[3]);
@@ -247,16 +272,17 @@ __device__ __forceinline__ void weigh_keys(const uint8_t *k, uint8_t *hi, uint8_
 __device__ __forceinline__ void clear_rows(uint8_t *tile, int L) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = lane & 7;
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int row = 32 * it + 4 * warp + (lane >> 3);
+    for (int it = 0; it < 128 / (4 * kLinWarps); ++it) {
+        const int row = 4 * kLinWarps * it + 4 * warp + (lane >> 3);
         if (row < L) continue;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
             *reinterpret_cast<uint4 *>(tile + kb * kBlk + tc::swz(row, ch)) = make_uint4(0, 0, 0, 0);
     }
 }
-// 64 floats of one row as bf16 into block `blk` of a tile.
-__device__ __forceinline__ void store_row(uint8_t *tile, int blk, int row, const float *v, int n0) {
+// 32 floats of one row as bf16 into columns 32 quarter .. of a tile.
+__device__ __forceinline__ void store_row(uint8_t *tile, int quarter, int row, const float (&v)[32]) {
+    const int blk = quarter >> 1, n0 = 32 * (quarter & 1);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         uint4 u;
@@ -298,7 +324,7 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     if (tid == 0) {
         S.abort = 0;
         LinBars &b = S.bar;
-        for (uint64_t *x : {&b.q, &b.k, &b.v[0], &b.qk, &b.qs, &b.kv[0], &b.pv, &b.gates, &b.fin})
+        for (uint64_t *x : {&b.q, &b.k[0], &b.v[0], &b.qk, &b.qs, &b.kv[0], &b.pv, &b.gates, &b.fin})
             tc::mbar_init(x, 1);
         for (uint64_t *x : {&b.r_kt[0], &b.r_p, &b.r_s, &b.r_o, &b.r_arr}) tc::mbar_init(x, kLinWarps);
         tc::mbar_fence_init();
@@ -309,11 +335,11 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     const uint32_t tmem = S.tmem;
 
     if (warp < kLinWarps) {
-        const int lq = warp & 3, hf = warp >> 2;
+        const int lq = warp & 3, jb = warp >> 2;    // rows 32 lq .., columns 32 jb ..
         const int row = 32 * lq + lane;
-        const uint32_t lane_off = (uint32_t)(32 * lq) << 16;
-        const int64_t st_off = (int64_t)row * 128 + 64 * hf;
-        float st[64];
+        const uint32_t tm = tmem + ((uint32_t)(32 * lq) << 16) + 32 * jb;
+        const int64_t st_off = (int64_t)row * 128 + 32 * jb;
+        float st[32];
         const float *src = nullptr;
         if (range > 0 || (p.in_place && rc < nch)) {
             grid_dependency_wait();
@@ -322,14 +348,13 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             src = p.h0 + ((int64_t)n * p.Hv + hv) * 16384;
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
+        for (int e = 0; e < 8; ++e) {
             const float4 x = src ? reinterpret_cast<const float4 *>(src + st_off)[e]
                                  : make_float4(0.f, 0.f, 0.f, 0.f);
             st[4 * e] = x.x; st[4 * e + 1] = x.y; st[4 * e + 2] = x.z; st[4 * e + 3] = x.w;
         }
         if (count > 0) {
-            store_row(sS, hf, row, st, 0);
-            store_row(sS, hf, row, st + 32, 32);
+            store_row(sS, jb, row, st);
             warp_arrive(&S.bar.r_s);
         }
         for (int i = 0; i < count; ++i) {
@@ -337,7 +362,7 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             const int t = t0 + (c_first + i) * kLinC;
             const int L = min(kLinC, t0 + len - t);
             // ---- A: weighted keys
-            if (!warp_wait(S, &S.bar.gates, ph) || !warp_wait(S, &S.bar.k, ph)) break;
+            if (!warp_wait(S, &S.bar.gates, ph) || !warp_wait(S, &S.bar.k[0], ph)) break;
             weigh_keys(sK, sHi, sLo, S.w, L);
             if (L < kLinC) {
                 if (!warp_wait(S, &S.bar.v[0], ph)) break;
@@ -347,79 +372,85 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             // ---- B: P = decay-weighted lower triangle of Q K^T
             if (!warp_wait(S, &S.bar.qk, ph)) break;
             tc::fence_after_sync();
-            const float gi = S.g2[row], eg = S.eg[row], decay = S.decay;
+            const float eg = S.eg[row], decay = S.decay;
+            float v[32];
+            if (jb <= lq) {
+                const float gi = S.g2[row];
+                tc::tmem_ld32(tm + colSc, v);
+                if (jb < lq) {
+                    const float f = p.scale * ex2(gi - S.ref[jb]);
+                    float4 b4[8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int jb = 2 * hf + h;       // columns 32 jb ..
-                float v[32];
-                if (jb <= lq) {
-                    tc::tmem_ld32(tmem + lane_off + colSc + 32 * jb, v);
+                    for (int j = 0; j < 8; ++j) b4[j] = reinterpret_cast<const float4 *>(S.b)[8 * jb + j];
                     tc::tmem_wait_ld();
-                    if (jb < lq) {
-                        const float f = p.scale * ex2(gi - S.ref[jb]);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] *= f * S.b[32 * jb + j];
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = j <= lane ? v[j] * (p.scale * ex2(gi - S.g2[32 * jb + j])) : 0.f;
+                    for (int j = 0; j < 8; ++j) {
+                        v[4 * j] *= f * b4[j].x;
+                        v[4 * j + 1] *= f * b4[j].y;
+                        v[4 * j + 2] *= f * b4[j].z;
+                        v[4 * j + 3] *= f * b4[j].w;
                     }
                 } else {
+                    float w[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                    for (int j = 0; j < 32; ++j) w[j] = p.scale * ex2(gi - S.g2[32 * jb + j]);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = j <= lane ? v[j] * w[j] : 0.f;
                 }
-                store_row(sP, hf, row, v, 32 * h);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0.f;
             }
+            store_row(sP, jb, row, v);
             warp_arrive(&S.bar.r_p);
             if (lane == 0) mbar_arrive(&S.bar.r_arr);
             // ---- C: state
             if (!warp_wait(S, &S.bar.kv[0], ph)) break;
             tc::fence_after_sync();
+            tc::tmem_ld32(tm + colD, v);
+            tc::tmem_wait_ld();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float v[32];
-                tc::tmem_ld32(tmem + lane_off + colD + 64 * hf + 32 * h, v);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 32; ++j) st[32 * h + j] = fmaf(decay, st[32 * h + j], v[j]);
-            }
+            for (int j = 0; j < 32; ++j) st[j] = fmaf(decay, st[j], v[j]);
             if (!warp_wait(S, &S.bar.qs, ph)) break;
-            store_row(sS, hf, row, st, 0);
-            store_row(sS, hf, row, st + 32, 32);
+            store_row(sS, jb, row, st);
             warp_arrive(&S.bar.r_s);
-            // ---- D: output
+            // ---- D: output, through this warp's own part of the P tile (PV has read it), so
+            // that a row's 64 bytes leave as full sectors
             if (!warp_wait(S, &S.bar.pv, ph)) break;
             tc::fence_after_sync();
-            uint4 *dst = reinterpret_cast<uint4 *>(p.o + (int64_t)(t + row) * p.o_tok + (int64_t)hv * 128 + 64 * hf);
+            float a[32];
+            tc::tmem_ld32(tm + colOi, a);
+            tc::tmem_ld32(tm + colOa, v);
+            tc::tmem_wait_ld();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.bar.r_o);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float a[32], b[32];
-                tc::tmem_ld32(tmem + lane_off + colOi + 64 * hf + 32 * h, a);
-                tc::tmem_ld32(tmem + lane_off + colOa + 64 * hf + 32 * h, b);
-                tc::tmem_wait_ld();
-                if (row < L) {
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(eg, a[j], v[j]);
+            store_row(sP, jb, row, v);
+            __syncwarp();
+            bf16 *dst = p.o + (int64_t)(t + 32 * lq) * p.o_tok + (int64_t)hv * 128 + 32 * jb;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float f[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = fmaf(eg, a[8 * c + e], b[8 * c + e]);
-                        dst[4 * h + c] = pack8(f);
-                    }
-                }
+            for (int x = 0; x < 4; ++x) {
+                const int rr = 8 * x + (lane >> 2), cc = lane & 3;
+                const uint4 u = *reinterpret_cast<const uint4 *>(
+                    sP + (jb >> 1) * kBlk + tc::swz(32 * lq + rr, 4 * (jb & 1) + cc));
+                if (32 * lq + rr < L) reinterpret_cast<uint4 *>(dst + rr * p.o_tok)[cc] = u;
             }
-            warp_arrive(&S.bar.r_o);
+            __syncwarp();
         }
         if (last && p.hT && !*(volatile int *)&S.abort) {
             float4 *out = reinterpret_cast<float4 *>(p.hT + ((int64_t)n * p.Hv + hv) * 16384 + st_off);
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < 8; ++e)
                 out[e] = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
         }
     } else if (warp == kLinWarps) {
         // ---- products
         for (int i = 0; i < count; ++i) {
             const uint32_t ph = i & 1;
-            if (!warp_wait(S, &S.bar.q, ph) || !warp_wait(S, &S.bar.k, ph)) break;
+            if (!warp_wait(S, &S.bar.q, ph) || !warp_wait(S, &S.bar.k[0], ph)) break;
             tc::fence_after_sync();
             product<0, 0>(tmem + colSc, sQ, sK, false);
             tc::mma_commit_warp(&S.bar.qk);
@@ -452,14 +483,14 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                 const uint32_t pp = (i & 1) ^ 1;
                 const int t = t0 + (c_first + i) * kLinC;
                 if (i > 0 && (!lin_wait(S, &S.bar.qk, pp) || !lin_wait(S, &S.bar.r_kt[0], pp))) break;
-                load_tile(sK, &maps.k, &S.bar.k, hk, t);
+                load_tile(sK, &maps.k, &S.bar.k[0], hk, t);
                 if (i > 0 && !lin_wait(S, &S.bar.qs, pp)) {
-                    wait_copy(&S.bar.k, i & 1);
+                    wait_copy(&S.bar.k[0], i & 1);
                     break;
                 }
                 load_tile(sQ, &maps.q, &S.bar.q, hk, t);
                 if (i > 0 && (!lin_wait(S, &S.bar.kv[0], pp) || !lin_wait(S, &S.bar.pv, pp))) {
-                    wait_copy(&S.bar.k, i & 1);
+                    wait_copy(&S.bar.k[0], i & 1);
                     wait_copy(&S.bar.q, i & 1);
                     break;
                 }
@@ -468,7 +499,7 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             }
             if (loads > 0) {
                 // (bounded) everything loaded has landed
-                wait_copy(&S.bar.k, (loads - 1) & 1);
+                wait_copy(&S.bar.k[0], (loads - 1) & 1);
                 wait_copy(&S.bar.q, (loads - 1) & 1);
                 wait_copy(&S.bar.v[0], (loads - 1) & 1);
             }
@@ -519,7 +550,7 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
 // -------------------------------------------------------------------------- range states
 // State that one range adds, from zero, with decays to the range's end: its chunks in
 // reverse, each chunk's weights carrying the sum of the later ones, all added up in TMEM.
-// Tiles: K, V x 2, (hi, lo) x 2.
+// Tiles: K x 3 (hi replaces K in place), lo x 2, V x 2; the products bound it.
 __global__ void __launch_bounds__(kLinThreads, 1)
 linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -528,7 +559,6 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         if (threadIdx.x == 0) report(p.status, GDN_ERR_CUDA);
         return;
     }
-    uint8_t *sK = S.tile[0];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int range = blockIdx.x, hv = blockIdx.y, n = blockIdx.z, hk = hv / (p.Hv / p.Hk);
     const int t0 = p.cu[n], len = p.cu[n + 1] - t0;
@@ -545,7 +575,7 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     if (tid == 0) {
         S.abort = 0;
         LinBars &b = S.bar;
-        for (uint64_t *x : {&b.k, &b.v[0], &b.v[1], &b.kv[0], &b.kv[1], &b.gates, &b.fin})
+        for (uint64_t *x : {&b.k[0], &b.k[1], &b.k[2], &b.v[0], &b.v[1], &b.kv[0], &b.kv[1], &b.gates, &b.fin})
             tc::mbar_init(x, 1);
         for (uint64_t *x : {&b.r_kt[0], &b.r_kt[1], &b.r_arr}) tc::mbar_init(x, kLinWarps);
         tc::mbar_fence_init();
@@ -554,60 +584,62 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = S.tmem;
-    // step i takes chunk c_first + count - 1 - i; buffers alternate, so step i's use of
-    // buffer i & 1 is its (i >> 1)-th
+    // step i takes chunk c_first + count - 1 - i; its use of a buffer among two is that
+    // buffer's (i >> 1)-th, among three its (i / 3)-th
     if (warp < kLinWarps) {
         bool ok = true;
         for (int i = 0; i < count && ok; ++i) {
-            const int bf = i & 1;
-            if (!(ok = warp_wait(S, &S.bar.gates, i & 1) && warp_wait(S, &S.bar.k, i & 1))) break;
+            const int bf = i & 1, kb = i % 3;
+            if (!(ok = warp_wait(S, &S.bar.gates, i & 1) && warp_wait(S, &S.bar.k[kb], (i / 3) & 1))) break;
             if (i >= 2 && !(ok = warp_wait(S, &S.bar.kv[bf], ((i >> 1) & 1) ^ 1))) break;
-            weigh_keys(sK, S.tile[3 + 2 * bf], S.tile[4 + 2 * bf], S.w, kLinC);
+            weigh_keys(S.tile[kb], S.tile[kb], S.tile[3 + bf], S.w, kLinC);
             warp_arrive(&S.bar.r_kt[bf]);
             if (lane == 0) mbar_arrive(&S.bar.r_arr);
         }
         const int e = count - 1;
         if (ok && warp_wait(S, &S.bar.kv[e & 1], (e >> 1) & 1)) {
             tc::fence_after_sync();
-            const int lq = warp & 3, hf = warp >> 2;
-            float4 *out = reinterpret_cast<float4 *>(p.ranges + slot * 16384 + (32 * lq + lane) * 128 + 64 * hf);
+            const int lq = warp & 3, jb = warp >> 2;
+            float4 *out = reinterpret_cast<float4 *>(p.ranges + slot * 16384 + (32 * lq + lane) * 128 + 32 * jb);
+            float v[32];
+            tc::tmem_ld32(tmem + ((uint32_t)(32 * lq) << 16) + 32 * jb, v);
+            tc::tmem_wait_ld();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float v[32];
-                tc::tmem_ld32(tmem + ((uint32_t)(32 * lq) << 16) + 64 * hf + 32 * h, v);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    out[8 * h + x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-            }
+            for (int x = 0; x < 8; ++x)
+                out[x] = make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
         }
     } else if (warp == kLinWarps) {
         for (int i = 0; i < count; ++i) {
             const int bf = i & 1;
             if (!warp_wait(S, &S.bar.r_kt[bf], (i >> 1) & 1) || !warp_wait(S, &S.bar.v[bf], (i >> 1) & 1)) break;
             tc::fence_after_sync();
-            product<1, 1>(tmem, S.tile[3 + 2 * bf], S.tile[1 + bf], i > 0);
-            product<1, 1>(tmem, S.tile[4 + 2 * bf], S.tile[1 + bf], true);
+            product<1, 1>(tmem, S.tile[i % 3], S.tile[5 + bf], i > 0);
+            product<1, 1>(tmem, S.tile[3 + bf], S.tile[5 + bf], true);
             tc::mma_commit_warp(&S.bar.kv[bf]);
         }
         tc::mma_commit_warp(&S.bar.fin);
         wait_copy(&S.bar.fin, 0);
     } else if (warp == kLinWarps + 1) {
         if (lane == 0) {
-            int loads = 0;
-            for (int i = 0; i < count; ++i) {
-                const int bf = i & 1, t = t0 + (c_first + count - 1 - i) * kLinC;
-                if (i > 0 && !lin_wait(S, &S.bar.r_kt[bf ^ 1], ((i - 1) >> 1) & 1)) break;
-                load_tile(sK, &maps.k, &S.bar.k, hk, t);
-                if (i >= 2 && !lin_wait(S, &S.bar.kv[bf], ((i >> 1) & 1) ^ 1)) {
-                    wait_copy(&S.bar.k, i & 1);
-                    break;
-                }
-                load_tile(S.tile[1 + bf], &maps.v, &S.bar.v[bf], hv, t);
-                ++loads;
+            // K of step i goes where step i - 3 was, V where step i - 2 was; K is asked for
+            // a step ahead of V
+            int ks = 0, vs = 0;
+            auto load_k = [&](int i) {
+                if (i >= 3 && !lin_wait(S, &S.bar.kv[(i - 3) & 1], ((i - 3) >> 1) & 1)) return false;
+                load_tile(S.tile[i % 3], &maps.k, &S.bar.k[i % 3], hk, t0 + (c_first + count - 1 - i) * kLinC);
+                ++ks;
+                return true;
+            };
+            bool ok = load_k(0);
+            for (int i = 0; i < count && ok; ++i) {
+                if (i + 1 < count && !(ok = load_k(i + 1))) break;
+                if (i >= 2 && !(ok = lin_wait(S, &S.bar.kv[i & 1], ((i >> 1) & 1) ^ 1))) break;
+                load_tile(S.tile[5 + (i & 1)], &maps.v, &S.bar.v[i & 1], hv,
+                          t0 + (c_first + count - 1 - i) * kLinC);
+                ++vs;
             }
-            if (loads > 0) wait_copy(&S.bar.k, (loads - 1) & 1);
-            for (int x = std::max(0, loads - 2); x < loads; ++x) wait_copy(&S.bar.v[x & 1], (x >> 1) & 1);
+            for (int x = max(0, ks - 3); x < ks; ++x) wait_copy(&S.bar.k[x % 3], (x / 3) & 1);
+            for (int x = max(0, vs - 2); x < vs; ++x) wait_copy(&S.bar.v[x & 1], (x >> 1) & 1);
         }
     } else {
         float x[4], carry = 0.f;
