@@ -414,9 +414,60 @@ def gdn_layer_decode(x_qkv, conv_w, conv_bias, g, beta, conv_state, state, Hk, H
                                 status)
 
 
+# The entries below are called once per layer and token, so their host side is kept short:
+# descriptors are filled in one go, pointers go to ctypes as plain integers and offsets that
+# are already int32 on the right device are used as they are.
+
+_PACK = _lib.GDN_TENSOR_PACK.pack
+# os.environ without its per-lookup key encoding: most calls find neither variable set
+_ENV = getattr(os.environ, "_data", os.environ)
+_ENV_FORCE, _ENV_DEBUG = (getattr(os.environ, "encodekey", str)(x)
+                          for x in ("GDN_FORCE_ERROR", "GDN_DEBUG"))
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _entry(name):
+    """What every call starts with: forced errors, the library, the debug flags."""
+    if _ENV_FORCE in _ENV:
+        _forced(name)
+    return _lib.load(), _debug_flags() if _ENV_DEBUG in _ENV else 0
+
+
+def _view(t):
+    """gdn_tensor_t of an activation view (as _desc), packed."""
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        raise TypeError("activations must be bf16 or fp32, got %s" % t.dtype)
+    if t.dim() == 3:
+        a, b, c = t.shape
+        x, y, z = t.stride()
+        return _PACK(t.data_ptr(), 3, dt, a, b, c, 0, x, y, z, 0)
+    if t.dim() == 4:
+        return _PACK(t.data_ptr(), 4, dt, *t.shape, *t.stride())
+    raise ValueError("activations must be [T,H,D] or [1,T,H,D]")
+
+
+def _raw_stream(t):
+    """The current stream of t's device, as the integer that ctypes passes on."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _offsets(cu_seqlens, cu_seqlens_host):
+    """_seqlens without conversions where none are needed."""
+    if cu_seqlens_host is not None and cu_seqlens_host.dtype is torch.int32 and \
+            cu_seqlens.dtype is torch.int32 and cu_seqlens.is_cuda and \
+            cu_seqlens.is_contiguous() and cu_seqlens_host.is_contiguous() and \
+            not cu_seqlens_host.is_cuda:
+        return cu_seqlens, cu_seqlens_host
+    return _seqlens(cu_seqlens, cu_seqlens_host)
+
+
 def _gates(g, T, Hv):
     """(contiguous fp32 log decays, per-token flag) of g [Hv] or [T, Hv]."""
-    if g.dtype != torch.float32:
+    if g.dtype is not torch.float32:
         raise TypeError("g must be fp32, got %s" % g.dtype)
     if g.dim() == 1 and g.shape[0] == Hv:
         return g.contiguous(), 0
@@ -426,9 +477,21 @@ def _gates(g, T, Hv):
 
 
 def _states(name, t, shape):
-    if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or
-                          tuple(t.shape) != tuple(shape)):
+    if t is not None and (t.dtype is not torch.float32 or t.shape != shape or
+                          not t.is_contiguous()):
         raise ValueError("%s must be a contiguous fp32 tensor of shape %s" % (name, tuple(shape)))
+
+
+def _int32(name, t, shape):
+    if t is not None and (t.dtype is not torch.int32 or t.shape != shape or
+                          not t.is_contiguous()):
+        raise ValueError("%s must be a contiguous int32 tensor of shape %s" % (name, tuple(shape)))
+
+
+def _scratch(workspace, size, like):
+    if size and (workspace is None or workspace.numel() * workspace.element_size() < size):
+        return torch.empty(size, dtype=torch.uint8, device=like.device)
+    return workspace
 
 
 def gdn_linear_prefill_workspace_size(cu_seqlens_host, T, Hk, Hv, D, dtype=torch.bfloat16,
@@ -437,7 +500,7 @@ def gdn_linear_prefill_workspace_size(cu_seqlens_host, T, Hk, Hv, D, dtype=torch
     lib = _lib.load()
     cu_h = cu_seqlens_host.to(torch.int32).contiguous()
     return int(lib.gdn_linear_prefill_workspace_size(
-        ctypes.c_void_p(cu_h.data_ptr()), cu_h.numel() - 1, T, Hk, Hv, D, _DT[dtype],
+        cu_h.data_ptr(), cu_h.numel() - 1, T, Hk, Hv, D, _DT[dtype],
         GDN_PREFILL_SIMT if simt else 0))
 
 
@@ -450,10 +513,9 @@ def gdn_linear_prefill(q, k, v, g, cu_seqlens, scale=1.0, initial_state=None,
     q, k [T, Hk, D]; v [T, Hv, D], all bf16 or all fp32 (token-major views); g fp32 log
     decays, [Hv] or [T, Hv]; cu_seqlens [N+1]; initial_state [N, Hv, D, D] fp32 or None.
     """
-    _forced("gdn_linear_prefill")
-    lib = _lib.load()
+    lib, debug = _entry("gdn_linear_prefill")
     _need_cuda(q, k, v, g, initial_state, o, final_state, workspace, status)
-    cu, cu_h = _seqlens(cu_seqlens, cu_seqlens_host)
+    cu, cu_h = _offsets(cu_seqlens, cu_seqlens_host)
     N = cu_h.numel() - 1
     T, Hk, D = q.shape[-3:]
     Hv = v.shape[-2]
@@ -464,39 +526,38 @@ def gdn_linear_prefill(q, k, v, g, cu_seqlens, scale=1.0, initial_state=None,
         o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
     if final_state is None and output_final_state:
         final_state = torch.empty((N, Hv, D, D), dtype=torch.float32, device=q.device)
-    flags = (GDN_PREFILL_SIMT if simt else 0) | _debug_flags()
-    dq, dk_, dv_, do = _desc(q), _desc(k), _desc(v), _desc(o)
-    ws_bytes = int(lib.gdn_linear_prefill_workspace_size(
-        ctypes.c_void_p(cu_h.data_ptr()), N, T, Hk, Hv, D, dv_.dtype, flags))
-    if ws_bytes and (workspace is None or workspace.numel() * workspace.element_size() < ws_bytes):
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    rc = lib.gdn_linear_prefill(
-        ctypes.byref(dq), ctypes.byref(dk_), ctypes.byref(dv_), _vp(g), per_token, _vp(cu),
-        ctypes.c_void_p(cu_h.data_ptr()), N, float(scale), flags, _vp(initial_state),
-        ctypes.byref(do), _vp(final_state), _vp(workspace), ws_bytes, _vp(status), _stream())
-    _lib.check(rc, "gdn_linear_prefill")
+    flags = (GDN_PREFILL_SIMT if simt else 0) | debug
+    cu_hp = cu_h.data_ptr()
+    ws_bytes = lib.gdn_linear_prefill_workspace_size(cu_hp, N, T, Hk, Hv, D,
+                                                     _DT.get(v.dtype, 0), flags)
+    workspace = _scratch(workspace, ws_bytes, q)
+    rc = lib.gdn_linear_prefill(_view(q), _view(k), _view(v), g.data_ptr(), per_token,
+                                cu.data_ptr(), cu_hp, N, scale, flags, _ptr(initial_state),
+                                _view(o), _ptr(final_state), _ptr(workspace), ws_bytes,
+                                _ptr(status), _raw_stream(q))
+    if rc:
+        _lib.check(rc, "gdn_linear_prefill")
     return o, final_state
 
 
 def gdn_linear_decode(q, k, v, g, state, state_idx=None, scale=1.0, o=None, status=None):
     """One token per sequence of gdn_linear_prefill's recurrence; state [P, Hv, D, D] fp32
     updated in place.  g [Hv] or [N, Hv].  Returns o."""
-    _forced("gdn_linear_decode")
-    lib = _lib.load()
+    lib, debug = _entry("gdn_linear_decode")
     _need_cuda(q, k, v, g, state, state_idx, o, status)
     N, _, D = q.shape[-3:]
     Hv = v.shape[-2]
     g, per_token = _gates(g, N, Hv)
-    _states("state", state, (state.shape[0], Hv, D, D))
-    state_idx = _int32("state_idx", state_idx, (N,))
+    P = state.shape[0]
+    _states("state", state, (P, Hv, D, D))
+    _int32("state_idx", state_idx, (N,))
     if o is None:
         o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-    dq, dk_, dv_, do = _desc(q), _desc(k), _desc(v), _desc(o)
-    rc = lib.gdn_linear_decode(
-        ctypes.byref(dq), ctypes.byref(dk_), ctypes.byref(dv_), _vp(g), per_token, _vp(state),
-        state.shape[0], _vp(state_idx), float(scale), _debug_flags(), ctypes.byref(do),
-        _vp(status), _stream())
-    _lib.check(rc, "gdn_linear_decode")
+    rc = lib.gdn_linear_decode(_view(q), _view(k), _view(v), g.data_ptr(), per_token,
+                               state.data_ptr(), P, _ptr(state_idx), scale, debug,
+                               _view(o), _ptr(status), _raw_stream(q))
+    if rc:
+        _lib.check(rc, "gdn_linear_decode")
     return o
 
 
@@ -509,42 +570,34 @@ def gdn_kv_cache(pages, page_size, Hkv, head_dim, device="cuda"):
     return torch.zeros((pages, 2, Hkv, page_size, rec), dtype=torch.uint8, device=device)
 
 
-def _int32(name, t, shape):
-    if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or
-                          tuple(t.shape) != tuple(shape)):
-        raise ValueError("%s must be a contiguous int32 tensor of shape %s" % (name, tuple(shape)))
-    return t
-
-
 def _kv_cache(cache, block_table, kv_lens, head_dim):
-    """The C descriptor of a cache tensor with its table and lengths."""
-    if cache.dtype != torch.uint8 or cache.dim() != 5 or not cache.is_contiguous():
+    """(N, Hkv, packed gdn_kv_cache_t) of a cache tensor with its table and lengths."""
+    if cache.dtype is not torch.uint8 or cache.dim() != 5 or not cache.is_contiguous():
         raise ValueError("cache must be a contiguous uint8 tensor of five dimensions")
-    if cache.shape[1] != 2 or cache.shape[4] != _lib.load().gdn_kv_record_bytes(head_dim):
+    pages, two, Hkv, page, rec = cache.shape
+    if two != 2 or rec != head_dim // 2 + head_dim // 8:
         raise ValueError("cache of shape %s does not hold keys and values of head_dim %d"
                          % (tuple(cache.shape), head_dim))
     if block_table.dim() != 2:
         raise ValueError("block_table must be [N, pages of a sequence]")
-    N = block_table.shape[0]
-    _int32("block_table", block_table, (N, block_table.shape[1]))
+    N, width = block_table.shape
+    _int32("block_table", block_table, (N, width))
     _int32("kv_lens", kv_lens, (N,))
-    c = _lib.GdnKvCache()
-    c.data, c.block_table, c.kv_lens = cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr()
-    c.pages, c.Hkv, c.page_size = cache.shape[0], cache.shape[2], cache.shape[3]
-    c.head_dim, c.table_width, c.N = head_dim, block_table.shape[1], N
-    return c
+    return N, Hkv, _lib.GDN_KV_CACHE_PACK.pack(
+        cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(), pages, page, Hkv,
+        head_dim, width, N)
 
 
 def _kv_offsets(cu_seqlens, cu_seqlens_host, T, N):
-    """Device and host offsets of the new tokens as pointers (None: one per sequence)."""
+    """Device and host offsets of the new tokens (None, None: one per sequence)."""
     if cu_seqlens is None:
         if T != N:
             raise ValueError("%d new tokens for %d sequences need cu_seqlens" % (T, N))
-        return None, None, None, None
-    cu, cu_h = _seqlens(cu_seqlens, cu_seqlens_host)
+        return None, None
+    cu, cu_h = _offsets(cu_seqlens, cu_seqlens_host)
     if cu_h.numel() != N + 1 or cu.numel() != N + 1:
         raise ValueError("cu_seqlens must have %d entries" % (N + 1))
-    return cu, cu_h, _vp(cu), ctypes.c_void_p(cu_h.data_ptr())
+    return cu, cu_h
 
 
 def gdn_kv_append(k, v, cache, block_table, kv_lens, cu_seqlens=None, cos=None, sin=None,
@@ -557,31 +610,30 @@ def gdn_kv_append(k, v, cache, block_table, kv_lens, cu_seqlens=None, cos=None, 
     offsets of the new tokens, or None for one per sequence; cos, sin fp32
     [positions, rot / 2] or None for no rotation (rot = twice their width).
     """
-    _forced("gdn_kv_append")
-    lib = _lib.load()
+    lib, debug = _entry("gdn_kv_append")
     _need_cuda(k, v, cache, block_table, kv_lens, cos, sin, q, q_out, status)
-    T, Hkv, D = k.shape[-3:]
-    c = _kv_cache(cache, block_table, kv_lens, D)
-    cu, cu_h, cu_p, cu_hp = _kv_offsets(cu_seqlens, cu_seqlens_host, T, c.N)
+    T, _, D = k.shape[-3:]
+    N, Hkv, c = _kv_cache(cache, block_table, kv_lens, D)
+    cu, cu_h = _kv_offsets(cu_seqlens, cu_seqlens_host, T, N)
     rows = rot = 0
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
     if cos is not None:
-        for t in (cos, sin):
-            if t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous() or \
-                    t.shape != cos.shape:
-                raise ValueError("cos and sin must be contiguous fp32 [positions, rot / 2]")
+        if cos.dtype is not torch.float32 or sin.dtype is not torch.float32 or cos.dim() != 2 or \
+                cos.shape != sin.shape or not cos.is_contiguous() or not sin.is_contiguous():
+            raise ValueError("cos and sin must be contiguous fp32 [positions, rot / 2]")
         rows, rot = cos.shape[0], 2 * cos.shape[1]
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk_, dv_ = _desc(k), _desc(v)
-    dq, do = (None, None) if q is None else (_desc(q), _desc(q_out))
-    rc = lib.gdn_kv_append(
-        ctypes.byref(c), cu_p, cu_hp, ctypes.byref(dk_), ctypes.byref(dv_),
-        None if dq is None else ctypes.byref(dq), None if do is None else ctypes.byref(do),
-        _vp(cos), _vp(sin), rows, rot,
-        (GDN_KV_INTERLEAVED if interleaved else 0) | _debug_flags(), _vp(status), _stream())
-    _lib.check(rc, "gdn_kv_append")
+    dq = do = None
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dq, do = _view(q), _view(q_out)
+    rc = lib.gdn_kv_append(c, _ptr(cu), _ptr(cu_h), _view(k), _view(v), dq, do, _ptr(cos),
+                           _ptr(sin), rows, rot,
+                           (GDN_KV_INTERLEAVED if interleaved else 0) | debug,
+                           _ptr(status), _raw_stream(k))
+    if rc:
+        _lib.check(rc, "gdn_kv_append")
     return q_out
 
 
@@ -589,23 +641,19 @@ def gdn_kv_read(cache, block_table, kv_lens, cu_seqlens=None, head_dim=128,
                 dtype=torch.bfloat16, k=None, v=None, cu_seqlens_host=None, status=None):
     """The last tokens' keys and values (as many per sequence as cu_seqlens says; None:
     one) of a paged 4-bit cache, as values.  Returns (k, v), each [T, Hkv, head_dim]."""
-    _forced("gdn_kv_read")
-    lib = _lib.load()
+    lib, debug = _entry("gdn_kv_read")
     _need_cuda(cache, block_table, kv_lens, k, v, status)
-    c = _kv_cache(cache, block_table, kv_lens, head_dim)
-    if cu_seqlens is None:
-        T, cu, cu_h, cu_p, cu_hp = c.N, None, None, None, None
-    else:
-        cu, cu_h, cu_p, cu_hp = _kv_offsets(cu_seqlens, cu_seqlens_host, None, c.N)
-        T = int(cu_h[-1])
+    N, Hkv, c = _kv_cache(cache, block_table, kv_lens, head_dim)
+    cu, cu_h = _kv_offsets(cu_seqlens, cu_seqlens_host, N, N)
+    T = N if cu_h is None else int(cu_h[-1])
     if k is None:
-        k = torch.empty((T, c.Hkv, head_dim), dtype=dtype, device=cache.device)
+        k = torch.empty((T, Hkv, head_dim), dtype=dtype, device=cache.device)
     if v is None:
-        v = torch.empty((T, c.Hkv, head_dim), dtype=k.dtype, device=cache.device)
-    dk_, dv_ = _desc(k), _desc(v)
-    rc = lib.gdn_kv_read(ctypes.byref(c), cu_p, cu_hp, ctypes.byref(dk_), ctypes.byref(dv_),
-                         _debug_flags(), _vp(status), _stream())
-    _lib.check(rc, "gdn_kv_read")
+        v = torch.empty((T, Hkv, head_dim), dtype=k.dtype, device=cache.device)
+    rc = lib.gdn_kv_read(c, _ptr(cu), _ptr(cu_h), _view(k), _view(v), debug,
+                         _ptr(status), _raw_stream(cache))
+    if rc:
+        _lib.check(rc, "gdn_kv_read")
     return k, v
 
 
@@ -628,32 +676,35 @@ def gdn_kv_attention(q, cache, block_table, kv_lens, cu_seqlens=None, max_kv_len
     block_table can hold; a tighter one means a smaller grid and workspace); scale
     defaults to D^-1/2; lse: an fp32 [T, Hq] tensor that receives the log-sum-exp.
     """
-    _forced("gdn_kv_attention")
-    lib = _lib.load()
+    lib, debug = _entry("gdn_kv_attention")
     _need_cuda(q, cache, block_table, kv_lens, o, lse, workspace, status)
     T, Hq, D = q.shape[-3:]
-    c = _kv_cache(cache, block_table, kv_lens, D)
-    cu, cu_h, cu_p, cu_hp = _kv_offsets(cu_seqlens, cu_seqlens_host, T, c.N)
+    N, Hkv, c = _kv_cache(cache, block_table, kv_lens, D)
+    cu, cu_h = _kv_offsets(cu_seqlens, cu_seqlens_host, T, N)
     if max_kv_len is None:
-        max_kv_len = min(c.table_width * c.page_size, 0x7fffffff)
-    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or
-                            tuple(lse.shape) != (T, Hq)):
+        max_kv_len = min(block_table.shape[1] * cache.shape[3], 0x7fffffff)
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, Hq) or
+                            not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 tensor of shape [T, Hq]")
     if o is None:
         o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    flags = (GDN_PREFILL_SIMT if simt else 0) | _debug_flags()
-    dq, do = _desc(q), _desc(o)
-    max_q = 1 if cu_h is None else int((cu_h[1:] - cu_h[:-1]).max()) if c.N else 0
-    ws_bytes = int(lib.gdn_kv_attention_workspace_size(D, Hq, c.Hkv, T, c.N, max_q, max_kv_len,
-                                                       dq.dtype, flags))
-    if ws_bytes and (workspace is None or workspace.numel() * workspace.element_size() < ws_bytes):
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    rc = lib.gdn_kv_attention(
-        ctypes.byref(c), cu_p, cu_hp, int(max_kv_len), ctypes.byref(dq),
-        float(D ** -0.5 if scale is None else scale), flags, ctypes.byref(do), _vp(lse),
-        _vp(workspace), ws_bytes, _vp(status), _stream())
-    _lib.check(rc, "gdn_kv_attention")
+    flags = (GDN_PREFILL_SIMT if simt else 0) | debug
+    max_q = 1 if cu_h is None else T if N == 1 else _longest(cu_h)
+    dq = _view(q)
+    ws_bytes = lib.gdn_kv_attention_workspace_size(D, Hq, Hkv, T, N, max_q, max_kv_len,
+                                                   _DT[q.dtype], flags)
+    workspace = _scratch(workspace, ws_bytes, q)
+    rc = lib.gdn_kv_attention(c, _ptr(cu), _ptr(cu_h), max_kv_len, dq,
+                              D ** -0.5 if scale is None else scale, flags, _view(o), _ptr(lse),
+                              _ptr(workspace), ws_bytes, _ptr(status), _raw_stream(q))
+    if rc:
+        _lib.check(rc, "gdn_kv_attention")
     return o
+
+
+def _longest(cu_h):
+    cu = cu_h.tolist()
+    return max((b - a for a, b in zip(cu, cu[1:])), default=0)
 
 
 def gdn_selftest_bounded_wait(status=None):

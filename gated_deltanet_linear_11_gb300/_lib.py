@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libgdn.so")
@@ -52,6 +53,14 @@ class GdnKvCache(ctypes.Structure):
                 ("N", ctypes.c_int32)]
 
 
+# The same structures as struct formats: packing one is several times cheaper than filling
+# a ctypes.Structure.
+GDN_TENSOR_PACK = struct.Struct("@Pii4q4q")
+GDN_KV_CACHE_PACK = struct.Struct("@PPP6i")
+assert GDN_TENSOR_PACK.size == ctypes.sizeof(GdnTensor)
+assert GDN_KV_CACHE_PACK.size == ctypes.sizeof(GdnKvCache)
+
+
 class GdnError(RuntimeError):
     def __init__(self, code, where):
         self.code = code
@@ -73,7 +82,6 @@ def load(path: str = LIB_PATH):
     vp, i32, i64, u32, f32 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                               ctypes.c_uint32, ctypes.c_float)
     tp = ctypes.POINTER(GdnTensor)
-    cp = ctypes.POINTER(GdnKvCache)
     size = ctypes.c_size_t
     sig = {
         "gdn_status_string": ([i32], ctypes.c_char_p),
@@ -99,16 +107,17 @@ def load(path: str = LIB_PATH):
         "gdn_layer_prefill": ([vp, i64, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp, vp, vp,
                                vp, vp, f32, u32, vp, vp, vp, vp, ctypes.c_size_t, vp, vp,
                                vp], i32),
+        # descriptors may come as packed bytes (GDN_TENSOR_PACK, GDN_KV_CACHE_PACK)
         "gdn_linear_prefill_workspace_size": ([vp, i32, i64, i32, i32, i32, i32, u32], size),
-        "gdn_linear_prefill": ([tp, tp, tp, vp, i32, vp, vp, i32, f32, u32, vp, tp, vp, vp,
+        "gdn_linear_prefill": ([vp, vp, vp, vp, i32, vp, vp, i32, f32, u32, vp, vp, vp, vp,
                                 size, vp, vp], i32),
-        "gdn_linear_decode": ([tp, tp, tp, vp, i32, vp, i32, vp, f32, u32, tp, vp, vp], i32),
+        "gdn_linear_decode": ([vp, vp, vp, vp, i32, vp, i32, vp, f32, u32, vp, vp, vp], i32),
         "gdn_kv_record_bytes": ([i32], size),
-        "gdn_kv_append": ([cp, vp, vp, tp, tp, tp, tp, vp, vp, i32, i32, u32, vp, vp], i32),
-        "gdn_kv_read": ([cp, vp, vp, tp, tp, u32, vp, vp], i32),
+        "gdn_kv_append": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, u32, vp, vp], i32),
+        "gdn_kv_read": ([vp, vp, vp, vp, vp, u32, vp, vp], i32),
         "gdn_kv_attention_workspace_size": ([i32, i32, i32, i64, i32, i32, i32, i32, u32],
                                             size),
-        "gdn_kv_attention": ([cp, vp, vp, i32, tp, f32, u32, tp, vp, vp, size, vp, vp], i32),
+        "gdn_kv_attention": ([vp, vp, vp, i32, vp, f32, u32, vp, vp, vp, size, vp, vp], i32),
         "gdn_selftest_bounded_wait": ([vp, vp], i32),
     }
     for name, (args, res) in sig.items():
