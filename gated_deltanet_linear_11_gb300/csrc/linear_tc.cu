@@ -16,12 +16,16 @@
 // output: P, and S where it multiplies Q.  The state itself never goes through them.
 //
 // linear_out_kernel: one CTA per (sequence range, v-head) walks its chunks with the state
-// in registers (32 floats a thread).  Warps 0-7 do the elementwise work, a thread holding
-// one TMEM lane and half the columns: weighted keys (A), P (B), state (C), output (D);
-// warp 8 issues the products, warp 9 the tile loads, warp 10 the sums of the gates.  Seven
-// 32 KB tiles (Q, K, V, hi, lo, S, P) leave room for one buffer each; the order A B C D
-// lets every load and product run behind another phase, and the chain of a chunk is what
-// bounds the kernel (about 1.5 us; its products are 1.35 us of tensor time).
+// in registers (32 floats a thread).  Warps 0-15 do the elementwise work, a thread holding
+// one TMEM lane and a quarter of the columns: weighted keys (A), P (B), state (C), output
+// (D); warp 16 issues the products, warp 17 the tile loads, warp 18 the sums of the gates.
+//
+// An SM's shared memory passes 128 bytes a clock, which a 128 x 128 product with both
+// operands there uses up: with P and the weighted keys in shared memory a chunk moved 5100
+// clocks' worth (measured 8700 a chunk).  They are TMEM operands instead: P over the scores
+// it came from, the keys (transposed on the way by ldmatrix) over the output accumulator
+// that is not in use yet.  That leaves 3072 clocks of traffic and room for two buffers of
+// each of Q, K and V.  TMEM (512 columns): scores / P, Q S, P V / weighted keys, state.
 //
 // A long sequence over few heads would leave SMs idle, so it is cut into ranges that run
 // side by side: linear_range_kernel gives every range's own state (hi + lo products added
@@ -90,10 +94,12 @@ __device__ __forceinline__ int64_t range_slot0(const LinParams &p, int n, int t0
 // ------------------------------------------------------------------------ shared memory
 
 struct LinBars {
-    uint64_t q, k[3], v[2];              // tiles loaded
-    uint64_t qk, qs, kv[2], pv;          // products done
+    uint64_t q[2], k[3], v[4];           // tiles loaded
+    uint64_t qk[2], qs[2], kv[2], pv[2]; // products done (two: by the buffers they read)
     uint64_t gates;                      // this chunk's gate arrays are written
     uint64_t r_kt[2], r_p, r_s, r_o, r_arr;   // every elementwise warp: operands written, arrays read
+    uint64_t lanes[4];                   // the four warps that share 32 TMEM lanes
+    uint64_t kf[3], vf[4];               // range pass: tiles free
     uint64_t fin;
 };
 struct LinSmem {
@@ -144,24 +150,41 @@ __device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
 // Bounded wait on an mbarrier phase.  Gives up when the bound has passed or another thread
 // of the CTA has given up; every role then leaves its loop.
 __device__ __forceinline__ bool lin_wait(LinSmem &S, uint64_t *bar, uint32_t parity) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
+    if (try_wait_long(bar, parity)) return true;
     uint64_t t0, t;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
     volatile int *abort = &S.abort;
-    for (;;) {
-        if (tc::mbar_try_wait(bar, parity)) return true;
-        if (*abort) return false;
+    while (!try_wait_long(bar, parity)) {
         asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-        if (t - t0 > kCopyWaitNs) {
+        if (*abort || t - t0 > kCopyWaitNs) {
             *abort = 1;
             return false;
         }
     }
+    return true;
 }
 
 // The same by a whole warp, which stays together whatever its lanes saw.
 __device__ __forceinline__ bool warp_wait(LinSmem &S, uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, lin_wait(S, bar, parity)) != 0;
+}
+
+// Meeting of the four warps that share 32 TMEM lanes (bounded, unlike a named barrier).
+__device__ __forceinline__ bool lanes_sync(LinSmem &S, int lq, uint32_t &phase) {
+    tc::fence_before_sync();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&S.bar.lanes[lq]);
+    const bool ok = warp_wait(S, &S.bar.lanes[lq], phase);
+    phase ^= 1;
+    tc::fence_after_sync();
+    return ok;
+}
+
+// The TMEM accesses of this warp (waited for) happen before the arrival.
+__device__ __forceinline__ void warp_arrive_tmem(uint64_t *bar) {
+    tc::fence_before_sync();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // The writes of this warp (shared memory for the async proxy, TMEM reads done) happen
@@ -192,6 +215,21 @@ __device__ __forceinline__ void product(uint32_t d, const uint8_t *a, const uint
         const uint64_t da = A_MN ? tc::sdesc(a0 + mn, kBlk, 1024) : tc::sdesc(a0 + km, 16, 1024);
         const uint64_t db = B_MN ? tc::sdesc(b0 + mn, kBlk, 1024) : tc::sdesc(b0 + km, 16, 1024);
         tc::mma_bf16_warp(d, da, db, id, add || ks > 0);
+    }
+}
+
+// The same with A in TMEM: 128 lanes, two of the depth's elements a word; B MN-major.
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, const uint8_t *b, bool add) {
+    constexpr uint32_t id = tc::idesc_bf16(128, 128, 0, 1);
+    const uint32_t b0 = tc::smem_u32(b);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+        const uint64_t db = tc::sdesc(b0 + ks * 2048, kBlk, 1024);
+        asm volatile("{\n\t.reg .pred p, e;\n\t"
+                     "elect.sync _|e, 0xffffffff;\n\t"
+                     "setp.ne.b32 p, %4, 0;\n\t"
+                     "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                     :: "r"(d), "r"(a + 8 * ks), "l"(db), "r"(id), "r"((uint32_t)(add || ks > 0)) : "memory");
     }
 }
 
@@ -233,39 +271,72 @@ __device__ __forceinline__ float lanes_above(float x) {
 }
 
 // --------------------------------------------------------------- weighted keys (phase A)
-// hi, lo <- bf16 pair of w_j k_j for rows j < L, zero rows after (hi may be k).  A quarter
-// warp takes the eight 16-byte chunks of a row.
-__device__ __forceinline__ void weigh_keys(const uint8_t *k, uint8_t *hi, uint8_t *lo, const float *w,
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// 16 lanes x 16 words: register 2 x + y of lane l is lane l / 4 + 8 y, word 4 x + l % 4.
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+                    "r"(r[6]), "r"(r[7]) : "memory");
+}
+// 32 lanes x 16 words, a lane's words in its thread.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+                    "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+                    "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+
+// The bf16 pair hi, lo of w_j k_j, transposed: TMEM lane d, word j / 2 of 64 for hi and the
+// next 64 for lo, zero for tokens j >= L.  This warp takes d = 32 lq .. and j = 32 jb ..;
+// ldmatrix hands it 8 x 8 blocks transposed, in the layout the 16-lane store wants.
+template <bool TAIL>
+__device__ __forceinline__ void weigh_keys(const uint8_t *k, uint32_t tmem, int lq, int jb, const float *w,
                                            int L) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = lane & 7;
+    const int lane = threadIdx.x & 31;
+    float2 w2[4];
 #pragma unroll
-    for (int it = 0; it < 128 / (4 * kLinWarps); ++it) {
-        const int row = 4 * kLinWarps * it + 4 * warp + (lane >> 3);
-        const float wj = w[row];
-        const float2 w2 = make_float2(wj, wj), m1 = make_float2(-1.f, -1.f);
+    for (int tg = 0; tg < 4; ++tg)
+        w2[tg] = *reinterpret_cast<const float2 *>(w + 32 * jb + 8 * tg + 2 * (lane & 3));
+    const float2 m1 = make_float2(-1.f, -1.f);
+    const uint32_t base = tc::smem_u32(k) + (lq >> 1) * kBlk;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            const uint32_t at = kb * kBlk + tc::swz(row, ch);
-            const uint4 u = *reinterpret_cast<const uint4 *>(k + at);
-            const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
-            uint32_t h[4], r[4];
+    for (int th = 0; th < 2; ++th) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int tp = 0; tp < 2; ++tp) {
+            // matrix lane / 8: tokens of group 2 tp + (matrix / 2), columns of group 2 th + matrix % 2
+            const int mat = lane >> 3, tok = 32 * jb + 8 * (2 * tp + (mat >> 1)) + (lane & 7);
+            uint32_t x[4];
+            ldmatrix_x4_trans(x, base + tc::swz(tok, 4 * (lq & 1) + 2 * th + (mat & 1)));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 x = mul_f32x2(
-                    make_float2(__uint_as_float(uw[e] << 16), __uint_as_float(uw[e] & 0xffff0000u)), w2);
-                h[e] = pack_bf2(x.x, x.y);
+                const int tg = 2 * tp + (e >> 1);
+                const float2 v = mul_f32x2(
+                    make_float2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u)), w2[tg]);
+                uint32_t h = pack_bf2(v.x, v.y);
                 const float2 d = fma_f32x2(
-                    make_float2(__uint_as_float(h[e] << 16), __uint_as_float(h[e] & 0xffff0000u)), m1, x);
-                r[e] = pack_bf2(d.x, d.y);
+                    make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)), m1, v);
+                uint32_t r = pack_bf2(d.x, d.y);
+                if (TAIL) {
+                    const int j = 32 * jb + 8 * tg + 2 * (lane & 3);
+                    const uint32_t keep = j + 1 < L ? 0xffffffffu : j < L ? 0x0000ffffu : 0u;
+                    h &= keep;
+                    r &= keep;
+                }
+                hi[4 * tp + e] = h;
+                lo[4 * tp + e] = r;
             }
-            if (L < kLinC && row >= L) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] = r[e] = 0u;
-            }
-            *reinterpret_cast<uint4 *>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4 *>(lo + at) = make_uint4(r[0], r[1], r[2], r[3]);
         }
+        const uint32_t at = tmem + ((uint32_t)(32 * lq + 16 * th) << 16) + 16 * jb;
+        tmem_st_16x128b_x4(at, hi);
+        tmem_st_16x128b_x4(at + 64, lo);
     }
+    tc::tmem_wait_st();
 }
 // Rows past the end hold another sequence's values: zero them (a NaN there would survive
 // the zero weights).
@@ -294,6 +365,19 @@ __device__ __forceinline__ void store_row(uint8_t *tile, int quarter, int row, c
     }
 }
 
+// 32 bytes in one store (a whole sector) when the address allows it: o's rows are 16-byte
+// aligned at least.
+__device__ __forceinline__ void store_32b(bf16 *p, const uint32_t (&u)[8]) {
+    if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                     :: "l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]),
+                        "r"(u[6]), "r"(u[7]) : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+    }
+}
+
 // ------------------------------------------------------------------------- output pass
 
 __global__ void __launch_bounds__(kLinThreads, 1)
@@ -304,8 +388,7 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         if (threadIdx.x == 0) report(p.status, GDN_ERR_CUDA);
         return;
     }
-    uint8_t *sQ = S.tile[0], *sK = S.tile[1], *sV = S.tile[2], *sHi = S.tile[3], *sLo = S.tile[4],
-            *sS = S.tile[5], *sP = S.tile[6];
+    uint8_t *sS = S.tile[6];      // Q, K, V of chunk i: tiles 0, 2, 4 + (i & 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int range = blockIdx.x, hv = blockIdx.y, n = blockIdx.z, hk = hv / (p.Hv / p.Hk);
     const int t0 = p.cu[n], len = p.cu[n + 1] - t0;
@@ -315,7 +398,7 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     if (range > 0 && c_first >= nch) return;
     const int count = c_last - c_first;          // 0 for an empty sequence
     const bool last = c_last >= nch;
-    const uint32_t colSc = 0, colOi = 128, colOa = 256, colD = 384;
+    const uint32_t colSc = 0, colOi = 128, colOa = 256, colD = 384;   // P over Sc, keys over Oa
 
     if (warp == 0) {
         tc::tmem_alloc(&S.tmem, 512);
@@ -324,9 +407,11 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     if (tid == 0) {
         S.abort = 0;
         LinBars &b = S.bar;
-        for (uint64_t *x : {&b.q, &b.k[0], &b.v[0], &b.qk, &b.qs, &b.kv[0], &b.pv, &b.gates, &b.fin})
+        for (uint64_t *x : {&b.q[0], &b.q[1], &b.k[0], &b.k[1], &b.v[0], &b.v[1], &b.qk[0], &b.qk[1], &b.qs[0], &b.qs[1],
+                            &b.kv[0], &b.pv[0], &b.pv[1], &b.gates, &b.fin})
             tc::mbar_init(x, 1);
-        for (uint64_t *x : {&b.r_kt[0], &b.r_p, &b.r_s, &b.r_o, &b.r_arr}) tc::mbar_init(x, kLinWarps);
+        for (uint64_t *x : {&b.r_kt[0], &b.r_kt[1], &b.r_p, &b.r_s, &b.r_o, &b.r_arr}) tc::mbar_init(x, kLinWarps);
+        for (int x = 0; x < 4; ++x) tc::mbar_init(&b.lanes[x], 4);
         tc::mbar_fence_init();
     }
     tc::fence_before_sync();
@@ -357,20 +442,26 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             store_row(sS, jb, row, st);
             warp_arrive(&S.bar.r_s);
         }
+        uint32_t lanes_ph = 0;
         for (int i = 0; i < count; ++i) {
-            const uint32_t ph = i & 1;
+            // a buffer of two serves every other chunk
+            const uint32_t ph = i & 1, ph2 = (i >> 1) & 1;
             const int t = t0 + (c_first + i) * kLinC;
             const int L = min(kLinC, t0 + len - t);
-            // ---- A: weighted keys
-            if (!warp_wait(S, &S.bar.gates, ph) || !warp_wait(S, &S.bar.k[0], ph)) break;
-            weigh_keys(sK, sHi, sLo, S.w, L);
-            if (L < kLinC) {
-                if (!warp_wait(S, &S.bar.v[0], ph)) break;
-                clear_rows(sV, L);
+            // ---- A: weighted keys, over the P V that the four warps have read
+            if (!warp_wait(S, &S.bar.gates, ph) || !warp_wait(S, &S.bar.k[ph], ph2)) break;
+            if (!lanes_sync(S, lq, lanes_ph)) break;
+            if (L == kLinC) {
+                weigh_keys<false>(S.tile[2 + ph], tmem + colOa, lq, jb, S.w, L);
+            } else {
+                weigh_keys<true>(S.tile[2 + ph], tmem + colOa, lq, jb, S.w, L);
+                if (!warp_wait(S, &S.bar.v[ph], ph2)) break;
+                clear_rows(S.tile[4 + ph], L);
+                tc::fence_async_smem();
             }
-            warp_arrive(&S.bar.r_kt[0]);
+            warp_arrive_tmem(&S.bar.r_kt[ph]);
             // ---- B: P = decay-weighted lower triangle of Q K^T
-            if (!warp_wait(S, &S.bar.qk, ph)) break;
+            if (!warp_wait(S, &S.bar.qk[ph], ph2)) break;
             tc::fence_after_sync();
             const float eg = S.eg[row], decay = S.decay;
             float v[32];
@@ -391,19 +482,22 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                         v[4 * j + 3] *= f * b4[j].w;
                     }
                 } else {
-                    float w[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) w[j] = p.scale * ex2(gi - S.g2[32 * jb + j]);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = j <= lane ? v[j] * w[j] : 0.f;
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = j <= lane ? v[j] * (p.scale * ex2(gi - S.g2[32 * jb + j])) : 0.f;
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = 0.f;
             }
-            store_row(sP, jb, row, v);
-            warp_arrive(&S.bar.r_p);
+            uint32_t pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) pk[j] = pack_bf2(v[2 * j], v[2 * j + 1]);
+            if (!lanes_sync(S, lq, lanes_ph)) break;   // P goes over scores that the other three warps read
+            tmem_st16(tmem + ((uint32_t)(32 * lq) << 16) + colSc + 16 * jb, pk);
+            tc::tmem_wait_st();
+            warp_arrive_tmem(&S.bar.r_p);
             if (lane == 0) mbar_arrive(&S.bar.r_arr);
             // ---- C: state
             if (!warp_wait(S, &S.bar.kv[0], ph)) break;
@@ -412,33 +506,26 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             tc::tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 32; ++j) st[j] = fmaf(decay, st[j], v[j]);
-            if (!warp_wait(S, &S.bar.qs, ph)) break;
+            if (!warp_wait(S, &S.bar.qs[ph], ph2)) break;
             store_row(sS, jb, row, st);
             warp_arrive(&S.bar.r_s);
-            // ---- D: output, through this warp's own part of the P tile (PV has read it), so
-            // that a row's 64 bytes leave as full sectors
-            if (!warp_wait(S, &S.bar.pv, ph)) break;
+            // ---- D: output, 64 bytes of a row a thread
+            if (!warp_wait(S, &S.bar.pv[ph], ph2)) break;
             tc::fence_after_sync();
-            float a[32];
-            tc::tmem_ld32(tm + colOi, a);
-            tc::tmem_ld32(tm + colOa, v);
-            tc::tmem_wait_ld();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.bar.r_o);
+            bf16 *dst = p.o + (int64_t)(t + row) * p.o_tok + (int64_t)hv * 128 + 32 * jb;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = fmaf(eg, a[j], v[j]);
-            store_row(sP, jb, row, v);
-            __syncwarp();
-            bf16 *dst = p.o + (int64_t)(t + 32 * lq) * p.o_tok + (int64_t)hv * 128 + 32 * jb;
+            for (int c = 0; c < 2; ++c) {
+                float a[16];
+                tc::tmem_ld16(tm + colOi + 16 * c, a);
+                tc::tmem_ld16(tm + colOa + 16 * c, v);
+                tc::tmem_wait_ld();
+                if (c == 1) warp_arrive_tmem(&S.bar.r_o);
+                uint32_t u[8];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int rr = 8 * x + (lane >> 2), cc = lane & 3;
-                const uint4 u = *reinterpret_cast<const uint4 *>(
-                    sP + (jb >> 1) * kBlk + tc::swz(32 * lq + rr, 4 * (jb & 1) + cc));
-                if (32 * lq + rr < L) reinterpret_cast<uint4 *>(dst + rr * p.o_tok)[cc] = u;
+                for (int e = 0; e < 8; ++e)
+                    u[e] = pack_bf2(fmaf(eg, a[2 * e], v[2 * e]), fmaf(eg, a[2 * e + 1], v[2 * e + 1]));
+                if (row < L) store_32b(dst + 16 * c, u);
             }
-            __syncwarp();
         }
         if (last && p.hT && !*(volatile int *)&S.abort) {
             float4 *out = reinterpret_cast<float4 *>(p.hT + ((int64_t)n * p.Hv + hv) * 16384 + st_off);
@@ -449,60 +536,56 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     } else if (warp == kLinWarps) {
         // ---- products
         for (int i = 0; i < count; ++i) {
-            const uint32_t ph = i & 1;
-            if (!warp_wait(S, &S.bar.q, ph) || !warp_wait(S, &S.bar.k[0], ph)) break;
+            const uint32_t ph = i & 1, ph2 = (i >> 1) & 1;
+            const uint8_t *sQ = S.tile[ph], *sK = S.tile[2 + ph], *sV = S.tile[4 + ph];
+            if (!warp_wait(S, &S.bar.q[ph], ph2) || !warp_wait(S, &S.bar.k[ph], ph2)) break;
+            if (i > 0 && !warp_wait(S, &S.bar.pv[ph ^ 1], ((i - 1) >> 1) & 1)) break;      // P is read: the scores' turn
             tc::fence_after_sync();
             product<0, 0>(tmem + colSc, sQ, sK, false);
-            tc::mma_commit_warp(&S.bar.qk);
+            tc::mma_commit_warp(&S.bar.qk[ph]);
             if (!warp_wait(S, &S.bar.r_s, ph)) break;
             if (i > 0 && !warp_wait(S, &S.bar.r_o, ph ^ 1)) break;
             tc::fence_after_sync();
             product<0, 1>(tmem + colOi, sQ, sS, false);
-            tc::mma_commit_warp(&S.bar.qs);
-            if (!warp_wait(S, &S.bar.r_kt[0], ph) || !warp_wait(S, &S.bar.v[0], ph)) break;
+            tc::mma_commit_warp(&S.bar.qs[ph]);
+            if (!warp_wait(S, &S.bar.r_kt[ph], ph2) || !warp_wait(S, &S.bar.v[ph], ph2)) break;
             tc::fence_after_sync();
-            product<1, 1>(tmem + colD, sHi, sV, false);
-            product<1, 1>(tmem + colD, sLo, sV, true);
+            product_ts(tmem + colD, tmem + colOa, sV, false);
+            product_ts(tmem + colD, tmem + colOa + 64, sV, true);
             tc::mma_commit_warp(&S.bar.kv[0]);
-            if (!warp_wait(S, &S.bar.r_p, ph)) break;
+            // the keys' columns take P V next
+            if (!warp_wait(S, &S.bar.r_p, ph) || !warp_wait(S, &S.bar.kv[0], ph)) break;
             tc::fence_after_sync();
-            product<0, 1>(tmem + colOa, sP, sV, false);
-            tc::mma_commit_warp(&S.bar.pv);
+            product_ts(tmem + colOa, tmem + colSc, sV, false);
+            tc::mma_commit_warp(&S.bar.pv[ph]);
         }
         // everything issued has completed before the TMEM is freed
         tc::mma_commit_warp(&S.bar.fin);
         wait_copy(&S.bar.fin, 0);
     } else if (warp == kLinWarps + 1) {
-        // ---- tile loads
-        int loads = 0;
+        // ---- tile loads: buffers of two, each refilled when its last reader is done
         if (lane == 0) {
             tc::prefetch_tmap(&maps.q);
             tc::prefetch_tmap(&maps.k);
             tc::prefetch_tmap(&maps.v);
+            int nk = 0, nq = 0, nv = 0;
             for (int i = 0; i < count; ++i) {
-                const uint32_t pp = (i & 1) ^ 1;
+                const uint32_t b = i & 1, was = ((i >> 1) & 1) ^ 1;   // chunk i - 2's use of the buffer
                 const int t = t0 + (c_first + i) * kLinC;
-                if (i > 0 && (!lin_wait(S, &S.bar.qk, pp) || !lin_wait(S, &S.bar.r_kt[0], pp))) break;
-                load_tile(sK, &maps.k, &S.bar.k[0], hk, t);
-                if (i > 0 && !lin_wait(S, &S.bar.qs, pp)) {
-                    wait_copy(&S.bar.k[0], i & 1);
-                    break;
-                }
-                load_tile(sQ, &maps.q, &S.bar.q, hk, t);
-                if (i > 0 && (!lin_wait(S, &S.bar.kv[0], pp) || !lin_wait(S, &S.bar.pv, pp))) {
-                    wait_copy(&S.bar.k[0], i & 1);
-                    wait_copy(&S.bar.q, i & 1);
-                    break;
-                }
-                load_tile(sV, &maps.v, &S.bar.v[0], hv, t);
-                ++loads;
+                if (i >= 2 && (!lin_wait(S, &S.bar.qk[b], was) || !lin_wait(S, &S.bar.r_kt[b], was))) break;
+                load_tile(S.tile[2 + b], &maps.k, &S.bar.k[b], hk, t);
+                ++nk;
+                if (i >= 2 && !lin_wait(S, &S.bar.qs[b], was)) break;
+                load_tile(S.tile[b], &maps.q, &S.bar.q[b], hk, t);
+                ++nq;
+                if (i >= 2 && !lin_wait(S, &S.bar.pv[b], was)) break;
+                load_tile(S.tile[4 + b], &maps.v, &S.bar.v[b], hv, t);
+                ++nv;
             }
-            if (loads > 0) {
-                // (bounded) everything loaded has landed
-                wait_copy(&S.bar.k[0], (loads - 1) & 1);
-                wait_copy(&S.bar.q, (loads - 1) & 1);
-                wait_copy(&S.bar.v[0], (loads - 1) & 1);
-            }
+            // (bounded) everything loaded has landed
+            for (int x = max(0, nk - 2); x < nk; ++x) wait_copy(&S.bar.k[x & 1], (x >> 1) & 1);
+            for (int x = max(0, nq - 2); x < nq; ++x) wait_copy(&S.bar.q[x & 1], (x >> 1) & 1);
+            for (int x = max(0, nv - 2); x < nv; ++x) wait_copy(&S.bar.v[x & 1], (x >> 1) & 1);
         }
     } else {
         // ---- gates
@@ -550,7 +633,7 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
 // -------------------------------------------------------------------------- range states
 // State that one range adds, from zero, with decays to the range's end: its chunks in
 // reverse, each chunk's weights carrying the sum of the later ones, all added up in TMEM.
-// Tiles: K x 3 (hi replaces K in place), lo x 2, V x 2; the products bound it.
+// Tiles: K x 3, V x 4; the weighted keys alternate between two TMEM places.
 __global__ void __launch_bounds__(kLinThreads, 1)
 linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -569,31 +652,35 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     const int64_t slot = (range_slot0(p, n, t0) + range + 1) * p.Hv + hv;
 
     if (warp == 0) {
-        tc::tmem_alloc(&S.tmem, 128);
+        tc::tmem_alloc(&S.tmem, 512);
         tc::tmem_relinquish();
     }
     if (tid == 0) {
         S.abort = 0;
         LinBars &b = S.bar;
-        for (uint64_t *x : {&b.k[0], &b.k[1], &b.k[2], &b.v[0], &b.v[1], &b.kv[0], &b.kv[1], &b.gates, &b.fin})
+        for (uint64_t *x : {&b.k[0], &b.k[1], &b.k[2], &b.v[0], &b.v[1], &b.v[2], &b.v[3], &b.kv[0],
+                            &b.kv[1], &b.vf[0], &b.vf[1], &b.vf[2], &b.vf[3], &b.gates, &b.fin})
             tc::mbar_init(x, 1);
-        for (uint64_t *x : {&b.r_kt[0], &b.r_kt[1], &b.r_arr}) tc::mbar_init(x, kLinWarps);
+        for (uint64_t *x : {&b.r_kt[0], &b.r_kt[1], &b.kf[0], &b.kf[1], &b.kf[2], &b.r_arr})
+            tc::mbar_init(x, kLinWarps);
         tc::mbar_fence_init();
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = S.tmem;
-    // step i takes chunk c_first + count - 1 - i; its use of a buffer among two is that
-    // buffer's (i >> 1)-th, among three its (i / 3)-th
+    // step i takes chunk c_first + count - 1 - i; its use of a buffer among x is that
+    // buffer's (i / x)-th.  TMEM: the state at 0, weighted keys at 128 and 256.
     if (warp < kLinWarps) {
         bool ok = true;
         for (int i = 0; i < count && ok; ++i) {
             const int bf = i & 1, kb = i % 3;
             if (!(ok = warp_wait(S, &S.bar.gates, i & 1) && warp_wait(S, &S.bar.k[kb], (i / 3) & 1))) break;
             if (i >= 2 && !(ok = warp_wait(S, &S.bar.kv[bf], ((i >> 1) & 1) ^ 1))) break;
-            weigh_keys(S.tile[kb], S.tile[kb], S.tile[3 + bf], S.w, kLinC);
-            warp_arrive(&S.bar.r_kt[bf]);
+            tc::fence_after_sync();
+            weigh_keys<false>(S.tile[kb], tmem + 128 + 128 * bf, warp & 3, warp >> 2, S.w, kLinC);
+            warp_arrive_tmem(&S.bar.r_kt[bf]);
+            if (lane == 0) mbar_arrive(&S.bar.kf[kb]);
             if (lane == 0) mbar_arrive(&S.bar.r_arr);
         }
         const int e = count - 1;
@@ -610,36 +697,30 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         }
     } else if (warp == kLinWarps) {
         for (int i = 0; i < count; ++i) {
-            const int bf = i & 1;
-            if (!warp_wait(S, &S.bar.r_kt[bf], (i >> 1) & 1) || !warp_wait(S, &S.bar.v[bf], (i >> 1) & 1)) break;
+            const int bf = i & 1, vb = i & 3;
+            if (!warp_wait(S, &S.bar.r_kt[bf], (i >> 1) & 1) || !warp_wait(S, &S.bar.v[vb], (i >> 2) & 1)) break;
             tc::fence_after_sync();
-            product<1, 1>(tmem, S.tile[i % 3], S.tile[5 + bf], i > 0);
-            product<1, 1>(tmem, S.tile[3 + bf], S.tile[5 + bf], true);
+            product_ts(tmem, tmem + 128 + 128 * bf, S.tile[3 + vb], i > 0);
+            product_ts(tmem, tmem + 192 + 128 * bf, S.tile[3 + vb], true);
             tc::mma_commit_warp(&S.bar.kv[bf]);
+            tc::mma_commit_warp(&S.bar.vf[vb]);
         }
         tc::mma_commit_warp(&S.bar.fin);
         wait_copy(&S.bar.fin, 0);
     } else if (warp == kLinWarps + 1) {
         if (lane == 0) {
-            // K of step i goes where step i - 3 was, V where step i - 2 was; K is asked for
-            // a step ahead of V
-            int ks = 0, vs = 0;
-            auto load_k = [&](int i) {
-                if (i >= 3 && !lin_wait(S, &S.bar.kv[(i - 3) & 1], ((i - 3) >> 1) & 1)) return false;
-                load_tile(S.tile[i % 3], &maps.k, &S.bar.k[i % 3], hk, t0 + (c_first + count - 1 - i) * kLinC);
-                ++ks;
-                return true;
-            };
-            bool ok = load_k(0);
-            for (int i = 0; i < count && ok; ++i) {
-                if (i + 1 < count && !(ok = load_k(i + 1))) break;
-                if (i >= 2 && !(ok = lin_wait(S, &S.bar.kv[i & 1], ((i >> 1) & 1) ^ 1))) break;
-                load_tile(S.tile[5 + (i & 1)], &maps.v, &S.bar.v[i & 1], hv,
-                          t0 + (c_first + count - 1 - i) * kLinC);
-                ++vs;
+            int nk = 0, nv = 0;
+            for (int i = 0; i < count; ++i) {
+                const int kb = i % 3, vb = i & 3, t = t0 + (c_first + count - 1 - i) * kLinC;
+                if (i >= 3 && !lin_wait(S, &S.bar.kf[kb], ((i / 3) & 1) ^ 1)) break;
+                load_tile(S.tile[kb], &maps.k, &S.bar.k[kb], hk, t);
+                ++nk;
+                if (i >= 4 && !lin_wait(S, &S.bar.vf[vb], ((i >> 2) & 1) ^ 1)) break;
+                load_tile(S.tile[3 + vb], &maps.v, &S.bar.v[vb], hv, t);
+                ++nv;
             }
-            for (int x = max(0, ks - 3); x < ks; ++x) wait_copy(&S.bar.k[x % 3], (x / 3) & 1);
-            for (int x = max(0, vs - 2); x < vs; ++x) wait_copy(&S.bar.v[x & 1], (x >> 1) & 1);
+            for (int x = max(0, nk - 3); x < nk; ++x) wait_copy(&S.bar.k[x % 3], (x / 3) & 1);
+            for (int x = max(0, nv - 4); x < nv; ++x) wait_copy(&S.bar.v[x & 3], (x >> 2) & 1);
         }
     } else {
         float x[4], carry = 0.f;
@@ -668,7 +749,7 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 0) tc::tmem_dealloc(tmem, 128);
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
     if (tid == 0 && S.abort) report(p.status, GDN_ERR_TIMEOUT);
 }
 
