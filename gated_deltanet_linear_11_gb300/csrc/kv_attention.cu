@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::CTAS)
 kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__ o,
                         float *__restrict__ lse, float *__restrict__ part_o,
                         float2 *__restrict__ part_ml, int64_t q_tok, int64_t o_tok, int Hq,
-                        int row_tiles, int64_t slab, int max_kv_len, float scale,
+                        int row_tiles, int64_t slab, int tc_rows, int max_kv_len, float scale,
                         int32_t *status) {
     using R = KvRec<D>;
     using A = AttnShape<D, NT>;
@@ -281,7 +281,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     const int t0 = kv.cu ? kv.cu[n] : n, m = kv.cu ? kv.cu[n + 1] - t0 : 1;
     const int len = kv.kv_lens[n];
     const int G = Hq / kv.Hkv, rows = G * m, row0 = rt * A::ROWS;
-    if (row0 >= rows) return;
+    if (row0 >= rows || Hq * m >= tc_rows) return;   // (tc_rows: the other kernel's sequences)
     if (len < 0 || len > max_kv_len || len > kv.capacity()) {
         if (tid == 0) report(status, GDN_ERR_SEQLENS);
         return;
@@ -679,7 +679,8 @@ template <int D>
 __global__ void __launch_bounds__(128)
 kv_attention_join_kernel(KvView kv, bf16 *__restrict__ o, float *__restrict__ lse,
                          const float *__restrict__ part_o, const float2 *__restrict__ part_ml,
-                         int64_t o_tok, int Hq, int tile_rows, int64_t slab, int max_kv_len) {
+                         int64_t o_tok, int Hq, int tile_rows, int64_t slab, int tc_rows,
+                         int max_kv_len) {
     __shared__ __align__(16) float sacc[4][D];
     __shared__ float sl[4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -688,7 +689,7 @@ kv_attention_join_kernel(KvView kv, bf16 *__restrict__ o, float *__restrict__ ls
     const int n = kv.cu ? sequence_of(kv.cu, kv.N, (int)t) : (int)t;
     const int t0 = kv.cu ? kv.cu[n] : n, m = kv.cu ? kv.cu[n + 1] - t0 : 1;
     const int len = kv.kv_lens[n];
-    if (len < 0 || len > max_kv_len || len > kv.capacity()) return;
+    if (len < 0 || len > max_kv_len || len > kv.capacity() || Hq * m >= tc_rows) return;
     const int G = Hq / kv.Hkv, rows = G * m, row = (int)(t - t0) * G + hq % G;
     const int last = min((row / tile_rows + 1) * tile_rows, rows) - 1;
     const int see_last = len - m + last / G + 1;
@@ -776,6 +777,10 @@ gdn_status_t launch_kv_attention_simt(const KvArgs &a, cudaStream_t st) {
 
 namespace {
 
+// Query heads times new tokens from which a sequence takes the tcgen05 kernel: 20 of its
+// CTAs (256 rows each).  Below that too few SMs would be at work on it.
+constexpr int kTcMinRows = 20 * 256;
+
 int attn_max_nt(int D) { return D == 64 ? 8 : D == 128 ? 4 : 2; }
 
 // n-tiles per CTA: the fewest of 1, 2, 4 (8) that take every row of a kv-head, at most as
@@ -813,7 +818,7 @@ int64_t attn_slab(int Hq, int64_t T, int N, int max_q_len, int max_len) {
 size_t part_ml_bytes(int64_t rows) { return ((size_t)rows * 8 + 255) / 256 * 256; }
 
 template <int D, int NT>
-gdn_status_t mma_launch(const KvArgs &a, int row_tiles, int splits, cudaStream_t st) {
+gdn_status_t mma_launch(const KvArgs &a, int row_tiles, int splits, int tc_rows, cudaStream_t st) {
     using A = gdn::AttnShape<D, NT>;
     auto kern = gdn::kv_attention_mma_kernel<D, NT>;
     static std::atomic<uint64_t> ready{0};   // one bit per device (beyond 63: set every time)
@@ -829,11 +834,12 @@ gdn_status_t mma_launch(const KvArgs &a, int row_tiles, int splits, cudaStream_t
     float *po = slab ? (float *)((uint8_t *)a.ws + part_ml_bytes(slab * a.kv.N)) : nullptr;
     kern<<<dim3((unsigned)((int64_t)splits * row_tiles), a.kv.Hkv, a.kv.N), gdn::kAttnThreads, A::SMEM, st>>>(
         a.kv, (const gdn::bf16 *)a.q, (gdn::bf16 *)a.q_out, a.lse, po, ml, a.q_tok, a.o_tok, a.Hq,
-        row_tiles, slab, a.max_kv_len, a.scale, a.status);
+        row_tiles, slab, tc_rows, a.max_kv_len, a.scale, a.status);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
     if (splits > 1 &&
         launch_dependent(gdn::kv_attention_join_kernel<D>, dim3((unsigned)a.T, a.Hq), dim3(128), 0, st, a.kv,
-                         (gdn::bf16 *)a.q_out, a.lse, po, ml, a.o_tok, a.Hq, 8 * NT, slab, a.max_kv_len) != cudaSuccess)
+                         (gdn::bf16 *)a.q_out, a.lse, po, ml, a.o_tok, a.Hq, 8 * NT, slab, tc_rows,
+                         a.max_kv_len) != cudaSuccess)
         return GDN_ERR_CUDA;
     return GDN_OK;
 }
@@ -849,21 +855,30 @@ size_t kv_attention_workspace(int32_t D, int32_t Hq, int32_t Hkv, int64_t T, int
 
 gdn_status_t launch_kv_attention(const KvArgs &a, cudaStream_t st) {
     if (a.in_f32 || (a.flags & GDN_PREFILL_SIMT)) return launch_kv_attention_simt(a, st);
-    const int64_t rows = (int64_t)(a.Hq / a.kv.Hkv) * a.max_q_len;
+    // sequences of many rows go to the tcgen05 kernel, the others to this one
+    const bool tc = a.kv.cu && kv_attention_tc_supported(a.D);
+    const int tc_rows = tc ? kTcMinRows : 0x7fffffff;
+    int64_t m_most = a.max_q_len;
+    if (tc && a.Hq * m_most >= tc_rows) {
+        const gdn_status_t s = launch_kv_attention_tc(a, tc_rows, st);
+        if (s != GDN_OK || (int64_t)a.Hq * a.min_q_len >= tc_rows) return s;
+        m_most = (tc_rows - 1) / a.Hq;
+    }
+    const int64_t rows = (int64_t)(a.Hq / a.kv.Hkv) * m_most;
     const int nt = attn_nt(a.D, rows);
     const int64_t tiles = (rows + 8 * nt - 1) / (8 * nt);
     const int splits = attn_max_splits(a.max_kv_len, a.min_q_len);
     if (tiles * splits > 0x7fffffff || a.kv.N > 65535) return GDN_ERR_SHAPE;
     switch (a.D * 10 + nt) {
-    case 641: return mma_launch<64, 1>(a, (int)tiles, splits, st);
-    case 642: return mma_launch<64, 2>(a, (int)tiles, splits, st);
-    case 644: return mma_launch<64, 4>(a, (int)tiles, splits, st);
-    case 648: return mma_launch<64, 8>(a, (int)tiles, splits, st);
-    case 1281: return mma_launch<128, 1>(a, (int)tiles, splits, st);
-    case 1282: return mma_launch<128, 2>(a, (int)tiles, splits, st);
-    case 1284: return mma_launch<128, 4>(a, (int)tiles, splits, st);
-    case 2561: return mma_launch<256, 1>(a, (int)tiles, splits, st);
-    case 2562: return mma_launch<256, 2>(a, (int)tiles, splits, st);
+    case 641: return mma_launch<64, 1>(a, (int)tiles, splits, tc_rows, st);
+    case 642: return mma_launch<64, 2>(a, (int)tiles, splits, tc_rows, st);
+    case 644: return mma_launch<64, 4>(a, (int)tiles, splits, tc_rows, st);
+    case 648: return mma_launch<64, 8>(a, (int)tiles, splits, tc_rows, st);
+    case 1281: return mma_launch<128, 1>(a, (int)tiles, splits, tc_rows, st);
+    case 1282: return mma_launch<128, 2>(a, (int)tiles, splits, tc_rows, st);
+    case 1284: return mma_launch<128, 4>(a, (int)tiles, splits, tc_rows, st);
+    case 2561: return mma_launch<256, 1>(a, (int)tiles, splits, tc_rows, st);
+    case 2562: return mma_launch<256, 2>(a, (int)tiles, splits, tc_rows, st);
     }
     return GDN_ERR_UNSUPPORTED;
 }

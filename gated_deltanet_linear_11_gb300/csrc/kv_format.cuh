@@ -93,6 +93,9 @@ struct KvArgs {
 gdn_status_t launch_kv_append(const KvArgs &a, cudaStream_t st);
 gdn_status_t launch_kv_read(const KvArgs &a, cudaStream_t st);
 gdn_status_t launch_kv_attention(const KvArgs &a, cudaStream_t st);
+// Sequences with Hq m >= min_rows only, m new tokens each (kv.cu set).
+bool kv_attention_tc_supported(int32_t D);
+gdn_status_t launch_kv_attention_tc(const KvArgs &a, int min_rows, cudaStream_t st);
 size_t kv_attention_workspace(int32_t D, int32_t Hq, int32_t Hkv, int64_t T, int32_t N,
                               int32_t max_q_len, int32_t max_kv_len, int in_f32,
                               uint32_t flags);

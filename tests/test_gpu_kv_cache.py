@@ -266,6 +266,82 @@ def test_attention_long(D, Hq, Hkv):
     check_attention(c, *run_attention(c, scale=0.11), scale=0.11)
 
 
+# sequences of many rows (heads times new tokens from 5120 on), alone and beside others
+MANY = [(64, 32, 8), (64, 40, 40), (128, 32, 8), (128, 48, 2)]
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", MANY)
+def test_attention_many_rows(D, Hq, Hkv):
+    ms, lens = [200, 1, 129, 161], [200, 400, 300, 777]
+    c = attention_case(18, D, Hq, Hkv, 32, ms, lens)
+    check_attention(c, *run_attention(c))
+
+
+def test_attention_many_rows_peaked_and_scaled():
+    """Large scores of both signs of the scale, so that the running maximum moves often."""
+    for scale in (0.3, -0.25):
+        c = attention_case(19, 128, 32, 4, 16, [170], [600], spread=2.0)
+        check_attention(c, *run_attention(c, scale=scale), scale=scale)
+
+
+def test_attention_many_rows_without_keys():
+    for m, L in ((200, 150), (200, 0), (180, 1)):
+        c = attention_case(20, 128, 32, 8, 16, [m], [L])
+        o, lse = run_attention(c)
+        check_attention(c, o, lse)
+        assert not bool(o[:m - L].any())
+
+
+@pytest.mark.parametrize("ms,Hq", [([4, 1], 8), ([180, 1], 32)])
+def test_attention_nan_values_reach_only_rows_that_see_them(ms, Hq):
+    """A value group holding a NaN at a late position: earlier rows do not see it."""
+    L = ms[0] + 30
+    c = attention_case(21, 128, Hq, 2, 16, ms, [L, 40])
+    o1, l1 = run_attention(c)
+    at, g = L - 2, 2                       # the row before last sees it, and the last
+    rec = c["cache"][c["table"][0, at // 16], 1, 1, at % 16]
+    rec[64 + 4 * g + 2:64 + 4 * g + 4] = (0xFF, 0x7F)
+    o2, l2 = run_attention(c)
+    h = slice(Hq // 2, Hq)                 # the second kv-head's query heads
+    assert bool(o2[ms[0] - 2:ms[0], h, 32 * g:32 * g + 32].isnan().all())
+    keep = torch.ones(o1.shape, dtype=torch.bool)
+    keep[ms[0] - 2:ms[0], h, 32 * g:32 * g + 32] = False
+    assert_bits_equal(o1[keep], o2[keep], "outputs that the NaN does not reach")
+    assert_bits_equal(l1, l2, "lse")
+
+
+def test_attention_many_rows_bad_page_strides_and_batch():
+    c = attention_case(22, 128, 32, 8, 16, [170, 165], [300, 280])
+    o, lse = run_attention(c)
+    for n in range(2):
+        cu = offsets(c["ms"]).tolist()
+        one = dict(c, q=c["q"][cu[n]:cu[n + 1]], table=c["table"][n:n + 1], lens=c["lens"][n:n + 1],
+                   ms=[c["ms"][n]])
+        o1, l1 = run_attention(one)
+        assert_bits_equal(o[cu[n]:cu[n + 1]], o1, "o of sequence %d" % n)
+        assert_bits_equal(lse[cu[n]:cu[n + 1]], l1, "lse of sequence %d" % n)
+    # a page outside the cache: its keys are left out
+    bad = dict(c, table=c["table"].copy())
+    bad["table"][1, 3] = -5
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o2, _ = run_attention(bad, status=status)
+    assert int(status) == 10
+    assert_bits_equal(o2[:170], o[:170], "the other sequence")
+    keys = [p for p in range(280) if not 48 <= p < 64]
+    kk = ref.values(ref.gather(c["cache"], c["table"][1], 280, 0)[keys], ref.key_order(128))
+    vv = ref.values(ref.gather(c["cache"], c["table"][1], 280, 1)[keys], ref.value_order(128))
+    s = np.einsum("hd,lhd->hl", np64(c["q"])[-1], np.repeat(kk, 4, 1)) * 128 ** -0.5
+    p = np.exp(s - s.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    ro = np.einsum("hl,lhd->hd", p, np.repeat(vv, 4, 1))
+    oa = np.einsum("hl,lhd->hd", p, np.abs(np.repeat(vv, 4, 1)))
+    assert np.all(np.abs(np64(o2[-1]) - ro) <= ref.U_BF16 * np.abs(ro) + 2.0 ** -9 * oa)
+    # lengths past the bound
+    status.zero_()
+    run_attention(c, status=status, max_kv_len=290)
+    assert int(status) == 5
+
+
 @pytest.mark.parametrize("m", [3, 40])
 def test_attention_rows_without_keys(m):
     """Lengths below the new rows: the first rows see nothing and give zeros."""
