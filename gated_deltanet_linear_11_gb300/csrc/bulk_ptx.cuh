@@ -15,27 +15,27 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 
 constexpr uint64_t kCopyWaitNs = 2000000000ull;   // 2 s bound on any single wait
 
-// mbarrier.try_wait with a hint of how long the thread may be suspended (20 us): a waiting
-// warp then stays off the issue slots instead of polling.
-__device__ __forceinline__ bool try_wait_long(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity), "r"(20000u) : "memory");
-    return ok != 0;
+// Waits for an mbarrier phase; false when the bound has passed, or when *abort is set
+// (another thread has given up; may be null).  SLEEP_NS = 0 polls, for waits on a kernel's
+// critical chain; otherwise the warp sleeps between polls and leaves the issue slots to the
+// others.  The clock is read every 64 polls only.
+template <int SLEEP_NS>
+__device__ __forceinline__ bool wait_bounded_poll(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    uint64_t t0 = 0, t;
+    for (uint32_t i = 1;; ++i) {
+        if (SLEEP_NS > 0) __nanosleep(SLEEP_NS);
+        if (tc::mbar_try_wait(bar, parity)) return true;
+        if ((i & 63u) == 0) {
+            if (abort && *abort) return false;
+            asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kCopyWaitNs) return false;
+        }
+    }
 }
-
-// Wait for an mbarrier phase; false when it has not completed within the bound.
 __device__ __forceinline__ bool wait_copy(uint64_t *bar, uint32_t parity) {
-    if (try_wait_long(bar, parity)) return true;
-    uint64_t t0, t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
-    do {
-        if (try_wait_long(bar, parity)) return true;
-        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    } while (t - t0 < kCopyWaitNs);
-    return false;
+    return wait_bounded_poll<0>(bar, parity, nullptr);
 }
 
 // Two floats rounded to a bf16 pair (lo in the low half).

@@ -7,20 +7,26 @@
 // S, P and O live in TMEM (P over S, as the A operand of P V); K and V are unpacked once per
 // CTA into fp16 shared-memory tiles that both row tiles use.
 //
+// Scores are as exact as fp32 sums allow: a key is minimum + scale * code, and scale * code
+// (15 bits) goes in as an fp16 pair hi + lo, the minima as sixteen more columns against the
+// sums of q over each group (again a pair), so a 128-deep product becomes 272 deep:
+//     q.k = q.(hi + lo) + sum_g (sum of q over g) min_g.
+//
 // Warps 0-7: softmax, a thread owning one row of a tile; warps 8-15: unpacking, a warp
-// taking 16 records of keys and of values straight from the cache into registers, one tile
-// ahead; warp 16: products.  The two row tiles take turns: while one is in its softmax the
-// tensor pipe works for the other.
+// taking 16 records of keys, then of values, straight from the cache into registers while
+// the ones before are converted; warp 16: products.  The two row tiles take turns: while one is in
+// its softmax the tensor pipe works for the other.
 //
-// Bound by the tensor pipe and the exponentials alike: a 256 x 128 step has 2 x 2 x 512
-// clocks of products at D = 128, 2048 clocks of base-2 exponentials (16 a clock), and about
-// 1800 clocks of instruction issue (softmax 1160, unpacking 670).
+// Bound by the chain of a row tile (scores, softmax, P V) and the exponentials: a 256 x 128
+// step has 2 x (1088 + 512) clocks of products at D = 128 and 2048 clocks of base-2
+// exponentials (16 a clock).
 //
-// Fewer bits than fp32: q is scaled by a power of two per row into [2^11, 2^12) and held in
-// fp16 (exact down to 2^-26 of the largest); a key or value is minimum + scale * code
-// rounded once to fp16 (2^-11, after the sum, so nothing cancels later); p is rounded to
-// fp16, taken against a reference within 8 (in powers of two) of the running maximum, so it
-// stays below 256.  Scores, sums and outputs are fp32.
+// Fewer bits than fp32: q is scaled by a power of two per row into [2^6, 2^7) and held in
+// fp16 (exact down to 2^-21 of the largest); a value is minimum + scale * code rounded once
+// to fp16 (2^-11, after the sum, so nothing cancels later); p is rounded to fp16, taken
+// against a reference within 8 (in powers of two) of the running maximum and lifted by 2^7,
+// so it stays below 2^15 and a weight of 2^-31 of the largest is still held.  Scores, sums
+// and outputs are fp32.
 #include <algorithm>
 #include <atomic>
 
@@ -33,6 +39,7 @@ constexpr int kTcRows = 256;
 constexpr int kTcSoftWarps = 8, kTcUnpackWarps = 8;
 constexpr int kTcThreads = 32 * (kTcSoftWarps + kTcUnpackWarps + 1);
 constexpr float kTcSlack = 8.f;     // how far (log2) the maximum may pass the reference
+constexpr float kTcLift = 7.f;      // weights are kept at 2^7 times their value (below 2^15)
 
 template <int D> struct TcShape {
     static constexpr int NG = D / 32;
@@ -40,16 +47,18 @@ template <int D> struct TcShape {
     static constexpr int BLK = 16384;            // 64 columns of it
 };
 struct TcBars {
-    uint64_t full[2], empty[2];      // K/V stages
+    uint64_t k_full, k_free, v_full[2], v_free[2];
     uint64_t s_full[2], p_full[2], pv[2];   // per row tile
     uint64_t fin;
 };
 template <int D> struct TcSmem {
     uint8_t q[2][TcShape<D>::TILE];
-    uint8_t k[2][TcShape<D>::TILE];
+    uint8_t hi[TcShape<D>::TILE], lo[TcShape<D>::TILE];   // scale * code of the keys
     uint8_t v[2][TcShape<D>::TILE];
+    // group sums of q and minima of the keys: [128][16] fp16 in 8 x 8 blocks of 128 bytes
+    uint8_t qx[2][4096], kx[4096];
     uint32_t nan_groups[kTcRows];    // groups of the row's output that a NaN value reached
-    uint8_t have[2][8];              // per 16 keys of a stage: records present
+    uint8_t have[2][8];              // per 16 keys of a tile (even, odd): records present
     uint32_t tmem;
     int abort;
     TcBars bar;
@@ -59,19 +68,10 @@ __device__ __forceinline__ void tc_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(tc::smem_u32(bar)) : "memory");
 }
 // Bounded wait by a warp; false once any thread of the CTA has given up.
+template <int SLEEP_NS = 0>
 __device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    bool ok = try_wait_long(bar, parity);
-    if (!ok) {
-        uint64_t t0, t;
-        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
-        while (!(ok = try_wait_long(bar, parity))) {
-            asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-            if (*abort || t - t0 > kCopyWaitNs) {
-                *abort = 1;
-                break;
-            }
-        }
-    }
+    const bool ok = wait_bounded_poll<SLEEP_NS>(bar, parity, abort);
+    if (!ok) *abort = 1;
     return __all_sync(0xffffffffu, ok) != 0;
 }
 
@@ -94,6 +94,11 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&r)[16])
                     "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
                     "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
+__device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+                    "r"(r[6]), "r"(r[7]) : "memory");
+}
 __device__ __forceinline__ float tc_ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -102,17 +107,20 @@ __device__ __forceinline__ float tc_ex2(float x) {
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<const __half2 *>(&u); }
 
-// minimum + scale * code for the nibble pairs (i, i + 4) of a word, i = 0..3.  A code is
-// taken as 1024 + u (fp16, exact), less 1024; the sum is rounded once and kept finite.
-__device__ __forceinline__ uint4 unpack_word(uint32_t w, __half2 s, __half2 m) {
-    const __half2 k1024 = __floats2half2_rn(1024.f, 1024.f), top = __floats2half2_rn(65504.f, 65504.f);
-    uint32_t r[4];
+// Descriptor of such a [128][16] operand: K-major without swizzle, 128 bytes between the two
+// blocks of a row group, 256 to the next eight rows.
+__device__ __forceinline__ uint64_t desc_x(const uint8_t *p) {
+    return (uint64_t)((tc::smem_u32(p) >> 4) & 0x3FFFu) | (uint64_t)(128 >> 4) << 16 |
+           (uint64_t)(256 >> 4) << 32 | (uint64_t)1u << 46;
+}
+__device__ __forceinline__ uint32_t at_x(int row, int half) { return (row >> 3) * 256 + half * 128 + (row & 7) * 16; }
+
+// Codes of the nibble pairs (i, i + 4) of a word, i = 0..3, as fp16: 1024 + u, less 1024.
+__device__ __forceinline__ void codes_of(uint32_t w, __half2 (&u)[4]) {
+    const __half2 k1024 = __floats2half2_rn(1024.f, 1024.f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2 u = __hsub2(bits_h2(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u), k1024);
-        r[i] = h2_bits(__hmin2_nan(__hfma2(u, s, m), top));
-    }
-    return make_uint4(r[0], r[1], r[2], r[3]);
+    for (int i = 0; i < 4; ++i)
+        u[i] = __hsub2(bits_h2(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u), k1024);
 }
 __device__ __forceinline__ bool pair_nonfinite(uint32_t w) {
     return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
@@ -155,9 +163,11 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
     }
     if (tid == 0) {
         S.abort = 0;
+        tc::mbar_init(&S.bar.k_full, kTcUnpackWarps);
+        tc::mbar_init(&S.bar.k_free, 1);
         for (int x = 0; x < 2; ++x) {
-            tc::mbar_init(&S.bar.full[x], kTcUnpackWarps);
-            tc::mbar_init(&S.bar.empty[x], 1);
+            tc::mbar_init(&S.bar.v_full[x], kTcUnpackWarps);
+            tc::mbar_init(&S.bar.v_free[x], 1);
             tc::mbar_init(&S.bar.s_full[x], 1);
             tc::mbar_init(&S.bar.p_full[x], 4);
             tc::mbar_init(&S.bar.pv[x], 1);
@@ -184,19 +194,41 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
             for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(f[e]));
         }
         if (row >= rows) mx = 0.f;
-        const int ex = mx < INFINITY ? min(11 + 127 - (int)(__float_as_uint(mx) >> 23), 120) : 0;
+        const int ex = mx < INFINITY ? min(6 + 127 - (int)(__float_as_uint(mx) >> 23), 120) : 0;
         const float up = __int_as_float((127 + ex) << 23) * (scale < 0.f ? -1.f : 1.f);
-        fac = fabsf(scale) * 1.4426950408889634f * __int_as_float((127 - ex) << 23);
+        // never 0, so that a masked score stays -inf
+        fac = fmaxf(fabsf(scale) * 1.4426950408889634f * __int_as_float((127 - ex) << 23), 1e-37f);
+        __half hi[8] = {}, lo[8] = {};            // sums of q over each group, as pairs
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-            float f[8];
-            unpack8(row < rows ? reinterpret_cast<const uint4 *>(src)[c] : make_uint4(0, 0, 0, 0), f);
+        for (int g = 0; g < NG; ++g) {
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 4 * g; c < 4 * g + 4; ++c) {
+                float f[8];
+                unpack8(row < rows ? reinterpret_cast<const uint4 *>(src)[c] : make_uint4(0, 0, 0, 0), f);
+                uint4 u;
+                uint32_t *w = &u.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __half2 h = __floats2half2_rn(f[e] * up, f[e + 4] * up);
+                    sum += __low2float(h) + __high2float(h);
+                    w[e] = h2_bits(h);
+                }
+                *reinterpret_cast<uint4 *>(S.q[rt] + (c >> 3) * T::BLK + tc::swz(tid & 127, c & 7)) = u;
+            }
+            hi[g] = __float2half_rn(sum);
+            lo[g] = __float2half_rn(sum - __half2float(hi[g]));
+        }
+        // columns 0..7: hi of the groups, 8..15: lo
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
             uint4 u;
-            u.x = h2_bits(__floats2half2_rn(f[0] * up, f[4] * up));
-            u.y = h2_bits(__floats2half2_rn(f[1] * up, f[5] * up));
-            u.z = h2_bits(__floats2half2_rn(f[2] * up, f[6] * up));
-            u.w = h2_bits(__floats2half2_rn(f[3] * up, f[7] * up));
-            *reinterpret_cast<uint4 *>(S.q[rt] + (c >> 3) * T::BLK + tc::swz(tid & 127, c & 7)) = u;
+            uint32_t *w = &u.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = half ? h2_bits(__halves2half2(lo[2 * e], lo[2 * e + 1]))
+                            : h2_bits(__halves2half2(hi[2 * e], hi[2 * e + 1]));
+            *reinterpret_cast<uint4 *>(S.qx[rt] + at_x(tid & 127, half)) = u;
         }
         tc::fence_async_smem();
     }
@@ -209,73 +241,78 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
         const uint32_t tS = tmem + 256 * rt + ((uint32_t)(32 * (warp & 3)) << 16), tO = tS + 128;
         const int see = row < rows ? len - m + row / G + 1 : 0x7fffffff;   // keys this row sees
         // (rows past the end compute on zeros and are not stored)
-        const int see_first = len - m + min(row0 + 128 * rt, rows - 1) / G + 1;
+        const int see_first = min(len - m + min(row0 + 128 * rt, rows - 1) / G + 1, see_last);
         float ref = -INFINITY, l = 0.f;
         bool ok = true;
         for (int t = 0; t < steps; ++t) {
             if (!(ok = tc_wait(&S.bar.s_full[rt], t & 1, abort))) break;
             tc::fence_after_sync();
             const uint2 have = *reinterpret_cast<const uint2 *>(S.have[t & 1]);
-            const bool full = 128 * (t + 1) <= see_first && (have.x & have.y) == 0x01010101u;
-            // what this row may use of the tile: its first `cnt` keys, in present blocks
-            const int cnt = min(see, see_last) - 128 * t;
-            float mx = -INFINITY;
+            if (128 * (t + 1) > see_first || (have.x & have.y) != 0x01010101u) {
+                // keys this row may not use get a score of -inf: those past the ones it sees,
+                // and blocks whose records are not there
+                const int cnt = min(see, see_last) - 128 * t;
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    const int stay = (((c < 4 ? have.x : have.y) >> (8 * (c & 3))) & 1u) ? cnt - 16 * c : 0;
+                    float v[16];
+                    tc::tmem_ld16(tS + 16 * c, v);
+                    tc::tmem_wait_ld();
+                    uint32_t u[16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float s[32];
-                tc::tmem_ld32(tS + 32 * c, s);
-                tc::tmem_wait_ld();
-                if (full) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) mx = fmaxf(mx, s[j]);
-                } else {
-                    const uint32_t h = c < 2 ? have.x : have.y;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (32 * c + j < cnt && ((h >> (8 * ((2 * c + (j >> 4)) & 3))) & 1u)) mx = fmaxf(mx, s[j]);
+                    for (int j = 0; j < 16; ++j) u[j] = j < stay ? __float_as_uint(v[j]) : 0xff800000u;
+                    tc_st16(tS + 16 * c, u);
                 }
+                tc::tmem_wait_st();
             }
-            mx *= fac;
+            // two passes over the scores, each load issued one chunk of 16 ahead
+            float s[2][16];
+            tc::tmem_ld16(tS, s[0]);
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                tc::tmem_wait_ld();
+                tc::tmem_ld16(tS + 16 * ((c + 1) & 7), s[(c + 1) & 1]);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) m4[j & 3] = fmaxf(m4[j & 3], s[c & 1][j]);
+            }
+            const float mx = fac * fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
             const bool move = mx > ref + kTcSlack;
             if (__any_sync(0xffffffffu, move)) {
                 const float keep = move ? tc_ex2(ref - mx) : 1.f;
                 if (move) ref = mx;
                 l *= keep;
                 if (t > 0) {
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        float v[32];
-                        tc::tmem_ld32(tO + 32 * c, v);
+                    tc::tmem_wait_ld();
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        float v[16];
+                        tc::tmem_ld16(tO + 16 * c, v);
                         tc::tmem_wait_ld();
+                        uint32_t u[16];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] *= keep;
-                        tc::tmem_st32(tO + 32 * c, v);
+                        for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(v[j] * keep);
+                        tc_st16(tO + 16 * c, u);
                     }
                     tc::tmem_wait_st();
                 }
             }
-            const float sub = ref == -INFINITY ? 0.f : -ref;
+            const float sub = ref == -INFINITY ? 0.f : kTcLift - ref;
             float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float s[32];
-                tc::tmem_ld32(tS + 32 * c, s);
+            for (int c = 0; c < 8; ++c) {
                 tc::tmem_wait_ld();
+                if (c < 7) tc::tmem_ld16(tS + 16 * (c + 1), s[(c + 1) & 1]);
+                float *x = s[c & 1];
+                uint32_t p[8];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) s[j] = tc_ex2(fmaf(s[j], fac, sub));
-                if (!full) {
-                    const uint32_t h = c < 2 ? have.x : have.y;
+                for (int j = 0; j < 16; ++j) x[j] = tc_ex2(fmaf(x[j], fac, sub));
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (!(32 * c + j < cnt && ((h >> (8 * ((2 * c + (j >> 4)) & 3))) & 1u))) s[j] = 0.f;
+                for (int j = 0; j < 8; ++j) {
+                    p[j] = h2_bits(__floats2half2_rn(x[2 * j], x[2 * j + 1]));
+                    ls[j & 3] += x[2 * j] + x[2 * j + 1];
                 }
-                uint32_t p[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    p[j] = h2_bits(__floats2half2_rn(s[2 * j], s[2 * j + 1]));
-                    ls[j & 3] += s[2 * j] + s[2 * j + 1];
-                }
-                tc_st16(tS + 16 * c, p);       // over scores that this thread has read
+                tc_st8(tS + 8 * c, p);         // over scores that this thread has read
             }
             l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
             tc::tmem_wait_st();
@@ -318,11 +355,11 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
                 }
             }
             if (lse && row < rows)
-                lse[t * Hq + hq] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+                lse[t * Hq + hq] = l == 0.f ? -INFINITY : (ref - kTcLift + log2f(l)) * 0.6931471805599453f;
         }
     } else if (warp < kTcSoftWarps + kTcUnpackWarps) {
-        // ---- unpacking: this warp has keys 16 w .. +15 of each tile; lane (r, x) takes 16
-        // bytes (D = 128) of the codes of keys r and r + 8
+        // ---- unpacking: this warp has keys 16 w .. +15 of each tile, then their values; lane
+        // (r, x) takes a quarter of the codes of records r and r + 8
         const int w = warp - kTcSoftWarps, r = lane >> 2, x = lane & 3;
         constexpr int NW = D / 32;               // words of codes a lane takes
         const int32_t *table = kv.table + (int64_t)n * kv.table_width;
@@ -331,115 +368,143 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
         const int64_t to_v = kv.block(0, 1, hkv, REC) - base;
         const int slot_mask = (1 << kv.page_log2) - 1;
         uint32_t code[2][2][NW], par[2][2][NG];  // [keys / values][r, r + 8]
-        auto fetch = [&](int t, int page) {
-            const int j = 128 * t + 16 * w;
-            const bool want = j < see_last && page >= 0 && page < kv.pages;
-            if (j < see_last && !want && lane == 0) report(status, GDN_ERR_INDEX);
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const uint8_t *rec = base + (int64_t)page * page_bytes + ((j & slot_mask) + r + 8 * y) * REC;
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const uint8_t *p = rec + (z ? to_v : 0);
-                    // a record past the tile's last key reads as zeros, like one not there
-                    const bool in = want && j + r + 8 * y < see_last;
-                    if constexpr (D == 128) {
-                        const uint4 a = in ? *reinterpret_cast<const uint4 *>(p + 16 * x) : make_uint4(0, 0, 0, 0);
-                        const uint4 b = in ? *reinterpret_cast<const uint4 *>(p + R::CODES) : make_uint4(0, 0, 0, 0);
-                        code[z][y][0] = a.x; code[z][y][1] = a.y; code[z][y][2] = a.z; code[z][y][3] = a.w;
-                        par[z][y][0] = b.x; par[z][y][1] = b.y; par[z][y][2] = b.z; par[z][y][3] = b.w;
-                    } else {
-                        const uint2 a = in ? *reinterpret_cast<const uint2 *>(p + 8 * x) : make_uint2(0, 0);
-                        const uint2 b = in ? *reinterpret_cast<const uint2 *>(p + R::CODES) : make_uint2(0, 0);
-                        code[z][y][0] = a.x; code[z][y][1] = a.y;
-                        par[z][y][0] = b.x; par[z][y][1] = b.y;
-                    }
-                }
-            }
-            return want;
-        };
         auto lookup = [&](int t) {
             const int j = 128 * t + 16 * w;
-            return j < see_last ? table[j >> kv.page_log2] : -1;
+            return j < see_last ? table[j >> kv.page_log2] : -2;
         };
-        int page = steps > 0 ? lookup(0) : -1;
-        bool there = steps > 0 && fetch(0, page);
-        page = lookup(1);
+        // keys (u = 0) or values (1) of tile t; records that are not there, or past the last key
+        // the tile's rows see, read as zeros
+        auto fetch = [&](int t, int u, int pg) {
+            const int j = 128 * t + 16 * w;
+            const bool want = pg >= 0 && pg < kv.pages;
+            if (!want && pg != -2 && u == 0 && lane == 0) report(status, GDN_ERR_INDEX);
+            const uint8_t *rec = base + (int64_t)pg * page_bytes + (u ? to_v : 0) + ((j & slot_mask) + r) * REC;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const uint8_t *p = rec + 8 * y * REC;
+                const bool in = want && j + r + 8 * y < see_last;
+                if constexpr (D == 128) {
+                    const uint4 a = in ? *reinterpret_cast<const uint4 *>(p + 16 * x) : make_uint4(0, 0, 0, 0);
+                    const uint4 b = in ? *reinterpret_cast<const uint4 *>(p + R::CODES) : make_uint4(0, 0, 0, 0);
+                    code[u][y][0] = a.x; code[u][y][1] = a.y; code[u][y][2] = a.z; code[u][y][3] = a.w;
+                    par[u][y][0] = b.x; par[u][y][1] = b.y; par[u][y][2] = b.z; par[u][y][3] = b.w;
+                } else {
+                    const uint2 a = in ? *reinterpret_cast<const uint2 *>(p + 8 * x) : make_uint2(0, 0);
+                    const uint2 b = in ? *reinterpret_cast<const uint2 *>(p + R::CODES) : make_uint2(0, 0);
+                    code[u][y][0] = a.x; code[u][y][1] = a.y;
+                    par[u][y][0] = b.x; par[u][y][1] = b.y;
+                }
+            }
+        };
+        int page = steps > 0 ? lookup(0) : -2;
+        if (steps > 0) {
+            fetch(0, 0, page);
+            fetch(0, 1, page);
+        }
         const int first_row_sees = len - m + row0 / G + 1;
         for (int t = 0; t < steps; ++t) {
             const int s = t & 1;
-            if (t >= 2 && !tc_wait(&S.bar.empty[s], ((t >> 1) & 1) ^ 1, abort)) break;
-            if (128 * (t + 1) > first_row_sees) {
-                // some row does not see some key of this tile: a non-finite value pair would
-                // reach it through its zero weight, so such a group is zeroed here and made
-                // NaN in just the rows that see the key
+            const int page_next = lookup(t + 1);
+            if (t >= 1 && !tc_wait<100>(&S.bar.k_free, (t - 1) & 1, abort)) break;
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+                for (int y = 0; y < 2; ++y) {
+                    // word x NG + g is elements 32 g + 8 x ..: 16-byte chunk 4 g + x
+                    const int key = 16 * w + r + 8 * y;
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
-                        if (!pair_nonfinite(par[1][y][g])) continue;
-                        const int j = 128 * t + 16 * w + r + 8 * y;
-                        if (x == 0)
-                            for (int i = 0; i < kTcRows && row0 + i < rows; ++i)
-                                if (j < len - m + (row0 + i) / G + 1) atomicOr(S.nan_groups + i, 1u << g);
-                        par[1][y][g] = 0u;
+                        const __half2 sc = __low2half2(bits_h2(par[0][y][g]));
+                        __half2 c[4];
+                        codes_of(code[0][y][g], c);
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __half2 h = __hmul2(c[i], sc);
+                            hi[i] = h2_bits(h);
+                            lo[i] = h2_bits(__hfma2(c[i], sc, __hneg2(h)));
+                        }
+                        const uint32_t at = ((4 * g + x) >> 3) * T::BLK + tc::swz(key, (4 * g + x) & 7);
+                        *reinterpret_cast<uint4 *>(S.hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(S.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-            }
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int key = 16 * w + r + 8 * y;
-                // keys: word x NG + g is elements 32 g + 8 x ..: 16-byte chunk 4 g + x
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const __half2 p = bits_h2(par[0][y][g]);
-                    const int c = 4 * g + x;
-                    *reinterpret_cast<uint4 *>(S.k[s] + (c >> 3) * T::BLK + tc::swz(key, c & 7)) =
-                        unpack_word(code[0][y][g], __low2half2(p), __high2half2(p));
-                }
-                // values: word W is chunk W; its low nibbles are of group 2 (W / 8), its high of the next
-#pragma unroll
-                for (int e = 0; e < NW; ++e) {
-                    const int W = NW * x + e;
-                    uint32_t a, b;
-                    if constexpr (NG == 4) {
-                        a = x < 2 ? par[1][y][0] : par[1][y][2];
-                        b = x < 2 ? par[1][y][1] : par[1][y][3];
-                    } else {
-                        a = par[1][y][0];
-                        b = par[1][y][1];
+                    if (x < 2) {                 // the minima, against the sums' hi and lo
+                        uint4 v = make_uint4(__byte_perm(par[0][y][0], par[0][y][1], 0x7632), 0u, 0u, 0u);
+                        if (NG == 4) v.y = __byte_perm(par[0][y][NG - 2], par[0][y][NG - 1], 0x7632);
+                        *reinterpret_cast<uint4 *>(S.kx + at_x(key, x)) = v;
                     }
-                    *reinterpret_cast<uint4 *>(S.v[s] + (W >> 3) * T::BLK + tc::swz(key, W & 7)) =
-                        unpack_word(code[1][y][e], bits_h2(__byte_perm(a, b, 0x5410)), bits_h2(__byte_perm(a, b, 0x7632)));
                 }
-            }
-            if (lane == 0) S.have[s][w] = there ? 1 : 0;
+                if (lane == 0) S.have[s][w] = page >= 0 && page < kv.pages ? 1 : 0;
+                if (t + 1 < steps) fetch(t + 1, 0, page_next);
             tc::fence_async_smem();
             __syncwarp();
-            if (lane == 0) tc_arrive(&S.bar.full[s]);
-            if (t + 1 < steps) {
-                there = fetch(t + 1, page);
-                page = lookup(t + 2);
-            }
+            if (lane == 0) tc_arrive(&S.bar.k_full);
+            if (t >= 2 && !tc_wait<100>(&S.bar.v_free[s], ((t >> 1) & 1) ^ 1, abort)) break;
+                if (128 * (t + 1) > first_row_sees) {
+                    // some row does not see some key of this tile: a non-finite value pair would
+                    // reach it through its zero weight, so such a group is zeroed here and made
+                    // NaN in just the rows that see the key
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            if (!pair_nonfinite(par[1][y][g])) continue;
+                            const int j = 128 * t + 16 * w + r + 8 * y;
+                            if (x == 0)
+                                for (int i = 0; i < kTcRows && row0 + i < rows; ++i)
+                                    if (j < len - m + (row0 + i) / G + 1) atomicOr(S.nan_groups + i, 1u << g);
+                            par[1][y][g] = 0u;
+                        }
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    // word W is chunk W; its low nibbles are of group 2 (W / 8), its high of the next
+                    const int key = 16 * w + r + 8 * y;
+                    const uint32_t a = NG == 4 && x >= 2 ? par[1][y][NG - 2] : par[1][y][0];
+                    const uint32_t b = NG == 4 && x >= 2 ? par[1][y][NG - 1] : par[1][y][1];
+                    const __half2 sc = bits_h2(__byte_perm(a, b, 0x5410)), mn = bits_h2(__byte_perm(a, b, 0x7632));
+                    const __half2 top = __floats2half2_rn(65504.f, 65504.f);
+#pragma unroll
+                    for (int e = 0; e < NW; ++e) {
+                        const int W = NW * x + e;
+                        __half2 c[4];
+                        codes_of(code[1][y][e], c);
+                        uint32_t v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = h2_bits(__hmin2_nan(__hfma2(c[i], sc, mn), top));
+                        *reinterpret_cast<uint4 *>(S.v[s] + (W >> 3) * T::BLK + tc::swz(key, W & 7)) =
+                            make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+                if (t + 1 < steps) fetch(t + 1, 1, page_next);
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tc_arrive(&S.bar.v_full[s]);
+            page = page_next;
         }
     } else {
         // ---- products.  P V of a tile completes before the next scores overwrite P.
         constexpr uint32_t idS = idesc_f16(128, 128, 0), idO = idesc_f16(128, D, 1);
-        auto scores = [&](int t, int i) {
-            const uint32_t a = tc::smem_u32(S.q[i]), b = tc::smem_u32(S.k[t & 1]);
+        auto scores = [&](int i) {
+            const uint32_t a = tc::smem_u32(S.q[i]), h = tc::smem_u32(S.hi), l = tc::smem_u32(S.lo);
+            tc::mma_bf16_warp(tmem + 256 * i, desc_x(S.qx[i]), desc_x(S.kx), idS, 0);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 const uint32_t off = (ks >> 2) * T::BLK + (ks & 3) * 32;
-                tc::mma_bf16_warp(tmem + 256 * i, tc::sdesc(a + off, 16, 1024), tc::sdesc(b + off, 16, 1024), idS, ks > 0);
+                const uint64_t da = tc::sdesc(a + off, 16, 1024);
+                tc::mma_bf16_warp(tmem + 256 * i, da, tc::sdesc(h + off, 16, 1024), idS, 1);
+                tc::mma_bf16_warp(tmem + 256 * i, da, tc::sdesc(l + off, 16, 1024), idS, 1);
             }
             tc::mma_commit_warp(&S.bar.s_full[i]);
+            if (i == 1) tc::mma_commit_warp(&S.bar.k_free);
         };
-        bool ok = steps > 0 && tc_wait(&S.bar.full[0], 0, abort);
+        bool ok = steps > 0 && tc_wait(&S.bar.k_full, 0, abort);
         if (ok) {
             tc::fence_after_sync();
-            scores(0, 0);
-            scores(0, 1);
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) scores(i);
         }
         for (int t = 0; t < steps && ok; ++t) {
+            if (!(ok = tc_wait(&S.bar.v_full[t & 1], (t >> 1) & 1, abort))) break;
+#pragma unroll 1
             for (int i = 0; i < 2 && ok; ++i) {
                 if (!(ok = tc_wait(&S.bar.p_full[i], t & 1, abort))) break;
                 tc::fence_after_sync();
@@ -449,12 +514,12 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
                     mma_ts(tmem + 256 * i + 128, tmem + 256 * i + 8 * ks, tc::sdesc(b + ks * 2048, T::BLK, 1024), idO,
                            t > 0 || ks > 0);
                 tc::mma_commit_warp(&S.bar.pv[i]);
-                if (i == 1) tc::mma_commit_warp(&S.bar.empty[t & 1]);
+                if (i == 1) tc::mma_commit_warp(&S.bar.v_free[t & 1]);
                 if (t + 1 < steps) {
-                    if (i == 0 && !(ok = tc_wait(&S.bar.full[(t + 1) & 1], ((t + 1) >> 1) & 1, abort))) break;
+                    if (i == 0 && !(ok = tc_wait(&S.bar.k_full, (t + 1) & 1, abort))) break;
                     if (!(ok = tc_wait(&S.bar.pv[i], t & 1, abort))) break;
                     tc::fence_after_sync();
-                    scores(t + 1, i);
+                    scores(i);
                 }
             }
         }

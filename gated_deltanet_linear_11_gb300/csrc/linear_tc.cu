@@ -150,18 +150,10 @@ __device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
 // Bounded wait on an mbarrier phase.  Gives up when the bound has passed or another thread
 // of the CTA has given up; every role then leaves its loop.
 __device__ __forceinline__ bool lin_wait(LinSmem &S, uint64_t *bar, uint32_t parity) {
-    if (try_wait_long(bar, parity)) return true;
-    uint64_t t0, t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
     volatile int *abort = &S.abort;
-    while (!try_wait_long(bar, parity)) {
-        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-        if (*abort || t - t0 > kCopyWaitNs) {
-            *abort = 1;
-            return false;
-        }
-    }
-    return true;
+    const bool ok = wait_bounded_poll<0>(bar, parity, abort);
+    if (!ok) *abort = 1;
+    return ok;
 }
 
 // The same by a whole warp, which stays together whatever its lanes saw.
