@@ -98,7 +98,6 @@ struct LinBars {
     uint64_t qk[2], qs[2], kv[2], pv[2]; // products done (two: by the buffers they read)
     uint64_t gates;                      // this chunk's gate arrays are written
     uint64_t r_kt[2], r_p, r_s, r_o, r_arr;   // every elementwise warp: operands written, arrays read
-    uint64_t lanes[4];                   // the four warps that share 32 TMEM lanes
     uint64_t kf[3], vf[4];               // range pass: tiles free
     uint64_t fin;
 };
@@ -149,27 +148,18 @@ __device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
 
 // Bounded wait on an mbarrier phase.  Gives up when the bound has passed or another thread
 // of the CTA has given up; every role then leaves its loop.
+template <int SLEEP_NS = 0>
 __device__ __forceinline__ bool lin_wait(LinSmem &S, uint64_t *bar, uint32_t parity) {
     volatile int *abort = &S.abort;
-    const bool ok = wait_bounded_poll<0>(bar, parity, abort);
+    const bool ok = wait_bounded_poll<SLEEP_NS>(bar, parity, abort);
     if (!ok) *abort = 1;
     return ok;
 }
 
 // The same by a whole warp, which stays together whatever its lanes saw.
+template <int SLEEP_NS = 0>
 __device__ __forceinline__ bool warp_wait(LinSmem &S, uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, lin_wait(S, bar, parity)) != 0;
-}
-
-// Meeting of the four warps that share 32 TMEM lanes (bounded, unlike a named barrier).
-__device__ __forceinline__ bool lanes_sync(LinSmem &S, int lq, uint32_t &phase) {
-    tc::fence_before_sync();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&S.bar.lanes[lq]);
-    const bool ok = warp_wait(S, &S.bar.lanes[lq], phase);
-    phase ^= 1;
-    tc::fence_after_sync();
-    return ok;
+    return __all_sync(0xffffffffu, lin_wait<SLEEP_NS>(S, bar, parity)) != 0;
 }
 
 // The TMEM accesses of this warp (waited for) happen before the arrival.
@@ -210,7 +200,8 @@ __device__ __forceinline__ void product(uint32_t d, const uint8_t *a, const uint
     }
 }
 
-// The same with A in TMEM: 128 lanes, two of the depth's elements a word; B MN-major.
+// The same with A in TMEM: 128 lanes, two of the depth's elements a word, 32 elements in the
+// first 16 of each 32 columns; B MN-major.
 __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, const uint8_t *b, bool add) {
     constexpr uint32_t id = tc::idesc_bf16(128, 128, 0, 1);
     const uint32_t b0 = tc::smem_u32(b);
@@ -221,7 +212,7 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, const uint8_t
                      "elect.sync _|e, 0xffffffff;\n\t"
                      "setp.ne.b32 p, %4, 0;\n\t"
                      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                     :: "r"(d), "r"(a + 8 * ks), "l"(db), "r"(id), "r"((uint32_t)(add || ks > 0)) : "memory");
+                     :: "r"(d), "r"(a + 32 * (ks >> 1) + 8 * (ks & 1)), "l"(db), "r"(id), "r"((uint32_t)(add || ks > 0)) : "memory");
     }
 }
 
@@ -283,9 +274,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
                     "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
 
-// The bf16 pair hi, lo of w_j k_j, transposed: TMEM lane d, word j / 2 of 64 for hi and the
-// next 64 for lo, zero for tokens j >= L.  This warp takes d = 32 lq .. and j = 32 jb ..;
-// ldmatrix hands it 8 x 8 blocks transposed, in the layout the 16-lane store wants.
+// The bf16 pair hi, lo of w_j k_j, transposed: TMEM lane d; of each 32 columns, 16 words of
+// hi for 32 tokens, then 16 of lo; zero for tokens j >= L.  This warp takes d = 32 lq .. and
+// j = 32 jb .., so it writes only columns that it alone has read before; ldmatrix hands it
+// 8 x 8 blocks transposed, in the layout the 16-lane store wants.
 template <bool TAIL>
 __device__ __forceinline__ void weigh_keys(const uint8_t *k, uint32_t tmem, int lq, int jb, const float *w,
                                            int L) {
@@ -324,9 +316,9 @@ __device__ __forceinline__ void weigh_keys(const uint8_t *k, uint32_t tmem, int 
                 lo[4 * tp + e] = r;
             }
         }
-        const uint32_t at = tmem + ((uint32_t)(32 * lq + 16 * th) << 16) + 16 * jb;
+        const uint32_t at = tmem + ((uint32_t)(32 * lq + 16 * th) << 16) + 32 * jb;
         tmem_st_16x128b_x4(at, hi);
-        tmem_st_16x128b_x4(at + 64, lo);
+        tmem_st_16x128b_x4(at + 16, lo);
     }
     tc::tmem_wait_st();
 }
@@ -403,7 +395,6 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                             &b.kv[0], &b.pv[0], &b.pv[1], &b.gates, &b.fin})
             tc::mbar_init(x, 1);
         for (uint64_t *x : {&b.r_kt[0], &b.r_kt[1], &b.r_p, &b.r_s, &b.r_o, &b.r_arr}) tc::mbar_init(x, kLinWarps);
-        for (int x = 0; x < 4; ++x) tc::mbar_init(&b.lanes[x], 4);
         tc::mbar_fence_init();
     }
     tc::fence_before_sync();
@@ -434,15 +425,14 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             store_row(sS, jb, row, st);
             warp_arrive(&S.bar.r_s);
         }
-        uint32_t lanes_ph = 0;
         for (int i = 0; i < count; ++i) {
             // a buffer of two serves every other chunk
             const uint32_t ph = i & 1, ph2 = (i >> 1) & 1;
             const int t = t0 + (c_first + i) * kLinC;
             const int L = min(kLinC, t0 + len - t);
-            // ---- A: weighted keys, over the P V that the four warps have read
-            if (!warp_wait(S, &S.bar.gates, ph) || !warp_wait(S, &S.bar.k[ph], ph2)) break;
-            if (!lanes_sync(S, lq, lanes_ph)) break;
+            // ---- A: weighted keys, over the P V that this warp has read (the gates' warp has
+            // seen the keys' tile arrive)
+            if (!warp_wait(S, &S.bar.gates, ph)) break;
             if (L == kLinC) {
                 weigh_keys<false>(S.tile[2 + ph], tmem + colOa, lq, jb, S.w, L);
             } else {
@@ -486,8 +476,7 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             uint32_t pk[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) pk[j] = pack_bf2(v[2 * j], v[2 * j + 1]);
-            if (!lanes_sync(S, lq, lanes_ph)) break;   // P goes over scores that the other three warps read
-            tmem_st16(tmem + ((uint32_t)(32 * lq) << 16) + colSc + 16 * jb, pk);
+            tmem_st16(tm + colSc, pk);       // over scores that this warp has read
             tc::tmem_wait_st();
             warp_arrive_tmem(&S.bar.r_p);
             if (lane == 0) mbar_arrive(&S.bar.r_arr);
@@ -498,26 +487,30 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             tc::tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 32; ++j) st[j] = fmaf(decay, st[j], v[j]);
-            if (!warp_wait(S, &S.bar.qs[ph], ph2)) break;
-            store_row(sS, jb, row, st);
+            store_row(sS, jb, row, st);      // Q S came before the keys' product: it is done
+
             warp_arrive(&S.bar.r_s);
             // ---- D: output, 64 bytes of a row a thread
             if (!warp_wait(S, &S.bar.pv[ph], ph2)) break;
             tc::fence_after_sync();
             bf16 *dst = p.o + (int64_t)(t + row) * p.o_tok + (int64_t)hv * 128 + 32 * jb;
+            float a[16];
+            tc::tmem_ld16(tm + colOi, a);
+            tc::tmem_ld16(tm + colOa, v);
+            tc::tmem_wait_ld();
+            uint32_t u[8];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float a[16];
-                tc::tmem_ld16(tm + colOi + 16 * c, a);
-                tc::tmem_ld16(tm + colOa + 16 * c, v);
-                tc::tmem_wait_ld();
-                if (c == 1) warp_arrive_tmem(&S.bar.r_o);
-                uint32_t u[8];
+            for (int e = 0; e < 8; ++e)
+                u[e] = pack_bf2(fmaf(eg, a[2 * e], v[2 * e]), fmaf(eg, a[2 * e + 1], v[2 * e + 1]));
+            tc::tmem_ld16(tm + colOi + 16, a);
+            tc::tmem_ld16(tm + colOa + 16, v);
+            if (row < L) store_32b(dst, u);
+            tc::tmem_wait_ld();
+            warp_arrive_tmem(&S.bar.r_o);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    u[e] = pack_bf2(fmaf(eg, a[2 * e], v[2 * e]), fmaf(eg, a[2 * e + 1], v[2 * e + 1]));
-                if (row < L) store_32b(dst + 16 * c, u);
-            }
+            for (int e = 0; e < 8; ++e)
+                u[e] = pack_bf2(fmaf(eg, a[2 * e], v[2 * e]), fmaf(eg, a[2 * e + 1], v[2 * e + 1]));
+            if (row < L) store_32b(dst + 16, u);
         }
         if (last && p.hT && !*(volatile int *)&S.abort) {
             float4 *out = reinterpret_cast<float4 *>(p.hT + ((int64_t)n * p.Hv + hv) * 16384 + st_off);
@@ -543,7 +536,7 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             if (!warp_wait(S, &S.bar.r_kt[ph], ph2) || !warp_wait(S, &S.bar.v[ph], ph2)) break;
             tc::fence_after_sync();
             product_ts(tmem + colD, tmem + colOa, sV, false);
-            product_ts(tmem + colD, tmem + colOa + 64, sV, true);
+            product_ts(tmem + colD, tmem + colOa + 16, sV, true);
             tc::mma_commit_warp(&S.bar.kv[0]);
             // the keys' columns take P V next
             if (!warp_wait(S, &S.bar.r_p, ph) || !warp_wait(S, &S.bar.kv[0], ph)) break;
@@ -564,13 +557,13 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             for (int i = 0; i < count; ++i) {
                 const uint32_t b = i & 1, was = ((i >> 1) & 1) ^ 1;   // chunk i - 2's use of the buffer
                 const int t = t0 + (c_first + i) * kLinC;
-                if (i >= 2 && (!lin_wait(S, &S.bar.qk[b], was) || !lin_wait(S, &S.bar.r_kt[b], was))) break;
+                if (i >= 2 && (!lin_wait<100>(S, &S.bar.qk[b], was) || !lin_wait<100>(S, &S.bar.r_kt[b], was))) break;
                 load_tile(S.tile[2 + b], &maps.k, &S.bar.k[b], hk, t);
                 ++nk;
-                if (i >= 2 && !lin_wait(S, &S.bar.qs[b], was)) break;
+                if (i >= 2 && !lin_wait<100>(S, &S.bar.qs[b], was)) break;
                 load_tile(S.tile[b], &maps.q, &S.bar.q[b], hk, t);
                 ++nq;
-                if (i >= 2 && !lin_wait(S, &S.bar.pv[b], was)) break;
+                if (i >= 2 && !lin_wait<100>(S, &S.bar.pv[b], was)) break;
                 load_tile(S.tile[4 + b], &maps.v, &S.bar.v[b], hv, t);
                 ++nv;
             }
@@ -595,7 +588,8 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             float y[4];
             const int t = t0 + (c_first + i + 1) * kLinC;
             if (i + 1 < count) load_gates(p, hv, t, min(kLinC, t0 + len - t), y);
-            if (i > 0 && !warp_wait(S, &S.bar.r_arr, (i & 1) ^ 1)) break;
+            if (i > 0 && !warp_wait<100>(S, &S.bar.r_arr, (i & 1) ^ 1)) break;
+            if (!warp_wait<100>(S, &S.bar.k[i & 1], (i >> 1) & 1)) break;
             const float end = below + pre[3];
             const float ref = __shfl_sync(0xffffffffu, end, lane | 7) * kLog2E;
 #pragma unroll
@@ -693,7 +687,7 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             if (!warp_wait(S, &S.bar.r_kt[bf], (i >> 1) & 1) || !warp_wait(S, &S.bar.v[vb], (i >> 2) & 1)) break;
             tc::fence_after_sync();
             product_ts(tmem, tmem + 128 + 128 * bf, S.tile[3 + vb], i > 0);
-            product_ts(tmem, tmem + 192 + 128 * bf, S.tile[3 + vb], true);
+            product_ts(tmem, tmem + 144 + 128 * bf, S.tile[3 + vb], true);
             tc::mma_commit_warp(&S.bar.kv[bf]);
             tc::mma_commit_warp(&S.bar.vf[vb]);
         }
@@ -704,10 +698,10 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             int nk = 0, nv = 0;
             for (int i = 0; i < count; ++i) {
                 const int kb = i % 3, vb = i & 3, t = t0 + (c_first + count - 1 - i) * kLinC;
-                if (i >= 3 && !lin_wait(S, &S.bar.kf[kb], ((i / 3) & 1) ^ 1)) break;
+                if (i >= 3 && !lin_wait<100>(S, &S.bar.kf[kb], ((i / 3) & 1) ^ 1)) break;
                 load_tile(S.tile[kb], &maps.k, &S.bar.k[kb], hk, t);
                 ++nk;
-                if (i >= 4 && !lin_wait(S, &S.bar.vf[vb], ((i >> 2) & 1) ^ 1)) break;
+                if (i >= 4 && !lin_wait<100>(S, &S.bar.vf[vb], ((i >> 2) & 1) ^ 1)) break;
                 load_tile(S.tile[3 + vb], &maps.v, &S.bar.v[vb], hv, t);
                 ++nv;
             }
@@ -727,7 +721,7 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             const float all = __shfl_sync(0xffffffffu, above + sum, 0);
             float y[4];
             if (i + 1 < count) load_gates(p, hv, t0 + (c_first + count - 2 - i) * kLinC, kLinC, y);
-            if (i > 0 && !warp_wait(S, &S.bar.r_arr, (i & 1) ^ 1)) break;
+            if (i > 0 && !warp_wait<100>(S, &S.bar.r_arr, (i & 1) ^ 1)) break;
 #pragma unroll
             for (int e = 0; e < 4; ++e) S.w[4 * lane + e] = expf(carry + (above + suf[e]));
             __syncwarp();
