@@ -55,7 +55,7 @@ constexpr int kMinRangeChunks = 4;
 constexpr int kMinRangeTokens = kMinRangeChunks * kLinC;
 
 struct LinMaps {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;
 };
 
 struct LinParams {
@@ -98,6 +98,7 @@ struct LinBars {
     uint64_t qk[2], qs[2], kv[2], pv[2]; // products done (two: by the buffers they read)
     uint64_t gates;                      // this chunk's gate arrays are written
     uint64_t r_kt[2], r_p, r_s, r_o, r_arr;   // every elementwise warp: operands written, arrays read
+    uint64_t out[2];                     // an output tile is written (over its chunk's Q)
     uint64_t kf[3], vf[4];               // range pass: tiles free
     uint64_t fin;
 };
@@ -349,19 +350,6 @@ __device__ __forceinline__ void store_row(uint8_t *tile, int quarter, int row, c
     }
 }
 
-// 32 bytes in one store (a whole sector) when the address allows it: o's rows are 16-byte
-// aligned at least.
-__device__ __forceinline__ void store_32b(bf16 *p, const uint32_t (&u)[8]) {
-    if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                     :: "l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]),
-                        "r"(u[6]), "r"(u[7]) : "memory");
-    } else {
-        reinterpret_cast<uint4 *>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-        reinterpret_cast<uint4 *>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-    }
-}
-
 // ------------------------------------------------------------------------- output pass
 
 __global__ void __launch_bounds__(kLinThreads, 1)
@@ -394,7 +382,8 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         for (uint64_t *x : {&b.q[0], &b.q[1], &b.k[0], &b.k[1], &b.v[0], &b.v[1], &b.qk[0], &b.qk[1], &b.qs[0], &b.qs[1],
                             &b.kv[0], &b.pv[0], &b.pv[1], &b.gates, &b.fin})
             tc::mbar_init(x, 1);
-        for (uint64_t *x : {&b.r_kt[0], &b.r_kt[1], &b.r_p, &b.r_s, &b.r_o, &b.r_arr}) tc::mbar_init(x, kLinWarps);
+        for (uint64_t *x : {&b.r_kt[0], &b.r_kt[1], &b.r_p, &b.r_s, &b.r_o, &b.r_arr, &b.out[0], &b.out[1]})
+            tc::mbar_init(x, kLinWarps);
         tc::mbar_fence_init();
     }
     tc::fence_before_sync();
@@ -490,27 +479,34 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             store_row(sS, jb, row, st);      // Q S came before the keys' product: it is done
 
             warp_arrive(&S.bar.r_s);
-            // ---- D: output, 64 bytes of a row a thread
+            // ---- D: output; a full chunk goes over its Q tile (Q K and Q S are done) and leaves
+            // by tensor store, a last, partial one straight from the threads
             if (!warp_wait(S, &S.bar.pv[ph], ph2)) break;
             tc::fence_after_sync();
-            bf16 *dst = p.o + (int64_t)(t + row) * p.o_tok + (int64_t)hv * 128 + 32 * jb;
-            float a[16];
-            tc::tmem_ld16(tm + colOi, a);
-            tc::tmem_ld16(tm + colOa, v);
-            tc::tmem_wait_ld();
-            uint32_t u[8];
+            uint32_t u[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                u[e] = pack_bf2(fmaf(eg, a[2 * e], v[2 * e]), fmaf(eg, a[2 * e + 1], v[2 * e + 1]));
-            tc::tmem_ld16(tm + colOi + 16, a);
-            tc::tmem_ld16(tm + colOa + 16, v);
-            if (row < L) store_32b(dst, u);
-            tc::tmem_wait_ld();
+            for (int c = 0; c < 2; ++c) {
+                float a[16];
+                tc::tmem_ld16(tm + colOi + 16 * c, a);
+                tc::tmem_ld16(tm + colOa + 16 * c, v);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    u[8 * c + e] = pack_bf2(fmaf(eg, a[2 * e], v[2 * e]), fmaf(eg, a[2 * e + 1], v[2 * e + 1]));
+            }
             warp_arrive_tmem(&S.bar.r_o);
+            if (L == kLinC) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                u[e] = pack_bf2(fmaf(eg, a[2 * e], v[2 * e]), fmaf(eg, a[2 * e + 1], v[2 * e + 1]));
-            if (row < L) store_32b(dst + 16, u);
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint4 *>(S.tile[ph] + (jb >> 1) * kBlk + tc::swz(row, 4 * (jb & 1) + c)) =
+                        make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+                warp_arrive(&S.bar.out[ph]);
+            } else if (row < L) {
+                uint4 *dst = reinterpret_cast<uint4 *>(p.o + (int64_t)(t + row) * p.o_tok + (int64_t)hv * 128 + 32 * jb);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    dst[c] = make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+            }
         }
         if (last && p.hT && !*(volatile int *)&S.abort) {
             float4 *out = reinterpret_cast<float4 *>(p.hT + ((int64_t)n * p.Hv + hv) * 16384 + st_off);
@@ -554,19 +550,35 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             tc::prefetch_tmap(&maps.k);
             tc::prefetch_tmap(&maps.v);
             int nk = 0, nq = 0, nv = 0;
-            for (int i = 0; i < count; ++i) {
+            const int full = last && len % kLinC ? count - 1 : count;     // chunks of 128 tokens
+            // the output of chunk i, when it is written over Q
+            auto put = [&](int i) {
+                if (!lin_wait<100>(S, &S.bar.out[i & 1], (i >> 1) & 1)) return false;
+                const int t = t0 + (c_first + i) * kLinC;
+                tc::tma_store_3d(&maps.o, S.tile[i & 1], 0, hv, t);
+                tc::tma_store_3d(&maps.o, S.tile[i & 1] + kBlk, 64, hv, t);
+                tc::bulk_commit();
+                return true;
+            };
+            bool ok = true;
+            for (int i = 0; i < count && ok; ++i) {
                 const uint32_t b = i & 1, was = ((i >> 1) & 1) ^ 1;   // chunk i - 2's use of the buffer
                 const int t = t0 + (c_first + i) * kLinC;
-                if (i >= 2 && (!lin_wait<100>(S, &S.bar.qk[b], was) || !lin_wait<100>(S, &S.bar.r_kt[b], was))) break;
+                if (i >= 2 && !(ok = lin_wait<100>(S, &S.bar.qk[b], was) && lin_wait<100>(S, &S.bar.r_kt[b], was))) break;
                 load_tile(S.tile[2 + b], &maps.k, &S.bar.k[b], hk, t);
                 ++nk;
-                if (i >= 2 && !lin_wait<100>(S, &S.bar.qs[b], was)) break;
+                if (i >= 2) {
+                    if (!(ok = put(i - 2))) break;
+                    tc::bulk_wait_read<0>();
+                }
                 load_tile(S.tile[b], &maps.q, &S.bar.q[b], hk, t);
                 ++nq;
-                if (i >= 2 && !lin_wait<100>(S, &S.bar.pv[b], was)) break;
+                if (i >= 2 && !(ok = lin_wait<100>(S, &S.bar.pv[b], was))) break;
                 load_tile(S.tile[4 + b], &maps.v, &S.bar.v[b], hv, t);
                 ++nv;
             }
+            for (int i = max(0, count - 2); i < full && ok; ++i) ok = put(i);
+            tc::bulk_wait_all();
             // (bounded) everything loaded has landed
             for (int x = max(0, nk - 2); x < nk; ++x) wait_copy(&S.bar.k[x & 1], (x >> 1) & 1);
             for (int x = max(0, nq - 2); x < nq; ++x) wait_copy(&S.bar.q[x & 1], (x >> 1) & 1);
@@ -851,7 +863,7 @@ gdn_status_t launch_linear_tc(const LinearArgs &a, cudaStream_t st) {
     const Plan pl = plan_ranges(a.cu_host, a.N, a.T, a.Hv);
     gdn::LinMaps maps;
     if (!tile_map(&maps.q, a.q, a.T, a.Hk, a.q_tok) || !tile_map(&maps.k, a.k, a.T, a.Hk, a.k_tok) ||
-        !tile_map(&maps.v, a.v, a.T, a.Hv, a.v_tok))
+        !tile_map(&maps.v, a.v, a.T, a.Hv, a.v_tok) || !tile_map(&maps.o, a.o, a.T, a.Hv, a.o_tok))
         return GDN_ERR_CUDA;
     gdn::LinParams p = {};
     p.g = a.g;
