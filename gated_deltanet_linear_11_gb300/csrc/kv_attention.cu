@@ -163,36 +163,42 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kAttnBlock = 32;      // keys per step of a warp
 
+// NT tiles of eight rows; VS: warps that share a slice of the keys and split the values'
+// elements between them (2 where the output accumulators, D NT / 4 registers a thread, would
+// not fit otherwise).
 template <int D, int NT> struct AttnShape {
     using R = KvRec<D>;
     static constexpr int ROWS = 8 * NT;
-    static constexpr int STAGE = 2 * kAttnBlock * R::BYTES;
-    static constexpr int STAGES = 2;
-    static constexpr int RING = kAttnWarps * STAGES * STAGE;
-    static constexpr int JOIN = kAttnWarps * ROWS * D * 4;      // reuses the ring
+    static constexpr int VS = D * NT > 256 ? 2 : 1;
+    static constexpr int SLICES = kAttnWarps / VS;
+    static constexpr int HALF = kAttnBlock * R::BYTES;          // one block's keys, or values
+    static constexpr int RING = kAttnWarps * 4 * HALF;          // two blocks of each, per warp
+    static constexpr int JOIN = SLICES * ROWS * D * 4;          // reuses the ring
     static constexpr int BUF = RING > JOIN ? RING : JOIN;
     static constexpr int QF = NT * R::NG * 32 * 16;             // q fragments
     static constexpr int QM = NT * 32 * 8;                      // group sums of q
-    static constexpr int TAIL = ROWS * (4 + 4) + kAttnWarps * ROWS * 8 + 8 * kAttnWarps * STAGES +
-                                4 * kAttnWarps * STAGES;
+    static constexpr int TAIL = ROWS * (4 + 4) + SLICES * ROWS * 8 + 8 * 4 * kAttnWarps + 4 * 4 * kAttnWarps;
     static constexpr int SMEM = BUF + QF + QM + TAIL;
-    // CTAs per SM that registers allow without spilling the accumulators (D NT / 4 a thread)
-    static constexpr int CTAS = D * NT <= 128 ? 4 : D * NT <= 256 ? 2 : 1;
+    // CTAs per SM that registers allow without spilling
+    static constexpr int CTAS = D * NT <= 128 ? 4 : D * NT <= 256 ? 2 : 2;
 };
 
-// Keys per split of a context of len keys with m new rows: 128 up to 1024 keys, doubling
-// with every fourfold length, so that both the number of splits and their length grow with
-// the context; and doubling with m, whose row tiles are work to spread by themselves (from
-// 256 rows on nothing is split).  It depends on the sequence's own lengths only.
+// Keys per split of a context of len keys.  A warp's start and join cost about as much as 64
+// keys, so long splits serve a full device and short ones a lone sequence: 128 keys up to
+// 512, 256 up to 2048, 1024 up to 65536, then doubling with every fourfold length (64
+// sequences of up to 16384 keys, 8 kv-heads: 173 us with 1024 at the longest, 180 with 512,
+// 203 with 256 at the mean; one sequence of 32768: 24.6 us with 1024, 32 with 2048).  It
+// doubles with the row tiles too, which are work to spread by themselves (from 256 new rows
+// on nothing is split).  All of it depends on the sequence's own lengths only.
 constexpr int kSplitMaxRows = 256;
-__host__ __device__ __forceinline__ int kv_split_len(int len, int m) {
+constexpr int kSplitTileRows = 32;
+__host__ __device__ __forceinline__ int kv_split_len(int len, int m, int G) {
     if (m >= kSplitMaxRows) return 1 << 30;
-    int s = 128;
-    for (int64_t top = 1024; top < len; top *= 4) s *= 2;
-    for (int x = 1; 2 * x <= m; x *= 2) s *= 2;
+    int s = len <= 512 ? 128 : len <= 2048 ? 256 : 1024;
+    for (int64_t top = 65536; top < len; top *= 4) s *= 2;
+    for (int x = (G * m + kSplitTileRows - 1) / kSplitTileRows; x > 1; x >>= 1) s *= 2;
     return s;
 }
-
 // Splits a row of a context of len keys has room for.
 __device__ __forceinline__ int splits_of(int len, int split_len) { return (len + split_len - 1) / split_len; }
 
@@ -272,8 +278,8 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     float *sfac = reinterpret_cast<float *>(smem + A::BUF + A::QF + A::QM);
     uint32_t *snan = reinterpret_cast<uint32_t *>(sfac + A::ROWS);
     float2 *sml = reinterpret_cast<float2 *>(snan + A::ROWS);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sml + kAttnWarps * A::ROWS);
-    uint32_t *spages = reinterpret_cast<uint32_t *>(bars + kAttnWarps * A::STAGES);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sml + A::SLICES * A::ROWS);
+    uint32_t *spages = reinterpret_cast<uint32_t *>(bars + 4 * kAttnWarps);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const int split = blockIdx.x / row_tiles, rt = blockIdx.x % row_tiles;
@@ -289,49 +295,58 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     // keys seen by the tile's first and last row
     const int see_first = len - m + row0 / G + 1;
     const int see_last = len - m + (min(row0 + A::ROWS, rows) - 1) / G + 1;
-    const int split_len = kv_split_len(len, m);
+    const int split_len = kv_split_len(len, m, G);
     const int k0 = split * split_len, k1 = min(k0 + split_len, see_last);
     if (k0 >= k1 && split > 0) return;
     const int splits = (see_last + split_len - 1) / split_len;   // <= 0: no key at all
 
-    // ---- the warp's ring: block b holds keys k0 + 32 (warp + 4 b) ..
-    uint64_t *bar = bars + warp * A::STAGES;
-    uint32_t *pg = spages + warp * A::STAGES;
-    uint8_t *wring = ring + warp * A::STAGES * A::STAGE;
-    const int first = k0 + kAttnBlock * warp;
-    const int blocks = k1 > first ? (k1 - first + kAttnBlock * kAttnWarps - 1) / (kAttnBlock * kAttnWarps) : 0;
-    // Lanes 0..3 copy (keys, values) x (first, second 16 records); a page outside the cache
-    // is left out and marked.  The page of the block after is looked up one fetch ahead.
+    // ---- the warp's rings of keys and of values: block b holds keys k0 + 32 (slice + SLICES b) ..
+    const int slice = warp / A::VS, dh = warp % A::VS;
+    constexpr int STEP = kAttnBlock * A::SLICES;
+    uint64_t *bar_k = bars + 4 * warp, *bar_v = bar_k + 2;
+    uint32_t *pg = spages + 4 * warp;          // per block (mod 4): which 16 records are there
+    uint8_t *ring_k = ring + warp * 4 * A::HALF, *ring_v = ring_k + 2 * A::HALF;
+    const int first = k0 + kAttnBlock * slice;
+    const int blocks = k1 > first ? (k1 - first + STEP - 1) / STEP : 0;
+    // Lanes 0, 1 copy the two 16-record parts of a block's keys, lanes 2, 3 of its values; a
+    // page outside the cache is left out and marked.  Keys run two blocks ahead, values one;
+    // the page of a lane's next copy is looked up one copy ahead.
     const int sub_l = lane & 1, which = (lane >> 1) & 1;
     const int32_t *table = kv.table + (int64_t)n * kv.table_width;
     const int64_t page_bytes = (int64_t)(2 * kv.Hkv * REC) << kv.page_log2;
     const uint8_t *base = kv.block(0, which, hkv, REC);
     const int slot_mask = (1 << kv.page_log2) - 1;
-    int jf = lane < 4 ? first + 16 * sub_l : 0x40000000;   // the next fetch's first key
+    int jf = lane < 4 ? first + 16 * sub_l : 0x40000000;   // the next copy's first key
     int page_next = jf < k1 ? table[jf >> kv.page_log2] : -2;
-    auto fetch = [&](int b) {
-        const int s = b % A::STAGES;
+    auto fetch = [&](int bk, int bv) {         // block bk of the keys, bv of the values; -1: none
+        const bool mine = lane < 4 && (which ? bv : bk) >= 0;
         const int j = jf, page = page_next;
-        jf += kAttnBlock * kAttnWarps;
-        page_next = jf < k1 ? table[jf >> kv.page_log2] : -2;
-        const bool want = page >= 0 && page < kv.pages;
-        if (!want && page != -2) report(status, GDN_ERR_INDEX);
-        const uint32_t ok = __ballot_sync(0xffffffffu, want);
-        if (lane == 0) {
-            pg[s] = ok & 3u;
-            tc::mbar_expect_tx(bar + s, __popc(ok) * 16 * REC);
+        if (mine) {
+            jf += STEP;
+            page_next = jf < k1 ? table[jf >> kv.page_log2] : -2;
         }
+        const bool want = mine && page >= 0 && page < kv.pages;
+        if (mine && !want && page != -2) report(status, GDN_ERR_INDEX);
+        const uint32_t ok = __ballot_sync(0xffffffffu, want);
+        if (lane == 0 && bk >= 0) {
+            pg[bk & 3] = ok & 3u;
+            tc::mbar_expect_tx(bar_k + (bk & 1), __popc(ok & 3u) * 16 * REC);
+        }
+        if (lane == 0 && bv >= 0) tc::mbar_expect_tx(bar_v + (bv & 1), __popc(ok & 12u) * 16 * REC);
         __syncwarp();
-        if (want)
-            bulk_load(wring + s * A::STAGE + (2 * which + sub_l) * 16 * REC,
-                      base + page * page_bytes + (j & slot_mask) * REC, 16 * REC, bar + s);
+        if (want) {
+            uint8_t *dst = (which ? ring_v + (bv & 1) * A::HALF : ring_k + (bk & 1) * A::HALF) + sub_l * 16 * REC;
+            bulk_load(dst, base + page * page_bytes + (j & slot_mask) * REC, 16 * REC,
+                      which ? bar_v + (bv & 1) : bar_k + (bk & 1));
+        }
     };
     if (lane == 0) {
-        for (int s = 0; s < A::STAGES; ++s) tc::mbar_init(bar + s, 1);
+        for (int x = 0; x < 4; ++x) tc::mbar_init(bar_k + x, 1);
         tc::mbar_fence_init();
     }
     __syncwarp();
-    for (int b = 0; b < A::STAGES - 1 && b < blocks; ++b) fetch(b);
+    if (blocks > 0) fetch(0, 0);
+    if (blocks > 1) fetch(1, -1);
 
     // ---- q as fragments: lane (r, c) of a tile's warp holds elements 32 g + 8 c .. +7 of
     // row r, scaled; odd elements also by 1/16 (their codes come as u << 4)
@@ -356,7 +371,9 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         // 2^ex brings the largest element into [2^11, 2^12) (rows below 2^-109 stay smaller)
         const int ex = mx < INFINITY ? min(11 + 127 - (int)(__float_as_uint(mx) >> 23), 120) : 0;
-        const float up = __int_as_float((127 + ex) << 23), down = __int_as_float((127 - ex) << 23);
+        // (the scale's sign goes to q, so that larger products mean larger scores)
+        const float up = __int_as_float((127 + ex) << 23) * (scale < 0.f ? -1.f : 1.f);
+        const float down = __int_as_float((127 - ex) << 23);
         float sums[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -388,17 +405,18 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         qm[nt * 32 + lane] = make_uint2(mw[0], mw[1]);
         // a score is (sum of products) 2^24 2^-ex scale; its log2 weight times log2 e
         if (c == 0) {
-            sfac[8 * nt + r] = scale * (1.4426950408889634f * 16777216.f) * down;
+            sfac[8 * nt + r] = fmaxf(fabsf(scale) * (1.4426950408889634f * 16777216.f) * down, 1e-37f);   // not 0
             snan[8 * nt + r] = 0;
         }
     }
     __syncthreads();
 
-    float O[NT][2 * NG][4], Om[NT][4], mrun[NT][2], lrun[NT][2], fac[NT][2];
+    constexpr int NGV = NG / A::VS, NPV = NP / A::VS;      // this warp's groups, words of the values
+    float O[NT][2 * NGV][4], Om[NT][4], mrun[NT][2], lrun[NT][2], fac[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int x = 0; x < 2 * NG; ++x)
+        for (int x = 0; x < 2 * NGV; ++x)
 #pragma unroll
             for (int e = 0; e < 4; ++e) O[nt][x][e] = 0.f;
 #pragma unroll
@@ -411,30 +429,11 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         }
     }
 
-    int gave_up = -1;
-    for (int b = 0; b < blocks; ++b) {
-        const int s = b % A::STAGES;
-        if (b + A::STAGES - 1 < blocks) fetch(b + A::STAGES - 1);
-        if (!wait_copy(bar + s, (b / A::STAGES) & 1)) {
-            gave_up = b;
-            break;
-        }
-        const uint8_t *st = wring + s * A::STAGE;
-        const int j0 = first + b * kAttnBlock * kAttnWarps;
-        const uint32_t have = pg[s];
-        // every key of the block is in the cache and seen by every row
-        const bool full = have == 3u && j0 + kAttnBlock <= min(k1, see_first);
-
-        // ---- scores
-        float S[2][NT][4];
+    // products of the block's keys with q, in units of 2^-24 of q's scale
+    auto scores = [&](const uint8_t *st, float (&S)[2][NT][4]) {
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
             const uint8_t *rec0 = st + (16 * sub + r) * REC, *rec1 = rec0 + 8 * REC;
-            uint32_t w0[NG], w1[NG], s0[NG], s1[NG];
-            load_words<NG>(rec0 + c * 4 * NG, w0);
-            load_words<NG>(rec1 + c * 4 * NG, w1);
-            load_words<NG>(rec0 + R::CODES, s0);
-            load_words<NG>(rec1 + R::CODES, s1);
             // minima: k slots (2c, 2c+1) take group c against the pair (hi, lo)
             // (with two groups, lanes 2 and 3 repeat them against zeros)
             uint32_t am[4] = {0u, 0u, 0u, 0u};
@@ -452,51 +451,68 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
 #pragma unroll
                 for (int e = 0; e < 4; ++e) S[sub][nt][e] = t[e] * 0.000244140625f;
             }
+            constexpr int GL = NG < 4 ? NG : 4;      // groups per load
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const float f0 = __low2float(*reinterpret_cast<const __half2 *>(&s0[g]));
-                const float f1 = __low2float(*reinterpret_cast<const __half2 *>(&s1[g]));
-                const uint32_t h0 = w0[g] >> 8, h1 = w1[g] >> 8;
+            for (int gl = 0; gl < NG; gl += GL) {
+                uint32_t w0[GL], w1[GL], s0[GL], s1[GL];
+                load_words<GL>(rec0 + c * 4 * NG + 4 * gl, w0);
+                load_words<GL>(rec1 + c * 4 * NG + 4 * gl, w1);
+                load_words<GL>(rec0 + R::CODES + 4 * gl, s0);
+                load_words<GL>(rec1 + R::CODES + 4 * gl, s1);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint4 bq = qf[(nt * NG + g) * 32 + lane];
-                    float t[4];
-                    mma16816_first(t, w0[g] & kNib0, w1[g] & kNib0, w0[g] & kNib1, w1[g] & kNib1, bq.x, bq.y);
-                    mma16816(t, h0 & kNib0, h1 & kNib0, h0 & kNib1, h1 & kNib1, bq.z, bq.w);
-                    S[sub][nt][0] = fmaf(f0, t[0], S[sub][nt][0]);
-                    S[sub][nt][1] = fmaf(f0, t[1], S[sub][nt][1]);
-                    S[sub][nt][2] = fmaf(f1, t[2], S[sub][nt][2]);
-                    S[sub][nt][3] = fmaf(f1, t[3], S[sub][nt][3]);
+                for (int g = 0; g < GL; ++g) {
+                    const float f0 = __low2float(*reinterpret_cast<const __half2 *>(&s0[g]));
+                    const float f1 = __low2float(*reinterpret_cast<const __half2 *>(&s1[g]));
+                    const uint32_t h0 = w0[g] >> 8, h1 = w1[g] >> 8;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint4 bq = qf[(nt * NG + gl + g) * 32 + lane];
+                        float t[4];
+                        mma16816_first(t, w0[g] & kNib0, w1[g] & kNib0, w0[g] & kNib1, w1[g] & kNib1, bq.x, bq.y);
+                        mma16816(t, h0 & kNib0, h1 & kNib0, h0 & kNib1, h1 & kNib1, bq.z, bq.w);
+                        S[sub][nt][0] = fmaf(f0, t[0], S[sub][nt][0]);
+                        S[sub][nt][1] = fmaf(f0, t[1], S[sub][nt][1]);
+                        S[sub][nt][2] = fmaf(f1, t[2], S[sub][nt][2]);
+                        S[sub][nt][3] = fmaf(f1, t[3], S[sub][nt][3]);
+                    }
                 }
             }
         }
-
-        // ---- softmax step: columns 2c, 2c+1 of each tile; keys r, r+8, r+16, r+24
-        uint32_t P[2][NT][2];
+    };
+    // every key of the block is in the cache and seen by every row
+    auto is_full = [&](int b) {
+        return pg[b & 3] == 3u && first + b * STEP + kAttnBlock <= min(k1, see_first);
+    };
+    uint32_t P[2][NT][2];      // the last block's weights, as the second operand's fragments
+    // softmax step: columns 2c, 2c+1 of each tile; keys r, r+8, r+16, r+24 of block b
+    auto weigh = [&](int b, float (&S)[2][NT][4]) {
+        if (!is_full(b)) {
+            const int j0 = first + b * STEP;
+            const uint32_t have = pg[b & 3];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = min(row0 + 8 * nt + 2 * c + e, rows - 1);
+                    const int stop = min(k1, len - m + row / G + 1) - j0;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int kk = 8 * x + r;
+                        if (kk >= stop || !((have >> (kk >> 4)) & 1u)) S[x >> 1][nt][2 * (x & 1) + e] = -INFINITY;
+                    }
+                }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float bm[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = S[sub][nt][e] * fac[nt][e & 1];
-                    if (!full) {
-                        const int row = min(row0 + 8 * nt + 2 * c + (e & 1), rows - 1);
-                        const int j = j0 + 16 * sub + r + 8 * (e >> 1);
-                        if (j >= min(k1, len - m + row / G + 1) || !((have >> sub) & 1u)) x = -INFINITY;
-                    }
-                    S[sub][nt][e] = x;
-                    bm[e & 1] = fmaxf(bm[e & 1], x);
-                }
-            // the reference moves only when a score passes it by 2, so p stays below 4
-            float msub[2];
+            // the reference moves only when a score passes it by 2 (powers of two), so p < 4
+            float bm[2];
             bool move[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                bm[e] = fmaxf(fmaxf(S[0][nt][e], S[0][nt][2 + e]), fmaxf(S[1][nt][e], S[1][nt][2 + e]));
                 bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 4));
                 bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 8));
-                bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 16));
+                bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 16)) * fac[nt][e];
                 move[e] = bm[e] > mrun[nt][e] + 2.f;
             }
             if (__any_sync(0xffffffffu, move[0] || move[1])) {
@@ -508,64 +524,49 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                     lrun[nt][e] *= keep[e];
                 }
 #pragma unroll
-                for (int x = 0; x < 2 * NG; ++x)
+                for (int x = 0; x < 2 * NGV; ++x)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) O[nt][x][e] *= keep[e & 1];
                 Om[nt][0] *= keep[0];
                 Om[nt][1] *= keep[1];
             }
+            float msub[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) msub[e] = mrun[nt][e] == -INFINITY ? 0.f : mrun[nt][e];
+            for (int e = 0; e < 2; ++e) msub[e] = mrun[nt][e] == -INFINITY ? 0.f : -mrun[nt][e];
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
                 float p[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    p[e] = exp2_approx(S[sub][nt][e] - msub[e & 1]);
+                    p[e] = exp2_approx(fmaf(S[sub][nt][e], fac[nt][e & 1], msub[e & 1]));
                     lrun[nt][e & 1] += p[e];
                 }
                 P[sub][nt][0] = transpose8x8(pack_half2(p[0], p[1]));
                 P[sub][nt][1] = transpose8x8(pack_half2(p[2], p[3]));
             }
         }
-
-        // ---- values: k slots 2c, 2c+1, 2c+8, 2c+9 are the keys of the same number
+    };
+    // O += V^T P over the block's values: k slots 2c, 2c+1, 2c+8, 2c+9 are the keys of the
+    // same number
+    auto values = [&](const uint8_t *st) {
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
-            const uint8_t *v0 = st + (32 + 16 * sub + 2 * c) * REC;
+            const uint8_t *v0 = st + (16 * sub + 2 * c) * REC;
             const uint8_t *vk[4] = {v0, v0 + REC, v0 + 8 * REC, v0 + 9 * REC};
-            uint32_t pr[4][NG], mr[4];
+            uint32_t pr[4][NGV], mr[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                load_words<NG>(vk[x] + R::CODES, pr[x]);
+                load_words<NGV>(vk[x] + R::CODES + 4 * NGV * dh, pr[x]);
                 mr[x] = reinterpret_cast<const uint32_t *>(vk[x] + R::CODES)[r % NG];   // rows past NG are not read
-            }
-            if (!full) {
-                // records no row of this tile sees are taken as zero; so are non-finite
-                // pairs, whose group becomes NaN in just the rows that see the key
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int j = j0 + 16 * sub + 2 * c + (x & 1) + 8 * (x >> 1);
-                    const bool in = j < k1 && ((have >> sub) & 1u);
-                    if (!in || half_pair_nonfinite(mr[x])) mr[x] = 0u;
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        if (in && r == 0 && half_pair_nonfinite(pr[x][g])) {
-                            for (int y = 0; y < A::ROWS && row0 + y < rows; ++y)
-                                if (j < len - m + (row0 + y) / G + 1) atomicOr(snan + y, 1u << g);
-                        }
-                        if (!in || half_pair_nonfinite(pr[x][g])) pr[x][g] = 0u;
-                    }
-                }
             }
             const uint32_t a0 = __byte_perm(mr[0], mr[1], 0x7632), a2 = __byte_perm(mr[2], mr[3], 0x7632);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816(Om[nt], a0, 0u, a2, 0u, P[sub][nt][0], P[sub][nt][1]);
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
+            for (int p = 0; p < NPV; ++p) {
                 uint32_t w[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) w[x] = reinterpret_cast<const uint32_t *>(vk[x])[8 * p + r];
+                for (int x = 0; x < 4; ++x) w[x] = reinterpret_cast<const uint32_t *>(vk[x])[8 * (NPV * dh + p) + r];
 #pragma unroll
                 for (int hgrp = 0; hgrp < 2; ++hgrp) {
                     const int g = 2 * p + hgrp;
@@ -588,13 +589,55 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                 }
             }
         }
-        __syncwarp();   // the stage is free for the fetch after the next
+    };
+    // Values of a block that some row does not see in full: records no row of this tile sees
+    // are taken as zero; so are non-finite pairs, whose group becomes NaN in just the rows
+    // that see the key (through a zero weight it would reach the others too).
+    auto clean = [&](int b, uint8_t *st) {
+        const int j = first + b * STEP + lane;
+        const bool in = j < k1 && ((pg[b & 3] >> (lane >> 4)) & 1u);
+        uint32_t *par = reinterpret_cast<uint32_t *>(st + lane * REC + R::CODES);
+#pragma unroll 1
+        for (int g = 0; g < NG; ++g) {
+            const bool bad = in && half_pair_nonfinite(par[g]);
+            if (bad)
+                for (int y = 0; y < A::ROWS && row0 + y < rows; ++y)
+                    if (j < len - m + (row0 + y) / G + 1) atomicOr(snan + y, 1u << g);
+            if (bad || !in) par[g] = 0u;
+        }
+        __syncwarp();
+    };
+
+    // The scores of block b + 1 come before the values of block b: independent products that
+    // hide each other's latency.
+    bool ok = true;
+    if (blocks > 0) {
+        ok = __all_sync(0xffffffffu, wait_copy(bar_k, 0));
+        if (ok) {
+            float S[2][NT][4];
+            scores(ring_k, S);
+            weigh(0, S);
+        }
     }
-    if (gave_up >= 0) {
+    int b = 0;
+    for (; b < blocks && ok; ++b) {
+        const bool more = b + 1 < blocks;
+        if (more) fetch(b + 2 < blocks ? b + 2 : -1, b + 1);
+        if (!(ok = __all_sync(0xffffffffu, wait_copy(bar_v + (b & 1), (b >> 1) & 1)))) break;
+        uint8_t *sv = ring_v + (b & 1) * A::HALF;
+        if (!is_full(b)) clean(b, sv);
+        if (more && !(ok = __all_sync(0xffffffffu, wait_copy(bar_k + ((b + 1) & 1), ((b + 1) >> 1) & 1)))) break;
+        float S[2][NT][4];
+        if (more) scores(ring_k + ((b + 1) & 1) * A::HALF, S);
+        values(sv);
+        __syncwarp();          // the tiles read here are free for the next fetch
+        if (more) weigh(b + 1, S);
+    }
+    if (!ok) {
         // a copy never signalled: report, and let what is in flight land (bounded too)
         if (lane == 0) report(status, GDN_ERR_TIMEOUT);
-        for (int b = gave_up; b < blocks && b < gave_up + A::STAGES; ++b)
-            wait_copy(bar + b % A::STAGES, (b / A::STAGES) & 1);
+        for (int x = b; x < blocks && x < b + 3; ++x) wait_copy(bar_k + (x & 1), (x >> 1) & 1);
+        for (int x = b; x < blocks && x < b + 2; ++x) wait_copy(bar_v + (x & 1), (x >> 1) & 1);
     }
 
     // ---- join the warps: maxima and sums, then outputs through shared memory
@@ -607,7 +650,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
             l += __shfl_xor_sync(0xffffffffu, l, 8);
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             lrun[nt][e] = l;
-            if (r == 0) sml[warp * A::ROWS + 8 * nt + 2 * c + e] = make_float2(mrun[nt][e], l);
+            if (r == 0 && dh == 0) sml[slice * A::ROWS + 8 * nt + 2 * c + e] = make_float2(mrun[nt][e], l);
         }
     __syncthreads();     // every warp is done with its ring
     float *join = reinterpret_cast<float *>(smem);
@@ -618,13 +661,14 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         for (int e = 0; e < 2; ++e) {
             float mall = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) mall = fmaxf(mall, sml[w * A::ROWS + 8 * nt + 2 * c + e].x);
+            for (int w = 0; w < A::SLICES; ++w) mall = fmaxf(mall, sml[w * A::ROWS + 8 * nt + 2 * c + e].x);
             wgt[e] = mrun[nt][e] == -INFINITY ? 0.f : exp2_approx(mrun[nt][e] - mall);
         }
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const float m0 = __shfl_sync(0xffffffffu, Om[nt][0], 4 * g + c);
-            const float m1 = __shfl_sync(0xffffffffu, Om[nt][1], 4 * g + c);
+        for (int g = 0; g < NGV; ++g) {
+            const int gd = NGV * dh + g;
+            const float m0 = __shfl_sync(0xffffffffu, Om[nt][0], 4 * gd + c);
+            const float m1 = __shfl_sync(0xffffffffu, Om[nt][1], 4 * gd + c);
             const float up = 16777216.f, up16 = 1048576.f;   // 2^24; 2^20 where u came as u << 4
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -634,7 +678,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                 v.y = wgt[e] * fmaf(O[nt][2 * g][2 + e], up16, mm);
                 v.z = wgt[e] * fmaf(O[nt][2 * g + 1][e], up, mm);
                 v.w = wgt[e] * fmaf(O[nt][2 * g + 1][2 + e], up16, mm);
-                reinterpret_cast<float4 *>(join + (size_t)(warp * A::ROWS + 8 * nt + 2 * c + e) * D)[8 * g + r] = v;
+                reinterpret_cast<float4 *>(join + (size_t)(slice * A::ROWS + 8 * nt + 2 * c + e) * D)[8 * gd + r] = v;
             }
         }
     }
@@ -644,10 +688,10 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         if (row >= rows) continue;
         float mall = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) mall = fmaxf(mall, sml[w * A::ROWS + y].x);
+        for (int w = 0; w < A::SLICES; ++w) mall = fmaxf(mall, sml[w * A::ROWS + y].x);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) {
+        for (int w = 0; w < A::SLICES; ++w) {
             const float2 ml = sml[w * A::ROWS + y];
             if (ml.x != -INFINITY || ml.y != ml.y) l += ml.y * (ml.x == -INFINITY ? 1.f : exp2_approx(ml.x - mall));
             const float4 t = reinterpret_cast<const float4 *>(join + (size_t)(w * A::ROWS + y) * D)[d4];
@@ -693,7 +737,7 @@ kv_attention_join_kernel(KvView kv, bf16 *__restrict__ o, float *__restrict__ ls
     const int G = Hq / kv.Hkv, rows = G * m, row = (int)(t - t0) * G + hq % G;
     const int last = min((row / tile_rows + 1) * tile_rows, rows) - 1;
     const int see_last = len - m + last / G + 1;
-    const int split_len = kv_split_len(len, m);
+    const int split_len = kv_split_len(len, m, G);
     const int splits = (see_last + split_len - 1) / split_len;
     if (splits <= 1) return;
     const int64_t at = n * slab + ((t - t0) * Hq + hq) * splits_of(len, split_len);
@@ -781,38 +825,41 @@ namespace {
 // CTAs (256 rows each).  Below that too few SMs would be at work on it.
 constexpr int kTcMinRows = 20 * 256;
 
-int attn_max_nt(int D) { return D == 64 ? 8 : D == 128 ? 4 : 2; }
-
-// n-tiles per CTA: the fewest of 1, 2, 4 (8) that take every row of a kv-head, at most as
-// many as the accumulators' registers allow.
-int attn_nt(int D, int64_t rows) {
+// Tiles of eight rows per CTA: as many as take every row of a kv-head, at most four (what the
+// accumulators' registers allow).
+int attn_nt(int64_t rows) {
     int nt = 1;
-    while (8 * nt < rows && nt < attn_max_nt(D)) nt *= 2;
+    while (8 * nt < rows && nt < 4) ++nt;
     return nt;
 }
 
-// The most splits that a context of at most max_len keys with m new rows has.
-int attn_max_splits(int max_len, int m) {
+// The most splits that a context of at most max_len keys with m new rows has: at max_len or
+// at the end of an interval of one split length before it.
+int attn_max_splits(int max_len, int m, int G) {
     int most = 1;
-    for (int64_t top = 1024;; top *= 4) {
-        const int len = (int)std::min<int64_t>(top, max_len);
-        const int s = gdn::kv_split_len(len, m);
-        most = std::max(most, (int)(((int64_t)len + s - 1) / s));
-        if (top >= max_len) return most;
-    }
+    auto at = [&](int64_t len) {
+        if (len > max_len) return;
+        const int s = gdn::kv_split_len((int)len, m, G);
+        most = std::max(most, (int)((len + s - 1) / s));
+    };
+    at(max_len);
+    at(512);
+    at(2048);
+    for (int64_t top = 65536; top <= max_len; top *= 4) at(top);
+    return most;
 }
 
-// Partial results of one sequence, in rows: Hq m rows of S(m) splits, where S(m) is at most
-// S(1) / 2^floor(log2 m) + 1, so m S(m) <= 2 S(1) + m, and nothing is split from
-// kSplitMaxRows rows on.
-int64_t attn_slab(int Hq, int64_t T, int N, int max_q_len, int max_len) {
-    const int64_t one = attn_max_splits(max_len, 1);
+// Partial results of one sequence, in rows: Hq m rows of S(m) splits.  With t tiles of 32 of
+// the G m rows, S(m) <= 2 S(1) / t + 1 and t >= G m / 32, so m S(m) <= 64 S(1) / G + m; and
+// nothing is split from kSplitMaxRows new rows on.
+int64_t attn_slab(int Hq, int Hkv, int64_t T, int N, int max_q_len, int max_len) {
+    const int64_t G = Hq / Hkv, one = attn_max_splits(max_len, 1, 1);
     if (one <= 1) return 0;
     if (N == 1) {
-        const int s = attn_max_splits(max_len, (int)std::min<int64_t>(T, gdn::kSplitMaxRows));
+        const int s = attn_max_splits(max_len, (int)std::min<int64_t>(T, gdn::kSplitMaxRows), (int)G);
         return s > 1 ? T * Hq * s : 0;
     }
-    return max_q_len == 1 ? Hq * one : Hq * (2 * one + gdn::kSplitMaxRows);
+    return std::min<int64_t>(Hq * max_q_len * one, Hq * (64 * one / G + 1 + gdn::kSplitMaxRows));
 }
 
 size_t part_ml_bytes(int64_t rows) { return ((size_t)rows * 8 + 255) / 256 * 256; }
@@ -829,7 +876,7 @@ gdn_status_t mma_launch(const KvArgs &a, int row_tiles, int splits, int tc_rows,
             return GDN_ERR_CUDA;
         if (dev <= 63) ready.fetch_or(1ull << dev);
     }
-    const int64_t slab = attn_slab(a.Hq, a.T, a.kv.N, a.max_q_len, a.max_kv_len);
+    const int64_t slab = attn_slab(a.Hq, a.kv.Hkv, a.T, a.kv.N, a.max_q_len, a.max_kv_len);
     float2 *ml = (float2 *)a.ws;
     float *po = slab ? (float *)((uint8_t *)a.ws + part_ml_bytes(slab * a.kv.N)) : nullptr;
     kern<<<dim3((unsigned)((int64_t)splits * row_tiles), a.kv.Hkv, a.kv.N), gdn::kAttnThreads, A::SMEM, st>>>(
@@ -848,8 +895,8 @@ gdn_status_t mma_launch(const KvArgs &a, int row_tiles, int splits, int tc_rows,
 
 size_t kv_attention_workspace(int32_t D, int32_t Hq, int32_t Hkv, int64_t T, int32_t N,
                               int32_t max_q_len, int32_t max_kv_len, int in_f32, uint32_t flags) {
-    if (in_f32 || (flags & GDN_PREFILL_SIMT) || T <= 0 || Hq <= 0 || Hkv <= 0) return 0;
-    const int64_t slab = attn_slab(Hq, T, N, max_q_len, max_kv_len);
+    if (in_f32 || (flags & GDN_PREFILL_SIMT) || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv) return 0;
+    const int64_t slab = attn_slab(Hq, Hkv, T, N, max_q_len, max_kv_len);
     return slab ? part_ml_bytes(slab * N) + (size_t)slab * N * D * sizeof(float) : 0;
 }
 
@@ -865,20 +912,23 @@ gdn_status_t launch_kv_attention(const KvArgs &a, cudaStream_t st) {
         m_most = (tc_rows - 1) / a.Hq;
     }
     const int64_t rows = (int64_t)(a.Hq / a.kv.Hkv) * m_most;
-    const int nt = attn_nt(a.D, rows);
+    const int nt = attn_nt(rows);
     const int64_t tiles = (rows + 8 * nt - 1) / (8 * nt);
-    const int splits = attn_max_splits(a.max_kv_len, a.min_q_len);
+    const int splits = attn_max_splits(a.max_kv_len, a.min_q_len, a.Hq / a.kv.Hkv);
     if (tiles * splits > 0x7fffffff || a.kv.N > 65535) return GDN_ERR_SHAPE;
     switch (a.D * 10 + nt) {
     case 641: return mma_launch<64, 1>(a, (int)tiles, splits, tc_rows, st);
     case 642: return mma_launch<64, 2>(a, (int)tiles, splits, tc_rows, st);
+    case 643: return mma_launch<64, 3>(a, (int)tiles, splits, tc_rows, st);
     case 644: return mma_launch<64, 4>(a, (int)tiles, splits, tc_rows, st);
-    case 648: return mma_launch<64, 8>(a, (int)tiles, splits, tc_rows, st);
     case 1281: return mma_launch<128, 1>(a, (int)tiles, splits, tc_rows, st);
     case 1282: return mma_launch<128, 2>(a, (int)tiles, splits, tc_rows, st);
+    case 1283: return mma_launch<128, 3>(a, (int)tiles, splits, tc_rows, st);
     case 1284: return mma_launch<128, 4>(a, (int)tiles, splits, tc_rows, st);
     case 2561: return mma_launch<256, 1>(a, (int)tiles, splits, tc_rows, st);
     case 2562: return mma_launch<256, 2>(a, (int)tiles, splits, tc_rows, st);
+    case 2563: return mma_launch<256, 3>(a, (int)tiles, splits, tc_rows, st);
+    case 2564: return mma_launch<256, 4>(a, (int)tiles, splits, tc_rows, st);
     }
     return GDN_ERR_UNSUPPORTED;
 }
