@@ -30,7 +30,7 @@ template <int D> struct LinShape {
     static constexpr int WARPS = D / CW < 4 ? D / CW : 4;
     static constexpr int COLS = CW * WARPS;              // columns per CTA
     static constexpr int RX = D / (4 * RG);              // groups of four rows per lane
-    static constexpr int TB = 32;                        // tokens staged at a time
+    static constexpr int TB = 16;                        // tokens staged at a time
     static constexpr int FIX = 8;                        // tokens per correction of the decay
 };
 
@@ -43,9 +43,10 @@ linear_scan_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__
                    int Hk, int Hv, float scale) {
     using L = LinShape<D>;
     constexpr int THREADS = L::WARPS * 32;
-    __shared__ float4 sq[L::TB][D / 4], sk[L::TB][D / 4];
-    __shared__ float2 sv[L::TB][L::COLS / 2];
-    __shared__ float sa[L::TB], slo[L::TB];
+    constexpr int NQ = L::TB * D / THREADS, NV = L::TB * L::COLS / THREADS;   // staged per thread
+    __shared__ float4 sq[2][L::TB][D / 4], sk[2][L::TB][D / 4];
+    __shared__ float2 sv[2][L::TB][L::COLS / 2];
+    __shared__ float sa[2][L::TB], slo[2][L::TB];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rg = lane % L::RG, cp = warp * (L::CW / 2) + lane / L::RG;
     const int j0 = blockIdx.x * L::COLS, hv = blockIdx.y, n = blockIdx.z;
@@ -62,67 +63,112 @@ linear_scan_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__
                                h0 + st0 + (size_t)(4 * rg + 4 * L::RG * x + e) * D)
                          : make_float2(0.f, 0.f);
 
+    // The next block of tokens is on its way to registers while this one is worked on; rows
+    // past the end read as zeros.
+    T rq[NQ], rk[NQ], rv[NV];
+    float rgate = 0.f;
+    auto load = [&](int b) {
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            const int i = tid + THREADS * x, t = b + i / D, d = i % D;
+            const bool in = t < len;
+            const int64_t row = t0 + (in ? t : 0);
+            rq[x] = in ? q[row * q_tok + (int64_t)hk * D + d] : from_f32<T>(0.f);
+            rk[x] = in ? k[row * k_tok + (int64_t)hk * D + d] : from_f32<T>(0.f);
+        }
+#pragma unroll
+        for (int x = 0; x < NV; ++x) {
+            const int i = tid + THREADS * x, t = b + i / L::COLS, j = i % L::COLS;
+            rv[x] = t < len ? v[(t0 + t) * v_tok + (int64_t)hv * D + j0 + j] : from_f32<T>(0.f);
+        }
+        if (tid < L::TB) rgate = b + tid < len ? g[(t0 + b + tid) * g_tok + hv] : 0.f;
+    };
+    auto stage = [&](int u) {
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            const int i = tid + THREADS * x;
+            reinterpret_cast<float *>(sq[u][i / D])[i % D] = to_f32(rq[x]);
+            reinterpret_cast<float *>(sk[u][i / D])[i % D] = to_f32(rk[x]);
+        }
+#pragma unroll
+        for (int x = 0; x < NV; ++x) {
+            const int i = tid + THREADS * x;
+            reinterpret_cast<float *>(sv[u][i / L::COLS])[i % L::COLS] = to_f32(rv[x]);
+        }
+        if (tid < L::TB) {
+            const float2 a = decay_pair(rgate);
+            sa[u][tid] = a.x;
+            slo[u][tid] = a.x > 0.f ? a.y / a.x : 0.f;
+        }
+    };
+    T *out = o + t0 * o_tok + (int64_t)hv * D + j0 + 2 * cp;
+    if (len > 0) {
+        load(0);
+        stage(0);
+    }
     for (int b = 0; b < len; b += L::TB) {
-        const int m = min(L::TB, len - b);
+        const int u = (b / L::TB) & 1;
         __syncthreads();
-        for (int i = tid; i < m * D; i += THREADS) {
-            const int t = i / D, d = i % D;
-            const int64_t row = t0 + b + t;
-            reinterpret_cast<float *>(sq[t])[d] = to_f32(q[row * q_tok + (int64_t)hk * D + d]);
-            reinterpret_cast<float *>(sk[t])[d] = to_f32(k[row * k_tok + (int64_t)hk * D + d]);
-        }
-        for (int i = tid; i < m * L::COLS; i += THREADS) {
-            const int t = i / L::COLS, j = i % L::COLS;
-            reinterpret_cast<float *>(sv[t])[j] =
-                to_f32(v[(t0 + b + t) * v_tok + (int64_t)hv * D + j0 + j]);
-        }
-        if (tid < m) {
-            const float2 a = decay_pair(g[(t0 + b + tid) * g_tok + hv]);
-            sa[tid] = a.x;
-            slo[tid] = a.x > 0.f ? a.y / a.x : 0.f;
-        }
-        __syncthreads();
-#pragma unroll 2
-        for (int t = 0; t < m; ++t) {
-            const float a = sa[t];
-            const float2 vv = sv[t][cp];
-            float2 acc = make_float2(0.f, 0.f);
+        const bool more = b + L::TB < len;
+        if (more) load(b + L::TB);
+        // eight tokens in one stretch, so that their loads and the shuffles of o overlap;
+        // tokens past the end have k = v = q = 0 and no decay, and only their o is left out
+#pragma unroll 1
+        for (int f = 0; f < L::TB && b + f < len; f += L::FIX) {
+            float fix = 0.f;
+            float2 acc[L::FIX];
 #pragma unroll
-            for (int x = 0; x < L::RX; ++x) {
-                const float4 k4 = sk[t][rg + L::RG * x], q4 = sq[t][rg + L::RG * x];
-                const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
+            for (int e = 0; e < L::FIX; ++e) {
+                const int t = f + e;
+                const float a = sa[u][t];
+                const float2 vv = sv[u][t][cp];
+                fix += slo[u][t];
+                acc[e] = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    S[x][e].x = fmaf(S[x][e].x, a, kk[e] * vv.x);
-                    S[x][e].y = fmaf(S[x][e].y, a, kk[e] * vv.y);
-                    acc.x = fmaf(qq[e], S[x][e].x, acc.x);
-                    acc.y = fmaf(qq[e], S[x][e].y, acc.y);
+                for (int x = 0; x < L::RX; ++x) {
+                    const float4 k4 = sk[u][t][rg + L::RG * x], q4 = sq[u][t][rg + L::RG * x];
+                    const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        S[x][y].x = fmaf(S[x][y].x, a, kk[y] * vv.x);
+                        S[x][y].y = fmaf(S[x][y].y, a, kk[y] * vv.y);
+                        acc[e].x = fmaf(qq[y], S[x][y].x, acc[e].x);
+                        acc[e].y = fmaf(qq[y], S[x][y].y, acc[e].y);
+                    }
+                }
+            }
+            // sum over the RG lanes, halving the tokens a lane keeps at each step: lane rg ends
+            // with tokens rg FIX / RG ..
+            int keep = L::FIX;
+#pragma unroll
+            for (int off = L::RG / 2; off > 0; off >>= 1) {
+                keep >>= 1;
+                const bool up = rg & off;
+#pragma unroll
+                for (int e = 0; e < keep; ++e) {
+                    const float2 mine = up ? acc[keep + e] : acc[e], theirs = up ? acc[e] : acc[keep + e];
+                    acc[e].x = mine.x + __shfl_xor_sync(0xffffffffu, theirs.x, off);
+                    acc[e].y = mine.y + __shfl_xor_sync(0xffffffffu, theirs.y, off);
                 }
             }
 #pragma unroll
-            for (int off = 1; off < L::RG; off <<= 1) {
-                acc.x += __shfl_xor_sync(0xffffffffu, acc.x, off);
-                acc.y += __shfl_xor_sync(0xffffffffu, acc.y, off);
+            for (int e = 0; e < L::FIX / L::RG; ++e) {
+                const int64_t t = b + f + rg * (L::FIX / L::RG) + e;
+                if (t < len) {
+                    out[t * o_tok] = from_f32<T>(scale * acc[e].x);
+                    out[t * o_tok + 1] = from_f32<T>(scale * acc[e].y);
+                }
             }
-            if (rg == 0) {
-                T *dst = o + (t0 + b + t) * o_tok + (int64_t)hv * D + j0 + 2 * cp;
-                dst[0] = from_f32<T>(scale * acc.x);
-                dst[1] = from_f32<T>(scale * acc.y);
-            }
-            // the low parts of the last FIX decays at once (the sum is at most about 2^-21)
-            if (t % L::FIX == L::FIX - 1) {
-                float fix = 0.f;
+            // the low parts of these decays at once (the sum is at most about 2^-21)
 #pragma unroll
-                for (int e = 0; e < L::FIX; ++e) fix += slo[t - e];
+            for (int x = 0; x < L::RX; ++x)
 #pragma unroll
-                for (int x = 0; x < L::RX; ++x)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        S[x][e].x = fmaf(S[x][e].x, fix, S[x][e].x);
-                        S[x][e].y = fmaf(S[x][e].y, fix, S[x][e].y);
-                    }
-            }
+                for (int e = 0; e < 4; ++e) {
+                    S[x][e].x = fmaf(S[x][e].x, fix, S[x][e].x);
+                    S[x][e].y = fmaf(S[x][e].y, fix, S[x][e].y);
+                }
         }
+        if (more) stage(u ^ 1);
     }
     if (hT) {
 #pragma unroll
