@@ -163,9 +163,10 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kAttnBlock = 32;      // keys per step of a warp
 
-// NT tiles of eight rows; VS: warps that share a slice of the keys and split the values'
-// elements between them (2 where the output accumulators, D NT / 4 registers a thread, would
-// not fit otherwise).
+// NT tiles of eight rows; VS: warps that share a slice of the keys (2 where the output
+// accumulators, D NT / 4 registers a thread, would not fit otherwise).  Each of the two takes
+// the scores of half a block's keys and, with the other's weights, half the values' elements
+// (116 -> 109 us on the 131072 keys above; before, both computed all scores).
 template <int D, int NT> struct AttnShape {
     using R = KvRec<D>;
     static constexpr int ROWS = 8 * NT;
@@ -177,27 +178,32 @@ template <int D, int NT> struct AttnShape {
     static constexpr int BUF = RING > JOIN ? RING : JOIN;
     static constexpr int QF = NT * R::NG * 32 * 16;             // q fragments
     static constexpr int QM = NT * 32 * 8;                      // group sums of q
-    static constexpr int TAIL = ROWS * (4 + 4) + SLICES * ROWS * 8 + 8 * 4 * kAttnWarps + 4 * 4 * kAttnWarps;
+    static constexpr int SWAP = VS > 1 ? kAttnWarps * (NT * 256 + ROWS * 4 + 16) : 0;   // weights, maxima, flag
+    static constexpr int TAIL = SWAP + ROWS * (4 + 4) + kAttnWarps * ROWS * 8 + 8 * 4 * kAttnWarps + 4 * 4 * kAttnWarps;
     static constexpr int SMEM = BUF + QF + QM + TAIL;
     // CTAs per SM that registers allow without spilling
-    static constexpr int CTAS = D * NT <= 128 ? 4 : D * NT <= 256 ? 2 : 2;
+    static constexpr int CTAS = D * NT <= 128 ? 4 : 2;
 };
 
 // Keys per split of a context of len keys.  A warp's start and join cost about as much as 64
 // keys, so long splits serve a full device and short ones a lone sequence: 128 keys up to
-// 512, 256 up to 2048, 1024 up to 65536, then doubling with every fourfold length (64
-// sequences of up to 16384 keys, 8 kv-heads: 173 us with 1024 at the longest, 180 with 512,
-// 203 with 256 at the mean; one sequence of 32768: 24.6 us with 1024, 32 with 2048).  It
-// doubles with the row tiles too, which are work to spread by themselves (from 256 new rows
-// on nothing is split).  All of it depends on the sequence's own lengths only.
+// 512, 256 up to 2048, 1024 above (64 sequences of up to 16384 keys, 8 kv-heads: 173 us with
+// 1024 at the longest, 180 with 512, 203 with 256 at the mean; one sequence of 32768: 24.6 us
+// with 1024, 32 with 2048); and so long that one sequence's CTAs, tiles of 32 rows times
+// kv-heads times splits, all fit on the device at once (one sequence of 131072, 4 kv-heads,
+// 24 rows of 256 elements: 116 us with 1728, 131 with 2048, 144 with 1024, 204 with 3456).  From 256 new rows on nothing is split.  All of it depends on the
+// sequence's own lengths and heads only.
 constexpr int kSplitMaxRows = 256;
 constexpr int kSplitTileRows = 32;
-__host__ __device__ __forceinline__ int kv_split_len(int len, int m, int G) {
-    if (m >= kSplitMaxRows) return 1 << 30;
-    int s = len <= 512 ? 128 : len <= 2048 ? 256 : 1024;
-    for (int64_t top = 65536; top < len; top *= 4) s *= 2;
-    for (int x = (G * m + kSplitTileRows - 1) / kSplitTileRows; x > 1; x >>= 1) s *= 2;
-    return s;
+constexpr int kSplitCtas = 2 * 152;
+__host__ __device__ __forceinline__ int kv_split_base(int len) { return len <= 512 ? 128 : len <= 2048 ? 256 : 1024; }
+__host__ __device__ __forceinline__ int kv_split_tiles(int m, int G) { return (G * m + kSplitTileRows - 1) / kSplitTileRows; }
+__host__ __device__ __forceinline__ int kv_split_len(int len, int m, int G, int Hkv) {
+    if (m >= kSplitMaxRows) return 0x40000000;
+    const int64_t fit = ((int64_t)len * Hkv * kv_split_tiles(m, G) + kSplitCtas - 1) / kSplitCtas;
+    const int64_t s = (fit + 63) / 64 * 64;
+    const int base = kv_split_base(len);
+    return s < base ? base : s > 0x40000000 ? 0x40000000 : (int)s;
 }
 // Splits a row of a context of len keys has room for.
 __device__ __forceinline__ int splits_of(int len, int split_len) { return (len + split_len - 1) / split_len; }
@@ -275,10 +281,11 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     uint8_t *ring = smem;
     uint4 *qf = reinterpret_cast<uint4 *>(smem + A::BUF);
     uint2 *qm = reinterpret_cast<uint2 *>(smem + A::BUF + A::QF);
-    float *sfac = reinterpret_cast<float *>(smem + A::BUF + A::QF + A::QM);
+    uint8_t *swap = smem + A::BUF + A::QF + A::QM;
+    float *sfac = reinterpret_cast<float *>(swap + A::SWAP);
     uint32_t *snan = reinterpret_cast<uint32_t *>(sfac + A::ROWS);
     float2 *sml = reinterpret_cast<float2 *>(snan + A::ROWS);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sml + A::SLICES * A::ROWS);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sml + kAttnWarps * A::ROWS);
     uint32_t *spages = reinterpret_cast<uint32_t *>(bars + 4 * kAttnWarps);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
@@ -295,7 +302,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     // keys seen by the tile's first and last row
     const int see_first = len - m + row0 / G + 1;
     const int see_last = len - m + (min(row0 + A::ROWS, rows) - 1) / G + 1;
-    const int split_len = kv_split_len(len, m, G);
+    const int split_len = kv_split_len(len, m, G, kv.Hkv);
     const int k0 = split * split_len, k1 = min(k0 + split_len, see_last);
     if (k0 >= k1 && split > 0) return;
     const int splits = (see_last + split_len - 1) / split_len;   // <= 0: no key at all
@@ -308,10 +315,11 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     uint8_t *ring_k = ring + warp * 4 * A::HALF, *ring_v = ring_k + 2 * A::HALF;
     const int first = k0 + kAttnBlock * slice;
     const int blocks = k1 > first ? (k1 - first + STEP - 1) / STEP : 0;
-    // Lanes 0, 1 copy the two 16-record parts of a block's keys, lanes 2, 3 of its values; a
-    // page outside the cache is left out and marked.  Keys run two blocks ahead, values one;
+    // Lanes 0, 1 copy the two 16-record parts of a block's keys (or the one that this warp
+    // takes), lanes 2, 3 of its values; a page outside the cache is left out and marked.  Keys run two blocks ahead, values one;
     // the page of a lane's next copy is looked up one copy ahead.
     const int sub_l = lane & 1, which = (lane >> 1) & 1;
+    const uint32_t my_keys = A::VS > 1 ? 1u << dh : 3u;
     const int32_t *table = kv.table + (int64_t)n * kv.table_width;
     const int64_t page_bytes = (int64_t)(2 * kv.Hkv * REC) << kv.page_log2;
     const uint8_t *base = kv.block(0, which, hkv, REC);
@@ -330,11 +338,11 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         const uint32_t ok = __ballot_sync(0xffffffffu, want);
         if (lane == 0 && bk >= 0) {
             pg[bk & 3] = ok & 3u;
-            tc::mbar_expect_tx(bar_k + (bk & 1), __popc(ok & 3u) * 16 * REC);
+            tc::mbar_expect_tx(bar_k + (bk & 1), __popc(ok & my_keys) * 16 * REC);
         }
         if (lane == 0 && bv >= 0) tc::mbar_expect_tx(bar_v + (bv & 1), __popc(ok & 12u) * 16 * REC);
         __syncwarp();
-        if (want) {
+        if (want && (which || (my_keys >> sub_l) & 1u)) {
             uint8_t *dst = (which ? ring_v + (bv & 1) * A::HALF : ring_k + (bk & 1) * A::HALF) + sub_l * 16 * REC;
             bulk_load(dst, base + page * page_bytes + (j & slot_mask) * REC, 16 * REC,
                       which ? bar_v + (bv & 1) : bar_k + (bk & 1));
@@ -430,10 +438,11 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     }
 
     // products of the block's keys with q, in units of 2^-24 of q's scale
-    auto scores = [&](const uint8_t *st, float (&S)[2][NT][4]) {
+    constexpr int SUBS = 2 / A::VS;        // 16-key parts of a block that this warp scores
+    auto scores = [&](const uint8_t *st, float (&S)[SUBS][NT][4]) {
 #pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-            const uint8_t *rec0 = st + (16 * sub + r) * REC, *rec1 = rec0 + 8 * REC;
+        for (int sub = 0; sub < SUBS; ++sub) {
+            const uint8_t *rec0 = st + (16 * (A::VS > 1 ? dh : sub) + r) * REC, *rec1 = rec0 + 8 * REC;
             // minima: k slots (2c, 2c+1) take group c against the pair (hi, lo)
             // (with two groups, lanes 2 and 3 repeat them against zeros)
             uint32_t am[4] = {0u, 0u, 0u, 0u};
@@ -484,8 +493,12 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         return pg[b & 3] == 3u && first + b * STEP + kAttnBlock <= min(k1, see_first);
     };
     uint32_t P[2][NT][2];      // the last block's weights, as the second operand's fragments
-    // softmax step: columns 2c, 2c+1 of each tile; keys r, r+8, r+16, r+24 of block b
-    auto weigh = [&](int b, float (&S)[2][NT][4]) {
+    // The block's maxima, before scaling: columns 2c, 2c+1 of each tile; keys r, r+8 of each
+    // part of block b.  A warp of two leaves its own for the other.
+    float *smax = reinterpret_cast<float *>(swap + kAttnWarps * NT * 256);
+    int *sok = reinterpret_cast<int *>(smax + kAttnWarps * A::ROWS);
+    uint2 *sp = reinterpret_cast<uint2 *>(swap);
+    auto maxima = [&](int b, float (&S)[SUBS][NT][4], float (&bm)[NT][2]) {
         if (!is_full(b)) {
             const int j0 = first + b * STEP;
             const uint32_t have = pg[b & 3];
@@ -496,31 +509,59 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                     const int row = min(row0 + 8 * nt + 2 * c + e, rows - 1);
                     const int stop = min(k1, len - m + row / G + 1) - j0;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int kk = 8 * x + r;
+                    for (int x = 0; x < 2 * SUBS; ++x) {
+                        const int kk = 8 * x + r + (A::VS > 1 ? 16 * dh : 0);
                         if (kk >= stop || !((have >> (kk >> 4)) & 1u)) S[x >> 1][nt][2 * (x & 1) + e] = -INFINITY;
                     }
                 }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            // the reference moves only when a score passes it by 2 (powers of two), so p < 4
-            float bm[2];
-            bool move[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                bm[e] = fmaxf(fmaxf(S[0][nt][e], S[0][nt][2 + e]), fmaxf(S[1][nt][e], S[1][nt][2 + e]));
-                bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 4));
-                bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 8));
-                bm[e] = fmaxf(bm[e], __shfl_xor_sync(0xffffffffu, bm[e], 16)) * fac[nt][e];
-                move[e] = bm[e] > mrun[nt][e] + 2.f;
+                float x = fmaxf(S[0][nt][e], S[0][nt][2 + e]);
+                if (SUBS > 1) x = fmaxf(x, fmaxf(S[SUBS - 1][nt][e], S[SUBS - 1][nt][2 + e]));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                bm[nt][e] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            }
+            if (A::VS > 1 && r == 0)
+                reinterpret_cast<float2 *>(smax + warp * A::ROWS + 8 * nt)[c] = make_float2(bm[nt][0], bm[nt][1]);
+        }
+    };
+    // The two warps of a slice at one point (they take the same number of steps); false where
+    // either has given up on a copy.
+    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + slice) : "memory"); };
+    auto agree = [&](bool ok) {
+        if (A::VS > 1) {
+            if (lane == 0) sok[warp] = ok;
+            pair_sync();
+            ok = ok && sok[warp ^ 1];
+        }
+        return ok;
+    };
+    // Softmax step.  The reference moves only when a score passes it by 2 (powers of two), so
+    // p < 4.
+    auto weigh = [&](float (&S)[SUBS][NT][4], float (&bm)[NT][2]) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            bool move[2];
+            if (A::VS > 1) {
+                const float2 x = reinterpret_cast<const float2 *>(smax + (warp ^ 1) * A::ROWS + 8 * nt)[c];
+                bm[nt][0] = fmaxf(bm[nt][0], x.x);
+                bm[nt][1] = fmaxf(bm[nt][1], x.y);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                bm[nt][e] *= fac[nt][e];
+                move[e] = bm[nt][e] > mrun[nt][e] + 2.f;
             }
             if (__any_sync(0xffffffffu, move[0] || move[1])) {
                 float keep[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    keep[e] = move[e] ? exp2_approx(mrun[nt][e] - bm[e]) : 1.f;
-                    mrun[nt][e] = move[e] ? bm[e] : mrun[nt][e];
+                    keep[e] = move[e] ? exp2_approx(mrun[nt][e] - bm[nt][e]) : 1.f;
+                    mrun[nt][e] = move[e] ? bm[nt][e] : mrun[nt][e];
                     lrun[nt][e] *= keep[e];
                 }
 #pragma unroll
@@ -534,7 +575,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
 #pragma unroll
             for (int e = 0; e < 2; ++e) msub[e] = mrun[nt][e] == -INFINITY ? 0.f : -mrun[nt][e];
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
+            for (int sub = 0; sub < SUBS; ++sub) {
                 float p[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -543,6 +584,16 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                 }
                 P[sub][nt][0] = transpose8x8(pack_half2(p[0], p[1]));
                 P[sub][nt][1] = transpose8x8(pack_half2(p[2], p[3]));
+                if (A::VS > 1) sp[(warp * NT + nt) * 32 + lane] = make_uint2(P[0][nt][0], P[0][nt][1]);
+            }
+        }
+        if (A::VS > 1) {
+            pair_sync();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {      // both parts, in order for both warps
+                const uint2 x = sp[((warp & ~1) * NT + nt) * 32 + lane], y = sp[((warp | 1) * NT + nt) * 32 + lane];
+                P[0][nt][0] = x.x; P[0][nt][1] = x.y;
+                P[1][nt][0] = y.x; P[1][nt][1] = y.y;
             }
         }
     };
@@ -612,26 +663,32 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     // hide each other's latency.
     bool ok = true;
     if (blocks > 0) {
+        float S[SUBS][NT][4], bm[NT][2];
         ok = __all_sync(0xffffffffu, wait_copy(bar_k, 0));
         if (ok) {
-            float S[2][NT][4];
             scores(ring_k, S);
-            weigh(0, S);
+            maxima(0, S, bm);
         }
+        if ((ok = agree(ok))) weigh(S, bm);
     }
     int b = 0;
     for (; b < blocks && ok; ++b) {
         const bool more = b + 1 < blocks;
         if (more) fetch(b + 2 < blocks ? b + 2 : -1, b + 1);
-        if (!(ok = __all_sync(0xffffffffu, wait_copy(bar_v + (b & 1), (b >> 1) & 1)))) break;
         uint8_t *sv = ring_v + (b & 1) * A::HALF;
-        if (!is_full(b)) clean(b, sv);
-        if (more && !(ok = __all_sync(0xffffffffu, wait_copy(bar_k + ((b + 1) & 1), ((b + 1) >> 1) & 1)))) break;
-        float S[2][NT][4];
-        if (more) scores(ring_k + ((b + 1) & 1) * A::HALF, S);
-        values(sv);
-        __syncwarp();          // the tiles read here are free for the next fetch
-        if (more) weigh(b + 1, S);
+        ok = __all_sync(0xffffffffu, wait_copy(bar_v + (b & 1), (b >> 1) & 1));
+        if (ok && !is_full(b)) clean(b, sv);
+        if (ok && more) ok = __all_sync(0xffffffffu, wait_copy(bar_k + ((b + 1) & 1), ((b + 1) >> 1) & 1));
+        float S[SUBS][NT][4], bm[NT][2];
+        if (ok) {
+            if (more) scores(ring_k + ((b + 1) & 1) * A::HALF, S);
+            if (more && A::VS > 1) maxima(b + 1, S, bm);
+            values(sv);
+            if (more && A::VS == 1) maxima(b + 1, S, bm);
+            __syncwarp();          // the tiles read here are free for the next fetch
+        }
+        if (more && (ok = agree(ok))) weigh(S, bm);
+        if (!ok) break;
     }
     if (!ok) {
         // a copy never signalled: report, and let what is in flight land (bounded too)
@@ -650,7 +707,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
             l += __shfl_xor_sync(0xffffffffu, l, 8);
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             lrun[nt][e] = l;
-            if (r == 0 && dh == 0) sml[slice * A::ROWS + 8 * nt + 2 * c + e] = make_float2(mrun[nt][e], l);
+            if (r == 0) sml[warp * A::ROWS + 8 * nt + 2 * c + e] = make_float2(mrun[nt][e], l);
         }
     __syncthreads();     // every warp is done with its ring
     float *join = reinterpret_cast<float *>(smem);
@@ -661,7 +718,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         for (int e = 0; e < 2; ++e) {
             float mall = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < A::SLICES; ++w) mall = fmaxf(mall, sml[w * A::ROWS + 8 * nt + 2 * c + e].x);
+            for (int w = 0; w < kAttnWarps; w += A::VS) mall = fmaxf(mall, sml[w * A::ROWS + 8 * nt + 2 * c + e].x);
             wgt[e] = mrun[nt][e] == -INFINITY ? 0.f : exp2_approx(mrun[nt][e] - mall);
         }
 #pragma unroll
@@ -688,13 +745,14 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         if (row >= rows) continue;
         float mall = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < A::SLICES; ++w) mall = fmaxf(mall, sml[w * A::ROWS + y].x);
+        for (int w = 0; w < kAttnWarps; w += A::VS) mall = fmaxf(mall, sml[w * A::ROWS + y].x);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < A::SLICES; ++w) {
+        for (int w = 0; w < kAttnWarps; ++w) {
             const float2 ml = sml[w * A::ROWS + y];
             if (ml.x != -INFINITY || ml.y != ml.y) l += ml.y * (ml.x == -INFINITY ? 1.f : exp2_approx(ml.x - mall));
-            const float4 t = reinterpret_cast<const float4 *>(join + (size_t)(w * A::ROWS + y) * D)[d4];
+            if (w % A::VS) continue;
+            const float4 t = reinterpret_cast<const float4 *>(join + (size_t)(w / A::VS * A::ROWS + y) * D)[d4];
             v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
         }
         if ((snan[y] >> (d4 >> 3)) & 1u) v.x = v.y = v.z = v.w = __int_as_float(0x7fffffff);
@@ -737,7 +795,7 @@ kv_attention_join_kernel(KvView kv, bf16 *__restrict__ o, float *__restrict__ ls
     const int G = Hq / kv.Hkv, rows = G * m, row = (int)(t - t0) * G + hq % G;
     const int last = min((row / tile_rows + 1) * tile_rows, rows) - 1;
     const int see_last = len - m + last / G + 1;
-    const int split_len = kv_split_len(len, m, G);
+    const int split_len = kv_split_len(len, m, G, kv.Hkv);
     const int splits = (see_last + split_len - 1) / split_len;
     if (splits <= 1) return;
     const int64_t at = n * slab + ((t - t0) * Hq + hq) * splits_of(len, split_len);
@@ -833,33 +891,28 @@ int attn_nt(int64_t rows) {
     return nt;
 }
 
-// The most splits that a context of at most max_len keys with m new rows has: at max_len or
-// at the end of an interval of one split length before it.
-int attn_max_splits(int max_len, int m, int G) {
-    int most = 1;
-    auto at = [&](int64_t len) {
-        if (len > max_len) return;
-        const int s = gdn::kv_split_len((int)len, m, G);
-        most = std::max(most, (int)((len + s - 1) / s));
-    };
-    at(max_len);
-    at(512);
-    at(2048);
-    for (int64_t top = 65536; top <= max_len; top *= 4) at(top);
-    return most;
+// The most splits that a context of at most max_len keys with m new rows can have: by the
+// least length of a split, and by the CTAs that have room.
+int attn_max_splits(int max_len, int m, int G, int Hkv) {
+    if (m >= gdn::kSplitMaxRows) return 1;
+    const int64_t w = (int64_t)Hkv * gdn::kv_split_tiles(std::max(m, 1), G);
+    const int s = gdn::kv_split_base(max_len), most = max_len <= 512 ? 1 : max_len <= 2048 ? 4 : 8;
+    const int64_t room = std::max<int64_t>(1, (gdn::kSplitCtas + w - 1) / w);
+    return (int)std::min<int64_t>(std::max(most, max_len / s + (max_len % s != 0)), room);
 }
 
-// Partial results of one sequence, in rows: Hq m rows of S(m) splits.  With t tiles of 32 of
-// the G m rows, S(m) <= 2 S(1) / t + 1 and t >= G m / 32, so m S(m) <= 64 S(1) / G + m; and
-// nothing is split from kSplitMaxRows new rows on.
+// Partial results of one sequence, in rows: Hq m rows of S(m) splits.  With t >= G m / 32
+// tiles, S(m) <= 304 / (Hkv t) + 1, so Hq m S(m) <= 32 * 304 + Hq m; and nothing is split
+// from kSplitMaxRows new rows on.
 int64_t attn_slab(int Hq, int Hkv, int64_t T, int N, int max_q_len, int max_len) {
-    const int64_t G = Hq / Hkv, one = attn_max_splits(max_len, 1, 1);
+    const int G = Hq / Hkv, one = attn_max_splits(max_len, 1, G, Hkv);
     if (one <= 1) return 0;
     if (N == 1) {
-        const int s = attn_max_splits(max_len, (int)std::min<int64_t>(T, gdn::kSplitMaxRows), (int)G);
+        const int s = attn_max_splits(max_len, (int)std::min<int64_t>(T, gdn::kSplitMaxRows), G, Hkv);
         return s > 1 ? T * Hq * s : 0;
     }
-    return std::min<int64_t>(Hq * max_q_len * one, Hq * (64 * one / G + 1 + gdn::kSplitMaxRows));
+    const int64_t m = std::min(max_q_len, gdn::kSplitMaxRows);
+    return std::min<int64_t>(Hq * m * one, gdn::kSplitTileRows * gdn::kSplitCtas + Hq * m);
 }
 
 size_t part_ml_bytes(int64_t rows) { return ((size_t)rows * 8 + 255) / 256 * 256; }
@@ -914,7 +967,7 @@ gdn_status_t launch_kv_attention(const KvArgs &a, cudaStream_t st) {
     const int64_t rows = (int64_t)(a.Hq / a.kv.Hkv) * m_most;
     const int nt = attn_nt(rows);
     const int64_t tiles = (rows + 8 * nt - 1) / (8 * nt);
-    const int splits = attn_max_splits(a.max_kv_len, a.min_q_len, a.Hq / a.kv.Hkv);
+    const int splits = attn_max_splits(a.max_kv_len, a.min_q_len, a.Hq / a.kv.Hkv, a.kv.Hkv);
     if (tiles * splits > 0x7fffffff || a.kv.N > 65535) return GDN_ERR_SHAPE;
     switch (a.D * 10 + nt) {
     case 641: return mma_launch<64, 1>(a, (int)tiles, splits, tc_rows, st);
