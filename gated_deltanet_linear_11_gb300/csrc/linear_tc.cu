@@ -5,9 +5,11 @@
 // log decays, T their total and S the fp32 state at the chunk's start,
 //     O = scale (e^{G_i} q_i S + sum_{j <= i} e^{G_i - G_j} (q_i.k_j) v_j)
 //     S <- e^T S + sum_j e^{T - G_j} k_j v_j^T
-// which is four 128 x 128 x 128 products a chunk, two of them over the weighted keys, which
-// go in as a bf16 pair hi + lo so that the state keeps fp32-level accuracy:
-//     Q K^T,   Q S,   P V,   (hi + lo)^T V
+// which is four 128 x 128 x 128 products a chunk, the last of them over the weighted keys,
+// which go in as three bf16 terms, 24 bits together, so that the state keeps fp32 accuracy
+// (a pair left it off by 3e-6 of its norm, ten times what sums in fp32 are; 62 -> 71 us on
+// 4096 tokens of 48 heads):
+//     Q K^T,   Q S,   P V,   (hi + lo + rest)^T V
 // e^{T - G_j} comes from sums taken from the chunk's end and e^{G_i - G_j} inside a 32 x 32
 // block from its exponent, elsewhere as a product of two factors at most 1, so nothing
 // overflows however strong the decay.
@@ -24,11 +26,12 @@
 // operands there uses up: with P and the weighted keys in shared memory a chunk moved 5100
 // clocks' worth (measured 8700 a chunk).  They are TMEM operands instead: P over the scores
 // it came from, the keys (transposed on the way by ldmatrix) over the output accumulator
-// that is not in use yet.  That leaves 3072 clocks of traffic and room for two buffers of
-// each of Q, K and V.  TMEM (512 columns): scores / P, Q S, P V / weighted keys, state.
+// that is not in use yet, their third term over the half of the scores that P leaves.  That
+// leaves 3328 clocks of traffic and room for two buffers of each of Q, K and V.  TMEM (512
+// columns): scores / P and rest, Q S, P V / weighted keys, state.
 //
 // A long sequence over few heads would leave SMs idle, so it is cut into ranges that run
-// side by side: linear_range_kernel gives every range's own state (hi + lo products added
+// side by side: linear_range_kernel gives every range's own state (the products added
 // up in TMEM with decays to the range's end), linear_start_kernel folds them in order into
 // start states, and linear_out_kernel runs the ranges from those.  The cut depends on the
 // sequence's own length, the head count and the SM count only, so a sequence's bits do not
@@ -202,7 +205,8 @@ __device__ __forceinline__ void product(uint32_t d, const uint8_t *a, const uint
 }
 
 // The same with A in TMEM: 128 lanes, two of the depth's elements a word, 32 elements in the
-// first 16 of each 32 columns; B MN-major.
+// first 16 of each PITCH columns; B MN-major.
+template <int PITCH>
 __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, const uint8_t *b, bool add) {
     constexpr uint32_t id = tc::idesc_bf16(128, 128, 0, 1);
     const uint32_t b0 = tc::smem_u32(b);
@@ -213,7 +217,7 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, const uint8_t
                      "elect.sync _|e, 0xffffffff;\n\t"
                      "setp.ne.b32 p, %4, 0;\n\t"
                      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                     :: "r"(d), "r"(a + 32 * (ks >> 1) + 8 * (ks & 1)), "l"(db), "r"(id), "r"((uint32_t)(add || ks > 0)) : "memory");
+                     :: "r"(d), "r"(a + PITCH * (ks >> 1) + 8 * (ks & 1)), "l"(db), "r"(id), "r"((uint32_t)(add || ks > 0)) : "memory");
     }
 }
 
@@ -275,13 +279,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
                     "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
 
-// The bf16 pair hi, lo of w_j k_j, transposed: TMEM lane d; of each 32 columns, 16 words of
-// hi for 32 tokens, then 16 of lo; zero for tokens j >= L.  This warp takes d = 32 lq .. and
-// j = 32 jb .., so it writes only columns that it alone has read before; ldmatrix hands it
-// 8 x 8 blocks transposed, in the layout the 16-lane store wants.
-template <bool TAIL>
+// w_j k_j as three bf16 terms hi, lo, rest, transposed: TMEM lane d; of each PITCH columns, 16
+// words of hi for 32 tokens, then 16 of lo; zero for tokens j >= L.  This warp takes d = 32 lq
+// .. and j = 32 jb .., so it writes only columns that it alone has read before; ldmatrix hands
+// it 8 x 8 blocks transposed, in the layout the 16-lane store wants.  rest is handed back, for
+// store_rest() to place.
+__device__ __forceinline__ void store_rest(uint32_t tmem, int lq, const uint32_t (&rest)[2][8]) {
+#pragma unroll
+    for (int th = 0; th < 2; ++th) tmem_st_16x128b_x4(tmem + ((uint32_t)(32 * lq + 16 * th) << 16), rest[th]);
+}
+template <bool TAIL, int PITCH>
 __device__ __forceinline__ void weigh_keys(const uint8_t *k, uint32_t tmem, int lq, int jb, const float *w,
-                                           int L) {
+                                           int L, uint32_t (&rest)[2][8]) {
     const int lane = threadIdx.x & 31;
     float2 w2[4];
 #pragma unroll
@@ -307,21 +316,25 @@ __device__ __forceinline__ void weigh_keys(const uint8_t *k, uint32_t tmem, int 
                 const float2 d = fma_f32x2(
                     make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)), m1, v);
                 uint32_t r = pack_bf2(d.x, d.y);
+                const float2 dd = fma_f32x2(
+                    make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u)), m1, d);
+                uint32_t rr = pack_bf2(dd.x, dd.y);
                 if (TAIL) {
                     const int j = 32 * jb + 8 * tg + 2 * (lane & 3);
                     const uint32_t keep = j + 1 < L ? 0xffffffffu : j < L ? 0x0000ffffu : 0u;
                     h &= keep;
                     r &= keep;
+                    rr &= keep;
                 }
                 hi[4 * tp + e] = h;
                 lo[4 * tp + e] = r;
+                rest[th][4 * tp + e] = rr;
             }
         }
-        const uint32_t at = tmem + ((uint32_t)(32 * lq + 16 * th) << 16) + 32 * jb;
+        const uint32_t at = tmem + ((uint32_t)(32 * lq + 16 * th) << 16) + PITCH * jb;
         tmem_st_16x128b_x4(at, hi);
         tmem_st_16x128b_x4(at + 16, lo);
     }
-    tc::tmem_wait_st();
 }
 // Rows past the end hold another sequence's values: zero them (a NaN there would survive
 // the zero weights).
@@ -380,7 +393,7 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         S.abort = 0;
         LinBars &b = S.bar;
         for (uint64_t *x : {&b.q[0], &b.q[1], &b.k[0], &b.k[1], &b.v[0], &b.v[1], &b.qk[0], &b.qk[1], &b.qs[0], &b.qs[1],
-                            &b.kv[0], &b.pv[0], &b.pv[1], &b.gates, &b.fin})
+                            &b.kv[0], &b.kv[1], &b.pv[0], &b.pv[1], &b.gates, &b.fin})
             tc::mbar_init(x, 1);
         for (uint64_t *x : {&b.r_kt[0], &b.r_kt[1], &b.r_p, &b.r_s, &b.r_o, &b.r_arr, &b.out[0], &b.out[1]})
             tc::mbar_init(x, kLinWarps);
@@ -422,56 +435,64 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             // ---- A: weighted keys, over the P V that this warp has read (the gates' warp has
             // seen the keys' tile arrive)
             if (!warp_wait(S, &S.bar.gates, ph)) break;
+            uint32_t rest[2][8];
             if (L == kLinC) {
-                weigh_keys<false>(S.tile[2 + ph], tmem + colOa, lq, jb, S.w, L);
+                weigh_keys<false, 32>(S.tile[2 + ph], tmem + colOa, lq, jb, S.w, L, rest);
             } else {
-                weigh_keys<true>(S.tile[2 + ph], tmem + colOa, lq, jb, S.w, L);
+                weigh_keys<true, 32>(S.tile[2 + ph], tmem + colOa, lq, jb, S.w, L, rest);
                 if (!warp_wait(S, &S.bar.v[ph], ph2)) break;
                 clear_rows(S.tile[4 + ph], L);
                 tc::fence_async_smem();
             }
+            tc::tmem_wait_st();
             warp_arrive_tmem(&S.bar.r_kt[ph]);
             // ---- B: P = decay-weighted lower triangle of Q K^T
             if (!warp_wait(S, &S.bar.qk[ph], ph2)) break;
             tc::fence_after_sync();
             const float eg = S.eg[row], decay = S.decay;
-            float v[32];
+            uint32_t pk[16];
             if (jb <= lq) {
                 const float gi = S.g2[row];
-                tc::tmem_ld32(tm + colSc, v);
-                if (jb < lq) {
-                    const float f = p.scale * ex2(gi - S.ref[jb]);
-                    float4 b4[8];
+                const float f = jb < lq ? p.scale * ex2(gi - S.ref[jb]) : 0.f;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) b4[j] = reinterpret_cast<const float4 *>(S.b)[8 * jb + j];
-                    tc::tmem_wait_ld();
+                for (int c = 0; c < 2; ++c) {
+                    float v[16];
+                    tc::tmem_ld16(tm + colSc + 16 * c, v);
+                    if (jb < lq) {
+                        float4 b4[4];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        v[4 * j] *= f * b4[j].x;
-                        v[4 * j + 1] *= f * b4[j].y;
-                        v[4 * j + 2] *= f * b4[j].z;
-                        v[4 * j + 3] *= f * b4[j].w;
+                        for (int j = 0; j < 4; ++j) b4[j] = reinterpret_cast<const float4 *>(S.b)[8 * jb + 4 * c + j];
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            v[4 * j] *= f * b4[j].x;
+                            v[4 * j + 1] *= f * b4[j].y;
+                            v[4 * j + 2] *= f * b4[j].z;
+                            v[4 * j + 3] *= f * b4[j].w;
+                        }
+                    } else {
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            v[j] = 16 * c + j <= lane ? v[j] * (p.scale * ex2(gi - S.g2[32 * jb + 16 * c + j])) : 0.f;
                     }
-                } else {
-                    tc::tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = j <= lane ? v[j] * (p.scale * ex2(gi - S.g2[32 * jb + j])) : 0.f;
+                    for (int j = 0; j < 8; ++j) pk[8 * c + j] = pack_bf2(v[2 * j], v[2 * j + 1]);
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                for (int j = 0; j < 16; ++j) pk[j] = 0u;
             }
-            uint32_t pk[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) pk[j] = pack_bf2(v[2 * j], v[2 * j + 1]);
-            tmem_st16(tm + colSc, pk);       // over scores that this warp has read
+            // P and the keys' rest over the scores that this warp has read
+            tmem_st16(tm + colSc, pk);
+            store_rest(tmem + colSc + 32 * jb + 16, lq, rest);
             tc::tmem_wait_st();
             warp_arrive_tmem(&S.bar.r_p);
             if (lane == 0) mbar_arrive(&S.bar.r_arr);
             // ---- C: state
-            if (!warp_wait(S, &S.bar.kv[0], ph)) break;
+            if (!warp_wait(S, &S.bar.kv[1], ph)) break;
             tc::fence_after_sync();
+            float v[32];
             tc::tmem_ld32(tm + colD, v);
             tc::tmem_wait_ld();
 #pragma unroll
@@ -531,13 +552,17 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             tc::mma_commit_warp(&S.bar.qs[ph]);
             if (!warp_wait(S, &S.bar.r_kt[ph], ph2) || !warp_wait(S, &S.bar.v[ph], ph2)) break;
             tc::fence_after_sync();
-            product_ts(tmem + colD, tmem + colOa, sV, false);
-            product_ts(tmem + colD, tmem + colOa + 16, sV, true);
+            product_ts<32>(tmem + colD, tmem + colOa, sV, false);
+            product_ts<32>(tmem + colD, tmem + colOa + 16, sV, true);
             tc::mma_commit_warp(&S.bar.kv[0]);
-            // the keys' columns take P V next
-            if (!warp_wait(S, &S.bar.r_p, ph) || !warp_wait(S, &S.bar.kv[0], ph)) break;
+            if (!warp_wait(S, &S.bar.r_p, ph)) break;
             tc::fence_after_sync();
-            product_ts(tmem + colOa, tmem + colSc, sV, false);
+            product_ts<32>(tmem + colD, tmem + colSc + 16, sV, true);
+            tc::mma_commit_warp(&S.bar.kv[1]);
+            // the keys' columns take P V next
+            if (!warp_wait(S, &S.bar.kv[0], ph)) break;
+            tc::fence_after_sync();
+            product_ts<32>(tmem + colOa, tmem + colSc, sV, false);
             tc::mma_commit_warp(&S.bar.pv[ph]);
         }
         // everything issued has completed before the TMEM is freed
@@ -668,7 +693,7 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     tc::fence_after_sync();
     const uint32_t tmem = S.tmem;
     // step i takes chunk c_first + count - 1 - i; its use of a buffer among x is that
-    // buffer's (i / x)-th.  TMEM: the state at 0, weighted keys at 128 and 256.
+    // buffer's (i / x)-th.  TMEM: the state at 0, weighted keys at 128 and 320.
     if (warp < kLinWarps) {
         bool ok = true;
         for (int i = 0; i < count && ok; ++i) {
@@ -676,7 +701,10 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             if (!(ok = warp_wait(S, &S.bar.gates, i & 1) && warp_wait(S, &S.bar.k[kb], (i / 3) & 1))) break;
             if (i >= 2 && !(ok = warp_wait(S, &S.bar.kv[bf], ((i >> 1) & 1) ^ 1))) break;
             tc::fence_after_sync();
-            weigh_keys<false>(S.tile[kb], tmem + 128 + 128 * bf, warp & 3, warp >> 2, S.w, kLinC);
+            uint32_t rest[2][8];
+            weigh_keys<false, 48>(S.tile[kb], tmem + 128 + 192 * bf, warp & 3, warp >> 2, S.w, kLinC, rest);
+            store_rest(tmem + 128 + 192 * bf + 48 * (warp >> 2) + 32, warp & 3, rest);
+            tc::tmem_wait_st();
             warp_arrive_tmem(&S.bar.r_kt[bf]);
             if (lane == 0) mbar_arrive(&S.bar.kf[kb]);
             if (lane == 0) mbar_arrive(&S.bar.r_arr);
@@ -698,8 +726,9 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             const int bf = i & 1, vb = i & 3;
             if (!warp_wait(S, &S.bar.r_kt[bf], (i >> 1) & 1) || !warp_wait(S, &S.bar.v[vb], (i >> 2) & 1)) break;
             tc::fence_after_sync();
-            product_ts(tmem, tmem + 128 + 128 * bf, S.tile[3 + vb], i > 0);
-            product_ts(tmem, tmem + 144 + 128 * bf, S.tile[3 + vb], true);
+            product_ts<48>(tmem, tmem + 128 + 192 * bf, S.tile[3 + vb], i > 0);
+            product_ts<48>(tmem, tmem + 144 + 192 * bf, S.tile[3 + vb], true);
+            product_ts<48>(tmem, tmem + 160 + 192 * bf, S.tile[3 + vb], true);
             tc::mma_commit_warp(&S.bar.kv[bf]);
             tc::mma_commit_warp(&S.bar.vf[vb]);
         }
