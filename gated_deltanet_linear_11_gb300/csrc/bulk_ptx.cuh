@@ -1,4 +1,5 @@
-// bulk_ptx.cuh -- bulk copies into shared memory and bounded waits for them.
+// bulk_ptx.cuh -- bulk copies into shared memory, bounded waits for them, and paired fp32
+// and bf16 operations.
 #pragma once
 
 #include "common.cuh"
@@ -36,6 +37,33 @@ __device__ __forceinline__ bool wait_bounded_poll(uint64_t *bar, uint32_t parity
 }
 __device__ __forceinline__ bool wait_copy(uint64_t *bar, uint32_t parity) {
     return wait_bounded_poll<0>(bar, parity, nullptr);
+}
+
+// Two fp32 operations in one instruction, rounded like the single ones.
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<unsigned long long *>(&d))
+        : "l"(*reinterpret_cast<const unsigned long long *>(&a)),
+          "l"(*reinterpret_cast<const unsigned long long *>(&b)));
+    return d;
+}
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(*reinterpret_cast<unsigned long long *>(&d))
+        : "l"(*reinterpret_cast<const unsigned long long *>(&a)),
+          "l"(*reinterpret_cast<const unsigned long long *>(&b)),
+          "l"(*reinterpret_cast<const unsigned long long *>(&c)));
+    return d;
+}
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<unsigned long long *>(&d))
+        : "l"(*reinterpret_cast<const unsigned long long *>(&a)),
+          "l"(*reinterpret_cast<const unsigned long long *>(&b)));
+    return d;
 }
 
 // Two floats rounded to a bf16 pair (lo in the low half).

@@ -14,12 +14,16 @@
 //
 // Warps 0-7: softmax, a thread owning one row of a tile; warps 8-15: unpacking, a warp
 // taking 16 records of keys, then of values, straight from the cache into registers while
-// the ones before are converted; warp 16: products.  The two row tiles take turns: while one is in
-// its softmax the tensor pipe works for the other.
+// the ones before are converted; warp 16: products.  The two row tiles take turns: while one
+// is in its softmax the tensor pipe works for the other.
 //
-// Bound by the chain of a row tile (scores, softmax, P V) and the exponentials: a 256 x 128
-// step has 2 x (1088 + 512) clocks of products at D = 128 and 2048 clocks of base-2
-// exponentials (16 a clock).
+// A 256 x 128 step has 2 x (1088 + 512) clocks of products at D = 128 (operands at 128 bytes
+// a clock), 2048 clocks of base-2 exponentials (16 a clock) and about 2600 instructions a
+// scheduler, and takes 5500: the scores of both row tiles, then the unpacking of the next
+// keys into the one buffer there is room for, form its chain, and the issue slots are half
+// taken.  Tried and slower: two buffers for hi with lo converted again (462 us where this
+// form takes 432), sixteen unpacking warps (482), two threads a row (486), a warp of
+// products for each row tile (543, their softmaxes fall together).
 //
 // Fewer bits than fp32: q is scaled by a power of two per row into [2^6, 2^7) and held in
 // fp16 (exact down to 2^-21 of the largest); a value is minimum + scale * code rounded once
@@ -115,12 +119,17 @@ __device__ __forceinline__ uint64_t desc_x(const uint8_t *p) {
 }
 __device__ __forceinline__ uint32_t at_x(int row, int half) { return (row >> 3) * 256 + half * 128 + (row & 7) * 16; }
 
-// Codes of the nibble pairs (i, i + 4) of a word, i = 0..3, as fp16: 1024 + u, less 1024.
+// Codes of the nibble pairs (i, i + 4) of a word, i = 0..3, as fp16: 1024 + u, less 1024, or
+// 1024 + 16 u, over 16 and less 64 (both exact).
 __device__ __forceinline__ void codes_of(uint32_t w, __half2 (&u)[4]) {
     const __half2 k1024 = __floats2half2_rn(1024.f, 1024.f);
+    const __half2 k16 = __floats2half2_rn(0.0625f, 0.0625f), k64 = __floats2half2_rn(-64.f, -64.f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        u[i] = __hsub2(bits_h2(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u), k1024);
+    for (int i = 0; i < 4; i += 2) {
+        const uint32_t x = w >> (4 * i);
+        u[i] = __hsub2(bits_h2((x & 0x000F000Fu) | 0x64006400u), k1024);
+        u[i + 1] = __hfma2(bits_h2((x & 0x00F000F0u) | 0x64006400u), k16, k64);
+    }
 }
 __device__ __forceinline__ bool pair_nonfinite(uint32_t w) {
     return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
@@ -298,7 +307,8 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
                 }
             }
             const float sub = ref == -INFINITY ? 0.f : kTcLift - ref;
-            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 fac2 = make_float2(fac, fac), sub2 = make_float2(sub, sub);
+            float2 ls[2] = {};
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 tc::tmem_wait_ld();
@@ -306,15 +316,15 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
                 float *x = s[c & 1];
                 uint32_t p[8];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = tc_ex2(fmaf(x[j], fac, sub));
-#pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    p[j] = h2_bits(__floats2half2_rn(x[2 * j], x[2 * j + 1]));
-                    ls[j & 3] += x[2 * j] + x[2 * j + 1];
+                    float2 e = fma_f32x2(make_float2(x[2 * j], x[2 * j + 1]), fac2, sub2);
+                    e = make_float2(tc_ex2(e.x), tc_ex2(e.y));
+                    p[j] = h2_bits(__floats2half2_rn(e.x, e.y));
+                    ls[j & 1] = add_f32x2(ls[j & 1], e);
                 }
                 tc_st8(tS + 8 * c, p);         // over scores that this thread has read
             }
-            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
             tc::tmem_wait_st();
             tc::fence_before_sync();
             __syncwarp();
@@ -360,7 +370,12 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
     } else if (warp < kTcSoftWarps + kTcUnpackWarps) {
         // ---- unpacking: this warp has keys 16 w .. +15 of each tile, then their values; lane
         // (r, x) takes a quarter of the codes of records r and r + 8
-        const int w = warp - kTcSoftWarps, r = lane >> 2, x = lane & 3;
+        const int w = warp - kTcSoftWarps, x = lane & 3;
+        // Eight lanes store 16 bytes each at a time, two rows of a swizzled tile.  A row's four
+        // chunks of keys fill half of the banks, and rows r and r + 4 opposite halves; its chunks
+        // of values (D = 128, with words exchanged in pairs for x >= 2) meet those of r + 2 nowhere.
+        const int rk = 4 * ((lane >> 2) & 1) + (lane >> 3);
+        const int rv = D == 128 ? 2 * ((lane >> 2) & 1) + ((lane >> 3) & 1) + 4 * (lane >> 4) : lane >> 2;
         constexpr int NW = D / 32;               // words of codes a lane takes
         const int32_t *table = kv.table + (int64_t)n * kv.table_width;
         const int64_t page_bytes = (int64_t)(2 * kv.Hkv * REC) << kv.page_log2;
@@ -378,11 +393,11 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
             const int j = 128 * t + 16 * w;
             const bool want = pg >= 0 && pg < kv.pages;
             if (!want && pg != -2 && u == 0 && lane == 0) report(status, GDN_ERR_INDEX);
-            const uint8_t *rec = base + (int64_t)pg * page_bytes + (u ? to_v : 0) + ((j & slot_mask) + r) * REC;
+            const uint8_t *rec = base + (int64_t)pg * page_bytes + (u ? to_v : 0) + ((j & slot_mask) + (u ? rv : rk)) * REC;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const uint8_t *p = rec + 8 * y * REC;
-                const bool in = want && j + r + 8 * y < see_last;
+                const bool in = want && j + (u ? rv : rk) + 8 * y < see_last;
                 if constexpr (D == 128) {
                     const uint4 a = in ? *reinterpret_cast<const uint4 *>(p + 16 * x) : make_uint4(0, 0, 0, 0);
                     const uint4 b = in ? *reinterpret_cast<const uint4 *>(p + R::CODES) : make_uint4(0, 0, 0, 0);
@@ -407,74 +422,74 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
             const int page_next = lookup(t + 1);
             if (t >= 1 && !tc_wait<100>(&S.bar.k_free, (t - 1) & 1, abort)) break;
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    // word x NG + g is elements 32 g + 8 x ..: 16-byte chunk 4 g + x
-                    const int key = 16 * w + r + 8 * y;
+            for (int y = 0; y < 2; ++y) {
+                // word x NG + g is elements 32 g + 8 x ..: 16-byte chunk 4 g + x
+                const int key = 16 * w + rk + 8 * y;
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        const __half2 sc = __low2half2(bits_h2(par[0][y][g]));
-                        __half2 c[4];
-                        codes_of(code[0][y][g], c);
-                        uint32_t hi[4], lo[4];
+                for (int g = 0; g < NG; ++g) {
+                    const __half2 sc = __low2half2(bits_h2(par[0][y][g]));
+                    __half2 c[4];
+                    codes_of(code[0][y][g], c);
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const __half2 h = __hmul2(c[i], sc);
-                            hi[i] = h2_bits(h);
-                            lo[i] = h2_bits(__hfma2(c[i], sc, __hneg2(h)));
-                        }
-                        const uint32_t at = ((4 * g + x) >> 3) * T::BLK + tc::swz(key, (4 * g + x) & 7);
-                        *reinterpret_cast<uint4 *>(S.hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(S.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    for (int i = 0; i < 4; ++i) {
+                        const __half2 h = __hmul2(c[i], sc);
+                        hi[i] = h2_bits(h);
+                        lo[i] = h2_bits(__hfma2(c[i], sc, __hneg2(h)));
                     }
-                    if (x < 2) {                 // the minima, against the sums' hi and lo
-                        uint4 v = make_uint4(__byte_perm(par[0][y][0], par[0][y][1], 0x7632), 0u, 0u, 0u);
-                        if (NG == 4) v.y = __byte_perm(par[0][y][NG - 2], par[0][y][NG - 1], 0x7632);
-                        *reinterpret_cast<uint4 *>(S.kx + at_x(key, x)) = v;
-                    }
+                    const uint32_t at = ((4 * g + x) >> 3) * T::BLK + tc::swz(key, (4 * g + x) & 7);
+                    *reinterpret_cast<uint4 *>(S.hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(S.lo + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-                if (lane == 0) S.have[s][w] = page >= 0 && page < kv.pages ? 1 : 0;
-                if (t + 1 < steps) fetch(t + 1, 0, page_next);
+                if (x < 2) {                 // the minima, against the sums' hi and lo
+                    uint4 v = make_uint4(__byte_perm(par[0][y][0], par[0][y][1], 0x7632), 0u, 0u, 0u);
+                    if (NG == 4) v.y = __byte_perm(par[0][y][NG - 2], par[0][y][NG - 1], 0x7632);
+                    *reinterpret_cast<uint4 *>(S.kx + at_x(key, x)) = v;
+                }
+            }
+            if (lane == 0) S.have[s][w] = page >= 0 && page < kv.pages ? 1 : 0;
+            if (t + 1 < steps) fetch(t + 1, 0, page_next);
             tc::fence_async_smem();
             __syncwarp();
             if (lane == 0) tc_arrive(&S.bar.k_full);
             if (t >= 2 && !tc_wait<100>(&S.bar.v_free[s], ((t >> 1) & 1) ^ 1, abort)) break;
-                if (128 * (t + 1) > first_row_sees) {
-                    // some row does not see some key of this tile: a non-finite value pair would
-                    // reach it through its zero weight, so such a group is zeroed here and made
-                    // NaN in just the rows that see the key
+            if (128 * (t + 1) > first_row_sees) {
+                // some row does not see some key of this tile: a non-finite value pair would
+                // reach it through its zero weight, so such a group is zeroed here and made
+                // NaN in just the rows that see the key
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
+                for (int y = 0; y < 2; ++y)
 #pragma unroll
-                        for (int g = 0; g < NG; ++g) {
-                            if (!pair_nonfinite(par[1][y][g])) continue;
-                            const int j = 128 * t + 16 * w + r + 8 * y;
-                            if (x == 0)
-                                for (int i = 0; i < kTcRows && row0 + i < rows; ++i)
-                                    if (j < len - m + (row0 + i) / G + 1) atomicOr(S.nan_groups + i, 1u << g);
-                            par[1][y][g] = 0u;
-                        }
-                }
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    // word W is chunk W; its low nibbles are of group 2 (W / 8), its high of the next
-                    const int key = 16 * w + r + 8 * y;
-                    const uint32_t a = NG == 4 && x >= 2 ? par[1][y][NG - 2] : par[1][y][0];
-                    const uint32_t b = NG == 4 && x >= 2 ? par[1][y][NG - 1] : par[1][y][1];
-                    const __half2 sc = bits_h2(__byte_perm(a, b, 0x5410)), mn = bits_h2(__byte_perm(a, b, 0x7632));
-                    const __half2 top = __floats2half2_rn(65504.f, 65504.f);
-#pragma unroll
-                    for (int e = 0; e < NW; ++e) {
-                        const int W = NW * x + e;
-                        __half2 c[4];
-                        codes_of(code[1][y][e], c);
-                        uint32_t v[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = h2_bits(__hmin2_nan(__hfma2(c[i], sc, mn), top));
-                        *reinterpret_cast<uint4 *>(S.v[s] + (W >> 3) * T::BLK + tc::swz(key, W & 7)) =
-                            make_uint4(v[0], v[1], v[2], v[3]);
+                    for (int g = 0; g < NG; ++g) {
+                        if (!pair_nonfinite(par[1][y][g])) continue;
+                        const int j = 128 * t + 16 * w + rv + 8 * y;
+                        if (x == 0)
+                            for (int i = 0; i < kTcRows && row0 + i < rows; ++i)
+                                if (j < len - m + (row0 + i) / G + 1) atomicOr(S.nan_groups + i, 1u << g);
+                        par[1][y][g] = 0u;
                     }
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                // word W is chunk W; its low nibbles are of group 2 (W / 8), its high of the next
+                const int key = 16 * w + rv + 8 * y;
+                const uint32_t a = NG == 4 && x >= 2 ? par[1][y][NG - 2] : par[1][y][0];
+                const uint32_t b = NG == 4 && x >= 2 ? par[1][y][NG - 1] : par[1][y][1];
+                const __half2 sc = bits_h2(__byte_perm(a, b, 0x5410)), mn = bits_h2(__byte_perm(a, b, 0x7632));
+                const __half2 top = __floats2half2_rn(65504.f, 65504.f);
+#pragma unroll
+                for (int e = 0; e < NW; ++e) {
+                    const int W = NW * x + (D == 128 && x >= 2 ? e ^ 1 : e);
+                    __half2 c[4];
+                    codes_of(D == 128 && x >= 2 ? code[1][y][e ^ 1] : code[1][y][e], c);
+                    uint32_t v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = h2_bits(__hmin2_nan(__hfma2(c[i], sc, mn), top));
+                    *reinterpret_cast<uint4 *>(S.v[s] + (W >> 3) * T::BLK + tc::swz(key, W & 7)) =
+                        make_uint4(v[0], v[1], v[2], v[3]);
                 }
-                if (t + 1 < steps) fetch(t + 1, 1, page_next);
+            }
+            if (t + 1 < steps) fetch(t + 1, 1, page_next);
             tc::fence_async_smem();
             __syncwarp();
             if (lane == 0) tc_arrive(&S.bar.v_full[s]);

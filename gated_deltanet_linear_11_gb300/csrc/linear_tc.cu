@@ -131,25 +131,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(tc::smem_u32(bar)) : "memory");
 }
 
-// Two fp32 operations in one instruction, rounded like the single ones.
-__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
-    float2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(*reinterpret_cast<unsigned long long *>(&d))
-        : "l"(*reinterpret_cast<const unsigned long long *>(&a)),
-          "l"(*reinterpret_cast<const unsigned long long *>(&b)));
-    return d;
-}
-__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(*reinterpret_cast<unsigned long long *>(&d))
-        : "l"(*reinterpret_cast<const unsigned long long *>(&a)),
-          "l"(*reinterpret_cast<const unsigned long long *>(&b)),
-          "l"(*reinterpret_cast<const unsigned long long *>(&c)));
-    return d;
-}
-
 // Bounded wait on an mbarrier phase.  Gives up when the bound has passed or another thread
 // of the CTA has given up; every role then leaves its loop.
 template <int SLEEP_NS = 0>
