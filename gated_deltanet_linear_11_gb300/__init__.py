@@ -682,7 +682,7 @@ def gdn_kv_attention(q, cache, block_table, kv_lens, cu_seqlens=None, max_kv_len
     N, Hkv, c = _kv_cache(cache, block_table, kv_lens, D)
     cu, cu_h = _kv_offsets(cu_seqlens, cu_seqlens_host, T, N)
     if max_kv_len is None:
-        max_kv_len = min(block_table.shape[1] * cache.shape[3], 0x7fffffff)
+        max_kv_len = min(block_table.shape[1] * cache.shape[3], 1 << 30)
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, Hq) or
                             not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 tensor of shape [T, Hq]")

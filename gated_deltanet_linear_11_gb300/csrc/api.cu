@@ -759,7 +759,7 @@ gdn_status_t gdn_kv_attention(const gdn_kv_cache_t *cache, const int32_t *cu_seq
     gdn_host::KvArgs a;
     if ((s = kv_args(cache, cu_seqlens_dev, cu_seqlens_host, Q.T, a)) != GDN_OK) return s;
     if (O.T != Q.T || O.H != Q.H || O.D != Q.D || Q.D != a.D || Q.H % a.kv.Hkv != 0 ||
-        Q.H > 65535 || max_kv_len < 0)
+        Q.H > 65535 || Q.T * Q.H > 0x7fffffff || max_kv_len < 0 || max_kv_len > GDN_KV_MAX_LEN)
         return GDN_ERR_SHAPE;
     if (Q.dtype != O.dtype) return GDN_ERR_DTYPE;
     if (Q.T == 0) return GDN_OK;

@@ -185,28 +185,39 @@ template <int D, int NT> struct AttnShape {
     static constexpr int CTAS = D * NT <= 128 ? 4 : 2;
 };
 
-// Keys per split of a context of len keys.  A warp's start and join cost about as much as 64
+// Keys per split of a context of len keys.  A warp's start and join cost about as much as 40
 // keys, so long splits serve a full device and short ones a lone sequence: 128 keys up to
-// 512, 256 up to 2048, 1024 above (64 sequences of up to 16384 keys, 8 kv-heads: 173 us with
-// 1024 at the longest, 180 with 512, 203 with 256 at the mean; one sequence of 32768: 24.6 us
-// with 1024, 32 with 2048); and so long that one sequence's CTAs, tiles of 32 rows times
-// kv-heads times splits, all fit on the device at once (one sequence of 131072, 4 kv-heads,
-// 24 rows of 256 elements: 116 us with 1728, 131 with 2048, 144 with 1024, 204 with 3456).  From 256 new rows on nothing is split.  All of it depends on the
-// sequence's own lengths and heads only.
+// 512, 256 up to 2048, 1024 above (8 kv-heads of 128, 64 sequences of 4096 to 8192 keys: 140
+// us with 1024, 161 with 512, 206 with 256; one sequence of 8192: 21, 16.5 and 14.5); and so
+// long that one sequence's CTAs, row tiles times kv-heads times splits, all fit on the device
+// at once (one sequence of 131072, 4 kv-heads, 24 rows of 256 elements: 116 us with 1728, 131
+// with 2048, 144 with 1024, 204 with 3456).  From 256 new rows on nothing is split.  All of
+// it depends on the sequence's own lengths and heads only.
 constexpr int kSplitMaxRows = 256;
-constexpr int kSplitTileRows = 32;
 constexpr int kSplitCtas = 2 * 152;
+// Most tiles of eight rows a CTA takes.  What more would save in reading and unpacking keys is
+// lost again where two warps have to share the elements (D NT > 256): 16 sequences of 4096 to
+// 8192 keys, 32 rows of 128, 131 us with two, 155 with four; but D = 256, 72 rows, 250 with
+// three, 303 with one.
+__host__ __device__ constexpr int attn_max_nt(int D) { return D == 256 ? 3 : D == 128 ? 2 : 4; }
 __host__ __device__ __forceinline__ int kv_split_base(int len) { return len <= 512 ? 128 : len <= 2048 ? 256 : 1024; }
-__host__ __device__ __forceinline__ int kv_split_tiles(int m, int G) { return (G * m + kSplitTileRows - 1) / kSplitTileRows; }
-__host__ __device__ __forceinline__ int kv_split_len(int len, int m, int G, int Hkv) {
-    if (m >= kSplitMaxRows) return 0x40000000;
-    const int64_t fit = ((int64_t)len * Hkv * kv_split_tiles(m, G) + kSplitCtas - 1) / kSplitCtas;
-    const int64_t s = (fit + 63) / 64 * 64;
-    const int base = kv_split_base(len);
-    return s < base ? base : s > 0x40000000 ? 0x40000000 : (int)s;
+// Splits that one sequence of m new rows has room for on the device.
+__host__ __device__ __forceinline__ int kv_split_room(int m, int G, int Hkv, int D) {
+    const int rows = 8 * attn_max_nt(D);
+    const int64_t ctas = (int64_t)Hkv * ((G * m + rows - 1) / rows);
+    return m >= kSplitMaxRows || 2 * ctas > kSplitCtas ? 1 : (int)(kSplitCtas / (ctas > 0 ? ctas : 1));
 }
-// Splits a row of a context of len keys has room for.
-__device__ __forceinline__ int splits_of(int len, int split_len) { return (len + split_len - 1) / split_len; }
+// (room for single tokens comes with the launch: a division less on the way to the first load)
+__device__ __forceinline__ int kv_split_len(int len, int m, int G, int Hkv, int D, int room_one) {
+    const int room = m == 1 ? room_one : kv_split_room(m, G, Hkv, D), base = kv_split_base(len);
+    if (room <= 1) return 0x40000000;
+    if ((int64_t)room * base >= len) return base;
+    return ((len + room - 1) / room + 63) / 64 * 64;
+}
+// Splits of len keys (0 where there are none).
+__device__ __forceinline__ int splits_of(int len, int split_len) {
+    return len > 0 ? (int)(((uint32_t)len + (uint32_t)split_len - 1) / (uint32_t)split_len) : 0;
+}
 
 // d = a b + c on 16 x 8 x 16, fp16 in, fp32 out.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -272,8 +283,8 @@ __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::CTAS)
 kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__ o,
                         float *__restrict__ lse, float *__restrict__ part_o,
                         float2 *__restrict__ part_ml, int64_t q_tok, int64_t o_tok, int Hq,
-                        int row_tiles, int64_t slab, int tc_rows, int max_kv_len, float scale,
-                        int32_t *status) {
+                        int row_tiles, int64_t slab, int tc_rows, int room_one, int max_kv_len,
+                        float scale, int32_t *status) {
     using R = KvRec<D>;
     using A = AttnShape<D, NT>;
     constexpr int NG = R::NG, NP = D / 64, REC = R::BYTES;
@@ -302,10 +313,10 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     // keys seen by the tile's first and last row
     const int see_first = len - m + row0 / G + 1;
     const int see_last = len - m + (min(row0 + A::ROWS, rows) - 1) / G + 1;
-    const int split_len = kv_split_len(len, m, G, kv.Hkv);
-    const int k0 = split * split_len, k1 = min(k0 + split_len, see_last);
-    if (k0 >= k1 && split > 0) return;
-    const int splits = (see_last + split_len - 1) / split_len;   // <= 0: no key at all
+    const int split_len = kv_split_len(len, m, G, kv.Hkv, D, room_one);
+    const int splits = splits_of(see_last, split_len);   // 0: no key at all
+    if (split > 0 && split >= splits) return;            // (the grid is made for the most)
+    const int k0 = split * split_len, k1 = see_last - k0 > split_len ? k0 + split_len : see_last;
 
     // ---- the warp's rings of keys and of values: block b holds keys k0 + 32 (slice + SLICES b) ..
     const int slice = warp / A::VS, dh = warp % A::VS;
@@ -782,7 +793,7 @@ __global__ void __launch_bounds__(128)
 kv_attention_join_kernel(KvView kv, bf16 *__restrict__ o, float *__restrict__ lse,
                          const float *__restrict__ part_o, const float2 *__restrict__ part_ml,
                          int64_t o_tok, int Hq, int tile_rows, int64_t slab, int tc_rows,
-                         int max_kv_len) {
+                         int room_one, int max_kv_len) {
     __shared__ __align__(16) float sacc[4][D];
     __shared__ float sl[4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -795,8 +806,8 @@ kv_attention_join_kernel(KvView kv, bf16 *__restrict__ o, float *__restrict__ ls
     const int G = Hq / kv.Hkv, rows = G * m, row = (int)(t - t0) * G + hq % G;
     const int last = min((row / tile_rows + 1) * tile_rows, rows) - 1;
     const int see_last = len - m + last / G + 1;
-    const int split_len = kv_split_len(len, m, G, kv.Hkv);
-    const int splits = (see_last + split_len - 1) / split_len;
+    const int split_len = kv_split_len(len, m, G, kv.Hkv, D, room_one);
+    const int splits = splits_of(see_last, split_len);
     if (splits <= 1) return;
     const int64_t at = n * slab + ((t - t0) * Hq + hq) * splits_of(len, split_len);
     const float2 *ml = part_ml + at;
@@ -880,39 +891,36 @@ gdn_status_t launch_kv_attention_simt(const KvArgs &a, cudaStream_t st) {
 namespace {
 
 // Query heads times new tokens from which a sequence takes the tcgen05 kernel: 20 of its
-// CTAs (256 rows each).  Below that too few SMs would be at work on it.
+// CTAs (256 rows each).  Below that too few SMs would be at work on it (8192 keys; this kernel
+// against that one, us, at 4096 and at 5120: D = 128 over 8 kv-heads 138, 186 and 240, 187;
+// over 2 138, 185 and 238, 185; D = 64 over 2 125, 133 and 149, 133).
 constexpr int kTcMinRows = 20 * 256;
 
-// Tiles of eight rows per CTA: as many as take every row of a kv-head, at most four (what the
-// accumulators' registers allow).
-int attn_nt(int64_t rows) {
-    int nt = 1;
-    while (8 * nt < rows && nt < 4) ++nt;
-    return nt;
+// Tiles of eight rows per CTA: as few CTAs as can take every row of a kv-head, alike.
+int attn_nt(int64_t rows, int D) {
+    const int64_t most = 8 * gdn::attn_max_nt(D), tiles = std::max<int64_t>(1, (rows + most - 1) / most);
+    return (int)std::max<int64_t>(1, (rows + 8 * tiles - 1) / (8 * tiles));
 }
 
 // The most splits that a context of at most max_len keys with m new rows can have: by the
-// least length of a split, and by the CTAs that have room.
-int attn_max_splits(int max_len, int m, int G, int Hkv) {
-    if (m >= gdn::kSplitMaxRows) return 1;
-    const int64_t w = (int64_t)Hkv * gdn::kv_split_tiles(std::max(m, 1), G);
+// least length of a split, and by what has room.
+int attn_max_splits(int max_len, int m, int G, int Hkv, int D) {
     const int s = gdn::kv_split_base(max_len), most = max_len <= 512 ? 1 : max_len <= 2048 ? 4 : 8;
-    const int64_t room = std::max<int64_t>(1, (gdn::kSplitCtas + w - 1) / w);
-    return (int)std::min<int64_t>(std::max(most, max_len / s + (max_len % s != 0)), room);
+    return std::min(std::max(most, max_len / s + (max_len % s != 0)), gdn::kv_split_room(std::max(m, 1), G, Hkv, D));
 }
 
-// Partial results of one sequence, in rows: Hq m rows of S(m) splits.  With t >= G m / 32
-// tiles, S(m) <= 304 / (Hkv t) + 1, so Hq m S(m) <= 32 * 304 + Hq m; and nothing is split
-// from kSplitMaxRows new rows on.
-int64_t attn_slab(int Hq, int Hkv, int64_t T, int N, int max_q_len, int max_len) {
-    const int G = Hq / Hkv, one = attn_max_splits(max_len, 1, G, Hkv);
+// Partial results of one sequence, in rows: Hq m rows of S(m) splits.  S(m) is at most the
+// 304 CTAs over Hkv times the tiles of at most 32 of the G m rows, so Hq m S(m) <= 32 * 304
+// where anything is split.
+int64_t attn_slab(int Hq, int Hkv, int64_t T, int N, int max_q_len, int max_len, int D) {
+    const int G = Hq / Hkv, one = attn_max_splits(max_len, 1, G, Hkv, D);
     if (one <= 1) return 0;
     if (N == 1) {
-        const int s = attn_max_splits(max_len, (int)std::min<int64_t>(T, gdn::kSplitMaxRows), G, Hkv);
+        const int s = attn_max_splits(max_len, (int)std::min<int64_t>(T, gdn::kSplitMaxRows), G, Hkv, D);
         return s > 1 ? T * Hq * s : 0;
     }
     const int64_t m = std::min(max_q_len, gdn::kSplitMaxRows);
-    return std::min<int64_t>(Hq * m * one, gdn::kSplitTileRows * gdn::kSplitCtas + Hq * m);
+    return std::min<int64_t>(Hq * m * one, 32 * gdn::kSplitCtas);
 }
 
 size_t part_ml_bytes(int64_t rows) { return ((size_t)rows * 8 + 255) / 256 * 256; }
@@ -929,17 +937,18 @@ gdn_status_t mma_launch(const KvArgs &a, int row_tiles, int splits, int tc_rows,
             return GDN_ERR_CUDA;
         if (dev <= 63) ready.fetch_or(1ull << dev);
     }
-    const int64_t slab = attn_slab(a.Hq, a.kv.Hkv, a.T, a.kv.N, a.max_q_len, a.max_kv_len);
+    const int64_t slab = attn_slab(a.Hq, a.kv.Hkv, a.T, a.kv.N, a.max_q_len, a.max_kv_len, D);
+    const int room = gdn::kv_split_room(1, a.Hq / a.kv.Hkv, a.kv.Hkv, D);
     float2 *ml = (float2 *)a.ws;
     float *po = slab ? (float *)((uint8_t *)a.ws + part_ml_bytes(slab * a.kv.N)) : nullptr;
     kern<<<dim3((unsigned)((int64_t)splits * row_tiles), a.kv.Hkv, a.kv.N), gdn::kAttnThreads, A::SMEM, st>>>(
         a.kv, (const gdn::bf16 *)a.q, (gdn::bf16 *)a.q_out, a.lse, po, ml, a.q_tok, a.o_tok, a.Hq,
-        row_tiles, slab, tc_rows, a.max_kv_len, a.scale, a.status);
+        row_tiles, slab, tc_rows, room, a.max_kv_len, a.scale, a.status);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
     if (splits > 1 &&
         launch_dependent(gdn::kv_attention_join_kernel<D>, dim3((unsigned)a.T, a.Hq), dim3(128), 0, st, a.kv,
                          (gdn::bf16 *)a.q_out, a.lse, po, ml, a.o_tok, a.Hq, 8 * NT, slab, tc_rows,
-                         a.max_kv_len) != cudaSuccess)
+                         room, a.max_kv_len) != cudaSuccess)
         return GDN_ERR_CUDA;
     return GDN_OK;
 }
@@ -949,7 +958,7 @@ gdn_status_t mma_launch(const KvArgs &a, int row_tiles, int splits, int tc_rows,
 size_t kv_attention_workspace(int32_t D, int32_t Hq, int32_t Hkv, int64_t T, int32_t N,
                               int32_t max_q_len, int32_t max_kv_len, int in_f32, uint32_t flags) {
     if (in_f32 || (flags & GDN_PREFILL_SIMT) || T <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv) return 0;
-    const int64_t slab = attn_slab(Hq, Hkv, T, N, max_q_len, max_kv_len);
+    const int64_t slab = attn_slab(Hq, Hkv, T, N, max_q_len, max_kv_len, D);
     return slab ? part_ml_bytes(slab * N) + (size_t)slab * N * D * sizeof(float) : 0;
 }
 
@@ -965,9 +974,9 @@ gdn_status_t launch_kv_attention(const KvArgs &a, cudaStream_t st) {
         m_most = (tc_rows - 1) / a.Hq;
     }
     const int64_t rows = (int64_t)(a.Hq / a.kv.Hkv) * m_most;
-    const int nt = attn_nt(rows);
+    const int nt = attn_nt(rows, a.D);
     const int64_t tiles = (rows + 8 * nt - 1) / (8 * nt);
-    const int splits = attn_max_splits(a.max_kv_len, a.min_q_len, a.Hq / a.kv.Hkv, a.kv.Hkv);
+    const int splits = attn_max_splits(a.max_kv_len, a.min_q_len, a.Hq / a.kv.Hkv, a.kv.Hkv, a.D);
     if (tiles * splits > 0x7fffffff || a.kv.N > 65535) return GDN_ERR_SHAPE;
     switch (a.D * 10 + nt) {
     case 641: return mma_launch<64, 1>(a, (int)tiles, splits, tc_rows, st);
@@ -976,12 +985,9 @@ gdn_status_t launch_kv_attention(const KvArgs &a, cudaStream_t st) {
     case 644: return mma_launch<64, 4>(a, (int)tiles, splits, tc_rows, st);
     case 1281: return mma_launch<128, 1>(a, (int)tiles, splits, tc_rows, st);
     case 1282: return mma_launch<128, 2>(a, (int)tiles, splits, tc_rows, st);
-    case 1283: return mma_launch<128, 3>(a, (int)tiles, splits, tc_rows, st);
-    case 1284: return mma_launch<128, 4>(a, (int)tiles, splits, tc_rows, st);
     case 2561: return mma_launch<256, 1>(a, (int)tiles, splits, tc_rows, st);
     case 2562: return mma_launch<256, 2>(a, (int)tiles, splits, tc_rows, st);
     case 2563: return mma_launch<256, 3>(a, (int)tiles, splits, tc_rows, st);
-    case 2564: return mma_launch<256, 4>(a, (int)tiles, splits, tc_rows, st);
     }
     return GDN_ERR_UNSUPPORTED;
 }

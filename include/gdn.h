@@ -472,14 +472,17 @@ gdn_status_t gdn_kv_read(const gdn_kv_cache_t *cache, const int32_t *cu_seqlens_
  * 0..p, weighted by exp(scale q.k).  A row that sees no key (kv_lens[n] smaller than its
  * sequence's new rows) gives zeros, and -inf in lse.
  * q, o [T, Hq, D], one type; lse fp32 [T, Hq] (natural logarithm of the weights' sum) or
- * NULL.  max_kv_len: an upper bound of kv_lens (sizes the grid); a sequence with a length
- * above it, above the block table's reach or negative sets *status_dev = GDN_ERR_SEQLENS
- * and its rows are not written.  Keys in a page outside [0, pages) are left out and set
- * GDN_ERR_INDEX.  What lies past kv_lens in a page is never used, whatever it holds.
+ * NULL.  T Hq is at most 2^31 - 1.  max_kv_len: an upper bound of kv_lens (sizes the
+ * grid), at most GDN_KV_MAX_LEN; a sequence with a length above it, above the block table's
+ * reach or negative sets *status_dev = GDN_ERR_SEQLENS and its rows are not written.  Keys
+ * in a page outside [0, pages) are left out and set GDN_ERR_INDEX.  What lies past kv_lens
+ * in a page is never used, whatever it holds.
  * workspace: device scratch of gdn_kv_attention_workspace_size() bytes, 256-byte aligned
  * (may be NULL when 0).  A sequence's results are bit-identical alone and in any batch
- * called with the same number of new rows.
+ * whose longest sequence brings the same number of new tokens.
  */
+#define GDN_KV_MAX_LEN 0x40000000
+
 size_t gdn_kv_attention_workspace_size(int32_t head_dim, int32_t Hq, int32_t Hkv, int64_t T,
                                        int32_t N, int32_t max_q_len, int32_t max_kv_len,
                                        int32_t dtype, uint32_t flags);

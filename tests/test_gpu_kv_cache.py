@@ -277,6 +277,15 @@ def test_attention_many_rows(D, Hq, Hkv):
     check_attention(c, *run_attention(c))
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 2, 2), (128, 2, 2), (256, 4, 2)])
+def test_attention_unsplit_beside_split(D, Hq, Hkv):
+    """Sequences of so many rows that their keys stay whole, in a grid made for another's
+    splits."""
+    ms, lens = [257, 1, 300, 2], [600, 1500, 301, 2500]
+    c = attention_case(28, D, Hq, Hkv, 32, ms, lens)
+    check_attention(c, *run_attention(c))
+
+
 def test_attention_many_rows_peaked_and_scaled():
     """Large scores of both signs of the scale, so that the running maximum moves often."""
     for scale in (0.3, -0.25):
