@@ -53,7 +53,7 @@ constexpr uint32_t kTile = 32768;          // one 128 x 128 bf16 tile: two 64-co
 constexpr uint32_t kBlk = 16384;
 constexpr int kLinWarps = 16;              // warps that do elementwise work
 constexpr int kLinThreads = 32 * (kLinWarps + 3);
-constexpr int kMinSplitChunks = 12;        // shorter sequences are one range
+constexpr int kMinSplitChunks = 10;        // shorter sequences are one range
 constexpr int kMinRangeChunks = 4;
 constexpr int kMinRangeTokens = kMinRangeChunks * kLinC;
 
@@ -81,8 +81,9 @@ struct LinParams {
     int32_t *status;
 };
 
-// Chunks per range of a sequence of nch chunks.  Under 12 chunks the second pass and its
-// launches cost more than they save (12 chunks of 1.5 us against 4 + 4 of 0.6 and 6 us).
+// Chunks per range of a sequence of nch chunks.  Under 10 chunks the other passes cost more
+// than they save (split against whole: 8 chunks 37 us against 33, 10 chunks 35 against 39
+// with 8 heads and 40 against 39 with 48, 11 chunks 35 and 40 against 41).
 __host__ __device__ __forceinline__ int range_chunks_of(int nch, int max_par) {
     if (nch < kMinSplitChunks || max_par <= 1) return nch > 0 ? nch : 1;
     const int rc = (nch + max_par - 1) / max_par;
