@@ -592,9 +592,10 @@ size_t gdn_linear_prefill_workspace_size(const int32_t *cu_seqlens_host, int32_t
                                          int32_t Hk, int32_t Hv, int32_t D, int32_t dtype,
                                          uint32_t flags) {
     (void)Hk;
-    if (!cu_seqlens_host || N <= 0 || T <= 0 || Hv <= 0) return 0;
-    if (!gdn_host::linear_tc_supported(D, dtype == GDN_F32, flags)) return 0;
-    return gdn_host::linear_tc_workspace(cu_seqlens_host, N, T, Hv);
+    if (!cu_seqlens_host || N <= 0 || T <= 0 || Hv <= 0 || !gdn_host::linear_supported(D)) return 0;
+    return gdn_host::linear_tc_supported(D, dtype == GDN_F32, flags)
+               ? gdn_host::linear_tc_workspace(cu_seqlens_host, N, T, Hv)
+               : gdn_host::linear_scan_workspace(cu_seqlens_host, N, T, Hv, D);
 }
 
 gdn_status_t gdn_linear_prefill(const gdn_tensor_t *q, const gdn_tensor_t *k,
@@ -628,11 +629,12 @@ gdn_status_t gdn_linear_prefill(const gdn_tensor_t *q, const gdn_tensor_t *k,
     a.status = status_dev;
     a.ws = workspace;
     a.ws_bytes = workspace_bytes;
-    if (a.T == 0 || !gdn_host::linear_tc_supported(a.D, a.in_f32, flags))
-        return gdn_host::launch_linear_scan(a, st);
-    const size_t need = gdn_host::linear_tc_workspace(cu_seqlens_host, N, a.T, a.Hv);
+    const size_t need = gdn_linear_prefill_workspace_size(cu_seqlens_host, N, a.T, a.Hk, a.Hv, a.D,
+                                                          a.in_f32 ? GDN_F32 : GDN_BF16, flags);
     if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)))
         return GDN_ERR_WORKSPACE;
+    if (a.T == 0 || !gdn_host::linear_tc_supported(a.D, a.in_f32, flags))
+        return gdn_host::launch_linear_scan(a, st);
     return gdn_host::launch_linear_tc(a, st);
 }
 

@@ -7,6 +7,8 @@
 //
 // It is the gated delta rule without its correction term, so the state's columns do not
 // interact: column j of S needs v_j only.
+#include <algorithm>
+
 #include "linear.cuh"
 
 namespace gdn {
@@ -20,7 +22,28 @@ __device__ __forceinline__ float2 decay_pair(float g) {
     return make_float2(hi, e - (hi - 1.f));
 }
 
-// One CTA per (sequence, v-head, tile of columns), walking the tokens.  A lane holds two
+// Ranges of one sequence that run side by side, where a walk over all its tokens would leave
+// SMs idle: linear_scan_kernel first gives each range's own state from zero (STATE_ONLY), then
+// linear_fold_kernel the ranges' start states, then linear_scan_kernel runs the ranges from
+// those.  A token costs a walk 118 ns (D = 64), all of it latency, so ranges are short: 64
+// tokens or more, from 256 tokens on (fp32, D = 64, 8 v-heads: 4096 tokens 438 us whole, 64 in
+// ranges; 256 tokens 33 and 21; ranges of 32, 64 and 128 tokens, two sequences of 800: 39, 37
+// and 42; 64 sequences of 384, which fill the device by themselves, 204 whole and 273 so).
+// The cut depends on the sequence's own length, the heads and the column tiles only.
+constexpr int kScanMinTokens = 256;      // shorter sequences are one range
+constexpr int kScanMinRange = 64;
+constexpr int kScanCtas = 4 * 152;       // CTAs that ranges are made for
+__host__ __device__ __forceinline__ int scan_range_tokens(int len, int ctas) {   // ctas: of one range
+    if (len < kScanMinTokens) return len > 0 ? len : 1;
+    const int par = kScanCtas / ctas > 1 ? kScanCtas / ctas : 1;
+    const int rt = ((len + par - 1) / par + 15) / 16 * 16;
+    return rt > kScanMinRange ? rt : kScanMinRange;
+}
+// A sequence's first slot in the workspace (a state and a decay for each v-head); it has one
+// slot more than ranges after its first, at most len / 64.
+__device__ __forceinline__ int64_t scan_slot0(int n, int t0) { return t0 / kScanMinRange + n; }
+
+// One CTA per (sequence, range, v-head, tile of columns), walking the tokens.  A lane holds two
 // columns of D / RG rows: lanes with equal column pairs split the rows in groups of four
 // (rows 4 rg + 4 RG x ..+3), so a float4 of k or q is read by all lanes of a warp without
 // bank conflicts, and o is summed over the RG lanes by shuffles in a fixed order.
@@ -34,14 +57,15 @@ template <int D> struct LinShape {
     static constexpr int FIX = 8;                        // tokens per correction of the decay
 };
 
-template <typename T, int D>
+template <typename T, int D, bool STATE_ONLY>
 __global__ void __launch_bounds__(LinShape<D>::WARPS * 32)
 linear_scan_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
                    T *__restrict__ o, int64_t q_tok, int64_t k_tok, int64_t v_tok,
                    int64_t o_tok, const float *__restrict__ g, int64_t g_tok,
-                   const int32_t *__restrict__ cu, const float *__restrict__ h0, float *hT,
-                   int Hk, int Hv, float scale) {
+                   const int32_t *__restrict__ cu, const float *h0, float *hT,
+                   float *ranges, float *range_decay, int in_place, int Hk, int Hv, float scale) {
     using L = LinShape<D>;
+    constexpr int TILES = D / L::COLS;
     constexpr int THREADS = L::WARPS * 32;
     constexpr int NQ = L::TB * D / THREADS, NV = L::TB * L::COLS / THREADS;   // staged per thread
     __shared__ float4 sq[2][L::TB][D / 4], sk[2][L::TB][D / 4];
@@ -49,31 +73,46 @@ linear_scan_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__
     __shared__ float sa[2][L::TB], slo[2][L::TB];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rg = lane % L::RG, cp = warp * (L::CW / 2) + lane / L::RG;
-    const int j0 = blockIdx.x * L::COLS, hv = blockIdx.y, n = blockIdx.z;
+    const int j0 = blockIdx.x % TILES * L::COLS, range = blockIdx.x / TILES, hv = blockIdx.y, n = blockIdx.z;
     const int hk = hv / (Hv / Hk);
-    const int t0 = cu[n], len = cu[n + 1] - t0;
-    const size_t st0 = ((size_t)n * Hv + hv) * D * D + j0 + 2 * cp;
+    const int seq0 = cu[n], seq_len = cu[n + 1] - seq0;
+    const int rt = scan_range_tokens(seq_len, Hv * TILES);
+    const bool last = (range + 1) * rt >= seq_len;
+    if (range > 0 && range * rt >= seq_len || STATE_ONLY && last) return;
+    const int t0 = seq0 + range * rt, len = min(rt, seq_len - range * rt);
+    const size_t col0 = j0 + 2 * cp;
+    const size_t slot = ((size_t)(scan_slot0(n, seq0) + range) * Hv + hv) * D * D;
+    // where the range starts from: the caller's state, or its slot (which has a copy of the
+    // caller's where that may be overwritten by the last range)
+    const float *from = nullptr;
+    if (!STATE_ONLY) {
+        if (range > 0 || in_place && !last) {
+            grid_dependency_wait();
+            from = ranges + slot;
+        } else if (h0) from = h0 + ((size_t)n * Hv + hv) * D * D;
+    }
 
     float2 S[L::RX][4];
 #pragma unroll
     for (int x = 0; x < L::RX; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            S[x][e] = h0 ? *reinterpret_cast<const float2 *>(
-                               h0 + st0 + (size_t)(4 * rg + 4 * L::RG * x + e) * D)
-                         : make_float2(0.f, 0.f);
+            S[x][e] = from ? *reinterpret_cast<const float2 *>(
+                                 from + col0 + (size_t)(4 * rg + 4 * L::RG * x + e) * D)
+                           : make_float2(0.f, 0.f);
 
     // The next block of tokens is on its way to registers while this one is worked on; rows
     // past the end read as zeros.
     T rq[NQ], rk[NQ], rv[NV];
     float rgate = 0.f;
+    double gates = 0.;           // STATE_ONLY: sum of this thread's
     auto load = [&](int b) {
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
             const int i = tid + THREADS * x, t = b + i / D, d = i % D;
             const bool in = t < len;
             const int64_t row = t0 + (in ? t : 0);
-            rq[x] = in ? q[row * q_tok + (int64_t)hk * D + d] : from_f32<T>(0.f);
+            if (!STATE_ONLY) rq[x] = in ? q[row * q_tok + (int64_t)hk * D + d] : from_f32<T>(0.f);
             rk[x] = in ? k[row * k_tok + (int64_t)hk * D + d] : from_f32<T>(0.f);
         }
 #pragma unroll
@@ -87,7 +126,7 @@ linear_scan_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
             const int i = tid + THREADS * x;
-            reinterpret_cast<float *>(sq[u][i / D])[i % D] = to_f32(rq[x]);
+            if (!STATE_ONLY) reinterpret_cast<float *>(sq[u][i / D])[i % D] = to_f32(rq[x]);
             reinterpret_cast<float *>(sk[u][i / D])[i % D] = to_f32(rk[x]);
         }
 #pragma unroll
@@ -96,6 +135,7 @@ linear_scan_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__
             reinterpret_cast<float *>(sv[u][i / L::COLS])[i % L::COLS] = to_f32(rv[x]);
         }
         if (tid < L::TB) {
+            if (STATE_ONLY) gates += rgate;
             const float2 a = decay_pair(rgate);
             sa[u][tid] = a.x;
             slo[u][tid] = a.x > 0.f ? a.y / a.x : 0.f;
@@ -126,14 +166,17 @@ linear_scan_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__
                 acc[e] = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int x = 0; x < L::RX; ++x) {
-                    const float4 k4 = sk[u][t][rg + L::RG * x], q4 = sq[u][t][rg + L::RG * x];
+                    const float4 k4 = sk[u][t][rg + L::RG * x];
+                    const float4 q4 = STATE_ONLY ? make_float4(0.f, 0.f, 0.f, 0.f) : sq[u][t][rg + L::RG * x];
                     const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
                         S[x][y].x = fmaf(S[x][y].x, a, kk[y] * vv.x);
                         S[x][y].y = fmaf(S[x][y].y, a, kk[y] * vv.y);
-                        acc[e].x = fmaf(qq[y], S[x][y].x, acc[e].x);
-                        acc[e].y = fmaf(qq[y], S[x][y].y, acc[e].y);
+                        if (!STATE_ONLY) {
+                            acc[e].x = fmaf(qq[y], S[x][y].x, acc[e].x);
+                            acc[e].y = fmaf(qq[y], S[x][y].y, acc[e].y);
+                        }
                     }
                 }
             }
@@ -141,7 +184,7 @@ linear_scan_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__
             // with tokens rg FIX / RG ..
             int keep = L::FIX;
 #pragma unroll
-            for (int off = L::RG / 2; off > 0; off >>= 1) {
+            for (int off = STATE_ONLY ? 0 : L::RG / 2; off > 0; off >>= 1) {
                 keep >>= 1;
                 const bool up = rg & off;
 #pragma unroll
@@ -152,7 +195,7 @@ linear_scan_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__
                 }
             }
 #pragma unroll
-            for (int e = 0; e < L::FIX / L::RG; ++e) {
+            for (int e = 0; e < (STATE_ONLY ? 0 : L::FIX / L::RG); ++e) {
                 const int64_t t = b + f + rg * (L::FIX / L::RG) + e;
                 if (t < len) {
                     out[t * o_tok] = from_f32<T>(scale * acc[e].x);
@@ -170,13 +213,66 @@ linear_scan_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__
         }
         if (more) stage(u ^ 1);
     }
-    if (hT) {
+    float *to = STATE_ONLY ? ranges + slot + (size_t)Hv * D * D
+                           : last && hT ? hT + ((size_t)n * Hv + hv) * D * D : nullptr;
+    if (to) {
 #pragma unroll
         for (int x = 0; x < L::RX; ++x)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<float2 *>(hT + st0 + (size_t)(4 * rg + 4 * L::RG * x + e) * D) =
+                *reinterpret_cast<float2 *>(to + col0 + (size_t)(4 * rg + 4 * L::RG * x + e) * D) =
                     S[x][e];
+    }
+    if (STATE_ONLY && warp == 0) {
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) gates += __shfl_xor_sync(0xffffffffu, gates, off);
+        if (tid == 0 && j0 == 0) range_decay[slot / (D * D) + Hv] = (float)gates;
+    }
+}
+
+// Start states of a sequence's ranges, in order, over the ranges' own states: the slot of range
+// r has the state that range r - 1 adds, and receives the start of range r,
+// S <- e^{decay of r - 1} S + it.  Four elements a thread; bound by memory.
+template <int D> struct LinFold {
+    static constexpr int THREADS = D * D / 4 < 256 ? D * D / 4 : 256;
+};
+template <int D>
+__global__ void __launch_bounds__(LinFold<D>::THREADS)
+linear_fold_kernel(const int32_t *__restrict__ cu, const float *__restrict__ h0, float *ranges,
+                   const float *__restrict__ range_decay, int in_place, int ctas, int Hv) {
+    const int hv = blockIdx.y, n = blockIdx.z;
+    const int t0 = cu[n], len = cu[n + 1] - t0;
+    const int rt = scan_range_tokens(len, ctas), count = (len + rt - 1) / rt;
+    if (count <= 1) return;
+    const int at = blockIdx.x * LinFold<D>::THREADS + threadIdx.x;
+    const int64_t row = scan_slot0(n, t0) * Hv + hv;
+    float4 *R = reinterpret_cast<float4 *>(ranges + row * D * D) + at;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    grid_dependency_wait();
+    if (h0) s = reinterpret_cast<const float4 *>(h0 + ((int64_t)n * Hv + hv) * D * D)[at];
+    if (in_place) *R = s;
+    constexpr int AHEAD = 8;         // loads that do not wait for the chain
+    const int64_t step = (int64_t)Hv * (D * D / 4);
+    for (int r0 = 1; r0 < count; r0 += AHEAD) {
+        float4 x[AHEAD];
+        float a[AHEAD];
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) {
+            if (r0 + e < count) {
+                x[e] = R[(r0 + e) * step];
+                a[e] = expf(range_decay[row + (int64_t)(r0 + e) * Hv]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) {
+            if (r0 + e < count) {
+                s.x = fmaf(a[e], s.x, x[e].x);
+                s.y = fmaf(a[e], s.y, x[e].y);
+                s.z = fmaf(a[e], s.z, x[e].z);
+                s.w = fmaf(a[e], s.w, x[e].w);
+                R[(r0 + e) * step] = s;
+            }
+        }
     }
 }
 
@@ -248,13 +344,52 @@ namespace gdn_host {
 
 namespace {
 
+template <int D> constexpr int scan_tiles() { return D / gdn::LinShape<D>::COLS; }
+int scan_tiles_of(int64_t D) { return D == 16 ? scan_tiles<16>() : D == 32 ? scan_tiles<32>() : D == 64 ? scan_tiles<64>() : scan_tiles<128>(); }
+
+// Most ranges that a sequence of the batch has, and slots of the workspace (0: none needed).
+struct ScanPlan {
+    int ranges;
+    int64_t slots;
+};
+ScanPlan plan_scan(const int32_t *cu, int32_t N, int64_t T, int ctas) {
+    int most = 1;
+    for (int32_t n = 0; n < N; ++n) {
+        const int len = cu[n + 1] - cu[n], rt = gdn::scan_range_tokens(len, ctas);
+        most = std::max(most, (len + rt - 1) / rt);
+    }
+    return {most, most > 1 ? T / gdn::kScanMinRange + N : 0};
+}
+size_t scan_state_bytes(int64_t slots, int32_t Hv, int64_t D) { return (size_t)slots * Hv * D * D * sizeof(float); }
+
 template <typename T, int D>
 gdn_status_t scan_launch(const LinearArgs &a, cudaStream_t st) {
     using L = gdn::LinShape<D>;
-    gdn::linear_scan_kernel<T, D><<<dim3(D / L::COLS, a.Hv, a.N), L::WARPS * 32, 0, st>>>(
-        (const T *)a.q, (const T *)a.k, (const T *)a.v, (T *)a.o, a.q_tok, a.k_tok, a.v_tok,
-        a.o_tok, a.g, a.g_tok, a.cu, a.h0, a.hT, a.Hk, a.Hv, a.scale);
-    return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    constexpr int tiles = scan_tiles<D>();
+    const ScanPlan pl = plan_scan(a.cu_host, a.N, a.T, a.Hv * tiles);
+    float *ranges = (float *)a.ws;
+    float *decay = (float *)((uint8_t *)a.ws + scan_state_bytes(pl.slots, a.Hv, D));
+    const int in_place = a.h0 && a.h0 == a.hT;
+    const dim3 block(L::WARPS * 32), grid(pl.ranges * tiles, a.Hv, a.N);
+    const T *q = (const T *)a.q, *k = (const T *)a.k, *v = (const T *)a.v;
+    if (pl.ranges <= 1) {
+        gdn::linear_scan_kernel<T, D, false><<<grid, block, 0, st>>>(
+            q, k, v, (T *)a.o, a.q_tok, a.k_tok, a.v_tok, a.o_tok, a.g, a.g_tok, a.cu, a.h0, a.hT,
+            ranges, decay, in_place, a.Hk, a.Hv, a.scale);
+        return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    }
+    gdn::linear_scan_kernel<T, D, true><<<dim3((pl.ranges - 1) * tiles, a.Hv, a.N), block, 0, st>>>(
+        q, k, v, (T *)a.o, a.q_tok, a.k_tok, a.v_tok, a.o_tok, a.g, a.g_tok, a.cu, a.h0, a.hT,
+        ranges, decay, in_place, a.Hk, a.Hv, a.scale);
+    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+    constexpr int threads = gdn::LinFold<D>::THREADS;
+    if (launch_dependent(gdn::linear_fold_kernel<D>, dim3(D * D / 4 / threads, a.Hv, a.N), dim3(threads), 0, st,
+                         a.cu, a.h0, ranges, decay, in_place, a.Hv * tiles, a.Hv) != cudaSuccess ||
+        launch_dependent(gdn::linear_scan_kernel<T, D, false>, grid, block, 0, st, q, k, v, (T *)a.o, a.q_tok,
+                         a.k_tok, a.v_tok, a.o_tok, a.g, a.g_tok, a.cu, a.h0, a.hT, ranges, decay, in_place,
+                         a.Hk, a.Hv, a.scale) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    return GDN_OK;
 }
 
 template <typename T, int D>
@@ -279,6 +414,11 @@ gdn_status_t decode_launch(const LinearArgs &a, cudaStream_t st) {
     return GDN_ERR_UNSUPPORTED
 
 bool linear_supported(int64_t D) { return D == 16 || D == 32 || D == 64 || D == 128; }
+
+size_t linear_scan_workspace(const int32_t *cu, int32_t N, int64_t T, int32_t Hv, int64_t D) {
+    const int64_t slots = plan_scan(cu, N, T, Hv * scan_tiles_of(D)).slots;
+    return slots ? scan_state_bytes(slots, Hv, D) + (size_t)slots * Hv * sizeof(float) : 0;
+}
 
 gdn_status_t launch_linear_scan(const LinearArgs &a, cudaStream_t st) {
     GDN_LIN_DISPATCH(scan_launch, a, st);

@@ -31,6 +31,7 @@ bool linear_supported(int64_t D);
 bool linear_tc_supported(int64_t D, int in_f32, uint32_t flags);
 size_t linear_tc_workspace(const int32_t *cu_host, int32_t N, int64_t T, int32_t Hv);
 gdn_status_t launch_linear_tc(const LinearArgs &a, cudaStream_t st);
+size_t linear_scan_workspace(const int32_t *cu_host, int32_t N, int64_t T, int32_t Hv, int64_t D);
 gdn_status_t launch_linear_scan(const LinearArgs &a, cudaStream_t st);
 gdn_status_t launch_linear_decode(const LinearArgs &a, cudaStream_t st);
 }  // namespace gdn_host

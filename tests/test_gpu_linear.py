@@ -85,6 +85,37 @@ def test_prefill_cuda_cores(D, dtype):
     check(d, o, h, dtype == torch.float32 or D != 128, 0.5)
 
 
+@pytest.mark.parametrize("D,dtype", [(16, torch.float32), (32, torch.bfloat16),
+                                     (64, torch.float32), (64, torch.bfloat16),
+                                     (128, torch.float32)])
+def test_prefill_cuda_cores_ranges(D, dtype):
+    """Sequences cut into ranges beside short ones: a memory of hundreds of tokens, cleared
+    states, the state in place, and the bits that each sequence gives alone."""
+    lens = [700, 255, 1, 256, 0, 1000]
+    d = make(12, lens, 1, 2, D, dtype, True, True, slow=True)
+    d["g"][300, 1] = -float("inf")
+    d["g"][1500:1510, 0] = -300.0
+    o, h = call(d, simt=True)
+    check(d, o, h, True)
+    state = d["h0"].cuda()
+    o2, _ = gdn.gdn_linear_prefill(d["q"].cuda(), d["k"].cuda(), d["v"].cuda(), d["g"].cuda(),
+                                   d["cu"].cuda(), initial_state=state, final_state=state,
+                                   simt=True, cu_seqlens_host=d["cu"])
+    assert_bits_equal(o, o2, "o with the state in place")
+    assert_bits_equal(h, state, "state in place")
+    cu = d["cu"].tolist()
+    for n in (0, 1, 5):
+        sl = slice(cu[n], cu[n + 1])
+        one = dict(q=d["q"][sl], k=d["k"][sl], v=d["v"][sl], g=d["g"][sl], h0=d["h0"][n:n + 1],
+                   cu=torch.tensor([0, lens[n]], dtype=torch.int32))
+        o1, h1 = call(one, simt=True)
+        assert_bits_equal(o[sl], o1, "o of sequence %d" % n)
+        assert_bits_equal(h[n:n + 1], h1, "state of sequence %d" % n)
+    # per-head decays, no state to start from
+    d = make(13, [511, 257], 1, 2, D, dtype, False, False)
+    check(d, *call(d, simt=True), True)
+
+
 @pytest.mark.parametrize("Hk,Hv", [(1, 1), (3, 3), (1, 5), (4, 8)])
 def test_prefill_head_layouts(Hk, Hv):
     d = make(3, [200, 17], Hk, Hv, 128, torch.bfloat16, True, True)
