@@ -11,8 +11,9 @@
 // 4096 tokens of 48 heads):
 //     Q K^T,   Q S,   P V,   (hi + lo + rest)^T V
 // e^{T - G_j} comes from sums taken from the chunk's end and e^{G_i - G_j} inside a 32 x 32
-// block from its exponent, elsewhere as a product of two factors at most 1, so nothing
-// overflows however strong the decay.
+// block as a product of two factors where the block decays by less than 2^60, else from its
+// exponent, and elsewhere as a product of two factors at most 1: nothing overflows however
+// strong the decay.
 //
 // Roundings below fp32, all to bf16 and all in operands whose products only reach the bf16
 // output: P, and S where it multiplies Q.  The state itself never goes through them.
@@ -53,7 +54,7 @@ constexpr uint32_t kTile = 32768;          // one 128 x 128 bf16 tile: two 64-co
 constexpr uint32_t kBlk = 16384;
 constexpr int kLinWarps = 16;              // warps that do elementwise work
 constexpr int kLinThreads = 32 * (kLinWarps + 3);
-constexpr int kMinSplitChunks = 10;        // shorter sequences are one range
+constexpr int kMinSplitChunks = 12;        // shorter sequences are one range
 constexpr int kMinRangeChunks = 4;
 constexpr int kMinRangeTokens = kMinRangeChunks * kLinC;
 
@@ -81,9 +82,10 @@ struct LinParams {
     int32_t *status;
 };
 
-// Chunks per range of a sequence of nch chunks.  Under 10 chunks the other passes cost more
-// than they save (split against whole: 8 chunks 37 us against 33, 10 chunks 35 against 39
-// with 8 heads and 40 against 39 with 48, 11 chunks 35 and 40 against 41).
+// Chunks per range of a sequence of nch chunks.  Under 12 chunks the other passes cost more
+// than they save wherever the device is busy (alone, split against whole: 8 chunks 37 us
+// against 33, 10 chunks 35 against 39 with 8 heads and 40 against 39 with 48; a batch of
+// eight ragged sequences of 48 heads, split from 10 on: 434 against 419).
 __host__ __device__ __forceinline__ int range_chunks_of(int nch, int max_par) {
     if (nch < kMinSplitChunks || max_par <= 1) return nch > 0 ? nch : 1;
     const int rc = (nch + max_par - 1) / max_par;
@@ -435,12 +437,13 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             uint32_t pk[16];
             if (jb <= lq) {
                 const float gi = S.g2[row];
-                const float f = jb < lq ? p.scale * ex2(gi - S.ref[jb]) : 0.f;
+                const bool slow = jb == lq && S.g2[32 * jb] - S.ref[jb] >= 60.f;
+                const float f = p.scale * ex2(gi - S.ref[jb]);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     float v[16];
                     tc::tmem_ld16(tm + colSc + 16 * c, v);
-                    if (jb < lq) {
+                    if (!slow) {
                         float4 b4[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) b4[j] = reinterpret_cast<const float4 *>(S.b)[8 * jb + 4 * c + j];
@@ -451,6 +454,10 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                             v[4 * j + 1] *= f * b4[j].y;
                             v[4 * j + 2] *= f * b4[j].z;
                             v[4 * j + 3] *= f * b4[j].w;
+                        }
+                        if (jb == lq) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] = 16 * c + j <= lane ? v[j] : 0.f;
                         }
                     } else {
                         tc::tmem_wait_ld();
