@@ -4,7 +4,7 @@ Bounds, from the roundings that each path makes (A: the same sums over absolute 
 * bf16 o: its own rounding (2^-8 |o|), and at most two of the factors of a term rounded to
   bf16 (2 * 2^-8 A), with half of one more for everything in fp32.
 * fp32 o and all states: (T + D) roundings of 2^-24 A at most, and 2^-16 A for states whose
-  keys go through the tensor cores as a pair of bf16 (twice the 2^-17 that the pair leaves
+  keys go through the tensor cores in bf16 terms (twice the 2^-17 that two of them leave
   out).
 """
 import numpy as np
