@@ -13,7 +13,7 @@
 // elements (a 16-byte load of bf16), four lanes share a group.  The token's place and its
 // angles are found once for all its heads, and rows of q skip the quantisation; with one row
 // per lane group and everything per row the kernel was bound by instruction issue (362 a
-// warp, 83 us for 8314 tokens of 32 + 2 x 8 heads of 128; 45 us now, 192 MB at 63% of the HBM
+// warp, 83 us for 8314 tokens of 32 + 2 x 8 heads of 128; 48 us now, 192 MB at 59% of the HBM
 // rate, issue slots 56% taken).  Reading the same rows back moves 55 MB in 12 us where the
 // cache is still in the L2, 25 from HBM.
 #include <algorithm>
@@ -247,11 +247,12 @@ namespace gdn_host {
 
 namespace {
 
-// Parts a token's rows are cut into, so that a few tokens still fill the device: enough for
-// 2400 warps in all (16 an SM), at most one part per row step.  (20000 warps, three parts of
-// 8314 tokens each: writing 49.9 us against 49.3, reading 12.4 against 12.5.)
+// Parts a token's rows are cut into, so that a few tokens fill the device and many leave no
+// long last round: enough for 16000 warps in all (three rounds of what fits), at most one part
+// per row step.  Every part looks the place and the angles up again (8314 tokens written and
+// read back, from HBM: one part 73.5 us, two 69, four 69, six 82).
 int kv_parts(int64_t tokens, int steps) {
-    const int64_t want = (2400 + tokens - 1) / tokens;
+    const int64_t want = (16000 + tokens - 1) / tokens;
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, steps), 65535));
 }
 
