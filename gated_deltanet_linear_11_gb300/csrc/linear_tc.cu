@@ -31,8 +31,8 @@
 // leaves 3328 clocks of traffic and room for two buffers of each of Q, K and V.  TMEM (512
 // columns): scores / P and rest, Q S, P V / weighted keys, state.
 //
-// 4096 tokens of 16 k-heads and 48 v-heads take 68 us, 8 packed prompts of 27598 tokens 407:
-// 2.0 and 2.4 TB/s of what has to be moved, 188 and 213 TFLOP/s.  A chunk takes about 5700
+// 4096 tokens of 16 k-heads and 48 v-heads take 68 us, 8 packed prompts of 27598 tokens 399:
+// 2.0 and 2.4 TB/s of what has to be moved, 188 and 218 TFLOP/s.  A chunk takes about 5700
 // clocks, A 1500 (packing on the ALU pipe), B 1300, C 750, D 900 and the waits for products
 // between them; one CTA fills an SM's TMEM and shared memory, so nothing else hides them.
 //
@@ -63,6 +63,8 @@ constexpr int kMinSplitChunks = 12;        // shorter sequences are one range
 constexpr int kMinRangeChunks = 4;
 constexpr int kMinRangeTokens = kMinRangeChunks * kLinC;
 
+constexpr int kOrdered = 64;
+
 struct LinMaps {
     CUtensorMap q, k, v, o;
 };
@@ -85,6 +87,12 @@ struct LinParams {
                           // sequence may overwrite before its first range has read it
     float scale;
     int32_t *status;
+    // Sequences from the longest to the shortest, where there are at most kOrdered of them: a
+    // long one started last would leave the device to itself (eight packed prompts of 951 to
+    // 8192 tokens: 407 us as they come, 399 so; with more of them each is a small part).
+    int ordered;
+    uint8_t order[kOrdered];
+    __device__ __forceinline__ int sequence(int z) const { return ordered ? order[z] : z; }
 };
 
 // Chunks per range of a sequence of nch chunks.  Under 12 chunks the other passes cost more
@@ -363,7 +371,7 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     }
     uint8_t *sS = S.tile[6];      // Q, K, V of chunk i: tiles 0, 2, 4 + (i & 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int range = blockIdx.x, hv = blockIdx.y, n = blockIdx.z, hk = hv / (p.Hv / p.Hk);
+    const int range = blockIdx.x, hv = blockIdx.y, n = p.sequence(blockIdx.z), hk = hv / (p.Hv / p.Hk);
     const int t0 = p.cu[n], len = p.cu[n + 1] - t0;
     const int nch = (len + kLinC - 1) / kLinC;
     const int rc = range_chunks_of(nch, p.max_par);
@@ -659,7 +667,7 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         return;
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int range = blockIdx.x, hv = blockIdx.y, n = blockIdx.z, hk = hv / (p.Hv / p.Hk);
+    const int range = blockIdx.x, hv = blockIdx.y, n = p.sequence(blockIdx.z), hk = hv / (p.Hv / p.Hk);
     const int t0 = p.cu[n], len = p.cu[n + 1] - t0;
     const int nch = (len + kLinC - 1) / kLinC;
     const int rc = range_chunks_of(nch, p.max_par);
@@ -904,6 +912,15 @@ gdn_status_t launch_linear_tc(const LinearArgs &a, cudaStream_t st) {
     p.slots_per_seq = pl.slots_per_seq;
     p.scale = a.scale;
     p.status = a.status;
+    p.ordered = a.N > 1 && a.N <= gdn::kOrdered;
+    if (p.ordered) {
+        for (int n = 0; n < a.N; ++n) p.order[n] = (uint8_t)n;
+        const int32_t *cu = a.cu_host;
+        std::sort(p.order, p.order + a.N, [cu](int x, int y) {
+            const int lx = cu[x + 1] - cu[x], ly = cu[y + 1] - cu[y];
+            return lx != ly ? lx > ly : x < y;
+        });
+    }
     static std::atomic<uint64_t> ready{0};   // one bit per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
