@@ -106,6 +106,29 @@ def test_kv_refusals(lib):
     assert [lib.gdn_kv_record_bytes(d) for d in (64, 128, 256, 96, 0)] == [40, 80, 160, 0, 0]
 
 
+@no_gpu
+def test_limits_and_missing_workspaces(lib):
+    r = ctypes.byref
+
+    def attend(T=8, Hq=4, max_len=32):
+        x = desc(T, Hq, 128)
+        return lib.gdn_kv_attention(cache(), FAKE, offsets(0, T), max_len, r(x), 1.0, 0, r(x), None,
+                                    None, 0, None, None)
+    assert attend(max_len=(1 << 30) + 1) == 2
+    assert attend(T=1 << 26, Hq=32) == 2
+    assert attend(max_len=1000) == 9                   # splits need a workspace
+    x = desc(300, 2, 64, dtype=_lib.GDN_F32)
+    size = lib.gdn_linear_prefill_workspace_size(offsets(0, 300), 1, 300, 2, 2, 64, _lib.GDN_F32, 0)
+    assert size >= 3 * 2 * 64 * 64 * 4                 # three ranges begin from a state each
+
+    def prefill(ws, nbytes):
+        return lib.gdn_linear_prefill(r(x), r(x), r(x), FAKE, 1, FAKE, offsets(0, 300), 1, 1.0, 0,
+                                      None, r(x), None, ws, nbytes, None, None)
+    assert prefill(None, size) == 9
+    assert prefill(FAKE, size - 1) == 9
+    assert prefill(FAKE + 16, size) == 9
+
+
 def test_forced_errors_reach_the_new_entries(monkeypatch):
     gdn = pytest.importorskip("gated_deltanet_linear_11_gb300")
     z = torch.zeros(1)
