@@ -166,19 +166,23 @@ kv_attention_simt_kernel(KvView kv, const T *__restrict__ q, T *__restrict__ o, 
 // 23% of the HBM rate, bound by latency at eight warps an SM.
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kAttnBlock = 32;      // keys per step of a warp
 
-// NT tiles of eight rows; VS: warps that share a slice of the keys (2 where the output
-// accumulators, D NT / 4 registers a thread, would not fit otherwise).  Each of the two takes
-// the scores of half a block's keys and, with the other's weights, half the values' elements
-// (116 -> 109 us on the 131072 keys above; before, both computed all scores).
+// NT tiles of eight rows; VS: warps that share a slice of the keys (four where the output
+// accumulators, D NT / 4 registers a thread, would not fit otherwise).  Each of the four takes
+// the scores of a quarter of a block's keys and, with the others' weights, a quarter of the
+// values' elements.
 template <int D, int NT> struct AttnShape {
     using R = KvRec<D>;
     static constexpr int ROWS = 8 * NT;
-    static constexpr int VS = D * NT > 256 ? 2 : 1;
+    static constexpr int VS = D * NT > 256 ? 4 : 1;
     static constexpr int SLICES = kAttnWarps / VS;
-    static constexpr int HALF = kAttnBlock * R::BYTES;          // one block's keys, or values
-    static constexpr int RING = kAttnWarps * 4 * HALF;          // two blocks of each, per warp
+    static constexpr int KSUB = VS > 1 ? 4 : 2;                 // a block: parts of 16 keys
+    static constexpr int BLOCK = 16 * KSUB;
+    static constexpr int PART = 16 * R::BYTES;
+    static constexpr int KEYS = BLOCK / VS * R::BYTES;          // a block's keys of one warp
+    static constexpr int VALUES = BLOCK * R::BYTES;             // and its values
+    // two blocks of each: keys for every warp, values for every slice
+    static constexpr int RING = 2 * (kAttnWarps * KEYS + SLICES * VALUES);
     static constexpr int JOIN = SLICES * ROWS * D * 4;          // reuses the ring
     static constexpr int BUF = RING > JOIN ? RING : JOIN;
     static constexpr int QF = NT * R::NG * 32 * 16;             // q fragments
@@ -188,7 +192,7 @@ template <int D, int NT> struct AttnShape {
     static constexpr int SMEM = BUF + QF + QM + TAIL;
     // CTAs per SM: latency is what more of them hide, until registers spill (64 sequences of
     // up to 16384 keys, D NT = 128: 173 us with four, 192 with three, 191 with five)
-    static constexpr int CTAS = D * NT <= 128 ? 4 : 2;
+    static constexpr int CTAS = D * NT <= 128 ? 4 : VS > 1 ? 3 : 2;
 };
 
 // Keys per split of a context of len keys.  A warp's start and join cost about as much as 40
@@ -200,22 +204,25 @@ template <int D, int NT> struct AttnShape {
 // with 2048, 144 with 1024, 204 with 3456).  From 256 new rows on nothing is split.  All of
 // it depends on the sequence's own lengths and heads only.
 constexpr int kSplitMaxRows = 256;
-constexpr int kSplitCtas = 2 * 152;
+// CTAs on the device at once that splits are made for (tiles of 256 elements: two an SM for
+// eight rows, three for more), and the most of them.
+__host__ __device__ __forceinline__ int split_ctas(int rows, int D) { return (D == 256 && rows > 8 ? 3 : 2) * 152; }
+constexpr int kSplitMaxCtas = 3 * 152;
 // Most tiles of eight rows a CTA takes.  What more would save in reading and unpacking keys is
 // lost again where two warps have to share the elements (D NT > 256): 16 sequences of 4096 to
 // 8192 keys, 32 rows of 128, 131 us with two, 155 with four; but D = 256, 72 rows, 250 with
 // three, 303 with one.
 __host__ __device__ constexpr int attn_max_nt(int D) { return D == 256 ? 3 : D == 128 ? 2 : 4; }
 __host__ __device__ __forceinline__ int kv_split_base(int len) { return len <= 512 ? 128 : len <= 2048 ? 256 : 1024; }
-// Splits that one sequence of m new rows has room for on the device.
-__host__ __device__ __forceinline__ int kv_split_room(int m, int G, int Hkv, int D) {
+// Splits that one sequence of m new rows has room for among `fit` CTAs.
+__host__ __device__ __forceinline__ int kv_split_room(int m, int G, int Hkv, int D, int fit) {
     const int rows = 8 * attn_max_nt(D);
     const int64_t ctas = (int64_t)Hkv * ((G * m + rows - 1) / rows);
-    return m >= kSplitMaxRows || 2 * ctas > kSplitCtas ? 1 : (int)(kSplitCtas / (ctas > 0 ? ctas : 1));
+    return m >= kSplitMaxRows || 2 * ctas > fit ? 1 : (int)(fit / (ctas > 0 ? ctas : 1));
 }
 // (room for single tokens comes with the launch: a division less on the way to the first load)
 __device__ __forceinline__ int kv_split_len(int len, int m, int G, int Hkv, int D, int room_one) {
-    const int room = m == 1 ? room_one : kv_split_room(m, G, Hkv, D), base = kv_split_base(len);
+    const int room = m == 1 ? room_one : kv_split_room(m, G, Hkv, D, split_ctas(G * m, D)), base = kv_split_base(len);
     if (room <= 1) return 0x40000000;
     if ((int64_t)room * base >= len) return base;
     return ((len + room - 1) / room + 63) / 64 * 64;
@@ -326,25 +333,27 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
 
     // ---- the warp's rings of keys and of values: block b holds keys k0 + 32 (slice + SLICES b) ..
     const int slice = warp / A::VS, dh = warp % A::VS;
-    constexpr int STEP = kAttnBlock * A::SLICES;
-    uint64_t *bar_k = bars + 4 * warp, *bar_v = bar_k + 2;
-    uint32_t *pg = spages + 4 * warp;          // per block (mod 4): which 16 records are there
-    uint8_t *ring_k = ring + warp * 4 * A::HALF, *ring_v = ring_k + 2 * A::HALF;
-    const int first = k0 + kAttnBlock * slice;
+    constexpr int STEP = A::BLOCK * A::SLICES, KSUB = A::KSUB;
+    uint64_t *bar_k = bars + 4 * warp, *bar_v = (A::VS > 1 ? bars : bar_k) + 2;
+    uint32_t *pg = spages + 4 * warp;          // per block (mod 4): which parts are there
+    uint8_t *ring_k = ring + warp * 2 * A::KEYS, *ring_v = ring + 2 * (kAttnWarps * A::KEYS + slice * A::VALUES);
+    const int first = k0 + A::BLOCK * slice;
     const int blocks = k1 > first ? (k1 - first + STEP - 1) / STEP : 0;
-    // Lanes 0, 1 copy the two 16-record parts of a block's keys (or the one that this warp
-    // takes), lanes 2, 3 of its values; a page outside the cache is left out and marked.  Keys run two blocks ahead, values one;
-    // the page of a lane's next copy is looked up one copy ahead.
-    const int sub_l = lane & 1, which = (lane >> 1) & 1;
-    const uint32_t my_keys = A::VS > 1 ? 1u << dh : 3u;
+    // A lane each looks up the pages of a block's parts, for its keys and then for its values,
+    // and copies them (warps that share a slice: each its own part); a page outside the cache
+    // is left out and marked.  Keys run two blocks ahead, values one; the page of a lane's next
+    // copy is looked up one copy ahead.
+    const int sub_l = lane % KSUB, which = (lane / KSUB) & 1;
+    const bool copies = A::VS == 1 || sub_l == dh;
+    const uint32_t all_parts = (1u << KSUB) - 1, my_parts = A::VS > 1 ? 1u << dh : all_parts;
     const int32_t *table = kv.table + (int64_t)n * kv.table_width;
     const int64_t page_bytes = (int64_t)(2 * kv.Hkv * REC) << kv.page_log2;
     const uint8_t *base = kv.block(0, which, hkv, REC);
     const int slot_mask = (1 << kv.page_log2) - 1;
-    int jf = lane < 4 ? first + 16 * sub_l : 0x40000000;   // the next copy's first key
+    int jf = lane < 2 * KSUB ? first + 16 * sub_l : 0x40000000;   // the next copy's first key
     int page_next = jf < k1 ? table[jf >> kv.page_log2] : -2;
     auto fetch = [&](int bk, int bv) {         // block bk of the keys, bv of the values; -1: none
-        const bool mine = lane < 4 && (which ? bv : bk) >= 0;
+        const bool mine = lane < 2 * KSUB && (which ? bv : bk) >= 0;
         const int j = jf, page = page_next;
         if (mine) {
             jf += STEP;
@@ -354,21 +363,23 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         if (mine && !want && page != -2) report(status, GDN_ERR_INDEX);
         const uint32_t ok = __ballot_sync(0xffffffffu, want);
         if (lane == 0 && bk >= 0) {
-            pg[bk & 3] = ok & 3u;
-            tc::mbar_expect_tx(bar_k + (bk & 1), __popc(ok & my_keys) * 16 * REC);
+            pg[bk & 3] = ok & all_parts;
+            tc::mbar_expect_tx(bar_k + (bk & 1), __popc(ok & my_parts) * A::PART);
         }
-        if (lane == 0 && bv >= 0) tc::mbar_expect_tx(bar_v + (bv & 1), __popc(ok & 12u) * 16 * REC);
+        if (lane == 0 && bv >= 0) tc::mbar_expect_tx(bar_v + (bv & 1), __popc((ok >> KSUB) & my_parts) * A::PART);
         __syncwarp();
-        if (want && (which || (my_keys >> sub_l) & 1u)) {
-            uint8_t *dst = (which ? ring_v + (bv & 1) * A::HALF : ring_k + (bk & 1) * A::HALF) + sub_l * 16 * REC;
-            bulk_load(dst, base + page * page_bytes + (j & slot_mask) * REC, 16 * REC,
+        if (want && copies) {
+            uint8_t *dst = which ? ring_v + (bv & 1) * A::VALUES + sub_l * A::PART
+                                 : ring_k + (bk & 1) * A::KEYS + (A::VS > 1 ? 0 : sub_l * A::PART);
+            bulk_load(dst, base + page * page_bytes + (j & slot_mask) * REC, A::PART,
                       which ? bar_v + (bv & 1) : bar_k + (bk & 1));
         }
     };
     if (lane == 0) {
-        for (int x = 0; x < 4; ++x) tc::mbar_init(bar_k + x, 1);
+        for (int x = 0; x < 4; ++x) tc::mbar_init(bar_k + x, x < 2 ? 1 : A::VS);
         tc::mbar_fence_init();
     }
+    if (A::VS > 1) __syncthreads();            // the values' barriers are everyone's
     __syncwarp();
     if (blocks > 0) fetch(0, 0);
     if (blocks > 1) fetch(1, -1);
@@ -455,11 +466,11 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     }
 
     // products of the block's keys with q, in units of 2^-24 of q's scale
-    constexpr int SUBS = 2 / A::VS;        // 16-key parts of a block that this warp scores
+    constexpr int SUBS = KSUB / A::VS;     // 16-key parts of a block that this warp scores
     auto scores = [&](const uint8_t *st, float (&S)[SUBS][NT][4]) {
 #pragma unroll
         for (int sub = 0; sub < SUBS; ++sub) {
-            const uint8_t *rec0 = st + (16 * (A::VS > 1 ? dh : sub) + r) * REC, *rec1 = rec0 + 8 * REC;
+            const uint8_t *rec0 = st + (16 * sub + r) * REC, *rec1 = rec0 + 8 * REC;
             // minima: k slots (2c, 2c+1) take group c against the pair (hi, lo)
             // (with two groups, lanes 2 and 3 repeat them against zeros)
             uint32_t am[4] = {0u, 0u, 0u, 0u};
@@ -507,11 +518,11 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     };
     // every key of the block is in the cache and seen by every row
     auto is_full = [&](int b) {
-        return pg[b & 3] == 3u && first + b * STEP + kAttnBlock <= min(k1, see_first);
+        return pg[b & 3] == all_parts && first + b * STEP + A::BLOCK <= min(k1, see_first);
     };
-    uint32_t P[2][NT][2];      // the last block's weights, as the second operand's fragments
+    uint32_t P[SUBS][NT][2];   // this warp's weights of the last block, as fragments of the second operand
     // The block's maxima, before scaling: columns 2c, 2c+1 of each tile; keys r, r+8 of each
-    // part of block b.  A warp of two leaves its own for the other.
+    // part of block b.  Warps that share a slice leave theirs for one another.
     float *smax = reinterpret_cast<float *>(swap + kAttnWarps * NT * 256);
     int *sok = reinterpret_cast<int *>(smax + kAttnWarps * A::ROWS);
     uint2 *sp = reinterpret_cast<uint2 *>(swap);
@@ -546,14 +557,14 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                 reinterpret_cast<float2 *>(smax + warp * A::ROWS + 8 * nt)[c] = make_float2(bm[nt][0], bm[nt][1]);
         }
     };
-    // The two warps of a slice at one point (they take the same number of steps); false where
-    // either has given up on a copy.
-    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + slice) : "memory"); };
+    // The warps of a slice at one point (they take the same steps); false where one of them has
+    // given up on a copy.
+    auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kAttnThreads) : "memory"); };
     auto agree = [&](bool ok) {
         if (A::VS > 1) {
             if (lane == 0) sok[warp] = ok;
-            pair_sync();
-            ok = ok && sok[warp ^ 1];
+            meet();
+            ok = sok[0] && sok[1] && sok[2] && sok[3];
         }
         return ok;
     };
@@ -564,9 +575,12 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         for (int nt = 0; nt < NT; ++nt) {
             bool move[2];
             if (A::VS > 1) {
-                const float2 x = reinterpret_cast<const float2 *>(smax + (warp ^ 1) * A::ROWS + 8 * nt)[c];
-                bm[nt][0] = fmaxf(bm[nt][0], x.x);
-                bm[nt][1] = fmaxf(bm[nt][1], x.y);
+#pragma unroll
+                for (int w = 1; w < A::VS; ++w) {
+                    const float2 x = reinterpret_cast<const float2 *>(smax + (warp ^ w) * A::ROWS + 8 * nt)[c];
+                    bm[nt][0] = fmaxf(bm[nt][0], x.x);
+                    bm[nt][1] = fmaxf(bm[nt][1], x.y);
+                }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -604,21 +618,23 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                 if (A::VS > 1) sp[(warp * NT + nt) * 32 + lane] = make_uint2(P[0][nt][0], P[0][nt][1]);
             }
         }
-        if (A::VS > 1) {
-            pair_sync();
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {      // both parts, in order for both warps
-                const uint2 x = sp[((warp & ~1) * NT + nt) * 32 + lane], y = sp[((warp | 1) * NT + nt) * 32 + lane];
-                P[0][nt][0] = x.x; P[0][nt][1] = x.y;
-                P[1][nt][0] = y.x; P[1][nt][1] = y.y;
-            }
-        }
+        if (A::VS > 1) meet();
     };
     // O += V^T P over the block's values: k slots 2c, 2c+1, 2c+8, 2c+9 are the keys of the
     // same number
     auto values = [&](const uint8_t *st) {
 #pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
+        for (int sub = 0; sub < KSUB; ++sub) {
+            uint32_t Pv[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                if (A::VS > 1) {
+                    const uint2 x = sp[(sub * NT + nt) * 32 + lane];
+                    Pv[nt][0] = x.x; Pv[nt][1] = x.y;
+                } else {
+                    Pv[nt][0] = P[sub % SUBS][nt][0]; Pv[nt][1] = P[sub % SUBS][nt][1];
+                }
+            }
             const uint8_t *v0 = st + (16 * sub + 2 * c) * REC;
             const uint8_t *vk[4] = {v0, v0 + REC, v0 + 8 * REC, v0 + 9 * REC};
             uint32_t pr[4][NGV], mr[4];
@@ -629,7 +645,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
             }
             const uint32_t a0 = __byte_perm(mr[0], mr[1], 0x7632), a2 = __byte_perm(mr[2], mr[3], 0x7632);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(Om[nt], a0, 0u, a2, 0u, P[sub][nt][0], P[sub][nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma16816(Om[nt], a0, 0u, a2, 0u, Pv[nt][0], Pv[nt][1]);
 #pragma unroll
             for (int p = 0; p < NPV; ++p) {
                 uint32_t w[4];
@@ -645,10 +661,10 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                     const uint32_t sc2 = __byte_perm(pr[2][g], pr[3][g], 0x5410);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const uint32_t b0 = mul_half2(P[sub][nt][0], sc1);
-                        const uint32_t b1 = mul_half2(P[sub][nt][1], sc2);
-                        const uint32_t e0 = mul_rest(P[sub][nt][0], sc1, b0);
-                        const uint32_t e1 = mul_rest(P[sub][nt][1], sc2, b1);
+                        const uint32_t b0 = mul_half2(Pv[nt][0], sc1);
+                        const uint32_t b1 = mul_half2(Pv[nt][1], sc2);
+                        const uint32_t e0 = mul_rest(Pv[nt][0], sc1, b0);
+                        const uint32_t e1 = mul_rest(Pv[nt][1], sc2, b1);
                         mma16816(O[nt][2 * g], x1 & kNib0, x1 & kNib1, x2 & kNib0, x2 & kNib1, b0, b1);
                         mma16816(O[nt][2 * g + 1], y1 & kNib0, y1 & kNib1, y2 & kNib0, y2 & kNib1, b0, b1);
                         mma16816(O[nt][2 * g], x1 & kNib0, x1 & kNib1, x2 & kNib0, x2 & kNib1, e0, e1);
@@ -662,11 +678,11 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     // are taken as zero; so are non-finite pairs, whose group becomes NaN in just the rows
     // that see the key (through a zero weight it would reach the others too).
     auto clean = [&](int b, uint8_t *st) {
-        const int j = first + b * STEP + lane;
-        const bool in = j < k1 && ((pg[b & 3] >> (lane >> 4)) & 1u);
-        uint32_t *par = reinterpret_cast<uint32_t *>(st + lane * REC + R::CODES);
+        const int at = A::VS > 1 ? 16 * dh + (lane & 15) : lane, j = first + b * STEP + at;
+        const bool in = j < k1 && ((pg[b & 3] >> (at >> 4)) & 1u);
+        uint32_t *par = reinterpret_cast<uint32_t *>(st + at * REC + R::CODES);
 #pragma unroll 1
-        for (int g = 0; g < NG; ++g) {
+        for (int g = 0; g < NG && (A::VS == 1 || lane < 16); ++g) {
             const bool bad = in && half_pair_nonfinite(par[g]);
             if (bad)
                 for (int y = 0; y < A::ROWS && row0 + y < rows; ++y)
@@ -692,13 +708,16 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     for (; b < blocks && ok; ++b) {
         const bool more = b + 1 < blocks;
         if (more) fetch(b + 2 < blocks ? b + 2 : -1, b + 1);
-        uint8_t *sv = ring_v + (b & 1) * A::HALF;
+        uint8_t *sv = ring_v + (b & 1) * A::VALUES;
         ok = __all_sync(0xffffffffu, wait_copy(bar_v + (b & 1), (b >> 1) & 1));
-        if (ok && !is_full(b)) clean(b, sv);
+        if (!is_full(b)) {
+            if (ok) clean(b, sv);
+            if (A::VS > 1) meet();               // each has cleaned its part (alike for all of them)
+        }
         if (ok && more) ok = __all_sync(0xffffffffu, wait_copy(bar_k + ((b + 1) & 1), ((b + 1) >> 1) & 1));
         float S[SUBS][NT][4], bm[NT][2];
         if (ok) {
-            if (more) scores(ring_k + ((b + 1) & 1) * A::HALF, S);
+            if (more) scores(ring_k + ((b + 1) & 1) * A::KEYS, S);
             if (more && A::VS > 1) maxima(b + 1, S, bm);
             values(sv);
             if (more && A::VS == 1) maxima(b + 1, S, bm);
@@ -909,15 +928,16 @@ int attn_nt(int64_t rows, int D) {
 }
 
 // The most splits that a context of at most max_len keys with m new rows can have: by the
-// least length of a split, and by what has room.
+// least length of a split, and by what has room.  It does not grow with m.
 int attn_max_splits(int max_len, int m, int G, int Hkv, int D) {
     const int s = gdn::kv_split_base(max_len), most = max_len <= 512 ? 1 : max_len <= 2048 ? 4 : 8;
-    return std::min(std::max(most, max_len / s + (max_len % s != 0)), gdn::kv_split_room(std::max(m, 1), G, Hkv, D));
+    return std::min(std::max(most, max_len / s + (max_len % s != 0)),
+                    gdn::kv_split_room(std::max(m, 1), G, Hkv, D, gdn::split_ctas(9, D)));
 }
 
 // Partial results of one sequence, in rows: Hq m rows of S(m) splits.  S(m) is at most the
-// 304 CTAs over Hkv times the tiles of at most 32 of the G m rows, so Hq m S(m) <= 32 * 304
-// where anything is split.
+// CTAs at once (456) over Hkv times the tiles of at most 32 of the G m rows, so Hq m S(m) <=
+// 32 * 456 where anything is split.
 int64_t attn_slab(int Hq, int Hkv, int64_t T, int N, int max_q_len, int max_len, int D) {
     const int G = Hq / Hkv, one = attn_max_splits(max_len, 1, G, Hkv, D);
     if (one <= 1) return 0;
@@ -926,7 +946,7 @@ int64_t attn_slab(int Hq, int Hkv, int64_t T, int N, int max_q_len, int max_len,
         return s > 1 ? T * Hq * s : 0;
     }
     const int64_t m = std::min(max_q_len, gdn::kSplitMaxRows);
-    return std::min<int64_t>(Hq * m * one, 32 * gdn::kSplitCtas);
+    return std::min<int64_t>(Hq * m * one, 32 * gdn::kSplitMaxCtas);
 }
 
 size_t part_ml_bytes(int64_t rows) { return ((size_t)rows * 8 + 255) / 256 * 256; }
@@ -944,7 +964,7 @@ gdn_status_t mma_launch(const KvArgs &a, int row_tiles, int splits, int tc_rows,
         if (dev <= 63) ready.fetch_or(1ull << dev);
     }
     const int64_t slab = attn_slab(a.Hq, a.kv.Hkv, a.T, a.kv.N, a.max_q_len, a.max_kv_len, D);
-    const int room = gdn::kv_split_room(1, a.Hq / a.kv.Hkv, a.kv.Hkv, D);
+    const int room = gdn::kv_split_room(1, a.Hq / a.kv.Hkv, a.kv.Hkv, D, gdn::split_ctas(a.Hq / a.kv.Hkv, D));
     float2 *ml = (float2 *)a.ws;
     float *po = slab ? (float *)((uint8_t *)a.ws + part_ml_bytes(slab * a.kv.N)) : nullptr;
     kern<<<dim3((unsigned)((int64_t)splits * row_tiles), a.kv.Hkv, a.kv.N), gdn::kAttnThreads, A::SMEM, st>>>(
