@@ -136,7 +136,7 @@ kv_attention_simt_kernel(KvView kv, const T *__restrict__ q, T *__restrict__ o, 
 // bf16 activations.  The rows of one kv-head (G query heads x m tokens, token-major) are
 // cut into tiles of 8 NT; one CTA takes one row tile and one split of the keys, its four
 // warps taking every fourth block of 32 keys with a softmax state of their own, joined at
-// the end.  All products run as m16n8k16 on fp16 with keys (then elements) as the 16 rows
+// the end (wide rows: blocks of 64 keys between the four of them, below).  All products run as m16n8k16 on fp16 with keys (then elements) as the 16 rows
 // and query rows as the 8 columns, so that few rows waste little of an instruction and
 // each stored code is unpacked once per warp however many rows use it:
 //     S^T = K Q^T      O^T = V^T P^T
@@ -158,19 +158,21 @@ kv_attention_simt_kernel(KvView kv, const T *__restrict__ q, T *__restrict__ o, 
 // carry a row.  Scores, sums, maxima and outputs are fp32.
 //
 // Keys come in blocks of 16 records of a page (pages hold a multiple of 16) by bulk copies
-// into a ring that each warp runs for itself: no barrier of the CTA inside the loop.
+// into a ring that each warp runs for itself: no barrier of the CTA inside the loop, but
+// where warps share the blocks.
 //
 // 64 sequences of up to 16384 keys, 32 query heads over 8 of 128, take 174 us: 640 MB, 54% of
 // the HBM rate, bound by issue (59%): a block of 32 keys costs a warp 880 instructions, start
-// and join of eight such blocks included.  24 rows of 256 elements over 131072 keys of 4 heads take 107 us,
-// 23% of the HBM rate, bound by latency at eight warps an SM.
+// and join of eight such blocks included.  24 rows of 256 elements over 131072 keys of 4 heads
+// take 98 us, 25% of the HBM rate, bound by latency at twelve warps an SM.
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 
 // NT tiles of eight rows; VS: warps that share a slice of the keys (four where the output
 // accumulators, D NT / 4 registers a thread, would not fit otherwise).  Each of the four takes
 // the scores of a quarter of a block's keys and, with the others' weights, a quarter of the
-// values' elements.
+// values' elements (24 rows of 256 over 131072 keys 98 us, with two warps a slice 107; 16
+// sequences of 4096 to 8192 keys 87 and 124).
 template <int D, int NT> struct AttnShape {
     using R = KvRec<D>;
     static constexpr int ROWS = 8 * NT;
@@ -198,22 +200,23 @@ template <int D, int NT> struct AttnShape {
 // Keys per split of a context of len keys.  A warp's start and join cost about as much as 40
 // keys, so long splits serve a full device and short ones a lone sequence: 128 keys up to
 // 512, 256 up to 2048, 1024 above (8 kv-heads of 128, 64 sequences of 4096 to 8192 keys: 140
-// us with 1024, 161 with 512, 206 with 256; one sequence of 8192: 21, 16.5 and 14.5); and so
-// long that one sequence's CTAs, row tiles times kv-heads times splits, all fit on the device
-// at once (one sequence of 131072, 4 kv-heads, 24 rows of 256 elements: 116 us with 1728, 131
-// with 2048, 144 with 1024, 204 with 3456).  From 256 new rows on nothing is split.  All of
-// it depends on the sequence's own lengths and heads only.
+// us with 1024, 161 with 512, 206 with 256; one sequence of 8192: 21, 16.5 and 14.5), 512
+// where four warps share them (24 rows of 256 elements over 4 kv-heads: 64 sequences 326 us
+// with 512, 297 with 1024; one 37 and 55); and so long that one sequence's CTAs, row tiles
+// times kv-heads times splits, all fit on the device at once (131072 keys, two CTAs an SM
+// then: 116 us with 1728, 131 with 2048, 144 with 1024, 204 with 3456).  From 256 new rows on
+// nothing is split.  All of it depends on the sequence's own lengths and heads only.
 constexpr int kSplitMaxRows = 256;
 // CTAs on the device at once that splits are made for (tiles of 256 elements: two an SM for
 // eight rows, three for more), and the most of them.
 __host__ __device__ __forceinline__ int split_ctas(int rows, int D) { return (D == 256 && rows > 8 ? 3 : 2) * 152; }
 constexpr int kSplitMaxCtas = 3 * 152;
 // Most tiles of eight rows a CTA takes.  What more would save in reading and unpacking keys is
-// lost again where two warps have to share the elements (D NT > 256): 16 sequences of 4096 to
-// 8192 keys, 32 rows of 128, 131 us with two, 155 with four; but D = 256, 72 rows, 250 with
-// three, 303 with one.
+// lost again in registers: 16 sequences of 4096 to 8192 keys, 32 rows of 128 elements, 131 us
+// with two tiles, 155 with four; 72 rows of 256, 223 us with three, 303 with one, and from 96
+// rows on four lose a little to three.
 __host__ __device__ constexpr int attn_max_nt(int D) { return D == 256 ? 3 : D == 128 ? 2 : 4; }
-__host__ __device__ __forceinline__ int kv_split_base(int len) { return len <= 512 ? 128 : len <= 2048 ? 256 : 1024; }
+__host__ __device__ __forceinline__ int kv_split_base(int len, bool shared) { return len <= 512 ? 128 : len <= 2048 ? 256 : shared ? 512 : 1024; }
 // Splits that one sequence of m new rows has room for among `fit` CTAs.
 __host__ __device__ __forceinline__ int kv_split_room(int m, int G, int Hkv, int D, int fit) {
     const int rows = 8 * attn_max_nt(D);
@@ -222,7 +225,7 @@ __host__ __device__ __forceinline__ int kv_split_room(int m, int G, int Hkv, int
 }
 // (room for single tokens comes with the launch: a division less on the way to the first load)
 __device__ __forceinline__ int kv_split_len(int len, int m, int G, int Hkv, int D, int room_one) {
-    const int room = m == 1 ? room_one : kv_split_room(m, G, Hkv, D, split_ctas(G * m, D)), base = kv_split_base(len);
+    const int room = m == 1 ? room_one : kv_split_room(m, G, Hkv, D, split_ctas(G * m, D)), base = kv_split_base(len, D == 256 && G * m > 8);
     if (room <= 1) return 0x40000000;
     if ((int64_t)room * base >= len) return base;
     return ((len + room - 1) / room + 63) / 64 * 64;
@@ -930,7 +933,7 @@ int attn_nt(int64_t rows, int D) {
 // The most splits that a context of at most max_len keys with m new rows can have: by the
 // least length of a split, and by what has room.  It does not grow with m.
 int attn_max_splits(int max_len, int m, int G, int Hkv, int D) {
-    const int s = gdn::kv_split_base(max_len), most = max_len <= 512 ? 1 : max_len <= 2048 ? 4 : 8;
+    const int s = gdn::kv_split_base(max_len, D == 256), most = max_len <= 512 ? 1 : max_len <= 2048 ? 4 : 8;
     return std::min(std::max(most, max_len / s + (max_len % s != 0)),
                     gdn::kv_split_room(std::max(m, 1), G, Hkv, D, gdn::split_ctas(9, D)));
 }
