@@ -161,10 +161,10 @@ kv_attention_simt_kernel(KvView kv, const T *__restrict__ q, T *__restrict__ o, 
 // into a ring that each warp runs for itself: no barrier of the CTA inside the loop, but
 // where warps share the blocks.
 //
-// 64 sequences of up to 16384 keys, 32 query heads over 8 of 128, take 174 us: 640 MB, 54% of
+// 64 sequences of up to 16384 keys, 32 query heads over 8 of 128, take 179 us: 640 MB, 53% of
 // the HBM rate, bound by issue (59%): a block of 32 keys costs a warp 880 instructions, start
 // and join of eight such blocks included.  24 rows of 256 elements over 131072 keys of 4 heads
-// take 98 us, 25% of the HBM rate, bound by latency at twelve warps an SM.
+// take 101 us, 24% of the HBM rate, bound by latency at twelve warps an SM.
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 
@@ -172,7 +172,7 @@ constexpr int kAttnThreads = 32 * kAttnWarps;
 // accumulators, D NT / 4 registers a thread, would not fit otherwise).  Each of the four takes
 // the scores of a quarter of a block's keys and, with the others' weights, a quarter of the
 // values' elements (24 rows of 256 over 131072 keys 98 us, with two warps a slice 107; 16
-// sequences of 4096 to 8192 keys 87 and 124).
+// sequences of 4096 to 8192 keys 87 and 124; before the centring below).
 template <int D, int NT> struct AttnShape {
     using R = KvRec<D>;
     static constexpr int ROWS = 8 * NT;
@@ -451,7 +451,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     __syncthreads();
 
     constexpr int NGV = NG / A::VS, NPV = NP / A::VS;      // this warp's groups, words of the values
-    float O[NT][2 * NGV][4], Om[NT][4], mrun[NT][2], lrun[NT][2], fac[NT][2];
+    float O[NT][2 * NGV][4], Om[NT][4], off[NT][2], mrun[NT][2], lrun[NT][2], fac[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -462,6 +462,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         for (int e = 0; e < 4; ++e) Om[nt][e] = 0.f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+            off[nt][e] = 0.f;
             mrun[nt][e] = -INFINITY;
             lrun[nt][e] = 0.f;
             fac[nt][e] = sfac[8 * nt + 2 * c + e];
@@ -602,8 +603,10 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                 for (int x = 0; x < 2 * NGV; ++x)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) O[nt][x][e] *= keep[e & 1];
-                Om[nt][0] *= keep[0];
-                Om[nt][1] *= keep[1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) Om[nt][e] *= keep[e & 1];
+                off[nt][0] *= keep[0];
+                off[nt][1] *= keep[1];
             }
             float msub[2];
 #pragma unroll
@@ -646,9 +649,11 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                 load_words<NGV>(vk[x] + R::CODES + 4 * NGV * dh, pr[x]);
                 mr[x] = reinterpret_cast<const uint32_t *>(vk[x] + R::CODES)[r % NG];   // rows past NG are not read
             }
+            // rows 0..7: sums of p times the groups' minima, 8..15: times their scales
             const uint32_t a0 = __byte_perm(mr[0], mr[1], 0x7632), a2 = __byte_perm(mr[2], mr[3], 0x7632);
+            const uint32_t a1 = __byte_perm(mr[0], mr[1], 0x5410), a3 = __byte_perm(mr[2], mr[3], 0x5410);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(Om[nt], a0, 0u, a2, 0u, Pv[nt][0], Pv[nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma16816(Om[nt], a0, a1, a2, a3, Pv[nt][0], Pv[nt][1]);
 #pragma unroll
             for (int p = 0; p < NPV; ++p) {
                 uint32_t w[4];
@@ -677,6 +682,36 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
             }
         }
     };
+    // Codes are sums of positive numbers, which the minima take back at the end, and the matrix
+    // instructions cut their sums off towards zero: over a long run of keys the error would
+    // grow with its length (1152 keys: outputs 0.23% off, as much as their own rounding).  So
+    // every 256 keys the mean code, 7.5 times the scales, is moved from the sums to `off`, in
+    // fp32 rounded to nearest, together with the minima that nearly cancel it (98 -> 101 us on
+    // those keys, 175 -> 179 for the 64 sequences).
+    auto center = [&]() {
+        const float mean = 7.5f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int g = 0; g < NGV; ++g) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float b = mean * __shfl_sync(0xffffffffu, Om[nt][2 + e], 4 * (NGV * dh + g) + c);
+#pragma unroll
+                    for (int y = 2 * g; y < 2 * g + 2; ++y) {
+                        O[nt][y][e] = fmaf(-0x1p-24f, b, O[nt][y][e]);
+                        O[nt][y][2 + e] = fmaf(-0x1p-20f, b, O[nt][y][2 + e]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                off[nt][e] += fmaf(mean, Om[nt][2 + e], Om[nt][e]);
+                Om[nt][e] = Om[nt][2 + e] = 0.f;
+            }
+        }
+    };
+    constexpr int EVERY = 256 / A::BLOCK;
     // Values of a block that some row does not see in full: records no row of this tile sees
     // are taken as zero; so are non-finite pairs, whose group becomes NaN in just the rows
     // that see the key (through a zero weight it would reach the others too).
@@ -723,6 +758,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
             if (more) scores(ring_k + ((b + 1) & 1) * A::KEYS, S);
             if (more && A::VS > 1) maxima(b + 1, S, bm);
             values(sv);
+            if (more && (b & (EVERY - 1)) == EVERY - 1) center();
             if (more && A::VS == 1) maxima(b + 1, S, bm);
             __syncwarp();          // the tiles read here are free for the next fetch
         }
@@ -736,6 +772,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         for (int x = b; x < blocks && x < b + 2; ++x) wait_copy(bar_v + (x & 1), (x >> 1) & 1);
     }
 
+    center();
     // ---- join the warps: maxima and sums, then outputs through shared memory
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -763,8 +800,8 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
 #pragma unroll
         for (int g = 0; g < NGV; ++g) {
             const int gd = NGV * dh + g;
-            const float m0 = __shfl_sync(0xffffffffu, Om[nt][0], 4 * gd + c);
-            const float m1 = __shfl_sync(0xffffffffu, Om[nt][1], 4 * gd + c);
+            const float m0 = __shfl_sync(0xffffffffu, off[nt][0], 4 * gd + c);
+            const float m1 = __shfl_sync(0xffffffffu, off[nt][1], 4 * gd + c);
             const float up = 16777216.f, up16 = 1048576.f;   // 2^24; 2^20 where u came as u << 4
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
