@@ -11,6 +11,8 @@
 // (15 bits) goes in as an fp16 pair hi + lo, the minima as sixteen more columns against the
 // sums of q over each group (again a pair), so a 128-deep product becomes 272 deep:
 //     q.k = q.(hi + lo) + sum_g (sum of q over g) min_g.
+// Where a scale of 16 keys would carry 15 * scale past fp16, that block's scales and minima go
+// in at a quarter, and its scores take the factor of four in fp32.
 //
 // Warps 0-7: softmax, a thread owning one row of a tile; warps 8-15: unpacking, a warp
 // taking 16 records of keys, then of values, straight from the cache into registers while
@@ -43,6 +45,7 @@ constexpr int kTcRows = 256;
 constexpr int kTcSoftWarps = 8, kTcUnpackWarps = 8;
 constexpr int kTcThreads = 32 * (kTcSoftWarps + kTcUnpackWarps + 1);
 constexpr float kTcSlack = 8.f;     // how far (log2) the maximum may pass the reference
+constexpr uint32_t kTcTopScale = 0x6c43u;   // fp16 4364: 15 times the next one rounds to infinity
 constexpr float kTcLift = 7.f;      // weights are kept at 2^7 times their value (below 2^15)
 
 template <int D> struct TcShape {
@@ -62,7 +65,8 @@ template <int D> struct TcSmem {
     // group sums of q and minima of the keys: [128][16] fp16 in 8 x 8 blocks of 128 bytes
     uint8_t qx[2][4096], kx[4096];
     uint32_t nan_groups[kTcRows];    // groups of the row's output that a NaN value reached
-    uint8_t have[2][8];              // per 16 keys of a tile (even, odd): records present
+    uint8_t have[2][8];              // per 16 keys of a tile (even, odd): 1 records present,
+                                     // 3 and their scores come at a quarter
     uint32_t tmem;
     int abort;
     TcBars bar;
@@ -257,19 +261,21 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
             if (!(ok = tc_wait(&S.bar.s_full[rt], t & 1, abort))) break;
             tc::fence_after_sync();
             const uint2 have = *reinterpret_cast<const uint2 *>(S.have[t & 1]);
-            if (128 * (t + 1) > see_first || (have.x & have.y) != 0x01010101u) {
+            if (128 * (t + 1) > see_first || have.x != 0x01010101u || have.y != 0x01010101u) {
                 // keys this row may not use get a score of -inf: those past the ones it sees,
-                // and blocks whose records are not there
+                // and blocks whose records are not there; blocks at a quarter are put right
                 const int cnt = min(see, see_last) - 128 * t;
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
-                    const int stay = (((c < 4 ? have.x : have.y) >> (8 * (c & 3))) & 1u) ? cnt - 16 * c : 0;
+                    const uint32_t hv = (c < 4 ? have.x : have.y) >> (8 * (c & 3));
+                    const int stay = (hv & 1u) ? cnt - 16 * c : 0;
+                    const float f = (hv & 2u) ? 4.f : 1.f;
                     float v[16];
                     tc::tmem_ld16(tS + 16 * c, v);
                     tc::tmem_wait_ld();
                     uint32_t u[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) u[j] = j < stay ? __float_as_uint(v[j]) : 0xff800000u;
+                    for (int j = 0; j < 16; ++j) u[j] = j < stay ? __float_as_uint(f * v[j]) : 0xff800000u;
                     tc_st16(tS + 16 * c, u);
                 }
                 tc::tmem_wait_st();
@@ -421,6 +427,17 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
             const int s = t & 1;
             const int page_next = lookup(t + 1);
             if (t >= 1 && !tc_wait<100>(&S.bar.k_free, (t - 1) & 1, abort)) break;
+            uint32_t top_scale = 0;          // as fp16 bits, which order like the numbers
+#pragma unroll
+            for (int g = 0; g < NG; ++g) top_scale = max(top_scale, max(par[0][0][g] & 0x7fffu, par[0][1][g] & 0x7fffu));
+            const bool quarter = __any_sync(0xffffffffu, top_scale > kTcTopScale);
+            if (quarter) {
+                const __half2 q4 = __floats2half2_rn(0.25f, 0.25f);
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) par[0][y][g] = h2_bits(__hmul2(bits_h2(par[0][y][g]), q4));
+            }
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 // word x NG + g is elements 32 g + 8 x ..: 16-byte chunk 4 g + x
@@ -447,7 +464,7 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
                     *reinterpret_cast<uint4 *>(S.kx + at_x(key, x)) = v;
                 }
             }
-            if (lane == 0) S.have[s][w] = page >= 0 && page < kv.pages ? 1 : 0;
+            if (lane == 0) S.have[s][w] = page >= 0 && page < kv.pages ? (quarter ? 3 : 1) : 0;
             if (t + 1 < steps) fetch(t + 1, 0, page_next);
             tc::fence_async_smem();
             __syncwarp();

@@ -1,0 +1,66 @@
+"""Attention over the 4-bit cache across the format's range: groups of large and of small scale,
+rows that one key dominates, and bad entries of the block table.  Bounds as in
+test_gpu_kv_cache.py: q or the values are scaled by powers of two, which changes no rounding.
+"""
+import numpy as np
+import pytest
+import torch
+
+import linear_ref as ref
+from gpu_util import assert_bits_equal, np64
+from test_gpu_kv_cache import attention_case, check_attention, offsets, run_attention
+
+pytestmark = pytest.mark.gpu
+
+gdn = pytest.importorskip("gated_deltanet_linear_11_gb300")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    gdn.load()
+
+
+def scale_records(c, which, f, every=1):
+    """Scales and minima of every `every`-th slot of the keys (0) or values (1) times f, within
+    the format's range."""
+    D = c["D"]
+    par = c["cache"][:, which, :, ::every, D // 2:]
+    with np.errstate(invalid="ignore"):    # NaN past the sequences' ends
+        x = np.ascontiguousarray(par).view(np.float16).astype(np.float32) * np.float32(f)
+        x = np.clip(x, -65504, 65504).astype(np.float16)
+    c["cache"][:, which, :, ::every, D // 2:] = x.view(np.uint8)
+    return c
+
+
+# a few rows (split and whole), and pieces of prompts with many
+ROWS = [([1, 3], [700, 40]), ([40, 1], [300, 700]), ([200, 161], [400, 170])]
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 32, 8), (128, 32, 8), (256, 8, 2)])
+@pytest.mark.parametrize("ms,lens", ROWS)
+@pytest.mark.parametrize("every", [1, 5, 16])
+def test_attention_keys_of_large_scale(D, Hq, Hkv, ms, lens, every):
+    """Key groups with scales up to 6550 (codes times scales past the fp16 range), alone and
+    among others, against queries as much smaller."""
+    c = attention_case(41, D, Hq, Hkv, 16, ms, lens)
+    scale_records(c, 0, 2.0 ** 14, every)
+    c["q"] *= 2.0 ** -14
+    check_attention(c, *run_attention(c))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 32, 8), (128, 32, 8), (256, 8, 2)])
+@pytest.mark.parametrize("ms,lens", ROWS)
+@pytest.mark.parametrize("simt", [False, True])
+def test_attention_over_clamped_keys(D, Hq, Hkv, ms, lens, simt):
+    """Keys as append stores them, with infinities and values past fp16 clamped to +-65504."""
+    c = attention_case(42, D, Hq, Hkv, 16, ms, lens)
+    rng = np.random.default_rng(43)
+    k = rng.standard_normal(c["cache"][:, 0].shape[:-1] + (D,)).astype(np.float32)
+    k[:, :, ::7, 5] = np.inf
+    k[:, :, ::11, 40] = -np.inf
+    k[:, :, 3, 32:64] *= np.float32(1e6)
+    c["cache"][:, 0] = ref.records(k, ref.key_order(D))
+    c["q"] *= 2.0 ** -15
+    check_attention(c, *run_attention(c, simt=simt))
