@@ -426,11 +426,16 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
         for (int t = 0; t < steps; ++t) {
             const int s = t & 1;
             const int page_next = lookup(t + 1);
-            if (t >= 1 && !tc_wait<100>(&S.bar.k_free, (t - 1) & 1, abort)) break;
-            uint32_t top_scale = 0;          // as fp16 bits, which order like the numbers
+            uint32_t any = 0u;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) top_scale = max(top_scale, max(par[0][0][g] & 0x7fffu, par[0][1][g] & 0x7fffu));
-            const bool quarter = __any_sync(0xffffffffu, top_scale > kTcTopScale);
+            for (int g = 0; g < NG; ++g) any |= par[0][0][g] | par[0][1][g];
+            bool quarter = false;
+            if (__any_sync(0xffffffffu, any & 0x4000u)) {        // some scale of 2 or more
+                uint32_t most = 0u;          // as fp16 bits, which order like the numbers
+#pragma unroll
+                for (int g = 0; g < NG; ++g) most = max(most, max(par[0][0][g] & 0x7fffu, par[0][1][g] & 0x7fffu));
+                quarter = __any_sync(0xffffffffu, most > kTcTopScale);
+            }
             if (quarter) {
                 const __half2 q4 = __floats2half2_rn(0.25f, 0.25f);
 #pragma unroll
@@ -438,6 +443,7 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
 #pragma unroll
                     for (int g = 0; g < NG; ++g) par[0][y][g] = h2_bits(__hmul2(bits_h2(par[0][y][g]), q4));
             }
+            if (t >= 1 && !tc_wait<100>(&S.bar.k_free, (t - 1) & 1, abort)) break;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 // word x NG + g is elements 32 g + 8 x ..: 16-byte chunk 4 g + x
