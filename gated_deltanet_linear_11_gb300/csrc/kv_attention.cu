@@ -152,10 +152,14 @@ kv_attention_simt_kernel(KvView kv, const T *__restrict__ q, T *__restrict__ o, 
 // Fewer bits than fp32: q is scaled by a power of two per row so that its largest element
 // lies in [2^11, 2^12), where fp16 holds a bf16 exactly (down to 2^-26 of the largest);
 // p is rounded to fp16 (2^-11); it is taken against a reference within 2 (in powers of two)
-// of the running maximum, so p < 4 and p scale stays in the fp16 range.  p scale goes in as
-// an fp16 pair (product and what its rounding left out): scale * code and minimum cancel to
-// a value several times smaller than either, so one fp16 product would show where few keys
-// carry a row.  Scores, sums, maxima and outputs are fp32.
+// of the running maximum and lifted by 2^13, so it stays below 2^15 and a weight of 2^-37 of
+// the largest is still held.  p scale goes in as an fp16 pair (product and what its rounding
+// left out): scale * code and minimum cancel to a value several times smaller than either, so
+// one fp16 product would show where few keys carry a row.  Scales of 2 and more lower the lift,
+// down to 1 for the largest there are, so that the product stays in the fp16 range.  (Without
+// the lift, values of 2^-11 their usual size left outputs 30 times their bound off, and a key
+// that outweighs each of 12000 others by 2^18 four times.)  Scores, sums, maxima and outputs
+// are fp32.
 //
 // Keys come in blocks of 16 records of a page (pages hold a multiple of 16) by bulk copies
 // into a ring that each warp runs for itself: no barrier of the CTA inside the loop, but
@@ -291,6 +295,11 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[K]) {
 __device__ __forceinline__ bool half_pair_nonfinite(uint32_t w) {
     return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
 }
+
+// Weights are held at 2^lift times their size, below 2^15 with the reference's slack of 2.  With
+// a lift of 13 - k the scales may be up to 1.984 * 2^k.
+constexpr float kMmaLift = 13.f;
+constexpr uint32_t kTopScale = 0x3ff0u, kHalfExp = 0x0400u;     // fp16 bits
 
 constexpr uint32_t kNib0 = 0x000F000Fu, kNib1 = 0x00F000F0u;
 
@@ -561,6 +570,9 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                 reinterpret_cast<float2 *>(smax + warp * A::ROWS + 8 * nt)[c] = make_float2(bm[nt][0], bm[nt][1]);
         }
     };
+    float lift = kMmaLift;
+    uint32_t top_scale = kTopScale;
+    uint32_t fresh = 0u;         // not 0: what a change of lift asks of the block's shared weights
     // The warps of a slice at one point (they take the same steps); false where one of them has
     // given up on a copy.
     auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kAttnThreads) : "memory"); };
@@ -573,7 +585,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         return ok;
     };
     // Softmax step.  The reference moves only when a score passes it by 2 (powers of two), so
-    // p < 4.
+    // p < 4 before the lift.
     auto weigh = [&](float (&S)[SUBS][NT][4], float (&bm)[NT][2]) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -610,7 +622,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
             }
             float msub[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) msub[e] = mrun[nt][e] == -INFINITY ? 0.f : -mrun[nt][e];
+            for (int e = 0; e < 2; ++e) msub[e] = mrun[nt][e] == -INFINITY ? 0.f : lift - mrun[nt][e];
 #pragma unroll
             for (int sub = 0; sub < SUBS; ++sub) {
                 float p[4];
@@ -637,6 +649,10 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                 if (A::VS > 1) {
                     const uint2 x = sp[(sub * NT + nt) * 32 + lane];
                     Pv[nt][0] = x.x; Pv[nt][1] = x.y;
+                    if (fresh != 0u) {
+                        Pv[nt][0] = mul_half2(Pv[nt][0], fresh);
+                        Pv[nt][1] = mul_half2(Pv[nt][1], fresh);
+                    }
                 } else {
                     Pv[nt][0] = P[sub % SUBS][nt][0]; Pv[nt][1] = P[sub % SUBS][nt][1];
                 }
@@ -730,6 +746,48 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         __syncwarp();
     };
 
+    // Scales of a block's values (one key a lane, or two) that the lift leaves no room for: it
+    // is lowered, and with it the weights of the block and all sums so far.  Warps that share a
+    // slice see the same scales and keep the same lift.
+    auto fit_scales = [&](const uint8_t *st) {
+        __half2 m = __floats2half2_rn(0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < A::BLOCK / 32; ++x) {
+            uint32_t w[NG];
+            load_words<NG>(st + (lane + 32 * x) * REC + R::CODES, w);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) m = __hmax2(m, *reinterpret_cast<const __half2 *>(&w[g]));
+        }
+        const uint32_t h = __half_as_ushort(__low2half(m));
+        if (__any_sync(0xffffffffu, h > top_scale)) {
+            const uint32_t most = min(__reduce_max_sync(0xffffffffu, h), 0x7000u);     // 2^13 and more: k = 13
+            const uint32_t k = min((most >> 10) - 14u, 13u);
+            const float was = lift;
+            lift = kMmaLift - (float)k;
+            top_scale = k == 13u ? 0x7fffu : kTopScale + k * kHalfExp;
+            const float f = __int_as_float((127 + (int)(lift - was)) << 23);
+            fresh = pack_half2(f, f);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int x = 0; x < 2 * NGV; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) O[nt][x][e] *= f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) Om[nt][e] *= f;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    off[nt][e] *= f;
+                    lrun[nt][e] *= f;
+                }
+#pragma unroll
+                for (int x = 0; x < SUBS; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) P[x][nt][e] = mul_half2(P[x][nt][e], fresh);
+            }
+        }
+    };
+
     // The scores of block b + 1 come before the values of block b: independent products that
     // hide each other's latency.
     bool ok = true;
@@ -752,12 +810,14 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
             if (ok) clean(b, sv);
             if (A::VS > 1) meet();               // each has cleaned its part (alike for all of them)
         }
+        if (ok) fit_scales(sv);
         if (ok && more) ok = __all_sync(0xffffffffu, wait_copy(bar_k + ((b + 1) & 1), ((b + 1) >> 1) & 1));
         float S[SUBS][NT][4], bm[NT][2];
         if (ok) {
             if (more) scores(ring_k + ((b + 1) & 1) * A::KEYS, S);
             if (more && A::VS > 1) maxima(b + 1, S, bm);
             values(sv);
+            fresh = 0u;
             if (more && (b & (EVERY - 1)) == EVERY - 1) center();
             if (more && A::VS == 1) maxima(b + 1, S, bm);
             __syncwarp();          // the tiles read here are free for the next fetch
@@ -773,6 +833,10 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     }
 
     center();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) mrun[nt][e] -= lift;      // sums are in units of 2^mrun from here on
     // ---- join the warps: maxima and sums, then outputs through shared memory
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)

@@ -64,3 +64,35 @@ def test_attention_over_clamped_keys(D, Hq, Hkv, ms, lens, simt):
     c["cache"][:, 0] = ref.records(k, ref.key_order(D))
     c["q"] *= 2.0 ** -15
     check_attention(c, *run_attention(c, simt=simt))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 4, 4), (64, 8, 1), (128, 8, 2), (128, 12, 1), (256, 2, 2),
+                                      (256, 12, 1), (256, 24, 1)])
+@pytest.mark.parametrize("ms,lens", [([1, 2], [1500, 90]), ([260], [700])])
+@pytest.mark.parametrize("f", [2.0 ** -8, 2.0 ** -11, 2.0 ** 10, 2.0 ** 14])
+def test_attention_values_of_any_scale(D, Hq, Hkv, ms, lens, f):
+    c = attention_case(44, D, Hq, Hkv, 16, ms, lens)
+    check_attention(c, *run_attention(scale_records(c, 1, f)))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 8, 1), (128, 8, 2), (256, 8, 1), (256, 24, 1)])
+@pytest.mark.parametrize("big", ["late", "early", "rows"])
+def test_attention_values_of_mixed_scale(D, Hq, Hkv, big):
+    """Groups of very different scales: each is held to its own size."""
+    c = attention_case(45, D, Hq, Hkv, 16, [2, 1], [1500, 600])
+    with np.errstate(invalid="ignore"):    # NaN past the sequences' ends
+        par = c["cache"][:, 1, :, :, D // 2:].copy().view(np.float16).astype(np.float32)
+    par = par.reshape(par.shape[:-1] + (D // 32, 2))
+    f = np.ones(par.shape[:-1], np.float32)
+    if big == "rows":                      # groups of one record
+        f[..., 1] = 4096.0
+    else:                                  # blocks of a sequence
+        for n, L in enumerate(c["lens"]):
+            pages = c["table"][n, :-(-int(L) // 16)]
+            half = len(pages) // 2
+            for x, p in enumerate(pages[half:] if big == "late" else pages[:half]):
+                f[p] = 2.0 ** (4 + 2 * (x % 5))
+    par = np.clip(par * f[..., None], -65504, 65504).astype(np.float16)
+    c["cache"][:, 1, :, :, D // 2:] = np.ascontiguousarray(par).reshape(
+        par.shape[:-2] + (-1,)).view(np.uint8)
+    check_attention(c, *run_attention(c))
