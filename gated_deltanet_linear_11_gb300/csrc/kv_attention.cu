@@ -298,12 +298,13 @@ __device__ __forceinline__ bool half_pair_nonfinite(uint32_t w) {
 
 // Weights are held at 2^lift times their size, below 2^15 with the reference's slack of 2.  With
 // a lift of 13 - k the scales may be up to 1.984 * 2^k.
+constexpr int kStowKeys = 2048;
 constexpr float kMmaLift = 13.f;
 constexpr uint32_t kTopScale = 0x3ff0u, kHalfExp = 0x0400u;     // fp16 bits
 
 constexpr uint32_t kNib0 = 0x000F000Fu, kNib1 = 0x00F000F0u;
 
-template <int D, int NT>
+template <int D, int NT, bool LONG>
 __global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::CTAS)
 kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__ o,
                         float *__restrict__ lse, float *__restrict__ part_o,
@@ -570,6 +571,8 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                 reinterpret_cast<float2 *>(smax + warp * A::ROWS + 8 * nt)[c] = make_float2(bm[nt][0], bm[nt][1]);
         }
     };
+    volatile float held[LONG ? NT : 1][2 * NGV][4], held_at[LONG ? NT : 1][2];     // see stow(); local memory
+    bool stowed = false;
     float lift = kMmaLift;
     uint32_t top_scale = kTopScale;
     uint32_t fresh = 0u;         // not 0: what a change of lift asks of the block's shared weights
@@ -728,6 +731,36 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         }
     };
     constexpr int EVERY = 256 / A::BLOCK;
+    // What centring leaves is small where many keys carry a row, but not where one does: its code
+    // stays in the sums, and each smaller product that joins it is cut off (one key that weighs
+    // 2^21 times as much as each of 12000 others left outputs of 256 elements 1.2 times their
+    // bound off).  So every kStowKeys keys of a warp the sums move to fp32 words in local memory
+    // and start again from zero.  LONG is for calls whose runs can be that long, which splits
+    // are not: without it 64 sequences of up to 16384 keys take 184 us, with it 195.
+    auto stow = [&](bool again) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float f[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float at = held_at[LONG ? nt : 0][e], now = mrun[nt][e] - lift;
+                f[e] = stowed && at != -INFINITY ? exp2_approx(at - now) : 0.f;
+                held_at[LONG ? nt : 0][e] = now;
+            }
+#pragma unroll
+            for (int x = 0; x < 2 * NGV; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (stowed) O[nt][x][e] = fmaf(held[LONG ? nt : 0][x][e], f[e & 1], O[nt][x][e]);
+                    if (again) {
+                        held[LONG ? nt : 0][x][e] = O[nt][x][e];
+                        O[nt][x][e] = 0.f;
+                    }
+                }
+        }
+        stowed = true;
+    };
+    constexpr int STOW = kStowKeys / A::BLOCK;
     // Values of a block that some row does not see in full: records no row of this tile sees
     // are taken as zero; so are non-finite pairs, whose group becomes NaN in just the rows
     // that see the key (through a zero weight it would reach the others too).
@@ -819,6 +852,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
             values(sv);
             fresh = 0u;
             if (more && (b & (EVERY - 1)) == EVERY - 1) center();
+            if (LONG && more && (b & (STOW - 1)) == STOW - 1) stow(true);
             if (more && A::VS == 1) maxima(b + 1, S, bm);
             __syncwarp();          // the tiles read here are free for the next fetch
         }
@@ -833,6 +867,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     }
 
     center();
+    if (LONG && stowed) stow(false);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1039,6 +1074,13 @@ int attn_max_splits(int max_len, int m, int G, int Hkv, int D) {
                     gdn::kv_split_room(std::max(m, 1), G, Hkv, D, gdn::split_ctas(9, D)));
 }
 
+// The most keys in one piece for a sequence of m new rows.
+int attn_longest(int max_len, int m, int G, int Hkv, int D) {
+    const int room = gdn::kv_split_room(m, G, Hkv, D, gdn::split_ctas(G * m, D));
+    if (room <= 1) return max_len;
+    return std::max(gdn::kv_split_base(max_len, D == 256 && G * m > 8), (max_len + room - 1) / room + 63);
+}
+
 // Partial results of one sequence, in rows: Hq m rows of S(m) splits.  S(m) is at most the
 // CTAs at once (456) over Hkv times the tiles of at most 32 of the G m rows, so Hq m S(m) <=
 // 32 * 456 where anything is split.
@@ -1056,12 +1098,14 @@ int64_t attn_slab(int Hq, int Hkv, int64_t T, int N, int max_q_len, int max_len,
 size_t part_ml_bytes(int64_t rows) { return ((size_t)rows * 8 + 255) / 256 * 256; }
 
 template <int D, int NT>
-gdn_status_t mma_launch(const KvArgs &a, int row_tiles, int splits, int tc_rows, cudaStream_t st) {
+gdn_status_t mma_launch(const KvArgs &a, int row_tiles, int splits, int tc_rows, int longest, cudaStream_t st) {
     using A = gdn::AttnShape<D, NT>;
-    auto kern = gdn::kv_attention_mma_kernel<D, NT>;
-    static std::atomic<uint64_t> ready{0};   // one bit per device (beyond 63: set every time)
+    const bool is_long = longest > gdn::kStowKeys * A::SLICES;      // keys of one warp
+    auto kern = is_long ? gdn::kv_attention_mma_kernel<D, NT, true> : gdn::kv_attention_mma_kernel<D, NT, false>;
+    static std::atomic<uint64_t> readies[2];   // one bit per device (beyond 63: set every time)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+    std::atomic<uint64_t> &ready = readies[is_long];
     if (dev > 63 || !((ready.load() >> dev) & 1u)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, A::SMEM) != cudaSuccess)
             return GDN_ERR_CUDA;
@@ -1108,16 +1152,20 @@ gdn_status_t launch_kv_attention(const KvArgs &a, cudaStream_t st) {
     const int64_t tiles = (rows + 8 * nt - 1) / (8 * nt);
     const int splits = attn_max_splits(a.max_kv_len, a.min_q_len, a.Hq / a.kv.Hkv, a.kv.Hkv, a.D);
     if (tiles * splits > 0x7fffffff || a.kv.N > 65535) return GDN_ERR_SHAPE;
+    // (over all m between these two: room falls as m grows, but for the step in split_ctas)
+    const int G = a.Hq / a.kv.Hkv;
+    const int longest = std::max(attn_longest(a.max_kv_len, a.min_q_len, G, a.kv.Hkv, a.D),
+                                 attn_longest(a.max_kv_len, (int)m_most, G, a.kv.Hkv, a.D));
     switch (a.D * 10 + nt) {
-    case 641: return mma_launch<64, 1>(a, (int)tiles, splits, tc_rows, st);
-    case 642: return mma_launch<64, 2>(a, (int)tiles, splits, tc_rows, st);
-    case 643: return mma_launch<64, 3>(a, (int)tiles, splits, tc_rows, st);
-    case 644: return mma_launch<64, 4>(a, (int)tiles, splits, tc_rows, st);
-    case 1281: return mma_launch<128, 1>(a, (int)tiles, splits, tc_rows, st);
-    case 1282: return mma_launch<128, 2>(a, (int)tiles, splits, tc_rows, st);
-    case 2561: return mma_launch<256, 1>(a, (int)tiles, splits, tc_rows, st);
-    case 2562: return mma_launch<256, 2>(a, (int)tiles, splits, tc_rows, st);
-    case 2563: return mma_launch<256, 3>(a, (int)tiles, splits, tc_rows, st);
+    case 641: return mma_launch<64, 1>(a, (int)tiles, splits, tc_rows, longest, st);
+    case 642: return mma_launch<64, 2>(a, (int)tiles, splits, tc_rows, longest, st);
+    case 643: return mma_launch<64, 3>(a, (int)tiles, splits, tc_rows, longest, st);
+    case 644: return mma_launch<64, 4>(a, (int)tiles, splits, tc_rows, longest, st);
+    case 1281: return mma_launch<128, 1>(a, (int)tiles, splits, tc_rows, longest, st);
+    case 1282: return mma_launch<128, 2>(a, (int)tiles, splits, tc_rows, longest, st);
+    case 2561: return mma_launch<256, 1>(a, (int)tiles, splits, tc_rows, longest, st);
+    case 2562: return mma_launch<256, 2>(a, (int)tiles, splits, tc_rows, longest, st);
+    case 2563: return mma_launch<256, 3>(a, (int)tiles, splits, tc_rows, longest, st);
     }
     return GDN_ERR_UNSUPPORTED;
 }

@@ -96,3 +96,56 @@ def test_attention_values_of_mixed_scale(D, Hq, Hkv, big):
     c["cache"][:, 1, :, :, D // 2:] = np.ascontiguousarray(par).reshape(
         par.shape[:-2] + (-1,)).view(np.uint8)
     check_attention(c, *run_attention(c))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 2, 1), (128, 4, 1), (256, 2, 1), (256, 12, 1)])
+@pytest.mark.parametrize("ms,L", [([1], 30000), ([260], 12000)])
+@pytest.mark.parametrize("down", [13, 18, 21])
+def test_attention_one_key_dominates(D, Hq, Hkv, ms, L, down):
+    """Every other key weighs about 2^-down of the first; together they still count."""
+    c = dominated_case(D, Hq, Hkv, ms, L, down)
+    check_attention(c, *run_attention(c))
+
+
+def dominated_case(D, Hq, Hkv, ms, L, down):
+    c = attention_case(46, D, Hq, Hkv, 64, ms, [L])
+    scale_records(c, 0, 2.0 ** -4)         # the others' scores lie close together
+    scale_records(c, 1, 2.0 ** -3)
+    q = c["q"].float()
+    q[..., :32] = q[..., :32] * 0.1 + 1.0
+    c["q"] = q.to(torch.bfloat16)
+    at = c["cache"][c["table"][0, 0], 0, :, 0]
+    at[:, :D // 2] = 0
+    x = down * np.log(2.0) * D ** 0.5 / 32
+    pair = np.zeros((D // 32, 2), np.float16)
+    pair[0, 1] = x
+    at[:, D // 2:] = pair.reshape(-1).view(np.uint8)
+    # values that do not cancel over the keys
+    par = c["cache"][:, 1, :, :, D // 2:].copy().view(np.float16)
+    par[..., 1::2] = 0.25 * par[..., 0::2]
+    c["cache"][:, 1, :, :, D // 2:] = par.view(np.uint8)
+    return c
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("down", [13, 21])
+def test_attention_one_key_dominates_many_rows(D, down):
+    """The same for a piece of a prompt; its last rows are looked at."""
+    c = dominated_case(D, 32, 1, [170], 30000, down)
+    o, lse = run_attention(c)
+    end = dict(c, q=c["q"][-3:], ms=[3])
+    check_attention(end, o[-3:], lse[-3:])
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 8, 2), (128, 8, 2), (256, 8, 2)])
+def test_attention_long_runs_beside_splits(D, Hq, Hkv):
+    """Sequences beside one whose keys stay in a long run: the bits that they give beside one of
+    as many new tokens and a short run."""
+    ms, lens = [260, 1, 2], [9500, 1900, 700]
+    c = attention_case(48, D, Hq, Hkv, 32, ms, lens)
+    o, lse = run_attention(c)
+    check_attention(c, o, lse)
+    short = dict(c, lens=np.array([300, 1900, 700], np.int32))
+    o1, l1 = run_attention(short, max_kv_len=1900)
+    assert_bits_equal(o[260:], o1[260:], "o beside a long run")
+    assert_bits_equal(lse[260:], l1[260:], "lse beside a long run")
