@@ -364,16 +364,16 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     const uint8_t *base = kv.block(0, which, hkv, REC);
     const int slot_mask = (1 << kv.page_log2) - 1;
     int jf = lane < 2 * KSUB ? first + 16 * sub_l : 0x40000000;   // the next copy's first key
-    int page_next = jf < k1 ? table[jf >> kv.page_log2] : -2;
+    int page_next = jf < k1 ? table[jf >> kv.page_log2] : -1;
     auto fetch = [&](int bk, int bv) {         // block bk of the keys, bv of the values; -1: none
         const bool mine = lane < 2 * KSUB && (which ? bv : bk) >= 0;
         const int j = jf, page = page_next;
         if (mine) {
             jf += STEP;
-            page_next = jf < k1 ? table[jf >> kv.page_log2] : -2;
+            page_next = jf < k1 ? table[jf >> kv.page_log2] : -1;
         }
         const bool want = mine && page >= 0 && page < kv.pages;
-        if (mine && !want && page != -2) report(status, GDN_ERR_INDEX);
+        if (mine && !want && j < k1) report(status, GDN_ERR_INDEX);
         const uint32_t ok = __ballot_sync(0xffffffffu, want);
         if (lane == 0 && bk >= 0) {
             pg[bk & 3] = ok & all_parts;

@@ -391,14 +391,14 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
         uint32_t code[2][2][NW], par[2][2][NG];  // [keys / values][r, r + 8]
         auto lookup = [&](int t) {
             const int j = 128 * t + 16 * w;
-            return j < see_last ? table[j >> kv.page_log2] : -2;
+            return j < see_last ? table[j >> kv.page_log2] : -1;
         };
         // keys (u = 0) or values (1) of tile t; records that are not there, or past the last key
         // the tile's rows see, read as zeros
         auto fetch = [&](int t, int u, int pg) {
             const int j = 128 * t + 16 * w;
             const bool want = pg >= 0 && pg < kv.pages;
-            if (!want && pg != -2 && u == 0 && lane == 0) report(status, GDN_ERR_INDEX);
+            if (!want && j < see_last && u == 0 && lane == 0) report(status, GDN_ERR_INDEX);
             const uint8_t *rec = base + (int64_t)pg * page_bytes + (u ? to_v : 0) + ((j & slot_mask) + (u ? rv : rk)) * REC;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
@@ -417,7 +417,7 @@ kv_attention_tc_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__
                 }
             }
         };
-        int page = steps > 0 ? lookup(0) : -2;
+        int page = steps > 0 ? lookup(0) : -1;
         if (steps > 0) {
             fetch(0, 0, page);
             fetch(0, 1, page);

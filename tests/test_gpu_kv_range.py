@@ -149,3 +149,21 @@ def test_attention_long_runs_beside_splits(D, Hq, Hkv):
     o1, l1 = run_attention(short, max_kv_len=1900)
     assert_bits_equal(o[260:], o1[260:], "o beside a long run")
     assert_bits_equal(lse[260:], l1[260:], "lse beside a long run")
+
+
+@pytest.mark.parametrize("D,Hq,ms,simt", [(128, 8, [1], False), (256, 24, [2], False),
+                                          (128, 32, [170], False), (64, 32, [170], False),
+                                          (128, 8, [3], True)])
+@pytest.mark.parametrize("page", [-1, -2, -(1 << 31), 1 << 30])
+def test_attention_reports_every_bad_page(D, Hq, ms, simt, page):
+    """Any entry outside the cache within a sequence's length is left out and reported, the last
+    one too; entries past its length are not looked at."""
+    c = attention_case(47, D, Hq, 1, 16, ms, [ms[0] + 130])
+    last = (ms[0] + 129) // 16
+    for at in (2, last, last + 1):
+        bad = dict(c, table=c["table"].copy())
+        bad["table"][0, at] = page
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        o, _ = run_attention(bad, simt=simt, status=status)
+        assert int(status) == (10 if at <= last else 0), (at, int(status))
+        assert bool(o.isfinite().all())
