@@ -16,8 +16,12 @@ namespace gdn {
 // ------------------------------------------------------------------ prompts, CUDA cores
 // The decay factor as a sum hi + lo of two floats.  A slow decay multiplies the state
 // hundreds of times, so e^g rounded to 24 bits would leave a relative error of that many
-// half-ulps; 1 + expm1(g) keeps it to about |g| 2^-24 a step.
+// half-ulps; for g above -1/2, 1 + expm1(g) keeps it to about |g| 2^-23 a step.  Below, expm1
+// near -1 has no finer step than 2^-24, which is much of a small factor (2.6% at g = -15) and
+// all of it from -17.4 on; there e^g itself is good to 2^-22 and its error counts for the few
+// steps that such a decay leaves anything of.
 __device__ __forceinline__ float2 decay_pair(float g) {
+    if (g < -0.5f) return make_float2(expf(g), 0.f);
     const float e = expm1f(g), hi = 1.f + e;
     return make_float2(hi, e - (hi - 1.f));
 }
