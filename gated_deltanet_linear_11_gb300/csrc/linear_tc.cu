@@ -11,9 +11,9 @@
 // tokens of 48 heads):
 //     Q K^T,   Q S,   P V,   (hi + lo + rest)^T V
 // e^{T - G_j} comes from sums taken from the chunk's end and e^{G_i - G_j} inside a 32 x 32
-// block as a product of two factors where the block decays by less than 2^60, else from its
-// exponent, and elsewhere as a product of two factors at most 1: nothing overflows however
-// strong the decay.
+// block as a product of two factors where the block decays by less than 2^60, else (or with a
+// NaN in it) from its exponent, and elsewhere as a product of two factors at most 1: nothing
+// overflows however strong the decay.
 //
 // Roundings below fp32, all to bf16 and all in operands whose products only reach the bf16
 // output: P, and S where it multiplies Q.  The state itself never goes through them.
@@ -449,7 +449,8 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             uint32_t pk[16];
             if (jb <= lq) {
                 const float gi = S.g2[row];
-                const bool slow = jb == lq && S.g2[32 * jb] - S.ref[jb] >= 60.f;
+                // (a NaN among the block's gates makes its end NaN, but not the rows before it)
+                const bool slow = jb == lq && !(S.g2[32 * jb] - S.ref[jb] < 60.f);
                 const float f = p.scale * ex2(gi - S.ref[jb]);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {

@@ -69,3 +69,38 @@ def test_prefill_decays(D, dtype, T, simt):
     # g of up to 40 is summed in fp32 before the tensor cores' and the ranges' exp: 80 * 2^-24
     lim = (16 + 80) * ref.U_F32
     assert err.max() <= lim, "%.3g at g = %g" % (err.max(), DECAYS[int(err.max((1, 2)).argmax())])
+
+
+# where a value or a gate is not finite: inside a block of 32 tokens, at the start and the end of
+# one, in a last chunk that is not full, in a sequence cut into ranges
+PLACES = [([150], 5), ([150], 32), ([150], 127), ([150], 149), ([150], 0), ([60, 90], 100),
+          ([300, 128], 200), ([2100], 1000), ([2100], 2090)]
+
+
+def upto(lens, j):
+    """(first token, end, index) of the sequence of token j."""
+    cu = np.concatenate(([0], np.cumsum(lens))).tolist()
+    n = max(i for i in range(len(lens)) if cu[i] <= j)
+    return cu[n], cu[n + 1], n
+
+
+@pytest.mark.parametrize("lens,j", PLACES)
+@pytest.mark.parametrize("simt", [False, True])
+def test_prefill_gate_nan_reaches_only_later_tokens(lens, j, simt):
+    d = make(34, lens, 1, 2, 128, torch.bfloat16, True, True)
+    o1, h1 = call(d, simt=simt)
+    d["g"][j, 1] = float("nan")
+    o2, h2 = call(d, simt=simt)
+    a, b, n = upto(lens, j)
+    assert bool(o2[j:b, 1].isnan().all()) and bool(h2[n, 1].isnan().all())
+    assert_bits_equal(o1[:, 0], o2[:, 0], "the other head")
+    rest = [i for i in range(len(lens)) if i != n]
+    assert_bits_equal(h1[rest], h2[rest], "other sequences' states")
+    before = [i for i in range(sum(lens)) if not a <= i or i >= b or i < j]
+    if simt:
+        assert_bits_equal(o1[before], o2[before], "earlier tokens")
+    # (the tensor-core form takes the weights of that block of 32 from their exponents)
+    _, _, oa, _ = ref.linear_scan(np64(d["q"]), np64(d["k"]), np64(d["v"]),
+                                  np.nan_to_num(np64(d["g"])),
+                                  np.concatenate(([0], np.cumsum(lens))).tolist(), np64(d["h0"]))
+    assert np.all(np.abs(np64(o1[before]) - np64(o2[before])) <= 4 * ref.U_BF16 * oa[before])
