@@ -23,6 +23,12 @@
 // one TMEM lane and a quarter of the columns: weighted keys (A), P (B), state (C), output
 // (D); warp 16 issues the products, warp 17 the tile loads, warp 18 the sums of the gates.
 //
+// A value that is not finite would reach the chunk's earlier tokens through its weights of zero.
+// It leaves its column of the state so to the end, which costs nothing to see; a CTA that sees it
+// runs once more, and this time warp 18 takes such values out before the products and their
+// columns become NaN from their tokens on, in the outputs and in the state.  (4096 tokens of 48
+// heads 70 us, 68.5 without all this, 81 where every call looks at every chunk's values.)
+//
 // An SM's shared memory passes 128 bytes a clock, which a 128 x 128 product with both
 // operands there uses up: with P and the weighted keys in shared memory a chunk moved 5100
 // clocks' worth (measured 8700 a chunk).  They are TMEM operands instead: P over the scores
@@ -116,6 +122,7 @@ struct LinBars {
     uint64_t q[2], k[3], v[4];           // tiles loaded
     uint64_t qk[2], qs[2], kv[2], pv[2]; // products done (two: by the buffers they read)
     uint64_t gates;                      // this chunk's gate arrays are written
+    uint64_t vs[2];                      // the values have been looked at
     uint64_t r_kt[2], r_p, r_s, r_o, r_arr;   // every elementwise warp: operands written, arrays read
     uint64_t out[2];                     // an output tile is written (over its chunk's Q)
     uint64_t kf[3], vf[4];               // range pass: tiles free
@@ -131,7 +138,11 @@ struct LinSmem {
     float decay;         // e^T
     uint32_t tmem;
     int abort;
-    LinBars bar;
+    // by chunk mod 3: whether some value is not finite, and each column's first such token
+    int bad[3];
+    int again;           // the first pass saw a state that is not finite
+    uint32_t first_bad[3][kLinC / 4];    // four columns a word; 255: none
+    LinBars bar[2];      // one set for each pass
 };
 static_assert(sizeof(LinSmem) <= 227 * 1024, "one CTA fits on an SM");
 
@@ -345,6 +356,41 @@ __device__ __forceinline__ void clear_rows(uint8_t *tile, int L) {
             *reinterpret_cast<uint4 *>(tile + kb * kBlk + tc::swz(row, ch)) = make_uint4(0, 0, 0, 0);
     }
 }
+// Whether some value of the first L tokens is not finite (one warp): 0 times it is NaN.
+__device__ __forceinline__ bool any_nonfinite(const uint8_t *tile, int L) {
+    const int lane = threadIdx.x & 31;
+    const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+    __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
+#pragma unroll 4
+    for (int r0 = 0; r0 < L; r0 += 4) {
+        const int row = r0 + (lane >> 3);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (row < L) x = *reinterpret_cast<const uint4 *>(tile + kb * kBlk + tc::swz(row, lane & 7));
+            const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = __hfma2(p[e], zero, acc[e]);
+        }
+    }
+    uint32_t any = 0u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) any |= *reinterpret_cast<const uint32_t *>(&acc[e]);
+    return __any_sync(0xffffffffu, (any & 0x7f807f80u) != 0u) != 0;
+}
+// Zeroes them and notes each column's first token with one.
+__device__ __noinline__ void take_out_nonfinite(uint8_t *tile, int L, uint8_t *first_bad) {
+    for (int c = threadIdx.x & 31; c < 128; c += 32) {
+        int first = 255;
+        for (int row = L - 1; row >= 0; --row) {
+            uint16_t *x = reinterpret_cast<uint16_t *>(tile + (c >> 6) * kBlk + tc::swz(row, (c & 63) >> 3)) + (c & 7);
+            if ((*x & 0x7f80u) != 0x7f80u) continue;
+            first = row;
+            *x = 0;
+        }
+        first_bad[c] = (uint8_t)first;
+    }
+}
 // 32 floats of one row as bf16 into columns 32 quarter .. of a tile.
 __device__ __forceinline__ void store_row(uint8_t *tile, int quarter, int row, const float (&v)[32]) {
     const int blk = quarter >> 1, n0 = 32 * (quarter & 1);
@@ -361,14 +407,11 @@ __device__ __forceinline__ void store_row(uint8_t *tile, int quarter, int row, c
 
 // ------------------------------------------------------------------------- output pass
 
-__global__ void __launch_bounds__(kLinThreads, 1)
-linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    LinSmem &S = *reinterpret_cast<LinSmem *>(smem_raw);
-    if (tc::smem_u32(smem_raw) & 1023u) {        // the tiles' swizzle needs it; never seen
-        if (threadIdx.x == 0) report(p.status, GDN_ERR_CUDA);
-        return;
-    }
+// A range's pass over its chunks.  CAREFUL: values that are not finite are taken out; otherwise
+// true where they have to be, and no final state is written then.
+template <bool CAREFUL>
+__device__ __forceinline__ bool linear_out_pass(const LinMaps &maps, const LinParams &p, LinSmem &S) {
+    LinBars &B = S.bar[CAREFUL];
     uint8_t *sS = S.tile[6];      // Q, K, V of chunk i: tiles 0, 2, 4 + (i & 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int range = blockIdx.x, hv = blockIdx.y, n = p.sequence(blockIdx.z), hk = hv / (p.Hv / p.Hk);
@@ -376,20 +419,14 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     const int nch = (len + kLinC - 1) / kLinC;
     const int rc = range_chunks_of(nch, p.max_par);
     const int c_first = range * rc, c_last = min(nch, c_first + rc);
-    if (range > 0 && c_first >= nch) return;
     const int count = c_last - c_first;          // 0 for an empty sequence
     const bool last = c_last >= nch;
     const uint32_t colSc = 0, colOi = 128, colOa = 256, colD = 384;   // P over Sc, keys over Oa
 
-    if (warp == 0) {
-        tc::tmem_alloc(&S.tmem, 512);
-        tc::tmem_relinquish();
-    }
     if (tid == 0) {
-        S.abort = 0;
-        LinBars &b = S.bar;
+        LinBars &b = B;
         for (uint64_t *x : {&b.q[0], &b.q[1], &b.k[0], &b.k[1], &b.v[0], &b.v[1], &b.qk[0], &b.qk[1], &b.qs[0], &b.qs[1],
-                            &b.kv[0], &b.kv[1], &b.pv[0], &b.pv[1], &b.gates, &b.fin})
+                            &b.kv[0], &b.kv[1], &b.pv[0], &b.pv[1], &b.gates, &b.vs[0], &b.vs[1], &b.fin})
             tc::mbar_init(x, 1);
         for (uint64_t *x : {&b.r_kt[0], &b.r_kt[1], &b.r_p, &b.r_s, &b.r_o, &b.r_arr, &b.out[0], &b.out[1]})
             tc::mbar_init(x, kLinWarps);
@@ -400,12 +437,12 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     tc::fence_after_sync();
     const uint32_t tmem = S.tmem;
 
+    const int lq = warp & 3, jb = warp >> 2;        // rows 32 lq .., columns 32 jb ..
+    const int row = 32 * lq + lane;
+    const int64_t st_off = (int64_t)row * 128 + 32 * jb;
+    float st[32];                                   // (the elementwise warps')
     if (warp < kLinWarps) {
-        const int lq = warp & 3, jb = warp >> 2;    // rows 32 lq .., columns 32 jb ..
-        const int row = 32 * lq + lane;
         const uint32_t tm = tmem + ((uint32_t)(32 * lq) << 16) + 32 * jb;
-        const int64_t st_off = (int64_t)row * 128 + 32 * jb;
-        float st[32];
         const float *src = nullptr;
         if (range > 0 || (p.in_place && rc < nch)) {
             grid_dependency_wait();
@@ -421,7 +458,7 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         }
         if (count > 0) {
             store_row(sS, jb, row, st);
-            warp_arrive(&S.bar.r_s);
+            warp_arrive(&B.r_s);
         }
         for (int i = 0; i < count; ++i) {
             // a buffer of two serves every other chunk
@@ -430,20 +467,20 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             const int L = min(kLinC, t0 + len - t);
             // ---- A: weighted keys, over the P V that this warp has read (the gates' warp has
             // seen the keys' tile arrive)
-            if (!warp_wait(S, &S.bar.gates, ph)) break;
+            if (!warp_wait(S, &B.gates, ph)) break;
             uint32_t rest[2][8];
             if (L == kLinC) {
                 weigh_keys<false, 32>(S.tile[2 + ph], tmem + colOa, lq, jb, S.w, L, rest);
             } else {
                 weigh_keys<true, 32>(S.tile[2 + ph], tmem + colOa, lq, jb, S.w, L, rest);
-                if (!warp_wait(S, &S.bar.v[ph], ph2)) break;
+                if (!warp_wait(S, &B.v[ph], ph2)) break;
                 clear_rows(S.tile[4 + ph], L);
                 tc::fence_async_smem();
             }
             tc::tmem_wait_st();
-            warp_arrive_tmem(&S.bar.r_kt[ph]);
+            warp_arrive_tmem(&B.r_kt[ph]);
             // ---- B: P = decay-weighted lower triangle of Q K^T
-            if (!warp_wait(S, &S.bar.qk[ph], ph2)) break;
+            if (!warp_wait(S, &B.qk[ph], ph2)) break;
             tc::fence_after_sync();
             const float eg = S.eg[row], decay = S.decay;
             uint32_t pk[16];
@@ -489,22 +526,31 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             tmem_st16(tm + colSc, pk);
             store_rest(tmem + colSc + 32 * jb + 16, lq, rest);
             tc::tmem_wait_st();
-            warp_arrive_tmem(&S.bar.r_p);
-            if (lane == 0) mbar_arrive(&S.bar.r_arr);
+            warp_arrive_tmem(&B.r_p);
+            // (the values two chunks on are looked at after this arrival only)
+            if (CAREFUL && !warp_wait(S, &B.vs[ph], ph2)) break;
+            if (lane == 0) mbar_arrive(&B.r_arr);
             // ---- C: state
-            if (!warp_wait(S, &S.bar.kv[1], ph)) break;
+            if (!warp_wait(S, &B.kv[1], ph)) break;
             tc::fence_after_sync();
             float v[32];
             tc::tmem_ld32(tm + colD, v);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 32; ++j) st[j] = fmaf(decay, st[j], v[j]);
+            const bool bad = CAREFUL && S.bad[i % 3] != 0;
+            const uint32_t *first_bad = S.first_bad[i % 3] + 8 * jb;
+            if (bad) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (((first_bad[j >> 2] >> (8 * (j & 3))) & 255u) != 255u) st[j] = __int_as_float(0x7fffffff);
+            }
             store_row(sS, jb, row, st);      // Q S came before the keys' product: it is done
 
-            warp_arrive(&S.bar.r_s);
+            warp_arrive(&B.r_s);
             // ---- D: output; a full chunk goes over its Q tile (Q K and Q S are done) and leaves
             // by tensor store, a last, partial one straight from the threads
-            if (!warp_wait(S, &S.bar.pv[ph], ph2)) break;
+            if (!warp_wait(S, &B.pv[ph], ph2)) break;
             tc::fence_after_sync();
             uint32_t u[16];
 #pragma unroll
@@ -517,13 +563,18 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                 for (int e = 0; e < 8; ++e)
                     u[8 * c + e] = pack_bf2(fmaf(eg, a[2 * e], v[2 * e]), fmaf(eg, a[2 * e + 1], v[2 * e + 1]));
             }
-            warp_arrive_tmem(&S.bar.r_o);
+            warp_arrive_tmem(&B.r_o);
+            if (bad) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (((first_bad[j >> 2] >> (8 * (j & 3))) & 255u) <= (uint32_t)row) u[j >> 1] |= 0x7fffu << (16 * (j & 1));
+            }
             if (L == kLinC) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     *reinterpret_cast<uint4 *>(S.tile[ph] + (jb >> 1) * kBlk + tc::swz(row, 4 * (jb & 1) + c)) =
                         make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
-                warp_arrive(&S.bar.out[ph]);
+                warp_arrive(&B.out[ph]);
             } else if (row < L) {
                 uint4 *dst = reinterpret_cast<uint4 *>(p.o + (int64_t)(t + row) * p.o_tok + (int64_t)hv * 128 + 32 * jb);
 #pragma unroll
@@ -531,45 +582,46 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
                     dst[c] = make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
             }
         }
-        if (last && p.hT && !*(volatile int *)&S.abort) {
-            float4 *out = reinterpret_cast<float4 *>(p.hT + ((int64_t)n * p.Hv + hv) * 16384 + st_off);
+        if (!CAREFUL && count > 0) {
+            float zero = 0.f;                       // or NaN
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                out[e] = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
+            for (int j = 0; j < 32; ++j) zero = fmaf(st[j], 0.f, zero);
+            if (__any_sync(0xffffffffu, zero != zero) && lane == 0) S.again = 1;
         }
     } else if (warp == kLinWarps) {
         // ---- products
         for (int i = 0; i < count; ++i) {
             const uint32_t ph = i & 1, ph2 = (i >> 1) & 1;
             const uint8_t *sQ = S.tile[ph], *sK = S.tile[2 + ph], *sV = S.tile[4 + ph];
-            if (!warp_wait(S, &S.bar.q[ph], ph2) || !warp_wait(S, &S.bar.k[ph], ph2)) break;
-            if (i > 0 && !warp_wait(S, &S.bar.pv[ph ^ 1], ((i - 1) >> 1) & 1)) break;      // P is read: the scores' turn
+            if (!warp_wait(S, &B.q[ph], ph2) || !warp_wait(S, &B.k[ph], ph2)) break;
+            if (i > 0 && !warp_wait(S, &B.pv[ph ^ 1], ((i - 1) >> 1) & 1)) break;      // P is read: the scores' turn
             tc::fence_after_sync();
             product<0, 0>(tmem + colSc, sQ, sK, false);
-            tc::mma_commit_warp(&S.bar.qk[ph]);
-            if (!warp_wait(S, &S.bar.r_s, ph)) break;
-            if (i > 0 && !warp_wait(S, &S.bar.r_o, ph ^ 1)) break;
+            tc::mma_commit_warp(&B.qk[ph]);
+            if (!warp_wait(S, &B.r_s, ph)) break;
+            if (i > 0 && !warp_wait(S, &B.r_o, ph ^ 1)) break;
             tc::fence_after_sync();
             product<0, 1>(tmem + colOi, sQ, sS, false);
-            tc::mma_commit_warp(&S.bar.qs[ph]);
-            if (!warp_wait(S, &S.bar.r_kt[ph], ph2) || !warp_wait(S, &S.bar.v[ph], ph2)) break;
+            tc::mma_commit_warp(&B.qs[ph]);
+            if (!warp_wait(S, &B.r_kt[ph], ph2) || !warp_wait(S, &B.v[ph], ph2)) break;
+            if (CAREFUL && !warp_wait(S, &B.vs[ph], ph2)) break;
             tc::fence_after_sync();
             product_ts<32>(tmem + colD, tmem + colOa, sV, false);
             product_ts<32>(tmem + colD, tmem + colOa + 16, sV, true);
-            tc::mma_commit_warp(&S.bar.kv[0]);
-            if (!warp_wait(S, &S.bar.r_p, ph)) break;
+            tc::mma_commit_warp(&B.kv[0]);
+            if (!warp_wait(S, &B.r_p, ph)) break;
             tc::fence_after_sync();
             product_ts<32>(tmem + colD, tmem + colSc + 16, sV, true);
-            tc::mma_commit_warp(&S.bar.kv[1]);
+            tc::mma_commit_warp(&B.kv[1]);
             // the keys' columns take P V next
-            if (!warp_wait(S, &S.bar.kv[0], ph)) break;
+            if (!warp_wait(S, &B.kv[0], ph)) break;
             tc::fence_after_sync();
             product_ts<32>(tmem + colOa, tmem + colSc, sV, false);
-            tc::mma_commit_warp(&S.bar.pv[ph]);
+            tc::mma_commit_warp(&B.pv[ph]);
         }
         // everything issued has completed before the TMEM is freed
-        tc::mma_commit_warp(&S.bar.fin);
-        wait_copy(&S.bar.fin, 0);
+        tc::mma_commit_warp(&B.fin);
+        wait_copy(&B.fin, 0);
     } else if (warp == kLinWarps + 1) {
         // ---- tile loads: buffers of two, each refilled when its last reader is done
         if (lane == 0) {
@@ -580,7 +632,7 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             const int full = last && len % kLinC ? count - 1 : count;     // chunks of 128 tokens
             // the output of chunk i, when it is written over Q
             auto put = [&](int i) {
-                if (!lin_wait<100>(S, &S.bar.out[i & 1], (i >> 1) & 1)) return false;
+                if (!lin_wait<100>(S, &B.out[i & 1], (i >> 1) & 1)) return false;
                 const int t = t0 + (c_first + i) * kLinC;
                 tc::tma_store_3d(&maps.o, S.tile[i & 1], 0, hv, t);
                 tc::tma_store_3d(&maps.o, S.tile[i & 1] + kBlk, 64, hv, t);
@@ -591,28 +643,42 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             for (int i = 0; i < count && ok; ++i) {
                 const uint32_t b = i & 1, was = ((i >> 1) & 1) ^ 1;   // chunk i - 2's use of the buffer
                 const int t = t0 + (c_first + i) * kLinC;
-                if (i >= 2 && !(ok = lin_wait<100>(S, &S.bar.qk[b], was) && lin_wait<100>(S, &S.bar.r_kt[b], was))) break;
-                load_tile(S.tile[2 + b], &maps.k, &S.bar.k[b], hk, t);
+                if (i >= 2 && !(ok = lin_wait<100>(S, &B.qk[b], was) && lin_wait<100>(S, &B.r_kt[b], was))) break;
+                load_tile(S.tile[2 + b], &maps.k, &B.k[b], hk, t);
                 ++nk;
                 if (i >= 2) {
                     if (!(ok = put(i - 2))) break;
                     tc::bulk_wait_read<0>();
                 }
-                load_tile(S.tile[b], &maps.q, &S.bar.q[b], hk, t);
+                load_tile(S.tile[b], &maps.q, &B.q[b], hk, t);
                 ++nq;
-                if (i >= 2 && !(ok = lin_wait<100>(S, &S.bar.pv[b], was))) break;
-                load_tile(S.tile[4 + b], &maps.v, &S.bar.v[b], hv, t);
+                if (i >= 2 && !(ok = lin_wait<100>(S, &B.pv[b], was))) break;
+                load_tile(S.tile[4 + b], &maps.v, &B.v[b], hv, t);
                 ++nv;
             }
             for (int i = max(0, count - 2); i < full && ok; ++i) ok = put(i);
             tc::bulk_wait_all();
             // (bounded) everything loaded has landed
-            for (int x = max(0, nk - 2); x < nk; ++x) wait_copy(&S.bar.k[x & 1], (x >> 1) & 1);
-            for (int x = max(0, nq - 2); x < nq; ++x) wait_copy(&S.bar.q[x & 1], (x >> 1) & 1);
-            for (int x = max(0, nv - 2); x < nv; ++x) wait_copy(&S.bar.v[x & 1], (x >> 1) & 1);
+            for (int x = max(0, nk - 2); x < nk; ++x) wait_copy(&B.k[x & 1], (x >> 1) & 1);
+            for (int x = max(0, nq - 2); x < nq; ++x) wait_copy(&B.q[x & 1], (x >> 1) & 1);
+            for (int x = max(0, nv - 2); x < nv; ++x) wait_copy(&B.v[x & 1], (x >> 1) & 1);
         }
     } else {
-        // ---- gates
+        // ---- gates; carefully, a look at the next chunk's values too
+        auto look = [&](int i) {
+            if (!warp_wait<100>(S, &B.v[i & 1], (i >> 1) & 1)) return false;
+            const int L = min(kLinC, len - (c_first + i) * kLinC);
+            uint8_t *tile = S.tile[4 + (i & 1)];
+            const bool bad = any_nonfinite(tile, L);
+            if (bad) {
+                take_out_nonfinite(tile, L, reinterpret_cast<uint8_t *>(S.first_bad[i % 3]));
+                tc::fence_async_smem();
+            }
+            if (lane == 0) S.bad[i % 3] = bad;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.vs[i & 1]);
+            return true;
+        };
         float x[4];
         if (count > 0) load_gates(p, hv, t0 + c_first * kLinC, min(kLinC, len - c_first * kLinC), x);
         for (int i = 0; i < count; ++i) {
@@ -627,8 +693,8 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             float y[4];
             const int t = t0 + (c_first + i + 1) * kLinC;
             if (i + 1 < count) load_gates(p, hv, t, min(kLinC, t0 + len - t), y);
-            if (i > 0 && !warp_wait<100>(S, &S.bar.r_arr, (i & 1) ^ 1)) break;
-            if (!warp_wait<100>(S, &S.bar.k[i & 1], (i >> 1) & 1)) break;
+            if (i > 0 && !warp_wait<100>(S, &B.r_arr, (i & 1) ^ 1)) break;
+            if (!warp_wait<100>(S, &B.k[i & 1], (i >> 1) & 1)) break;
             const float end = below + pre[3];
             const float ref = __shfl_sync(0xffffffffu, end, lane | 7) * kLog2E;
 #pragma unroll
@@ -643,17 +709,55 @@ linear_out_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             if ((lane & 7) == 7) S.ref[lane >> 3] = ref;
             if (lane == 31) S.decay = expf(end);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&S.bar.gates);
+            if (lane == 0) mbar_arrive(&B.gates);
+            // (chunk i + 1 has the words of chunk i - 2, which every warp has left)
+            if (CAREFUL && i == 0 && !look(0)) break;
+            if (CAREFUL && i + 1 < count && !look(i + 1)) break;
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = y[e];
         }
     }
+    // everything that was issued has completed
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 0) tc::tmem_dealloc(tmem, 512);
-    if (tid == 0 && S.abort) report(p.status, GDN_ERR_TIMEOUT);
+    if (!CAREFUL && S.again && !S.abort) return true;
+    if (warp < kLinWarps && last && p.hT && !S.abort) {
+        float4 *out = reinterpret_cast<float4 *>(p.hT + ((int64_t)n * p.Hv + hv) * 16384 + st_off);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            out[e] = make_float4(st[4 * e], st[4 * e + 1], st[4 * e + 2], st[4 * e + 3]);
+    }
+    return false;
 }
+// (a function of its own, so that the first pass is compiled without it)
+__device__ __noinline__ void linear_out_careful(const LinMaps &maps, const LinParams &p, LinSmem &S) {
+    linear_out_pass<true>(maps, p, S);
+}
+
+__global__ void __launch_bounds__(kLinThreads, 1)
+linear_out_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    LinSmem &S = *reinterpret_cast<LinSmem *>(smem_raw);
+    if (tc::smem_u32(smem_raw) & 1023u) {        // the tiles' swizzle needs it; never seen
+        if (threadIdx.x == 0) report(p.status, GDN_ERR_CUDA);
+        return;
+    }
+    const int n = p.sequence(blockIdx.z), len = p.cu[n + 1] - p.cu[n];
+    const int nch = (len + kLinC - 1) / kLinC;
+    if (blockIdx.x > 0 && (int)blockIdx.x * range_chunks_of(nch, p.max_par) >= nch) return;
+    const int warp = threadIdx.x >> 5;
+    if (warp == 0) {
+        tc::tmem_alloc(&S.tmem, 512);
+        tc::tmem_relinquish();
+    }
+    if (threadIdx.x == 0) S.abort = S.again = 0;
+    if (linear_out_pass<false>(maps, p, S)) linear_out_careful(maps, p, S);
+    __syncthreads();
+    if (warp == 0) tc::tmem_dealloc(S.tmem, 512);
+    if (threadIdx.x == 0 && S.abort) report(p.status, GDN_ERR_TIMEOUT);
+}
+
 
 // -------------------------------------------------------------------------- range states
 // State that one range adds, from zero, with decays to the range's end: its chunks in
@@ -668,6 +772,7 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         return;
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    LinBars &B = S.bar[0];
     const int range = blockIdx.x, hv = blockIdx.y, n = p.sequence(blockIdx.z), hk = hv / (p.Hv / p.Hk);
     const int t0 = p.cu[n], len = p.cu[n + 1] - t0;
     const int nch = (len + kLinC - 1) / kLinC;
@@ -682,7 +787,7 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     }
     if (tid == 0) {
         S.abort = 0;
-        LinBars &b = S.bar;
+        LinBars &b = B;
         for (uint64_t *x : {&b.k[0], &b.k[1], &b.k[2], &b.v[0], &b.v[1], &b.v[2], &b.v[3], &b.kv[0],
                             &b.kv[1], &b.vf[0], &b.vf[1], &b.vf[2], &b.vf[3], &b.gates, &b.fin})
             tc::mbar_init(x, 1);
@@ -700,19 +805,19 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
         bool ok = true;
         for (int i = 0; i < count && ok; ++i) {
             const int bf = i & 1, kb = i % 3;
-            if (!(ok = warp_wait(S, &S.bar.gates, i & 1) && warp_wait(S, &S.bar.k[kb], (i / 3) & 1))) break;
-            if (i >= 2 && !(ok = warp_wait(S, &S.bar.kv[bf], ((i >> 1) & 1) ^ 1))) break;
+            if (!(ok = warp_wait(S, &B.gates, i & 1) && warp_wait(S, &B.k[kb], (i / 3) & 1))) break;
+            if (i >= 2 && !(ok = warp_wait(S, &B.kv[bf], ((i >> 1) & 1) ^ 1))) break;
             tc::fence_after_sync();
             uint32_t rest[2][8];
             weigh_keys<false, 48>(S.tile[kb], tmem + 128 + 192 * bf, warp & 3, warp >> 2, S.w, kLinC, rest);
             store_rest(tmem + 128 + 192 * bf + 48 * (warp >> 2) + 32, warp & 3, rest);
             tc::tmem_wait_st();
-            warp_arrive_tmem(&S.bar.r_kt[bf]);
-            if (lane == 0) mbar_arrive(&S.bar.kf[kb]);
-            if (lane == 0) mbar_arrive(&S.bar.r_arr);
+            warp_arrive_tmem(&B.r_kt[bf]);
+            if (lane == 0) mbar_arrive(&B.kf[kb]);
+            if (lane == 0) mbar_arrive(&B.r_arr);
         }
         const int e = count - 1;
-        if (ok && warp_wait(S, &S.bar.kv[e & 1], (e >> 1) & 1)) {
+        if (ok && warp_wait(S, &B.kv[e & 1], (e >> 1) & 1)) {
             tc::fence_after_sync();
             const int lq = warp & 3, jb = warp >> 2;
             float4 *out = reinterpret_cast<float4 *>(p.ranges + slot * 16384 + (32 * lq + lane) * 128 + 32 * jb);
@@ -726,30 +831,30 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
     } else if (warp == kLinWarps) {
         for (int i = 0; i < count; ++i) {
             const int bf = i & 1, vb = i & 3;
-            if (!warp_wait(S, &S.bar.r_kt[bf], (i >> 1) & 1) || !warp_wait(S, &S.bar.v[vb], (i >> 2) & 1)) break;
+            if (!warp_wait(S, &B.r_kt[bf], (i >> 1) & 1) || !warp_wait(S, &B.v[vb], (i >> 2) & 1)) break;
             tc::fence_after_sync();
             product_ts<48>(tmem, tmem + 128 + 192 * bf, S.tile[3 + vb], i > 0);
             product_ts<48>(tmem, tmem + 144 + 192 * bf, S.tile[3 + vb], true);
             product_ts<48>(tmem, tmem + 160 + 192 * bf, S.tile[3 + vb], true);
-            tc::mma_commit_warp(&S.bar.kv[bf]);
-            tc::mma_commit_warp(&S.bar.vf[vb]);
+            tc::mma_commit_warp(&B.kv[bf]);
+            tc::mma_commit_warp(&B.vf[vb]);
         }
-        tc::mma_commit_warp(&S.bar.fin);
-        wait_copy(&S.bar.fin, 0);
+        tc::mma_commit_warp(&B.fin);
+        wait_copy(&B.fin, 0);
     } else if (warp == kLinWarps + 1) {
         if (lane == 0) {
             int nk = 0, nv = 0;
             for (int i = 0; i < count; ++i) {
                 const int kb = i % 3, vb = i & 3, t = t0 + (c_first + count - 1 - i) * kLinC;
-                if (i >= 3 && !lin_wait<100>(S, &S.bar.kf[kb], ((i / 3) & 1) ^ 1)) break;
-                load_tile(S.tile[kb], &maps.k, &S.bar.k[kb], hk, t);
+                if (i >= 3 && !lin_wait<100>(S, &B.kf[kb], ((i / 3) & 1) ^ 1)) break;
+                load_tile(S.tile[kb], &maps.k, &B.k[kb], hk, t);
                 ++nk;
-                if (i >= 4 && !lin_wait<100>(S, &S.bar.vf[vb], ((i >> 2) & 1) ^ 1)) break;
-                load_tile(S.tile[3 + vb], &maps.v, &S.bar.v[vb], hv, t);
+                if (i >= 4 && !lin_wait<100>(S, &B.vf[vb], ((i >> 2) & 1) ^ 1)) break;
+                load_tile(S.tile[3 + vb], &maps.v, &B.v[vb], hv, t);
                 ++nv;
             }
-            for (int x = max(0, nk - 3); x < nk; ++x) wait_copy(&S.bar.k[x % 3], (x / 3) & 1);
-            for (int x = max(0, nv - 4); x < nv; ++x) wait_copy(&S.bar.v[x & 3], (x >> 2) & 1);
+            for (int x = max(0, nk - 3); x < nk; ++x) wait_copy(&B.k[x % 3], (x / 3) & 1);
+            for (int x = max(0, nv - 4); x < nv; ++x) wait_copy(&B.v[x & 3], (x >> 2) & 1);
         }
     } else {
         float x[4], carry = 0.f;
@@ -764,11 +869,11 @@ linear_range_kernel(const __grid_constant__ LinMaps maps, const LinParams p) {
             const float all = __shfl_sync(0xffffffffu, above + sum, 0);
             float y[4];
             if (i + 1 < count) load_gates(p, hv, t0 + (c_first + count - 2 - i) * kLinC, kLinC, y);
-            if (i > 0 && !warp_wait<100>(S, &S.bar.r_arr, (i & 1) ^ 1)) break;
+            if (i > 0 && !warp_wait<100>(S, &B.r_arr, (i & 1) ^ 1)) break;
 #pragma unroll
             for (int e = 0; e < 4; ++e) S.w[4 * lane + e] = expf(carry + (above + suf[e]));
             __syncwarp();
-            if (lane == 0) mbar_arrive(&S.bar.gates);
+            if (lane == 0) mbar_arrive(&B.gates);
             carry += all;
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = y[e];

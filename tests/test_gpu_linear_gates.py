@@ -104,3 +104,59 @@ def test_prefill_gate_nan_reaches_only_later_tokens(lens, j, simt):
                                   np.nan_to_num(np64(d["g"])),
                                   np.concatenate(([0], np.cumsum(lens))).tolist(), np64(d["h0"]))
     assert np.all(np.abs(np64(o1[before]) - np64(o2[before])) <= 4 * ref.U_BF16 * oa[before])
+
+
+@pytest.mark.parametrize("lens,j", PLACES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("simt", [False, True])
+def test_prefill_values_reach_only_later_tokens(lens, j, bad, simt):
+    """A value that is not finite makes its column so from its token on, and nothing else."""
+    d = make(32, lens, 1, 2, 128, torch.bfloat16, True, True, slow=True)
+    o1, h1 = call(d, simt=simt)
+    d["v"][j, 1, 70] = bad
+    d["v"][j, 0, 3] = bad
+    o2, h2 = call(d, simt=simt)
+    a, b, n = upto(lens, j)
+    keep, keep_h = torch.ones(o1.shape, dtype=torch.bool), torch.ones(h1.shape, dtype=torch.bool)
+    for h, c in ((1, 70), (0, 3)):
+        assert not bool(o2[j:b, h, c].isfinite().any())
+        assert not bool(h2[n, h, :, c].isfinite().any())
+        keep[j:b, h, c] = False
+        keep_h[n, h, :, c] = False
+    assert_bits_equal(o1[keep], o2[keep], "outputs that the value does not reach")
+    assert_bits_equal(h1[keep_h], h2[keep_h], "state columns that the value does not reach")
+
+
+@pytest.mark.parametrize("simt", [False, True])
+def test_prefill_many_values_not_finite(simt):
+    """Several of them in one column and chunk, in all columns of a token, and in every token
+    of a chunk; the first counts."""
+    d = make(33, [400], 1, 3, 128, torch.bfloat16, True, False, slow=True)
+    o1, h1 = call(d, simt=simt)
+    d["v"][[40, 90, 200], 0, 9] = float("nan")
+    d["v"][77, 1] = float("inf")
+    d["v"][256:384, 2] = float("nan")
+    o2, h2 = call(d, simt=simt)
+    keep = torch.ones(o1.shape, dtype=torch.bool)
+    keep[40:, 0, 9] = False
+    keep[77:, 1] = False
+    keep[256:, 2] = False
+    assert_bits_equal(o1[keep], o2[keep], "outputs that no value reaches")
+    assert not bool(o2[~keep.to(o2.device)].isfinite().any())
+    assert not bool(h2[0, 1:].isfinite().any()) and not bool(h2[0, 0, :, 9].isfinite().any())
+
+
+@pytest.mark.parametrize("lens,j", [([150], 40), ([2100], 700), ([2100, 90], 2150)])
+def test_prefill_value_not_finite_with_the_state_in_place(lens, j):
+    """The state that such a call starts from is still there where it runs again."""
+    d = make(37, lens, 1, 2, 128, torch.bfloat16, True, True, slow=True)
+    d["v"][j, 1, 70] = float("nan")
+    o1, h1 = call(d)
+    state = d["h0"].cuda()
+    dev = {x: d[x].cuda() for x in ("q", "k", "v", "g", "cu")}
+    o2, h2 = gdn.gdn_linear_prefill(dev["q"], dev["k"], dev["v"], dev["g"], dev["cu"],
+                                    initial_state=state, final_state=state,
+                                    cu_seqlens_host=d["cu"])
+    assert_bits_equal(o1, o2, "o with the state in place")
+    assert_bits_equal(h1, state, "state in place")
+    assert bool(o2.isnan().any()) and int(h2.isnan().sum()) == 128
