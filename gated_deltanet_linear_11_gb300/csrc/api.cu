@@ -536,9 +536,16 @@ gdn_status_t linear_args(const gdn_tensor_t *q, const gdn_tensor_t *k, const gdn
     return GDN_OK;
 }
 
-gdn_status_t check_gates(const gdn_host::LinearArgs &a, cudaStream_t st) {
-    const size_t n = a.g_tok ? (size_t)a.T * a.Hv : (size_t)a.Hv;
-    return check_finite(a.g, a.g, n, st);
+// GDN_CHECK_INPUTS: no log decay is NaN or +inf (-inf clears the state).
+gdn_status_t check_decays(const gdn_host::LinearArgs &a, cudaStream_t st) {
+    std::vector<float> h(a.g_tok ? (size_t)a.T * a.Hv : (size_t)a.Hv);
+    if (cudaMemcpyAsync(h.data(), a.g, h.size() * sizeof(float), cudaMemcpyDeviceToHost, st) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    for (float g : h)
+        if (!std::isfinite(g) && !(g < 0.f)) return GDN_ERR_NONFINITE;
+    return GDN_OK;
 }
 
 // The cache's own fields, and the new tokens' offsets (cu_host may be NULL: one each).
@@ -616,7 +623,7 @@ gdn_status_t gdn_linear_prefill(const gdn_tensor_t *q, const gdn_tensor_t *k,
     cudaStream_t st = (cudaStream_t)stream;
     if (N == 0) return GDN_OK;
     if ((flags & GDN_CHECK_INPUTS) &&
-        ((a.T > 0 && (s = check_gates(a, st)) != GDN_OK) ||
+        ((a.T > 0 && (s = check_decays(a, st)) != GDN_OK) ||
          (s = check_seqlens_copy(cu_seqlens_dev, cu_seqlens_host, N, st)) != GDN_OK))
         return s;
     a.cu = cu_seqlens_dev;
@@ -652,7 +659,7 @@ gdn_status_t gdn_linear_decode(const gdn_tensor_t *q, const gdn_tensor_t *k,
     if (!state) return GDN_ERR_NULL;
     if (!state_idx && P < a.T) return GDN_ERR_SHAPE;
     if (!aligned16(state)) return GDN_ERR_LAYOUT;
-    if ((flags & GDN_CHECK_INPUTS) && (s = check_gates(a, (cudaStream_t)stream)) != GDN_OK)
+    if ((flags & GDN_CHECK_INPUTS) && (s = check_decays(a, (cudaStream_t)stream)) != GDN_OK)
         return s;
     a.state = state;
     a.P = P;

@@ -377,7 +377,8 @@ gdn_status_t gdn_fused_decode(const void *x, int32_t N, int32_t Hk, int32_t Hv, 
  * likewise or NULL (not written; may equal initial_state).  Every sequence's results are
  * bit-identical alone and in any batch on one device.  workspace: device scratch of
  * gdn_linear_prefill_workspace_size() bytes, 256-byte aligned (may be NULL when 0).
- * flags: GDN_PREFILL_SIMT forces the CUDA-core kernel, GDN_CHECK_INPUTS as above.
+ * flags: GDN_PREFILL_SIMT forces the CUDA-core kernel, GDN_CHECK_INPUTS as above, but for
+ * g = -inf, which is valid here.
  */
 size_t gdn_linear_prefill_workspace_size(const int32_t *cu_seqlens_host, int32_t N, int64_t T,
                                          int32_t Hk, int32_t Hv, int32_t D, int32_t dtype,

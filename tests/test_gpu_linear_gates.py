@@ -160,3 +160,25 @@ def test_prefill_value_not_finite_with_the_state_in_place(lens, j):
     assert_bits_equal(o1, o2, "o with the state in place")
     assert_bits_equal(h1, state, "state in place")
     assert bool(o2.isnan().any()) and int(h2.isnan().sum()) == 128
+
+
+def test_debug_checks_take_cleared_states(monkeypatch):
+    """g = -inf clears a state: a valid gate, with and without the debug checks."""
+    d = make(36, [9], 2, 4, 128, torch.bfloat16)
+    d["g"][3, 1] = d["g"][0, 0] = -float("inf")
+    o1, h1 = call(d)
+    dec = [d[x][:1].cuda() for x in "qkvg"]
+    state = torch.ones(1, 4, 128, 128, device="cuda")
+    monkeypatch.setenv("GDN_DEBUG", "1")
+    o2, h2 = call(d)
+    assert_bits_equal(o1, o2, "o")
+    assert_bits_equal(h1, h2, "state")
+    gdn.gdn_linear_decode(*dec, state)
+    for bad in (float("inf"), float("nan")):
+        d["g"][3, 1] = bad
+        with pytest.raises(gdn.GdnError) as e:
+            call(d)
+        assert e.value.code == 11
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.gdn_linear_decode(*dec[:3], torch.full((4,), bad, device="cuda"), state)
+        assert e.value.code == 11
