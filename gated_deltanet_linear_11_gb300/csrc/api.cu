@@ -5,7 +5,7 @@
 #include <string.h>
 
 #include <cmath>
-#include <vector>
+#include <initializer_list>
 
 #include "common.cuh"
 #include "kv_format.cuh"
@@ -64,32 +64,38 @@ gdn_status_t view_of(const gdn_tensor_t *t, View &out) {
     return GDN_OK;
 }
 
-// GDN_CHECK_INPUTS: n floats at each of two device arrays, copied to the host in order on
-// `st` (waiting for it), must all be finite.
-gdn_status_t check_finite(const float *a, const float *b, size_t n, cudaStream_t st) {
-    if (n == 0) return GDN_OK;
-    std::vector<float> h(n);
-    for (const float *src : {a, b}) {
-        if (cudaMemcpyAsync(h.data(), src, n * sizeof(float), cudaMemcpyDeviceToHost, st) !=
-                cudaSuccess ||
+// For the checks of GDN_CHECK_INPUTS: n words of device memory, copied to the host in order on
+// `st` (waiting for it), must all satisfy good(word, index).  Through a buffer on the stack:
+// nothing here can throw out of a C entry.
+template <typename T, typename F>
+gdn_status_t check_words(const T *dev, size_t n, gdn_status_t bad, cudaStream_t st, F good) {
+    T h[4096];
+    for (size_t at = 0; at < n; at += 4096) {
+        const size_t m = n - at < 4096 ? n - at : 4096;
+        if (cudaMemcpyAsync(h, dev + at, m * sizeof(T), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
             cudaStreamSynchronize(st) != cudaSuccess)
             return GDN_ERR_CUDA;
-        for (size_t i = 0; i < n; ++i)
-            if (!std::isfinite(h[i])) return GDN_ERR_NONFINITE;
+        for (size_t i = 0; i < m; ++i)
+            if (!good(h[i], at + i)) return bad;
     }
     return GDN_OK;
 }
 
-// GDN_CHECK_INPUTS: the device offsets, copied back on `st` (waiting for it), must equal
-// the host copy that was validated.
+// GDN_CHECK_INPUTS: n floats at each of two device arrays must all be finite.
+gdn_status_t check_finite(const float *a, const float *b, size_t n, cudaStream_t st) {
+    for (const float *src : {a, b}) {
+        const gdn_status_t s = check_words(src, n, GDN_ERR_NONFINITE, st,
+                                           [](float x, size_t) { return std::isfinite(x); });
+        if (s != GDN_OK) return s;
+    }
+    return GDN_OK;
+}
+
+// GDN_CHECK_INPUTS: the device offsets must equal the host copy that was validated.
 gdn_status_t check_seqlens_copy(const int32_t *cu_dev, const int32_t *cu_host, int32_t N,
                                 cudaStream_t st) {
-    std::vector<int32_t> h((size_t)N + 1);
-    if (cudaMemcpyAsync(h.data(), cu_dev, h.size() * sizeof(int32_t), cudaMemcpyDeviceToHost,
-                        st) != cudaSuccess ||
-        cudaStreamSynchronize(st) != cudaSuccess)
-        return GDN_ERR_CUDA;
-    return memcmp(h.data(), cu_host, h.size() * sizeof(int32_t)) == 0 ? GDN_OK : GDN_ERR_SEQLENS;
+    return check_words(cu_dev, (size_t)N + 1, GDN_ERR_SEQLENS, st,
+                       [cu_host](int32_t x, size_t i) { return x == cu_host[i]; });
 }
 
 gdn_status_t check_seqlens(const int32_t *cu, int32_t N, int64_t T, int32_t *max_len) {
@@ -538,14 +544,8 @@ gdn_status_t linear_args(const gdn_tensor_t *q, const gdn_tensor_t *k, const gdn
 
 // GDN_CHECK_INPUTS: no log decay is NaN or +inf (-inf clears the state).
 gdn_status_t check_decays(const gdn_host::LinearArgs &a, cudaStream_t st) {
-    std::vector<float> h(a.g_tok ? (size_t)a.T * a.Hv : (size_t)a.Hv);
-    if (cudaMemcpyAsync(h.data(), a.g, h.size() * sizeof(float), cudaMemcpyDeviceToHost, st) !=
-            cudaSuccess ||
-        cudaStreamSynchronize(st) != cudaSuccess)
-        return GDN_ERR_CUDA;
-    for (float g : h)
-        if (!std::isfinite(g) && !(g < 0.f)) return GDN_ERR_NONFINITE;
-    return GDN_OK;
+    return check_words(a.g, a.g_tok ? (size_t)a.T * a.Hv : (size_t)a.Hv, GDN_ERR_NONFINITE, st,
+                       [](float g, size_t) { return std::isfinite(g) || g < 0.f; });
 }
 
 // The cache's own fields, and the new tokens' offsets (cu_host may be NULL: one each).

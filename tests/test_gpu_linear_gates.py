@@ -182,3 +182,25 @@ def test_debug_checks_take_cleared_states(monkeypatch):
         with pytest.raises(gdn.GdnError) as e:
             gdn.gdn_linear_decode(*dec[:3], torch.full((4,), bad, device="cuda"), state)
         assert e.value.code == 11
+
+
+def test_debug_checks_reach_the_last_word(monkeypatch):
+    """More gates and more offsets than one step of the checks copies."""
+    T, N = 6000, 5000
+    d = make(38, [2] * 1000 + [1] * 4000, 1, 2, 16, torch.float32)
+    dev = {x: d[x].cuda() for x in ("q", "k", "v", "g", "cu")}
+    monkeypatch.setenv("GDN_DEBUG", "1")
+
+    def prefill():
+        return gdn.gdn_linear_prefill(dev["q"], dev["k"], dev["v"], dev["g"], dev["cu"],
+                                      cu_seqlens_host=d["cu"])
+    assert prefill()[0].shape[0] == T and d["cu"].numel() == N + 1
+    dev["cu"][N - 1] -= 1
+    with pytest.raises(gdn.GdnError) as e:
+        prefill()
+    assert e.value.code == 5
+    dev["cu"][N - 1] += 1
+    dev["g"][T - 1, 1] = float("nan")
+    with pytest.raises(gdn.GdnError) as e:
+        prefill()
+    assert e.value.code == 11
