@@ -108,8 +108,16 @@ def _need_cuda(*ts):
             raise ValueError("tensor must live on a CUDA device")
 
 
+def _same_offsets(cu_seqlens, cu_seqlens_host):
+    """The kernels read as many device offsets as the host copy has."""
+    if cu_seqlens_host is not None and cu_seqlens.numel() < cu_seqlens_host.numel():
+        raise ValueError("cu_seqlens has %d entries and cu_seqlens_host %d"
+                         % (cu_seqlens.numel(), cu_seqlens_host.numel()))
+
+
 def _seqlens(cu_seqlens, cu_seqlens_host):
     """Device and host int32 copies of the offsets (a host copy avoids a sync)."""
+    _same_offsets(cu_seqlens, cu_seqlens_host)
     if cu_seqlens_host is None:
         cu_seqlens_host = cu_seqlens.detach().to("cpu", torch.int32).contiguous()
     else:
@@ -461,6 +469,7 @@ def _offsets(cu_seqlens, cu_seqlens_host):
             cu_seqlens.dtype is torch.int32 and cu_seqlens.is_cuda and \
             cu_seqlens.is_contiguous() and cu_seqlens_host.is_contiguous() and \
             not cu_seqlens_host.is_cuda:
+        _same_offsets(cu_seqlens, cu_seqlens_host)
         return cu_seqlens, cu_seqlens_host
     return _seqlens(cu_seqlens, cu_seqlens_host)
 

@@ -3,7 +3,9 @@ import shutil
 import subprocess
 
 import pytest
+import torch
 
+import gated_deltanet_linear_11_gb300 as gdn
 from gated_deltanet_linear_11_gb300 import build
 
 
@@ -15,3 +17,21 @@ def test_no_allocation_that_throws():
     names = {line.split()[-1].split("@")[0] for line in out.stdout.splitlines() if line.split()}
     assert not names & {"_Znwm", "_Znam", "_ZSt17__throw_bad_allocv",
                         "_ZSt20__throw_length_errorPKc", "__cxa_throw"}
+
+
+class _OnDevice(torch.Tensor):
+    """A host tensor that says it lives on a GPU."""
+    is_cuda = True
+
+
+def test_too_few_device_offsets_are_refused():
+    """The kernels index the device offsets by the host copy's count."""
+    host = torch.tensor([0, 3, 5, 9], dtype=torch.int32)
+    for n in (1, 3):
+        short = host[:n].clone().as_subclass(_OnDevice)
+        for pair in (gdn._offsets, gdn._seqlens):
+            with pytest.raises(ValueError, match="%d entries and cu_seqlens_host 4" % n):
+                pair(short, host)
+    for more in (0, 2):                # a longer device tensor does no harm
+        dev = torch.cat((host, host[:more])).as_subclass(_OnDevice)
+        assert gdn._offsets(dev, host)[0] is dev and gdn._offsets(dev, host)[1] is host
