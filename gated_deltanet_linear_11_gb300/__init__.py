@@ -37,6 +37,8 @@ Two environment variables serve debugging and callers' failure tests, read at ea
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 
 import torch
@@ -103,9 +105,30 @@ def _forced(name):
 
 
 def _need_cuda(*ts):
+    device = ts[0].get_device()              # -1 on the host
     for t in ts:
-        if t is not None and not t.is_cuda:
-            raise ValueError("tensor must live on a CUDA device")
+        if t is not None and (t.get_device() != device or device < 0):
+            raise ValueError("tensor must live on a CUDA device" if not t.is_cuda or device < 0
+                             else "tensors live on different devices")
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _on_device(fn):
+    """Entries that launch: run with the device of the first tensor as the current one, since
+    the C side launches on the current device and the stream is that device's."""
+    first = next(iter(inspect.signature(fn).parameters))
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        t = args[0] if args else kw.get(first)
+        d = -1 if t is None else t.get_device()
+        if d < 0 or d == _current_device():
+            return fn(*args, **kw)
+        with torch.cuda.device(d):
+            return fn(*args, **kw)
+    return call
 
 
 def _same_offsets(cu_seqlens, cu_seqlens_host):
@@ -128,6 +151,7 @@ def _seqlens(cu_seqlens, cu_seqlens_host):
     return cu_seqlens, cu_seqlens_host
 
 
+@_on_device
 def gdn_conv1d_fwd(x, w, bias, cu_seqlens, conv_state_in=None, conv_state_out=None,
                    y=None, cu_seqlens_host=None):
     """y = silu(conv1d(cat(conv_state, x_seq))) per sequence; returns (y, conv_state_out).
@@ -153,6 +177,7 @@ def gdn_conv1d_fwd(x, w, bias, cu_seqlens, conv_state_in=None, conv_state_out=No
     return y, conv_state_out
 
 
+@_on_device
 def gdn_conv1d_update(x, w, bias, conv_state, state_idx=None, y=None, status=None):
     """One-token conv step; conv_state [P, 3, C] is shifted in place.  Returns y [N, C]."""
     _forced("gdn_conv1d_update")
@@ -183,6 +208,7 @@ def _tile_flag(tiles):
     return GDN_PREFILL_TILES2 if tiles == 2 else GDN_PREFILL_TILES3
 
 
+@_on_device
 def gdn_chunk_prefill(q, k, v, g, beta, cu_seqlens, chunk=64, scale=1.0, l2norm=False,
                       initial_state=None, output_final_state=True, o=None,
                       final_state=None, simt=False, cu_seqlens_host=None, workspace=None,
@@ -243,6 +269,7 @@ def gdn_chunk_prefill_cp_range_hint(seq_len, Hv, sm_count=None):
     return int(lib.gdn_chunk_prefill_cp_range_hint_for(int(seq_len), int(Hv), int(sm_count)))
 
 
+@_on_device
 def gdn_chunk_prefill_cp(q, k, v, g, beta, cu_seqlens, range_chunks, chunk=64, scale=1.0,
                          l2norm=False, initial_state=None, output_final_state=True, o=None,
                          final_state=None, cu_seqlens_host=None, workspace=None, status=None,
@@ -276,6 +303,7 @@ def gdn_chunk_prefill_cp(q, k, v, g, beta, cu_seqlens, range_chunks, chunk=64, s
     return o, final_state
 
 
+@_on_device
 def gdn_chunk_prefill_noalloc(q, k, v, g, beta, cu_seqlens, chunk=64, scale=1.0,
                               l2norm=False, initial_state=None, output_final_state=True,
                               o=None, final_state=None, simt=False, cu_seqlens_host=None,
@@ -308,6 +336,7 @@ def gdn_chunk_prefill_noalloc(q, k, v, g, beta, cu_seqlens, chunk=64, scale=1.0,
     return o, final_state
 
 
+@_on_device
 def gdn_recurrent_decode(q, k, v, g, beta, state, state_idx=None, scale=1.0, l2norm=False,
                          o=None, status=None):
     """One token per sequence; state [P, Hv, dk, dv] fp32 updated in place.  Returns o."""
@@ -326,6 +355,7 @@ def gdn_recurrent_decode(q, k, v, g, beta, state, state_idx=None, scale=1.0, l2n
     return o
 
 
+@_on_device
 def gdn_fused_decode(x_qkv, conv_w, conv_bias, a_raw, b_raw, conv_state, state, Hk, Hv, dk,
                      dv, state_idx=None, scale=1.0, l2norm=True, o=None, status=None):
     """The whole one-token decode step in one call: conv update (conv_state shifted in
@@ -360,6 +390,7 @@ def split_qkv(y, Hk, Hv, dk, dv):
     return q, k, v
 
 
+@_on_device
 def gdn_layer_prefill(x_qkv, conv_w, conv_bias, g, beta, cu_seqlens, Hk, Hv, dk, dv,
                       conv_state_in=None, conv_state_out=None, initial_state=None,
                       final_state=None, scale=1.0, chunk=64, l2norm=True, y=None, o=None,
@@ -413,6 +444,7 @@ def gdn_layer_prefill(x_qkv, conv_w, conv_bias, g, beta, cu_seqlens, Hk, Hv, dk,
     return o, final_state, conv_state_out
 
 
+@_on_device
 def gdn_layer_decode(x_qkv, conv_w, conv_bias, g, beta, conv_state, state, Hk, Hv, dk, dv,
                      state_idx=None, scale=1.0, l2norm=True, y=None, o=None, status=None):
     """One-token layer step: conv update, then the recurrent step (states in place)."""
@@ -513,6 +545,7 @@ def gdn_linear_prefill_workspace_size(cu_seqlens_host, T, Hk, Hv, D, dtype=torch
         GDN_PREFILL_SIMT if simt else 0))
 
 
+@_on_device
 def gdn_linear_prefill(q, k, v, g, cu_seqlens, scale=1.0, initial_state=None,
                        output_final_state=True, o=None, final_state=None, simt=False,
                        cu_seqlens_host=None, workspace=None, status=None):
@@ -549,6 +582,7 @@ def gdn_linear_prefill(q, k, v, g, cu_seqlens, scale=1.0, initial_state=None,
     return o, final_state
 
 
+@_on_device
 def gdn_linear_decode(q, k, v, g, state, state_idx=None, scale=1.0, o=None, status=None):
     """One token per sequence of gdn_linear_prefill's recurrence; state [P, Hv, D, D] fp32
     updated in place.  g [Hv] or [N, Hv].  Returns o."""
@@ -609,6 +643,7 @@ def _kv_offsets(cu_seqlens, cu_seqlens_host, T, N):
     return cu, cu_h
 
 
+@_on_device
 def gdn_kv_append(k, v, cache, block_table, kv_lens, cu_seqlens=None, cos=None, sin=None,
                   q=None, q_out=None, interleaved=False, cu_seqlens_host=None, status=None):
     """Store new tokens' keys (rotated) and values in a paged 4-bit cache; with ``q``,
@@ -646,6 +681,7 @@ def gdn_kv_append(k, v, cache, block_table, kv_lens, cu_seqlens=None, cos=None, 
     return q_out
 
 
+@_on_device
 def gdn_kv_read(cache, block_table, kv_lens, cu_seqlens=None, head_dim=128,
                 dtype=torch.bfloat16, k=None, v=None, cu_seqlens_host=None, status=None):
     """The last tokens' keys and values (as many per sequence as cu_seqlens says; None:
@@ -674,6 +710,7 @@ def gdn_kv_attention_workspace_size(head_dim, Hq, Hkv, T, N, max_q_len, max_kv_l
         GDN_PREFILL_SIMT if simt else 0))
 
 
+@_on_device
 def gdn_kv_attention(q, cache, block_table, kv_lens, cu_seqlens=None, max_kv_len=None,
                      scale=None, o=None, lse=None, simt=False, cu_seqlens_host=None,
                      workspace=None, status=None):

@@ -35,3 +35,55 @@ def test_too_few_device_offsets_are_refused():
     for more in (0, 2):                # a longer device tensor does no harm
         dev = torch.cat((host, host[:more])).as_subclass(_OnDevice)
         assert gdn._offsets(dev, host)[0] is dev and gdn._offsets(dev, host)[1] is host
+
+
+def on(device):
+    class Fake(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return device
+    return torch.zeros(2).as_subclass(Fake)
+
+
+def test_entries_run_on_the_device_of_their_tensors(monkeypatch):
+    """The C side launches on the current device: a call whose tensors live on another one makes
+    that current for as long as it runs."""
+    now = [0]
+
+    class Device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            self.was, now[0] = now[0], self.d
+
+        def __exit__(self, *exc):
+            now[0] = self.was
+    monkeypatch.setattr(gdn, "_current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+
+    @gdn._on_device
+    def entry(q, fail=False):
+        if fail:
+            raise ValueError
+        return now[0]
+    assert entry(on(0)) == 0 and entry(on(1)) == 1 and entry(q=on(2)) == 2 and now[0] == 0
+    with pytest.raises(ValueError):
+        entry(on(1), fail=True)
+    assert now[0] == 0
+    launching = [n for n in gdn.__all__ if n.startswith("gdn_") and not n.endswith(
+        ("_size", "_hint", "gdn_kv_cache"))]
+    assert len(launching) == 14
+    for name in launching:
+        assert hasattr(getattr(gdn, name), "__wrapped__"), name
+
+
+def test_tensors_of_different_devices_are_refused():
+    gdn._need_cuda(on(1), None, on(1))
+    with pytest.raises(ValueError, match="different devices"):
+        gdn._need_cuda(on(1), None, on(0))
+    with pytest.raises(ValueError, match="CUDA device"):
+        gdn._need_cuda(on(0), torch.zeros(1))
+    with pytest.raises(ValueError, match="CUDA device"):
+        gdn._need_cuda(torch.zeros(1), None)
