@@ -966,13 +966,18 @@ kv_attention_join_kernel(KvView kv, bf16 *__restrict__ o, float *__restrict__ ls
     const int n = kv.cu ? sequence_of(kv.cu, kv.N, (int)t) : (int)t;
     const int t0 = kv.cu ? kv.cu[n] : n, m = kv.cu ? kv.cu[n + 1] - t0 : 1;
     const int len = kv.kv_lens[n];
-    if (len < 0 || len > max_kv_len || len > kv.capacity() || Hq * m >= tc_rows) return;
+    const bool ours = len >= 0 && len <= max_kv_len && len <= kv.capacity() && Hq * m < tc_rows;
     const int G = Hq / kv.Hkv, rows = G * m, row = (int)(t - t0) * G + hq % G;
     const int last = min((row / tile_rows + 1) * tile_rows, rows) - 1;
     const int see_last = len - m + last / G + 1;
-    const int split_len = kv_split_len(len, m, G, kv.Hkv, D, room_one);
-    const int splits = splits_of(see_last, split_len);
-    if (splits <= 1) return;
+    const int split_len = ours ? kv_split_len(len, m, G, kv.Hkv, D, room_one) : 0;
+    const int splits = ours ? splits_of(see_last, split_len) : 0;
+    if (splits <= 1) {
+        // a grid that has nothing to join must not end before the kernel whose rows are final
+        // already: what comes next in the stream waits for this one only
+        grid_dependency_wait();
+        return;
+    }
     const int64_t at = n * slab + ((t - t0) * Hq + hq) * splits_of(len, split_len);
     const float2 *ml = part_ml + at;
     grid_dependency_wait();

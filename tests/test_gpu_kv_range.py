@@ -167,3 +167,19 @@ def test_attention_reports_every_bad_page(D, Hq, ms, simt, page):
         o, _ = run_attention(bad, simt=simt, status=status)
         assert int(status) == (10 if at <= last else 0), (at, int(status))
         assert bool(o.isfinite().all())
+
+
+def test_attention_with_nothing_to_join():
+    """Short sequences under a bound that allows splits: the join has no row of its own, and what
+    comes next in the stream sees the outputs."""
+    c = attention_case(49, 128, 8, 2, 16, [1] * 40, [100] * 40)
+    want, _ = run_attention(c, max_kv_len=100)
+    q, cache, table, lens = c["q"].cuda(), torch.from_numpy(c["cache"]).cuda(), \
+        torch.from_numpy(c["table"]).cuda(), torch.from_numpy(c["lens"]).cuda()
+    o, got = torch.empty_like(want), []
+    for _ in range(50):
+        o.fill_(float("nan"))
+        gdn.gdn_kv_attention(q, cache, table, lens, max_kv_len=100000, o=o)
+        got.append(o.clone())
+    for x in got:
+        assert_bits_equal(x, want, "a copy of the outputs")
