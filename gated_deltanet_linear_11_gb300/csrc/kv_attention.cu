@@ -776,6 +776,8 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
                     if (j < len - m + (row0 + y) / G + 1) atomicOr(snan + y, 1u << g);
             if (bad || !in) par[g] = 0u;
         }
+        // the next copy into this buffer is the async proxy's, and comes after these writes
+        tc::fence_async_smem();
         __syncwarp();
     };
 
