@@ -204,3 +204,24 @@ def test_debug_checks_reach_the_last_word(monkeypatch):
     with pytest.raises(gdn.GdnError) as e:
         prefill()
     assert e.value.code == 11
+
+
+@pytest.mark.parametrize("lens,Hv", [([500], 2), ([2500, 1600], 2), ([4096], 48)])
+@pytest.mark.parametrize("slow", [True, False])
+def test_prefill_state_accuracy(lens, Hv, slow):
+    """Final states of the tensor-core form, whole and in ranges, by norm: keys as three bf16
+    terms leave 2^-24 of a product, the sums of 128 products in fp32 and one rounding a chunk
+    some more, together under 1.2e-6; with two terms the state is off by 3e-6."""
+    d = make(35, lens, 1, Hv, 128, torch.bfloat16, True, True, slow=slow)
+    if Hv > 2:                             # the same heads again: the 64-bit form is slow
+        for x in ("v", "g"):
+            d[x] = d[x][:, :2].repeat(*([1, Hv // 2] + [1] * (d[x].dim() - 2)))
+        d["h0"] = d["h0"][:, :2].repeat(1, Hv // 2, 1, 1)
+    _, h = call(d)
+    _, rh, _, _ = ref.linear_scan(np64(d["q"]), np64(d["k"]), np64(d["v"][:, :2]),
+                                  np64(d["g"][:, :2]),
+                                  np.concatenate(([0], np.cumsum(lens))).tolist(),
+                                  np64(d["h0"][:, :2]))
+    for i in range(Hv):
+        err = np.linalg.norm(np64(h[:, i]) - rh[:, i % 2]) / np.linalg.norm(rh[:, i % 2])
+        assert err <= 1.2e-6, (i, err)
