@@ -580,6 +580,7 @@ gdn_status_t kv_args(const gdn_kv_cache_t *c, const int32_t *cu_dev, const int32
     a.kv.table = c->block_table;
     a.kv.kv_lens = c->kv_lens;
     a.kv.cu = cu_dev;
+    a.cu_host = cu_host;
     a.kv.pages = c->pages;
     a.kv.page_log2 = 0;
     while ((1 << a.kv.page_log2) < c->page_size) ++a.kv.page_log2;

@@ -1159,10 +1159,16 @@ gdn_status_t launch_kv_attention(const KvArgs &a, cudaStream_t st) {
     const int64_t tiles = (rows + 8 * nt - 1) / (8 * nt);
     const int splits = attn_max_splits(a.max_kv_len, a.min_q_len, a.Hq / a.kv.Hkv, a.kv.Hkv, a.D);
     if (tiles * splits > 0x7fffffff || a.kv.N > 65535) return GDN_ERR_SHAPE;
-    // (over all m between these two: room falls as m grows, but for the step in split_ctas)
+    // the longest run of keys: of the most new rows that are there for this kernel, or the least
+    // (room falls as m grows, but for the step in split_ctas)
     const int G = a.Hq / a.kv.Hkv;
+    int m_there = a.min_q_len;
+    for (int n = 0; a.kv.cu && n < a.kv.N; ++n) {
+        const int m = a.cu_host[n + 1] - a.cu_host[n];
+        if ((int64_t)a.Hq * m < tc_rows) m_there = std::max(m_there, m);
+    }
     const int longest = std::max(attn_longest(a.max_kv_len, a.min_q_len, G, a.kv.Hkv, a.D),
-                                 attn_longest(a.max_kv_len, (int)m_most, G, a.kv.Hkv, a.D));
+                                 attn_longest(a.max_kv_len, m_there, G, a.kv.Hkv, a.D));
     switch (a.D * 10 + nt) {
     case 641: return mma_launch<64, 1>(a, (int)tiles, splits, tc_rows, longest, st);
     case 642: return mma_launch<64, 2>(a, (int)tiles, splits, tc_rows, longest, st);

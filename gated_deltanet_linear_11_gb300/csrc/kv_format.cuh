@@ -82,6 +82,7 @@ struct KvArgs {
     int32_t tab_rows, rot, interleaved;
     float *lse;
     int64_t T;
+    const int32_t *cu_host;   // the host copy of kv.cu
     int32_t D, Hq, max_q_len, min_q_len, max_kv_len;   // min_q_len: over sequences with rows
     float scale;
     uint32_t flags;
