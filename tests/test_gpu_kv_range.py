@@ -183,3 +183,10 @@ def test_attention_with_nothing_to_join():
         got.append(o.clone())
     for x in got:
         assert_bits_equal(x, want, "a copy of the outputs")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("f", [2.0 ** -11, 2.0 ** 10])
+def test_attention_many_rows_values_of_any_scale(D, f):
+    c = attention_case(50, D, 32, 8, 16, [170], [300])
+    check_attention(c, *run_attention(scale_records(c, 1, f)))
