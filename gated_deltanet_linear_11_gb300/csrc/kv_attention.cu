@@ -152,23 +152,26 @@ kv_attention_simt_kernel(KvView kv, const T *__restrict__ q, T *__restrict__ o, 
 // Fewer bits than fp32: q is scaled by a power of two per row so that its largest element
 // lies in [2^11, 2^12), where fp16 holds a bf16 exactly (down to 2^-26 of the largest);
 // p is rounded to fp16 (2^-11); it is taken against a reference within 2 (in powers of two)
-// of the running maximum and lifted by 2^13, so it stays below 2^15 and a weight of 2^-37 of
+// of the running maximum and lifted by 2^8, so it stays below 2^10 and a weight of 2^-32 of
 // the largest is still held.  p scale goes in as an fp16 pair (product and what its rounding
 // left out): scale * code and minimum cancel to a value several times smaller than either, so
-// one fp16 product would show where few keys carry a row.  Scales of 2 and more lower the lift,
-// down to 1 for the largest there are, so that the product stays in the fp16 range.  (Without
-// the lift, values of 2^-11 their usual size left outputs 30 times their bound off, and a key
-// that outweighs each of 12000 others by 2^18 four times.)  Scores, sums, maxima and outputs
-// are fp32.
+// one fp16 product would show where few keys carry a row.  (Without the lift, values of 2^-11
+// their usual size left outputs 30 times their bound off, and a key that outweighs each of
+// 12000 others by 2^18 four times.)  Scores, sums, maxima and outputs are fp32.
+//
+// Scales from 64 on (groups of values that span 960) may carry p scale past fp16.  Then sums
+// are not finite, and a CTA that ends with one takes its keys once more, with a lift that
+// follows the scales.  (64 sequences of up to 16384 keys 180 us, 178.5 without lift and end
+// check, 183 where every pass looks at its scales.)
 //
 // Keys come in blocks of 16 records of a page (pages hold a multiple of 16) by bulk copies
 // into a ring that each warp runs for itself: no barrier of the CTA inside the loop, but
 // where warps share the blocks.
 //
-// 64 sequences of up to 16384 keys, 32 query heads over 8 of 128, take 179 us: 640 MB, 53% of
+// 64 sequences of up to 16384 keys, 32 query heads over 8 of 128, take 180 us: 640 MB, 52% of
 // the HBM rate, bound by issue (59%): a block of 32 keys costs a warp 880 instructions, start
 // and join of eight such blocks included.  24 rows of 256 elements over 131072 keys of 4 heads
-// take 101 us, 24% of the HBM rate, bound by latency at twelve warps an SM.
+// take 102 us, 24% of the HBM rate, bound by latency at twelve warps an SM.
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 
@@ -194,7 +197,7 @@ template <int D, int NT> struct AttnShape {
     static constexpr int QF = NT * R::NG * 32 * 16;             // q fragments
     static constexpr int QM = NT * 32 * 8;                      // group sums of q
     static constexpr int SWAP = VS > 1 ? kAttnWarps * (NT * 256 + ROWS * 4 + 16) : 0;   // weights, maxima, flag
-    static constexpr int TAIL = SWAP + ROWS * (4 + 4) + kAttnWarps * ROWS * 8 + 8 * 4 * kAttnWarps + 4 * 4 * kAttnWarps;
+    static constexpr int TAIL = SWAP + ROWS * (4 + 4) + kAttnWarps * ROWS * 8 + 2 * 8 * 4 * kAttnWarps + 4 * 4 * kAttnWarps;
     static constexpr int SMEM = BUF + QF + QM + TAIL;
     // CTAs per SM: latency is what more of them hide, until registers spill (64 sequences of
     // up to 16384 keys, D NT = 128: 173 us with four, 192 with three, 191 with five)
@@ -296,21 +299,40 @@ __device__ __forceinline__ bool half_pair_nonfinite(uint32_t w) {
     return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
 }
 
-// Weights are held at 2^lift times their size, below 2^15 with the reference's slack of 2.  With
-// a lift of 13 - k the scales may be up to 1.984 * 2^k.
-constexpr int kStowKeys = 2048;
-constexpr float kMmaLift = 13.f;
+// Weights are held at 2^lift times their size, below 2^(lift + 2) with the reference's slack.
+// With a lift of 13 - k the scales may be up to 1.984 * 2^k; k is 5 where no pass has to be careful.
+constexpr int kLeastK = 5;
 constexpr uint32_t kTopScale = 0x3ff0u, kHalfExp = 0x0400u;     // fp16 bits
+// Keys of a warp after which sums of long runs are stowed.
+constexpr int kStowKeys = 2048;
 
 constexpr uint32_t kNib0 = 0x000F000Fu, kNib1 = 0x00F000F0u;
 
-template <int D, int NT, bool LONG>
-__global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::CTAS)
-kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict__ o,
-                        float *__restrict__ lse, float *__restrict__ part_o,
-                        float2 *__restrict__ part_ml, int64_t q_tok, int64_t o_tok, int Hq,
-                        int row_tiles, int64_t slab, int tc_rows, int room_one, int max_kv_len,
-                        float scale, int32_t *status) {
+struct AttnParams {
+    KvView kv;
+    const bf16 *q;
+    bf16 *o;
+    float *lse, *part_o;
+    float2 *part_ml;
+    int64_t q_tok, o_tok, slab;
+    int Hq, row_tiles, tc_rows, room_one, max_kv_len;
+    float scale;
+    int32_t *status;
+};
+
+// A CTA's pass over its keys.  CAREFUL: every block's scales are looked at before its products,
+// and the lift fits them; otherwise true where some sum is not finite, with nothing written.
+template <int D, int NT, bool LONG, bool CAREFUL>
+__device__ __forceinline__ bool attention_pass(const AttnParams &a) {
+    const KvView &kv = a.kv;
+    const bf16 *__restrict__ q = a.q;
+    bf16 *__restrict__ o = a.o;
+    float *__restrict__ lse = a.lse, *__restrict__ part_o = a.part_o;
+    float2 *__restrict__ part_ml = a.part_ml;
+    const int64_t q_tok = a.q_tok, o_tok = a.o_tok, slab = a.slab;
+    const int Hq = a.Hq, row_tiles = a.row_tiles, tc_rows = a.tc_rows, room_one = a.room_one, max_kv_len = a.max_kv_len;
+    const float scale = a.scale;
+    int32_t *status = a.status;
     using R = KvRec<D>;
     using A = AttnShape<D, NT>;
     constexpr int NG = R::NG, NP = D / 64, REC = R::BYTES;
@@ -322,8 +344,9 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     float *sfac = reinterpret_cast<float *>(swap + A::SWAP);
     uint32_t *snan = reinterpret_cast<uint32_t *>(sfac + A::ROWS);
     float2 *sml = reinterpret_cast<float2 *>(snan + A::ROWS);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sml + kAttnWarps * A::ROWS);
-    uint32_t *spages = reinterpret_cast<uint32_t *>(bars + 4 * kAttnWarps);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sml + kAttnWarps * A::ROWS);   // a set for each pass
+    uint32_t *spages = reinterpret_cast<uint32_t *>(bars + 8 * kAttnWarps);
+    if (CAREFUL) bars += 4 * kAttnWarps;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const int split = blockIdx.x / row_tiles, rt = blockIdx.x % row_tiles;
@@ -331,17 +354,17 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     const int t0 = kv.cu ? kv.cu[n] : n, m = kv.cu ? kv.cu[n + 1] - t0 : 1;
     const int len = kv.kv_lens[n];
     const int G = Hq / kv.Hkv, rows = G * m, row0 = rt * A::ROWS;
-    if (row0 >= rows || Hq * m >= tc_rows) return;   // (tc_rows: the other kernel's sequences)
+    if (row0 >= rows || Hq * m >= tc_rows) return false;   // (tc_rows: the other kernel's sequences)
     if (len < 0 || len > max_kv_len || len > kv.capacity()) {
         if (tid == 0) report(status, GDN_ERR_SEQLENS);
-        return;
+        return false;
     }
     // keys seen by the tile's first and last row
     const int see_first = len - m + row0 / G + 1;
     const int see_last = len - m + (min(row0 + A::ROWS, rows) - 1) / G + 1;
     const int split_len = kv_split_len(len, m, G, kv.Hkv, D, room_one);
     const int splits = splits_of(see_last, split_len);   // 0: no key at all
-    if (split > 0 && split >= splits) return;            // (the grid is made for the most)
+    if (split > 0 && split >= splits) return false;      // (the grid is made for the most)
     const int k0 = split * split_len, k1 = see_last - k0 > split_len ? k0 + split_len : see_last;
 
     // ---- the warp's rings of keys and of values: block b holds keys k0 + 32 (slice + SLICES b) ..
@@ -399,7 +422,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
 
     // ---- q as fragments: lane (r, c) of a tile's warp holds elements 32 g + 8 c .. +7 of
     // row r, scaled; odd elements also by 1/16 (their codes come as u << 4)
-    for (int nt = warp; nt < NT; nt += kAttnWarps) {
+    for (int nt = warp; nt < NT && !CAREFUL; nt += kAttnWarps) {
         const int row = row0 + 8 * nt + r;
         float x[NG][8];
         float mx = 0.f;
@@ -573,8 +596,8 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     };
     volatile float held[LONG ? NT : 1][2 * NGV][4], held_at[LONG ? NT : 1][2];     // see stow(); local memory
     bool stowed = false;
-    float lift = kMmaLift;
-    uint32_t top_scale = kTopScale;
+    float lift = 13.f - kLeastK;
+    uint32_t top_scale = kTopScale + kLeastK * kHalfExp;
     uint32_t fresh = 0u;         // not 0: what a change of lift asks of the block's shared weights
     // The warps of a slice at one point (they take the same steps); false where one of them has
     // given up on a copy.
@@ -736,7 +759,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
     // 2^21 times as much as each of 12000 others left outputs of 256 elements 1.2 times their
     // bound off).  So every kStowKeys keys of a warp the sums move to fp32 words in local memory
     // and start again from zero.  LONG is for calls whose runs can be that long, which splits
-    // are not: without it 64 sequences of up to 16384 keys take 184 us, with it 195.
+    // are not: without it 64 sequences of up to 16384 keys take 180 us, with it 193.
     auto stow = [&](bool again) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -798,7 +821,7 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
             const uint32_t most = min(__reduce_max_sync(0xffffffffu, h), 0x7000u);     // 2^13 and more: k = 13
             const uint32_t k = min((most >> 10) - 14u, 13u);
             const float was = lift;
-            lift = kMmaLift - (float)k;
+            lift = 13.f - (float)k;
             top_scale = k == 13u ? 0x7fffu : kTopScale + k * kHalfExp;
             const float f = __int_as_float((127 + (int)(lift - was)) << 23);
             fresh = pack_half2(f, f);
@@ -836,30 +859,40 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
         if ((ok = agree(ok))) weigh(S, bm);
     }
     int b = 0;
-    for (; b < blocks && ok; ++b) {
-        const bool more = b + 1 < blocks;
-        if (more) fetch(b + 2 < blocks ? b + 2 : -1, b + 1);
-        uint8_t *sv = ring_v + (b & 1) * A::VALUES;
-        ok = __all_sync(0xffffffffu, wait_copy(bar_v + (b & 1), (b >> 1) & 1));
-        if (!is_full(b)) {
-            if (ok) clean(b, sv);
-            if (A::VS > 1) meet();               // each has cleaned its part (alike for all of them)
+    auto walk = [&](int stop) {
+        for (; b < stop && ok; ++b) {
+            const bool more = b + 1 < blocks;
+            if (more) fetch(b + 2 < blocks ? b + 2 : -1, b + 1);
+            uint8_t *sv = ring_v + (b & 1) * A::VALUES;
+            ok = __all_sync(0xffffffffu, wait_copy(bar_v + (b & 1), (b >> 1) & 1));
+            if (!is_full(b)) {
+                if (ok) clean(b, sv);
+                if (A::VS > 1) meet();               // each has cleaned its part (alike for all of them)
+            }
+            if (CAREFUL && ok) fit_scales(sv);
+            if (ok && more) ok = __all_sync(0xffffffffu, wait_copy(bar_k + ((b + 1) & 1), ((b + 1) >> 1) & 1));
+            float S[SUBS][NT][4], bm[NT][2];
+            if (ok) {
+                if (more) scores(ring_k + ((b + 1) & 1) * A::KEYS, S);
+                if (more && A::VS > 1) maxima(b + 1, S, bm);
+                values(sv);
+                fresh = 0u;
+                if (more && (b & (EVERY - 1)) == EVERY - 1) center();
+                if (more && A::VS == 1) maxima(b + 1, S, bm);
+                __syncwarp();          // the tiles read here are free for the next fetch
+            }
+            if (more && (ok = agree(ok))) weigh(S, bm);
+            if (!ok) break;
         }
-        if (ok) fit_scales(sv);
-        if (ok && more) ok = __all_sync(0xffffffffu, wait_copy(bar_k + ((b + 1) & 1), ((b + 1) >> 1) & 1));
-        float S[SUBS][NT][4], bm[NT][2];
-        if (ok) {
-            if (more) scores(ring_k + ((b + 1) & 1) * A::KEYS, S);
-            if (more && A::VS > 1) maxima(b + 1, S, bm);
-            values(sv);
-            fresh = 0u;
-            if (more && (b & (EVERY - 1)) == EVERY - 1) center();
-            if (LONG && more && (b & (STOW - 1)) == STOW - 1) stow(true);
-            if (more && A::VS == 1) maxima(b + 1, S, bm);
-            __syncwarp();          // the tiles read here are free for the next fetch
+    };
+    if (LONG) {
+#pragma unroll 1
+        while (b < blocks && ok) {
+            walk(min(blocks, b + STOW));
+            if (b < blocks && ok) stow(true);
         }
-        if (more && (ok = agree(ok))) weigh(S, bm);
-        if (!ok) break;
+    } else {
+        walk(blocks);
     }
     if (!ok) {
         // a copy never signalled: report, and let what is in flight land (bounded too)
@@ -870,6 +903,17 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
 
     center();
     if (LONG && stowed) stow(false);
+    bool again = false;
+    if (!CAREFUL) {
+        float zero = 0.f;                       // or NaN
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2 * NGV; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) zero = fmaf(O[nt][x][e], 0.f, zero);
+        again = zero != zero;
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -886,7 +930,9 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
             lrun[nt][e] = l;
             if (r == 0) sml[warp * A::ROWS + 8 * nt + 2 * c + e] = make_float2(mrun[nt][e], l);
         }
-    __syncthreads();     // every warp is done with its ring
+    // every warp is done with its ring
+    if (CAREFUL) __syncthreads();
+    else if (__syncthreads_or(again) && __syncthreads_and(ok)) return true;
     float *join = reinterpret_cast<float *>(smem);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -949,6 +995,17 @@ kv_attention_mma_kernel(KvView kv, const bf16 *__restrict__ q, bf16 *__restrict_
             if (lse && d4 == 0) lse[t * Hq + hq] = l == 0.f ? -INFINITY : (mall + log2f(l)) * 0.6931471805599453f;
         }
     }
+    return false;
+}
+// (a function of its own, so that the first pass is compiled without it)
+template <int D, int NT>
+__device__ __noinline__ void attention_careful(const AttnParams &a) {
+    attention_pass<D, NT, true, true>(a);
+}
+template <int D, int NT, bool LONG>
+__global__ void __launch_bounds__(kAttnThreads, AttnShape<D, NT>::CTAS)
+kv_attention_mma_kernel(const __grid_constant__ AttnParams a) {
+    if (attention_pass<D, NT, LONG, false>(a)) attention_careful<D, NT>(a);
 }
 
 // Joins the splits of a row: one CTA per row, warp w taking splits w, w + 4, ..., with
@@ -1122,9 +1179,9 @@ gdn_status_t mma_launch(const KvArgs &a, int row_tiles, int splits, int tc_rows,
     const int room = gdn::kv_split_room(1, a.Hq / a.kv.Hkv, a.kv.Hkv, D, gdn::split_ctas(a.Hq / a.kv.Hkv, D));
     float2 *ml = (float2 *)a.ws;
     float *po = slab ? (float *)((uint8_t *)a.ws + part_ml_bytes(slab * a.kv.N)) : nullptr;
-    kern<<<dim3((unsigned)((int64_t)splits * row_tiles), a.kv.Hkv, a.kv.N), gdn::kAttnThreads, A::SMEM, st>>>(
-        a.kv, (const gdn::bf16 *)a.q, (gdn::bf16 *)a.q_out, a.lse, po, ml, a.q_tok, a.o_tok, a.Hq,
-        row_tiles, slab, tc_rows, room, a.max_kv_len, a.scale, a.status);
+    const gdn::AttnParams p = {a.kv, (const gdn::bf16 *)a.q, (gdn::bf16 *)a.q_out, a.lse, po, ml, a.q_tok, a.o_tok,
+                               slab, a.Hq, row_tiles, tc_rows, room, a.max_kv_len, a.scale, a.status};
+    kern<<<dim3((unsigned)((int64_t)splits * row_tiles), a.kv.Hkv, a.kv.N), gdn::kAttnThreads, A::SMEM, st>>>(p);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
     if (splits > 1 &&
         launch_dependent(gdn::kv_attention_join_kernel<D>, dim3((unsigned)a.T, a.Hq), dim3(128), 0, st, a.kv,
