@@ -23,9 +23,10 @@
 // a clock), 2048 clocks of base-2 exponentials (16 a clock) and about 2600 instructions a
 // scheduler, and takes 5500: the scores of both row tiles, then the unpacking of the next
 // keys into the one buffer there is room for, form its chain, and the issue slots are half
-// taken.  Tried and slower: two buffers for hi with lo converted again (462 us where this
-// form takes 432), sixteen unpacking warps (482), two threads a row (486), a warp of
-// products for each row tile (543, their softmaxes fall together).
+// taken.  2048 rows of 32 heads on 8 over 10240 keys take 437 us.  Tried and slower: two
+// buffers for hi with lo converted again (462 us where this form took 432), sixteen unpacking
+// warps (482), two threads a row (486), a warp of products for each row tile (543, their
+// softmaxes fall together).
 //
 // Fewer bits than fp32: q is scaled by a power of two per row into [2^6, 2^7) and held in
 // fp16 (exact down to 2^-21 of the largest); a value is minimum + scale * code rounded once

@@ -5,7 +5,8 @@
 // pair (scale, minimum).  Element d of group d / 32 stands for minimum + scale * code.
 // Per group of x (clamped to +-65504, the fp16 range):
 //     minimum = fp16(min x),  scale = fp16((max x - minimum) / 15),
-//     code    = round((x - minimum) * (1 / scale)) in 0..15, ties to even; 0 if scale = 0.
+//     code    = round((x - minimum) * (1 / scale)) in 0..15, ties to even; 0 if scale <= 0
+//               (a minimum that rounded above a nearly constant group's maximum).
 // A group that holds a NaN gets minimum = NaN: all of it reads as NaN.
 //
 // The codes are stored in the order in which the attention's matrix fragments take them:

@@ -13,9 +13,9 @@
 // elements (a 16-byte load of bf16), four lanes share a group.  The token's place and its
 // angles are found once for all its heads, and rows of q skip the quantisation; with one row
 // per lane group and everything per row the kernel was bound by instruction issue (362 a
-// warp, 83 us for 8314 tokens of 32 + 2 x 8 heads of 128; 48 us now, 192 MB at 59% of the HBM
-// rate, issue slots 56% taken).  Reading the same rows back moves 55 MB in 12 us where the
-// cache is still in the L2, 25 from HBM.
+// warp, 83 us for 8314 tokens of 32 + 2 x 8 heads of 128; 47 us now, 185 MB at 58% of the HBM
+// rate, issue slots 59% taken).  Reading the same rows back as fp32 moves 79 MB in 22 us, 53%
+// of the HBM rate, bound by the latency of its loads.
 #include <algorithm>
 
 #include "kv_format.cuh"
@@ -250,7 +250,7 @@ namespace {
 // Parts a token's rows are cut into, so that a few tokens fill the device and many leave no
 // long last round: enough for 16000 warps in all (three rounds of what fits), at most one part
 // per row step.  Every part looks the place and the angles up again (8314 tokens written and
-// read back, from HBM: one part 73.5 us, two 69, four 69, six 82).
+// read back, from HBM: one part 73.5 us, two 69.2, four 69, six 82).
 int kv_parts(int64_t tokens, int steps) {
     const int64_t want = (16000 + tokens - 1) / tokens;
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, steps), 65535));

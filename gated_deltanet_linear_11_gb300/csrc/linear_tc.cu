@@ -37,8 +37,8 @@
 // leaves 3328 clocks of traffic and room for two buffers of each of Q, K and V.  TMEM (512
 // columns): scores / P and rest, Q S, P V / weighted keys, state.
 //
-// 4096 tokens of 16 k-heads and 48 v-heads take 68 us, 8 packed prompts of 27598 tokens 399:
-// 2.0 and 2.4 TB/s of what has to be moved, 188 and 218 TFLOP/s.  A chunk takes about 5700
+// 4096 tokens of 16 k-heads and 48 v-heads take 70 us, 8 packed prompts of 27598 tokens 405:
+// 2.0 and 2.4 TB/s of what has to be moved, 183 and 214 TFLOP/s.  A chunk takes about 5700
 // clocks, A 1500 (packing on the ALU pipe), B 1300, C 750, D 900 and the waits for products
 // between them; one CTA fills an SM's TMEM and shared memory, so nothing else hides them.
 //

@@ -367,8 +367,10 @@ gdn_status_t gdn_fused_decode(const void *x, int32_t N, int32_t Hk, int32_t Hv, 
  * v, o [T, Hv, D]; v-head h reads q/k head h / (Hv / Hk); states [.., Hv, D, D] fp32 with
  * element [i][j] multiplying k_i and v_j.  g holds log decays (fp32): [Hv], one per head,
  * when g_per_token is 0, else [T, Hv] (contiguous).  g = -inf clears the state; a NaN
- * makes its head's later outputs NaN.  D in {16, 32, 64, 128}; all four views bf16 or all
- * fp32; D = 128 in bf16 runs on the tensor cores.
+ * makes its head's later outputs NaN; a v that is not finite makes its column so from its
+ * token on (an infinity may come out as NaN).  Earlier tokens keep their values.
+ * D in {16, 32, 64, 128}; all four views bf16 or all fp32; D = 128 in bf16 runs on the
+ * tensor cores.
  */
 
 /*
@@ -415,8 +417,8 @@ gdn_status_t gdn_linear_decode(const gdn_tensor_t *q, const gdn_tensor_t *k,
  *     keys:   d = 32 (W mod G) + 8 (W div G) + i
  *     values: d = 64 (W div 8) + 32 (i div 4) + 4 (W mod 8) + (i mod 4).
  * Per group, x clamped to +-65504: minimum = fp16(min x), scale = fp16((max x - minimum)/15),
- * code = (x - minimum)/scale rounded to the nearest of 0..15 (ties to even).  A group with
- * a NaN is stored with minimum = NaN.
+ * code = (x - minimum)/scale rounded to the nearest of 0..15 (ties to even; 0 where the scale
+ * is not above 0).  A group with a NaN is stored with minimum = NaN.
  * block_table [N, table_width] int32 (device): position p of sequence n is slot
  * p mod page_size of page block_table[n][p div page_size].
  * kv_lens [N] int32 (device): tokens of each sequence, the new ones of the call included.
@@ -438,7 +440,7 @@ size_t gdn_kv_record_bytes(int32_t head_dim);
 
 /*
  * gdn_kv_append -- rotates the new tokens' k and stores k and v in the cache; with q,
- * also writes the rotated q to q_out (which must not be q).
+ * also writes the rotated q to q_out (which must not overlap q).
  * k, v [T, Hkv, D]; q, q_out [T, Hq, D] or both NULL; one element type.  cos_table,
  * sin_table fp32 [table_rows, rot / 2], 16-byte aligned, row = position, or both NULL (no
  * rotation); rot a multiple of 16, at most D: the first rot elements turn in pairs
