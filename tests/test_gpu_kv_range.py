@@ -190,3 +190,19 @@ def test_attention_with_nothing_to_join():
 def test_attention_many_rows_values_of_any_scale(D, f):
     c = attention_case(50, D, 32, 8, 16, [170], [300])
     check_attention(c, *run_attention(scale_records(c, 1, f)))
+
+
+@pytest.mark.parametrize("D,Hq", [(64, 2), (128, 2), (256, 2), (256, 12)])
+def test_attention_scales_that_grow_along_a_long_run(D, Hq):
+    """Sums that have been stowed before the first scales that the lift has no room for."""
+    c = attention_case(51, D, Hq, 1, 64, [258], [9000])
+    par = c["cache"][:, 1, :, :, D // 2:].copy()
+    with np.errstate(invalid="ignore"):
+        x = par.view(np.float16).astype(np.float32)
+    for i, f in ((70, 2.0 ** 8), (100, 2.0 ** 9), (120, 2.0 ** 12)):
+        x[c["table"][0, i]] *= f
+    x = np.clip(x, -65504, 65504).astype(np.float16)
+    c["cache"][:, 1, :, :, D // 2:] = x.view(np.uint8)
+    end = dict(c, q=c["q"][-4:], ms=[4])
+    o, lse = run_attention(c)
+    check_attention(end, o[-4:], lse[-4:])

@@ -225,3 +225,21 @@ def test_prefill_state_accuracy(lens, Hv, slow):
     for i in range(Hv):
         err = np.linalg.norm(np64(h[:, i]) - rh[:, i % 2]) / np.linalg.norm(rh[:, i % 2])
         assert err <= 1.2e-6, (i, err)
+
+
+def test_prefill_values_not_finite_in_long_ranges():
+    """Ranges of many chunks, some heads with such values and some without."""
+    T, Hv = 4096, 48
+    d = make(39, [T - 700, 700], 16, Hv, 128, torch.bfloat16, True, True, slow=True)
+    o1, h1 = call(d)
+    keep, keep_h = torch.ones(o1.shape, dtype=torch.bool), torch.ones(h1.shape, dtype=torch.bool)
+    for t, h, c in ((0, 3, 0), (1300, 3, 127), (1407, 20, 64), (3000, 47, 31), (3395, 11, 90),
+                    (3396, 12, 7), (4095, 5, 5)):
+        d["v"][t, h, c] = float("nan")
+        n, end = (0, T - 700) if t < T - 700 else (1, T)
+        keep[t:end, h, c] = False
+        keep_h[n, h, :, c] = False
+    o2, h2 = call(d)
+    assert_bits_equal(o1[keep], o2[keep], "outputs that no value reaches")
+    assert_bits_equal(h1[keep_h], h2[keep_h], "state columns that no value reaches")
+    assert bool(o2[~keep].isnan().all()) and bool(h2[~keep_h].isnan().all())
