@@ -16,6 +16,9 @@ in this package's CUDA kernels.  The functions keep the C entry points' names:
 * :func:`gdn_kv_append`, :func:`gdn_kv_read`, :func:`gdn_kv_attention` -- a paged
   key/value cache held in 4 bits: rotate and store, read back, attend
   (:func:`gdn_kv_cache` allocates one)
+* :func:`gdn_add_rmsnorm`, :func:`gdn_gated_rmsnorm`, :func:`gdn_quantize_rows` -- the norms
+  around the mixers, and rows in 8 bits with a scale each
+* :func:`gdn_matmul_i8` -- product of 8-bit integers with a scale for each token and channel
 
 plus :func:`gdn_layer_prefill` / :func:`gdn_layer_decode`, which chain the conv and the
 scan over the packed q||k||v channels (q, k, v are strided views of the conv output;
@@ -764,3 +767,8 @@ def gdn_selftest_bounded_wait(status=None):
     _lib.check(lib.gdn_selftest_bounded_wait(_vp(status), _stream()),
                "gdn_selftest_bounded_wait")
     return status
+
+
+# the entries around the mixers: they use the helpers above
+from .eight_bit import (gdn_add_rmsnorm, gdn_gated_rmsnorm, gdn_matmul_i8,  # noqa: E402,F401
+                        gdn_matmul_i8_workspace_size, gdn_quantize_rows)

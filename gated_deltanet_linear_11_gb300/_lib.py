@@ -10,7 +10,7 @@ import struct
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libgdn.so")
 
-GDN_BF16, GDN_F32, GDN_I32 = 0, 1, 2
+GDN_BF16, GDN_F32, GDN_I32, GDN_I8 = 0, 1, 2, 3
 GDN_QK_L2NORM = 0x1
 GDN_PREFILL_SIMT = 0x100
 GDN_PREFILL_TILES2 = 0x200
@@ -34,7 +34,8 @@ EXPORTS = ("gdn_status_string", "gdn_version", "gdn_conv1d_fwd", "gdn_conv1d_upd
            "gdn_layer_prefill", "gdn_linear_prefill_workspace_size", "gdn_linear_prefill",
            "gdn_linear_decode", "gdn_kv_record_bytes", "gdn_kv_append", "gdn_kv_read",
            "gdn_kv_attention_workspace_size", "gdn_kv_attention",
-           "gdn_selftest_bounded_wait")
+           "gdn_quantize_rows", "gdn_add_rmsnorm", "gdn_gated_rmsnorm",
+           "gdn_matmul_i8_workspace_size", "gdn_matmul_i8", "gdn_selftest_bounded_wait")
 
 NOALLOC_SCRATCH_BYTES = 128 << 20
 
@@ -53,12 +54,19 @@ class GdnKvCache(ctypes.Structure):
                 ("N", ctypes.c_int32)]
 
 
+class GdnMatrix(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("stride", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
 # The same structures as struct formats: packing one is several times cheaper than filling
 # a ctypes.Structure.
 GDN_TENSOR_PACK = struct.Struct("@Pii4q4q")
 GDN_KV_CACHE_PACK = struct.Struct("@PPP6i")
+GDN_MATRIX_PACK = struct.Struct("@P3qi4x")
 assert GDN_TENSOR_PACK.size == ctypes.sizeof(GdnTensor)
 assert GDN_KV_CACHE_PACK.size == ctypes.sizeof(GdnKvCache)
+assert GDN_MATRIX_PACK.size == ctypes.sizeof(GdnMatrix)
 
 
 class GdnError(RuntimeError):
@@ -118,6 +126,11 @@ def load(path: str = LIB_PATH):
         "gdn_kv_attention_workspace_size": ([i32, i32, i32, i64, i32, i32, i32, i32, u32],
                                             size),
         "gdn_kv_attention": ([vp, vp, vp, i32, vp, f32, u32, vp, vp, vp, size, vp, vp], i32),
+        "gdn_quantize_rows": ([vp, vp, vp, vp], i32),
+        "gdn_add_rmsnorm": ([vp, vp, vp, vp, f32, f32, vp, vp, vp], i32),
+        "gdn_gated_rmsnorm": ([vp, vp, vp, f32, vp, vp, vp], i32),
+        "gdn_matmul_i8_workspace_size": ([i64, i64, i64, u32], size),
+        "gdn_matmul_i8": ([vp, vp, vp, vp, vp, vp, u32, vp, size, vp, vp], i32),
         "gdn_selftest_bounded_wait": ([vp, vp], i32),
     }
     for name, (args, res) in sig.items():

@@ -10,6 +10,8 @@
 #include "common.cuh"
 #include "kv_format.cuh"
 #include "linear.cuh"
+#include "matmul_i8.cuh"
+#include "rows.cuh"
 
 namespace {
 
@@ -792,6 +794,189 @@ gdn_status_t gdn_kv_attention(const gdn_kv_cache_t *cache, const int32_t *cu_seq
     if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)))
         return GDN_ERR_WORKSPACE;
     return gdn_host::launch_kv_attention(a, st);
+}
+
+}  // extern "C"
+
+namespace {
+
+struct Matrix {
+    void *ptr;
+    int64_t rows, cols, st;
+    int32_t dtype;
+};
+
+// A matrix whose element type is `dt` (any floating type: -1).  A vector's stride is unused.
+gdn_status_t matrix_of(const gdn_matrix_t *t, int32_t dt, Matrix &out) {
+    if (!t) return GDN_ERR_NULL;
+    if (dt >= 0 ? t->dtype != dt : t->dtype != GDN_BF16 && t->dtype != GDN_F32) return GDN_ERR_DTYPE;
+    if (t->rows < 0 || t->cols < 0) return GDN_ERR_SHAPE;
+    const int size = t->dtype == GDN_I8 ? 1 : elem_size(t->dtype);
+    if (t->rows > 0 && t->cols > 0) {
+        if (!t->ptr) return GDN_ERR_NULL;
+        if ((uintptr_t)t->ptr % size) return GDN_ERR_LAYOUT;
+        if (t->rows > 1 && t->stride < t->cols) return GDN_ERR_LAYOUT;
+        if (t->rows > 1 && t->stride > INT64_MAX / 4 / t->rows) return GDN_ERR_SHAPE;
+    }
+    out.ptr = t->ptr;
+    out.rows = t->rows;
+    out.cols = t->cols;
+    out.st = t->rows > 1 ? t->stride : t->cols;
+    out.dtype = t->dtype;
+    return GDN_OK;
+}
+
+// Every row starts on `align` bytes.
+bool rows_aligned(const Matrix &m, uintptr_t align) {
+    const int64_t size = m.dtype == GDN_I8 ? 1 : elem_size(m.dtype);
+    return (uintptr_t)m.ptr % align == 0 && (m.rows <= 1 || m.st * size % (int64_t)align == 0);
+}
+
+// The weight and the output of the norms: fills p.w, p.y and their layout.
+gdn_status_t norm_args(const gdn_matrix_t *weight, int64_t width, float eps, const gdn_matrix_t *y,
+                       float *scale, int32_t dtype, int64_t T, int64_t D, gdn::RowParams &p) {
+    Matrix W, Y;
+    gdn_status_t s;
+    if ((s = matrix_of(weight, -1, W)) != GDN_OK) return s;
+    if (!y) return GDN_ERR_NULL;
+    if ((s = matrix_of(y, y->dtype == GDN_I8 ? GDN_I8 : dtype, Y)) != GDN_OK) return s;
+    if (W.rows != 1 || W.cols != width || Y.rows != T || Y.cols != D) return GDN_ERR_SHAPE;
+    if (!(eps > 0.f) || !std::isfinite(eps)) return GDN_ERR_UNSUPPORTED;
+    if (T > 0 && D > 0 && (Y.dtype == GDN_I8) != (scale != nullptr)) return GDN_ERR_NULL;
+    if ((uintptr_t)scale & 3u) return GDN_ERR_LAYOUT;
+    p.w = W.ptr;
+    p.w_f32 = W.dtype == GDN_F32;
+    p.y = Y.ptr;
+    p.y_st = Y.st;
+    p.scale = scale;
+    p.eps = eps;
+    p.vec = p.vec && rows_aligned(Y, Y.dtype == GDN_I8 ? 8 : 16) && aligned16(W.ptr);
+    return GDN_OK;
+}
+
+gdn::RowParams row_params(int64_t T, int64_t D) {
+    gdn::RowParams p;
+    memset(&p, 0, sizeof(p));
+    p.T = T;
+    p.D = (int32_t)D;
+    p.head = 16;
+    p.vec = D % 8 == 0;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status_t gdn_quantize_rows(const gdn_matrix_t *x, const gdn_matrix_t *q, float *scale,
+                               void *stream) {
+    gdn_host::CallRange nvtx_range("gdn_quantize_rows");
+    Matrix X, Q;
+    gdn_status_t s;
+    if ((s = matrix_of(x, -1, X)) != GDN_OK) return s;
+    if ((s = matrix_of(q, GDN_I8, Q)) != GDN_OK) return s;
+    if (Q.rows != X.rows || Q.cols != X.cols || X.cols < 1 || X.rows > 0x7fffffff) return GDN_ERR_SHAPE;
+    if (X.cols > GDN_MAX_ROW) return GDN_ERR_UNSUPPORTED;
+    if (X.rows == 0) return GDN_OK;
+    if (!scale) return GDN_ERR_NULL;
+    if ((uintptr_t)scale & 3u) return GDN_ERR_LAYOUT;
+    gdn::RowParams p = row_params(X.rows, X.cols);
+    p.x = X.ptr; p.x_st = X.st;
+    p.y = Q.ptr; p.y_st = Q.st;
+    p.scale = scale;
+    p.vec = p.vec && rows_aligned(X, 16) && rows_aligned(Q, 8);
+    return gdn_host::launch_rows(p, gdn::kRowQuantize, X.dtype == GDN_F32, true, (cudaStream_t)stream);
+}
+
+gdn_status_t gdn_add_rmsnorm(const gdn_matrix_t *x, const gdn_matrix_t *residual,
+                             const gdn_matrix_t *residual_out, const gdn_matrix_t *weight,
+                             float weight_offset, float eps, const gdn_matrix_t *y, float *scale,
+                             void *stream) {
+    gdn_host::CallRange nvtx_range("gdn_add_rmsnorm");
+    Matrix X, R, O;
+    gdn_status_t s;
+    if ((s = matrix_of(x, -1, X)) != GDN_OK) return s;
+    if (!residual != !residual_out) return GDN_ERR_NULL;
+    if (X.cols < 1 || X.rows > 0x7fffffff) return GDN_ERR_SHAPE;
+    if (X.cols > GDN_MAX_ROW) return GDN_ERR_UNSUPPORTED;
+    gdn::RowParams p = row_params(X.rows, X.cols);
+    p.x = X.ptr; p.x_st = X.st;
+    p.offset = weight_offset;
+    p.vec = p.vec && rows_aligned(X, 16);
+    if (residual) {
+        if ((s = matrix_of(residual, X.dtype, R)) != GDN_OK) return s;
+        if ((s = matrix_of(residual_out, X.dtype, O)) != GDN_OK) return s;
+        if (R.rows != X.rows || R.cols != X.cols || O.rows != X.rows || O.cols != X.cols)
+            return GDN_ERR_SHAPE;
+        p.res = R.ptr; p.res_st = R.st;
+        p.res_out = O.ptr; p.res_out_st = O.st;
+        p.vec = p.vec && rows_aligned(R, 16) && rows_aligned(O, 16);
+    }
+    if ((s = norm_args(weight, X.cols, eps, y, scale, X.dtype, X.rows, X.cols, p)) != GDN_OK) return s;
+    if (X.rows == 0) return GDN_OK;
+    return gdn_host::launch_rows(p, gdn::kRowAddNorm, X.dtype == GDN_F32, y->dtype == GDN_I8,
+                                 (cudaStream_t)stream);
+}
+
+gdn_status_t gdn_gated_rmsnorm(const gdn_tensor_t *x, const gdn_tensor_t *z,
+                               const gdn_matrix_t *weight, float eps, const gdn_matrix_t *y,
+                               float *scale, void *stream) {
+    gdn_host::CallRange nvtx_range("gdn_gated_rmsnorm");
+    View X, Z;
+    gdn_status_t s;
+    if ((s = view_of(x, X)) != GDN_OK) return s;
+    if ((s = view_of(z, Z)) != GDN_OK) return s;
+    if (Z.T != X.T || Z.H != X.H || Z.D != X.D || X.T > 0x7fffffff) return GDN_ERR_SHAPE;
+    if (Z.dtype != X.dtype) return GDN_ERR_DTYPE;
+    if (X.D < 16 || X.D > 256 || (X.D & (X.D - 1)) || X.H > GDN_MAX_ROW / X.D) return GDN_ERR_UNSUPPORTED;
+    const int64_t D = X.H * X.D;
+    gdn::RowParams p = row_params(X.T, D);
+    p.x = X.ptr; p.x_st = X.tok;
+    p.z = Z.ptr; p.z_st = Z.tok;
+    p.head = (int32_t)X.D;
+    if ((s = norm_args(weight, X.D, eps, y, scale, X.dtype, X.T, D, p)) != GDN_OK) return s;
+    if (X.T == 0) return GDN_OK;
+    return gdn_host::launch_rows(p, gdn::kRowGatedNorm, X.dtype == GDN_F32, y->dtype == GDN_I8,
+                                 (cudaStream_t)stream);
+}
+
+size_t gdn_matmul_i8_workspace_size(int64_t M, int64_t N, int64_t K, uint32_t flags) {
+    if (M <= 0 || N <= 0 || K <= 0 || K > GDN_MATMUL_MAX_K) return 0;
+    return gdn_host::matmul_i8_workspace(M, N, K, flags);
+}
+
+gdn_status_t gdn_matmul_i8(const gdn_matrix_t *a, const float *a_scale, const gdn_matrix_t *w,
+                           const float *w_scale, const gdn_matrix_t *bias,
+                           const gdn_matrix_t *out, uint32_t flags, void *workspace,
+                           size_t workspace_bytes, int32_t *status_dev, void *stream) {
+    gdn_host::CallRange nvtx_range("gdn_matmul_i8");
+    Matrix A, W, B, O;
+    gdn_status_t s;
+    if ((s = matrix_of(a, GDN_I8, A)) != GDN_OK) return s;
+    if ((s = matrix_of(w, GDN_I8, W)) != GDN_OK) return s;
+    if ((s = matrix_of(out, -1, O)) != GDN_OK) return s;
+    if (A.cols != W.cols || A.cols < 1 || O.rows != A.rows || O.cols != W.rows) return GDN_ERR_SHAPE;
+    if (A.rows > 0x7fffffff || W.rows > 0x7fffffff) return GDN_ERR_SHAPE;
+    if (A.cols > GDN_MATMUL_MAX_K) return GDN_ERR_UNSUPPORTED;
+    if (bias) {
+        if ((s = matrix_of(bias, -1, B)) != GDN_OK) return s;
+        if (B.rows != 1 || B.cols != W.rows) return GDN_ERR_SHAPE;
+    }
+    if (A.rows == 0 || W.rows == 0) return GDN_OK;
+    if (!a_scale || !w_scale) return GDN_ERR_NULL;
+    if (((uintptr_t)a_scale | (uintptr_t)w_scale) & 3u) return GDN_ERR_LAYOUT;
+    gdn::MatmulParams p;
+    memset(&p, 0, sizeof(p));
+    p.a = (const int8_t *)A.ptr; p.a_st = A.st; p.a_scale = a_scale;
+    p.w = (const int8_t *)W.ptr; p.w_st = W.st; p.w_scale = w_scale;
+    if (bias) { p.bias = B.ptr; p.bias_f32 = B.dtype == GDN_F32; }
+    p.out = O.ptr; p.out_st = O.st; p.out_f32 = O.dtype == GDN_F32;
+    p.M = A.rows; p.N = W.rows; p.K = (int32_t)A.cols;
+    p.status = status_dev;
+    const size_t need = gdn_matmul_i8_workspace_size(p.M, p.N, p.K, flags);
+    if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)))
+        return GDN_ERR_WORKSPACE;
+    return gdn_host::launch_matmul_i8(p, flags, workspace, workspace_bytes, (cudaStream_t)stream);
 }
 
 gdn_status_t gdn_selftest_bounded_wait(int32_t *status_dev, void *stream) {

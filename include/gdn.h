@@ -66,7 +66,7 @@ typedef enum {
     GDN_ERR_NONFINITE = 11   /* GDN_CHECK_INPUTS: a gate input is a NaN or an infinity */
 } gdn_status_t;
 
-typedef enum { GDN_BF16 = 0, GDN_F32 = 1, GDN_I32 = 2 } gdn_dtype_t;
+typedef enum { GDN_BF16 = 0, GDN_F32 = 1, GDN_I32 = 2, GDN_I8 = 3 } gdn_dtype_t;
 
 /* Strided view of an activation tensor.  Strides are in elements.  q/k/v/o must have a
  * unit element stride, a head stride equal to D, a token stride >= H*D that is a multiple
@@ -495,6 +495,86 @@ gdn_status_t gdn_kv_attention(const gdn_kv_cache_t *cache, const int32_t *cu_seq
                               const gdn_tensor_t *q, float scale, uint32_t flags,
                               const gdn_tensor_t *o, float *lse, void *workspace,
                               size_t workspace_bytes, int32_t *status_dev, void *stream);
+
+/*
+ * Operators on rows, around the mixers: norms, 8-bit rows and their products.
+ *
+ * gdn_matrix_t: rows x cols elements at ptr, consecutive rows `stride` elements apart and the
+ * elements of a row next to each other.  stride >= cols where there is more than one row; any
+ * alignment of the element type works, and rows that start on 16 bytes are faster.  A vector
+ * is a matrix of one row.  A matrix without elements may have a NULL ptr.
+ *
+ * A row y in 8 bits is int8 codes with an fp32 scale: an element stands for scale * code.
+ *     scale = max(max|y|, 127 * 2^-126) / 127,
+ *     code  = y / scale rounded to the nearest integer (ties to even), -127..127.
+ * fp32 arithmetic: an element within 2^-10 of a border between codes may take either, but for
+ * bf16 rows in gdn_quantize_rows, whose codes are those of the exact quotients.  A row with a
+ * NaN or an infinity has the scale NaN and codes of zero.
+ *
+ * Every row's results depend on that row alone and are the same bits in any batch, layout
+ * and alignment.  An output may be the input of the same type it stands for (residual_out
+ * the residual, y the x); other overlaps are not allowed.
+ */
+typedef struct {
+    void *ptr;
+    int64_t rows, cols, stride;
+    int32_t dtype;      /* gdn_dtype_t */
+} gdn_matrix_t;
+
+/*
+ * gdn_quantize_rows -- rows x [T, D] (bf16 or fp32) in 8 bits: q [T, D] int8, scale fp32 [T].
+ * D is at most GDN_MAX_ROW.
+ */
+#define GDN_MAX_ROW 32768
+
+gdn_status_t gdn_quantize_rows(const gdn_matrix_t *x, const gdn_matrix_t *q, float *scale,
+                               void *stream);
+
+/*
+ * gdn_add_rmsnorm -- the residual's addition and the root-mean-square norm of the sum:
+ *     h = x + residual,   residual_out = h,
+ *     y = h (weight_offset + weight) / sqrt(mean h^2 + eps).
+ * The norm is that of the fp32 sum; residual_out is the sum rounded once.
+ * x [T, D] bf16 or fp32; residual and residual_out likewise and of x's type, or both NULL
+ * (h = x); weight [D] bf16 or fp32; y [T, D] of x's type, or int8 with scale fp32 [T] (NULL
+ * otherwise).  eps is positive and finite.  D is at most GDN_MAX_ROW.
+ */
+gdn_status_t gdn_add_rmsnorm(const gdn_matrix_t *x, const gdn_matrix_t *residual,
+                             const gdn_matrix_t *residual_out, const gdn_matrix_t *weight,
+                             float weight_offset, float eps, const gdn_matrix_t *y, float *scale,
+                             void *stream);
+
+/*
+ * gdn_gated_rmsnorm -- the Gated DeltaNet layer's output norm, over each head, times the
+ * gate:
+ *     y = x weight / sqrt(mean_head x^2 + eps) * silu(z),   silu(z) = z / (1 + e^-z).
+ * x, z [T, H, D] views as above, of one type, D a power of two from 16 to 256 and H D at most
+ * GDN_MAX_ROW; weight [D] bf16 or fp32; y [T, H D] of x's type, or int8 with scale fp32 [T],
+ * one for all heads of a token (NULL otherwise).  eps is positive and finite.
+ */
+gdn_status_t gdn_gated_rmsnorm(const gdn_tensor_t *x, const gdn_tensor_t *z,
+                               const gdn_matrix_t *weight, float eps, const gdn_matrix_t *y,
+                               float *scale, void *stream);
+
+/*
+ * gdn_matmul_i8 -- product of 8-bit integers with a scale for each token and channel:
+ *     out[m][n] = a_scale[m] w_scale[n] sum_k a[m][k] w[n][k] + bias[n].
+ * a [M, K] and w [N, K] int8 (all 256 values); a_scale fp32 [M], w_scale fp32 [N]; bias [N]
+ * bf16 or fp32, or NULL; out [M, N] bf16 or fp32, not overlapping an input.  K is at most
+ * GDN_MATMUL_MAX_K, so that the sum, which is exact, fits 32 bits; it is then rounded to fp32,
+ * and so is each of the two products and the addition after it, in this order.  Every output
+ * is the same bits whatever the other rows and channels, the layout and the kernel are.
+ * workspace: device scratch of gdn_matmul_i8_workspace_size() bytes, 256-byte aligned (may be
+ * NULL when 0).  flags: GDN_PREFILL_SIMT forces the CUDA-core kernel.
+ */
+#define GDN_MATMUL_MAX_K 131071
+
+size_t gdn_matmul_i8_workspace_size(int64_t M, int64_t N, int64_t K, uint32_t flags);
+
+gdn_status_t gdn_matmul_i8(const gdn_matrix_t *a, const float *a_scale, const gdn_matrix_t *w,
+                           const float *w_scale, const gdn_matrix_t *bias,
+                           const gdn_matrix_t *out, uint32_t flags, void *workspace,
+                           size_t workspace_bytes, int32_t *status_dev, void *stream);
 
 /* gdn_selftest_bounded_wait -- checks the failure path of the bounded waits.  Every wait
  * of the tensor-core kernels on an mbarrier (a TMA copy or an MMA completing) gives up

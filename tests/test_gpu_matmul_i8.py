@@ -1,0 +1,156 @@
+"""gdn_matmul_i8 against the exact sum and the documented fp32 steps after it, to the bit."""
+import pytest
+import torch
+
+import eight_bit_ref as ref
+from gpu_util import assert_bits_equal
+
+pytestmark = pytest.mark.gpu
+
+gdn = pytest.importorskip("gated_deltanet_linear_11_gb300")
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    gdn.load()
+
+
+def codes(seed, rows, cols, lo=-128, hi=127, pad=0):
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randint(lo, hi + 1, (rows, cols + pad), generator=gen, dtype=torch.int8)
+    return x.cuda()[:, :cols]
+
+
+def scales(seed, n):
+    gen = torch.Generator().manual_seed(seed)
+    return (torch.rand(n, generator=gen) * 0.01 + 1e-4).cuda()
+
+
+def check(a, w, bias=None, dtype=BF, simt=False, **kw):
+    M, N = a.shape[0], w.shape[0]
+    sa, sw = scales(1, M), scales(2, N)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = gdn.gdn_matmul_i8(a, sa, w, sw, bias=bias, dtype=dtype, simt=simt, status=status, **kw)
+    want = ref.product(a, sa, w, sw, bias, dtype)
+    assert int(status) == 0
+    assert_bits_equal(out.cpu().contiguous(), want, "out %s" % (tuple(out.shape),))
+    return out
+
+
+SIZES = [(1, 1, 1), (1, 16, 16), (1, 128, 64), (2, 130, 100), (3, 5, 1001), (8, 64, 48),
+         (9, 257, 2064), (16, 1000, 512), (17, 96, 5120), (33, 300, 1040), (64, 515, 1024),
+         (65, 128, 1025), (100, 1024, 4096), (128, 129, 272), (129, 640, 3200), (200, 200, 200),
+         (256, 256, 1088), (257, 384, 2048), (333, 515, 1001), (512, 130, 96), (700, 900, 1536)]
+
+
+@pytest.mark.parametrize("simt", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_sizes(M, N, K, dtype, simt):
+    gen = torch.Generator().manual_seed(M)
+    bias = None if M % 2 else torch.randn(N, generator=gen).to(dtype).cuda()
+    check(codes(M + K, M, K), codes(N + K, N, K), bias, dtype, simt)
+
+
+@pytest.mark.parametrize("M", [1, 4, 16, 64, 300])
+@pytest.mark.parametrize("lo,hi", [(-128, -128), (127, 127), (-128, -120), (120, 127)])
+def test_largest_sums(M, lo, hi):
+    """All products of one sign: sums far past 2^24, where fp32 no longer holds every integer."""
+    for K in (1024, 1040, 5120, 131071):
+        a, w = codes(1, M, K, lo, hi, pad=-K % 16), codes(2, 40, K, lo, hi, pad=-K % 16)
+        check(a, w, dtype=F32)
+
+
+def test_cancelling_sums():
+    """Large partial sums that cancel to small ones."""
+    K = 8192
+    a, w = codes(1, 70, K, 100, 127), codes(2, 150, K, 100, 127)
+    w[:, K // 2:] = -w[:, :K // 2]
+    a[:, K // 2:] = a[:, :K // 2]
+    a[:, 0] += 1 * (a[:, 0] < 127).to(torch.int8)
+    check(a, w, dtype=F32)
+
+
+@pytest.mark.parametrize("M", [1, 12, 80, 400])
+@pytest.mark.parametrize("pad_a,pad_w", [(0, 0), (5, 0), (0, 3), (16, 32), (1, 1)])
+def test_strides(M, pad_a, pad_w):
+    """Rows with any distance between them; what lies behind a row is not read into sums."""
+    K, N = 528, 200
+    a, w = codes(1, M, K, pad=pad_a), codes(2, N, K, pad=pad_w)
+    wide = torch.full((M, N + 7), 3.0, device="cuda", dtype=BF)
+    out = check(a, w, out=wide[:, 2:2 + N])
+    assert out.data_ptr() == wide[:, 2:].data_ptr()
+    assert (wide[:, :2] == 3).all() and (wide[:, 2 + N:] == 3).all()
+    # rows whose length is not a multiple of 16 bytes, on 16-byte starts
+    check(codes(3, M, 500, pad=12), codes(4, N, 500, pad=12))
+    # views that start inside their storage
+    check(codes(5, M, 560)[:, 16:], codes(6, N, 560)[:, 16:])
+    check(codes(5, M, 560)[:, 3:], codes(6, N, 560)[:, 3:])
+
+
+def test_bits_do_not_depend_on_the_batch():
+    a, w = codes(1, 300, 1200, pad=0), codes(2, 333, 1200)
+    sa, sw = scales(3, 300), scales(4, 333)
+    full = gdn.gdn_matmul_i8(a, sa, w, sw, dtype=F32)
+    for rows in (slice(0, 1), slice(7, 11), slice(299, 300), slice(100, 230)):
+        part = gdn.gdn_matmul_i8(a[rows], sa[rows].contiguous(), w, sw, dtype=F32)
+        assert_bits_equal(part, full[rows].contiguous(), "rows")
+    part = gdn.gdn_matmul_i8(a, sa, w[50:51], sw[50:51].contiguous(), dtype=F32)
+    assert_bits_equal(part, full[:, 50:51].contiguous(), "channel")
+
+
+def test_nothing_to_do_and_scales_that_are_not_finite():
+    a, w = codes(1, 5, 64), codes(2, 7, 64)
+    sa, sw = scales(1, 5), scales(2, 7)
+    assert gdn.gdn_matmul_i8(a[:0], sa[:0], w, sw).shape == (0, 7)
+    assert gdn.gdn_matmul_i8(a, sa, w[:0], sw[:0]).shape == (5, 0)
+    sa[2], sw[3] = float("nan"), float("inf")
+    out = gdn.gdn_matmul_i8(a, sa, w, sw)
+    assert out[2].isnan().all() and not out[:, 3].isfinite().any()
+    keep = out[[0, 1, 3, 4]][:, [0, 1, 2, 4, 5, 6]]
+    assert keep.isfinite().all()
+
+
+def test_outputs_past_2_31():
+    M, N, K = 70000, 32768, 16
+    a, w = codes(1, M, K), codes(2, N, K)
+    sa, sw = scales(1, M), scales(2, N)
+    out = gdn.gdn_matmul_i8(a, sa, w, sw)
+    for m in (0, 65535, 65536, M - 1):
+        want = ref.product(a[m:m + 1], sa[m:m + 1], w, sw, None, BF)
+        assert_bits_equal(out[m:m + 1].cpu(), want, "row %d" % m)
+
+
+@pytest.mark.parametrize("M", [1, 40, 500])
+def test_graphs_and_streams(M):
+    """Two captured products with scratch of their own, and one on another stream, at once."""
+    K, N = 5120, 640
+    a = [codes(i, M, K) for i in range(3)]
+    w, sa, sw = codes(9, N, K), scales(1, M), scales(2, N)
+    want = [ref.product(x, sa, w, sw, None, BF) for x in a]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        gdn.gdn_matmul_i8(a[0], sa, w, sw)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(gdn.gdn_matmul_i8(a[i], sa, w, sw))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+            third = gdn.gdn_matmul_i8(a[2], sa, w, sw)
+        torch.cuda.synchronize()
+        for got, exp in zip(outs + [third], want):
+            assert_bits_equal(got.cpu(), exp, "out")
+            got.zero_()
+        torch.cuda.synchronize()

@@ -1,0 +1,226 @@
+"""gdn_quantize_rows, gdn_add_rmsnorm and gdn_gated_rmsnorm against their formulas in 64 bits,
+at the bounds of eight_bit_ref."""
+import numpy as np
+import pytest
+import torch
+
+import eight_bit_ref as ref
+from gpu_util import assert_bits_equal
+
+pytestmark = pytest.mark.gpu
+
+gdn = pytest.importorskip("gated_deltanet_linear_11_gb300")
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    gdn.load()
+
+
+def rnd(seed, *shape, dtype=BF):
+    gen = torch.Generator().manual_seed(seed)
+    return torch.randn(shape, generator=gen).to(dtype).cuda()
+
+
+def strided(x, pad):
+    """The same rows inside wider ones, `pad` elements in."""
+    wide = torch.full((x.shape[0], x.shape[1] + 2 * pad), 7.0, dtype=x.dtype, device=x.device)
+    wide[:, pad:pad + x.shape[1]] = x
+    return wide[:, pad:pad + x.shape[1]]
+
+
+# lengths on both sides of every split: part of a vector, a warp's one and four vectors, a CTA's
+# two and four, and the longest row
+WIDTHS = [1, 7, 8, 255, 256, 264, 1024, 1025, 2047, 5120, 16384, 16392, 32768]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", WIDTHS)
+def test_quantize_rows(D, dtype):
+    x = rnd(D, 5, D, dtype=dtype) * torch.tensor([1.0, 1e-30, 1e30, 3.0, 1.0]).to(dtype).cuda()[:, None]
+    x[3] = 0
+    q, scale = gdn.gdn_quantize_rows(x)
+    assert q.shape == x.shape and q.dtype is torch.int8 and scale.shape == (5,)
+    ref.assert_codes(q, scale, ref.f64(x), 2 * ref.U)
+    assert scale[3] == 2.0 ** -126 and not q[3].any()
+    assert (q.int().abs().amax(-1)[[0, 1, 2, 4]] == 127).all()
+
+
+def test_bf16_codes_are_exact():
+    """Every pair of significands, a few octaves apart: ties go to the even code, and no other
+    quotient changes sides."""
+    sig = torch.arange(128, 256).float()
+    rows = []
+    for s in range(0, 9):
+        x = (sig * 2.0 ** -s).repeat(128, 1)
+        x = torch.where(x <= sig[:, None], x, torch.zeros(()))
+        rows.append(torch.cat((sig[:, None], x, -x), 1))
+    x = torch.cat(rows).to(BF).cuda()
+    q, scale = gdn.gdn_quantize_rows(x)
+    want, s = ref.quotients(ref.f64(x))
+    assert (np.abs(want - np.floor(want) - 0.5) == 0).any()
+    assert (ref.f64(q) == np.rint(want)).all()
+    assert (np.abs(ref.f64(scale) - s) <= ref.U * s).all()
+
+
+def test_rows_that_are_not_finite():
+    for dtype in (BF, F32):
+        x = rnd(1, 6, 300, dtype=dtype)
+        x[1, 7], x[2, 299], x[4, 0] = float("nan"), float("inf"), float("-inf")
+        q, scale = gdn.gdn_quantize_rows(x)
+        bad = torch.tensor([1, 2, 4], device="cuda")
+        good = torch.tensor([0, 3, 5], device="cuda")
+        assert scale[bad].isnan().all() and not q[bad].any()
+        ref.assert_codes(q[good], scale[good], ref.f64(x[good]), 2 * ref.U)
+        w = torch.ones(300, device="cuda")
+        (q, scale), _ = gdn.gdn_add_rmsnorm(x, w, eight_bit=True)
+        assert scale[bad].isnan().all() and not q[bad].any() and scale[good].isfinite().all()
+        y, _ = gdn.gdn_add_rmsnorm(x, w)
+        assert not y[bad].isfinite().all(-1).any() and y[good].isfinite().all()
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("dtype,wt", [(BF, BF), (F32, F32), (BF, F32), (F32, BF)])
+@pytest.mark.parametrize("D", WIDTHS)
+def test_add_rmsnorm(D, dtype, wt, eight):
+    for res, offset, eps in ((True, 1.0, 1e-6), (False, 0.0, 1e-5)):
+        x, w = rnd(D, 3, D, dtype=dtype), rnd(D + 1, D, dtype=wt)
+        r = rnd(D + 2, 3, D, dtype=dtype) * 5 if res else None
+        y, out = gdn.gdn_add_rmsnorm(x, w, r, eps=eps, weight_offset=offset, eight_bit=eight)
+        want, h = ref.add_rmsnorm(x, w, r, eps, offset)
+        if eight:
+            ref.assert_codes(*y, want, ref.NORM)
+        else:
+            ref.assert_close(y, want, ref.NORM, dtype)
+        if res:
+            assert out.dtype is dtype
+            assert_bits_equal(out, (x.float() + r.float()).to(dtype), "residual")
+        else:
+            assert out is None
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norms_of_extreme_rows(dtype):
+    """Squares past fp32, zeros, and rows so small that eps rules."""
+    size = torch.tensor([1e25, 3e37, 0.0, 1e-25, 1e-12, 1.0], device="cuda")
+    x = (rnd(5, 6, 640, dtype=F32) * size[:, None]).to(dtype)
+    w = rnd(6, 640, dtype=F32) * 20
+    want, _ = ref.add_rmsnorm(x, w, None, 1e-6, 0.0)
+    y, _ = gdn.gdn_add_rmsnorm(x, w)
+    ref.assert_close(y, want, ref.NORM, dtype)
+    (q, scale), _ = gdn.gdn_add_rmsnorm(x, w, eight_bit=True)
+    keep = [0, 1, 2, 4, 5]              # 1e-25 of x gives y of 1e-22: fp32 holds it
+    ref.assert_codes(q, scale, want, ref.NORM)
+    assert scale[2] == 2.0 ** -126 and not q[2].any() and keep
+    x3, z = x.view(6, 5, 128), rnd(7, 6, 5, 128, dtype=dtype)
+    z[0, 0, :4] = torch.tensor([100.0, -100.0, -80.0, 0.0])
+    w3 = w[:128].contiguous()
+    want = ref.gated_rmsnorm(x3, z, w3, 1e-6)
+    got = gdn.gdn_gated_rmsnorm(x3, z, w3)
+    # silu(-100) = -3.7e-42 is under the fp32 range, where the kernel gives a zero
+    want = np.where(np.abs(want) < 1e-36, ref.f64(got) * (np.abs(ref.f64(got)) < 1e-36), want)
+    # the exponent -80 log2 e is rounded before e^-z: 116 half steps of it times ln 2
+    ref.assert_close(got, want, ref.GATED[dtype] + 116 * ref.U, dtype)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H,D", [(1, 16), (3, 16), (5, 32), (7, 64), (48, 128), (9, 128), (16, 256),
+                                 (128, 256)])
+def test_gated_rmsnorm(H, D, dtype, eight):
+    T = 5
+    x = rnd(H, T, H, D, dtype=dtype) * torch.arange(1, H + 1, device="cuda").to(dtype)[:, None]
+    rows = rnd(H + 1, T, 2 * H * D, dtype=dtype)
+    z = rows[:, H * D:].view(T, H, D)
+    w = rnd(H + 2, D, dtype=F32)
+    y = gdn.gdn_gated_rmsnorm(x, z, w, eps=1e-5, eight_bit=eight)
+    want = ref.gated_rmsnorm(x, z, w, 1e-5)
+    if eight:
+        ref.assert_codes(*y, want, ref.GATED[dtype])
+    else:
+        assert y.shape == (T, H * D)
+        ref.assert_close(y, want, ref.GATED[dtype], dtype)
+    assert_bits_equal(gdn.gdn_gated_rmsnorm(x[None], z[None], w, eps=1e-5),
+                      gdn.gdn_gated_rmsnorm(x, z, w, eps=1e-5), "[1, T, H, D]")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [40, 1000, 1031, 6144])
+def test_bits_do_not_depend_on_batch_or_layout(D, dtype):
+    x, r, w = rnd(1, 37, D, dtype=dtype), rnd(2, 37, D, dtype=dtype), rnd(3, D, dtype=dtype)
+    (q, s), h = gdn.gdn_add_rmsnorm(x, w, r, eight_bit=True)
+    y, _ = gdn.gdn_add_rmsnorm(x, w, r)
+    for rows in (slice(0, 1), slice(36, 37), slice(5, 9)):
+        (q1, s1), h1 = gdn.gdn_add_rmsnorm(x[rows], w, r[rows], eight_bit=True)
+        assert_bits_equal(q1, q[rows], "codes")
+        assert_bits_equal(s1, s[rows], "scale")
+        assert_bits_equal(h1, h[rows], "residual")
+    for pad in (1, 3, 8):
+        wide = torch.zeros(37, D + pad, dtype=torch.int8, device="cuda")
+        ws = torch.zeros(D + 1, dtype=dtype, device="cuda")
+        ws[1:] = w
+        (q1, s1), h1 = gdn.gdn_add_rmsnorm(strided(x, pad), ws[1:], strided(r, pad),
+                                           eight_bit=True, y=wide[:, pad:])
+        assert_bits_equal(q1, q, "codes")
+        assert_bits_equal(s1, s, "scale")
+        assert_bits_equal(h1, h, "residual")
+        assert not wide[:, :pad].any()
+        out = strided(x, pad)
+        gdn.gdn_add_rmsnorm(out, ws[1:], strided(r, pad), y=out)        # in place
+        assert_bits_equal(out.contiguous(), y, "y")
+    # the residual updated in place
+    r2 = r.clone()
+    y2, h2 = gdn.gdn_add_rmsnorm(x, w, r2, residual_out=r2)
+    assert h2 is r2
+    assert_bits_equal(r2, h, "residual")
+    assert_bits_equal(y2, y, "y")
+
+
+def test_no_rows_and_many():
+    e = torch.empty(0, 64, dtype=BF, device="cuda")
+    q, s = gdn.gdn_quantize_rows(e)
+    assert q.shape == (0, 64) and s.shape == (0,)
+    y, h = gdn.gdn_add_rmsnorm(e, torch.ones(64, device="cuda"), e)
+    assert y.shape == h.shape == (0, 64)
+    assert gdn.gdn_gated_rmsnorm(e.view(0, 4, 16), e.view(0, 4, 16),
+                                 torch.ones(16, device="cuda")).shape == (0, 64)
+    x = rnd(3, 100001, 8)
+    q, s = gdn.gdn_quantize_rows(x)
+    ref.assert_codes(q[-3:], s[-3:], ref.f64(x[-3:]), 2 * ref.U)
+    ref.assert_codes(q[:3], s[:3], ref.f64(x[:3]), 2 * ref.U)
+
+
+def test_rows_far_apart():
+    """Row offsets past 2^31 elements."""
+    st = (1 << 30) + 8
+    wide = torch.empty(2 * st + 64, dtype=BF, device="cuda")
+    x = wide.as_strided((3, 64), (st, 1))
+    x.copy_(rnd(4, 3, 64))
+    q, s = gdn.gdn_quantize_rows(x)
+    ref.assert_codes(q, s, ref.f64(x), 2 * ref.U)
+    y, h = gdn.gdn_add_rmsnorm(x, torch.ones(64, device="cuda"), x, residual_out=x, y=None)
+    assert h is x and y.isfinite().all()
+
+
+def test_norm_in_a_graph():
+    """A captured pass, replayed on new values, gives what the plain calls give."""
+    x, r, w = rnd(1, 9, 700), rnd(2, 9, 700), rnd(3, 700)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        gdn.gdn_add_rmsnorm(x, w, r, eight_bit=True)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        (q, s), h = gdn.gdn_add_rmsnorm(x, w, r, eight_bit=True)
+    for seed in (5, 6):
+        x.copy_(rnd(seed, 9, 700))
+        graph.replay()
+        (q1, s1), h1 = gdn.gdn_add_rmsnorm(x, w, r, eight_bit=True)
+        assert_bits_equal(q, q1, "codes")
+        assert_bits_equal(s, s1, "scale")
+        assert_bits_equal(h, h1, "residual")
