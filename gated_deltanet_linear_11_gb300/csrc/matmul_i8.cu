@@ -71,7 +71,8 @@ size_t matmul_i8_workspace(int64_t M, int64_t N, int64_t K, uint32_t flags) {
 
 gdn_status_t launch_matmul_i8(const MatmulParams &p, uint32_t flags, void *ws, size_t ws_bytes,
                               cudaStream_t st) {
-    (void)flags; (void)ws; (void)ws_bytes;
+    (void)ws; (void)ws_bytes;
+    if (matmul_i8_tc_supported(p, flags)) return launch_matmul_i8_tc(p, st);
     const int64_t tiles = ((p.M + kSimtTile - 1) / kSimtTile) * ((p.N + kSimtTile - 1) / kSimtTile);
     if (tiles > 0x7fffffff) return GDN_ERR_SHAPE;
     return launch_dependent(matmul_i8_simt_kernel, dim3((unsigned)tiles), dim3(256), 0, st, p) == cudaSuccess

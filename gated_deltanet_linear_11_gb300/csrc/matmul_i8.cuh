@@ -36,4 +36,7 @@ namespace gdn_host {
 size_t matmul_i8_workspace(int64_t M, int64_t N, int64_t K, uint32_t flags);
 gdn_status_t launch_matmul_i8(const gdn::MatmulParams &p, uint32_t flags, void *ws, size_t ws_bytes,
                               cudaStream_t st);
+// the tensor-core kernels: rows of both operands on 16 bytes
+bool matmul_i8_tc_supported(const gdn::MatmulParams &p, uint32_t flags);
+gdn_status_t launch_matmul_i8_tc(const gdn::MatmulParams &p, cudaStream_t st);
 }  // namespace gdn_host

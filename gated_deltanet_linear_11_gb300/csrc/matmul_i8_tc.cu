@@ -1,0 +1,405 @@
+// matmul_i8_tc.cu -- gdn_matmul_i8 on tcgen05.
+//
+// sm_103a has no 8-bit integer form of tcgen05.mma, and its legacy integer path is a small
+// part of the fp16 rate.  An int8 is exact in fp16, a product of two is exact in fp32, and so
+// is a sum of 1024 of them (at most 2^24): the products run as kind::f16 with fp32 sums in
+// TMEM, which move to int32 registers every 1024 products.  The result is the exact integer
+// for any input, whatever the split.
+//
+// Channels are the rows of the product (M = 128): their codes go from shared memory through
+// registers into TMEM as fp16, where the tensor core takes them as operand A.  Tokens are its
+// columns: converted into fp16 tiles in shared memory, operand B.
+//
+// A CTA makes 128 channels x NT tokens over a range of K; the CTAs of a cluster share a tile
+// by ranges of K and add up their int32 sums through distributed shared memory.
+//
+// Conversion: x ^ 0x80 is x + 128 in 0..255; as the low byte of 0x6400 that is the fp16
+// number 1024 + 128 + x, less 1152 (exact).  Two bytes take a byte permute and a subtraction.
+#include <atomic>
+
+#include "bulk_ptx.cuh"
+#include "matmul_i8.cuh"
+#include "tmap.cuh"
+
+#include <cuda_fp16.h>
+
+namespace gdn {
+
+struct I8Maps {
+    CUtensorMap w, a;               // boxes of 128 and NT rows of 128 codes
+};
+
+constexpr int kI8Channels = 128;    // channels of a tile
+constexpr int kI8Step = 128;        // codes of a row per step
+constexpr int kI8Exact = 8;         // steps whose sums fp32 holds exactly
+constexpr int kI8ConvWarps = 8;
+constexpr int kI8Threads = 32 * (kI8ConvWarps + 2);
+
+template <int NT> struct I8Shape {
+    static constexpr int RAW_W = kI8Channels * kI8Step, RAW_A = NT * kI8Step;
+    static constexpr int STAGES = NT <= 32 ? 4 : NT == 64 ? 3 : 4;
+    static constexpr int CONV = NT * kI8Step * 2;
+    static constexpr int CTAS = NT <= 64 ? 2 : 1;        // that fit on an SM
+    // TMEM columns: two accumulators of NT, two steps of 64 columns of operand A
+    static constexpr int COL_A = 2 * NT, COLS = NT <= 64 ? 256 : 512;
+};
+template <int NT> struct I8Smem {
+    uint8_t raw_w[I8Shape<NT>::STAGES][I8Shape<NT>::RAW_W];
+    uint8_t raw_a[I8Shape<NT>::STAGES][I8Shape<NT>::RAW_A];
+    uint8_t conv[2][I8Shape<NT>::CONV];      // [step][64-code block][token][128 bytes]
+    uint64_t raw_full[I8Shape<NT>::STAGES], raw_free[I8Shape<NT>::STAGES];
+    uint64_t ab_full[2], ab_free[2], d_full[2], d_free[2];
+    uint32_t tmem;
+    int abort;
+};
+
+__device__ __forceinline__ void i8_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(tc::smem_u32(bar)) : "memory");
+}
+// Bounded wait by a warp; false once any thread of the CTA has given up.
+__device__ __forceinline__ bool i8_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const bool ok = wait_bounded_poll<0>(bar, parity, abort);
+    if (!ok) *abort = 1;
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+
+// 32-bit instruction descriptor: fp16 A and B, both K-major, fp32 D.
+__device__ constexpr uint32_t i8_idesc(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void i8_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t add) {
+    asm volatile("{\n\t.reg .pred p, e;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(add) : "memory");
+}
+__device__ __forceinline__ void i8_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+                    "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+                    "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
+}
+__device__ __forceinline__ void i8_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(tc::smem_u32(bar)) : "memory");
+}
+
+// Four codes as fp16 pairs (elements 0 and 1, 2 and 3).
+__device__ __forceinline__ void i8_halves(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 less = __floats2half2_rn(1152.f, 1152.f);
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&a), less);
+    const __half2 y = __hsub2(*reinterpret_cast<__half2 *>(&b), less);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+// 16 codes: eight words of fp16 pairs.
+__device__ __forceinline__ void i8_halves16(const uint4 &v, uint32_t *r) {
+    i8_halves(v.x, r[0], r[1]);
+    i8_halves(v.y, r[2], r[3]);
+    i8_halves(v.z, r[4], r[5]);
+    i8_halves(v.w, r[6], r[7]);
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int32_t cluster_load(uint32_t addr, uint32_t rank) {
+    uint32_t remote;
+    int32_t v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void matmul_store(const MatmulParams &p, int64_t m, int64_t n, float v) {
+    if (p.out_f32) ((float *)p.out)[m * p.out_st + n] = v;
+    else ((bf16 *)p.out)[m * p.out_st + n] = from_f32<bf16>(v);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kI8Threads, I8Shape<NT>::CTAS)
+matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__ MatmulParams p, int tiles_m) {
+    using Sh = I8Shape<NT>;
+    constexpr int HALF = NT / 2;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    I8Smem<NT> &S = *reinterpret_cast<I8Smem<NT> *>(smem_raw);
+    if (tc::smem_u32(smem_raw) & 1023u) {        // the tiles' swizzle needs it; never seen
+        if (threadIdx.x == 0) report(p.status, GDN_ERR_CUDA);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank(), parts = cluster_size();
+    const int tile = blockIdx.x / parts;
+    const int m0 = (tile % tiles_m) * NT, n0 = (tile / tiles_m) * kI8Channels;
+    const int all = (p.K + kI8Step - 1) / kI8Step;
+    const int first = (int)((int64_t)all * rank / parts), n = (int)((int64_t)all * (rank + 1) / parts) - first;
+    const int chunks = (n + kI8Exact - 1) / kI8Exact;
+    volatile int *abort = &S.abort;
+
+    if (warp == 0) {
+        tc::tmem_alloc(&S.tmem, Sh::COLS);
+        tc::tmem_relinquish();
+    }
+    if (tid == 0) {
+        S.abort = 0;
+        for (int i = 0; i < Sh::STAGES; ++i) {
+            tc::mbar_init(&S.raw_full[i], 1);
+            tc::mbar_init(&S.raw_free[i], kI8ConvWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&S.ab_full[i], kI8ConvWarps);
+            tc::mbar_init(&S.ab_free[i], 1);
+            tc::mbar_init(&S.d_full[i], 1);
+            tc::mbar_init(&S.d_free[i], kI8ConvWarps);
+        }
+        tc::mbar_fence_init();
+        tc::prefetch_tmap(&maps.w);
+        tc::prefetch_tmap(&maps.a);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = S.tmem;
+    grid_dependents_launch();
+    grid_dependency_wait();
+
+    int32_t sums[HALF];                          // this thread's channel, half of the tokens
+#pragma unroll
+    for (int i = 0; i < HALF; ++i) sums[i] = 0;
+    const int row = 32 * (warp & 3) + lane, half = warp >> 2;
+
+    if (warp < kI8ConvWarps) {
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        // sums of the products of chunk c, which are whole numbers up to 2^24
+        auto drain = [&](int c) {
+            if (!i8_wait(&S.d_full[c & 1], (c >> 1) & 1, abort)) return;
+            tc::fence_after_sync();
+            const uint32_t at = tmem + lanes + (c & 1) * NT + half * HALF;
+            constexpr int W = HALF < 16 ? 8 : 16;
+#pragma unroll
+            for (int i = 0; i < HALF; i += W) {
+                float v[W];
+                if constexpr (W == 8) tc::tmem_ld8(at + i, v);
+                else tc::tmem_ld16(at + i, v);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < W; ++j) sums[i + j] += __float2int_rn(v[j]);
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) i8_arrive(&S.d_free[c & 1]);
+        };
+        int drained = 0;
+        bool ok = true;
+        for (int s = 0; s < n; ++s) {
+            const int slot = s % Sh::STAGES, buf = s & 1;
+            if (!(ok = i8_wait(&S.raw_full[slot], (s / Sh::STAGES) & 1, abort))) break;
+            if (s >= 2 && !(ok = i8_wait(&S.ab_free[buf], ((s >> 1) - 1) & 1, abort))) break;
+            tc::fence_after_sync();
+            // channels: half a step of this thread's row
+#pragma unroll
+            for (int c = 0; c < 4; c += 2) {
+                uint32_t r[16];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    i8_halves16(*reinterpret_cast<const uint4 *>(S.raw_w[slot] + tc::swz(row, 4 * half + c + i)),
+                                r + 8 * i);
+                i8_st16(tmem + lanes + Sh::COL_A + 64 * buf + 32 * half + 8 * c, r);
+            }
+            // Tokens: a warp takes eight rows of one 64-code block.  Eight lanes take four chunks
+            // of rows r and r ^ 5, whose swizzled places differ both where they are read
+            // (chunks 0-3 or 4-7) and where they are written (even or odd chunks).
+            for (int u = warp; u < NT / 4; u += kI8ConvWarps) {
+                const int blk = u & 1, t = 8 * (u >> 1) + ((lane >> 3) ^ (lane & 4 ? 5 : 0)), c = lane & 3;
+                uint32_t r[8];
+                i8_halves16(*reinterpret_cast<const uint4 *>(S.raw_a[slot] + tc::swz(t, 4 * blk + c)), r);
+                uint8_t *dst = S.conv[buf] + blk * NT * 128;
+                *reinterpret_cast<uint4 *>(dst + tc::swz(t, 2 * c)) = make_uint4(r[0], r[1], r[2], r[3]);
+                *reinterpret_cast<uint4 *>(dst + tc::swz(t, 2 * c + 1)) = make_uint4(r[4], r[5], r[6], r[7]);
+            }
+            tc::fence_async_smem();
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                i8_arrive(&S.raw_free[slot]);
+                i8_arrive(&S.ab_full[buf]);
+            }
+            // a chunk is fetched while the next one's first steps run
+            if (s % kI8Exact == 1 && s > kI8Exact) drain(drained++);
+        }
+        while (ok && drained < chunks) drain(drained++);
+    } else if (warp == kI8ConvWarps) {
+        int issued = 0;
+        for (int s = 0; s < n; ++s) {
+            const int slot = s % Sh::STAGES;
+            if (s >= Sh::STAGES && !i8_wait(&S.raw_free[slot], ((s / Sh::STAGES) - 1) & 1, abort)) break;
+            if (lane == 0) {
+                tc::mbar_expect_tx(&S.raw_full[slot], Sh::RAW_W + Sh::RAW_A);
+                i8_load_2d(S.raw_w[slot], &maps.w, &S.raw_full[slot], (first + s) * kI8Step, n0);
+                i8_load_2d(S.raw_a[slot], &maps.a, &S.raw_full[slot], (first + s) * kI8Step, m0);
+            }
+            __syncwarp();
+            issued = s + 1;
+        }
+        // nothing may land after the CTA has left
+        for (int s = max(0, issued - Sh::STAGES); s < issued; ++s)
+            wait_bounded_poll<0>(&S.raw_full[s % Sh::STAGES], (s / Sh::STAGES) & 1, nullptr);
+    } else {
+        const uint32_t id = i8_idesc(kI8Channels, NT);
+        for (int s = 0; s < n; ++s) {
+            const int buf = s & 1, c = s / kI8Exact;
+            if (s % kI8Exact == 0 && c >= 2 && !i8_wait(&S.d_free[c & 1], ((c >> 1) - 1) & 1, abort)) break;
+            if (!i8_wait(&S.ab_full[buf], (s >> 1) & 1, abort)) break;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int k = 0; k < kI8Step / 16; ++k)
+                i8_mma(tmem + (c & 1) * NT, tmem + Sh::COL_A + 64 * buf + 8 * k,
+                       tc::sdesc(tc::smem_u32(S.conv[buf] + (k >> 2) * NT * 128 + (k & 3) * 32), 0, 1024), id,
+                       s % kI8Exact != 0 || k > 0);
+            tc::mma_commit_warp(&S.ab_free[buf]);
+            if (s % kI8Exact == kI8Exact - 1 || s == n - 1) tc::mma_commit_warp(&S.d_full[c & 1]);
+        }
+    }
+    __syncwarp();
+
+    if (parts == 1) {
+        if (warp < kI8ConvWarps && n0 + row < p.N) {
+            const float ws = p.w_scale[n0 + row], bias = matmul_bias(p, n0 + row);
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) {
+                const int64_t m = (int64_t)m0 + half * HALF + i;
+                if (m < p.M) matmul_store(p, m, n0 + row, matmul_value(sums[i], p.a_scale[m], ws, bias));
+            }
+        }
+    } else {
+        // [token][channel] sums over the codes that have all been used
+        int32_t *part = reinterpret_cast<int32_t *>(S.raw_w);
+        static_assert(NT * kI8Channels * 4 <= sizeof(S.raw_w) + sizeof(S.raw_a), "the sums fit");
+        if (warp < kI8ConvWarps)
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) part[(half * HALF + i) * kI8Channels + row] = sums[i];
+        cluster_sync();
+        const int rows = (int)min((int64_t)NT, p.M - m0);
+        const uint32_t base = tc::smem_u32(part);
+        for (int i = rank * kI8Threads + tid; i < rows * kI8Channels; i += parts * kI8Threads) {
+            const int64_t m = (int64_t)m0 + i / kI8Channels, nn = (int64_t)n0 + i % kI8Channels;
+            if (nn >= p.N) continue;
+            int32_t sum = 0;
+            for (uint32_t r = 0; r < parts; ++r) sum += cluster_load(base + 4 * i, r);
+            matmul_store(p, m, nn, matmul_value(sum, p.a_scale[m], p.w_scale[nn], matmul_bias(p, nn)));
+        }
+        cluster_sync();                          // before any CTA's memory goes
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 0) tc::tmem_dealloc(tmem, Sh::COLS);
+    if (tid == 0 && *abort) report(p.status, GDN_ERR_TIMEOUT);
+}
+
+}  // namespace gdn
+
+namespace gdn_host {
+
+using namespace gdn;
+
+namespace {
+
+// Rows of 128 codes at a time; a row's end and the rows' end read as zeros.
+bool code_map(CUtensorMap *m, const int8_t *ptr, int64_t rows, int64_t K, int64_t stride, int box_rows) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? stride : (K + 15) / 16 * 16)};
+    cuuint32_t box[2] = {kI8Step, (cuuint32_t)box_rows}, unit[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(ptr), dims, strides, box, unit,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count(int dev) {
+    static std::atomic<int> known[64];
+    if (dev < 64) {
+        const int n = known[dev].load();
+        if (n > 0) return n;
+    }
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 0;
+    if (dev < 64) known[dev].store(n);
+    return n;
+}
+
+template <int NT>
+gdn_status_t launch_tc(const MatmulParams &p, cudaStream_t st) {
+    using Sh = I8Shape<NT>;
+    auto kern = matmul_i8_tc_kernel<NT>;
+    constexpr int smem = sizeof(I8Smem<NT>);
+    static_assert(Sh::CTAS * (smem + 1024) <= 228 * 1024, "the CTAs of an SM fit");
+    static std::atomic<uint64_t> ready{0};   // one bit per device (beyond 63: set every time)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+    if (dev > 63 || !((ready.load() >> dev) & 1u)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return GDN_ERR_CUDA;
+        if (dev <= 63) ready.fetch_or(1ull << dev);
+    }
+    const int sms = sm_count(dev);
+    if (sms <= 0) return GDN_ERR_CUDA;
+    I8Maps maps;
+    if (!code_map(&maps.w, p.w, p.N, p.K, p.w_st, kI8Channels) || !code_map(&maps.a, p.a, p.M, p.K, p.a_st, NT))
+        return GDN_ERR_CUDA;
+    const int64_t tiles_m = (p.M + NT - 1) / NT, tiles = tiles_m * ((p.N + kI8Channels - 1) / kI8Channels);
+    // as many ranges of K as keep every SM busy, of at least two steps each
+    const int64_t steps = (p.K + kI8Step - 1) / kI8Step, want = (int64_t)sms * Sh::CTAS / tiles;
+    int64_t parts = want < 1 ? 1 : want > 8 ? 8 : want;
+    if (parts > (steps + 1) / 2) parts = (steps + 1) / 2;
+    if (tiles * parts > 0x7fffffff) return GDN_ERR_SHAPE;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * parts));
+    cfg.blockDim = dim3(kI8Threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)parts;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, maps, p, (int)tiles_m) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // namespace
+
+bool matmul_i8_tc_supported(const MatmulParams &p, uint32_t flags) {
+    const auto aligned = [](const int8_t *ptr, int64_t rows, int64_t st) {
+        return ((uintptr_t)ptr & 15u) == 0 && (rows == 1 || st % 16 == 0);
+    };
+    return !(flags & GDN_PREFILL_SIMT) && aligned(p.a, p.M, p.a_st) && aligned(p.w, p.N, p.w_st);
+}
+
+gdn_status_t launch_matmul_i8_tc(const MatmulParams &p, cudaStream_t st) {
+    if (p.M <= 16) return launch_tc<16>(p, st);
+    if (p.M <= 32) return launch_tc<32>(p, st);
+    if (p.M <= 64) return launch_tc<64>(p, st);
+    return launch_tc<128>(p, st);
+}
+
+}  // namespace gdn_host
