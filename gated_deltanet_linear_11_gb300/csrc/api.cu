@@ -956,7 +956,7 @@ gdn_status_t gdn_matmul_i8(const gdn_matrix_t *a, const float *a_scale, const gd
     if ((s = matrix_of(w, GDN_I8, W)) != GDN_OK) return s;
     if ((s = matrix_of(out, -1, O)) != GDN_OK) return s;
     if (A.cols != W.cols || A.cols < 1 || O.rows != A.rows || O.cols != W.rows) return GDN_ERR_SHAPE;
-    if (A.rows > 0x7fffffff || W.rows > 0x7fffffff) return GDN_ERR_SHAPE;
+    if (A.rows > 0x7fff0000 || W.rows > 0x7fff0000) return GDN_ERR_SHAPE;    // tiles past the end
     if (A.cols > GDN_MATMUL_MAX_K) return GDN_ERR_UNSUPPORTED;
     if (bias) {
         if ((s = matrix_of(bias, -1, B)) != GDN_OK) return s;

@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(256) matmul_i8_simt_kernel(const MatmulParams 
         for (int i = 0; i < 4; ++i) {
             const int64_t m = m0 + ty + 16 * i;
             if (m >= p.M) continue;
-            const float v = matmul_value(acc[i][j], p.a_scale[m], ws, bias);
+            const float v = matmul_value((float)acc[i][j], p.a_scale[m], ws, bias);
             if (p.out_f32) ((float *)p.out)[m * p.out_st + n] = v;
             else ((bf16 *)p.out)[m * p.out_st + n] = from_f32<bf16>(v);
         }
@@ -65,14 +65,14 @@ namespace gdn_host {
 using namespace gdn;
 
 size_t matmul_i8_workspace(int64_t M, int64_t N, int64_t K, uint32_t flags) {
-    (void)M; (void)N; (void)K; (void)flags;
-    return 0;
+    (void)N;
+    return flags & GDN_PREFILL_SIMT ? 0 : matmul_i8_tc_workspace(M, K);
 }
 
 gdn_status_t launch_matmul_i8(const MatmulParams &p, uint32_t flags, void *ws, size_t ws_bytes,
                               cudaStream_t st) {
-    (void)ws; (void)ws_bytes;
-    if (matmul_i8_tc_supported(p, flags)) return launch_matmul_i8_tc(p, st);
+    (void)ws_bytes;
+    if (matmul_i8_tc_supported(p, flags)) return launch_matmul_i8_tc(p, ws, st);
     const int64_t tiles = ((p.M + kSimtTile - 1) / kSimtTile) * ((p.N + kSimtTile - 1) / kSimtTile);
     if (tiles > 0x7fffffff) return GDN_ERR_SHAPE;
     return launch_dependent(matmul_i8_simt_kernel, dim3((unsigned)tiles), dim3(256), 0, st, p) == cudaSuccess

@@ -20,9 +20,9 @@ struct MatmulParams {
     int32_t *status;
 };
 
-// sum * a_scale * w_scale + bias, each step rounded to fp32.
-__device__ __forceinline__ float matmul_value(int32_t sum, float as, float ws, float bias) {
-    return __fadd_rn(__fmul_rn(__fmul_rn((float)sum, as), ws), bias);
+// sum * a_scale * w_scale + bias, each step rounded to fp32 (sum: the integer, rounded once).
+__device__ __forceinline__ float matmul_value(float sum, float as, float ws, float bias) {
+    return __fadd_rn(__fmul_rn(__fmul_rn(sum, as), ws), bias);
 }
 
 __device__ __forceinline__ float matmul_bias(const MatmulParams &p, int64_t n) {
@@ -38,5 +38,6 @@ gdn_status_t launch_matmul_i8(const gdn::MatmulParams &p, uint32_t flags, void *
                               cudaStream_t st);
 // the tensor-core kernels: rows of both operands on 16 bytes
 bool matmul_i8_tc_supported(const gdn::MatmulParams &p, uint32_t flags);
-gdn_status_t launch_matmul_i8_tc(const gdn::MatmulParams &p, cudaStream_t st);
+size_t matmul_i8_tc_workspace(int64_t M, int64_t K);
+gdn_status_t launch_matmul_i8_tc(const gdn::MatmulParams &p, void *ws, cudaStream_t st);
 }  // namespace gdn_host

@@ -57,8 +57,9 @@ __device__ __forceinline__ void i8_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(tc::smem_u32(bar)) : "memory");
 }
 // Bounded wait by a warp; false once any thread of the CTA has given up.
+template <int SLEEP_NS = 0>
 __device__ __forceinline__ bool i8_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    const bool ok = wait_bounded_poll<0>(bar, parity, abort);
+    const bool ok = wait_bounded_poll<SLEEP_NS>(bar, parity, abort);
     if (!ok) *abort = 1;
     return __all_sync(0xffffffffu, ok) != 0;
 }
@@ -126,6 +127,51 @@ __device__ __forceinline__ int32_t cluster_load(uint32_t addr, uint32_t rank) {
     return v;
 }
 
+// Sums of a thread's outputs over the chunks: fp32 while they stay below 2^24, where additions
+// of whole numbers are exact, which ordinary codes never leave.  A warp in which one would
+// moves its sums to int32 words in local memory first (a conversion to integers runs at a
+// sixteenth of the rate of an addition, and as many registers again are not to be had).
+template <int N> struct ExactSums {
+    float s[N];
+    volatile int32_t far[N];
+    bool moved;
+
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = 0.f;
+        moved = false;
+    }
+    // adds W whole numbers of at most 2^24 to elements at ..
+    template <int W> __device__ __forceinline__ void add(int at, const float (&v)[W]) {
+        float big = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) big = fmaxf(big, fabsf(s[at + j] + v[j]));
+        if (__any_sync(0xffffffffu, big >= 16777216.f)) {
+            if (!moved) {
+                for (int i = 0; i < N; ++i) far[i] = 0;
+                moved = true;
+            }
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                far[at + j] = far[at + j] + __float2int_rn(s[at + j]);
+                s[at + j] = v[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j) s[at + j] += v[j];
+        }
+    }
+    // makes s the sums, rounded once
+    __device__ __forceinline__ void finish() {
+        if (!moved) return;
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = (float)whole(i);
+    }
+    __device__ __forceinline__ int32_t whole(int i) const {
+        return (moved ? far[i] : 0) + __float2int_rn(s[i]);
+    }
+};
+
 __device__ __forceinline__ void matmul_store(const MatmulParams &p, int64_t m, int64_t n, float v) {
     if (p.out_f32) ((float *)p.out)[m * p.out_st + n] = v;
     else ((bf16 *)p.out)[m * p.out_st + n] = from_f32<bf16>(v);
@@ -178,9 +224,8 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
     grid_dependents_launch();
     grid_dependency_wait();
 
-    int32_t sums[HALF];                          // this thread's channel, half of the tokens
-#pragma unroll
-    for (int i = 0; i < HALF; ++i) sums[i] = 0;
+    ExactSums<HALF> sums;                        // this thread's channel, half of the tokens
+    sums.clear();
     const int row = 32 * (warp & 3) + lane, half = warp >> 2;
 
     if (warp < kI8ConvWarps) {
@@ -197,8 +242,7 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
                 if constexpr (W == 8) tc::tmem_ld8(at + i, v);
                 else tc::tmem_ld16(at + i, v);
                 tc::tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < W; ++j) sums[i + j] += __float2int_rn(v[j]);
+                sums.add(i, v);
             }
             tc::fence_before_sync();
             __syncwarp();
@@ -279,12 +323,13 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
     __syncwarp();
 
     if (parts == 1) {
+        sums.finish();
         if (warp < kI8ConvWarps && n0 + row < p.N) {
             const float ws = p.w_scale[n0 + row], bias = matmul_bias(p, n0 + row);
 #pragma unroll
             for (int i = 0; i < HALF; ++i) {
                 const int64_t m = (int64_t)m0 + half * HALF + i;
-                if (m < p.M) matmul_store(p, m, n0 + row, matmul_value(sums[i], p.a_scale[m], ws, bias));
+                if (m < p.M) matmul_store(p, m, n0 + row, matmul_value(sums.s[i], p.a_scale[m], ws, bias));
             }
         }
     } else {
@@ -293,7 +338,7 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
         static_assert(NT * kI8Channels * 4 <= sizeof(S.raw_w) + sizeof(S.raw_a), "the sums fit");
         if (warp < kI8ConvWarps)
 #pragma unroll
-            for (int i = 0; i < HALF; ++i) part[(half * HALF + i) * kI8Channels + row] = sums[i];
+            for (int i = 0; i < HALF; ++i) part[(half * HALF + i) * kI8Channels + row] = sums.whole(i);
         cluster_sync();
         const int rows = (int)min((int64_t)NT, p.M - m0);
         const uint32_t base = tc::smem_u32(part);
@@ -302,7 +347,7 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
             if (nn >= p.N) continue;
             int32_t sum = 0;
             for (uint32_t r = 0; r < parts; ++r) sum += cluster_load(base + 4 * i, r);
-            matmul_store(p, m, nn, matmul_value(sum, p.a_scale[m], p.w_scale[nn], matmul_bias(p, nn)));
+            matmul_store(p, m, nn, matmul_value((float)sum, p.a_scale[m], p.w_scale[nn], matmul_bias(p, nn)));
         }
         cluster_sync();                          // before any CTA's memory goes
     }
@@ -313,6 +358,256 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
     if (tid == 0 && *abort) report(p.status, GDN_ERR_TIMEOUT);
 }
 
+// ------------------------------------------------------------------ pairs of CTAs
+//
+// Many tokens: two CTAs of a cluster make 256 channels x NT tokens (NT <= 256) with one
+// cta_group::2 product.  Each converts its own 128 channels into its TMEM and holds half of
+// the tokens in shared memory, as fp16 that a kernel before this one wrote: converting tokens
+// here as well would take 512 clocks of shared memory for 64 codes (128 bytes a clock: codes
+// and fp16 in, fp16 out to the tensor core), as many as their products take; without it they
+// take 320.
+//
+// Persistent: a pair takes tiles in turn.  Warps 0-7 move sums (a thread: one channel, 128
+// tokens), 8-11 convert, 12 copies, 13 issues products (in the first CTA of a pair).
+constexpr int kPairSumWarps = 8, kPairConvWarps = 4, kPairStages = 4;
+constexpr int kPairThreads = 32 * (kPairSumWarps + kPairConvWarps + 4);  // two warps idle
+constexpr int kPairTokens = 256;                 // most tokens of a tile
+constexpr int kPairColA = 256;                   // TMEM: sums, then four steps of operand A
+
+struct PairSmem {
+    uint8_t raw[kPairStages][kI8Channels * kI8Step];
+    uint8_t tok[kPairStages][2][kPairTokens / 2 * 128];      // [64-code block][token][128 bytes]
+    uint64_t full[kPairStages], conv[kPairStages], free[kPairStages], d_full, d_free;
+    uint32_t tmem;
+    int abort;
+};
+
+__device__ __forceinline__ void pair_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t add) {
+    asm volatile("{\n\t.reg .pred p, e;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(add) : "memory");
+}
+// Arrives on the barrier of both CTAs when the products issued so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t *bar) {
+    asm volatile("{\n\t.reg .pred e;\n\t.reg .b16 m;\n\t"
+                 "mov.b16 m, 3;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}"
+                 :: "r"(tc::smem_u32(bar)) : "memory");
+}
+// Arrives on the first CTA's barrier.  What it announces is ordered by tcgen05's own waits and
+// fences; with release.cluster the arrival alone would take 1300 clocks.
+__device__ __forceinline__ void pair_arrive(uint64_t *bar) {
+    uint32_t first;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(first) : "r"(tc::smem_u32(bar)));
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(first) : "memory");
+}
+
+template <int N> __device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
+}
+template <int N> __device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
+}
+// Registers a thread at launch, and then of the sums' warps, the converting ones and the rest;
+// a raise waits until the other warps' cuts cover it.
+constexpr int kPairRegs = 128, kPairSumRegs = 176, kPairConvRegs = 96, kPairRestRegs = 64;
+static_assert(2 * kPairSumRegs + kPairConvRegs + kPairRestRegs <= 4 * kPairRegs, "a raise waits forever");
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__ MatmulParams p,
+                      int NT, int tiles_m, int tiles) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    PairSmem &S = *reinterpret_cast<PairSmem *>(smem_raw);
+    if (tc::smem_u32(smem_raw) & 1023u) {        // the tiles' swizzle needs it; never seen
+        if (threadIdx.x == 0) report(p.status, GDN_ERR_CUDA);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int steps = (p.K + kI8Step - 1) / kI8Step;
+    volatile int *abort = &S.abort;
+
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;"
+                     :: "r"(tc::smem_u32(&S.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        S.abort = 0;
+        for (int i = 0; i < kPairStages; ++i) {
+            tc::mbar_init(&S.full[i], 1);
+            tc::mbar_init(&S.conv[i], 2 * kPairConvWarps);
+            tc::mbar_init(&S.free[i], 1);
+        }
+        tc::mbar_init(&S.d_full, 1);
+        tc::mbar_init(&S.d_free, 2 * kPairSumWarps);
+        tc::mbar_fence_init();
+        tc::prefetch_tmap(&maps.w);
+        tc::prefetch_tmap(&maps.a);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    cluster_sync();
+    tc::fence_after_sync();
+    const uint32_t tmem = S.tmem;
+    grid_dependents_launch();
+    grid_dependency_wait();
+
+    if (warp < kPairSumWarps) {
+        regs_up<kPairSumRegs>();
+        // groups of 16 tokens: this warp has groups q, q + 2, q + 4, ..
+        const int q = warp >> 2, row = 32 * (warp & 3) + lane, groups = NT / 16;
+        const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        uint32_t c = 0;                          // chunks so far
+        bool ok = true;
+        ExactSums<128> sums;
+        for (int tile = pair; tile < tiles && ok; tile += pairs) {
+            sums.clear();
+            for (int s = 0; s < steps; s += kI8Exact, ++c) {
+                if (!(ok = i8_wait<50>(&S.d_full, c & 1, abort))) break;
+                tc::fence_after_sync();
+                float v[2][16];
+                tc::tmem_ld16(at + 16 * q, v[0]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (q + 2 * i >= groups) continue;
+                    tc::tmem_wait_ld();
+                    if (i < 7 && q + 2 * i + 2 < groups) tc::tmem_ld16(at + 16 * (q + 2 * i + 2), v[(i + 1) & 1]);
+                    sums.add(16 * i, v[i & 1]);
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) pair_arrive(&S.d_free);
+            }
+            const int64_t n = (int64_t)(tile / tiles_m) * 256 + 128 * rank + row, m0 = (int64_t)(tile % tiles_m) * NT;
+            sums.finish();
+            if (ok && n < p.N) {
+                const float ws = p.w_scale[n], bias = matmul_bias(p, n);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (q + 2 * i >= groups) continue;
+                    const int64_t m = m0 + 16 * (q + 2 * i);
+                    float as[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) as[j] = __ldg(p.a_scale + min(m + j, p.M - 1));
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (m + j < p.M) matmul_store(p, m + j, n, matmul_value(sums.s[16 * i + j], as[j], ws, bias));
+                }
+            }
+            __syncwarp();
+        }
+    } else if (warp < kPairSumWarps + kPairConvWarps) {
+        regs_down<kPairConvRegs>();
+        const int row = 32 * (warp & 3) + lane;
+        const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kPairColA;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int tile = pair; tile < tiles && ok; tile += pairs)
+            for (int s = 0; s < steps; ++s, ++it) {
+                const int slot = it % kPairStages;
+                if (!(ok = i8_wait(&S.full[slot], (it / kPairStages) & 1, abort))) break;
+                tc::fence_after_sync();
+                uint4 codes[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    codes[c] = *reinterpret_cast<const uint4 *>(S.raw[slot] + tc::swz(row, c));
+#pragma unroll
+                for (int c = 0; c < 8; c += 2) {
+                    uint32_t r[16];
+                    i8_halves16(codes[c], r);
+                    i8_halves16(codes[c + 1], r + 8);
+                    i8_st16(at + 64 * slot + 8 * c, r);
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) pair_arrive(&S.conv[slot]);
+            }
+    } else {
+        regs_down<kPairRestRegs>();
+        if (warp == kPairSumWarps + kPairConvWarps) {
+            const uint32_t bytes = kI8Channels * kI8Step + NT / 2 * 256;
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += pairs) {
+                const int n0 = tile / tiles_m * 256 + 128 * rank, m0 = tile % tiles_m * NT + NT / 2 * rank;
+                for (int s = 0; s < steps; ++s, ++it) {
+                    const int slot = it % kPairStages;
+                    if (it >= kPairStages && !(ok = i8_wait(&S.free[slot], (it / kPairStages - 1) & 1, abort))) break;
+                    if (lane == 0) {
+                        tc::mbar_expect_tx(&S.full[slot], bytes);
+                        i8_load_2d(S.raw[slot], &maps.w, &S.full[slot], s * kI8Step, n0);
+                        i8_load_2d(S.tok[slot][0], &maps.a, &S.full[slot], s * kI8Step, m0);
+                        i8_load_2d(S.tok[slot][1], &maps.a, &S.full[slot], s * kI8Step + 64, m0);
+                    }
+                    __syncwarp();
+                }
+            }
+            // nothing may land after the CTA has left
+            for (uint32_t i = it < kPairStages ? 0 : it - kPairStages; i < it; ++i)
+                wait_bounded_poll<0>(&S.full[i % kPairStages], (i / kPairStages) & 1, nullptr);
+        } else if (warp == kPairSumWarps + kPairConvWarps + 1 && rank == 0) {
+            const uint32_t id = i8_idesc(256, NT);
+            uint32_t it = 0, c = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += pairs)
+                for (int s = 0; s < steps; ++s, ++it) {
+                    const int slot = it % kPairStages;
+                    if (s % kI8Exact == 0 && c > 0 && !(ok = i8_wait(&S.d_free, (c - 1) & 1, abort))) break;
+                    if (!(ok = i8_wait(&S.conv[slot], (it / kPairStages) & 1, abort))) break;
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int k = 0; k < kI8Step / 16; ++k)
+                        pair_mma(tmem, tmem + kPairColA + 64 * slot + 8 * k,
+                                 tc::sdesc(tc::smem_u32(S.tok[slot][k >> 2] + (k & 3) * 32), 0, 1024), id,
+                                 s % kI8Exact != 0 || k > 0);
+                    pair_commit(&S.free[slot]);
+                    if (s % kI8Exact == kI8Exact - 1 || s == steps - 1) {
+                        pair_commit(&S.d_full);
+                        ++c;
+                    }
+                }
+        }
+    }
+    __syncwarp();
+    tc::fence_before_sync();
+    cluster_sync();                              // the other CTA's products and arrivals are done
+    tc::fence_after_sync();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+    if (tid == 0 && *abort) report(p.status, GDN_ERR_TIMEOUT);
+}
+
+// Codes as fp16, rows `st` elements apart (a multiple of 8; what lies between K and st is not
+// read): a thread takes eight.
+__global__ void __launch_bounds__(256) matmul_i8_halves_kernel(const int8_t *a, int64_t a_st, __half *out,
+                                                               int64_t st, int64_t M, int32_t K, int vec) {
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int per = (K + 7) / 8;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * per; i += (int64_t)gridDim.x * 256) {
+        const int64_t m = i / per;
+        const int k = (int)(i - m * per) * 8;
+        const int8_t *src = a + m * a_st + k;
+        uint2 w = make_uint2(0, 0);
+        if (vec && k + 8 <= K) {
+            w = *reinterpret_cast<const uint2 *>(src);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (k + j < K) (j < 4 ? w.x : w.y) |= (uint32_t)(uint8_t)src[j] << (8 * (j & 3));
+        }
+        uint4 h;
+        i8_halves(w.x, h.x, h.y);
+        i8_halves(w.y, h.z, h.w);
+        *reinterpret_cast<uint4 *>(out + m * st + k) = h;
+    }
+}
+
 }  // namespace gdn
 
 namespace gdn_host {
@@ -321,15 +616,17 @@ using namespace gdn;
 
 namespace {
 
-// Rows of 128 codes at a time; a row's end and the rows' end read as zeros.
-bool code_map(CUtensorMap *m, const int8_t *ptr, int64_t rows, int64_t K, int64_t stride, int box_rows) {
+// Boxes of 128 bytes of `box_rows` rows; a row's end and the rows' end read as zeros.
+bool row_map(CUtensorMap *m, const void *ptr, bool half, int64_t rows, int64_t K, int64_t stride, int box_rows) {
     auto fn = tensor_map_encoder();
     if (!fn) return false;
+    const int size = half ? 2 : 1;
     cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? stride : (K + 15) / 16 * 16)};
-    cuuint32_t box[2] = {kI8Step, (cuuint32_t)box_rows}, unit[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(ptr), dims, strides, box, unit,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? stride * size : (K * size + 15) / 16 * 16)};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows}, unit[2] = {1, 1};
+    return fn(m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+              const_cast<void *>(ptr), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -362,7 +659,8 @@ gdn_status_t launch_tc(const MatmulParams &p, cudaStream_t st) {
     const int sms = sm_count(dev);
     if (sms <= 0) return GDN_ERR_CUDA;
     I8Maps maps;
-    if (!code_map(&maps.w, p.w, p.N, p.K, p.w_st, kI8Channels) || !code_map(&maps.a, p.a, p.M, p.K, p.a_st, NT))
+    if (!row_map(&maps.w, p.w, false, p.N, p.K, p.w_st, kI8Channels) ||
+        !row_map(&maps.a, p.a, false, p.M, p.K, p.a_st, NT))
         return GDN_ERR_CUDA;
     const int64_t tiles_m = (p.M + NT - 1) / NT, tiles = tiles_m * ((p.N + kI8Channels - 1) / kI8Channels);
     // as many ranges of K as keep every SM busy, of at least two steps each
@@ -386,16 +684,74 @@ gdn_status_t launch_tc(const MatmulParams &p, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, maps, p, (int)tiles_m) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+// Tokens of a tile: of the sizes that fill the pairs' last turn best, the largest.
+int pair_tokens(int64_t M, int64_t N, int pairs) {
+    const int64_t tiles_n = (N + 255) / 256;
+    int best = kPairTokens;
+    int64_t cost = -1;
+    for (int nt = kPairTokens; nt >= 96; nt -= 32) {     // a pair's product takes multiples of 32
+        const int64_t turns = (tiles_n * ((M + nt - 1) / nt) + pairs - 1) / pairs;
+        if (cost < 0 || turns * nt < cost) {
+            cost = turns * nt;
+            best = nt;
+        }
+    }
+    return best;
+}
+
+gdn_status_t launch_pair(const MatmulParams &p, void *ws, cudaStream_t st) {
+    auto kern = matmul_i8_pair_kernel;
+    constexpr int smem = sizeof(PairSmem);
+    static_assert(smem <= 227 * 1024, "one CTA fits on an SM");
+    static std::atomic<uint64_t> ready{0};   // one bit per device (beyond 63: set every time)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+    if (dev > 63 || !((ready.load() >> dev) & 1u)) {
+        cudaFuncAttributes built;
+        if (cudaFuncGetAttributes(&built, kern) != cudaSuccess) return GDN_ERR_CUDA;
+        if (built.numRegs != kPairRegs) return GDN_ERR_UNSUPPORTED;     // the raise would wait forever
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return GDN_ERR_CUDA;
+        if (dev <= 63) ready.fetch_or(1ull << dev);
+    }
+    const int sms = sm_count(dev);
+    if (sms <= 1) return GDN_ERR_CUDA;
+    const int pairs = sms / 2, NT = pair_tokens(p.M, p.N, pairs);
+    const int64_t tiles_m = (p.M + NT - 1) / NT, tiles = tiles_m * ((p.N + 255) / 256);
+    if (tiles > 0x3fffffff) return GDN_ERR_SHAPE;
+    const int64_t half_st = ((int64_t)p.K + 7) / 8 * 8;
+    I8Maps maps;
+    if (!row_map(&maps.w, p.w, false, p.N, p.K, p.w_st, kI8Channels) ||
+        !row_map(&maps.a, ws, true, p.M, p.K, half_st, NT / 2))
+        return GDN_ERR_CUDA;
+    const int64_t blocks = (p.M * (half_st / 8) + 255) / 256;
+    const bool vec = ((uintptr_t)p.a & 7u) == 0 && (p.M == 1 || p.a_st % 8 == 0);
+    if (launch_dependent(matmul_i8_halves_kernel, dim3((unsigned)(blocks < 16 * sms ? blocks : 16 * sms)), dim3(256),
+                         0, st, p.a, p.a_st, (__half *)ws, half_st, p.M, p.K, (int)vec) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    const unsigned grid = (unsigned)(2 * (tiles < pairs ? tiles : pairs));
+    return launch_dependent(kern, dim3(grid), dim3(kPairThreads), smem, st, maps, p, NT, (int)tiles_m,
+                            (int)tiles) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+constexpr int64_t kPairMinM = 96;                // fewer tokens: the other kernel
+
 }  // namespace
 
 bool matmul_i8_tc_supported(const MatmulParams &p, uint32_t flags) {
     const auto aligned = [](const int8_t *ptr, int64_t rows, int64_t st) {
         return ((uintptr_t)ptr & 15u) == 0 && (rows == 1 || st % 16 == 0);
     };
-    return !(flags & GDN_PREFILL_SIMT) && aligned(p.a, p.M, p.a_st) && aligned(p.w, p.N, p.w_st);
+    return !(flags & GDN_PREFILL_SIMT) && aligned(p.w, p.N, p.w_st) &&
+           (p.M >= kPairMinM || aligned(p.a, p.M, p.a_st));
 }
 
-gdn_status_t launch_matmul_i8_tc(const MatmulParams &p, cudaStream_t st) {
+size_t matmul_i8_tc_workspace(int64_t M, int64_t K) {
+    return M >= kPairMinM ? ((size_t)M * (size_t)((K + 7) / 8 * 8) * 2 + 255) / 256 * 256 : 0;
+}
+
+gdn_status_t launch_matmul_i8_tc(const MatmulParams &p, void *ws, cudaStream_t st) {
+    if (p.M >= kPairMinM) return launch_pair(p, ws, st);
     if (p.M <= 16) return launch_tc<16>(p, st);
     if (p.M <= 32) return launch_tc<32>(p, st);
     if (p.M <= 64) return launch_tc<64>(p, st);
