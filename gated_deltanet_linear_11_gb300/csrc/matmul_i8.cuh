@@ -26,7 +26,7 @@ __device__ __forceinline__ float matmul_value(float sum, float as, float ws, flo
 }
 
 __device__ __forceinline__ float matmul_bias(const MatmulParams &p, int64_t n) {
-    if (!p.bias) return 0.f;
+    if (!p.bias) return -0.f;       // leaves every value as it is
     return p.bias_f32 ? ((const float *)p.bias)[n] : to_f32(((const bf16 *)p.bias)[n]);
 }
 

@@ -3,8 +3,8 @@
 // sm_103a has no 8-bit integer form of tcgen05.mma, and its legacy integer path is a small
 // part of the fp16 rate.  An int8 is exact in fp16, a product of two is exact in fp32, and so
 // is a sum of 1024 of them (at most 2^24): the products run as kind::f16 with fp32 sums in
-// TMEM, which move to int32 registers every 1024 products.  The result is the exact integer
-// for any input, whatever the split.
+// TMEM, which move to registers every 896 products.  The result is the exact integer for any
+// input, whatever the split.
 //
 // Channels are the rows of the product (M = 128): their codes go from shared memory through
 // registers into TMEM as fp16, where the tensor core takes them as operand A.  Tokens are its
@@ -31,7 +31,8 @@ struct I8Maps {
 
 constexpr int kI8Channels = 128;    // channels of a tile
 constexpr int kI8Step = 128;        // codes of a row per step
-constexpr int kI8Exact = 8;         // steps whose sums fp32 holds exactly
+constexpr int kI8Exact = 7;         // steps whose sums, on top of kI8Near, fp32 holds exactly
+constexpr float kI8Near = 2097152.f;    // 2^21: 7 * 128 * 2^14 + 2^21 = 2^24
 constexpr int kI8ConvWarps = 8;
 constexpr int kI8Threads = 32 * (kI8ConvWarps + 2);
 
@@ -127,48 +128,52 @@ __device__ __forceinline__ int32_t cluster_load(uint32_t addr, uint32_t rank) {
     return v;
 }
 
-// Sums of a thread's outputs over the chunks: fp32 while they stay below 2^24, where additions
-// of whole numbers are exact, which ordinary codes never leave.  A warp in which one would
-// moves its sums to int32 words in local memory first (a conversion to integers runs at a
-// sixteenth of the rate of an addition, and as many registers again are not to be had).
+// Sums of a thread's outputs over the chunks: fp32 while they stay within kI8Near, so that the
+// next chunk's addition is exact, which ordinary codes never leave.  A warp in which one does
+// moves its sums to int32 words in local memory (a conversion to integers runs at an eighth of
+// the rate of an addition, and as many registers again are not to be had).
 template <int N> struct ExactSums {
     float s[N];
+    float big;                                   // largest |s| since the last look
     volatile int32_t far[N];
     bool moved;
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int i = 0; i < N; ++i) s[i] = 0.f;
+        big = 0.f;
         moved = false;
     }
-    // adds W whole numbers of at most 2^24 to elements at ..
+    // adds W whole numbers, sums of a chunk, to the elements from `at` on
     template <int W> __device__ __forceinline__ void add(int at, const float (&v)[W]) {
-        float big = 0.f;
 #pragma unroll
-        for (int j = 0; j < W; ++j) big = fmaxf(big, fabsf(s[at + j] + v[j]));
-        if (__any_sync(0xffffffffu, big >= 16777216.f)) {
-            if (!moved) {
-                for (int i = 0; i < N; ++i) far[i] = 0;
-                moved = true;
-            }
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                far[at + j] = far[at + j] + __float2int_rn(s[at + j]);
-                s[at + j] = v[j];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < W; ++j) s[at + j] += v[j];
+        for (int j = 0; j < W; j += 2) {
+            const float2 t = add_f32x2(make_float2(s[at + j], s[at + j + 1]), make_float2(v[j], v[j + 1]));
+            s[at + j] = t.x;
+            s[at + j + 1] = t.y;
+            big = fmaxf(big, fmaxf(fabsf(t.x), fabsf(t.y)));
         }
+    }
+    // before the same elements are added to again
+    __device__ __forceinline__ void settle() {
+        if (__any_sync(0xffffffffu, big > kI8Near)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                far[i] = (moved ? far[i] : 0) + __float2int_rn(s[i]);
+                s[i] = 0.f;
+            }
+            moved = true;
+        }
+        big = 0.f;
+    }
+    __device__ __forceinline__ int32_t whole(int i) const {
+        return (moved ? far[i] : 0) + __float2int_rn(s[i]);
     }
     // makes s the sums, rounded once
     __device__ __forceinline__ void finish() {
         if (!moved) return;
 #pragma unroll
         for (int i = 0; i < N; ++i) s[i] = (float)whole(i);
-    }
-    __device__ __forceinline__ int32_t whole(int i) const {
-        return (moved ? far[i] : 0) + __float2int_rn(s[i]);
     }
 };
 
@@ -247,6 +252,7 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) i8_arrive(&S.d_free[c & 1]);
+            sums.settle();
         };
         int drained = 0;
         bool ok = true;
@@ -360,27 +366,62 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
 
 // ------------------------------------------------------------------ pairs of CTAs
 //
-// Many tokens: two CTAs of a cluster make 256 channels x NT tokens (NT <= 256) with one
+// Many tokens: two CTAs of a cluster make 256 channels x NT tokens (NT = 128 or 256) with one
 // cta_group::2 product.  Each converts its own 128 channels into its TMEM and holds half of
 // the tokens in shared memory, as fp16 that a kernel before this one wrote: converting tokens
 // here as well would take 512 clocks of shared memory for 64 codes (128 bytes a clock: codes
 // and fp16 in, fp16 out to the tensor core), as many as their products take; without it they
-// take 320.
+// take 320.  A product of 16 codes takes 128 clocks for 256 tokens and no less for fewer
+// (operand A leaves TMEM at 32 bytes a clock), so a tile has as many tokens as there are.
 //
-// Persistent: a pair takes tiles in turn.  Warps 0-7 move sums (a thread: one channel, 128
-// tokens), 8-11 convert, 12 copies, 13 issues products (in the first CTA of a pair).
-constexpr int kPairSumWarps = 8, kPairConvWarps = 4, kPairStages = 4;
+// 256 columns of sums and four steps of operand A fill TMEM, so moving sums every 896 products
+// would leave the tensor core waiting a fifth of the time.  Most tiles need no move: with
+// |a|^2 and |w|^2 the sums of squares of a token's and a channel's codes, every partial sum is
+// at most |a||w| (Cauchy and Schwarz), and where that is at most 2^24 fp32 sums are exact to
+// the end.  |a|^2 comes with the fp16 tokens, |w|^2 from the converting warps when a tile is
+// done.  Tiles that turn out otherwise are made again with moves, after all others; tiles whose
+// tokens alone are above kPairCareful are made so at once.  Which it is changes no result.
+//
+// Persistent: a pair takes tiles in turn.  Warps 0-7 move sums (a thread: one channel, half of
+// the tokens), 8-11 convert, 12 copies, 13 issues products (in the first CTA of a pair).
+constexpr int kPairSumWarps = 8, kPairConvWarps = 4, kPairMaxStages = 4;
 constexpr int kPairThreads = 32 * (kPairSumWarps + kPairConvWarps + 4);  // two warps idle
 constexpr int kPairTokens = 256;                 // most tokens of a tile
-constexpr int kPairColA = 256;                   // TMEM: sums, then four steps of operand A
+constexpr int kPairCareful = 15000000;           // |a|^2: with a like |w|^2, near 2^24 squared
+constexpr int kPairMarks = 1024;                 // tiles of a pair with marks of their own
 
-struct PairSmem {
-    uint8_t raw[kPairStages][kI8Channels * kI8Step];
-    uint8_t tok[kPairStages][2][kPairTokens / 2 * 128];      // [64-code block][token][128 bytes]
-    uint64_t full[kPairStages], conv[kPairStages], free[kPairStages], d_full, d_free;
+struct PairShape {                               // of a launch
+    int NT, stages;                              // TMEM: 256 columns of sums, 64 a stage
+    uint32_t stage_bytes;                        // codes, then two 64-code blocks of tokens
+    int tiles_m, tiles;
+    const int32_t *squares;                      // |a|^2 of the tokens
+};
+struct PairBars {
+    uint64_t full[kPairMaxStages], conv[kPairMaxStages], free[kPairMaxStages], d_full[2], d_free[2];
+    uint32_t again[kPairMarks / 32];             // tiles to make again (the last mark: any after it too)
     uint32_t tmem;
     int abort;
 };
+constexpr uint32_t kPairRaw = kI8Channels * kI8Step;
+constexpr int kPairSmem = 208 * 1024 + (int)sizeof(PairBars);
+
+// Largest |a|^2 of the tile's tokens (a warp).
+__device__ __forceinline__ int32_t pair_squares(const PairShape &sh, int64_t M, int tile) {
+    const int64_t m0 = (int64_t)(tile % sh.tiles_m) * sh.NT;
+    int32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < kPairTokens / 32; ++i) {
+        const int64_t m = m0 + 32 * i + (threadIdx.x & 31);
+        if (32 * i < sh.NT && m < M) most = max(most, __ldg(sh.squares + m));
+    }
+    return __reduce_max_sync(0xffffffffu, most);
+}
+// Marks of both CTAs (turn: the pair's how manieth tile).
+__device__ __forceinline__ bool pair_marked(const PairBars &S, int turn) {
+    turn = min(turn, kPairMarks - 1);
+    const uint32_t at = tc::smem_u32(&S.again[turn >> 5]);
+    return ((cluster_load(at, 0) | cluster_load(at, 1)) >> (turn & 31)) & 1;
+}
 
 __device__ __forceinline__ void pair_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t add) {
     asm volatile("{\n\t.reg .pred p, e;\n\t"
@@ -418,16 +459,17 @@ static_assert(2 * kPairSumRegs + kPairConvRegs + kPairRestRegs <= 4 * kPairRegs,
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__ MatmulParams p,
-                      int NT, int tiles_m, int tiles) {
+                      const __grid_constant__ PairShape sh) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    PairSmem &S = *reinterpret_cast<PairSmem *>(smem_raw);
+    PairBars &S = *reinterpret_cast<PairBars *>(smem_raw + (kPairSmem - sizeof(PairBars)));
     if (tc::smem_u32(smem_raw) & 1023u) {        // the tiles' swizzle needs it; never seen
         if (threadIdx.x == 0) report(p.status, GDN_ERR_CUDA);
         return;
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int steps = (p.K + kI8Step - 1) / kI8Step;
+    const int steps = (p.K + kI8Step - 1) / kI8Step, NT = sh.NT, stages = sh.stages;
+    const int buffers = NT <= 128 ? 2 : 1;       // of sums
     volatile int *abort = &S.abort;
 
     if (warp == 0) {
@@ -437,13 +479,16 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
     }
     if (tid == 0) {
         S.abort = 0;
-        for (int i = 0; i < kPairStages; ++i) {
+        for (int i = 0; i < kPairMaxStages; ++i) {
             tc::mbar_init(&S.full[i], 1);
             tc::mbar_init(&S.conv[i], 2 * kPairConvWarps);
             tc::mbar_init(&S.free[i], 1);
         }
-        tc::mbar_init(&S.d_full, 1);
-        tc::mbar_init(&S.d_free, 2 * kPairSumWarps);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&S.d_full[i], 1);
+            tc::mbar_init(&S.d_free[i], 2 * kPairSumWarps);
+        }
+        for (int i = 0; i < kPairMarks / 32; ++i) S.again[i] = 0;
         tc::mbar_fence_init();
         tc::prefetch_tmap(&maps.w);
         tc::prefetch_tmap(&maps.a);
@@ -456,121 +501,171 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
     grid_dependents_launch();
     grid_dependency_wait();
 
+    // Every role goes over the pair's tiles twice; the second time over those marked by then.
     if (warp < kPairSumWarps) {
         regs_up<kPairSumRegs>();
-        // groups of 16 tokens: this warp has groups q, q + 2, q + 4, ..
+        // groups of 16 columns: this warp has q, q + 2, ..
         const int q = warp >> 2, row = 32 * (warp & 3) + lane, groups = NT / 16;
-        const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 16 * q;
         uint32_t c = 0;                          // chunks so far
         bool ok = true;
         ExactSums<128> sums;
-        for (int tile = pair; tile < tiles && ok; tile += pairs) {
-            sums.clear();
-            for (int s = 0; s < steps; s += kI8Exact, ++c) {
-                if (!(ok = i8_wait<50>(&S.d_full, c & 1, abort))) break;
-                tc::fence_after_sync();
-                float v[2][16];
-                tc::tmem_ld16(at + 16 * q, v[0]);
+        for (int pass = 0; pass < 2; ++pass) {
+            for (int tile = pair, turn = 0; tile < sh.tiles && ok; tile += pairs, ++turn) {
+                if (pass && !pair_marked(S, turn)) continue;
+                const int chunk = pass || pair_squares(sh, p.M, tile) > kPairCareful ? kI8Exact : steps;
+                sums.clear();
+                for (int s = 0; s < steps && ok; s += chunk) {
+                    const int buf = c & (buffers - 1);
+                    if (!(ok = i8_wait<20>(&S.d_full[buf], (c / buffers) & 1, abort))) break;
+                    ++c;
+                    tc::fence_after_sync();
+                    float v[2][16];
+                    tc::tmem_ld16(at + buf * 128, v[0]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (q + 2 * i >= groups) continue;
-                    tc::tmem_wait_ld();
-                    if (i < 7 && q + 2 * i + 2 < groups) tc::tmem_ld16(at + 16 * (q + 2 * i + 2), v[(i + 1) & 1]);
-                    sums.add(16 * i, v[i & 1]);
+                    for (int i = 0; i < 8; ++i) {
+                        if (q + 2 * i >= groups) continue;
+                        tc::tmem_wait_ld();
+                        if (i < 7 && q + 2 * i + 2 < groups) {
+                            tc::tmem_ld16(at + buf * 128 + 32 * (i + 1), v[(i + 1) & 1]);
+                        } else {                 // all read
+                            tc::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) pair_arrive(&S.d_free[buf]);
+                        }
+                        sums.add(16 * i, v[i & 1]);
+                    }
+                    if (chunk < steps) sums.settle();
                 }
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) pair_arrive(&S.d_free);
-            }
-            const int64_t n = (int64_t)(tile / tiles_m) * 256 + 128 * rank + row, m0 = (int64_t)(tile % tiles_m) * NT;
-            sums.finish();
-            if (ok && n < p.N) {
-                const float ws = p.w_scale[n], bias = matmul_bias(p, n);
+                sums.finish();
+                const int64_t n = (int64_t)(tile / sh.tiles_m) * 256 + 128 * rank + row;
+                const int64_t m0 = (int64_t)(tile % sh.tiles_m) * NT;
+                const bool in = ok && n < p.N;
+                const float ws = in ? p.w_scale[n] : 0.f, bias = in ? matmul_bias(p, n) : 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     if (q + 2 * i >= groups) continue;
                     const int64_t m = m0 + 16 * (q + 2 * i);
-                    float as[16];
+                    const float mine = p.a_scale[min(m + (lane & 15), p.M - 1)];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) as[j] = __ldg(p.a_scale + min(m + j, p.M - 1));
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (m + j < p.M) matmul_store(p, m + j, n, matmul_value(sums.s[16 * i + j], as[j], ws, bias));
+                    for (int j = 0; j < 16; ++j) {
+                        const float as = __shfl_sync(0xffffffffu, mine, j);
+                        if (in && m + j < p.M)
+                            matmul_store(p, m + j, n, matmul_value(sums.s[16 * i + j], as, ws, bias));
+                    }
                 }
+                __syncwarp();
             }
             __syncwarp();
+            if (pass == 0) cluster_sync();
         }
     } else if (warp < kPairSumWarps + kPairConvWarps) {
         regs_down<kPairConvRegs>();
         const int row = 32 * (warp & 3) + lane;
-        const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kPairColA;
-        uint32_t it = 0;
+        const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256;
+        int slot = 0;
+        uint32_t round = 0;
         bool ok = true;
-        for (int tile = pair; tile < tiles && ok; tile += pairs)
-            for (int s = 0; s < steps; ++s, ++it) {
-                const int slot = it % kPairStages;
-                if (!(ok = i8_wait(&S.full[slot], (it / kPairStages) & 1, abort))) break;
-                tc::fence_after_sync();
-                uint4 codes[8];
+        for (int pass = 0; pass < 2; ++pass) {
+            for (int tile = pair, turn = 0; tile < sh.tiles && ok; tile += pairs, ++turn) {
+                if (pass && !pair_marked(S, turn)) continue;
+                const int32_t tokens = pass ? 0 : pair_squares(sh, p.M, tile);
+                int32_t squares = 0;             // of this thread's channel
+                for (int s = 0; s < steps; ++s) {
+                    if (!(ok = i8_wait(&S.full[slot], round & 1, abort))) break;
+                    tc::fence_after_sync();
+                    const uint8_t *raw = smem_raw + slot * sh.stage_bytes;
+                    uint4 codes[8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    codes[c] = *reinterpret_cast<const uint4 *>(S.raw[slot] + tc::swz(row, c));
+                    for (int c = 0; c < 8; ++c) codes[c] = *reinterpret_cast<const uint4 *>(raw + tc::swz(row, c));
 #pragma unroll
-                for (int c = 0; c < 8; c += 2) {
-                    uint32_t r[16];
-                    i8_halves16(codes[c], r);
-                    i8_halves16(codes[c + 1], r + 8);
-                    i8_st16(at + 64 * slot + 8 * c, r);
+                    for (int c = 0; c < 8; c += 2) {
+                        uint32_t r[16];
+                        i8_halves16(codes[c], r);
+                        i8_halves16(codes[c + 1], r + 8);
+                        i8_st16(at + 64 * slot + 8 * c, r);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        squares = __dp4a((int)codes[c].x, (int)codes[c].x, squares);
+                        squares = __dp4a((int)codes[c].y, (int)codes[c].y, squares);
+                        squares = __dp4a((int)codes[c].z, (int)codes[c].z, squares);
+                        squares = __dp4a((int)codes[c].w, (int)codes[c].w, squares);
+                    }
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) pair_arrive(&S.conv[slot]);
+                    if (++slot == stages) slot = 0, ++round;
                 }
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) pair_arrive(&S.conv[slot]);
+                // 2^48 less what the product's rounding could hide
+                const bool far = (float)squares * (float)tokens > 2.8147e14f;
+                if (tokens <= kPairCareful && __any_sync(0xffffffffu, far) && lane == 0) {
+                    const int mark = min(turn, kPairMarks - 1);
+                    atomicOr(&S.again[mark >> 5], 1u << (mark & 31));
+                }
             }
+            __syncwarp();
+            if (pass == 0) cluster_sync();
+        }
     } else {
         regs_down<kPairRestRegs>();
-        if (warp == kPairSumWarps + kPairConvWarps) {
-            const uint32_t bytes = kI8Channels * kI8Step + NT / 2 * 256;
-            uint32_t it = 0;
-            bool ok = true;
-            for (int tile = pair; tile < tiles && ok; tile += pairs) {
-                const int n0 = tile / tiles_m * 256 + 128 * rank, m0 = tile % tiles_m * NT + NT / 2 * rank;
-                for (int s = 0; s < steps; ++s, ++it) {
-                    const int slot = it % kPairStages;
-                    if (it >= kPairStages && !(ok = i8_wait(&S.free[slot], (it / kPairStages - 1) & 1, abort))) break;
-                    if (lane == 0) {
-                        tc::mbar_expect_tx(&S.full[slot], bytes);
-                        i8_load_2d(S.raw[slot], &maps.w, &S.full[slot], s * kI8Step, n0);
-                        i8_load_2d(S.tok[slot][0], &maps.a, &S.full[slot], s * kI8Step, m0);
-                        i8_load_2d(S.tok[slot][1], &maps.a, &S.full[slot], s * kI8Step + 64, m0);
+        const bool copies = warp == kPairSumWarps + kPairConvWarps;
+        const bool products = warp == kPairSumWarps + kPairConvWarps + 1 && rank == 0;
+        const uint32_t bytes = kPairRaw + NT * 128, block = NT * 64, id = i8_idesc(256, NT);
+        int slot = 0, issued = 0;
+        uint32_t round = 0, c = 0;
+        bool ok = true;
+        for (int pass = 0; pass < 2; ++pass) {
+            for (int tile = pair, turn = 0; (copies || products) && tile < sh.tiles && ok; tile += pairs, ++turn) {
+                if (pass && !pair_marked(S, turn)) continue;
+                if (copies) {
+                    const int n0 = tile / sh.tiles_m * 256 + 128 * rank, m0 = tile % sh.tiles_m * NT + NT / 2 * rank;
+                    for (int s = 0; s < steps; ++s) {
+                        if (round > 0 && !(ok = i8_wait(&S.free[slot], (round - 1) & 1, abort))) break;
+                        if (lane == 0) {
+                            uint8_t *to = smem_raw + slot * sh.stage_bytes;
+                            tc::mbar_expect_tx(&S.full[slot], bytes);
+                            i8_load_2d(to, &maps.w, &S.full[slot], s * kI8Step, n0);
+                            i8_load_2d(to + kPairRaw, &maps.a, &S.full[slot], s * kI8Step, m0);
+                            i8_load_2d(to + kPairRaw + block, &maps.a, &S.full[slot], s * kI8Step + 64, m0);
+                        }
+                        __syncwarp();
+                        if (issued < stages) ++issued;
+                        if (++slot == stages) slot = 0, ++round;
                     }
-                    __syncwarp();
+                } else {
+                    const int chunk = pass || pair_squares(sh, p.M, tile) > kPairCareful ? kI8Exact : steps;
+                    for (int s = 0, left = 0; s < steps; ++s) {
+                        const int buf = c & (buffers - 1);
+                        const bool fresh = left == 0;
+                        if (fresh) {
+                            left = min(chunk, steps - s);
+                            if (c >= (uint32_t)buffers && !(ok = i8_wait(&S.d_free[buf], (c / buffers - 1) & 1, abort))) break;
+                        }
+                        if (!(ok = i8_wait(&S.conv[slot], round & 1, abort))) break;
+                        tc::fence_after_sync();
+                        const uint32_t tok = tc::smem_u32(smem_raw + slot * sh.stage_bytes + kPairRaw);
+#pragma unroll
+                        for (int k = 0; k < kI8Step / 16; ++k)
+                            pair_mma(tmem + buf * 128, tmem + 256 + 64 * slot + 8 * k,
+                                     tc::sdesc(tok + (k >> 2) * block + (k & 3) * 32, 0, 1024), id, !fresh || k > 0);
+                        pair_commit(&S.free[slot]);
+                        if (--left == 0) {
+                            pair_commit(&S.d_full[buf]);
+                            ++c;
+                        }
+                        if (++slot == stages) slot = 0, ++round;
+                    }
                 }
             }
-            // nothing may land after the CTA has left
-            for (uint32_t i = it < kPairStages ? 0 : it - kPairStages; i < it; ++i)
-                wait_bounded_poll<0>(&S.full[i % kPairStages], (i / kPairStages) & 1, nullptr);
-        } else if (warp == kPairSumWarps + kPairConvWarps + 1 && rank == 0) {
-            const uint32_t id = i8_idesc(256, NT);
-            uint32_t it = 0, c = 0;
-            bool ok = true;
-            for (int tile = pair; tile < tiles && ok; tile += pairs)
-                for (int s = 0; s < steps; ++s, ++it) {
-                    const int slot = it % kPairStages;
-                    if (s % kI8Exact == 0 && c > 0 && !(ok = i8_wait(&S.d_free, (c - 1) & 1, abort))) break;
-                    if (!(ok = i8_wait(&S.conv[slot], (it / kPairStages) & 1, abort))) break;
-                    tc::fence_after_sync();
-#pragma unroll
-                    for (int k = 0; k < kI8Step / 16; ++k)
-                        pair_mma(tmem, tmem + kPairColA + 64 * slot + 8 * k,
-                                 tc::sdesc(tc::smem_u32(S.tok[slot][k >> 2] + (k & 3) * 32), 0, 1024), id,
-                                 s % kI8Exact != 0 || k > 0);
-                    pair_commit(&S.free[slot]);
-                    if (s % kI8Exact == kI8Exact - 1 || s == steps - 1) {
-                        pair_commit(&S.d_full);
-                        ++c;
-                    }
-                }
+            __syncwarp();
+            if (pass == 0) cluster_sync();
+        }
+        // nothing may land after the CTA has left
+        for (int i = 0; i < issued; ++i) {
+            if (--slot < 0) slot = stages - 1, --round;
+            wait_bounded_poll<0>(&S.full[slot], round & 1, nullptr);
         }
     }
     __syncwarp();
@@ -582,16 +677,17 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
     if (tid == 0 && *abort) report(p.status, GDN_ERR_TIMEOUT);
 }
 
-// Codes as fp16, rows `st` elements apart (a multiple of 8; what lies between K and st is not
-// read): a thread takes eight.
-__global__ void __launch_bounds__(256) matmul_i8_halves_kernel(const int8_t *a, int64_t a_st, __half *out,
-                                                               int64_t st, int64_t M, int32_t K, int vec) {
+// Tokens' codes as fp16, rows `st` elements apart (a multiple of 8; what lies between K and st
+// is not read), and the sums of their squares: a warp per token, a lane takes eight codes.
+__global__ void __launch_bounds__(128) matmul_i8_tokens_kernel(const int8_t *a, int64_t a_st, __half *out, int64_t st,
+                                                               int32_t *squares, int64_t M, int32_t K, int vec) {
     grid_dependents_launch();
     grid_dependency_wait();
-    const int per = (K + 7) / 8;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * per; i += (int64_t)gridDim.x * 256) {
-        const int64_t m = i / per;
-        const int k = (int)(i - m * per) * 8;
+    const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (m >= M) return;
+    int32_t sum = 0;
+#pragma unroll 4
+    for (int k = (threadIdx.x & 31) * 8; k < K; k += 256) {
         const int8_t *src = a + m * a_st + k;
         uint2 w = make_uint2(0, 0);
         if (vec && k + 8 <= K) {
@@ -601,11 +697,14 @@ __global__ void __launch_bounds__(256) matmul_i8_halves_kernel(const int8_t *a, 
             for (int j = 0; j < 8; ++j)
                 if (k + j < K) (j < 4 ? w.x : w.y) |= (uint32_t)(uint8_t)src[j] << (8 * (j & 3));
         }
+        sum = __dp4a((int)w.x, (int)w.x, __dp4a((int)w.y, (int)w.y, sum));
         uint4 h;
         i8_halves(w.x, h.x, h.y);
         i8_halves(w.y, h.z, h.w);
         *reinterpret_cast<uint4 *>(out + m * st + k) = h;
     }
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if ((threadIdx.x & 31) == 0) squares[m] = sum;
 }
 
 }  // namespace gdn
@@ -684,24 +783,9 @@ gdn_status_t launch_tc(const MatmulParams &p, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, maps, p, (int)tiles_m) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-// Tokens of a tile: of the sizes that fill the pairs' last turn best, the largest.
-int pair_tokens(int64_t M, int64_t N, int pairs) {
-    const int64_t tiles_n = (N + 255) / 256;
-    int best = kPairTokens;
-    int64_t cost = -1;
-    for (int nt = kPairTokens; nt >= 96; nt -= 32) {     // a pair's product takes multiples of 32
-        const int64_t turns = (tiles_n * ((M + nt - 1) / nt) + pairs - 1) / pairs;
-        if (cost < 0 || turns * nt < cost) {
-            cost = turns * nt;
-            best = nt;
-        }
-    }
-    return best;
-}
-
 gdn_status_t launch_pair(const MatmulParams &p, void *ws, cudaStream_t st) {
     auto kern = matmul_i8_pair_kernel;
-    constexpr int smem = sizeof(PairSmem);
+    constexpr int smem = kPairSmem;
     static_assert(smem <= 227 * 1024, "one CTA fits on an SM");
     static std::atomic<uint64_t> ready{0};   // one bit per device (beyond 63: set every time)
     int dev = 0;
@@ -716,25 +800,33 @@ gdn_status_t launch_pair(const MatmulParams &p, void *ws, cudaStream_t st) {
     }
     const int sms = sm_count(dev);
     if (sms <= 1) return GDN_ERR_CUDA;
-    const int pairs = sms / 2, NT = pair_tokens(p.M, p.N, pairs);
+    const int pairs = sms / 2, NT = p.M <= 128 ? 128 : 256;
     const int64_t tiles_m = (p.M + NT - 1) / NT, tiles = tiles_m * ((p.N + 255) / 256);
     if (tiles > 0x3fffffff) return GDN_ERR_SHAPE;
+    gdn::PairShape sh;
+    sh.NT = NT;
+    sh.stage_bytes = gdn::kPairRaw + NT * 128;
+    sh.stages = (int)(208 * 1024 / sh.stage_bytes);
+    if (sh.stages > 4) sh.stages = 4;           // 64 of TMEM's columns each
+    sh.tiles_m = (int)tiles_m;
+    sh.tiles = (int)tiles;
     const int64_t half_st = ((int64_t)p.K + 7) / 8 * 8;
+    int32_t *squares = (int32_t *)((uint8_t *)ws + ((size_t)p.M * half_st * 2 + 255) / 256 * 256);
+    sh.squares = squares;
     I8Maps maps;
     if (!row_map(&maps.w, p.w, false, p.N, p.K, p.w_st, kI8Channels) ||
         !row_map(&maps.a, ws, true, p.M, p.K, half_st, NT / 2))
         return GDN_ERR_CUDA;
-    const int64_t blocks = (p.M * (half_st / 8) + 255) / 256;
     const bool vec = ((uintptr_t)p.a & 7u) == 0 && (p.M == 1 || p.a_st % 8 == 0);
-    if (launch_dependent(matmul_i8_halves_kernel, dim3((unsigned)(blocks < 16 * sms ? blocks : 16 * sms)), dim3(256),
-                         0, st, p.a, p.a_st, (__half *)ws, half_st, p.M, p.K, (int)vec) != cudaSuccess)
+    if (launch_dependent(matmul_i8_tokens_kernel, dim3((unsigned)((p.M + 3) / 4)), dim3(128), 0, st, p.a, p.a_st,
+                         (__half *)ws, half_st, (int32_t *)squares, p.M, p.K, (int)vec) != cudaSuccess)
         return GDN_ERR_CUDA;
     const unsigned grid = (unsigned)(2 * (tiles < pairs ? tiles : pairs));
-    return launch_dependent(kern, dim3(grid), dim3(kPairThreads), smem, st, maps, p, NT, (int)tiles_m,
-                            (int)tiles) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return launch_dependent(kern, dim3(grid), dim3(kPairThreads), smem, st, maps, p,
+                            sh) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-constexpr int64_t kPairMinM = 96;                // fewer tokens: the other kernel
+constexpr int64_t kPairMinM = 65;                // fewer tokens: the other kernel
 
 }  // namespace
 
@@ -747,15 +839,14 @@ bool matmul_i8_tc_supported(const MatmulParams &p, uint32_t flags) {
 }
 
 size_t matmul_i8_tc_workspace(int64_t M, int64_t K) {
-    return M >= kPairMinM ? ((size_t)M * (size_t)((K + 7) / 8 * 8) * 2 + 255) / 256 * 256 : 0;
+    return M >= kPairMinM ? ((size_t)M * (size_t)((K + 7) / 8 * 8) * 2 + 255) / 256 * 256 + (size_t)M * 4 : 0;
 }
 
 gdn_status_t launch_matmul_i8_tc(const MatmulParams &p, void *ws, cudaStream_t st) {
     if (p.M >= kPairMinM) return launch_pair(p, ws, st);
     if (p.M <= 16) return launch_tc<16>(p, st);
     if (p.M <= 32) return launch_tc<32>(p, st);
-    if (p.M <= 64) return launch_tc<64>(p, st);
-    return launch_tc<128>(p, st);
+    return launch_tc<64>(p, st);
 }
 
 }  // namespace gdn_host

@@ -154,3 +154,18 @@ def test_graphs_and_streams(M):
             assert_bits_equal(got.cpu(), exp, "out")
             got.zero_()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("M", [70, 128, 200, 300, 600])
+def test_some_tiles_with_large_sums(M):
+    """Ordinary codes but for a few tokens or channels whose sums pass 2^24 on the way, alone
+    and together; 700 channels are more than one tile of them."""
+    K, N = 6144, 700
+    a, w = codes(1, M, K, -30, 30), codes(2, N, K, -30, 30)
+    check(a, w, dtype=F32)
+    w[130:140], w[699] = 127, -128
+    check(a, w, dtype=F32)
+    a[M // 2], a[M - 1] = -128, 127
+    check(a, w, dtype=F32)
+    w[:] = codes(2, N, K, -30, 30)
+    check(a, w, dtype=F32)
