@@ -129,7 +129,7 @@ def load(path: str = LIB_PATH):
         "gdn_quantize_rows": ([vp, vp, vp, vp], i32),
         "gdn_add_rmsnorm": ([vp, vp, vp, vp, f32, f32, vp, vp, vp], i32),
         "gdn_gated_rmsnorm": ([vp, vp, vp, f32, vp, vp, vp], i32),
-        "gdn_matmul_i8_workspace_size": ([i64, i64, i64, u32], size),
+        "gdn_matmul_i8_workspace_size": ([vp, vp, u32], size),
         "gdn_matmul_i8": ([vp, vp, vp, vp, vp, vp, u32, vp, size, vp, vp], i32),
         "gdn_selftest_bounded_wait": ([vp, vp], i32),
     }

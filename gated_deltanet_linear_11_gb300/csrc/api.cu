@@ -854,6 +854,22 @@ gdn_status_t norm_args(const gdn_matrix_t *weight, int64_t width, float eps, con
     return GDN_OK;
 }
 
+// The operands of a product.
+gdn_status_t matmul_args(const gdn_matrix_t *a, const gdn_matrix_t *w, gdn::MatmulParams &p) {
+    Matrix A, W;
+    gdn_status_t s;
+    if ((s = matrix_of(a, GDN_I8, A)) != GDN_OK) return s;
+    if ((s = matrix_of(w, GDN_I8, W)) != GDN_OK) return s;
+    if (A.cols != W.cols || A.cols < 1) return GDN_ERR_SHAPE;
+    if (A.rows > 0x7fff0000 || W.rows > 0x7fff0000) return GDN_ERR_SHAPE;    // tiles past the end
+    if (A.cols > GDN_MATMUL_MAX_K) return GDN_ERR_UNSUPPORTED;
+    memset(&p, 0, sizeof(p));
+    p.a = (const int8_t *)A.ptr; p.a_st = A.st; p.M = A.rows;
+    p.w = (const int8_t *)W.ptr; p.w_st = W.st; p.N = W.rows;
+    p.K = (int32_t)A.cols;
+    return GDN_OK;
+}
+
 gdn::RowParams row_params(int64_t T, int64_t D) {
     gdn::RowParams p;
     memset(&p, 0, sizeof(p));
@@ -940,9 +956,9 @@ gdn_status_t gdn_gated_rmsnorm(const gdn_tensor_t *x, const gdn_tensor_t *z,
                                  (cudaStream_t)stream);
 }
 
-size_t gdn_matmul_i8_workspace_size(int64_t M, int64_t N, int64_t K, uint32_t flags) {
-    if (M <= 0 || N <= 0 || K <= 0 || K > GDN_MATMUL_MAX_K) return 0;
-    return gdn_host::matmul_i8_workspace(M, N, K, flags);
+size_t gdn_matmul_i8_workspace_size(const gdn_matrix_t *a, const gdn_matrix_t *w, uint32_t flags) {
+    gdn::MatmulParams p;
+    return matmul_args(a, w, p) == GDN_OK && p.M > 0 && p.N > 0 ? gdn_host::matmul_i8_workspace(p, flags) : 0;
 }
 
 gdn_status_t gdn_matmul_i8(const gdn_matrix_t *a, const float *a_scale, const gdn_matrix_t *w,
@@ -950,33 +966,31 @@ gdn_status_t gdn_matmul_i8(const gdn_matrix_t *a, const float *a_scale, const gd
                            const gdn_matrix_t *out, uint32_t flags, void *workspace,
                            size_t workspace_bytes, int32_t *status_dev, void *stream) {
     gdn_host::CallRange nvtx_range("gdn_matmul_i8");
-    Matrix A, W, B, O;
+    gdn::MatmulParams p;
+    Matrix B, O;
     gdn_status_t s;
-    if ((s = matrix_of(a, GDN_I8, A)) != GDN_OK) return s;
-    if ((s = matrix_of(w, GDN_I8, W)) != GDN_OK) return s;
+    if ((s = matmul_args(a, w, p)) != GDN_OK) return s;
     if ((s = matrix_of(out, -1, O)) != GDN_OK) return s;
-    if (A.cols != W.cols || A.cols < 1 || O.rows != A.rows || O.cols != W.rows) return GDN_ERR_SHAPE;
-    if (A.rows > 0x7fff0000 || W.rows > 0x7fff0000) return GDN_ERR_SHAPE;    // tiles past the end
-    if (A.cols > GDN_MATMUL_MAX_K) return GDN_ERR_UNSUPPORTED;
+    if (O.rows != p.M || O.cols != p.N) return GDN_ERR_SHAPE;
     if (bias) {
         if ((s = matrix_of(bias, -1, B)) != GDN_OK) return s;
-        if (B.rows != 1 || B.cols != W.rows) return GDN_ERR_SHAPE;
+        if (B.rows != 1 || B.cols != p.N) return GDN_ERR_SHAPE;
+        p.bias = B.ptr;
+        p.bias_f32 = B.dtype == GDN_F32;
     }
-    if (A.rows == 0 || W.rows == 0) return GDN_OK;
+    if (p.M == 0 || p.N == 0) return GDN_OK;
     if (!a_scale || !w_scale) return GDN_ERR_NULL;
     if (((uintptr_t)a_scale | (uintptr_t)w_scale) & 3u) return GDN_ERR_LAYOUT;
-    gdn::MatmulParams p;
-    memset(&p, 0, sizeof(p));
-    p.a = (const int8_t *)A.ptr; p.a_st = A.st; p.a_scale = a_scale;
-    p.w = (const int8_t *)W.ptr; p.w_st = W.st; p.w_scale = w_scale;
-    if (bias) { p.bias = B.ptr; p.bias_f32 = B.dtype == GDN_F32; }
-    p.out = O.ptr; p.out_st = O.st; p.out_f32 = O.dtype == GDN_F32;
-    p.M = A.rows; p.N = W.rows; p.K = (int32_t)A.cols;
+    p.a_scale = a_scale;
+    p.w_scale = w_scale;
+    p.out = O.ptr;
+    p.out_st = O.st;
+    p.out_f32 = O.dtype == GDN_F32;
     p.status = status_dev;
-    const size_t need = gdn_matmul_i8_workspace_size(p.M, p.N, p.K, flags);
+    const size_t need = gdn_host::matmul_i8_workspace(p, flags);
     if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)))
         return GDN_ERR_WORKSPACE;
-    return gdn_host::launch_matmul_i8(p, flags, workspace, workspace_bytes, (cudaStream_t)stream);
+    return gdn_host::launch_matmul_i8(p, flags, workspace, (cudaStream_t)stream);
 }
 
 gdn_status_t gdn_selftest_bounded_wait(int32_t *status_dev, void *stream) {

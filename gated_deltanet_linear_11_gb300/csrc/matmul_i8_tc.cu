@@ -1,33 +1,22 @@
-// matmul_i8_tc.cu -- gdn_matmul_i8 on tcgen05.
+// matmul_i8_tc.cu -- gdn_matmul_i8 for many tokens, on tcgen05.
 //
 // sm_103a has no 8-bit integer form of tcgen05.mma, and its legacy integer path is a small
 // part of the fp16 rate.  An int8 is exact in fp16, a product of two is exact in fp32, and so
-// is a sum of 1024 of them (at most 2^24): the products run as kind::f16 with fp32 sums in
-// TMEM, which move to registers every 896 products.  The result is the exact integer for any
-// input, whatever the split.
+// is every sum of them that stays within 2^24 (1024 products of any codes): the products run
+// as kind::f16 with fp32 sums in TMEM, and sums move to registers before they could pass 2^24.
+// The result is the exact integer for any input, whatever the split.
 //
-// Channels are the rows of the product (M = 128): their codes go from shared memory through
-// registers into TMEM as fp16, where the tensor core takes them as operand A.  Tokens are its
-// columns: converted into fp16 tiles in shared memory, operand B.
+// Channels are the rows of the product (M = 256, half in either CTA of a pair): their codes go
+// from shared memory through registers into TMEM as fp16, where the tensor core takes them as
+// operand A.  Tokens are its columns, operand B.
 //
-// A CTA makes 128 channels x NT tokens over a range of K; the CTAs of a cluster share a tile
-// by ranges of K and add up their int32 sums through distributed shared memory.
-//
-// Conversion: x ^ 0x80 is x + 128 in 0..255; as the low byte of 0x6400 that is the fp16
-// number 1024 + 128 + x, less 1152 (exact).  Two bytes take a byte permute and a subtraction.
 #include <atomic>
 
 #include "bulk_ptx.cuh"
 #include "matmul_i8.cuh"
 #include "tmap.cuh"
 
-#include <cuda_fp16.h>
-
 namespace gdn {
-
-struct I8Maps {
-    CUtensorMap w, a;               // boxes of 128 and NT rows of 128 codes
-};
 
 constexpr int kI8Channels = 128;    // channels of a tile
 constexpr int kI8Step = 128;        // codes of a row per step
@@ -82,22 +71,6 @@ __device__ __forceinline__ void i8_st16(uint32_t taddr, const uint32_t (&r)[16])
                  :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
                     "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
                     "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
-}
-__device__ __forceinline__ void i8_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3}], [%4];"
-                 :: "r"(tc::smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(tc::smem_u32(bar)) : "memory");
-}
-
-// Four codes as fp16 pairs (elements 0 and 1, 2 and 3).
-__device__ __forceinline__ void i8_halves(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    const uint32_t u = w ^ 0x80808080u;
-    const __half2 less = __floats2half2_rn(1152.f, 1152.f);
-    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&a), less);
-    const __half2 y = __hsub2(*reinterpret_cast<__half2 *>(&b), less);
-    lo = *reinterpret_cast<const uint32_t *>(&x);
-    hi = *reinterpret_cast<const uint32_t *>(&y);
 }
 // 16 codes: eight words of fp16 pairs.
 __device__ __forceinline__ void i8_halves16(const uint4 &v, uint32_t *r) {
@@ -177,11 +150,11 @@ template <int N> struct ExactSums {
     }
 };
 
-__device__ __forceinline__ void matmul_store(const MatmulParams &p, int64_t m, int64_t n, float v) {
-    if (p.out_f32) ((float *)p.out)[m * p.out_st + n] = v;
-    else ((bf16 *)p.out)[m * p.out_st + n] = from_f32<bf16>(v);
-}
-
+// ------------------------------------------------------------------ up to 64 tokens
+//
+// A CTA makes 128 channels x NT tokens over a range of K; the CTAs of a cluster share a tile
+// by ranges of K and add up their int32 sums through distributed shared memory.  Tokens are
+// converted into fp16 tiles in shared memory.
 template <int NT>
 __global__ void __launch_bounds__(kI8Threads, I8Shape<NT>::CTAS)
 matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__ MatmulParams p, int tiles_m) {
@@ -301,8 +274,8 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
             if (s >= Sh::STAGES && !i8_wait(&S.raw_free[slot], ((s / Sh::STAGES) - 1) & 1, abort)) break;
             if (lane == 0) {
                 tc::mbar_expect_tx(&S.raw_full[slot], Sh::RAW_W + Sh::RAW_A);
-                i8_load_2d(S.raw_w[slot], &maps.w, &S.raw_full[slot], (first + s) * kI8Step, n0);
-                i8_load_2d(S.raw_a[slot], &maps.a, &S.raw_full[slot], (first + s) * kI8Step, m0);
+                load_2d(S.raw_w[slot], &maps.w, &S.raw_full[slot], (first + s) * kI8Step, n0);
+                load_2d(S.raw_a[slot], &maps.a, &S.raw_full[slot], (first + s) * kI8Step, m0);
             }
             __syncwarp();
             issued = s + 1;
@@ -626,9 +599,9 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
                         if (lane == 0) {
                             uint8_t *to = smem_raw + slot * sh.stage_bytes;
                             tc::mbar_expect_tx(&S.full[slot], bytes);
-                            i8_load_2d(to, &maps.w, &S.full[slot], s * kI8Step, n0);
-                            i8_load_2d(to + kPairRaw, &maps.a, &S.full[slot], s * kI8Step, m0);
-                            i8_load_2d(to + kPairRaw + block, &maps.a, &S.full[slot], s * kI8Step + 64, m0);
+                            load_2d(to, &maps.w, &S.full[slot], s * kI8Step, n0);
+                            load_2d(to + kPairRaw, &maps.a, &S.full[slot], s * kI8Step, m0);
+                            load_2d(to + kPairRaw + block, &maps.a, &S.full[slot], s * kI8Step + 64, m0);
                         }
                         __syncwarp();
                         if (issued < stages) ++issued;
@@ -715,32 +688,6 @@ using namespace gdn;
 
 namespace {
 
-// Boxes of 128 bytes of `box_rows` rows; a row's end and the rows' end read as zeros.
-bool row_map(CUtensorMap *m, const void *ptr, bool half, int64_t rows, int64_t K, int64_t stride, int box_rows) {
-    auto fn = tensor_map_encoder();
-    if (!fn) return false;
-    const int size = half ? 2 : 1;
-    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? stride * size : (K * size + 15) / 16 * 16)};
-    cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows}, unit[2] = {1, 1};
-    return fn(m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-              const_cast<void *>(ptr), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int sm_count(int dev) {
-    static std::atomic<int> known[64];
-    if (dev < 64) {
-        const int n = known[dev].load();
-        if (n > 0) return n;
-    }
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 0;
-    if (dev < 64) known[dev].store(n);
-    return n;
-}
-
 template <int NT>
 gdn_status_t launch_tc(const MatmulParams &p, cudaStream_t st) {
     using Sh = I8Shape<NT>;
@@ -755,11 +702,11 @@ gdn_status_t launch_tc(const MatmulParams &p, cudaStream_t st) {
             return GDN_ERR_CUDA;
         if (dev <= 63) ready.fetch_or(1ull << dev);
     }
-    const int sms = sm_count(dev);
+    const int sms = matmul_sm_count(dev);
     if (sms <= 0) return GDN_ERR_CUDA;
     I8Maps maps;
-    if (!row_map(&maps.w, p.w, false, p.N, p.K, p.w_st, kI8Channels) ||
-        !row_map(&maps.a, p.a, false, p.M, p.K, p.a_st, NT))
+    if (!row_map(&maps.w, p.w, false, p.N, p.K, p.w_st, kI8Channels, true) ||
+        !row_map(&maps.a, p.a, false, p.M, p.K, p.a_st, NT, true))
         return GDN_ERR_CUDA;
     const int64_t tiles_m = (p.M + NT - 1) / NT, tiles = tiles_m * ((p.N + kI8Channels - 1) / kI8Channels);
     // as many ranges of K as keep every SM busy, of at least two steps each
@@ -782,8 +729,9 @@ gdn_status_t launch_tc(const MatmulParams &p, cudaStream_t st) {
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, maps, p, (int)tiles_m) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
+}  // namespace
 
-gdn_status_t launch_pair(const MatmulParams &p, void *ws, cudaStream_t st) {
+gdn_status_t launch_matmul_i8_pair(const MatmulParams &p, void *ws, cudaStream_t st) {
     auto kern = matmul_i8_pair_kernel;
     constexpr int smem = kPairSmem;
     static_assert(smem <= 227 * 1024, "one CTA fits on an SM");
@@ -798,7 +746,7 @@ gdn_status_t launch_pair(const MatmulParams &p, void *ws, cudaStream_t st) {
             return GDN_ERR_CUDA;
         if (dev <= 63) ready.fetch_or(1ull << dev);
     }
-    const int sms = sm_count(dev);
+    const int sms = matmul_sm_count(dev);
     if (sms <= 1) return GDN_ERR_CUDA;
     const int pairs = sms / 2, NT = p.M <= 128 ? 128 : 256;
     const int64_t tiles_m = (p.M + NT - 1) / NT, tiles = tiles_m * ((p.N + 255) / 256);
@@ -814,8 +762,8 @@ gdn_status_t launch_pair(const MatmulParams &p, void *ws, cudaStream_t st) {
     int32_t *squares = (int32_t *)((uint8_t *)ws + ((size_t)p.M * half_st * 2 + 255) / 256 * 256);
     sh.squares = squares;
     I8Maps maps;
-    if (!row_map(&maps.w, p.w, false, p.N, p.K, p.w_st, kI8Channels) ||
-        !row_map(&maps.a, ws, true, p.M, p.K, half_st, NT / 2))
+    if (!row_map(&maps.w, p.w, false, p.N, p.K, p.w_st, kI8Channels, true) ||
+        !row_map(&maps.a, ws, true, p.M, p.K, half_st, NT / 2, true))
         return GDN_ERR_CUDA;
     const bool vec = ((uintptr_t)p.a & 7u) == 0 && (p.M == 1 || p.a_st % 8 == 0);
     if (launch_dependent(matmul_i8_tokens_kernel, dim3((unsigned)((p.M + 3) / 4)), dim3(128), 0, st, p.a, p.a_st,
@@ -826,27 +774,14 @@ gdn_status_t launch_pair(const MatmulParams &p, void *ws, cudaStream_t st) {
                             sh) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-constexpr int64_t kPairMinM = 65;                // fewer tokens: the other kernel
-
-}  // namespace
-
-bool matmul_i8_tc_supported(const MatmulParams &p, uint32_t flags) {
-    const auto aligned = [](const int8_t *ptr, int64_t rows, int64_t st) {
-        return ((uintptr_t)ptr & 15u) == 0 && (rows == 1 || st % 16 == 0);
-    };
-    return !(flags & GDN_PREFILL_SIMT) && aligned(p.w, p.N, p.w_st) &&
-           (p.M >= kPairMinM || aligned(p.a, p.M, p.a_st));
-}
-
-size_t matmul_i8_tc_workspace(int64_t M, int64_t K) {
-    return M >= kPairMinM ? ((size_t)M * (size_t)((K + 7) / 8 * 8) * 2 + 255) / 256 * 256 + (size_t)M * 4 : 0;
-}
-
-gdn_status_t launch_matmul_i8_tc(const MatmulParams &p, void *ws, cudaStream_t st) {
-    if (p.M >= kPairMinM) return launch_pair(p, ws, st);
+gdn_status_t launch_matmul_i8_few(const MatmulParams &p, cudaStream_t st) {
     if (p.M <= 16) return launch_tc<16>(p, st);
     if (p.M <= 32) return launch_tc<32>(p, st);
     return launch_tc<64>(p, st);
+}
+
+size_t matmul_i8_pair_workspace(int64_t M, int64_t K) {
+    return ((size_t)M * (size_t)((K + 7) / 8 * 8) * 2 + 255) / 256 * 256 + (size_t)M * 4;
 }
 
 }  // namespace gdn_host

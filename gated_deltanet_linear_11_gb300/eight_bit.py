@@ -139,9 +139,10 @@ def gdn_gated_rmsnorm(x, z, weight, eps=1e-6, eight_bit=False, y=None, scale=Non
     return (y, scale) if eight_bit else y
 
 
-def gdn_matmul_i8_workspace_size(M, N, K, simt=False):
-    """Workspace bytes of gdn_matmul_i8."""
-    return int(_lib.load().gdn_matmul_i8_workspace_size(M, N, K, GDN_PREFILL_SIMT if simt else 0))
+def gdn_matmul_i8_workspace_size(a, w, simt=False):
+    """Workspace bytes of gdn_matmul_i8 (by the sizes and the alignment of a and w)."""
+    return int(_lib.load().gdn_matmul_i8_workspace_size(
+        _matrix("a", a, _I8), _matrix("w", w, _I8), GDN_PREFILL_SIMT if simt else 0))
 
 
 @_on_device
@@ -167,7 +168,7 @@ def gdn_matmul_i8(a, a_scale, w, w_scale, bias=None, dtype=torch.bfloat16, out=N
     elif out.shape != shape:
         raise ValueError("out must be of shape %s, got %s" % (tuple(shape), tuple(out.shape)))
     flags = (GDN_PREFILL_SIMT if simt else 0) | debug
-    ws_bytes = lib.gdn_matmul_i8_workspace_size(M, N, K, flags)
+    ws_bytes = lib.gdn_matmul_i8_workspace_size(ma, mw, flags)
     workspace = _scratch(workspace, ws_bytes, a)
     rc = lib.gdn_matmul_i8(ma, a_scale.data_ptr(), mw, w_scale.data_ptr(),
                            _vector("bias", bias, N, _DT), _matrix("out", out, _DT), flags,

@@ -564,12 +564,14 @@ gdn_status_t gdn_gated_rmsnorm(const gdn_tensor_t *x, const gdn_tensor_t *z,
  * GDN_MATMUL_MAX_K, so that the sum, which is exact, fits 32 bits; it is then rounded to fp32,
  * and so is each of the two products and the addition after it, in this order.  Every output
  * is the same bits whatever the other rows and channels, the layout and the kernel are.
- * workspace: device scratch of gdn_matmul_i8_workspace_size() bytes, 256-byte aligned (may be
- * NULL when 0).  flags: GDN_PREFILL_SIMT forces the CUDA-core kernel.
+ * Rows of a or w that do not start on 16 bytes are first copied to the workspace.
+ * workspace: device scratch of gdn_matmul_i8_workspace_size() bytes (which looks at the sizes
+ * and the alignment of a and w), 256-byte aligned (may be NULL when 0).
+ * flags: GDN_PREFILL_SIMT forces the CUDA-core kernel.
  */
 #define GDN_MATMUL_MAX_K 131071
 
-size_t gdn_matmul_i8_workspace_size(int64_t M, int64_t N, int64_t K, uint32_t flags);
+size_t gdn_matmul_i8_workspace_size(const gdn_matrix_t *a, const gdn_matrix_t *w, uint32_t flags);
 
 gdn_status_t gdn_matmul_i8(const gdn_matrix_t *a, const float *a_scale, const gdn_matrix_t *w,
                            const float *w_scale, const gdn_matrix_t *bias,

@@ -97,8 +97,25 @@ def test_matmul_i8_refusals(lib):
     assert call(bias=mat(1, 8, I8)) == 4
     assert call(a=mat(4, 131072, I8), w=mat(8, 131072, I8)) == 6
     assert call(a=mat(0, 64, I8, ptr=None), sa=None, out=mat(0, 8, ptr=None)) == 0
-    f = lib.gdn_matmul_i8_workspace_size
-    assert f(0, 8, 64, 0) == f(4, 0, 64, 0) == f(4, 8, 0, 0) == f(4, 8, 131072, 0) == 0
+
+
+def test_matmul_i8_workspace(lib):
+    """fp16 tokens and a sum of squares each for more than 64 tokens, and copies of rows that
+    do not start on 16 bytes."""
+    def f(a, w, flags=0):
+        return lib.gdn_matmul_i8_workspace_size(ref(a), ref(w), flags)
+    w = mat(8, 64, I8)
+    assert f(mat(0, 64, I8), w) == f(mat(4, 64, I8), mat(0, 64, I8)) == 0
+    assert f(mat(4, 0, I8), mat(8, 0, I8)) == f(mat(4, 64, I8), mat(8, 63, I8)) == 0
+    assert f(mat(64, 64, I8), w) == 0
+    assert f(mat(100, 64, I8), w) == 100 * 128 + 400
+    assert f(mat(100, 64, I8), w, _lib.GDN_PREFILL_SIMT) == 0
+    odd = mat(8, 65, I8)
+    assert f(mat(1, 65, I8), odd) == 768                        # 8 rows of 80, to 256 bytes
+    assert f(mat(3, 65, I8), odd) == 256 + 768
+    assert f(mat(3, 65, I8, stride=80), mat(8, 65, I8, stride=80)) == 0
+    assert f(mat(100, 65, I8), odd) == 768 + (100 * 72 * 2 + 255) // 256 * 256 + 400
+    assert f(mat(3, 64, I8, ptr=FAKE + 1), w) == 256
 
 
 def on_device(*shape, dtype=torch.bfloat16):
