@@ -986,6 +986,7 @@ gdn_status_t gdn_matmul_i8(const gdn_matrix_t *a, const float *a_scale, const gd
     p.out = O.ptr;
     p.out_st = O.st;
     p.out_f32 = O.dtype == GDN_F32;
+    p.out_vec = rows_aligned(O, 16);
     p.status = status_dev;
     const size_t need = gdn_host::matmul_i8_workspace(p, flags);
     if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)))

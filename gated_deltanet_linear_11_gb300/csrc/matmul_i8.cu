@@ -288,7 +288,7 @@ size_t matmul_i8_workspace(const MatmulParams &p, uint32_t flags) {
     if (flags & GDN_PREFILL_SIMT) return 0;
     size_t a, w;
     align_sizes(p, a, w);
-    return a + w + (p.M > kPairTokensFrom ? matmul_i8_pair_workspace(p.M, p.K) : 0);
+    return a + w + (p.M > kPairTokensFrom ? matmul_i8_pair_workspace(p.M, p.N, p.K) : 0);
 }
 
 gdn_status_t launch_matmul_i8(const MatmulParams &given, uint32_t flags, void *ws, cudaStream_t st) {

@@ -25,6 +25,7 @@ struct MatmulParams {
     int64_t M, N;
     int32_t K;
     int32_t bias_f32, out_f32;
+    int32_t out_vec;                // rows of out start on 16 bytes
     int32_t *status;
 };
 
@@ -79,6 +80,6 @@ size_t matmul_i8_workspace(const gdn::MatmulParams &p, uint32_t flags);
 gdn_status_t launch_matmul_i8(const gdn::MatmulParams &p, uint32_t flags, void *ws, cudaStream_t st);
 // rows of w (and of a, for few tokens) on 16 bytes
 gdn_status_t launch_matmul_i8_few(const gdn::MatmulParams &p, cudaStream_t st);
-size_t matmul_i8_pair_workspace(int64_t M, int64_t K);
+size_t matmul_i8_pair_workspace(int64_t M, int64_t N, int64_t K);
 gdn_status_t launch_matmul_i8_pair(const gdn::MatmulParams &p, void *ws, cudaStream_t st);
 }  // namespace gdn_host

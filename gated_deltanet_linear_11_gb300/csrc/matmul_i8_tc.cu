@@ -142,11 +142,14 @@ template <int N> struct ExactSums {
     __device__ __forceinline__ int32_t whole(int i) const {
         return (moved ? far[i] : 0) + __float2int_rn(s[i]);
     }
-    // makes s the sums, rounded once
-    __device__ __forceinline__ void finish() {
+    // makes s the sums, rounded once, or where they have moved leaves all of them in `far`
+    __device__ __forceinline__ void finish(bool stay = false) {
         if (!moved) return;
 #pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = (float)whole(i);
+        for (int i = 0; i < N; ++i) {
+            if (stay) far[i] = whole(i);
+            else s[i] = (float)whole(i);
+        }
     }
 };
 
@@ -352,31 +355,46 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
 // |a|^2 and |w|^2 the sums of squares of a token's and a channel's codes, every partial sum is
 // at most |a||w| (Cauchy and Schwarz), and where that is at most 2^24 fp32 sums are exact to
 // the end.  |a|^2 comes with the fp16 tokens, |w|^2 from the converting warps when a tile is
-// done.  Tiles that turn out otherwise are made again with moves, after all others; tiles whose
+// done.  Units that turn out otherwise are made again with moves, after all others; those whose
 // tokens alone are above kPairCareful are made so at once.  Which it is changes no result.
 //
-// Persistent: a pair takes tiles in turn.  Warps 0-7 move sums (a thread: one channel, half of
+// Persistent: a pair takes units in turn.  A unit is a tile; those tiles that are left when
+// every pair has had the same number are cut along K into PairShape::parts units each, whose
+// int32 sums go to the workspace and are added up by a kernel after this one.  Warps 0-7 move sums (a thread: one channel, half of
 // the tokens), 8-11 convert, 12 copies, 13 issues products (in the first CTA of a pair).
 constexpr int kPairSumWarps = 8, kPairConvWarps = 4, kPairMaxStages = 4;
 constexpr int kPairThreads = 32 * (kPairSumWarps + kPairConvWarps + 4);  // two warps idle
 constexpr int kPairTokens = 256;                 // most tokens of a tile
 constexpr int kPairCareful = 15000000;           // |a|^2: with a like |w|^2, near 2^24 squared
-constexpr int kPairMarks = 1024;                 // tiles of a pair with marks of their own
+constexpr int kPairMarks = 1024;                 // units of a pair with marks of their own
 
 struct PairShape {                               // of a launch
     int NT, stages;                              // TMEM: 256 columns of sums, 64 a stage
     uint32_t stage_bytes;                        // codes, then two 64-code blocks of tokens
-    int tiles_m, tiles;
+    int tiles_m, steps;                          // tiles along the tokens; steps of K
+    int full, parts, units;                      // whole tiles; units of each other tile; all units
     const int32_t *squares;                      // |a|^2 of the tokens
+    int32_t *sums;                               // [unit - full][64 fours of tokens][256 channels][4]
 };
+struct PairUnit {
+    int tile, first, last;                       // steps of K
+    bool whole;
+};
+__device__ __forceinline__ PairUnit pair_unit(const PairShape &sh, int unit) {
+    if (unit < sh.full) return {unit, 0, sh.steps, true};
+    const int j = unit - sh.full, part = j % sh.parts;
+    return {sh.full + j / sh.parts, sh.steps * part / sh.parts, sh.steps * (part + 1) / sh.parts, sh.parts == 1};
+}
 struct PairBars {
     uint64_t full[kPairMaxStages], conv[kPairMaxStages], free[kPairMaxStages], d_full[2], d_free[2];
-    uint32_t again[kPairMarks / 32];             // tiles to make again (the last mark: any after it too)
+    uint32_t again[kPairMarks / 32];             // units to make again (the last mark: any after it too)
+    uint32_t any;                                // whether there are any
     uint32_t tmem;
     int abort;
 };
 constexpr uint32_t kPairRaw = kI8Channels * kI8Step;
-constexpr int kPairSmem = 208 * 1024 + (int)sizeof(PairBars);
+constexpr uint32_t kPairRing = 208 * 1024, kPairOut = 16 * 144;  // of a warp: 16 tokens' 32 channels
+constexpr int kPairSmem = (int)(kPairRing + kPairSumWarps * kPairOut + sizeof(PairBars));
 
 // Largest |a|^2 of the tile's tokens (a warp).
 __device__ __forceinline__ int32_t pair_squares(const PairShape &sh, int64_t M, int tile) {
@@ -389,11 +407,21 @@ __device__ __forceinline__ int32_t pair_squares(const PairShape &sh, int64_t M, 
     }
     return __reduce_max_sync(0xffffffffu, most);
 }
-// Marks of both CTAs (turn: the pair's how manieth tile).
+// Marks the pair's unit `turn` in both CTAs' lists, or looks it up in this one's.
+__device__ __forceinline__ void pair_mark(PairBars &S, int turn) {
+    turn = min(turn, kPairMarks - 1);
+#pragma unroll
+    for (uint32_t r = 0; r < 2; ++r) {
+        uint32_t at, any;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(tc::smem_u32(&S.again[turn >> 5])), "r"(r));
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(any) : "r"(tc::smem_u32(&S.any)), "r"(r));
+        asm volatile("red.shared::cluster.or.b32 [%0], %1;" :: "r"(at), "r"(1u << (turn & 31)) : "memory");
+        asm volatile("red.shared::cluster.or.b32 [%0], 1;" :: "r"(any) : "memory");
+    }
+}
 __device__ __forceinline__ bool pair_marked(const PairBars &S, int turn) {
     turn = min(turn, kPairMarks - 1);
-    const uint32_t at = tc::smem_u32(&S.again[turn >> 5]);
-    return ((cluster_load(at, 0) | cluster_load(at, 1)) >> (turn & 31)) & 1;
+    return (*(volatile const uint32_t *)&S.again[turn >> 5] >> (turn & 31)) & 1;
 }
 
 __device__ __forceinline__ void pair_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t add) {
@@ -430,6 +458,28 @@ template <int N> __device__ __forceinline__ void regs_down() {
 constexpr int kPairRegs = 128, kPairSumRegs = 176, kPairConvRegs = 96, kPairRestRegs = 64;
 static_assert(2 * kPairSumRegs + kPairConvRegs + kPairRestRegs <= 4 * kPairRegs, "a raise waits forever");
 
+// Stores 16 tokens' values of 32 channels from `mid` ([token][36]); m, n: the first of them.
+__device__ __forceinline__ void pair_store(const MatmulParams &p, const float *mid, int64_t m, int64_t n) {
+    const int lane = threadIdx.x & 31, rows = (int)min(p.M - m, (int64_t)16);
+    if (!p.out_vec || n + 32 > p.N) {
+        for (int j = 0; j < rows; ++j)
+            if (n + lane < p.N) matmul_store(p, m + j, n + lane, mid[j * 36 + lane]);
+    } else if (p.out_f32) {
+#pragma unroll 1
+        for (int j = lane >> 3; j < rows; j += 4)
+            *reinterpret_cast<float4 *>((float *)p.out + (m + j) * p.out_st + n + 4 * (lane & 7)) =
+                *reinterpret_cast<const float4 *>(mid + j * 36 + 4 * (lane & 7));
+    } else {
+#pragma unroll 1
+        for (int j = lane >> 2; j < rows; j += 8) {
+            const float4 a = *reinterpret_cast<const float4 *>(mid + j * 36 + 8 * (lane & 3));
+            const float4 b = *reinterpret_cast<const float4 *>(mid + j * 36 + 8 * (lane & 3) + 4);
+            const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            *reinterpret_cast<uint4 *>((bf16 *)p.out + (m + j) * p.out_st + n + 8 * (lane & 3)) = pack8(f);
+        }
+    }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__ MatmulParams p,
                       const __grid_constant__ PairShape sh) {
@@ -441,7 +491,7 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int steps = (p.K + kI8Step - 1) / kI8Step, NT = sh.NT, stages = sh.stages;
+    const int NT = sh.NT, stages = sh.stages;
     const int buffers = NT <= 128 ? 2 : 1;       // of sums
     volatile int *abort = &S.abort;
 
@@ -462,6 +512,7 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
             tc::mbar_init(&S.d_free[i], 2 * kPairSumWarps);
         }
         for (int i = 0; i < kPairMarks / 32; ++i) S.again[i] = 0;
+        S.any = 0;
         tc::mbar_fence_init();
         tc::prefetch_tmap(&maps.w);
         tc::prefetch_tmap(&maps.a);
@@ -472,9 +523,16 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
     tc::fence_after_sync();
     const uint32_t tmem = S.tmem;
     grid_dependents_launch();
+    // codes of w on their way to L2 while the kernel before this one ends
+    if (tid < stages) {
+        const PairUnit u = pair_unit(sh, pair);
+        if (u.first + tid < u.last)
+            prefetch_2d(&maps.w, (u.first + tid) * kI8Step, u.tile / sh.tiles_m * 256 + 128 * rank);
+    }
+    __syncwarp();
     grid_dependency_wait();
 
-    // Every role goes over the pair's tiles twice; the second time over those marked by then.
+    // Every role goes over the pair's units twice; the second time over those marked by then.
     if (warp < kPairSumWarps) {
         regs_up<kPairSumRegs>();
         // groups of 16 columns: this warp has q, q + 2, ..
@@ -484,9 +542,20 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
         bool ok = true;
         ExactSums<128> sums;
         for (int pass = 0; pass < 2; ++pass) {
-            for (int tile = pair, turn = 0; tile < sh.tiles && ok; tile += pairs, ++turn) {
+            for (int unit = pair, turn = 0; unit < sh.units && ok; unit += pairs, ++turn) {
                 if (pass && !pair_marked(S, turn)) continue;
-                const int chunk = pass || pair_squares(sh, p.M, tile) > kPairCareful ? kI8Exact : steps;
+                const PairUnit u = pair_unit(sh, unit);
+                const int steps = u.last - u.first;
+                const int chunk = pass || pair_squares(sh, p.M, u.tile) > kPairCareful ? kI8Exact : steps;
+                const int64_t n = (int64_t)(u.tile / sh.tiles_m) * 256 + 128 * rank + row;
+                const int64_t m0 = (int64_t)(u.tile % sh.tiles_m) * NT;
+                const bool in = n < p.N;
+                const float ws = in ? p.w_scale[n] : 0.f, bias = in ? matmul_bias(p, n) : 0.f;
+                // scales of the tokens: lane l of scale[i] has group 2 i + l / 16, token l % 16
+                float scale[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    scale[i] = p.a_scale[min(m0 + 16 * (q + 2 * (2 * i + (lane >> 4))) + (lane & 15), p.M - 1)];
                 sums.clear();
                 for (int s = 0; s < steps && ok; s += chunk) {
                     const int buf = c & (buffers - 1);
@@ -510,27 +579,50 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
                     }
                     if (chunk < steps) sums.settle();
                 }
-                sums.finish();
-                const int64_t n = (int64_t)(tile / sh.tiles_m) * 256 + 128 * rank + row;
-                const int64_t m0 = (int64_t)(tile % sh.tiles_m) * NT;
-                const bool in = ok && n < p.N;
-                const float ws = in ? p.w_scale[n] : 0.f, bias = in ? matmul_bias(p, n) : 0.f;
+                sums.finish(!u.whole);
+                if (ok && u.whole) {
+                    // 16 tokens' values of the warp's 32 channels at a time, by way of shared memory:
+                    // one store then has 16 bytes a lane, and the straight-line part of this code,
+                    // which waits for instructions, stays short
+                    float *mid = reinterpret_cast<float *>(smem_raw + kPairRing + warp * kPairOut);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (q + 2 * i >= groups) continue;
-                    const int64_t m = m0 + 16 * (q + 2 * i);
-                    const float mine = p.a_scale[min(m + (lane & 15), p.M - 1)];
+                    for (int i = 0; i < 8; ++i) {
+                        const int64_t m = m0 + 16 * (q + 2 * i);
+                        if (q + 2 * i >= groups || m >= p.M) continue;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float as = __shfl_sync(0xffffffffu, mine, j);
-                        if (in && m + j < p.M)
-                            matmul_store(p, m + j, n, matmul_value(sums.s[16 * i + j], as, ws, bias));
+                        for (int j = 0; j < 16; ++j) {
+                            const float as = __shfl_sync(0xffffffffu, scale[i >> 1], 16 * (i & 1) + j);
+                            mid[j * 36 + lane] = matmul_value(sums.s[16 * i + j], as, ws, bias);
+                        }
+                        __syncwarp();
+                        pair_store(p, mid, m, n - lane);
+                        __syncwarp();
+                    }
+                } else if (ok) {
+                    int4 *to = reinterpret_cast<int4 *>(sh.sums) + ((int64_t)(unit - sh.full) << 14) + 128 * rank + row;
+                    if (sums.moved) {
+                        for (int i = 0; i < 32; ++i) {
+                            const int tok = 16 * (q + 2 * (i >> 2)) + 4 * (i & 3);
+                            if (tok < NT && m0 + tok < p.M)
+                                to[tok / 4 * 256] = make_int4(sums.far[4 * i], sums.far[4 * i + 1], sums.far[4 * i + 2],
+                                                              sums.far[4 * i + 3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const int tok = 16 * (q + 2 * (i >> 2)) + 4 * (i & 3);
+                            if (tok < NT && m0 + tok < p.M)
+                                to[tok / 4 * 256] =
+                                    make_int4(__float2int_rn(sums.s[4 * i]), __float2int_rn(sums.s[4 * i + 1]),
+                                              __float2int_rn(sums.s[4 * i + 2]), __float2int_rn(sums.s[4 * i + 3]));
+                        }
                     }
                 }
                 __syncwarp();
             }
             __syncwarp();
             if (pass == 0) cluster_sync();
+            if (*(volatile uint32_t *)&S.any == 0) break;
         }
     } else if (warp < kPairSumWarps + kPairConvWarps) {
         regs_down<kPairConvRegs>();
@@ -540,11 +632,12 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
         uint32_t round = 0;
         bool ok = true;
         for (int pass = 0; pass < 2; ++pass) {
-            for (int tile = pair, turn = 0; tile < sh.tiles && ok; tile += pairs, ++turn) {
+            for (int unit = pair, turn = 0; unit < sh.units && ok; unit += pairs, ++turn) {
                 if (pass && !pair_marked(S, turn)) continue;
-                const int32_t tokens = pass ? 0 : pair_squares(sh, p.M, tile);
+                const PairUnit u = pair_unit(sh, unit);
+                const int32_t tokens = pass ? 0 : pair_squares(sh, p.M, u.tile);
                 int32_t squares = 0;             // of this thread's channel
-                for (int s = 0; s < steps; ++s) {
+                for (int s = u.first; s < u.last; ++s) {
                     if (!(ok = i8_wait(&S.full[slot], round & 1, abort))) break;
                     tc::fence_after_sync();
                     const uint8_t *raw = smem_raw + slot * sh.stage_bytes;
@@ -573,13 +666,11 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
                 }
                 // 2^48 less what the product's rounding could hide
                 const bool far = (float)squares * (float)tokens > 2.8147e14f;
-                if (tokens <= kPairCareful && __any_sync(0xffffffffu, far) && lane == 0) {
-                    const int mark = min(turn, kPairMarks - 1);
-                    atomicOr(&S.again[mark >> 5], 1u << (mark & 31));
-                }
+                if (tokens <= kPairCareful && __any_sync(0xffffffffu, far) && lane == 0) pair_mark(S, turn);
             }
             __syncwarp();
             if (pass == 0) cluster_sync();
+            if (*(volatile uint32_t *)&S.any == 0) break;
         }
     } else {
         regs_down<kPairRestRegs>();
@@ -590,11 +681,13 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
         uint32_t round = 0, c = 0;
         bool ok = true;
         for (int pass = 0; pass < 2; ++pass) {
-            for (int tile = pair, turn = 0; (copies || products) && tile < sh.tiles && ok; tile += pairs, ++turn) {
+            for (int unit = pair, turn = 0; (copies || products) && unit < sh.units && ok; unit += pairs, ++turn) {
                 if (pass && !pair_marked(S, turn)) continue;
+                const PairUnit u = pair_unit(sh, unit);
                 if (copies) {
-                    const int n0 = tile / sh.tiles_m * 256 + 128 * rank, m0 = tile % sh.tiles_m * NT + NT / 2 * rank;
-                    for (int s = 0; s < steps; ++s) {
+                    const int n0 = u.tile / sh.tiles_m * 256 + 128 * rank;
+                    const int m0 = u.tile % sh.tiles_m * NT + NT / 2 * rank;
+                    for (int s = u.first; s < u.last; ++s) {
                         if (round > 0 && !(ok = i8_wait(&S.free[slot], (round - 1) & 1, abort))) break;
                         if (lane == 0) {
                             uint8_t *to = smem_raw + slot * sh.stage_bytes;
@@ -608,7 +701,8 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
                         if (++slot == stages) slot = 0, ++round;
                     }
                 } else {
-                    const int chunk = pass || pair_squares(sh, p.M, tile) > kPairCareful ? kI8Exact : steps;
+                    const int steps = u.last - u.first;
+                    const int chunk = pass || pair_squares(sh, p.M, u.tile) > kPairCareful ? kI8Exact : steps;
                     for (int s = 0, left = 0; s < steps; ++s) {
                         const int buf = c & (buffers - 1);
                         const bool fresh = left == 0;
@@ -634,6 +728,7 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
             }
             __syncwarp();
             if (pass == 0) cluster_sync();
+            if (*(volatile uint32_t *)&S.any == 0) break;
         }
         // nothing may land after the CTA has left
         for (int i = 0; i < issued; ++i) {
@@ -650,17 +745,46 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
     if (tid == 0 && *abort) report(p.status, GDN_ERR_TIMEOUT);
 }
 
+// The units' sums of tiles in parts, added up and scaled: a CTA takes four tokens of a tile, a
+// thread a channel.
+__global__ void __launch_bounds__(256) matmul_i8_join_kernel(const __grid_constant__ MatmulParams p,
+                                                             const __grid_constant__ PairShape sh) {
+    grid_dependents_launch();
+    const int tile = sh.full + blockIdx.y;
+    const int64_t n = (int64_t)(tile / sh.tiles_m) * 256 + threadIdx.x, m0 = (int64_t)(tile % sh.tiles_m) * sh.NT;
+    grid_dependency_wait();
+    if (n >= p.N) return;
+    const float ws = p.w_scale[n], bias = matmul_bias(p, n);
+    const int4 *from = reinterpret_cast<const int4 *>(sh.sums) + ((int64_t)blockIdx.y * sh.parts << 14) +
+                       blockIdx.x * 256 + threadIdx.x;
+    const int tok = blockIdx.x * 4;
+    if (m0 + tok >= p.M) return;
+    int32_t sum[4] = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int j = 0; j < sh.parts; ++j) {
+        const int4 v = from[(int64_t)j << 14];
+        sum[0] += v.x;
+        sum[1] += v.y;
+        sum[2] += v.z;
+        sum[3] += v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (m0 + tok + i < p.M)
+            matmul_store(p, m0 + tok + i, n, matmul_value((float)sum[i], p.a_scale[m0 + tok + i], ws, bias));
+}
+
 // Tokens' codes as fp16, rows `st` elements apart (a multiple of 8; what lies between K and st
-// is not read), and the sums of their squares: a warp per token, a lane takes eight codes.
-__global__ void __launch_bounds__(128) matmul_i8_tokens_kernel(const int8_t *a, int64_t a_st, __half *out, int64_t st,
-                                                               int32_t *squares, int64_t M, int32_t K, int vec) {
+// is not read), and the sums of their squares: a CTA per token, a thread takes eight codes.
+__global__ void __launch_bounds__(256) matmul_i8_tokens_kernel(const int8_t *a, int64_t a_st, __half *out, int64_t st,
+                                                               int32_t *squares, int32_t K, int vec) {
+    __shared__ int32_t part[8];
     grid_dependents_launch();
     grid_dependency_wait();
-    const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (m >= M) return;
+    const int64_t m = blockIdx.x;
     int32_t sum = 0;
 #pragma unroll 4
-    for (int k = (threadIdx.x & 31) * 8; k < K; k += 256) {
+    for (int k = threadIdx.x * 8; k < K; k += 2048) {
         const int8_t *src = a + m * a_st + k;
         uint2 w = make_uint2(0, 0);
         if (vec && k + 8 <= K) {
@@ -677,7 +801,12 @@ __global__ void __launch_bounds__(128) matmul_i8_tokens_kernel(const int8_t *a, 
         *reinterpret_cast<uint4 *>(out + m * st + k) = h;
     }
     sum = __reduce_add_sync(0xffffffffu, sum);
-    if ((threadIdx.x & 31) == 0) squares[m] = sum;
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < 8; ++i) sum += part[i];
+        squares[m] = sum;
+    }
 }
 
 }  // namespace gdn
@@ -687,6 +816,38 @@ namespace gdn_host {
 using namespace gdn;
 
 namespace {
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+int pair_tokens(int64_t M) { return M <= 128 ? 128 : 256; }
+
+// Tiles, those made whole, and the units of each other one.  The parts along K are as many as
+// make the last turns shortest; a part costs its fill and the join about kPairJoin steps.
+constexpr int kPairMaxParts = 12, kPairJoin = 10;
+struct PairPlan {
+    int64_t tiles, full;
+    int parts;
+};
+PairPlan pair_plan(int64_t M, int64_t N, int64_t K, int pairs) {
+    const int NT = pair_tokens(M);
+    const int64_t steps = (K + kI8Step - 1) / kI8Step;
+    PairPlan plan;
+    plan.tiles = (M + NT - 1) / NT * ((N + 255) / 256);
+    plan.full = plan.tiles;
+    plan.parts = 1;
+    if (pairs <= 0 || plan.tiles % pairs == 0) return plan;
+    const int64_t left = plan.tiles % pairs;
+    int64_t best = steps;
+    for (int parts = 2; parts <= kPairMaxParts && parts * 2 <= steps; ++parts) {
+        const int64_t turns = (left * parts + pairs - 1) / pairs, cost = turns * ((steps + parts - 1) / parts + 1) + kPairJoin;
+        if (cost < best) {
+            best = cost;
+            plan.parts = parts;
+            plan.full = plan.tiles - left;
+        }
+    }
+    return plan;
+}
 
 template <int NT>
 gdn_status_t launch_tc(const MatmulParams &p, cudaStream_t st) {
@@ -748,30 +909,39 @@ gdn_status_t launch_matmul_i8_pair(const MatmulParams &p, void *ws, cudaStream_t
     }
     const int sms = matmul_sm_count(dev);
     if (sms <= 1) return GDN_ERR_CUDA;
-    const int pairs = sms / 2, NT = p.M <= 128 ? 128 : 256;
-    const int64_t tiles_m = (p.M + NT - 1) / NT, tiles = tiles_m * ((p.N + 255) / 256);
-    if (tiles > 0x3fffffff) return GDN_ERR_SHAPE;
+    const int pairs = sms / 2, NT = pair_tokens(p.M);
+    const PairPlan plan = pair_plan(p.M, p.N, p.K, pairs);
+    if (plan.tiles > 0x3fffffff / kPairMaxParts) return GDN_ERR_SHAPE;
     gdn::PairShape sh;
     sh.NT = NT;
     sh.stage_bytes = gdn::kPairRaw + NT * 128;
-    sh.stages = (int)(208 * 1024 / sh.stage_bytes);
+    sh.stages = (int)(gdn::kPairRing / sh.stage_bytes);
     if (sh.stages > 4) sh.stages = 4;           // 64 of TMEM's columns each
-    sh.tiles_m = (int)tiles_m;
-    sh.tiles = (int)tiles;
+    sh.tiles_m = (int)((p.M + NT - 1) / NT);
+    sh.steps = (int)((p.K + kI8Step - 1) / kI8Step);
+    sh.full = (int)plan.full;
+    sh.parts = plan.parts;
+    sh.units = (int)(plan.full + (plan.tiles - plan.full) * plan.parts);
     const int64_t half_st = ((int64_t)p.K + 7) / 8 * 8;
-    int32_t *squares = (int32_t *)((uint8_t *)ws + ((size_t)p.M * half_st * 2 + 255) / 256 * 256);
+    int32_t *squares = (int32_t *)((uint8_t *)ws + up256((size_t)p.M * half_st * 2));
     sh.squares = squares;
+    sh.sums = (int32_t *)((uint8_t *)squares + up256((size_t)p.M * 4));
     I8Maps maps;
     if (!row_map(&maps.w, p.w, false, p.N, p.K, p.w_st, kI8Channels, true) ||
         !row_map(&maps.a, ws, true, p.M, p.K, half_st, NT / 2, true))
         return GDN_ERR_CUDA;
     const bool vec = ((uintptr_t)p.a & 7u) == 0 && (p.M == 1 || p.a_st % 8 == 0);
-    if (launch_dependent(matmul_i8_tokens_kernel, dim3((unsigned)((p.M + 3) / 4)), dim3(128), 0, st, p.a, p.a_st,
-                         (__half *)ws, half_st, (int32_t *)squares, p.M, p.K, (int)vec) != cudaSuccess)
+    if (launch_dependent(matmul_i8_tokens_kernel, dim3((unsigned)p.M), dim3(256), 0, st, p.a, p.a_st, (__half *)ws,
+                         half_st, squares, p.K, (int)vec) != cudaSuccess)
         return GDN_ERR_CUDA;
-    const unsigned grid = (unsigned)(2 * (tiles < pairs ? tiles : pairs));
-    return launch_dependent(kern, dim3(grid), dim3(kPairThreads), smem, st, maps, p,
-                            sh) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    const unsigned grid = (unsigned)(2 * (sh.units < pairs ? sh.units : pairs));
+    if (launch_dependent(kern, dim3(grid), dim3(kPairThreads), smem, st, maps, p, sh) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    if (sh.parts > 1 &&
+        launch_dependent(matmul_i8_join_kernel, dim3(NT / 4, (unsigned)(plan.tiles - plan.full)), dim3(256), 0, st, p,
+                         sh) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    return GDN_OK;
 }
 
 gdn_status_t launch_matmul_i8_few(const MatmulParams &p, cudaStream_t st) {
@@ -780,8 +950,12 @@ gdn_status_t launch_matmul_i8_few(const MatmulParams &p, cudaStream_t st) {
     return launch_tc<64>(p, st);
 }
 
-size_t matmul_i8_pair_workspace(int64_t M, int64_t K) {
-    return ((size_t)M * (size_t)((K + 7) / 8 * 8) * 2 + 255) / 256 * 256 + (size_t)M * 4;
+size_t matmul_i8_pair_workspace(int64_t M, int64_t N, int64_t K) {
+    int dev = 0;
+    const int sms = cudaGetDevice(&dev) == cudaSuccess ? matmul_sm_count(dev) : 0;
+    const PairPlan plan = pair_plan(M, N, K, sms / 2);
+    const size_t sums = plan.parts > 1 ? (size_t)((plan.tiles - plan.full) * plan.parts) << 18 : 0;
+    return up256((size_t)M * (size_t)((K + 7) / 8 * 8) * 2) + up256((size_t)M * 4) + sums;
 }
 
 }  // namespace gdn_host
