@@ -144,7 +144,7 @@ template <int N> struct ExactSums {
     }
     // makes s the sums, rounded once, or where they have moved leaves all of them in `far`
     __device__ __forceinline__ void finish(bool stay = false) {
-        if (!moved) return;
+        if (!__any_sync(0xffffffffu, moved)) return;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if (stay) far[i] = whole(i);
@@ -393,8 +393,15 @@ struct PairBars {
     int abort;
 };
 constexpr uint32_t kPairRaw = kI8Channels * kI8Step;
-constexpr uint32_t kPairRing = 208 * 1024, kPairOut = 16 * 144;  // of a warp: 16 tokens' 32 channels
-constexpr int kPairSmem = (int)(kPairRing + kPairSumWarps * kPairOut + sizeof(PairBars));
+constexpr uint32_t kPairRing = 192 * 1024;
+// Of a sums' warp, on the way out: 32 channels' sums of 16 tokens (20 words a channel, 8 more
+// after every eighth, so that neither a lane's row nor eight channels of eight tokens meet in a
+// bank), and the scales and bias.
+struct PairOut {
+    float sum[32 * 20 + 3 * 8];
+    float scale[32], bias[32], tokens[8][16];    // tokens: scales of the warp's groups
+};
+constexpr int kPairSmem = (int)(kPairRing + kPairSumWarps * sizeof(PairOut) + sizeof(PairBars));
 
 // Largest |a|^2 of the tile's tokens (a warp).
 __device__ __forceinline__ int32_t pair_squares(const PairShape &sh, int64_t M, int tile) {
@@ -458,24 +465,63 @@ template <int N> __device__ __forceinline__ void regs_down() {
 constexpr int kPairRegs = 128, kPairSumRegs = 176, kPairConvRegs = 96, kPairRestRegs = 64;
 static_assert(2 * kPairSumRegs + kPairConvRegs + kPairRestRegs <= 4 * kPairRegs, "a raise waits forever");
 
-// Stores 16 tokens' values of 32 channels from `mid` ([token][36]); m, n: the first of them.
-__device__ __forceinline__ void pair_store(const MatmulParams &p, const float *mid, int64_t m, int64_t n) {
-    const int lane = threadIdx.x & 31, rows = (int)min(p.M - m, (int64_t)16);
-    if (!p.out_vec || n + 32 > p.N) {
-        for (int j = 0; j < rows; ++j)
-            if (n + lane < p.N) matmul_store(p, m + j, n + lane, mid[j * 36 + lane]);
-    } else if (p.out_f32) {
-#pragma unroll 1
-        for (int j = lane >> 3; j < rows; j += 4)
-            *reinterpret_cast<float4 *>((float *)p.out + (m + j) * p.out_st + n + 4 * (lane & 7)) =
-                *reinterpret_cast<const float4 *>(mid + j * 36 + 4 * (lane & 7));
+// Puts group i of a warp's sums into o.sum: a choice of one in eight by halves.
+template <int LO, int N>
+__device__ __forceinline__ void pair_put(float *to, const float (&s)[128], int i) {
+    if constexpr (N == 1) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+            *reinterpret_cast<float4 *>(to + j) =
+                make_float4(s[16 * LO + j], s[16 * LO + j + 1], s[16 * LO + j + 2], s[16 * LO + j + 3]);
+    } else if (i < LO + N / 2) {
+        pair_put<LO, N / 2>(to, s, i);
     } else {
+        pair_put<LO + N / 2, N / 2>(to, s, i);
+    }
+}
+
+// Scales and stores 16 tokens of 32 channels; m, n: the first of them.  A lane takes eight
+// channels of two tokens, side by side: two warps a scheduler wait for every result.
+__device__ __forceinline__ void pair_store(const MatmulParams &p, const PairOut &o, int group, int64_t m, int64_t n) {
+    const int lane = threadIdx.x & 31, rows = (int)min(p.M - m, (int64_t)16), c = 8 * (lane & 3), j = lane >> 2;
+    const float *from = o.sum + c * 20 + c + j;
+    float2 f[2][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) f[x][e] = make_float2(from[40 * e + 8 * x], from[40 * e + 20 + 8 * x]);
+    const float as[2] = {o.tokens[group][j], o.tokens[group][j + 8]};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 ws = *reinterpret_cast<const float2 *>(o.scale + c + 2 * e);
+        const float2 bias = *reinterpret_cast<const float2 *>(o.bias + c + 2 * e);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            f[x][e] = make_float2(matmul_value(f[x][e].x, as[x], ws.x, bias.x),
+                                  matmul_value(f[x][e].y, as[x], ws.y, bias.y));
+    }
+    const bool wide = p.out_vec && n + 32 <= p.N;
+    const int64_t at = (m + j) * p.out_st + n + c;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        if (j + 8 * x >= rows) continue;
+        const int64_t here = at + 8 * x * p.out_st;
+        if (!wide) {
 #pragma unroll 1
-        for (int j = lane >> 2; j < rows; j += 8) {
-            const float4 a = *reinterpret_cast<const float4 *>(mid + j * 36 + 8 * (lane & 3));
-            const float4 b = *reinterpret_cast<const float4 *>(mid + j * 36 + 8 * (lane & 3) + 4);
-            const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            *reinterpret_cast<uint4 *>((bf16 *)p.out + (m + j) * p.out_st + n + 8 * (lane & 3)) = pack8(f);
+            for (int e = 0; e < 8; ++e)
+                if (n + c + e < p.N) {
+                    const float v = matmul_value(from[20 * e + 8 * x], as[x], o.scale[c + e], o.bias[c + e]);
+                    if (p.out_f32) ((float *)p.out)[here + e] = v;
+                    else ((bf16 *)p.out)[here + e] = from_f32<bf16>(v);
+                }
+        } else if (p.out_f32) {
+            float4 *to = reinterpret_cast<float4 *>((float *)p.out + here);
+            to[0] = make_float4(f[x][0].x, f[x][0].y, f[x][1].x, f[x][1].y);
+            to[1] = make_float4(f[x][2].x, f[x][2].y, f[x][3].x, f[x][3].y);
+        } else {
+            *reinterpret_cast<uint4 *>((bf16 *)p.out + here) =
+                make_uint4(pack_bf2(f[x][0].x, f[x][0].y), pack_bf2(f[x][1].x, f[x][1].y),
+                           pack_bf2(f[x][2].x, f[x][2].y), pack_bf2(f[x][3].x, f[x][3].y));
         }
     }
 }
@@ -530,102 +576,103 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
             prefetch_2d(&maps.w, (u.first + tid) * kI8Step, u.tile / sh.tiles_m * 256 + 128 * rank);
     }
     __syncwarp();
-    grid_dependency_wait();
 
     // Every role goes over the pair's units twice; the second time over those marked by then.
     if (warp < kPairSumWarps) {
         regs_up<kPairSumRegs>();
+        grid_dependency_wait();
         // groups of 16 columns: this warp has q, q + 2, ..
         const int q = warp >> 2, row = 32 * (warp & 3) + lane, groups = NT / 16;
         const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 16 * q;
         uint32_t c = 0;                          // chunks so far
         bool ok = true;
         ExactSums<128> sums;
+        PairOut &out = reinterpret_cast<PairOut *>(smem_raw + kPairRing)[warp];
         for (int pass = 0; pass < 2; ++pass) {
             for (int unit = pair, turn = 0; unit < sh.units && ok; unit += pairs, ++turn) {
                 if (pass && !pair_marked(S, turn)) continue;
                 const PairUnit u = pair_unit(sh, unit);
                 const int steps = u.last - u.first;
-                const int chunk = pass || pair_squares(sh, p.M, u.tile) > kPairCareful ? kI8Exact : steps;
                 const int64_t n = (int64_t)(u.tile / sh.tiles_m) * 256 + 128 * rank + row;
                 const int64_t m0 = (int64_t)(u.tile % sh.tiles_m) * NT;
-                const bool in = n < p.N;
-                const float ws = in ? p.w_scale[n] : 0.f, bias = in ? matmul_bias(p, n) : 0.f;
-                // scales of the tokens: lane l of scale[i] has group 2 i + l / 16, token l % 16
-                float scale[4];
+                const int chunk = pass || pair_squares(sh, p.M, u.tile) > kPairCareful ? kI8Exact : steps;
+                if (u.whole) {
+                    out.scale[lane] = n < p.N ? p.w_scale[n] : 0.f;
+                    out.bias[lane] = n < p.N ? matmul_bias(p, n) : 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    scale[i] = p.a_scale[min(m0 + 16 * (q + 2 * (2 * i + (lane >> 4))) + (lane & 15), p.M - 1)];
+                    for (int i = lane >> 4; i < 8; i += 2)
+                        out.tokens[i][lane & 15] = p.a_scale[min(m0 + 16 * (q + 2 * i) + (lane & 15), p.M - 1)];
+                }
                 sums.clear();
                 for (int s = 0; s < steps && ok; s += chunk) {
                     const int buf = c & (buffers - 1);
                     if (!(ok = i8_wait<20>(&S.d_full[buf], (c / buffers) & 1, abort))) break;
                     ++c;
                     tc::fence_after_sync();
-                    float v[2][16];
-                    tc::tmem_ld16(at + buf * 128, v[0]);
+                    if (chunk >= steps) {            // all there is
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (q + 2 * i >= groups) continue;
+                        for (int i = 0; i < 8; ++i)
+                            if (q + 2 * i < groups) tc::tmem_ld16(at + buf * 128 + 32 * i, sums.s + 16 * i);
                         tc::tmem_wait_ld();
-                        if (i < 7 && q + 2 * i + 2 < groups) {
-                            tc::tmem_ld16(at + buf * 128 + 32 * (i + 1), v[(i + 1) & 1]);
-                        } else {                 // all read
-                            tc::fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0) pair_arrive(&S.d_free[buf]);
+                    } else {
+                        float v[2][16];
+                        tc::tmem_ld16(at + buf * 128, v[0]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (q + 2 * i >= groups) continue;
+                            tc::tmem_wait_ld();
+                            if (i < 7 && q + 2 * i + 2 < groups)
+                                tc::tmem_ld16(at + buf * 128 + 32 * (i + 1), v[(i + 1) & 1]);
+                            sums.add(16 * i, v[i & 1]);
                         }
-                        sums.add(16 * i, v[i & 1]);
                     }
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) pair_arrive(&S.d_free[buf]);
                     if (chunk < steps) sums.settle();
                 }
-                sums.finish(!u.whole);
-                if (ok && u.whole) {
-                    // 16 tokens' values of the warp's 32 channels at a time, by way of shared memory:
-                    // one store then has 16 bytes a lane, and the straight-line part of this code,
-                    // which waits for instructions, stays short
-                    float *mid = reinterpret_cast<float *>(smem_raw + kPairRing + warp * kPairOut);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int64_t m = m0 + 16 * (q + 2 * i);
-                        if (q + 2 * i >= groups || m >= p.M) continue;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float as = __shfl_sync(0xffffffffu, scale[i >> 1], 16 * (i & 1) + j);
-                            mid[j * 36 + lane] = matmul_value(sums.s[16 * i + j], as, ws, bias);
-                        }
-                        __syncwarp();
-                        pair_store(p, mid, m, n - lane);
-                        __syncwarp();
+                if (!ok) break;
+                if (chunk < steps) sums.finish(!u.whole);
+                int4 *to = reinterpret_cast<int4 *>(sh.sums) + ((int64_t)(unit - sh.full) << 14) + 128 * rank + row;
+                if (!u.whole && sums.moved) {
+                    for (int i = 0; i < 32; ++i) {
+                        const int tok = 16 * (q + 2 * (i >> 2)) + 4 * (i & 3);
+                        if (tok < NT && m0 + tok < p.M)
+                            to[tok / 4 * 256] = make_int4(sums.far[4 * i], sums.far[4 * i + 1], sums.far[4 * i + 2],
+                                                          sums.far[4 * i + 3]);
                     }
-                } else if (ok) {
-                    int4 *to = reinterpret_cast<int4 *>(sh.sums) + ((int64_t)(unit - sh.full) << 14) + 128 * rank + row;
-                    if (sums.moved) {
-                        for (int i = 0; i < 32; ++i) {
-                            const int tok = 16 * (q + 2 * (i >> 2)) + 4 * (i & 3);
-                            if (tok < NT && m0 + tok < p.M)
-                                to[tok / 4 * 256] = make_int4(sums.far[4 * i], sums.far[4 * i + 1], sums.far[4 * i + 2],
-                                                              sums.far[4 * i + 3]);
-                        }
-                    } else {
+                } else if (!u.whole) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int tok = 16 * (q + 2 * (i >> 2)) + 4 * (i & 3);
-                            if (tok < NT && m0 + tok < p.M)
-                                to[tok / 4 * 256] =
-                                    make_int4(__float2int_rn(sums.s[4 * i]), __float2int_rn(sums.s[4 * i + 1]),
-                                              __float2int_rn(sums.s[4 * i + 2]), __float2int_rn(sums.s[4 * i + 3]));
-                        }
+                    for (int i = 0; i < 32; ++i) {
+                        const int tok = 16 * (q + 2 * (i >> 2)) + 4 * (i & 3);
+                        if (tok < NT && m0 + tok < p.M)
+                            to[tok / 4 * 256] =
+                                make_int4(__float2int_rn(sums.s[4 * i]), __float2int_rn(sums.s[4 * i + 1]),
+                                          __float2int_rn(sums.s[4 * i + 2]), __float2int_rn(sums.s[4 * i + 3]));
+                    }
+                } else {
+                    // 16 tokens at a time by way of shared memory
+                    float *mine = out.sum + lane * 20 + (lane >> 3) * 8;
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        const int tok = 16 * (q + 2 * i);
+                        if (tok >= NT || m0 + tok >= p.M) break;
+                        pair_put<0, 8>(mine, sums.s, i);
+                        __syncwarp();
+                        pair_store(p, out, i, m0 + tok, n - lane);
+                        __syncwarp();
                     }
                 }
                 __syncwarp();
             }
             __syncwarp();
-            if (pass == 0) cluster_sync();
+            tc::fence_before_sync();
+            cluster_sync();                      // the other CTA's products and arrivals are done
             if (*(volatile uint32_t *)&S.any == 0) break;
         }
     } else if (warp < kPairSumWarps + kPairConvWarps) {
         regs_down<kPairConvRegs>();
+        grid_dependency_wait();
         const int row = 32 * (warp & 3) + lane;
         const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 256;
         int slot = 0;
@@ -669,11 +716,13 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
                 if (tokens <= kPairCareful && __any_sync(0xffffffffu, far) && lane == 0) pair_mark(S, turn);
             }
             __syncwarp();
-            if (pass == 0) cluster_sync();
+            tc::fence_before_sync();
+            cluster_sync();                      // the other CTA's products and arrivals are done
             if (*(volatile uint32_t *)&S.any == 0) break;
         }
     } else {
         regs_down<kPairRestRegs>();
+        grid_dependency_wait();
         const bool copies = warp == kPairSumWarps + kPairConvWarps;
         const bool products = warp == kPairSumWarps + kPairConvWarps + 1 && rank == 0;
         const uint32_t bytes = kPairRaw + NT * 128, block = NT * 64, id = i8_idesc(256, NT);
@@ -727,7 +776,8 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
                 }
             }
             __syncwarp();
-            if (pass == 0) cluster_sync();
+            tc::fence_before_sync();
+            cluster_sync();                      // the other CTA's products and arrivals are done
             if (*(volatile uint32_t *)&S.any == 0) break;
         }
         // nothing may land after the CTA has left
@@ -736,9 +786,6 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
             wait_bounded_poll<0>(&S.full[slot], round & 1, nullptr);
         }
     }
-    __syncwarp();
-    tc::fence_before_sync();
-    cluster_sync();                              // the other CTA's products and arrivals are done
     tc::fence_after_sync();
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
