@@ -12,6 +12,9 @@
 // per thread; sums and maxima go over the row with shuffles and one pass through shared
 // memory.  The split of a row depends on its length alone, so a row's results are the same in
 // any batch.
+#include <atomic>
+
+#include "matmul_i8.cuh"
 #include "rows.cuh"
 
 namespace gdn {
@@ -20,52 +23,74 @@ namespace {
 
 constexpr float kTinyScale = 1.17549435e-38f;   // 2^-126: the scale of a row of zeros
 constexpr uint32_t kInfBits = 0x7f800000u;
+constexpr float kShrink = 8.271806125530277e-25f;   // 2^-80
 
-// n <= 8 elements from p on, the rest zero; vec: all 8, 16-byte aligned.
+// Eight elements from a 16-byte boundary on (weights, shared memory).
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, int n, bool vec, float (&f)[8]) {
-    if (vec) {
-        if constexpr (sizeof(T) == 2) {
-            unpack8(*reinterpret_cast<const uint4 *>(p), f);
-        } else {
-            const float4 a = reinterpret_cast<const float4 *>(p)[0];
-            const float4 b = reinterpret_cast<const float4 *>(p)[1];
-            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-        }
+__device__ __forceinline__ void load8(const T *p, float (&f)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        unpack8(*reinterpret_cast<const uint4 *>(p), f);
     } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = j < n ? to_f32(p[j]) : 0.f;
+        const float4 a = reinterpret_cast<const float4 *>(p)[0];
+        const float4 b = reinterpret_cast<const float4 *>(p)[1];
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
     }
+}
+// n <= 8 elements from p on, the rest zero.
+template <typename T>
+__device__ __forceinline__ void load_some(const T *p, int n, float (&f)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = j < n ? to_f32(p[j]) : 0.f;
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(T *p, int n, bool vec, const float (&f)[8]) {
-    if (vec) {
-        if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint4 *>(p) = pack8(f);
-        } else {
-            reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-            reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-        }
+__device__ __forceinline__ void store8(T *p, const float (&f)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4 *>(p) = pack8(f);
     } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) p[j] = from_f32<T>(f[j]);
+        reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
     }
 }
+// Codes in the low bytes of c.
+__device__ __forceinline__ void store8(int8_t *p, const int (&c)[8]) {
+    uint2 u;
+    u.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    u.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
+    *reinterpret_cast<uint2 *>(p) = u;
+}
 
-__device__ __forceinline__ void store_codes(int8_t *p, int n, bool vec, const int (&c)[8]) {
-    if (vec) {
-        uint2 u;
-        u.x = (c[0] & 255) | (c[1] & 255) << 8 | (c[2] & 255) << 16 | (uint32_t)c[3] << 24;
-        u.y = (c[4] & 255) | (c[5] & 255) << 8 | (c[6] & 255) << 16 | (uint32_t)c[7] << 24;
-        *reinterpret_cast<uint2 *>(p) = u;
-    } else {
+// Rows off the boundaries go by way of 1 KB of shared memory per warp: its 256 consecutive
+// elements are moved to and from memory by neighbouring lanes, one element each.  n: elements
+// of the warp that are in the row (all lanes; at most 0 for none).
+template <typename T>
+__device__ __forceinline__ void warp_load(const T *p, int n, float *mid, float (&f)[8]) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) p[j] = (int8_t)c[j];
-    }
+    for (int j = 0; j < 8; ++j) mid[32 * j + lane] = 32 * j + lane < n ? to_f32(p[32 * j + lane]) : 0.f;
+    __syncwarp();
+    load8(mid + 8 * lane, f);
+    __syncwarp();
+}
+template <typename T>
+__device__ __forceinline__ void warp_store(T *p, int n, float *mid, const float (&f)[8]) {
+    const int lane = threadIdx.x & 31;
+    store8(mid + 8 * lane, f);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (32 * j + lane < n) p[32 * j + lane] = from_f32<T>(mid[32 * j + lane]);
+    __syncwarp();
+}
+__device__ __forceinline__ void warp_store(int8_t *p, int n, float *mid, const int (&c)[8]) {
+    const int lane = threadIdx.x & 31;
+    store8(reinterpret_cast<int8_t *>(mid) + 8 * lane, c);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (32 * j + lane < n) p[32 * j + lane] = reinterpret_cast<const int8_t *>(mid)[32 * j + lane];
+    __syncwarp();
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -94,193 +119,242 @@ __device__ __forceinline__ void reduce_row(float &v, uint32_t &m, uint32_t *slot
 
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
+// |q| <= 127 to the nearest integer, ties to even: added to 1.5 * 2^23 it is the low bits of the
+// sum (a conversion to integers runs at an eighth of the rate).
+__device__ __forceinline__ int nearest(float q) { return __float_as_int(__fadd_rn(q, 12582912.f)); }
+
 template <typename T> __device__ __forceinline__ float gate(float z);
 template <> __device__ __forceinline__ float gate<float>(float z) { return z / (1.0f + expf(-z)); }
 template <> __device__ __forceinline__ float gate<bf16>(float z) { return silu(z); }
 
 }  // namespace
 
-// One row per warp (WARP_ROW) or per CTA; a thread holds NV times 8 consecutive elements.
-template <typename T, int MODE, bool OUT8, int NV, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? 128 : 1024)
-rows_kernel(const RowParams p) {
-    __shared__ uint32_t slots[2][64];
-    grid_dependency_wait();
-    const int G = WARP_ROW ? 32 : blockDim.x, t = WARP_ROW ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t row = WARP_ROW ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
-    if (row >= p.T) return;                         // a whole warp, which then meets no barrier
-    const bool vec = p.vec;
-    const int D = p.D;
-    const T *x = (const T *)p.x + row * p.x_st;
-
-    float v[NV][8], g[MODE == kRowGatedNorm ? NV : 1][8];
+// Asynchronous copy of 8 elements to shared memory (16-byte aligned).
+template <typename T>
+__device__ __forceinline__ void copy8(uint8_t *dst, const T *src) {
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int b = 0; b < 8 * (int)sizeof(T); b += 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                     :: "r"(to + b), "l"(reinterpret_cast<const uint8_t *>(src) + b) : "memory");
+}
+
+// One row per warp (WARP_ROW) or per CTA; a thread holds NV times 8 consecutive elements.
+// Rows go round the grid.  VEC (rows on 16 bytes): a thread copies its elements of the next two
+// rows into a place of its own in shared memory while it works on this one, so that the loads
+// never pause; the weights stay in registers.
+template <typename T, int MODE, bool OUT8, int NV, bool WARP_ROW, bool VEC>
+__global__ void __launch_bounds__(WARP_ROW ? 128 : 1024)
+rows_kernel(const __grid_constant__ RowParams p) {
+    constexpr int INPUTS = MODE == kRowQuantize ? 1 : 2, PIECE = 8 * (int)sizeof(T);
+    constexpr bool HELD = MODE != kRowQuantize && NV <= 2;  // weights in registers
+    extern __shared__ __align__(16) uint8_t ring[];     // [slot][input][NV][thread]
+    __shared__ uint32_t slots[2][2][64];
+    const int G = WARP_ROW ? 32 : blockDim.x, t = WARP_ROW ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t step = WARP_ROW ? (int64_t)gridDim.x * 4 : gridDim.x;
+    const int64_t begin = WARP_ROW ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+    const int D = p.D;
+    const T *second = (const T *)(MODE == kRowGatedNorm ? p.z : p.res);      // may be null
+    const int64_t second_st = MODE == kRowGatedNorm ? p.z_st : p.res_st;
+    grid_dependents_launch();
+    grid_dependency_wait();
+    if (begin >= p.T) return;                           // a whole warp, which then meets no barrier
+
+    float w[HELD ? NV : 1][8];
+    // the weights of vector i: zero past the row's end
+    auto weights = [&](int i, float (&f)[8]) {
         const int e = (i * G + t) * 8, n = D - e;
-        if (n > 0) {
-            load8(x + e, n, vec, v[i]);
-            if constexpr (MODE == kRowGatedNorm)
-                load8((const T *)p.z + row * p.z_st + e, n, vec, g[i]);
+        const int at = MODE == kRowGatedNorm ? e & (p.head - 1) : e;
+        if (VEC && n > 0) {
+            if (p.w_f32) load8((const float *)p.w + at, f);
+            else load8((const bf16 *)p.w + at, f);
+        } else {
+            if (p.w_f32) load_some((const float *)p.w + at, n, f);
+            else load_some((const bf16 *)p.w + at, n, f);
+        }
+        if (MODE == kRowAddNorm)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = j < n ? p.offset + f[j] : 0.f;
+    };
+    float *mid = reinterpret_cast<float *>(ring) + (threadIdx.x >> 5) * 256;     // not VEC
+    // vector i of an input: its 8 elements, zero past the row's end
+    auto input = [&](const T *row, const uint8_t *here, int i, float (&f)[8]) {
+        const int e = (i * G + t) * 8;
+        if constexpr (!VEC) {
+            const int first = e - 8 * (t & 31);
+            warp_load(row + first, D - first, mid, f);
+        } else if (e < D) {
+            load8(reinterpret_cast<const T *>(here), f);
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[i][j] = 0.f;
-                if constexpr (MODE == kRowGatedNorm) g[i][j] = 0.f;
+            for (int j = 0; j < 8; ++j) f[j] = 0.f;
+        }
+    };
+    auto output = [&](auto *row, int i, const auto &f) {
+        const int e = (i * G + t) * 8, first = e - 8 * (t & 31);
+        if constexpr (!VEC) warp_store(row + first, D - first, mid, f);
+        else if (e < D) store8(row + e, f);
+    };
+    auto place = [&](int slot, int input, int i) {
+        return ring + (((slot * INPUTS + input) * NV + i) * (int)blockDim.x + (int)threadIdx.x) * PIECE;
+    };
+    auto fetch = [&](int64_t row, int slot) {
+        if (row < p.T) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int e = (i * G + t) * 8;
+                if (e >= D) continue;
+                copy8(place(slot, 0, i), (const T *)p.x + row * p.x_st + e);
+                if (INPUTS == 2 && second) copy8(place(slot, 1, i), second + row * second_st + e);
             }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if constexpr (VEC) {
+        fetch(begin, 0);
+        fetch(begin + step, 1);
     }
+    if constexpr (HELD)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) weights(i, w[i]);
 
-    float r = 1.f;                                  // what the elements of v still lack
-    uint32_t m = 0;                                 // largest |v|, as bits
-    if constexpr (MODE == kRowQuantize) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = max(m, magnitude(v[i][j]));
-        float none = 0.f;
-        reduce_row<WARP_ROW>(none, m, slots[0]);
-    } else if constexpr (MODE == kRowAddNorm) {
-        if (p.res) {
-            const T *res = (const T *)p.res + row * p.res_st;
-            T *res_out = (T *)p.res_out + row * p.res_out_st;
+    int slot = 0;
+    for (int64_t row = begin; row < p.T; row += step, slot ^= 1) {
+        float v[NV][8];
+        const T *x = (const T *)p.x + row * p.x_st, *y = second + row * second_st;
+        if constexpr (VEC) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        if constexpr (MODE != kRowGatedNorm) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int e = (i * G + t) * 8, n = D - e;
-                if (n <= 0) continue;
-                float u[8];
-                load8(res + e, n, vec, u);
+                input(x, place(slot, 0, i), i, v[i]);
+                if (MODE == kRowAddNorm && second) {
+                    float u[8];
+                    input(y, place(slot, 1, i), i, u);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] += u[j];
-                store8(res_out + e, n, vec, v[i]);
-            }
-        }
-        // The largest |h (offset + w)| is found together with the sum of squares: the common
-        // factor r does not move the place of the maximum, so one reduction serves both.
-        float ss = 0.f;
-        float hw[NV][8];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = (i * G + t) * 8, n = D - e;
-            float w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = 0.f;
-            if (n > 0) {
-                if (p.w_f32) load8((const float *)p.w + e, n, vec, w);
-                else load8((const bf16 *)p.w + e, n, vec, w);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                ss = fmaf(v[i][j], v[i][j], ss);
-                hw[i][j] = v[i][j] * (p.offset + w[j]);
-                m = max(m, magnitude(hw[i][j]));
-            }
-        }
-        reduce_row<WARP_ROW>(ss, m, slots[0]);
-        float shrink = 1.f;
-        if (!(ss < __uint_as_float(kInfBits)) || m >= kInfBits) {
-            // Squares or products past fp32: once more with h / 2^80.  A row that holds an
-            // infinity or a NaN stays without a finite sum.
-            shrink = 8.271806125530277e-25f;
-            ss = 0.f;
-            m = 0;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int e = (i * G + t) * 8, n = D - e;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (j >= n) continue;
-                    const float h = v[i][j] * shrink;
-                    const float w = p.w_f32 ? ((const float *)p.w)[e + j] : to_f32(((const bf16 *)p.w)[e + j]);
-                    ss = fmaf(h, h, ss);
-                    hw[i][j] = h * (p.offset + w);
-                    m = max(m, magnitude(hw[i][j]));
+                    for (int j = 0; j < 8; ++j) v[i][j] += u[j];
                 }
             }
-            reduce_row<WARP_ROW>(ss, m, slots[1]);
+            if constexpr (VEC) fetch(row + 2 * step, slot);     // over what this thread has read
+            if (MODE == kRowAddNorm && second)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) output((T *)p.res_out + row * p.res_out_st, i, v[i]);
         }
-        r = 1.f / sqrtf(ss / (float)D + p.eps * shrink * shrink);
+
+        float r = 1.f;                                  // what the elements still lack
+        uint32_t m = 0;                                 // largest of them, as bits
+        if constexpr (MODE == kRowQuantize) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = hw[i][j];
-    } else {
-        const int lanes = p.head >> 3;              // threads of a head: a power of two up to 32
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = (i * G + t) * 8, n = D - e;
-            float ss = 0.f, shrink = 1.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-            for (int s = lanes >> 1; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
-            const bool big = !(ss < __uint_as_float(kInfBits));
-            if (__any_sync(0xffffffffu, big)) {     // as above, for the heads that need it
-                float s2 = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float h = v[i][j] * 8.271806125530277e-25f;
-                    s2 = fmaf(h, h, s2);
-                }
-                for (int s = lanes >> 1; s > 0; s >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, s);
-                if (big) {
-                    ss = s2;
-                    shrink = 8.271806125530277e-25f;
-                }
-            }
-            const float rh = 1.f / sqrtf(ss / (float)p.head + p.eps * shrink * shrink);
-            float w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = 0.f;
-            if (n > 0) {
-                const int o = e & (p.head - 1);
-                if (p.w_f32) load8((const float *)p.w + o, 8, vec, w);
-                else load8((const bf16 *)p.w + o, 8, vec, w);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[i][j] = v[i][j] * shrink * rh * w[j] * gate<T>(g[i][j]);
-                m = max(m, magnitude(v[i][j]));
-            }
-        }
-        if constexpr (OUT8) {
+                for (int j = 0; j < 8; ++j) m = max(m, magnitude(v[i][j]));
             float none = 0.f;
-            reduce_row<WARP_ROW>(none, m, slots[0]);
-        }
-    }
-
-    if constexpr (OUT8) {
-        // r max|v|, at least 127 * 2^-126: then neither the scale nor its inverse overflows.
-        const float largest = fmaxf(r * __uint_as_float(m), 127.f * kTinyScale);
-        const bool bad = m >= kInfBits || !(largest < __uint_as_float(kInfBits));
-        const float inv = bad ? 0.f : 127.f / largest;
-        if (t == 0) p.scale[row] = bad ? __uint_as_float(0x7fc00000u) : largest / 127.f;
-        int8_t *y = (int8_t *)p.y + row * p.y_st;
+            reduce_row<WARP_ROW>(none, m, slots[slot][0]);
+        } else if constexpr (MODE == kRowAddNorm) {
+            // The largest |h (offset + w)| is found together with the sum of squares: the common
+            // factor r does not move the place of the maximum, so one reduction serves both.
+            float ss = 0.f;
+            auto measure = [&]() {
+                ss = 0.f;
+                m = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = (i * G + t) * 8, n = D - e;
-            if (n <= 0) continue;
-            int c[8];
+                for (int i = 0; i < NV; ++i) {
+                    float f[8];
+                    if constexpr (!HELD) weights(i, f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float q = v[i][j] * r * inv;
-                // bf16 rows meet ties exactly (an element of half the largest stands at 63.5).
-                // With significands X and A of 8 bits, 127 X / (A 2^s) is a tie or at least
-                // 2^-16 of itself away from one, so rounding it to 18 bits brings ties back
-                // and moves nothing else across.
-                if (MODE == kRowQuantize && sizeof(T) == 2)
-                    q = __int_as_float((__float_as_int(q) + 32) & ~63);
-                c[j] = bad ? 0 : __float2int_rn(q);
+                    for (int j = 0; j < 8; ++j) {
+                        ss = fmaf(v[i][j], v[i][j], ss);
+                        m = max(m, magnitude(v[i][j] * (HELD ? w[HELD ? i : 0][j] : f[j])));
+                    }
+                }
+            };
+            measure();
+            reduce_row<WARP_ROW>(ss, m, slots[slot][0]);
+            float shrink = 1.f;
+            if (!(ss < __uint_as_float(kInfBits)) || m >= kInfBits) {
+                // Squares or products past fp32: once more with h / 2^80.  A row that holds an
+                // infinity or a NaN stays without a finite sum.
+                shrink = kShrink;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i][j] *= shrink;
+                measure();
+                reduce_row<WARP_ROW>(ss, m, slots[slot][1]);
             }
-            store_codes(y + e, n, vec, c);
+            r = 1.f / sqrtf(__fadd_rn(ss / (float)D, p.eps * shrink * shrink));
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float f[8];
+                if constexpr (!HELD) weights(i, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] *= HELD ? w[HELD ? i : 0][j] : f[j];
+            }
+        } else {
+            const int lanes = p.head >> 3;              // threads of a head: a power of two up to 32
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float g[8], f[8];
+                input(x, place(slot, 0, i), i, v[i]);
+                input(y, place(slot, INPUTS - 1, i), i, g);
+                float ss = 0.f, shrink = 1.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+                for (int s = lanes >> 1; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
+                const bool big = !(ss < __uint_as_float(kInfBits));
+                if (__any_sync(0xffffffffu, big)) {     // as above, for the heads that need it
+                    if (big) shrink = kShrink;
+                    ss = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        v[i][j] *= shrink;
+                        ss = fmaf(v[i][j], v[i][j], ss);
+                    }
+                    for (int s = lanes >> 1; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
+                }
+                const float rh = 1.f / sqrtf(__fadd_rn(ss / (float)p.head, p.eps * shrink * shrink));
+                if constexpr (!HELD) weights(i, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[i][j] = v[i][j] * rh * (HELD ? w[HELD ? i : 0][j] : f[j]) * gate<T>(g[j]);
+                    m = max(m, magnitude(v[i][j]));
+                }
+            }
+            if constexpr (VEC) fetch(row + 2 * step, slot);
+            if constexpr (OUT8) {
+                float none = 0.f;
+                reduce_row<WARP_ROW>(none, m, slots[slot][0]);
+            }
         }
-    } else {
-        T *y = (T *)p.y + row * p.y_st;
+
+        if constexpr (OUT8) {
+            // r max|v|, at least 127 * 2^-126: then neither the scale nor its inverse overflows.
+            const float largest = fmaxf(r * __uint_as_float(m), 127.f * kTinyScale);
+            const bool bad = m >= kInfBits || !(largest < __uint_as_float(kInfBits));
+            const float inv = bad ? 0.f : 127.f / largest;
+            if (t == 0) p.scale[row] = bad ? __uint_as_float(0x7fc00000u) : largest / 127.f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = (i * G + t) * 8, n = D - e;
-            if (n <= 0) continue;
+            for (int i = 0; i < NV; ++i) {
+                int c[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] *= r;
-            store8(y + e, n, vec, v[i]);
+                for (int j = 0; j < 8; ++j) {
+                    float q = v[i][j] * r * inv;
+                    // bf16 rows meet ties exactly (an element of half the largest stands at 63.5).
+                    // With significands X and A of 8 bits, 127 X / (A 2^s) is a tie or at least
+                    // 2^-16 of itself away from one, so rounding it to 18 bits brings ties back
+                    // and moves nothing else across.
+                    if (MODE == kRowQuantize && sizeof(T) == 2)
+                        q = __int_as_float((__float_as_int(q) + 32) & ~63);
+                    c[j] = bad ? 0 : nearest(q);
+                }
+                output((int8_t *)p.y + row * p.y_st, i, c);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] *= r;
+                output((T *)p.y + row * p.y_st, i, v[i]);
+            }
         }
     }
 }
@@ -291,21 +365,52 @@ namespace gdn_host {
 
 using namespace gdn;
 
+constexpr int kRowSmem = 220 * 1024;
+
+template <typename T, int MODE, bool OUT8, int NV, bool WARP_ROW, bool VEC>
+static gdn_status_t launch_rows_k(const RowParams &p, int threads, cudaStream_t st) {
+    auto kern = rows_kernel<T, MODE, OUT8, NV, WARP_ROW, VEC>;
+    const int smem = VEC ? 2 * (MODE == kRowQuantize ? 1 : 2) * NV * threads * 8 * (int)sizeof(T) : 32 * threads;
+    static std::atomic<uint64_t> ready{0};   // one bit per device (beyond 63: set every time)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+    if (VEC && (dev > 63 || !((ready.load() >> dev) & 1u))) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem) != cudaSuccess)
+            return GDN_ERR_CUDA;
+        if (dev <= 63) ready.fetch_or(1ull << dev);
+    }
+    const int sms = matmul_sm_count(dev);
+    if (sms <= 0) return GDN_ERR_CUDA;
+    // as many CTAs as the SMs take at once: by registers (64 a thread; 48 where a row has one
+    // input) and by shared memory
+    int per = 65536 / (threads * (MODE == kRowQuantize ? 48 : 64));
+    if (per > 220 * 1024 / (smem + 2048)) per = 220 * 1024 / (smem + 2048);
+    if (per < 1) per = 1;
+    const int64_t rows = WARP_ROW ? (p.T + 3) / 4 : p.T, most = VEC ? (int64_t)sms * per : rows;
+    return launch_dependent(kern, dim3((unsigned)(rows < most ? rows : most)), dim3(threads), smem, st, p) == cudaSuccess
+               ? GDN_OK : GDN_ERR_CUDA;
+}
+
 template <typename T, int MODE, bool OUT8>
 static gdn_status_t launch_rows_t(const RowParams &p, cudaStream_t st) {
     const int chunks = (p.D + 7) / 8;               // 8-element pieces of a row
-    cudaError_t e;
-    if (chunks <= 128) {                            // a warp per row
-        const dim3 grid((unsigned)((p.T + 3) / 4));
-        e = chunks <= 32 ? launch_dependent(rows_kernel<T, MODE, OUT8, 1, true>, grid, dim3(128), 0, st, p)
-                         : launch_dependent(rows_kernel<T, MODE, OUT8, 4, true>, grid, dim3(128), 0, st, p);
-    } else {
-        const int nv = chunks <= 2048 ? 2 : 4, threads = ((chunks + nv - 1) / nv + 31) / 32 * 32;
-        const dim3 grid((unsigned)p.T);
-        e = nv == 2 ? launch_dependent(rows_kernel<T, MODE, OUT8, 2, false>, grid, dim3(threads), 0, st, p)
-                    : launch_dependent(rows_kernel<T, MODE, OUT8, 4, false>, grid, dim3(threads), 0, st, p);
-    }
-    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    // two rows of both inputs have to fit: fp32 rows up to 16384 and all of bf16
+    const bool vec = p.vec && 4 * (size_t)p.D * sizeof(T) + 8192 <= (size_t)kRowSmem;
+    if (chunks <= 32)
+        return vec ? launch_rows_k<T, MODE, OUT8, 1, true, true>(p, 128, st)
+                   : launch_rows_k<T, MODE, OUT8, 1, true, false>(p, 128, st);
+    if (chunks <= 64)
+        return vec ? launch_rows_k<T, MODE, OUT8, 2, true, true>(p, 128, st)
+                   : launch_rows_k<T, MODE, OUT8, 2, true, false>(p, 128, st);
+    if (chunks <= 128)
+        return vec ? launch_rows_k<T, MODE, OUT8, 4, true, true>(p, 128, st)
+                   : launch_rows_k<T, MODE, OUT8, 4, true, false>(p, 128, st);
+    const int nv = chunks <= 2048 ? 2 : 4, threads = ((chunks + nv - 1) / nv + 31) / 32 * 32;
+    if (nv == 2)
+        return vec ? launch_rows_k<T, MODE, OUT8, 2, false, true>(p, threads, st)
+                   : launch_rows_k<T, MODE, OUT8, 2, false, false>(p, threads, st);
+    return vec ? launch_rows_k<T, MODE, OUT8, 4, false, true>(p, threads, st)
+               : launch_rows_k<T, MODE, OUT8, 4, false, false>(p, threads, st);
 }
 
 template <typename T>
