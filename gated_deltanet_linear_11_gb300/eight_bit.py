@@ -14,21 +14,33 @@ __all__ = ["gdn_quantize_rows", "gdn_add_rmsnorm", "gdn_gated_rmsnorm", "gdn_mat
            "gdn_matmul_i8_workspace_size"]
 
 
+# Called once per layer and token, as the entries of the package's own module: descriptors are
+# packed in one go, and the checks of the usual case come first.
+_PACK = _lib.GDN_MATRIX_PACK.pack
+
+
+def _names(dtypes):
+    return " or ".join(str(x).replace("torch.", "") for x in dtypes)
+
+
 def _matrix(name, t, dtypes):
     """gdn_matrix_t of a view [rows, cols] or [1, rows, cols], packed."""
     dt = dtypes.get(t.dtype)
     if dt is None:
-        raise TypeError("%s must be %s, got %s" % (
-            name, " or ".join(str(x).replace("torch.", "") for x in dtypes), t.dtype))
-    if t.dim() == 3 and t.shape[0] == 1:
-        t = t[0]
-    if t.dim() != 2:
+        raise TypeError("%s must be %s, got %s" % (name, _names(dtypes), t.dtype))
+    strides = t.stride()
+    if len(strides) == 2:
+        rows, cols = t.shape
+        stride, unit = strides
+    elif len(strides) == 3 and t.shape[0] == 1:
+        _, rows, cols = t.shape
+        _, stride, unit = strides
+    else:
         raise ValueError("%s must be [rows, cols] or [1, rows, cols], got %s"
                          % (name, tuple(t.shape)))
-    rows, cols = t.shape
-    if cols > 1 and rows > 0 and t.stride(1) != 1:
+    if unit != 1 and cols > 1 and rows > 0:
         raise ValueError("%s must have its rows' elements next to each other" % name)
-    return _lib.GDN_MATRIX_PACK.pack(t.data_ptr(), rows, cols, t.stride(0), dt)
+    return _PACK(t.data_ptr(), rows, cols, stride, dt)
 
 
 def _vector(name, t, n, dtypes):
@@ -36,11 +48,10 @@ def _vector(name, t, n, dtypes):
     if t is None:
         return None
     dt = dtypes.get(t.dtype)
-    if dt is None or t.shape != (n,) or not t.is_contiguous():
+    if dt is None or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
         raise ValueError("%s must be a contiguous vector of %d elements (%s), got %s %s"
-                         % (name, n, " or ".join(str(x).replace("torch.", "") for x in dtypes),
-                            t.dtype, tuple(t.shape)))
-    return _lib.GDN_MATRIX_PACK.pack(t.data_ptr(), 1, n, n, dt)
+                         % (name, n, _names(dtypes), t.dtype, tuple(t.shape)))
+    return _PACK(t.data_ptr(), 1, n, n, dt)
 
 
 _F32 = {torch.float32: _lib.GDN_F32}
@@ -49,15 +60,19 @@ _I8 = {torch.int8: _lib.GDN_I8}
 
 def _eight_bit_rows(shape, like, q, scale):
     """Codes (rows on 16 bytes, so that products read them fastest) and scales."""
-    T, D = shape[-2:]
+    D = shape[-1]
     if q is None:
-        q = torch.empty(shape[:-1] + (-(-D // 16) * 16,), dtype=torch.int8,
-                        device=like.device)[..., :D]
+        if D % 16 == 0:
+            q = torch.empty(shape, dtype=torch.int8, device=like.device)
+        else:
+            q = torch.empty((*shape[:-1], -(-D // 16) * 16), dtype=torch.int8,
+                            device=like.device)[..., :D]
     elif q.shape != shape:
         raise ValueError("8-bit rows must be of shape %s, got %s" % (tuple(shape), tuple(q.shape)))
     if scale is None:
-        scale = torch.empty(T, dtype=torch.float32, device=like.device)
-    _vector("scale", scale, T, _F32)
+        scale = torch.empty(shape[-2], dtype=torch.float32, device=like.device)
+    else:
+        _vector("scale", scale, shape[-2], _F32)
     return q, scale
 
 
@@ -106,11 +121,11 @@ def gdn_add_rmsnorm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, eight
         if residual_out is not None:
             raise ValueError("residual_out comes with a residual")
     else:
+        shape = x.shape
+        if residual.shape != shape or (residual_out is not None and residual_out.shape != shape):
+            raise ValueError("residual and residual_out must have x's shape %s" % (tuple(shape),))
         if residual_out is None:
-            residual_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if residual.shape != x.shape or residual_out.shape != x.shape:
-            raise ValueError("residual and residual_out must have x's shape %s"
-                             % (tuple(x.shape),))
+            residual_out = torch.empty(shape, dtype=x.dtype, device=x.device)
         res, out = _matrix("residual", residual, _DT), _matrix("residual_out", residual_out, _DT)
     y, scale, my = _norm_output(x.shape, x, eight_bit, y, scale)
     rc = lib.gdn_add_rmsnorm(mx, res, out, _vector("weight", weight, x.shape[-1], _DT),
@@ -156,13 +171,14 @@ def gdn_matmul_i8(a, a_scale, w, w_scale, bias=None, dtype=torch.bfloat16, out=N
     lib, debug = _entry("gdn_matmul_i8")
     _need_cuda(a, a_scale, w, w_scale, bias, out, workspace, status)
     ma, mw = _matrix("a", a, _I8), _matrix("w", w, _I8)
-    M, K = a.shape[-2:]
-    N = w.shape[-2]
-    if w.shape[-1] != K:
-        raise ValueError("a has rows of %d codes and w of %d" % (K, w.shape[-1]))
+    lead = a.shape
+    M, K = lead[-2:]
+    N, Kw = w.shape[-2:]
+    if Kw != K:
+        raise ValueError("a has rows of %d codes and w of %d" % (K, Kw))
     _vector("a_scale", a_scale, M, _F32)
     _vector("w_scale", w_scale, N, _F32)
-    shape = a.shape[:-1] + (N,)
+    shape = (M, N) if len(lead) == 2 else (1, M, N)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=a.device)
     elif out.shape != shape:

@@ -108,13 +108,13 @@ def test_matmul_i8_workspace(lib):
     assert f(mat(0, 64, I8), w) == f(mat(4, 64, I8), mat(0, 64, I8)) == 0
     assert f(mat(4, 0, I8), mat(8, 0, I8)) == f(mat(4, 64, I8), mat(8, 63, I8)) == 0
     assert f(mat(64, 64, I8), w) == 0
-    assert f(mat(100, 64, I8), w) == 100 * 128 + 400
+    assert f(mat(100, 64, I8), w) == 100 * 128 + 512            # 400 bytes, to 256
     assert f(mat(100, 64, I8), w, _lib.GDN_PREFILL_SIMT) == 0
     odd = mat(8, 65, I8)
     assert f(mat(1, 65, I8), odd) == 768                        # 8 rows of 80, to 256 bytes
     assert f(mat(3, 65, I8), odd) == 256 + 768
     assert f(mat(3, 65, I8, stride=80), mat(8, 65, I8, stride=80)) == 0
-    assert f(mat(100, 65, I8), odd) == 768 + (100 * 72 * 2 + 255) // 256 * 256 + 400
+    assert f(mat(100, 65, I8), odd) == 768 + (100 * 72 * 2 + 255) // 256 * 256 + 512
     assert f(mat(3, 64, I8, ptr=FAKE + 1), w) == 256
 
 
