@@ -2,9 +2,12 @@
 softmax attention over a paged 4-bit key/value cache, one after the other.
 
     python examples/hybrid_decode.py [--prompts 4] [--length 2000] [--tokens 64]
+                                     [--gate] [--eight-bit]
 
 Packed prompts of different lengths go through ``prefill``; then every ``step`` feeds one
-token per sequence, replayed as one CUDA graph.
+token per sequence, replayed as one CUDA graph.  ``--gate`` gives the Gated DeltaNet layers
+their output norm and gate; ``--eight-bit`` keeps the projections in 8 bits, fed by norms that
+write 8-bit rows.
 """
 import argparse
 import os
@@ -28,10 +31,12 @@ def rms_norm(x):
 class HybridStack:
     """Token mixers ``kinds`` with residuals around them; Hk key and Hv value heads (for
     attention: Hv query heads over Hk key/value heads).  Holds the states of up to
-    ``sequences`` sequences of up to ``max_len`` tokens."""
+    ``sequences`` sequences of up to ``max_len`` tokens.  ``gate``: the delta layers end in
+    norm(o) * silu(z), z from their input projection.  ``eight_bit``: projections as products
+    of 8-bit integers."""
 
     def __init__(self, kinds, hidden=512, vocab=1000, Hk=2, Hv=8, sequences=4, max_len=4096,
-                 page=32, seed=0, device="cuda"):
+                 page=32, seed=0, device="cuda", gate=False, eight_bit=False):
         self.kinds, self.Hk, self.Hv, self.N, self.max_len = kinds, Hk, Hv, sequences, max_len
         gen = torch.Generator().manual_seed(seed)
 
@@ -41,7 +46,8 @@ class HybridStack:
         self.embed = weight(hidden, vocab).t().contiguous() * hidden ** 0.5
         self.out = weight(hidden, vocab)
         self.qkv_width = (2 * Hk + Hv) * D
-        extra = {DELTA: 2 * Hv, LINEAR: 0, ATTENTION: 0}
+        self.gate, self.eight_bit = gate, eight_bit
+        extra = {DELTA: 2 * Hv + (Hv * D if gate else 0), LINEAR: 0, ATTENTION: 0}
         self.w_in = [weight(hidden, self.qkv_width + extra[x]) for x in kinds]
         self.w_out = [weight(Hv * D, hidden) for _ in kinds]
         self.conv = weight(4, self.qkv_width).t().contiguous()
@@ -59,6 +65,35 @@ class HybridStack:
         pages = torch.randperm(sequences * width, generator=gen)
         self.table = pages.int().view(sequences, width).to(device)
         self.lens = torch.zeros(sequences, dtype=torch.int32, device=device)
+        self.norm_weight = torch.ones(hidden, dtype=torch.bfloat16, device=device)
+        self.gate_weight = torch.ones(D, dtype=torch.bfloat16, device=device)
+        if eight_bit:                           # rows of a projection: its output channels
+            self.w_in = [gdn.gdn_quantize_rows(w.t().contiguous()) for w in self.w_in]
+            self.w_out = [gdn.gdn_quantize_rows(w.t().contiguous()) for w in self.w_out]
+            self.out = gdn.gdn_quantize_rows(self.out.t().contiguous())
+
+    def _norm(self, x, delta):
+        """(norm of x + delta, x + delta) in front of a projection; delta None at first."""
+        if not self.eight_bit:
+            x = x if delta is None else x + delta
+            return rms_norm(x), x
+        if delta is None:
+            return gdn.gdn_add_rmsnorm(x, self.norm_weight, eight_bit=True)[0], x
+        return gdn.gdn_add_rmsnorm(delta, self.norm_weight, x, eight_bit=True)
+
+    def _project(self, x, w):
+        return gdn.gdn_matmul_i8(*x, *w) if self.eight_bit else x @ w
+
+    def _project_out(self, i, o, h):
+        """A mixer's output [T, Hv, D] through its norm and gate, if any, and projection."""
+        if self.kinds[i] == DELTA and self.gate:
+            z = h[:, self.qkv_width + 2 * self.Hv:].unflatten(-1, (-1, D))
+            y = gdn.gdn_gated_rmsnorm(o, z, self.gate_weight, eight_bit=self.eight_bit)
+        elif self.eight_bit:
+            y = gdn.gdn_quantize_rows(o.flatten(1))
+        else:
+            y = o.flatten(1)
+        return self._project(y, self.w_out[i])
 
     def _split(self, qkv):
         q, k, v = qkv.split([self.Hk * D, self.Hk * D, self.Hv * D], dim=-1)
@@ -69,7 +104,7 @@ class HybridStack:
         return q.unflatten(-1, (-1, D)), k.unflatten(-1, (-1, D)), v.unflatten(-1, (-1, D))
 
     def _gates(self, h):
-        a, b = h[:, self.qkv_width:].float().chunk(2, dim=-1)
+        a, b = h[:, self.qkv_width:self.qkv_width + 2 * self.Hv].float().chunk(2, dim=-1)
         return -torch.nn.functional.softplus(a), torch.sigmoid(b)
 
     def _attend(self, i, qkv, **new):
@@ -83,9 +118,10 @@ class HybridStack:
         cu_dev = cu.to(tokens.device)
         self.lens.copy_(cu[1:] - cu[:-1])
         new = dict(cu_seqlens=cu_dev, cu_seqlens_host=cu)
-        x = self.embed[tokens]
+        x, delta = self.embed[tokens], None
         for i, kind in enumerate(self.kinds):
-            h = rms_norm(x) @ self.w_in[i]
+            y, x = self._norm(x, delta)
+            h = self._project(y, self.w_in[i])
             qkv = h[:, :self.qkv_width]
             if kind == DELTA:
                 g, beta = self._gates(h)
@@ -99,15 +135,17 @@ class HybridStack:
                                               final_state=self.state[i], **new)
             else:
                 o = self._attend(i, qkv, **new)
-            x = x + o.flatten(1) @ self.w_out[i]
-        return rms_norm(x[cu_dev[1:].long() - 1]) @ self.out
+            delta = self._project_out(i, o, h)
+        last = cu_dev[1:].long() - 1
+        return self._project(self._norm(x[last], delta[last])[0], self.out)
 
     def step(self, tokens):
         """Logits [N, vocab] after one more token per sequence."""
         self.lens += 1
-        x = self.embed[tokens]
+        x, delta = self.embed[tokens], None
         for i, kind in enumerate(self.kinds):
-            h = rms_norm(x) @ self.w_in[i]
+            y, x = self._norm(x, delta)
+            h = self._project(y, self.w_in[i])
             qkv = h[:, :self.qkv_width]
             if kind == DELTA:
                 g, beta = self._gates(h)
@@ -119,8 +157,8 @@ class HybridStack:
                 o = gdn.gdn_linear_decode(q, k, v, self.decay, self.state[i], scale=1 / D)
             else:
                 o = self._attend(i, qkv)
-            x = x + o.flatten(1) @ self.w_out[i]
-        return rms_norm(x) @ self.out
+            delta = self._project_out(i, o, h)
+        return self._project(self._norm(x, delta)[0], self.out)
 
 
 def main():
@@ -128,9 +166,12 @@ def main():
     ap.add_argument("--prompts", type=int, default=4)
     ap.add_argument("--length", type=int, default=2000, help="of the longest prompt")
     ap.add_argument("--tokens", type=int, default=64, help="to answer with, per prompt")
+    ap.add_argument("--gate", action="store_true", help="output gates of the delta layers")
+    ap.add_argument("--eight-bit", action="store_true", help="projections in 8 bits")
     a = ap.parse_args()
     kinds = (DELTA, LINEAR, DELTA, ATTENTION)
-    net = HybridStack(kinds, sequences=a.prompts, max_len=a.length + a.tokens + 4)
+    net = HybridStack(kinds, sequences=a.prompts, max_len=a.length + a.tokens + 4,
+                      gate=a.gate, eight_bit=a.eight_bit)
     lens = [max(1, a.length * (i + 1) // a.prompts) for i in range(a.prompts)]
     cu = torch.tensor([0] + lens).cumsum(0).int()
     prompt = torch.randint(0, 1000, (int(cu[-1]),), generator=torch.Generator().manual_seed(1))
