@@ -244,7 +244,7 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // Bytes of the aligned copies of a and of w (0: none needed).
 void align_sizes(const MatmulParams &p, size_t &a, size_t &w) {
     const size_t st = ((size_t)p.K + 15) / 16 * 16;
-    a = p.M > kPairTokensFrom || on_16_bytes(p.a, p.M, p.a_st) ? 0 : up256((size_t)p.M * st);
+    a = matmul_i8_pairs(p.M, p.N, p.K) || on_16_bytes(p.a, p.M, p.a_st) ? 0 : up256((size_t)p.M * st);
     w = on_16_bytes(p.w, p.N, p.w_st) ? 0 : up256((size_t)p.N * st);
 }
 
@@ -288,7 +288,7 @@ size_t matmul_i8_workspace(const MatmulParams &p, uint32_t flags) {
     if (flags & GDN_PREFILL_SIMT) return 0;
     size_t a, w;
     align_sizes(p, a, w);
-    return a + w + (p.M > kPairTokensFrom ? matmul_i8_pair_workspace(p.M, p.N, p.K) : 0);
+    return a + w + (matmul_i8_pairs(p.M, p.N, p.K) ? matmul_i8_pair_workspace(p.M, p.N, p.K) : 0);
 }
 
 gdn_status_t launch_matmul_i8(const MatmulParams &given, uint32_t flags, void *ws, cudaStream_t st) {
@@ -311,8 +311,8 @@ gdn_status_t launch_matmul_i8(const MatmulParams &given, uint32_t flags, void *w
     if (p.M == 2) return launch_stream<2>(p, st);
     if (p.M <= 4) return launch_stream<4>(p, st);
     if (p.M <= 8) return launch_stream<8>(p, st);
-    if (p.M <= kPairTokensFrom) return launch_matmul_i8_few(p, st);
-    return launch_matmul_i8_pair(p, at, st);
+    if (matmul_i8_pairs(p.M, p.N, p.K)) return launch_matmul_i8_pair(p, at, st);
+    return launch_matmul_i8_few(p, st);
 }
 
 }  // namespace gdn_host

@@ -69,8 +69,6 @@ __device__ __forceinline__ void i8_halves(uint32_t w, uint32_t &lo, uint32_t &hi
 }  // namespace gdn
 
 namespace gdn_host {
-constexpr int64_t kPairTokensFrom = 64; // more tokens than these: pairs of CTAs
-
 // Boxes of 128 bytes of `box_rows` rows of codes, or of fp16; a row's end and the rows' end
 // read as zeros.
 bool row_map(CUtensorMap *m, const void *ptr, bool half, int64_t rows, int64_t K, int64_t stride, int box_rows,
@@ -78,7 +76,8 @@ bool row_map(CUtensorMap *m, const void *ptr, bool half, int64_t rows, int64_t K
 int matmul_sm_count(int dev);           // 0 on an error
 size_t matmul_i8_workspace(const gdn::MatmulParams &p, uint32_t flags);
 gdn_status_t launch_matmul_i8(const gdn::MatmulParams &p, uint32_t flags, void *ws, cudaStream_t st);
-// rows of w (and of a, for few tokens) on 16 bytes
+// rows of w (and of a, unless by pairs) on 16 bytes
+bool matmul_i8_pairs(int64_t M, int64_t N, int64_t K);
 gdn_status_t launch_matmul_i8_few(const gdn::MatmulParams &p, cudaStream_t st);
 size_t matmul_i8_pair_workspace(int64_t M, int64_t N, int64_t K);
 gdn_status_t launch_matmul_i8_pair(const gdn::MatmulParams &p, void *ws, cudaStream_t st);

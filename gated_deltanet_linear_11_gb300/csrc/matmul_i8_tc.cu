@@ -480,10 +480,20 @@ __device__ __forceinline__ void pair_put(float *to, const float (&s)[128], int i
     }
 }
 
-// Scales and stores 16 tokens of 32 channels; m, n: the first of them.  A lane takes eight
-// channels of two tokens, side by side: two warps a scheduler wait for every result.
+// Scales and stores 16 tokens of 32 channels; m, n: the first of them.  Where rows start on 16
+// bytes a lane takes eight channels of two tokens, side by side: with two warps a scheduler
+// every result is waited for.
 __device__ __forceinline__ void pair_store(const MatmulParams &p, const PairOut &o, int group, int64_t m, int64_t n) {
     const int lane = threadIdx.x & 31, rows = (int)min(p.M - m, (int64_t)16), c = 8 * (lane & 3), j = lane >> 2;
+    if (!p.out_vec || n + 32 > p.N) {            // a lane takes a channel
+        const float *from = o.sum + lane * 20 + (lane >> 3) * 8;
+        const float ws = o.scale[lane], bias = o.bias[lane];
+        if (n + lane < p.N)
+#pragma unroll 4
+            for (int i = 0; i < rows; ++i)
+                matmul_store(p, m + i, n + lane, matmul_value(from[i], o.tokens[group][i], ws, bias));
+        return;
+    }
     const float *from = o.sum + c * 20 + c + j;
     float2 f[2][4];
 #pragma unroll
@@ -500,21 +510,12 @@ __device__ __forceinline__ void pair_store(const MatmulParams &p, const PairOut 
             f[x][e] = make_float2(matmul_value(f[x][e].x, as[x], ws.x, bias.x),
                                   matmul_value(f[x][e].y, as[x], ws.y, bias.y));
     }
-    const bool wide = p.out_vec && n + 32 <= p.N;
     const int64_t at = (m + j) * p.out_st + n + c;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         if (j + 8 * x >= rows) continue;
         const int64_t here = at + 8 * x * p.out_st;
-        if (!wide) {
-#pragma unroll 1
-            for (int e = 0; e < 8; ++e)
-                if (n + c + e < p.N) {
-                    const float v = matmul_value(from[20 * e + 8 * x], as[x], o.scale[c + e], o.bias[c + e]);
-                    if (p.out_f32) ((float *)p.out)[here + e] = v;
-                    else ((bf16 *)p.out)[here + e] = from_f32<bf16>(v);
-                }
-        } else if (p.out_f32) {
+        if (p.out_f32) {
             float4 *to = reinterpret_cast<float4 *>((float *)p.out + here);
             to[0] = make_float4(f[x][0].x, f[x][0].y, f[x][1].x, f[x][1].y);
             to[1] = make_float4(f[x][2].x, f[x][2].y, f[x][3].x, f[x][3].y);
@@ -917,10 +918,11 @@ gdn_status_t launch_tc(const MatmulParams &p, cudaStream_t st) {
         !row_map(&maps.a, p.a, false, p.M, p.K, p.a_st, NT, true))
         return GDN_ERR_CUDA;
     const int64_t tiles_m = (p.M + NT - 1) / NT, tiles = tiles_m * ((p.N + kI8Channels - 1) / kI8Channels);
-    // as many ranges of K as keep every SM busy, of at least two steps each
+    // as many ranges of K as keep every SM busy, of at least two steps each; clusters of a power
+    // of two fit the device best (40 tiles: 13.7 us in fours, 17.1 in sevens)
     const int64_t steps = (p.K + kI8Step - 1) / kI8Step, want = (int64_t)sms * Sh::CTAS / tiles;
-    int64_t parts = want < 1 ? 1 : want > 8 ? 8 : want;
-    if (parts > (steps + 1) / 2) parts = (steps + 1) / 2;
+    int64_t parts = 1;
+    while (parts < 8 && 2 * parts <= want && 4 * parts <= steps + 1) parts *= 2;
     if (tiles * parts > 0x7fffffff) return GDN_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * parts));
@@ -995,6 +997,23 @@ gdn_status_t launch_matmul_i8_few(const MatmulParams &p, cudaStream_t st) {
     if (p.M <= 16) return launch_tc<16>(p, st);
     if (p.M <= 32) return launch_tc<32>(p, st);
     return launch_tc<64>(p, st);
+}
+
+// Which kernel takes a product of more than eight tokens.
+bool matmul_i8_pairs(int64_t M, int64_t N, int64_t K) {
+    if (M <= 64) return false;
+    int dev = 0;
+    const int sms = cudaGetDevice(&dev) == cudaSuccess ? matmul_sm_count(dev) : 0;
+    if (sms <= 1) return true;
+    const int64_t pairs = sms / 2, steps = (K + kI8Step - 1) / kI8Step;
+    const PairPlan plan = pair_plan(M, N, K, (int)pairs);
+    const int64_t left = plan.tiles - plan.full;
+    const double turns = (double)((plan.full + pairs - 1) / pairs * steps) +
+                         (double)((left * plan.parts + pairs - 1) / pairs * ((steps + plan.parts - 1) / plan.parts));
+    // in us: 333 tokens of 515 channels of 1008 take 9 here and 30 by pairs, 128 of 2048 of 2048
+    // 11.3 and 13.4, 128 of 5120 of 6144 32 and 22
+    const double few = (double)((M + 63) / 64 * ((N + 127) / 128) * steps) / sms;
+    return 13 + 0.54 * turns < 8 + 0.75 * (few > steps / 8. ? few : steps / 8.);
 }
 
 size_t matmul_i8_pair_workspace(int64_t M, int64_t N, int64_t K) {
