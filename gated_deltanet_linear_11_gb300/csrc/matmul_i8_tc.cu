@@ -203,6 +203,9 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
     tc::fence_after_sync();
     const uint32_t tmem = S.tmem;
     grid_dependents_launch();
+    // codes of w on their way to L2 while the kernel before this one ends
+    if (tid < Sh::STAGES && tid < n) prefetch_2d(&maps.w, (first + tid) * kI8Step, n0);
+    __syncwarp();
     grid_dependency_wait();
 
     ExactSums<HALF> sums;                        // this thread's channel, half of the tokens
