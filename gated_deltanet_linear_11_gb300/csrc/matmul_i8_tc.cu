@@ -39,6 +39,7 @@ template <int NT> struct I8Smem {
     uint8_t conv[2][I8Shape<NT>::CONV];      // [step][64-code block][token][128 bytes]
     uint64_t raw_full[I8Shape<NT>::STAGES], raw_free[I8Shape<NT>::STAGES];
     uint64_t ab_full[2], ab_free[2], d_full[2], d_free[2];
+    float scale[NT];                         // of the tokens
     uint32_t tmem;
     int abort;
 };
@@ -96,8 +97,8 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ int32_t cluster_load(uint32_t addr, uint32_t rank) {
     uint32_t remote;
     int32_t v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote));
     return v;
 }
 
@@ -208,6 +209,10 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
     __syncwarp();
     grid_dependency_wait();
 
+    // scales for the end: this thread's channel, and the tokens'
+    const int64_t own = n0 + (tid & (kI8Channels - 1));
+    const float ws = own < p.N ? p.w_scale[own] : 0.f, bias = own < p.N ? matmul_bias(p, own) : 0.f;
+    for (int i = tid; i < NT; i += kI8Threads) S.scale[i] = p.a_scale[min((int64_t)m0 + i, p.M - 1)];
     ExactSums<HALF> sums;                        // this thread's channel, half of the tokens
     sums.clear();
     const int row = 32 * (warp & 3) + lane, half = warp >> 2;
@@ -253,6 +258,7 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
             // Tokens: a warp takes eight rows of one 64-code block.  Eight lanes take four chunks
             // of rows r and r ^ 5, whose swizzled places differ both where they are read
             // (chunks 0-3 or 4-7) and where they are written (even or odd chunks).
+#pragma unroll
             for (int u = warp; u < NT / 4; u += kI8ConvWarps) {
                 const int blk = u & 1, t = 8 * (u >> 1) + ((lane >> 3) ^ (lane & 4 ? 5 : 0)), c = lane & 3;
                 uint32_t r[8];
@@ -307,15 +313,17 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
     }
     __syncwarp();
 
+    static_assert(kI8ConvWarps == 8, "thread i of the converting warps has channel i mod 128 both ways");
+    __syncthreads();                             // the scales are there
+    const int rows = (int)min((int64_t)NT, p.M - m0);
     if (parts == 1) {
         sums.finish();
-        if (warp < kI8ConvWarps && n0 + row < p.N) {
-            const float ws = p.w_scale[n0 + row], bias = matmul_bias(p, n0 + row);
+        if (warp < kI8ConvWarps && own < p.N) {
 #pragma unroll
-            for (int i = 0; i < HALF; ++i) {
-                const int64_t m = (int64_t)m0 + half * HALF + i;
-                if (m < p.M) matmul_store(p, m, n0 + row, matmul_value(sums.s[i], p.a_scale[m], ws, bias));
-            }
+            for (int i = 0; i < HALF; ++i)
+                if (half * HALF + i < rows)
+                    matmul_store(p, (int64_t)m0 + half * HALF + i, own,
+                                 matmul_value(sums.s[i], S.scale[half * HALF + i], ws, bias));
         }
     } else {
         // [token][channel] sums over the codes that have all been used
@@ -325,15 +333,19 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
 #pragma unroll
             for (int i = 0; i < HALF; ++i) part[(half * HALF + i) * kI8Channels + row] = sums.whole(i);
         cluster_sync();
-        const int rows = (int)min((int64_t)NT, p.M - m0);
-        const uint32_t base = tc::smem_u32(part);
-        for (int i = rank * kI8Threads + tid; i < rows * kI8Channels; i += parts * kI8Threads) {
-            const int64_t m = (int64_t)m0 + i / kI8Channels, nn = (int64_t)n0 + i % kI8Channels;
-            if (nn >= p.N) continue;
-            int32_t sum = 0;
-            for (uint32_t r = 0; r < parts; ++r) sum += cluster_load(base + 4 * i, r);
-            matmul_store(p, m, nn, matmul_value((float)sum, p.a_scale[m], p.w_scale[nn], matmul_bias(p, nn)));
+        // the tokens go round the CTAs, two at a time
+        const uint32_t base = tc::smem_u32(part + row);
+        if (warp < kI8ConvWarps && own < p.N) {
+#pragma unroll 4
+            for (int t = 2 * rank + half; t < rows; t += 2 * parts) {
+                int32_t sum = 0;
+#pragma unroll
+                for (uint32_t r = 0; r < 8; ++r)
+                    if (r < parts) sum += cluster_load(base + 4 * kI8Channels * t, r);
+                matmul_store(p, (int64_t)m0 + t, own, matmul_value((float)sum, S.scale[t], ws, bias));
+            }
         }
+        __syncwarp();
         cluster_sync();                          // before any CTA's memory goes
     }
     tc::fence_before_sync();
