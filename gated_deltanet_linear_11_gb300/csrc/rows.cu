@@ -8,12 +8,13 @@
 //   8 bits:     scale = max|y| / 127, code = y / scale to the nearest integer
 //
 // All three read a row once and write it once, so HBM bounds them.  A row stays in the
-// registers of one warp (up to 1024 elements) or of one CTA, 8 consecutive elements at a time
+// registers of one warp (up to 512 elements) or of one CTA, 8 consecutive elements at a time
 // per thread; sums and maxima go over the row with shuffles and one pass through shared
 // memory.  The split of a row depends on its length alone, so a row's results are the same in
 // any batch.
 #include <atomic>
 
+#include "bulk_ptx.cuh"
 #include "matmul_i8.cuh"
 #include "rows.cuh"
 
@@ -117,7 +118,44 @@ __device__ __forceinline__ void reduce_row(float &v, uint32_t &m, uint32_t *slot
     }
 }
 
+// f op g and f op c, two elements an instruction (the kernel is short of issue slots).
+__device__ __forceinline__ void add8(float (&f)[8], const float (&g)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const float2 t = add_f32x2(make_float2(f[j], f[j + 1]), make_float2(g[j], g[j + 1]));
+        f[j] = t.x;
+        f[j + 1] = t.y;
+    }
+}
+__device__ __forceinline__ void mul8(float (&f)[8], const float (&g)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const float2 t = mul_f32x2(make_float2(f[j], f[j + 1]), make_float2(g[j], g[j + 1]));
+        f[j] = t.x;
+        f[j + 1] = t.y;
+    }
+}
+__device__ __forceinline__ void mul8(float (&f)[8], float c) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const float2 t = mul_f32x2(make_float2(f[j], f[j + 1]), make_float2(c, c));
+        f[j] = t.x;
+        f[j + 1] = t.y;
+    }
+}
+// sum += f^2, of even and of odd elements.
+__device__ __forceinline__ void squares8(float2 &sum, const float (&f)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const float2 t = make_float2(f[j], f[j + 1]);
+        sum = fma_f32x2(t, t, sum);
+    }
+}
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+__device__ __forceinline__ void largest8(uint32_t &m, const float (&f)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) m = max(m, max(magnitude(f[j]), magnitude(f[j + 1])));
+}
 
 // |q| <= 127 to the nearest integer, ties to even: added to 1.5 * 2^23 it is the low bits of the
 // sum (a conversion to integers runs at an eighth of the rate).
@@ -191,8 +229,8 @@ rows_kernel(const __grid_constant__ RowParams p) {
         }
     };
     auto output = [&](auto *row, int i, const auto &f) {
-        const int e = (i * G + t) * 8, first = e - 8 * (t & 31);
-        if constexpr (!VEC) warp_store(row + first, D - first, mid, f);
+        const int e = (i * G + t) * 8;
+        if constexpr (!VEC) warp_store(row + (e - 8 * (t & 31)), D - (e - 8 * (t & 31)), mid, f);
         else if (e < D) store8(row + e, f);
     };
     auto place = [&](int slot, int input, int i) {
@@ -230,8 +268,7 @@ rows_kernel(const __grid_constant__ RowParams p) {
                 if (MODE == kRowAddNorm && second) {
                     float u[8];
                     input(y, place(slot, 1, i), i, u);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[i][j] += u[j];
+                    add8(v[i], u);
                 }
             }
             if constexpr (VEC) fetch(row + 2 * step, slot);     // over what this thread has read
@@ -244,28 +281,32 @@ rows_kernel(const __grid_constant__ RowParams p) {
         uint32_t m = 0;                                 // largest of them, as bits
         if constexpr (MODE == kRowQuantize) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) m = max(m, magnitude(v[i][j]));
+            for (int i = 0; i < NV; ++i) largest8(m, v[i]);
             float none = 0.f;
             reduce_row<WARP_ROW>(none, m, slots[slot][0]);
         } else if constexpr (MODE == kRowAddNorm) {
-            // The largest |h (offset + w)| is found together with the sum of squares: the common
-            // factor r does not move the place of the maximum, so one reduction serves both.
+            // For 8 bits the largest |h (offset + w)| is found together with the sum of squares: the
+            // common factor r does not move the place of the maximum, so one reduction serves both.
             float ss = 0.f;
             auto measure = [&]() {
-                ss = 0.f;
+                float2 sum = make_float2(0.f, 0.f);
                 m = 0;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    float f[8];
-                    if constexpr (!HELD) weights(i, f);
+                    squares8(sum, v[i]);
+                    if constexpr (OUT8) {
+                        float f[8];
+                        if constexpr (HELD) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        ss = fmaf(v[i][j], v[i][j], ss);
-                        m = max(m, magnitude(v[i][j] * (HELD ? w[HELD ? i : 0][j] : f[j])));
+                            for (int j = 0; j < 8; ++j) f[j] = w[i][j];
+                        } else {
+                            weights(i, f);
+                        }
+                        mul8(f, v[i]);
+                        largest8(m, f);
                     }
                 }
+                ss = sum.x + sum.y;
             };
             measure();
             reduce_row<WARP_ROW>(ss, m, slots[slot][0]);
@@ -275,9 +316,7 @@ rows_kernel(const __grid_constant__ RowParams p) {
                 // infinity or a NaN stays without a finite sum.
                 shrink = kShrink;
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[i][j] *= shrink;
+                for (int i = 0; i < NV; ++i) mul8(v[i], shrink);
                 measure();
                 reduce_row<WARP_ROW>(ss, m, slots[slot][1]);
             }
@@ -286,8 +325,9 @@ rows_kernel(const __grid_constant__ RowParams p) {
             for (int i = 0; i < NV; ++i) {
                 float f[8];
                 if constexpr (!HELD) weights(i, f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] *= HELD ? w[HELD ? i : 0][j] : f[j];
+                if constexpr (!OUT8) mul8(v[i], r);         // h r first: no product can overflow
+                if constexpr (HELD) mul8(v[i], w[i]);
+                else mul8(v[i], f);
             }
         } else {
             const int lanes = p.head >> 3;              // threads of a head: a power of two up to 32
@@ -296,28 +336,32 @@ rows_kernel(const __grid_constant__ RowParams p) {
                 float g[8], f[8];
                 input(x, place(slot, 0, i), i, v[i]);
                 input(y, place(slot, INPUTS - 1, i), i, g);
-                float ss = 0.f, shrink = 1.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+                float shrink = 1.f;
+                float2 sum = make_float2(0.f, 0.f);
+                squares8(sum, v[i]);
+                float ss = sum.x + sum.y;
                 for (int s = lanes >> 1; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
                 const bool big = !(ss < __uint_as_float(kInfBits));
                 if (__any_sync(0xffffffffu, big)) {     // as above, for the heads that need it
                     if (big) shrink = kShrink;
-                    ss = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        v[i][j] *= shrink;
-                        ss = fmaf(v[i][j], v[i][j], ss);
-                    }
+                    mul8(v[i], shrink);
+                    sum = make_float2(0.f, 0.f);
+                    squares8(sum, v[i]);
+                    ss = sum.x + sum.y;
                     for (int s = lanes >> 1; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
                 }
                 const float rh = 1.f / sqrtf(__fadd_rn(ss / (float)p.head, p.eps * shrink * shrink));
-                if constexpr (!HELD) weights(i, f);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    v[i][j] = v[i][j] * rh * (HELD ? w[HELD ? i : 0][j] : f[j]) * gate<T>(g[j]);
-                    m = max(m, magnitude(v[i][j]));
+                mul8(v[i], rh);
+                if constexpr (HELD) {
+                    mul8(v[i], w[i]);
+                } else {
+                    weights(i, f);
+                    mul8(v[i], f);
                 }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[j] = gate<T>(g[j]);
+                mul8(v[i], g);
+                if constexpr (OUT8) largest8(m, v[i]);
             }
             if constexpr (VEC) fetch(row + 2 * step, slot);
             if constexpr (OUT8) {
@@ -332,12 +376,19 @@ rows_kernel(const __grid_constant__ RowParams p) {
             const bool bad = m >= kInfBits || !(largest < __uint_as_float(kInfBits));
             const float inv = bad ? 0.f : 127.f / largest;
             if (t == 0) p.scale[row] = bad ? __uint_as_float(0x7fc00000u) : largest / 127.f;
+            float to_code = r * inv;
+            if (!(to_code < __uint_as_float(kInfBits))) {       // a row near the smallest numbers
+                to_code = inv;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) mul8(v[i], r);
+            }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 int c[8];
+                mul8(v[i], to_code);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    float q = v[i][j] * r * inv;
+                    float q = v[i][j];
                     // bf16 rows meet ties exactly (an element of half the largest stands at 63.5).
                     // With significands X and A of 8 bits, 127 X / (A 2^s) is a tie or at least
                     // 2^-16 of itself away from one, so rounding it to 18 bits brings ties back
@@ -350,11 +401,7 @@ rows_kernel(const __grid_constant__ RowParams p) {
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] *= r;
-                output((T *)p.y + row * p.y_st, i, v[i]);
-            }
+            for (int i = 0; i < NV; ++i) output((T *)p.y + row * p.y_st, i, v[i]);
         }
     }
 }
@@ -381,9 +428,9 @@ static gdn_status_t launch_rows_k(const RowParams &p, int threads, cudaStream_t 
     }
     const int sms = matmul_sm_count(dev);
     if (sms <= 0) return GDN_ERR_CUDA;
-    // as many CTAs as the SMs take at once: by registers (64 a thread; 48 where a row has one
-    // input) and by shared memory
-    int per = 65536 / (threads * (MODE == kRowQuantize ? 48 : 64));
+    // as many CTAs as the SMs take at once: by registers (64 a thread; 48 where there is
+    // less in hand) and by shared memory
+    int per = 65536 / (threads * (MODE == kRowQuantize || NV == 1 ? 48 : 64));
     if (per > 220 * 1024 / (smem + 2048)) per = 220 * 1024 / (smem + 2048);
     if (per < 1) per = 1;
     const int64_t rows = WARP_ROW ? (p.T + 3) / 4 : p.T, most = VEC ? (int64_t)sms * per : rows;
@@ -403,8 +450,8 @@ static gdn_status_t launch_rows_t(const RowParams &p, cudaStream_t st) {
         return vec ? launch_rows_k<T, MODE, OUT8, 2, true, true>(p, 128, st)
                    : launch_rows_k<T, MODE, OUT8, 2, true, false>(p, 128, st);
     if (chunks <= 128)
-        return vec ? launch_rows_k<T, MODE, OUT8, 4, true, true>(p, 128, st)
-                   : launch_rows_k<T, MODE, OUT8, 4, true, false>(p, 128, st);
+        return vec ? launch_rows_k<T, MODE, OUT8, 1, false, true>(p, (chunks + 31) / 32 * 32, st)
+                   : launch_rows_k<T, MODE, OUT8, 1, false, false>(p, (chunks + 31) / 32 * 32, st);
     const int nv = chunks <= 2048 ? 2 : 4, threads = ((chunks + nv - 1) / nv + 31) / 32 * 32;
     if (nv == 2)
         return vec ? launch_rows_k<T, MODE, OUT8, 2, false, true>(p, threads, st)
