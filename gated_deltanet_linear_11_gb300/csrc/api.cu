@@ -876,6 +876,7 @@ gdn::RowParams row_params(int64_t T, int64_t D) {
     p.T = T;
     p.D = (int32_t)D;
     p.head = 16;
+    p.per_mean = (float)(1.0 / (double)D);
     p.vec = D % 8 == 0;
     return p;
 }
@@ -950,6 +951,7 @@ gdn_status_t gdn_gated_rmsnorm(const gdn_tensor_t *x, const gdn_tensor_t *z,
     p.x = X.ptr; p.x_st = X.tok;
     p.z = Z.ptr; p.z_st = Z.tok;
     p.head = (int32_t)X.D;
+    p.per_mean = 1.f / (float)X.D;
     if ((s = norm_args(weight, X.D, eps, y, scale, X.dtype, X.T, D, p)) != GDN_OK) return s;
     if (X.T == 0) return GDN_OK;
     return gdn_host::launch_rows(p, gdn::kRowGatedNorm, X.dtype == GDN_F32, y->dtype == GDN_I8,

@@ -8,7 +8,7 @@
 //   8 bits:     scale = max|y| / 127, code = y / scale to the nearest integer
 //
 // All three read a row once and write it once, so HBM bounds them.  A row stays in the
-// registers of one warp (up to 512 elements) or of one CTA, 8 consecutive elements at a time
+// registers of one warp (up to 512 elements, 1024 to be put in 8 bits) or of one CTA, 8 consecutive elements at a time
 // per thread; sums and maxima go over the row with shuffles and one pass through shared
 // memory.  The split of a row depends on its length alone, so a row's results are the same in
 // any batch.
@@ -100,20 +100,21 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sum of `v` and maximum of `m` over the row's threads.  Magnitudes are compared as bits, so
-// that a NaN is above everything.  slot: 64 words of shared memory used by no other call.
-template <bool WARP_ROW>
+// Sum of `v` (where SUM) and maximum of `m` over the row's threads.  Magnitudes are compared as
+// bits, so that a NaN is above everything.  slot: 64 words of shared memory used by no other
+// call.
+template <bool WARP_ROW, bool SUM>
 __device__ __forceinline__ void reduce_row(float &v, uint32_t &m, uint32_t *slot) {
-    v = warp_sum(v);
+    if (SUM) v = warp_sum(v);
     m = __reduce_max_sync(0xffffffffu, m);
     if constexpr (!WARP_ROW) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
         if (lane == 0) {
-            slot[warp] = __float_as_uint(v);
+            if (SUM) slot[warp] = __float_as_uint(v);
             slot[32 + warp] = m;
         }
         __syncthreads();
-        v = warp_sum(lane < warps ? __uint_as_float(slot[lane]) : 0.f);
+        if (SUM) v = warp_sum(lane < warps ? __uint_as_float(slot[lane]) : 0.f);
         m = __reduce_max_sync(0xffffffffu, lane < warps ? slot[32 + lane] : 0u);
     }
 }
@@ -161,9 +162,29 @@ __device__ __forceinline__ void largest8(uint32_t &m, const float (&f)[8]) {
 // sum (a conversion to integers runs at an eighth of the rate).
 __device__ __forceinline__ int nearest(float q) { return __float_as_int(__fadd_rn(q, 12582912.f)); }
 
-template <typename T> __device__ __forceinline__ float gate(float z);
-template <> __device__ __forceinline__ float gate<float>(float z) { return z / (1.0f + expf(-z)); }
-template <> __device__ __forceinline__ float gate<bf16>(float z) { return silu(z); }
+// v silu(z).  For bf16, 1 / (1 + e^-z) from the hardware's base-2 exponential and reciprocal
+// (about 2^-22 each, far under the half step of 2^-9); e^-z past fp32 gives a zero.
+template <typename T>
+__device__ __forceinline__ void gate8(float (&v)[8], const float (&z)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        float2 s;
+        if constexpr (sizeof(T) == 2) {
+            s = mul_f32x2(make_float2(z[j], z[j + 1]), make_float2(-1.4426950408889634f, -1.4426950408889634f));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(s.x));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(s.y));
+            s = add_f32x2(s, make_float2(1.f, 1.f));
+            asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s.x));
+            asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s.y));
+            s = mul_f32x2(s, make_float2(z[j], z[j + 1]));
+        } else {
+            s = make_float2(z[j] / (1.0f + expf(-z[j])), z[j + 1] / (1.0f + expf(-z[j + 1])));
+        }
+        s = mul_f32x2(s, make_float2(v[j], v[j + 1]));
+        v[j] = s.x;
+        v[j + 1] = s.y;
+    }
+}
 
 }  // namespace
 
@@ -182,7 +203,7 @@ __device__ __forceinline__ void copy8(uint8_t *dst, const T *src) {
 // rows into a place of its own in shared memory while it works on this one, so that the loads
 // never pause; the weights stay in registers.
 template <typename T, int MODE, bool OUT8, int NV, bool WARP_ROW, bool VEC>
-__global__ void __launch_bounds__(WARP_ROW ? 128 : 1024)
+__global__ void __launch_bounds__(WARP_ROW ? 128 : 1024, 1)
 rows_kernel(const __grid_constant__ RowParams p) {
     constexpr int INPUTS = MODE == kRowQuantize ? 1 : 2, PIECE = 8 * (int)sizeof(T);
     constexpr bool HELD = MODE != kRowQuantize && NV <= 2;  // weights in registers
@@ -283,7 +304,7 @@ rows_kernel(const __grid_constant__ RowParams p) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) largest8(m, v[i]);
             float none = 0.f;
-            reduce_row<WARP_ROW>(none, m, slots[slot][0]);
+            reduce_row<WARP_ROW, false>(none, m, slots[slot][0]);
         } else if constexpr (MODE == kRowAddNorm) {
             // For 8 bits the largest |h (offset + w)| is found together with the sum of squares: the
             // common factor r does not move the place of the maximum, so one reduction serves both.
@@ -309,7 +330,7 @@ rows_kernel(const __grid_constant__ RowParams p) {
                 ss = sum.x + sum.y;
             };
             measure();
-            reduce_row<WARP_ROW>(ss, m, slots[slot][0]);
+            reduce_row<WARP_ROW, true>(ss, m, slots[slot][0]);
             float shrink = 1.f;
             if (!(ss < __uint_as_float(kInfBits)) || m >= kInfBits) {
                 // Squares or products past fp32: once more with h / 2^80.  A row that holds an
@@ -318,9 +339,9 @@ rows_kernel(const __grid_constant__ RowParams p) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) mul8(v[i], shrink);
                 measure();
-                reduce_row<WARP_ROW>(ss, m, slots[slot][1]);
+                reduce_row<WARP_ROW, true>(ss, m, slots[slot][1]);
             }
-            r = 1.f / sqrtf(__fadd_rn(ss / (float)D, p.eps * shrink * shrink));
+            r = rsqrtf(__fadd_rn(ss * p.per_mean, p.eps * shrink * shrink));
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float f[8];
@@ -350,7 +371,7 @@ rows_kernel(const __grid_constant__ RowParams p) {
                     ss = sum.x + sum.y;
                     for (int s = lanes >> 1; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
                 }
-                const float rh = 1.f / sqrtf(__fadd_rn(ss / (float)p.head, p.eps * shrink * shrink));
+                const float rh = rsqrtf(__fadd_rn(ss * p.per_mean, p.eps * shrink * shrink));
                 mul8(v[i], rh);
                 if constexpr (HELD) {
                     mul8(v[i], w[i]);
@@ -358,15 +379,13 @@ rows_kernel(const __grid_constant__ RowParams p) {
                     weights(i, f);
                     mul8(v[i], f);
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) g[j] = gate<T>(g[j]);
-                mul8(v[i], g);
+                gate8<T>(v[i], g);
                 if constexpr (OUT8) largest8(m, v[i]);
             }
             if constexpr (VEC) fetch(row + 2 * step, slot);
             if constexpr (OUT8) {
                 float none = 0.f;
-                reduce_row<WARP_ROW>(none, m, slots[slot][0]);
+                reduce_row<WARP_ROW, false>(none, m, slots[slot][0]);
             }
         }
 
@@ -382,6 +401,13 @@ rows_kernel(const __grid_constant__ RowParams p) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) mul8(v[i], r);
             }
+            if (bad) {
+                to_code = 0.f;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+            }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 int c[8];
@@ -395,7 +421,7 @@ rows_kernel(const __grid_constant__ RowParams p) {
                     // and moves nothing else across.
                     if (MODE == kRowQuantize && sizeof(T) == 2)
                         q = __int_as_float((__float_as_int(q) + 32) & ~63);
-                    c[j] = bad ? 0 : nearest(q);
+                    c[j] = nearest(q);
                 }
                 output((int8_t *)p.y + row * p.y_st, i, c);
             }
@@ -449,6 +475,10 @@ static gdn_status_t launch_rows_t(const RowParams &p, cudaStream_t st) {
     if (chunks <= 64)
         return vec ? launch_rows_k<T, MODE, OUT8, 2, true, true>(p, 128, st)
                    : launch_rows_k<T, MODE, OUT8, 2, true, false>(p, 128, st);
+    if constexpr (MODE == kRowQuantize)
+        if (chunks <= 128)                          // little to hold: 4096 x 1000 in 4.5 us, by CTAs 6.1
+            return vec ? launch_rows_k<T, MODE, OUT8, 4, true, true>(p, 128, st)
+                       : launch_rows_k<T, MODE, OUT8, 4, true, false>(p, 128, st);
     if (chunks <= 128)
         return vec ? launch_rows_k<T, MODE, OUT8, 1, false, true>(p, (chunks + 31) / 32 * 32, st)
                    : launch_rows_k<T, MODE, OUT8, 1, false, false>(p, (chunks + 31) / 32 * 32, st);

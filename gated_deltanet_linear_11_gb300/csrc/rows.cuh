@@ -23,6 +23,7 @@ struct RowParams {
     int32_t vec;                            // every row starts on 16 bytes (8 of an 8-bit one)
                                             // and D is a multiple of 8
     float offset, eps;
+    float per_mean;                         // 1 / the elements that a mean is over
 };
 
 }  // namespace gdn

@@ -3,8 +3,8 @@
 Bounds count roundings, each at most half a step (U = 2^-24 in fp32, 2^-8 in bf16, relative to
 the value).  A norm's value takes at most: one rounding each for the residual's sum, the
 weight's offset and two products; half of the relative error of the sum of squares, which goes
-through at most 32 + 10 additions and a division; a square root and a division.  NORM = 40 U is
-above their sum (28 U).  A gate adds e^-z (a few units of U; from the base-2 hardware
+through at most 32 + 10 additions and a product with a rounded 1 / D; an inverse square root
+good to two units in the last place, 4 U.  NORM = 40 U is above their sum (31 U).  A gate adds e^-z (a few units of U; from the base-2 hardware
 exponential and the fast division in bf16, 2^-21 and the exponent's own rounding), a sum, a
 division and a product: GATED = 64 U in fp32, 2^-17 in bf16.
 """
