@@ -838,16 +838,16 @@ __global__ void __launch_bounds__(256) matmul_i8_join_kernel(const __grid_consta
 }
 
 // Tokens' codes as fp16, rows `st` elements apart (a multiple of 8; what lies between K and st
-// is not read), and the sums of their squares: a CTA per token, a thread takes eight codes.
-__global__ void __launch_bounds__(256) matmul_i8_tokens_kernel(const int8_t *a, int64_t a_st, __half *out, int64_t st,
+// is not read), and the sums of their squares: a CTA per token, a thread takes eight codes, all
+// at once for K up to 8192.
+__global__ void __launch_bounds__(1024) matmul_i8_tokens_kernel(const int8_t *a, int64_t a_st, __half *out, int64_t st,
                                                                int32_t *squares, int32_t K, int vec) {
-    __shared__ int32_t part[8];
+    __shared__ int32_t part[32];
     grid_dependents_launch();
     grid_dependency_wait();
     const int64_t m = blockIdx.x;
     int32_t sum = 0;
-#pragma unroll 4
-    for (int k = threadIdx.x * 8; k < K; k += 2048) {
+    for (int k = threadIdx.x * 8; k < K; k += blockDim.x * 8) {
         const int8_t *src = a + m * a_st + k;
         uint2 w = make_uint2(0, 0);
         if (vec && k + 8 <= K) {
@@ -866,9 +866,9 @@ __global__ void __launch_bounds__(256) matmul_i8_tokens_kernel(const int8_t *a, 
     sum = __reduce_add_sync(0xffffffffu, sum);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < 8; ++i) sum += part[i];
-        squares[m] = sum;
+    if (threadIdx.x < 32) {
+        sum = __reduce_add_sync(0xffffffffu, threadIdx.x < blockDim.x >> 5 ? part[threadIdx.x] : 0);
+        if (threadIdx.x == 0) squares[m] = sum;
     }
 }
 
@@ -994,8 +994,9 @@ gdn_status_t launch_matmul_i8_pair(const MatmulParams &p, void *ws, cudaStream_t
     if (!row_map(&maps.w, p.w, false, p.N, p.K, p.w_st, kI8Channels, true) ||
         !row_map(&maps.a, ws, true, p.M, p.K, half_st, NT / 2, true))
         return GDN_ERR_CUDA;
+    const int64_t eights = (half_st / 8 + 31) / 32 * 32, threads = eights < 1024 ? eights : 1024;
     const bool vec = ((uintptr_t)p.a & 7u) == 0 && (p.M == 1 || p.a_st % 8 == 0);
-    if (launch_dependent(matmul_i8_tokens_kernel, dim3((unsigned)p.M), dim3(256), 0, st, p.a, p.a_st, (__half *)ws,
+    if (launch_dependent(matmul_i8_tokens_kernel, dim3((unsigned)p.M), dim3((unsigned)threads), 0, st, p.a, p.a_st, (__half *)ws,
                          half_st, squares, p.K, (int)vec) != cudaSuccess)
         return GDN_ERR_CUDA;
     const unsigned grid = (unsigned)(2 * (sh.units < pairs ? sh.units : pairs));
