@@ -885,8 +885,10 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 int pair_tokens(int64_t M) { return M <= 128 ? 128 : 256; }
 
 // Tiles, those made whole, and the units of each other one.  The parts along K are as many as
-// make the last turns shortest; a part costs its fill and the join about kPairJoin steps.
-constexpr int kPairMaxParts = 12, kPairJoin = 10;
+// make the last turns shortest; a turn's fill and its sums' way out cost about six steps and
+// the join five (128 tokens of 5120 channels of 6144: whole 29 us, three parts 21; 500 tokens of
+// the same: whole 40, three parts in two turns 48).
+constexpr int kPairMaxParts = 12, kPairUnitCost = 6, kPairJoinCost = 5;
 struct PairPlan {
     int64_t tiles, full;
     int parts;
@@ -902,7 +904,8 @@ PairPlan pair_plan(int64_t M, int64_t N, int64_t K, int pairs) {
     const int64_t left = plan.tiles % pairs;
     int64_t best = steps;
     for (int parts = 2; parts <= kPairMaxParts && parts * 2 <= steps; ++parts) {
-        const int64_t turns = (left * parts + pairs - 1) / pairs, cost = turns * ((steps + parts - 1) / parts + 1) + kPairJoin;
+        const int64_t turns = (left * parts + pairs - 1) / pairs, 
+                      cost = turns * ((steps + parts - 1) / parts + kPairUnitCost) + kPairJoinCost;
         if (cost < best) {
             best = cost;
             plan.parts = parts;
