@@ -467,8 +467,9 @@ static gdn_status_t launch_rows_k(const RowParams &p, int threads, cudaStream_t 
 template <typename T, int MODE, bool OUT8>
 static gdn_status_t launch_rows_t(const RowParams &p, cudaStream_t st) {
     const int chunks = (p.D + 7) / 8;               // 8-element pieces of a row
-    // two rows of both inputs have to fit: fp32 rows up to 16384 and all of bf16
-    const bool vec = p.vec && 4 * (size_t)p.D * sizeof(T) + 8192 <= (size_t)kRowSmem;
+    // two rows of every input have to fit, padded to whole warps (norms: 27136 elements of bf16)
+    const size_t inputs = MODE == kRowQuantize ? 1 : 2;
+    const bool vec = p.vec && 2 * inputs * ((size_t)p.D + 1024) * sizeof(T) <= (size_t)kRowSmem;
     if (chunks <= 32)
         return vec ? launch_rows_k<T, MODE, OUT8, 1, true, true>(p, 128, st)
                    : launch_rows_k<T, MODE, OUT8, 1, true, false>(p, 128, st);

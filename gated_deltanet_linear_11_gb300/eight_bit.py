@@ -154,6 +154,7 @@ def gdn_gated_rmsnorm(x, z, weight, eps=1e-6, eight_bit=False, y=None, scale=Non
     return (y, scale) if eight_bit else y
 
 
+@_on_device
 def gdn_matmul_i8_workspace_size(a, w, simt=False):
     """Workspace bytes of gdn_matmul_i8 (by the sizes and the alignment of a and w)."""
     return int(_lib.load().gdn_matmul_i8_workspace_size(

@@ -97,6 +97,9 @@ def test_matmul_i8_refusals(lib):
     assert call(bias=mat(1, 8, I8)) == 4
     assert call(a=mat(4, 131072, I8), w=mat(8, 131072, I8)) == 6
     assert call(a=mat(0, 64, I8, ptr=None), sa=None, out=mat(0, 8, ptr=None)) == 0
+    # rows off 16 bytes, and many tokens, need scratch
+    assert call(a=mat(4, 65, I8), w=mat(8, 65, I8), flags=0) == 9
+    assert call(a=mat(300, 64, I8), w=mat(8, 64, I8), out=mat(300, 8), flags=0) == 9
 
 
 def test_matmul_i8_workspace(lib):

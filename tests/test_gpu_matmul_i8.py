@@ -115,6 +115,46 @@ def test_nothing_to_do_and_scales_that_are_not_finite():
     assert keep.isfinite().all()
 
 
+def test_leading_dimension_and_given_scratch():
+    """[1, T, K] operands, a workspace of the stated size, and one that is too small."""
+    a, w = codes(1, 400, 2048), codes(2, 2304, 2048)
+    sa, sw = scales(1, 400), scales(2, 2304)
+    want = gdn.gdn_matmul_i8(a, sa, w, sw)
+    size = gdn.gdn_matmul_i8_workspace_size(a, w)
+    assert size > 0
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")     # fp16 NaN, counts of -1
+    got = gdn.gdn_matmul_i8(a[None], sa, w[None], sw, workspace=ws)
+    assert got.shape == (1, 400, 2304)
+    assert_bits_equal(got[0], want, "out")
+    # shifted by a byte: rows off 16 bytes, so copies of both
+    b = torch.empty(400 * 2048 + 1, dtype=torch.int8, device="cuda")[1:].view(400, 2048)
+    v = torch.empty(2304 * 2048 + 1, dtype=torch.int8, device="cuda")[1:].view(2304, 2048)
+    b.copy_(a)
+    v.copy_(w)
+    assert gdn.gdn_matmul_i8_workspace_size(b, v) > size
+    assert_bits_equal(gdn.gdn_matmul_i8(b, sa, v, sw), want, "out")
+    assert gdn.gdn_matmul_i8_workspace_size(a, w, simt=True) == 0
+
+
+@pytest.mark.parametrize("shapes", [[(1, 5120, 5120), (200, 1000, 2048), (40, 4000, 3000)],
+                                    [(700, 2048, 2048), (600, 2048, 2048), (64, 9000, 1024)]])
+def test_products_on_streams_at_once(shapes):
+    """Kernels of every form side by side on three streams, many times over."""
+    cases = []
+    for i, (M, N, K) in enumerate(shapes):
+        a, w, sa, sw = codes(i, M, K, -90, 90), codes(9 + i, N, K, -90, 90), scales(i, M), scales(i, N)
+        cases.append((a, sa, w, sw, ref.product(a, sa, w, sw, None, BF), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        for a, sa, w, sw, want, stream in cases:
+            with torch.cuda.stream(stream):
+                outs.append((gdn.gdn_matmul_i8(a, sa, w, sw), want))
+    torch.cuda.synchronize()
+    for got, want in outs:
+        assert_bits_equal(got.cpu(), want, "out")
+
+
 def test_outputs_past_2_31():
     M, N, K = 70000, 32768, 16
     a, w = codes(1, M, K), codes(2, N, K)

@@ -180,6 +180,25 @@ def test_bits_do_not_depend_on_batch_or_layout(D, dtype):
     assert_bits_equal(y2, y, "y")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [512, 1000, 1001, 6144])
+def test_many_rows_in_place(D, dtype):
+    """More rows than run at once, each written where rows still to come are read ahead."""
+    T = 3000
+    x, r, w = rnd(1, T, D, dtype=dtype), rnd(2, T, D, dtype=dtype), rnd(3, D, dtype=dtype)
+    y, h = gdn.gdn_add_rmsnorm(x, w, r)
+    x2, r2 = x.clone(), r.clone()
+    gdn.gdn_add_rmsnorm(x2, w, r2, y=x2, residual_out=r2)
+    assert_bits_equal(x2, y, "y")
+    assert_bits_equal(r2, h, "residual")
+    assert_bits_equal(gdn.gdn_add_rmsnorm(x[2990:], w, r[2990:])[0], y[2990:], "last rows")
+    if D % 128 == 0:
+        z = rnd(4, T, D, dtype=dtype)
+        g = gdn.gdn_gated_rmsnorm(x.view(T, -1, 128), z.view(T, -1, 128), w[:128].contiguous())
+        gdn.gdn_gated_rmsnorm(x.view(T, -1, 128), z.view(T, -1, 128), w[:128].contiguous(), y=x)
+        assert_bits_equal(x, g, "gated")
+
+
 def test_no_rows_and_many():
     e = torch.empty(0, 64, dtype=BF, device="cuda")
     q, s = gdn.gdn_quantize_rows(e)
