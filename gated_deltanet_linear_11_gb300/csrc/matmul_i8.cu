@@ -124,17 +124,24 @@ matmul_i8_stream_kernel(const __grid_constant__ I8Maps maps, const __grid_consta
     if (tid == 0 && *abort) report(p.status, GDN_ERR_TIMEOUT);
 }
 
-// Rows of codes that do not start on 16 bytes, copied to rows that do (st bytes apart, zeros
-// from K on).  A thread makes 16 bytes of aligned words that hold any of them.
-__global__ void __launch_bounds__(256) matmul_i8_align_kernel(const int8_t *src, int64_t src_st, int8_t *dst, int64_t st,
-                                                              int64_t rows, int32_t K) {
+// Rows of codes that do not start on 16 bytes, of one operand or both, copied to rows that do
+// (st bytes apart, zeros from K on).  A thread makes 16 bytes of the aligned words that hold any
+// of them.
+struct AlignRows {
+    const int8_t *src;
+    int8_t *dst;
+    int64_t src_st, rows;                        // rows 0: nothing to copy
+};
+__global__ void __launch_bounds__(256) matmul_i8_align_kernel(const __grid_constant__ AlignRows a,
+                                                              const __grid_constant__ AlignRows b, int64_t st, int32_t K) {
     grid_dependents_launch();
     grid_dependency_wait();
-    const int64_t per = st / 16, total = rows * per;
+    const int64_t per = st / 16, first = a.rows * per, total = first + b.rows * per;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / per;
-        const int k = (int)(i - row * per) * 16, n = min(K - k, 16);
-        const uintptr_t at = (uintptr_t)(src + row * src_st + k);
+        const AlignRows &m = i < first ? a : b;
+        const int64_t piece = i < first ? i : i - first, row = piece / per;
+        const int k = (int)(piece - row * per) * 16, n = min(K - k, 16);
+        const uintptr_t at = (uintptr_t)(m.src + row * m.src_st + k);
         const uint32_t *word = (const uint32_t *)(at & ~(uintptr_t)3);
         const int off = (int)(at & 3u), words = (off + n + 3) / 4;
         uint32_t w[5], out[4];
@@ -146,7 +153,7 @@ __global__ void __launch_bounds__(256) matmul_i8_align_kernel(const int8_t *src,
             const int left = n - 4 * j;          // bytes of this word that are in the row
             if (left < 4) out[j] = left > 0 ? out[j] & ((1u << (8 * left)) - 1u) : 0u;
         }
-        *reinterpret_cast<uint4 *>(dst + row * st + k) = make_uint4(out[0], out[1], out[2], out[3]);
+        *reinterpret_cast<uint4 *>(m.dst + row * st + k) = make_uint4(out[0], out[1], out[2], out[3]);
     }
 }
 
@@ -248,13 +255,17 @@ void align_sizes(const MatmulParams &p, size_t &a, size_t &w) {
     w = on_16_bytes(p.w, p.N, p.w_st) ? 0 : up256((size_t)p.N * st);
 }
 
-gdn_status_t launch_align(const int8_t *&ptr, int64_t &row_st, int64_t rows, int32_t K, void *to, cudaStream_t st) {
-    const int64_t dst_st = ((int64_t)K + 15) / 16 * 16, blocks = (rows * (dst_st / 16) + 255) / 256;
-    if (launch_dependent(matmul_i8_align_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, ptr,
-                         row_st, (int8_t *)to, dst_st, rows, K) != cudaSuccess)
+// Copies the operands that need it to `to` and points p at the copies.
+gdn_status_t launch_align(MatmulParams &p, size_t a_bytes, size_t w_bytes, uint8_t *to, cudaStream_t st) {
+    const int64_t row = ((int64_t)p.K + 15) / 16 * 16;
+    const AlignRows a = {p.a, (int8_t *)to, p.a_st, a_bytes ? p.M : 0};
+    const AlignRows w = {p.w, (int8_t *)to + a_bytes, p.w_st, w_bytes ? p.N : 0};
+    const int64_t blocks = ((a.rows + w.rows) * (row / 16) + 255) / 256;
+    if (launch_dependent(matmul_i8_align_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, a, w,
+                         row, p.K) != cudaSuccess)
         return GDN_ERR_CUDA;
-    ptr = (const int8_t *)to;
-    row_st = dst_st;
+    if (a_bytes) { p.a = a.dst; p.a_st = row; }
+    if (w_bytes) { p.w = w.dst; p.w_st = row; }
     return GDN_OK;
 }
 
@@ -302,11 +313,11 @@ gdn_status_t launch_matmul_i8(const MatmulParams &given, uint32_t flags, void *w
     uint8_t *at = (uint8_t *)ws;
     size_t a, w;
     align_sizes(p, a, w);
-    gdn_status_t s;
-    if (a > 0 && (s = launch_align(p.a, p.a_st, p.M, p.K, at, st)) != GDN_OK) return s;
-    at += a;
-    if (w > 0 && (s = launch_align(p.w, p.w_st, p.N, p.K, at, st)) != GDN_OK) return s;
-    at += w;
+    if (a + w > 0) {
+        const gdn_status_t s = launch_align(p, a, w, at, st);
+        if (s != GDN_OK) return s;
+        at += a + w;
+    }
     if (p.M == 1) return launch_stream<1>(p, st);
     if (p.M == 2) return launch_stream<2>(p, st);
     if (p.M <= 4) return launch_stream<4>(p, st);
