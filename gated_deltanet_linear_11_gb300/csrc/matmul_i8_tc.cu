@@ -27,11 +27,12 @@ constexpr int kI8Threads = 32 * (kI8ConvWarps + 2);
 
 template <int NT> struct I8Shape {
     static constexpr int RAW_W = kI8Channels * kI8Step, RAW_A = NT * kI8Step;
-    static constexpr int STAGES = NT <= 32 ? 4 : NT == 64 ? 3 : 4;
+    static constexpr int STAGES = NT <= 32 ? 4 : 3;
     static constexpr int CONV = NT * kI8Step * 2;
-    static constexpr int CTAS = NT <= 64 ? 2 : 1;        // that fit on an SM
+    static constexpr int CTAS = 2;                       // that fit on an SM
     // TMEM columns: two accumulators of NT, two steps of 64 columns of operand A
-    static constexpr int COL_A = 2 * NT, COLS = NT <= 64 ? 256 : 512;
+    static constexpr int COL_A = 2 * NT, COLS = 256;
+    static_assert(COL_A + 128 <= COLS, "the columns fit");
 };
 template <int NT> struct I8Smem {
     uint8_t raw_w[I8Shape<NT>::STAGES][I8Shape<NT>::RAW_W];
