@@ -19,6 +19,8 @@ namespace gdn {
 // all lanes (one read of shared memory for the warp) and nothing is added across lanes; dp4a
 // makes four products an instruction, 64 lanes a clock: 512 clocks for 16 KB of w and 8 tokens,
 // where HBM takes 700.  The eight warps of a CTA add up their int32 sums in shared memory.
+// Measured: one token of 16480 channels of 5120 15.2 us (5.6 TB/s, 82% of a copy's rate), four
+// 16.2; of 5120 channels of 6144 9.1 us, 31 MB whose first and last bytes take half of the time.
 constexpr int kStreamWarps = 8, kStreamRows = 32, kStreamStep = 128;
 
 template <int MT> struct StreamSmem {

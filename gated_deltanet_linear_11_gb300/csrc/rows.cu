@@ -7,11 +7,17 @@
 //   gated norm: y = x w / sqrt(mean_head x^2 + eps) * z / (1 + e^-z)
 //   8 bits:     scale = max|y| / 127, code = y / scale to the nearest integer
 //
-// All three read a row once and write it once, so HBM bounds them.  A row stays in the
-// registers of one warp (up to 512 elements, 1024 to be put in 8 bits) or of one CTA, 8 consecutive elements at a time
-// per thread; sums and maxima go over the row with shuffles and one pass through shared
-// memory.  The split of a row depends on its length alone, so a row's results are the same in
-// any batch.
+// All of them read a row once and write it once, so HBM bounds them.  A row stays in the
+// registers of one warp (up to 512 elements, 1024 to be put in 8 bits) or of one CTA, 8
+// consecutive elements at a time per thread; sums and maxima go over the row with shuffles and
+// one pass through shared memory.  The split of a row depends on its length alone, so a row's
+// results are the same in any batch.
+//
+// Measured, 4096 bf16 rows: norm with residual of 5120 29.3 us (5.7 TB/s, 84% of a copy's rate),
+// to 8 bits 25.3 (86%); gated norm of 48 x 128 26.3 (85%), to 8 bits 30.9 (60%: the row's maximum
+// is one more barrier between its loads and its stores, and issue slots are 73% busy); 10240 rows
+// of 5120 to 8 bits 31.2 (74%), from fp32 43.6 (89%).  64 rows and fewer take 1.6 to 3 us, a
+// launch and the row's way through the SM.
 #include <atomic>
 
 #include "bulk_ptx.cuh"
