@@ -39,6 +39,7 @@ template <int NT> struct I8Smem {
     uint8_t conv[2][I8Shape<NT>::CONV];      // [step][64-code block][token][128 bytes]
     uint64_t raw_full[I8Shape<NT>::STAGES], raw_free[I8Shape<NT>::STAGES];
     uint64_t ab_full[2], ab_free[2], d_full[2], d_free[2];
+    uint64_t sums_full;
     float scale[NT];                         // of the tokens
     uint32_t tmem;
     int abort;
@@ -94,12 +95,22 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ int32_t cluster_load(uint32_t addr, uint32_t rank) {
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
     uint32_t remote;
-    int32_t v;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote));
-    return v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(tc::smem_u32(p)), "r"(rank));
+    return remote;
+}
+// The halves of a cluster's barrier that order no memory.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes to a CTA of the cluster, counted by its barrier when they are there.
+__device__ __forceinline__ void cluster_put(uint32_t to, uint32_t bar, int4 v) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.s32 [%0], {%1, %2, %3, %4}, [%5];"
+                 :: "r"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar) : "memory");
 }
 
 // Sums of a thread's outputs over the chunks: fp32 while they stay within kI8Near, so that the
@@ -128,7 +139,7 @@ template <int N> struct ExactSums {
             big = fmaxf(big, fmaxf(fabsf(t.x), fabsf(t.y)));
         }
     }
-    // before the same elements are added to again
+    // after every chunk
     __device__ __forceinline__ void settle() {
         if (__any_sync(0xffffffffu, big > kI8Near)) {
 #pragma unroll
@@ -140,8 +151,9 @@ template <int N> struct ExactSums {
         }
         big = 0.f;
     }
+    // |s| <= 2^21 here: added to 1.5 * 2^23 it is the low bits of the sum
     __device__ __forceinline__ int32_t whole(int i) const {
-        return (moved ? far[i] : 0) + __float2int_rn(s[i]);
+        return (moved ? far[i] : 0) + __float_as_int(__fadd_rn(s[i], 12582912.f)) - 0x4b400000;
     }
     // makes s the sums, rounded once, or where they have moved leaves all of them in `far`
     __device__ __forceinline__ void finish(bool stay = false) {
@@ -157,8 +169,9 @@ template <int N> struct ExactSums {
 // ------------------------------------------------------------------ up to 64 tokens
 //
 // A CTA makes 128 channels x NT tokens over a range of K; the CTAs of a cluster share a tile
-// by ranges of K and add up their int32 sums through distributed shared memory.  Tokens are
-// converted into fp16 tiles in shared memory.
+// by ranges of K.  Each sends its int32 sums to the CTA that adds them up, one of its share of
+// the channels (reading the others' memory between two barriers took 5 us of 27 at 64 tokens).
+// Tokens are converted into fp16 tiles in shared memory.
 // Measured, 16480 channels of 5120: 16 tokens 19.4 us, 64 tokens 27 us, where HBM takes 12.5:
 // each step's chain (copy, codes out of shared memory, conversion, TMEM, products) is waited for
 // with two CTAs an SM; issue slots are 54% busy, the tensor pipe 14%.  More converting warps
@@ -199,7 +212,9 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
             tc::mbar_init(&S.d_full[i], 1);
             tc::mbar_init(&S.d_free[i], kI8ConvWarps);
         }
+        tc::mbar_init(&S.sums_full, 1);
         tc::mbar_fence_init();
+        if (parts > 1) tc::mbar_expect_tx(&S.sums_full, NT * kI8Channels * 4);
         tc::prefetch_tmap(&maps.w);
         tc::prefetch_tmap(&maps.a);
     }
@@ -213,8 +228,9 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
     __syncwarp();
     grid_dependency_wait();
 
-    // scales for the end: this thread's channel, and the tokens'
-    const int64_t own = n0 + (tid & (kI8Channels - 1));
+    // scales for the end: those of the channel that this thread then stores, and the tokens'
+    const int share = kI8Channels / parts, share_log = __ffs(share) - 1;
+    const int64_t own = n0 + rank * share + (tid & (share - 1));
     const float ws = own < p.N ? p.w_scale[own] : 0.f, bias = own < p.N ? matmul_bias(p, own) : 0.f;
     for (int i = tid; i < NT; i += kI8Threads) S.scale[i] = p.a_scale[min((int64_t)m0 + i, p.M - 1)];
     ExactSums<HALF> sums;                        // this thread's channel, half of the tokens
@@ -282,6 +298,8 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
             // a chunk is fetched while the next one's first steps run
             if (s % kI8Exact == 1 && s > kI8Exact) drain(drained++);
         }
+        __syncwarp();
+        cluster_arrive_relaxed();                // of this warp's copied codes all are used
         while (ok && drained < chunks) drain(drained++);
     } else if (warp == kI8ConvWarps) {
         int issued = 0;
@@ -299,6 +317,8 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
         // nothing may land after the CTA has left
         for (int s = max(0, issued - Sh::STAGES); s < issued; ++s)
             wait_bounded_poll<0>(&S.raw_full[s % Sh::STAGES], (s / Sh::STAGES) & 1, nullptr);
+        __syncwarp();
+        cluster_arrive_relaxed();
     } else {
         const uint32_t id = i8_idesc(kI8Channels, NT);
         for (int s = 0; s < n; ++s) {
@@ -314,8 +334,11 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
             tc::mma_commit_warp(&S.ab_free[buf]);
             if (s % kI8Exact == kI8Exact - 1 || s == n - 1) tc::mma_commit_warp(&S.d_full[c & 1]);
         }
+        __syncwarp();
+        cluster_arrive_relaxed();
     }
     __syncwarp();
+    cluster_wait();                              // no CTA's ring is in use
 
     static_assert(kI8ConvWarps == 8, "thread i of the converting warps has channel i mod 128 both ways");
     __syncthreads();                             // the scales are there
@@ -330,27 +353,45 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
                                  matmul_value(sums.s[i], S.scale[half * HALF + i], ws, bias));
         }
     } else {
-        // [token][channel] sums over the codes that have all been used
-        int32_t *part = reinterpret_cast<int32_t *>(S.raw_w);
-        static_assert(NT * kI8Channels * 4 <= sizeof(S.raw_w) + sizeof(S.raw_a), "the sums fit");
-        if (warp < kI8ConvWarps)
+        // Over the codes that have all been used: sums as [CTA][four tokens][channel of the share].
+        // They are sent whatever went wrong before, so that none is on its way to a CTA that left.
+        int4 *in = reinterpret_cast<int4 *>(S.raw_w);
+        static_assert(NT * kI8Channels * 4 <= sizeof(S.raw_w), "the sums fit");
+        if (warp < kI8ConvWarps) {
+            const uint32_t to = row >> share_log, bar = cluster_addr(&S.sums_full, to);
+            const uint32_t at = cluster_addr(in + ((rank * (NT / 4) + half * (HALF / 4)) << share_log) +
+                                             (row & (share - 1)), to);
 #pragma unroll
-            for (int i = 0; i < HALF; ++i) part[(half * HALF + i) * kI8Channels + row] = sums.whole(i);
-        cluster_sync();
-        // the tokens go round the CTAs, two at a time
-        const uint32_t base = tc::smem_u32(part + row);
-        if (warp < kI8ConvWarps && own < p.N) {
-#pragma unroll 4
-            for (int t = 2 * rank + half; t < rows; t += 2 * parts) {
-                int32_t sum = 0;
-#pragma unroll
-                for (uint32_t r = 0; r < 8; ++r)
-                    if (r < parts) sum += cluster_load(base + 4 * kI8Channels * t, r);
-                matmul_store(p, (int64_t)m0 + t, own, matmul_value((float)sum, S.scale[t], ws, bias));
-            }
+            for (int i = 0; i < HALF; i += 4)
+                cluster_put(at + (i * 4 << share_log), bar,
+                            make_int4(sums.whole(i), sums.whole(i + 1), sums.whole(i + 2), sums.whole(i + 3)));
         }
         __syncwarp();
-        cluster_sync();                          // before any CTA's memory goes
+        cluster_arrive_relaxed();
+        if (warp < kI8ConvWarps) {
+            if (!wait_bounded_poll<0>(&S.sums_full, 0, nullptr)) *abort = 1;
+            if (own < p.N)
+                for (int g = tid >> share_log; 4 * g < rows; g += 32 * kI8ConvWarps >> share_log) {
+                    int4 sum = make_int4(0, 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        if (r < parts) {
+                            const int4 v = in[((r * (NT / 4) + g) << share_log) + (tid & (share - 1))];
+                            sum.x += v.x;
+                            sum.y += v.y;
+                            sum.z += v.z;
+                            sum.w += v.w;
+                        }
+                    const int32_t whole[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (4 * g + i < rows)
+                            matmul_store(p, (int64_t)m0 + 4 * g + i, own,
+                                         matmul_value((float)whole[i], S.scale[4 * g + i], ws, bias));
+                }
+        }
+        __syncwarp();
+        cluster_wait();                          // every CTA has sent
     }
     tc::fence_before_sync();
     __syncthreads();
