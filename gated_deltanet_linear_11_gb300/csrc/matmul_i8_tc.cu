@@ -40,7 +40,7 @@ template <int NT> struct I8Smem {
     uint64_t raw_full[I8Shape<NT>::STAGES], raw_free[I8Shape<NT>::STAGES];
     uint64_t ab_full[2], ab_free[2], d_full[2], d_free[2];
     uint64_t sums_full;
-    float scale[NT];                         // of the tokens
+    alignas(16) float scale[NT];             // of the tokens
     uint32_t tmem;
     int abort;
 };
@@ -108,9 +108,34 @@ __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // 16 bytes to a CTA of the cluster, counted by its barrier when they are there.
-__device__ __forceinline__ void cluster_put(uint32_t to, uint32_t bar, int4 v) {
-    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.s32 [%0], {%1, %2, %3, %4}, [%5];"
+__device__ __forceinline__ void cluster_put(uint32_t to, uint32_t bar, uint4 v) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
                  :: "r"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar) : "memory");
+}
+
+// A lane's four tokens of one channel, the first n of them, to rows st apart; neighbouring lanes
+// have neighbouring channels.  vec (bf16, all lanes, rows on 16 bytes): four lanes trade, and each
+// stores four channels of one token (stores of two bytes took 1 us of a kernel's 24).
+template <typename T>
+__device__ __forceinline__ void i8_put4(T *to, int64_t st, int n, const float (&v)[4], bool vec) {
+    if constexpr (sizeof(T) == 2) {
+        if (vec) {
+            const bool odd = threadIdx.x & 1, up = threadIdx.x & 2;
+            const uint32_t lo = pack_bf2(v[0], v[1]), hi = pack_bf2(v[2], v[3]);
+            uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+            const uint32_t left = odd ? got : lo, right = odd ? hi : got;       // two tokens' channels
+            const uint32_t first = __byte_perm(left, right, 0x5410), second = __byte_perm(left, right, 0x7632);
+            got = __shfl_xor_sync(0xffffffffu, up ? first : second, 2);
+            const int i = 2 * odd + up;
+            if (i < n)
+                *reinterpret_cast<uint2 *>(to + i * st - (threadIdx.x & 3)) =
+                    up ? make_uint2(got, second) : make_uint2(first, got);
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < n) to[i * st] = from_f32<T>(v[i]);
 }
 
 // Sums of a thread's outputs over the chunks: fp32 while they stay within kI8Near, so that the
@@ -151,9 +176,12 @@ template <int N> struct ExactSums {
         }
         big = 0.f;
     }
-    // |s| <= 2^21 here: added to 1.5 * 2^23 it is the low bits of the sum
+    // s + kRaised (mod 2^32): |s| <= 2^21 after a chunk, so added to 1.5 * 2^23 it is the low bits
+    // of the sum
+    static constexpr uint32_t kRaised = 0x4b400000;
+    __device__ __forceinline__ uint32_t raised(int i) const { return __float_as_uint(__fadd_rn(s[i], 12582912.f)); }
     __device__ __forceinline__ int32_t whole(int i) const {
-        return (moved ? far[i] : 0) + __float_as_int(__fadd_rn(s[i], 12582912.f)) - 0x4b400000;
+        return (int32_t)((moved ? (uint32_t)far[i] : 0u) + raised(i) - kRaised);
     }
     // makes s the sums, rounded once, or where they have moved leaves all of them in `far`
     __device__ __forceinline__ void finish(bool stay = false) {
@@ -343,52 +371,67 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
     static_assert(kI8ConvWarps == 8, "thread i of the converting warps has channel i mod 128 both ways");
     __syncthreads();                             // the scales are there
     const int rows = (int)min((int64_t)NT, p.M - m0);
+    const bool vec = p.out_vec && n0 + kI8Channels <= p.N;
+    auto put4 = [&](int t, const float (&v)[4]) {
+        const int n = own < p.N ? rows - t : 0;
+        const int64_t at = ((int64_t)m0 + t) * p.out_st + own;
+        if (p.out_f32) i8_put4((float *)p.out + at, p.out_st, n, v, vec);
+        else i8_put4((bf16 *)p.out + at, p.out_st, n, v, vec);
+    };
     if (parts == 1) {
         sums.finish();
-        if (warp < kI8ConvWarps && own < p.N) {
+        if (warp < kI8ConvWarps)
 #pragma unroll
-            for (int i = 0; i < HALF; ++i)
-                if (half * HALF + i < rows)
-                    matmul_store(p, (int64_t)m0 + half * HALF + i, own,
-                                 matmul_value(sums.s[i], S.scale[half * HALF + i], ws, bias));
-        }
+            for (int i = 0; i < HALF; i += 4) {
+                float v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = matmul_value(sums.s[i + j], S.scale[half * HALF + i + j], ws, bias);
+                put4(half * HALF + i, v);
+            }
     } else {
-        // Over the codes that have all been used: sums as [CTA][four tokens][channel of the share].
+        // Over the codes that have all been used: sums, raised, as [CTA][four tokens][channel of the
+        // share].
         // They are sent whatever went wrong before, so that none is on its way to a CTA that left.
-        int4 *in = reinterpret_cast<int4 *>(S.raw_w);
+        uint4 *in = reinterpret_cast<uint4 *>(S.raw_w);
         static_assert(NT * kI8Channels * 4 <= sizeof(S.raw_w), "the sums fit");
         if (warp < kI8ConvWarps) {
             const uint32_t to = row >> share_log, bar = cluster_addr(&S.sums_full, to);
             const uint32_t at = cluster_addr(in + ((rank * (NT / 4) + half * (HALF / 4)) << share_log) +
                                              (row & (share - 1)), to);
+            if (sums.moved)
 #pragma unroll
-            for (int i = 0; i < HALF; i += 4)
-                cluster_put(at + (i * 4 << share_log), bar,
-                            make_int4(sums.whole(i), sums.whole(i + 1), sums.whole(i + 2), sums.whole(i + 3)));
+                for (int i = 0; i < HALF; ++i) sums.far[i] = (int32_t)((uint32_t)sums.far[i] + sums.raised(i));
+#pragma unroll
+            for (int i = 0; i < HALF; i += 4) {
+                uint4 v = make_uint4(sums.raised(i), sums.raised(i + 1), sums.raised(i + 2), sums.raised(i + 3));
+                if (sums.moved) v = make_uint4(sums.far[i], sums.far[i + 1], sums.far[i + 2], sums.far[i + 3]);
+                cluster_put(at + (i * 4 << share_log), bar, v);
+            }
         }
         __syncwarp();
         cluster_arrive_relaxed();
         if (warp < kI8ConvWarps) {
             if (!wait_bounded_poll<0>(&S.sums_full, 0, nullptr)) *abort = 1;
-            if (own < p.N)
-                for (int g = tid >> share_log; 4 * g < rows; g += 32 * kI8ConvWarps >> share_log) {
-                    int4 sum = make_int4(0, 0, 0, 0);
-#pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        if (r < parts) {
-                            const int4 v = in[((r * (NT / 4) + g) << share_log) + (tid & (share - 1))];
-                            sum.x += v.x;
-                            sum.y += v.y;
-                            sum.z += v.z;
-                            sum.w += v.w;
-                        }
-                    const int32_t whole[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (4 * g + i < rows)
-                            matmul_store(p, (int64_t)m0 + 4 * g + i, own,
-                                         matmul_value((float)whole[i], S.scale[4 * g + i], ws, bias));
+            // (a warp's threads all or none: their number is a multiple of 32)
+#pragma unroll 1
+            for (int g = tid >> share_log; g < NT / 4; g += 32 * kI8ConvWarps >> share_log) {
+                const uint4 *at = in + (g << share_log) + (tid & (share - 1));
+                uint32_t sum[4] = {};
+#pragma unroll 2
+                for (int r = 0; r < parts; ++r, at += NT / 4 << share_log) {
+                    const uint4 u = *at;
+                    sum[0] += u.x - sums.kRaised;
+                    sum[1] += u.y - sums.kRaised;
+                    sum[2] += u.z - sums.kRaised;
+                    sum[3] += u.w - sums.kRaised;
                 }
+                float v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = matmul_value((float)(int32_t)sum[j], S.scale[4 * g + j], ws, bias);
+                put4(4 * g, v);
+            }
         }
         __syncwarp();
         cluster_wait();                          // every CTA has sent
