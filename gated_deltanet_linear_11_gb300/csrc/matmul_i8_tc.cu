@@ -568,8 +568,10 @@ template <int N> __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
 }
 // Registers a thread at launch, and then of the sums' warps, the converting ones and the rest;
-// a raise waits until the other warps' cuts cover it.
-constexpr int kPairRegs = 128, kPairSumRegs = 176, kPairConvRegs = 96, kPairRestRegs = 64;
+// a raise waits until the other warps' cuts cover it.  The ring leaves hardly any L1, so a value
+// that goes to local memory comes back from L2: with 176, 96 and 64, 42 of the sums' warps' did,
+// and 256 tokens of 16480 channels of 5120 took 38 us (34).
+constexpr int kPairRegs = 128, kPairSumRegs = 200, kPairConvRegs = 72, kPairRestRegs = 40;
 static_assert(2 * kPairSumRegs + kPairConvRegs + kPairRestRegs <= 4 * kPairRegs, "a raise waits forever");
 
 // Puts group i of a warp's sums into o.sum: a choice of one in eight by halves.
