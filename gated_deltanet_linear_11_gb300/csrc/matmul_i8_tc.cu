@@ -501,12 +501,12 @@ struct PairBars {
 };
 constexpr uint32_t kPairRaw = kI8Channels * kI8Step;
 constexpr uint32_t kPairRing = 192 * 1024;
-// Of a sums' warp, on the way out: 32 channels' sums of 16 tokens (20 words a channel, 8 more
-// after every eighth, so that neither a lane's row nor eight channels of eight tokens meet in a
-// bank), and the scales and bias.
+// Of a sums' warp, on the way out: 16 tokens of 32 channels as bf16 pairs of tokens (12 words a
+// channel, 8 more after every eighth, so that neither the channels' rows nor a pair of eight
+// channels meet in a bank), and the tokens' scales.
 struct PairOut {
-    float sum[32 * 20 + 3 * 8];
-    float scale[32], bias[32], tokens[8][16];    // tokens: scales of the warp's groups
+    uint32_t pairs[32 * 12 + 3 * 8];
+    float tokens[8][16];                         // of the warp's groups
 };
 constexpr int kPairSmem = (int)(kPairRing + kPairSumWarps * sizeof(PairOut) + sizeof(PairBars));
 
@@ -574,66 +574,50 @@ template <int N> __device__ __forceinline__ void regs_down() {
 constexpr int kPairRegs = 128, kPairSumRegs = 200, kPairConvRegs = 72, kPairRestRegs = 40;
 static_assert(2 * kPairSumRegs + kPairConvRegs + kPairRestRegs <= 4 * kPairRegs, "a raise waits forever");
 
-// Puts group i of a warp's sums into o.sum: a choice of one in eight by halves.
+// Group i of a thread's sums: a choice of one in eight by halves.
 template <int LO, int N>
-__device__ __forceinline__ void pair_put(float *to, const float (&s)[128], int i) {
+__device__ __forceinline__ void pair_take(float (&v)[16], const float (&s)[128], int i) {
     if constexpr (N == 1) {
 #pragma unroll
-        for (int j = 0; j < 16; j += 4)
-            *reinterpret_cast<float4 *>(to + j) =
-                make_float4(s[16 * LO + j], s[16 * LO + j + 1], s[16 * LO + j + 2], s[16 * LO + j + 3]);
+        for (int j = 0; j < 16; ++j) v[j] = s[16 * LO + j];
     } else if (i < LO + N / 2) {
-        pair_put<LO, N / 2>(to, s, i);
+        pair_take<LO, N / 2>(v, s, i);
     } else {
-        pair_put<LO + N / 2, N / 2>(to, s, i);
+        pair_take<LO + N / 2, N / 2>(v, s, i);
     }
 }
 
-// Scales and stores 16 tokens of 32 channels; m, n: the first of them.  Where rows start on 16
-// bytes a lane takes eight channels of two tokens, side by side: with two warps a scheduler
-// every result is waited for.
-__device__ __forceinline__ void pair_store(const MatmulParams &p, const PairOut &o, int group, int64_t m, int64_t n) {
-    const int lane = threadIdx.x & 31, rows = (int)min(p.M - m, (int64_t)16), c = 8 * (lane & 3), j = lane >> 2;
-    if (!p.out_vec || n + 32 > p.N) {            // a lane takes a channel
-        const float *from = o.sum + lane * 20 + (lane >> 3) * 8;
-        const float ws = o.scale[lane], bias = o.bias[lane];
-        if (n + lane < p.N)
-#pragma unroll 4
-            for (int i = 0; i < rows; ++i)
-                matmul_store(p, m + i, n + lane, matmul_value(from[i], o.tokens[group][i], ws, bias));
+// Stores the results of 16 tokens and this lane's channel; m, n: the first token, the channel.
+// As bf16 in rows on 16 bytes a lane takes eight channels of two tokens, by way of shared memory
+// in pairs (as sums, four bytes each, that took twice as long).
+__device__ __forceinline__ void pair_store(const MatmulParams &p, PairOut &o, int64_t m, int64_t n, const float (&v)[16]) {
+    const int lane = threadIdx.x & 31, rows = (int)min(p.M - m, (int64_t)16);
+    if (p.out_f32 || !p.out_vec || n - lane + 32 > p.N) {
+        if (n < p.N)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < rows) matmul_store(p, m + i, n, v[i]);
         return;
     }
-    const float *from = o.sum + c * 20 + c + j;
-    float2 f[2][4];
+    uint4 *to = reinterpret_cast<uint4 *>(o.pairs + lane * 12 + (lane >> 3) * 8);
+    to[0] = make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7]));
+    to[1] = make_uint4(pack_bf2(v[8], v[9]), pack_bf2(v[10], v[11]), pack_bf2(v[12], v[13]), pack_bf2(v[14], v[15]));
+    __syncwarp();
+    const int c = 8 * (lane & 3), j = lane >> 2;
+    const uint32_t *from = o.pairs + c * 12 + c + j;
+    uint32_t w[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) f[x][e] = make_float2(from[40 * e + 8 * x], from[40 * e + 20 + 8 * x]);
-    const float as[2] = {o.tokens[group][j], o.tokens[group][j + 8]};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 ws = *reinterpret_cast<const float2 *>(o.scale + c + 2 * e);
-        const float2 bias = *reinterpret_cast<const float2 *>(o.bias + c + 2 * e);
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-            f[x][e] = make_float2(matmul_value(f[x][e].x, as[x], ws.x, bias.x),
-                                  matmul_value(f[x][e].y, as[x], ws.y, bias.y));
-    }
-    const int64_t at = (m + j) * p.out_st + n + c;
+    for (int e = 0; e < 8; ++e) w[e] = from[12 * e];
+    bf16 *out = (bf16 *)p.out + (m + 2 * j) * p.out_st + (n - lane) + c;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        if (j + 8 * x >= rows) continue;
-        const int64_t here = at + 8 * x * p.out_st;
-        if (p.out_f32) {
-            float4 *to = reinterpret_cast<float4 *>((float *)p.out + here);
-            to[0] = make_float4(f[x][0].x, f[x][0].y, f[x][1].x, f[x][1].y);
-            to[1] = make_float4(f[x][2].x, f[x][2].y, f[x][3].x, f[x][3].y);
-        } else {
-            *reinterpret_cast<uint4 *>((bf16 *)p.out + here) =
-                make_uint4(pack_bf2(f[x][0].x, f[x][0].y), pack_bf2(f[x][1].x, f[x][1].y),
-                           pack_bf2(f[x][2].x, f[x][2].y), pack_bf2(f[x][3].x, f[x][3].y));
-        }
+        const uint32_t half = x ? 0x7632 : 0x5410;
+        if (2 * j + x < rows)
+            *reinterpret_cast<uint4 *>(out + x * p.out_st) =
+                make_uint4(__byte_perm(w[0], w[1], half), __byte_perm(w[2], w[3], half),
+                           __byte_perm(w[4], w[5], half), __byte_perm(w[6], w[7], half));
     }
+    __syncwarp();
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
@@ -706,9 +690,9 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
                 const int64_t n = (int64_t)(u.tile / sh.tiles_m) * 256 + 128 * rank + row;
                 const int64_t m0 = (int64_t)(u.tile % sh.tiles_m) * NT;
                 const int chunk = pass || pair_squares(sh, p.M, u.tile) > kPairCareful ? kI8Exact : steps;
+                float ws = 0.f, bias = 0.f;
                 if (u.whole) {
-                    out.scale[lane] = n < p.N ? p.w_scale[n] : 0.f;
-                    out.bias[lane] = n < p.N ? matmul_bias(p, n) : 0.f;
+                    if (n < p.N) ws = p.w_scale[n], bias = matmul_bias(p, n);
 #pragma unroll
                     for (int i = lane >> 4; i < 8; i += 2)
                         out.tokens[i][lane & 15] = p.a_scale[min(m0 + 16 * (q + 2 * i) + (lane & 15), p.M - 1)];
@@ -761,16 +745,15 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
                                           __float2int_rn(sums.s[4 * i + 2]), __float2int_rn(sums.s[4 * i + 3]));
                     }
                 } else {
-                    // 16 tokens at a time by way of shared memory
-                    float *mine = out.sum + lane * 20 + (lane >> 3) * 8;
 #pragma unroll 1
                     for (int i = 0; i < 8; ++i) {
                         const int tok = 16 * (q + 2 * i);
                         if (tok >= NT || m0 + tok >= p.M) break;
-                        pair_put<0, 8>(mine, sums.s, i);
-                        __syncwarp();
-                        pair_store(p, out, i, m0 + tok, n - lane);
-                        __syncwarp();
+                        float v[16];
+                        pair_take<0, 8>(v, sums.s, i);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = matmul_value(v[j], out.tokens[i][j], ws, bias);
+                        pair_store(p, out, m0 + tok, n, v);
                     }
                 }
                 __syncwarp();
