@@ -490,7 +490,7 @@ struct PairUnit {
 __device__ __forceinline__ PairUnit pair_unit(const PairShape &sh, int unit) {
     if (unit < sh.full) return {unit, 0, sh.steps, true};
     const int j = unit - sh.full, part = j % sh.parts;
-    return {sh.full + j / sh.parts, sh.steps * part / sh.parts, sh.steps * (part + 1) / sh.parts, sh.parts == 1};
+    return {sh.full + j / sh.parts, sh.steps * part / sh.parts, sh.steps * (part + 1) / sh.parts, false};
 }
 struct PairBars {
     uint64_t full[kPairMaxStages], conv[kPairMaxStages], free[kPairMaxStages], d_full[2], d_free[2];
@@ -760,7 +760,8 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
             }
             __syncwarp();
             tc::fence_before_sync();
-            cluster_sync();                      // the other CTA's products and arrivals are done
+            cluster_arrive_relaxed();            // no other warp reads what this one stored
+            cluster_wait();
             if (*(volatile uint32_t *)&S.any == 0) break;
         }
     } else if (warp < kPairSumWarps + kPairConvWarps) {
@@ -868,6 +869,9 @@ matmul_i8_pair_kernel(const __grid_constant__ I8Maps maps, const __grid_constant
                     }
                 }
             }
+            if (products)                        // the other CTA's sums' warps have arrived
+                for (uint32_t k = c < (uint32_t)buffers ? 0 : c - buffers; k < c && ok; ++k)
+                    ok = i8_wait(&S.d_free[k & (buffers - 1)], (k / buffers) & 1, abort);
             __syncwarp();
             tc::fence_before_sync();
             cluster_sync();                      // the other CTA's products and arrivals are done
