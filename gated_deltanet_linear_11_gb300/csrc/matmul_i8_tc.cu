@@ -997,6 +997,15 @@ PairPlan pair_plan(int64_t M, int64_t N, int64_t K, int pairs) {
     return plan;
 }
 
+// Ranges of K of a tile of the cluster kernel: as many as keep every SM busy, of at least two
+// steps each; clusters of a power of two fit the device best (40 tiles: 13.7 us in fours, 17.1
+// in sevens).
+int64_t few_parts(int64_t tiles, int64_t steps, int64_t ctas) {
+    int64_t parts = 1;
+    while (parts < 8 && 2 * parts * tiles <= ctas && 4 * parts <= steps + 1) parts *= 2;
+    return parts;
+}
+
 template <int NT>
 gdn_status_t launch_tc(const MatmulParams &p, cudaStream_t st) {
     using Sh = I8Shape<NT>;
@@ -1018,11 +1027,7 @@ gdn_status_t launch_tc(const MatmulParams &p, cudaStream_t st) {
         !row_map(&maps.a, p.a, false, p.M, p.K, p.a_st, NT, true))
         return GDN_ERR_CUDA;
     const int64_t tiles_m = (p.M + NT - 1) / NT, tiles = tiles_m * ((p.N + kI8Channels - 1) / kI8Channels);
-    // as many ranges of K as keep every SM busy, of at least two steps each; clusters of a power
-    // of two fit the device best (40 tiles: 13.7 us in fours, 17.1 in sevens)
-    const int64_t steps = (p.K + kI8Step - 1) / kI8Step, want = (int64_t)sms * Sh::CTAS / tiles;
-    int64_t parts = 1;
-    while (parts < 8 && 2 * parts <= want && 4 * parts <= steps + 1) parts *= 2;
+    const int64_t parts = few_parts(tiles, (p.K + kI8Step - 1) / kI8Step, (int64_t)sms * Sh::CTAS);
     if (tiles * parts > 0x7fffffff) return GDN_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * parts));
@@ -1111,10 +1116,12 @@ bool matmul_i8_pairs(int64_t M, int64_t N, int64_t K) {
     const int64_t left = plan.tiles - plan.full;
     const double turns = (double)((plan.full + pairs - 1) / pairs * steps) +
                          (double)((left * plan.parts + pairs - 1) / pairs * ((steps + plan.parts - 1) / plan.parts));
-    // in us: 333 tokens of 515 channels of 1008 take 9 here and 30 by pairs, 128 of 2048 of 2048
-    // 11.3 and 13.4, 128 of 5120 of 6144 32 and 22
-    const double few = (double)((M + 63) / 64 * ((N + 127) / 128) * steps) / sms;
-    return 13 + 0.54 * turns < 8 + 0.75 * (few > steps / 8. ? few : steps / 8.);
+    const int64_t tiles = (M + 63) / 64 * ((N + kI8Channels - 1) / kI8Channels), ctas = sms * I8Shape<64>::CTAS;
+    const int64_t parts = few_parts(tiles, steps, ctas);
+    const double few = (double)((tiles * parts + ctas - 1) / ctas * ((steps + parts - 1) / parts));
+    // in us: 333 tokens of 515 channels of 1008 take 7 here and 16 by pairs, 2000 of 1024 of 1024
+    // 11.5 and 14.5, 100 of 5120 of 6144 26.5 and 18
+    return 10.5 + 0.54 * turns + (plan.parts > 1 ? 1.5 : 0.) < 6 + 0.75 * few;
 }
 
 size_t matmul_i8_pair_workspace(int64_t M, int64_t N, int64_t K) {
