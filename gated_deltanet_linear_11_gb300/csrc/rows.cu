@@ -166,7 +166,8 @@ __device__ __forceinline__ void largest8(uint32_t &m, const float (&f)[8]) {
 
 // |q| <= 127 to the nearest integer, ties to even: added to 1.5 * 2^23 it is the low bits of the
 // sum (a conversion to integers runs at an eighth of the rate).
-__device__ __forceinline__ int nearest(float q) { return __float_as_int(__fadd_rn(q, 12582912.f)); }
+constexpr float kToInteger = 12582912.f;
+__device__ __forceinline__ int nearest(float q) { return __float_as_int(__fadd_rn(q, kToInteger)); }
 
 // v silu(z).  For bf16, 1 / (1 + e^-z) from the hardware's base-2 exponential and reciprocal
 // (about 2^-22 each, far under the half step of 2^-9); e^-z past fp32 gives a zero.
@@ -288,9 +289,18 @@ rows_kernel(const __grid_constant__ RowParams p) {
         float v[NV][8];
         const T *x = (const T *)p.x + row * p.x_st, *y = second + row * second_st;
         if constexpr (VEC) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        uint32_t pairs = 0;                             // largest magnitudes of bf16 elements, two by two
         if constexpr (MODE != kRowGatedNorm) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
+                if constexpr (MODE == kRowQuantize && sizeof(T) == 2 && VEC) {
+                    const uint4 u = (i * G + t) * 8 < D ? *reinterpret_cast<const uint4 *>(place(slot, 0, i))
+                                                        : make_uint4(0, 0, 0, 0);
+                    pairs = __vmaxu2(__vmaxu2(pairs, u.x & 0x7fff7fffu), u.y & 0x7fff7fffu);
+                    pairs = __vmaxu2(__vmaxu2(pairs, u.z & 0x7fff7fffu), u.w & 0x7fff7fffu);
+                    unpack8(u, v[i]);
+                    continue;
+                }
                 input(x, place(slot, 0, i), i, v[i]);
                 if (MODE == kRowAddNorm && second) {
                     float u[8];
@@ -307,8 +317,12 @@ rows_kernel(const __grid_constant__ RowParams p) {
         float r = 1.f;                                  // what the elements still lack
         uint32_t m = 0;                                 // largest of them, as bits
         if constexpr (MODE == kRowQuantize) {
+            if constexpr (sizeof(T) == 2 && VEC) {
+                m = max(pairs & 0xffff0000u, pairs << 16);
+            } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) largest8(m, v[i]);
+                for (int i = 0; i < NV; ++i) largest8(m, v[i]);
+            }
             float none = 0.f;
             reduce_row<WARP_ROW, false>(none, m, slots[slot][0]);
         } else if constexpr (MODE == kRowAddNorm) {
@@ -418,16 +432,23 @@ rows_kernel(const __grid_constant__ RowParams p) {
             for (int i = 0; i < NV; ++i) {
                 int c[8];
                 mul8(v[i], to_code);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float q = v[i][j];
+                if constexpr (MODE == kRowQuantize && sizeof(T) == 2) {
                     // bf16 rows meet ties exactly (an element of half the largest stands at 63.5).
                     // With significands X and A of 8 bits, 127 X / (A 2^s) is a tie or at least
                     // 2^-16 of itself away from one, so rounding it to 18 bits brings ties back
                     // and moves nothing else across.
-                    if (MODE == kRowQuantize && sizeof(T) == 2)
-                        q = __int_as_float((__float_as_int(q) + 32) & ~63);
-                    c[j] = nearest(q);
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        const float2 q = add_f32x2(
+                            make_float2(__int_as_float((__float_as_int(v[i][j]) + 32) & ~63),
+                                        __int_as_float((__float_as_int(v[i][j + 1]) + 32) & ~63)),
+                            make_float2(kToInteger, kToInteger));
+                        c[j] = __float_as_int(q.x);
+                        c[j + 1] = __float_as_int(q.y);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) c[j] = nearest(v[i][j]);
                 }
                 output((int8_t *)p.y + row * p.y_st, i, c);
             }
