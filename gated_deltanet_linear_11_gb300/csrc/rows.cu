@@ -164,10 +164,9 @@ __device__ __forceinline__ void largest8(uint32_t &m, const float (&f)[8]) {
     for (int j = 0; j < 8; j += 2) m = max(m, max(magnitude(f[j]), magnitude(f[j + 1])));
 }
 
-// |q| <= 127 to the nearest integer, ties to even: added to 1.5 * 2^23 it is the low bits of the
+// |q| <= 127 added to 1.5 * 2^23 leaves the nearest integer, ties to even, in the low bits of the
 // sum (a conversion to integers runs at an eighth of the rate).
 constexpr float kToInteger = 12582912.f;
-__device__ __forceinline__ int nearest(float q) { return __float_as_int(__fadd_rn(q, kToInteger)); }
 
 // v silu(z).  For bf16, 1 / (1 + e^-z) from the hardware's base-2 exponential and reciprocal
 // (about 2^-22 each, far under the half step of 2^-9); e^-z past fp32 gives a zero.
@@ -431,12 +430,12 @@ rows_kernel(const __grid_constant__ RowParams p) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 int c[8];
-                mul8(v[i], to_code);
                 if constexpr (MODE == kRowQuantize && sizeof(T) == 2) {
                     // bf16 rows meet ties exactly (an element of half the largest stands at 63.5).
                     // With significands X and A of 8 bits, 127 X / (A 2^s) is a tie or at least
                     // 2^-16 of itself away from one, so rounding it to 18 bits brings ties back
                     // and moves nothing else across.
+                    mul8(v[i], to_code);
 #pragma unroll
                     for (int j = 0; j < 8; j += 2) {
                         const float2 q = add_f32x2(
@@ -448,7 +447,12 @@ rows_kernel(const __grid_constant__ RowParams p) {
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) c[j] = nearest(v[i][j]);
+                    for (int j = 0; j < 8; j += 2) {        // rounded once
+                        const float2 q = fma_f32x2(make_float2(v[i][j], v[i][j + 1]), make_float2(to_code, to_code),
+                                                   make_float2(kToInteger, kToInteger));
+                        c[j] = __float_as_int(q.x);
+                        c[j + 1] = __float_as_int(q.y);
+                    }
                 }
                 output((int8_t *)p.y + row * p.y_st, i, c);
             }
