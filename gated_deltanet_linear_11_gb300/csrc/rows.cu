@@ -204,15 +204,23 @@ __device__ __forceinline__ void copy8(uint8_t *dst, const T *src) {
                      :: "r"(to + b), "l"(reinterpret_cast<const uint8_t *>(src) + b) : "memory");
 }
 
+// Registers of a thread, by which the launch counts the CTAs of an SM.  56 for the gated norm: a
+// third CTA of 384 threads fits beside two, which its barrier needs most (see below).
+constexpr int row_registers(int mode, int nv, bool warp_row, bool vec) {
+    if (warp_row && !vec) return 96;             // their number is not counted
+    if (!warp_row && nv == 2 && mode == kRowGatedNorm) return 56;
+    return nv == 1 || (nv == 2 && mode == kRowQuantize) ? 48 : 64;
+}
+
 // One row per warp (WARP_ROW) or per CTA; a thread holds NV times 8 consecutive elements.
 // Rows go round the grid.  VEC (rows on 16 bytes): a thread copies its elements of the next two
 // rows into a place of its own in shared memory while it works on this one, so that the loads
 // never pause; the weights stay in registers.
 template <typename T, int MODE, bool OUT8, int NV, bool WARP_ROW, bool VEC>
-__global__ void __launch_bounds__(WARP_ROW ? 128 : 1024, 1)
+__global__ void __maxnreg__(row_registers(MODE, NV, WARP_ROW, VEC))
 rows_kernel(const __grid_constant__ RowParams p) {
     constexpr int INPUTS = MODE == kRowQuantize ? 1 : 2, PIECE = 8 * (int)sizeof(T);
-    constexpr bool HELD = MODE != kRowQuantize && NV <= 2;  // weights in registers
+    constexpr bool HELD = MODE == kRowGatedNorm || (MODE == kRowAddNorm && NV <= 2);   // weights in registers
     extern __shared__ __align__(16) uint8_t ring[];     // [slot][input][NV][thread]
     __shared__ uint32_t slots[2][2][64];
     const int G = WARP_ROW ? 32 : blockDim.x, t = WARP_ROW ? threadIdx.x & 31 : threadIdx.x;
@@ -225,7 +233,9 @@ rows_kernel(const __grid_constant__ RowParams p) {
     grid_dependency_wait();
     if (begin >= p.T) return;                           // a whole warp, which then meets no barrier
 
-    float w[HELD ? NV : 1][8];
+    // A head's length divides 256, so all vectors of a thread have the same weights of a head.
+    constexpr int KEPT = HELD && MODE == kRowAddNorm ? NV : 1;
+    float w[KEPT][8];
     // the weights of vector i: zero past the row's end
     auto weights = [&](int i, float (&f)[8]) {
         const int e = (i * G + t) * 8, n = D - e;
@@ -281,7 +291,7 @@ rows_kernel(const __grid_constant__ RowParams p) {
     }
     if constexpr (HELD)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) weights(i, w[i]);
+        for (int i = 0; i < KEPT; ++i) weights(i, w[i]);
 
     int slot = 0;
     for (int64_t row = begin; row < p.T; row += step, slot ^= 1) {
@@ -393,7 +403,7 @@ rows_kernel(const __grid_constant__ RowParams p) {
                 const float rh = rsqrtf(__fadd_rn(ss * p.per_mean, p.eps * shrink * shrink));
                 mul8(v[i], rh);
                 if constexpr (HELD) {
-                    mul8(v[i], w[i]);
+                    mul8(v[i], w[0]);
                 } else {
                     weights(i, f);
                     mul8(v[i], f);
@@ -485,9 +495,8 @@ static gdn_status_t launch_rows_k(const RowParams &p, int threads, cudaStream_t 
     }
     const int sms = matmul_sm_count(dev);
     if (sms <= 0) return GDN_ERR_CUDA;
-    // as many CTAs as the SMs take at once: by registers (64 a thread; 48 where there is
-    // less in hand) and by shared memory
-    int per = 65536 / (threads * (MODE == kRowQuantize || NV == 1 ? 48 : 64));
+    // as many CTAs as the SMs take at once, by registers and by shared memory
+    int per = 65536 / (threads * row_registers(MODE, NV, WARP_ROW, VEC));
     if (per > 220 * 1024 / (smem + 2048)) per = 220 * 1024 / (smem + 2048);
     if (per < 1) per = 1;
     const int64_t rows = WARP_ROW ? (p.T + 3) / 4 : p.T, most = VEC ? (int64_t)sms * per : rows;
