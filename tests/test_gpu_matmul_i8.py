@@ -115,20 +115,21 @@ def test_nothing_to_do_and_scales_that_are_not_finite():
     assert keep.isfinite().all()
 
 
-def test_leading_dimension_and_given_scratch():
+@pytest.mark.parametrize("K", [2048, 4096])
+def test_leading_dimension_and_given_scratch(K):
     """[1, T, K] operands, a workspace of the stated size, and one that is too small."""
-    a, w = codes(1, 400, 2048), codes(2, 2304, 2048)
+    a, w = codes(1, 400, K), codes(2, 2304, K)
     sa, sw = scales(1, 400), scales(2, 2304)
     want = gdn.gdn_matmul_i8(a, sa, w, sw)
     size = gdn.gdn_matmul_i8_workspace_size(a, w)
-    assert size > 0
+    assert (size > 0) == (K == 4096)            # the longer rows go by pairs of CTAs
     ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")     # fp16 NaN, counts of -1
     got = gdn.gdn_matmul_i8(a[None], sa, w[None], sw, workspace=ws)
     assert got.shape == (1, 400, 2304)
     assert_bits_equal(got[0], want, "out")
     # shifted by a byte: rows off 16 bytes, so copies of both
-    b = torch.empty(400 * 2048 + 1, dtype=torch.int8, device="cuda")[1:].view(400, 2048)
-    v = torch.empty(2304 * 2048 + 1, dtype=torch.int8, device="cuda")[1:].view(2304, 2048)
+    b = torch.empty(400 * K + 1, dtype=torch.int8, device="cuda")[1:].view(400, K)
+    v = torch.empty(2304 * K + 1, dtype=torch.int8, device="cuda")[1:].view(2304, K)
     b.copy_(a)
     v.copy_(w)
     assert gdn.gdn_matmul_i8_workspace_size(b, v) > size
