@@ -115,7 +115,7 @@ __device__ __forceinline__ void cluster_put(uint32_t to, uint32_t bar, uint4 v) 
 
 // A lane's four tokens of one channel, the first n of them, to rows st apart; neighbouring lanes
 // have neighbouring channels.  vec (bf16, all lanes, rows on 16 bytes): four lanes trade, and each
-// stores four channels of one token (stores of two bytes took 1 us of a kernel's 24).
+// stores four channels of one token (by stores of two bytes 64 tokens took 0.6 us longer).
 template <typename T>
 __device__ __forceinline__ void i8_put4(T *to, int64_t st, int n, const float (&v)[4], bool vec) {
     if constexpr (sizeof(T) == 2) {
@@ -198,12 +198,12 @@ template <int N> struct ExactSums {
 //
 // A CTA makes 128 channels x NT tokens over a range of K; the CTAs of a cluster share a tile
 // by ranges of K.  Each sends its int32 sums to the CTA that adds them up, one of its share of
-// the channels (reading the others' memory between two barriers took 5 us of 27 at 64 tokens).
+// the channels (reading the others' memory between two barriers took 2 us longer at 64 tokens).
 // Tokens are converted into fp16 tiles in shared memory.
-// Measured, 16480 channels of 5120: 16 tokens 19.4 us, 64 tokens 27 us, where HBM takes 12.5:
+// Measured, 16480 channels of 5120: 16 tokens 18.3 us, 64 tokens 23.8 us, where HBM takes 12.5:
 // each step's chain (copy, codes out of shared memory, conversion, TMEM, products) is waited for
-// with two CTAs an SM; issue slots are 54% busy, the tensor pipe 14%.  More converting warps
-// shorten no chain and take the registers (16 of 56 registers: 64 tokens 30.5 us).
+// with two CTAs an SM; issue slots are 54% busy, the tensor pipe 16%.  More converting warps
+// shorten no chain and take the registers (16 of 56 registers took 3.6 us longer at 64 tokens).
 template <int NT>
 __global__ void __launch_bounds__(kI8Threads, I8Shape<NT>::CTAS)
 matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__ MatmulParams p, int tiles_m) {
@@ -466,9 +466,9 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
 // int32 sums go to the workspace and are added up by a kernel after this one.  Warps 0-7 move
 // sums (a thread: one channel, half of the tokens), 8-11 convert, 12 copies, 13 issues products
 // (in the first CTA of a pair).
-// Measured, 16480 channels of 5120: 4096 tokens 350 us (1970 TFLOP/s, a library bf16 product's
-// rate), 1024 tokens 100 us (1720; the tensor pipe is 76% busy), 256 tokens 38.5 us, of which
-// some 15 are the tokens' kernel, the first copies and the sums' way out.
+// Measured, 16480 channels of 5120: 4096 tokens 344 us (2000 TFLOP/s, above a library bf16
+// product's rate), 1024 tokens 97 us (1770; the tensor pipe is 78% busy), 256 tokens 33 us, of
+// which some 11 are the tokens' kernel, the first copies and the sums' way out.
 constexpr int kPairSumWarps = 8, kPairConvWarps = 4, kPairMaxStages = 4;
 constexpr int kPairThreads = 32 * (kPairSumWarps + kPairConvWarps + 4);  // two warps idle
 constexpr int kPairTokens = 256;                 // most tokens of a tile
@@ -589,7 +589,7 @@ __device__ __forceinline__ void pair_take(float (&v)[16], const float (&s)[128],
 
 // Stores the results of 16 tokens and this lane's channel; m, n: the first token, the channel.
 // As bf16 in rows on 16 bytes a lane takes eight channels of two tokens, by way of shared memory
-// in pairs (as sums, four bytes each, that took twice as long).
+// in pairs (as sums, four bytes each, 500 tokens of 10240 channels of 5120 took 0.5 us longer).
 __device__ __forceinline__ void pair_store(const MatmulParams &p, PairOut &o, int64_t m, int64_t n, const float (&v)[16]) {
     const int lane = threadIdx.x & 31, rows = (int)min(p.M - m, (int64_t)16);
     if (p.out_f32 || !p.out_vec || n - lane + 32 > p.N) {
@@ -969,7 +969,7 @@ int pair_tokens(int64_t M) { return M <= 128 ? 128 : 256; }
 // Tiles, those made whole, and the units of each other one.  The parts along K are as many as
 // make the last turns shortest; a turn's fill and its sums' way out cost about six steps and
 // the join five (128 tokens of 5120 channels of 6144: whole 29 us, three parts 21; 500 tokens of
-// the same: whole 40, three parts in two turns 48).
+// the same: whole 40, three parts in two turns 48; all four are 2 to 4 us less since).
 constexpr int kPairMaxParts = 12, kPairUnitCost = 6, kPairJoinCost = 5;
 struct PairPlan {
     int64_t tiles, full;

@@ -13,11 +13,11 @@
 // one pass through shared memory.  The split of a row depends on its length alone, so a row's
 // results are the same in any batch.
 //
-// Measured, 4096 bf16 rows: norm with residual of 5120 29.3 us (5.7 TB/s, 84% of a copy's rate),
-// to 8 bits 25.3 (86%); gated norm of 48 x 128 26.3 (85%), to 8 bits 30.9 (60%: the row's maximum
-// is one more barrier between its loads and its stores, and issue slots are 73% busy); 10240 rows
-// of 5120 to 8 bits 31.2 (74%), from fp32 43.6 (89%).  64 rows and fewer take 1.6 to 3 us, a
-// launch and the row's way through the SM.
+// Measured, 4096 bf16 rows: norm with residual of 5120 29.2 us (5.7 TB/s, 85% of a copy's rate),
+// to 8 bits 24.9 (87%); gated norm of 48 x 128 25.5 (87%), to 8 bits 29.1 (64%: the row's maximum
+// is one more barrier between its loads and its stores); 10240 rows of 5120 to 8 bits 29 (80%),
+// from fp32 43.4 (89%).  64 rows and fewer take 1.5 to 3 us, a launch and the row's way through
+// the SM.
 #include <atomic>
 
 #include "bulk_ptx.cuh"
