@@ -210,3 +210,40 @@ def test_some_tiles_with_large_sums(M):
     check(a, w, dtype=F32)
     w[:] = codes(2, N, K, -30, 30)
     check(a, w, dtype=F32)
+
+
+# Many channels or long rows: pairs of CTAs from 65 tokens on, tiles whole, in parts and both.
+PAIRS = [(65, 5130, 6144), (128, 5120, 6160), (129, 5200, 6145), (300, 2600, 12288), (500, 10240, 2048),
+         (700, 5131, 3008), (1500, 2311, 2048)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,N,K", PAIRS)
+def test_sizes_of_pairs(M, N, K, dtype):
+    a, w = codes(M + K, M, K, pad=-K % 16), codes(N + K, N, K, pad=-K % 16)
+    assert gdn.gdn_matmul_i8_workspace_size(a, w) > 0
+    gen = torch.Generator().manual_seed(M)
+    bias = None if M % 2 else torch.randn(N, generator=gen).to(dtype).cuda()
+    out = torch.zeros(M + 1, N + 24, dtype=dtype, device="cuda")
+    check(a, w, bias, dtype, out=out[:M, 8:8 + N])
+    assert not out[M].any() and not out[:, :8].any() and not out[:, 8 + N:].any()
+
+
+@pytest.mark.parametrize("M", [70, 300])
+@pytest.mark.parametrize("lo,hi", [(-128, -128), (120, 127)])
+def test_largest_sums_of_pairs(M, lo, hi):
+    a, w = codes(1, M, 6144, lo, hi), codes(2, 5130, 6144, lo, hi)
+    assert gdn.gdn_matmul_i8_workspace_size(a, w) > 0
+    check(a, w)
+
+
+@pytest.mark.parametrize("M", [70, 128, 300])
+def test_some_pairs_with_large_sums(M):
+    """As above, for tiles that are made a second time beside ones that are not."""
+    K, N = 6144, 5400
+    a, w = codes(1, M, K, -30, 30), codes(2, N, K, -30, 30)
+    assert gdn.gdn_matmul_i8_workspace_size(a, w) > 0
+    w[130:140], w[4000], w[5399] = 127, 127, -128
+    check(a, w, dtype=F32)
+    a[M // 2], a[M - 1] = -128, 127
+    check(a, w)
