@@ -31,6 +31,7 @@ namespace {
 constexpr float kTinyScale = 1.17549435e-38f;   // 2^-126: the scale of a row of zeros
 constexpr uint32_t kInfBits = 0x7f800000u;
 constexpr float kShrink = 8.271806125530277e-25f;   // 2^-80
+constexpr uint32_t kSmallBits = 0x0d800000u;        // 2^-100: what is 2^-26 of it is a normal number still
 
 // Eight elements from a 16-byte boundary on (weights, shared memory).
 template <typename T>
@@ -222,7 +223,7 @@ rows_kernel(const __grid_constant__ RowParams p) {
     constexpr int INPUTS = MODE == kRowQuantize ? 1 : 2, PIECE = 8 * (int)sizeof(T);
     constexpr bool HELD = MODE == kRowGatedNorm || (MODE == kRowAddNorm && NV <= 2);   // weights in registers
     extern __shared__ __align__(16) uint8_t ring[];     // [slot][input][NV][thread]
-    __shared__ uint32_t slots[2][2][64];
+    __shared__ uint32_t slots[2][3][64];
     const int G = WARP_ROW ? 32 : blockDim.x, t = WARP_ROW ? threadIdx.x & 31 : threadIdx.x;
     const int64_t step = WARP_ROW ? (int64_t)gridDim.x * 4 : gridDim.x;
     const int64_t begin = WARP_ROW ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
@@ -338,32 +339,39 @@ rows_kernel(const __grid_constant__ RowParams p) {
             // For 8 bits the largest |h (offset + w)| is found together with the sum of squares: the
             // common factor r does not move the place of the maximum, so one reduction serves both.
             float ss = 0.f;
-            auto measure = [&]() {
-                float2 sum = make_float2(0.f, 0.f);
+            auto times_weights = [&](int i, float (&f)[8]) {        // f w
+                if constexpr (HELD) {
+                    mul8(f, w[i]);
+                } else {
+                    float u[8];
+                    weights(i, u);
+                    mul8(f, u);
+                }
+            };
+            auto largest = [&]() {
                 m = 0;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    squares8(sum, v[i]);
-                    if constexpr (OUT8) {
-                        float f[8];
-                        if constexpr (HELD) {
+                    float f[8];
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) f[j] = w[i][j];
-                        } else {
-                            weights(i, f);
-                        }
-                        mul8(f, v[i]);
-                        largest8(m, f);
-                    }
+                    for (int j = 0; j < 8; ++j) f[j] = v[i][j];
+                    times_weights(i, f);
+                    largest8(m, f);
                 }
+            };
+            auto measure = [&]() {
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) squares8(sum, v[i]);
                 ss = sum.x + sum.y;
+                if constexpr (OUT8) largest();
             };
             measure();
             reduce_row<WARP_ROW, true>(ss, m, slots[slot][0]);
             float shrink = 1.f;
-            if (!(ss < __uint_as_float(kInfBits)) || m >= kInfBits) {
-                // Squares or products past fp32: once more with h / 2^80.  A row that holds an
-                // infinity or a NaN stays without a finite sum.
+            if (!(ss < __uint_as_float(kInfBits))) {
+                // Squares past fp32: once more with h / 2^80.  A row that holds an infinity or a NaN
+                // stays without a finite sum.
                 shrink = kShrink;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) mul8(v[i], shrink);
@@ -371,14 +379,20 @@ rows_kernel(const __grid_constant__ RowParams p) {
                 reduce_row<WARP_ROW, true>(ss, m, slots[slot][1]);
             }
             r = rsqrtf(__fadd_rn(ss * p.per_mean, p.eps * shrink * shrink));
+            // Products past fp32 or among its smallest numbers, though h r w may be neither: h r, at
+            // most sqrt(D), comes first then, as it does in rows of floating-point type.
+            if (!OUT8 || m >= kInfBits || m < kSmallBits) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float f[8];
-                if constexpr (!HELD) weights(i, f);
-                if constexpr (!OUT8) mul8(v[i], r);         // h r first: no product can overflow
-                if constexpr (HELD) mul8(v[i], w[i]);
-                else mul8(v[i], f);
+                for (int i = 0; i < NV; ++i) mul8(v[i], r);
+                if constexpr (OUT8) {
+                    r = 1.f;
+                    largest();
+                    float none = 0.f;
+                    reduce_row<WARP_ROW, false>(none, m, slots[slot][2]);
+                }
             }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) times_weights(i, v[i]);
         } else {
             const int lanes = p.head >> 3;              // threads of a head: a power of two up to 32
 #pragma unroll

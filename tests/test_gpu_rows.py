@@ -243,3 +243,23 @@ def test_norm_in_a_graph():
         assert_bits_equal(q, q1, "codes")
         assert_bits_equal(s, s1, "scale")
         assert_bits_equal(h, h1, "residual")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [256, 640, 2047, 5120, 20000])
+def test_weights_and_rows_far_from_one(D, dtype):
+    """Sizes of rows and weights whose products leave fp32's range, or its normal numbers, though
+    the norm stays inside; eps as small as it may be.  The largest of 20000 normal numbers is
+    about 4, so results stay under 1e38."""
+    sizes = [(30.0, 1e37, 1e-6), (100.0, 1e37, 1e-6), (1e3, 1e36, 1e-6), (3e37, 1e34, 1e-6),
+             (3e37, 1e-38, 1e-6), (1e-10, 1e-35, 1e-6), (1e-18, 1e-24, 2.0 ** -126),
+             (1e-20, 1e-20, 2.0 ** -126)]
+    for size, weight, eps in sizes:
+        x = (rnd(D, 4, D, dtype=F32) * size).to(dtype)
+        x[2] = 0
+        w = (1 + torch.rand(D, generator=torch.Generator().manual_seed(D))).cuda() * weight
+        want, _ = ref.add_rmsnorm(x, w, None, eps, 0.0)
+        (q, scale), _ = gdn.gdn_add_rmsnorm(x, w, eps=eps, eight_bit=True)
+        ref.assert_codes(q, scale, want, ref.NORM)
+        y, _ = gdn.gdn_add_rmsnorm(x, w, eps=eps)
+        ref.assert_close(y, want, ref.NORM, dtype)
