@@ -159,6 +159,14 @@ __device__ __forceinline__ void squares8(float2 &sum, const float (&f)[8]) {
         sum = fma_f32x2(t, t, sum);
     }
 }
+// The same of f c.
+__device__ __forceinline__ void shrunk_squares8(float2 &sum, const float (&f)[8], float c) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const float2 t = mul_f32x2(make_float2(f[j], f[j + 1]), make_float2(c, c));
+        sum = fma_f32x2(t, t, sum);
+    }
+}
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 __device__ __forceinline__ void largest8(uint32_t &m, const float (&f)[8]) {
 #pragma unroll
@@ -373,12 +381,24 @@ rows_kernel(const __grid_constant__ RowParams p) {
                 // Squares past fp32: once more with h / 2^80.  A row that holds an infinity or a NaN
                 // stays without a finite sum.
                 shrink = kShrink;
+                if constexpr (OUT8) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i) mul8(v[i], shrink);
-                measure();
+                    for (int i = 0; i < NV; ++i) mul8(v[i], shrink);
+                    measure();
+                } else {
+                    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) shrunk_squares8(sum, v[i], shrink);
+                    ss = sum.x + sum.y;
+                }
                 reduce_row<WARP_ROW, true>(ss, m, slots[slot][1]);
             }
             r = rsqrtf(__fadd_rn(ss * p.per_mean, p.eps * shrink * shrink));
+            if (!OUT8 && shrink != 1.f) {       // r first: the row's small elements stay normal numbers
+#pragma unroll
+                for (int i = 0; i < NV; ++i) mul8(v[i], r);
+                r = shrink;
+            }
             // Products past fp32 or among its smallest numbers, though h r w may be neither: h r, at
             // most sqrt(D), comes first then, as it does in rows of floating-point type.
             if (!OUT8 || m >= kInfBits || m < kSmallBits) {
@@ -408,13 +428,21 @@ rows_kernel(const __grid_constant__ RowParams p) {
                 const bool big = !(ss < __uint_as_float(kInfBits));
                 if (__any_sync(0xffffffffu, big)) {     // as above, for the heads that need it
                     if (big) shrink = kShrink;
-                    mul8(v[i], shrink);
                     sum = make_float2(0.f, 0.f);
-                    squares8(sum, v[i]);
+                    if constexpr (OUT8) {
+                        mul8(v[i], shrink);
+                        squares8(sum, v[i]);
+                    } else {
+                        shrunk_squares8(sum, v[i], shrink);
+                    }
                     ss = sum.x + sum.y;
                     for (int s = lanes >> 1; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
                 }
-                const float rh = rsqrtf(__fadd_rn(ss * p.per_mean, p.eps * shrink * shrink));
+                float rh = rsqrtf(__fadd_rn(ss * p.per_mean, p.eps * shrink * shrink));
+                if (!OUT8 && shrink != 1.f) {
+                    mul8(v[i], rh);
+                    rh = shrink;
+                }
                 mul8(v[i], rh);
                 if constexpr (HELD) {
                     mul8(v[i], w[0]);

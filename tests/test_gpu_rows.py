@@ -263,3 +263,19 @@ def test_weights_and_rows_far_from_one(D, dtype):
         ref.assert_codes(q, scale, want, ref.NORM)
         y, _ = gdn.gdn_add_rmsnorm(x, w, eps=eps)
         ref.assert_close(y, want, ref.NORM, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [256, 640, 5120])
+def test_small_elements_of_large_rows(D, dtype):
+    """Elements far under the others of a row whose squares pass fp32: their results are normal
+    numbers."""
+    x = rnd(1, 4, D, dtype=F32) * 1e19
+    x[:, ::7] *= 1e-37
+    x = x.to(dtype)
+    w = rnd(2, D, dtype=F32) * 20
+    want, _ = ref.add_rmsnorm(x, w, None, 1e-6, 0.0)
+    ref.assert_close(gdn.gdn_add_rmsnorm(x, w)[0], want, ref.NORM, dtype)
+    x3, z, w3 = x.view(4, -1, 128), rnd(3, 4, D // 128, 128, dtype=dtype) + 3, w[:128].contiguous()
+    want = ref.gated_rmsnorm(x3, z, w3, 1e-6)
+    ref.assert_close(gdn.gdn_gated_rmsnorm(x3, z, w3), want, ref.GATED[dtype], dtype)
