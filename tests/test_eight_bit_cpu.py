@@ -183,3 +183,10 @@ def test_binding_refusals(lib, monkeypatch):
     with pytest.raises(gdn.GdnError) as e:
         gdn.gdn_matmul_i8(z(2, 16, dtype=i8), None, z(3, 16, dtype=i8), None)
     assert e.value.code == 7
+
+
+def test_names_of_the_package():
+    """`from gated_deltanet_linear_11_gb300 import *` brings every entry."""
+    import gated_deltanet_linear_11_gb300 as gdn
+    assert set(eight_bit.__all__) <= set(gdn.__all__)
+    assert all(hasattr(gdn, name) for name in gdn.__all__)
