@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(256) matmul_i8_align_kernel(const __grid_const
         const int off = (int)(at & 3u), words = (off + n + 3) / 4;
         uint32_t w[5], out[4];
 #pragma unroll
-        for (int j = 0; j < 5; ++j) w[j] = j < words ? __ldg(word + j) : 0u;
+        for (int j = 0; j < 5; ++j) w[j] = j < words ? word[j] : 0u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             out[j] = __funnelshift_r(w[j], w[j + 1], 8 * off);

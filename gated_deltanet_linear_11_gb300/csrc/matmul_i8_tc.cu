@@ -510,14 +510,15 @@ struct PairOut {
 };
 constexpr int kPairSmem = (int)(kPairRing + kPairSumWarps * sizeof(PairOut) + sizeof(PairBars));
 
-// Largest |a|^2 of the tile's tokens (a warp).
+// Largest |a|^2 of the tile's tokens (a warp).  The kernel before this one writes them while this
+// one is already there, so the loads are not of the read-only kind.
 __device__ __forceinline__ int32_t pair_squares(const PairShape &sh, int64_t M, int tile) {
     const int64_t m0 = (int64_t)(tile % sh.tiles_m) * sh.NT;
     int32_t most = 0;
 #pragma unroll
     for (int i = 0; i < kPairTokens / 32; ++i) {
         const int64_t m = m0 + 32 * i + (threadIdx.x & 31);
-        if (32 * i < sh.NT && m < M) most = max(most, __ldg(sh.squares + m));
+        if (32 * i < sh.NT && m < M) most = max(most, sh.squares[m]);
     }
     return __reduce_max_sync(0xffffffffu, most);
 }

@@ -247,3 +247,24 @@ def test_some_pairs_with_large_sums(M):
     check(a, w, dtype=F32)
     a[M // 2], a[M - 1] = -128, 127
     check(a, w)
+
+
+@pytest.mark.parametrize("M,N,K,shift", [(128, 5120, 6144, 0), (300, 5131, 2049, 1), (64, 700, 1001, 1),
+                                         (4, 700, 1001, 3)])
+def test_calls_one_after_the_other_in_one_workspace(M, N, K, shift):
+    """Tokens written just before each product, small and large ones in turn, all through the same
+    buffers: nothing of the call before is seen."""
+    sets = [codes(1, M, K, -30, 30), codes(2, M, K, 100, 127), codes(3, M, K)]
+    room = torch.empty(M * K + shift, dtype=torch.int8, device="cuda")
+    a, w = room[shift:].view(M, K), codes(4, N, K)
+    sa, sw = scales(1, M), scales(2, N)
+    ws = torch.full((gdn.gdn_matmul_i8_workspace_size(a, w),), 255, dtype=torch.uint8, device="cuda")
+    assert (ws.numel() > 0) == (M > 64 or shift > 0)
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(24):
+        a.copy_(sets[i % 3])
+        outs.append(gdn.gdn_matmul_i8(a, sa, w, sw, dtype=F32, workspace=ws))
+    want = [ref.product(x, sa, w, sw, None, F32) for x in sets]
+    for i, out in enumerate(outs):
+        assert_bits_equal(out.cpu(), want[i % 3], "call %d" % i)
