@@ -159,11 +159,11 @@ __device__ __forceinline__ void squares8(float2 &sum, const float (&f)[8]) {
         sum = fma_f32x2(t, t, sum);
     }
 }
-// The same of f c.
-__device__ __forceinline__ void shrunk_squares8(float2 &sum, const float (&f)[8], float c) {
+// The same of f / 2^80.
+__device__ __forceinline__ void shrunk_squares8(float2 &sum, const float (&f)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-        const float2 t = mul_f32x2(make_float2(f[j], f[j + 1]), make_float2(c, c));
+        const float2 t = mul_f32x2(make_float2(f[j], f[j + 1]), make_float2(kShrink, kShrink));
         sum = fma_f32x2(t, t, sum);
     }
 }
@@ -388,7 +388,7 @@ rows_kernel(const __grid_constant__ RowParams p) {
                 } else {
                     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int i = 0; i < NV; ++i) shrunk_squares8(sum, v[i], shrink);
+                    for (int i = 0; i < NV; ++i) shrunk_squares8(sum, v[i]);
                     ss = sum.x + sum.y;
                 }
                 reduce_row<WARP_ROW, true>(ss, m, slots[slot][1]);
@@ -420,28 +420,21 @@ rows_kernel(const __grid_constant__ RowParams p) {
                 float g[8], f[8];
                 input(x, place(slot, 0, i), i, v[i]);
                 input(y, place(slot, INPUTS - 1, i), i, g);
-                float shrink = 1.f;
                 float2 sum = make_float2(0.f, 0.f);
                 squares8(sum, v[i]);
                 float ss = sum.x + sum.y;
                 for (int s = lanes >> 1; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
+                float rh = rsqrtf(__fadd_rn(ss * p.per_mean, p.eps));
                 const bool big = !(ss < __uint_as_float(kInfBits));
                 if (__any_sync(0xffffffffu, big)) {     // as above, for the heads that need it
-                    if (big) shrink = kShrink;
                     sum = make_float2(0.f, 0.f);
-                    if constexpr (OUT8) {
-                        mul8(v[i], shrink);
-                        squares8(sum, v[i]);
-                    } else {
-                        shrunk_squares8(sum, v[i], shrink);
-                    }
+                    shrunk_squares8(sum, v[i]);
                     ss = sum.x + sum.y;
                     for (int s = lanes >> 1; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
-                }
-                float rh = rsqrtf(__fadd_rn(ss * p.per_mean, p.eps * shrink * shrink));
-                if (!OUT8 && shrink != 1.f) {
-                    mul8(v[i], rh);
-                    rh = shrink;
+                    if (big) {
+                        mul8(v[i], rsqrtf(__fadd_rn(ss * p.per_mean, p.eps * kShrink * kShrink)));
+                        rh = kShrink;
+                    }
                 }
                 mul8(v[i], rh);
                 if constexpr (HELD) {
