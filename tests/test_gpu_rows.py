@@ -279,3 +279,92 @@ def test_small_elements_of_large_rows(D, dtype):
     x3, z, w3 = x.view(4, -1, 128), rnd(3, 4, D // 128, 128, dtype=dtype) + 3, w[:128].contiguous()
     want = ref.gated_rmsnorm(x3, z, w3, 1e-6)
     ref.assert_close(gdn.gdn_gated_rmsnorm(x3, z, w3), want, ref.GATED[dtype], dtype)
+
+
+def odd_rows(x):
+    """Among x's rows some of zeros, some whose squares pass fp32, some with a NaN."""
+    x[5::11] = 0
+    x[3::7] *= 1e25
+    x[6::13, x.shape[1] // 3] = float("nan")
+    return x
+
+
+def assert_rows(got, want, rel):
+    """8-bit rows against `want`; those of NaN are marked."""
+    q, scale = got
+    bad = torch.from_numpy(~np.isfinite(want).all(-1)).cuda()
+    assert scale[bad].isnan().all() and not q[bad].any()
+    ref.assert_codes(q[~bad], scale[~bad], want[~bad.cpu().numpy()], rel)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [512, 1000, 1001, 6144])
+def test_many_rows_in_eight_bits(D, dtype):
+    """More rows than run at once, so that every CTA makes several, ordinary and odd ones in turn:
+    all of them against 64 bits, and some against calls of a few rows."""
+    T = 3000
+    x, r, w = odd_rows(rnd(1, T, D, dtype=dtype)), rnd(2, T, D, dtype=dtype), rnd(3, D, dtype=dtype)
+    few = slice(1490, 1500)
+    with np.errstate(invalid="ignore"):
+        got = gdn.gdn_quantize_rows(x)
+        assert_rows(got, ref.f64(x), 2 * ref.U)
+        for a, b in zip(got, gdn.gdn_quantize_rows(x[few])):
+            assert_bits_equal(a[few], b, "rows to 8 bits")
+        got, h = gdn.gdn_add_rmsnorm(x, w, r, eight_bit=True)
+        assert_rows(got, ref.add_rmsnorm(x, w, r, 1e-6, 0.0)[0], ref.NORM)
+        one, _ = gdn.gdn_add_rmsnorm(x[few], w, r[few], eight_bit=True)
+        for a, b in zip(got, one):
+            assert_bits_equal(a[few], b, "norm")
+        if D % 128 == 0:
+            x3, z, w3 = x.view(T, -1, 128), r.view(T, -1, 128), w[:128].contiguous()
+            got = gdn.gdn_gated_rmsnorm(x3, z, w3, eight_bit=True)
+            assert_rows(got, ref.gated_rmsnorm(x3, z, w3, 1e-6), ref.GATED[dtype])
+            for a, b in zip(got, gdn.gdn_gated_rmsnorm(x3[few], z[few], w3, eight_bit=True)):
+                assert_bits_equal(a[few], b, "gated norm")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H,D", [(4, 16), (8, 128), (48, 128), (4, 256)])
+def test_gated_rows_that_are_not_finite_and_heads_that_overflow(H, D, dtype):
+    x, z, w = rnd(1, 7, H, D, dtype=dtype), rnd(2, 7, H, D, dtype=dtype), rnd(3, D, dtype=F32)
+    x[0, 1] *= 1e25                         # heads beside ordinary ones in the same warp
+    x[1, 0], x[1, H - 1] = 0, x[1, H - 1] * 3e37
+    want = ref.gated_rmsnorm(x, z, w, 1e-6)
+    y = gdn.gdn_gated_rmsnorm(x, z, w)
+    ref.assert_close(y, want, ref.GATED[dtype], dtype)
+    ref.assert_codes(*gdn.gdn_gated_rmsnorm(x, z, w, eight_bit=True), want, ref.GATED[dtype])
+    inf = float("inf")
+    for t, row, value in ((x, 2, float("nan")), (x, 3, inf), (x, 4, -inf), (z, 5, float("nan")), (z, 6, -inf)):
+        t[row, H - 1, D // 2] = value
+    q, scale = gdn.gdn_gated_rmsnorm(x, z, w, eight_bit=True)
+    assert scale[2:].isnan().all() and not q[2:].any() and scale[:2].isfinite().all()
+    ref.assert_codes(q[:2], scale[:2], want[:2], ref.GATED[dtype])
+    # the other heads are what they were
+    bad = gdn.gdn_gated_rmsnorm(x, z, w)
+    assert_bits_equal(bad[:, :(H - 1) * D].contiguous(), y[:, :(H - 1) * D].contiguous(), "other heads")
+    assert not bad[2:, (H - 1) * D:].isfinite().all(-1).any()
+
+
+def test_gated_rows_repeat_themselves():
+    """The same bits at every pass, other inputs in between, over memory that held other values;
+    codes that are not the nearest lie within 2^-10 of a border."""
+    H, D = 48, 128
+    w = 1 + 0.2 * rnd(1, D)
+    sets = []
+    for seed in (2, 3):
+        x = (rnd(seed, 64, H, D, dtype=F32) * rnd(seed + 5, 64, H, 1, dtype=F32).exp()).to(BF)
+        sets.append((x, rnd(seed + 9, 64, 2 * H * D)[:, H * D:].view(64, H, D)))
+    first = [gdn.gdn_gated_rmsnorm(x, z, w, eight_bit=True) for x, z in sets]
+    off = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(100):
+        junk = torch.full((64, H * D), 255, dtype=torch.uint8, device="cuda")
+        del junk
+        for (x, z), (q, scale) in zip(sets, first):
+            q2, scale2 = gdn.gdn_gated_rmsnorm(x, z, w, eight_bit=True)
+            off += (q != q2).sum() + (scale != scale2).sum()
+            del q2, scale2
+    assert int(off) == 0
+    for (x, z), (q, _) in zip(sets, first):
+        want, _ = ref.quotients(ref.gated_rmsnorm(x, z, w, 1e-6))
+        away = np.abs(want - np.floor(want) - 0.5)[ref.f64(q) != np.rint(want)]
+        assert (away <= 2.0 ** -10).all(), float(away.max())
