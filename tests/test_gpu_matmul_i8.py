@@ -268,3 +268,91 @@ def test_calls_one_after_the_other_in_one_workspace(M, N, K, shift):
     want = [ref.product(x, sa, w, sw, None, F32) for x in sets]
     for i, out in enumerate(outs):
         assert_bits_equal(out.cpu(), want[i % 3], "call %d" % i)
+
+
+# Tiles of pairs of CTAs whose sums turn out to be too large for one run along K, which are then
+# made again: tokens stay under the size at which tiles are made with moves from the start.
+CAREFUL, FAR = 15_000_000, 2 ** 48
+
+
+def squares(x):
+    return x.int().square().sum(-1, dtype=torch.int64)
+
+
+def large_tokens(a, rows):
+    """Tokens whose codes are large in one third of a row each, or of medium size all along:
+    |a|^2 just under the border, sums with channels of 127 above 2^24, their low bits at random."""
+    K = a.shape[1]
+    gen = torch.Generator().manual_seed(K)
+    for i, row in enumerate(rows):
+        if i % 4 == 3:
+            a[row] = torch.randint(47, 49, (K,), generator=gen, dtype=torch.int8).cuda()
+        else:
+            at = K // 3 * (i % 4)
+            a[row] = torch.randint(0, 2, (K,), generator=gen, dtype=torch.int8).cuda()
+            a[row, at:at + K // 3] = torch.randint(83, 85, (K // 3,), generator=gen, dtype=torch.int8).cuda()
+
+
+# whole tiles (76 of them fill 152 SMs once) of 128 and of 256 tokens, tiles in two and three parts,
+# both kinds in one launch
+AGAIN = [(128, 19456), (300, 9728), (300, 4864), (70, 5130), (700, 9000)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,N", AGAIN)
+def test_tiles_made_again(M, N, dtype):
+    K = 6144
+    a, w = codes(1, M, K, -30, 30), codes(2, N, K, -30, 30)
+    large_tokens(a, [0, 1, 2, 3, M // 2, M - 3, M - 2, M - 1])
+    gen = torch.Generator().manual_seed(3)
+    channels = [3, 256 + 130, N - 1, N - 300]           # in the first and the second CTA of a pair
+    w[channels] = torch.randint(126, 128, (4, K), generator=gen, dtype=torch.int8).cuda()
+    assert gdn.gdn_matmul_i8_workspace_size(a, w) > 0
+    most, far = int(squares(a).max()), squares(w).cpu().double() * int(squares(a).max())
+    assert most <= CAREFUL and (far > FAR).nonzero().flatten().tolist() == sorted(channels)
+    assert int((a.double() @ w[3].double()).max()) > 2 ** 24
+    check(a, w, dtype=dtype)
+
+
+@pytest.mark.parametrize("M", [128, 250])
+def test_sums_at_the_border(M):
+    """Every sum just under 2^24 in some tiles and just over it in others, with odd sums of both."""
+    K, N = 6144, 19456
+    a, w = torch.full((M, K), 41, dtype=torch.int8, device="cuda"), codes(2, N, K, -20, 20)
+    a[M // 3, 9] = 40
+    w[256:512], w[1024:1280] = 66, 67
+    w[300:400, 0], w[1100:1200, 0] = 65, 66
+    assert gdn.gdn_matmul_i8_workspace_size(a, w) > 0
+    sums = a.double() @ w.double().t()
+    assert 16_600_000 < sums[:, 256:512].min() and sums[:, 256:512].max() < 2 ** 24
+    assert sums[:, 1024:1280].min() > 2 ** 24
+    assert (sums[:, [300, 1100]] % 2 == 1).any(0).all() and int(squares(a).max()) <= CAREFUL
+    far = squares(w).cpu().double() * int(squares(a).max()) > FAR
+    assert not far[:1024].any() and far[1024:1280].all() and not far[1280:].any()
+    check(a, w, dtype=F32)
+
+
+def test_tiles_made_again_of_very_many():
+    """More than a thousand tiles a pair of CTAs: those behind share one mark."""
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    M, N, K = 65, pairs * 1026 * 256, 1280
+    if torch.cuda.mem_get_info()[0] < 2 * N * (K + 6 * M):
+        pytest.skip("not enough memory")
+    a, kinds = codes(1, M, K, -30, 30), codes(2, 64, K, -30, 30)
+    gen = torch.Generator().manual_seed(5)
+    a[[0, 64]] = torch.randint(107, 109, (2, K), generator=gen, dtype=torch.int8).cuda()
+    w = kinds.repeat(N // 64, 1)
+    tiles = [0, pairs * 500 + 3, pairs * 1022 + 1, pairs * 1023 + 5, pairs * 1024 + 5, pairs * 1026 - 1]
+    channels = [256 * t + (7 if t % 2 else 200) for t in tiles]
+    w[channels] = torch.randint(-128, -126, (len(channels), K), generator=gen, dtype=torch.int8).cuda()
+    assert gdn.gdn_matmul_i8_workspace_size(a, w) > 0
+    assert int(squares(a).max()) <= CAREFUL and int(squares(a).max()) * int(squares(w[channels]).max()) > FAR
+    assert int((a.double() @ w[channels].double().t()).abs().max()) > 2 ** 24
+    sa, sw = scales(1, M), scales(2, 64).repeat(N // 64)
+    out = gdn.gdn_matmul_i8(a, sa, w, sw, dtype=F32)
+    want = ref.product(a, sa, kinds, sw[:64], None, F32).cuda()
+    large = ref.product(a, sa, w[channels], sw[channels], None, F32)
+    assert_bits_equal(out[:, channels].cpu(), large, "large sums")
+    out[:, channels] = want[:, [c % 64 for c in channels]]
+    for m in range(M):
+        assert (out[m].view(-1, 64) == want[m]).all(), m
