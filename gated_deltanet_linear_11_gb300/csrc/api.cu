@@ -4,6 +4,7 @@
 // before launching anything; nothing here allocates device memory.
 #include <string.h>
 
+#include <cfloat>
 #include <cmath>
 #include <initializer_list>
 
@@ -841,7 +842,8 @@ gdn_status_t norm_args(const gdn_matrix_t *weight, int64_t width, float eps, con
     if (!y) return GDN_ERR_NULL;
     if ((s = matrix_of(y, y->dtype == GDN_I8 ? GDN_I8 : dtype, Y)) != GDN_OK) return s;
     if (W.rows != 1 || W.cols != width || Y.rows != T || Y.cols != D) return GDN_ERR_SHAPE;
-    if (!(eps > 0.f) || !std::isfinite(eps)) return GDN_ERR_UNSUPPORTED;
+    // squares under fp32's normal numbers are lost beside an eps of 2^-126, but not beside less
+    if (!(eps >= FLT_MIN) || !std::isfinite(eps)) return GDN_ERR_UNSUPPORTED;
     if (T > 0 && D > 0 && (Y.dtype == GDN_I8) != (scale != nullptr)) return GDN_ERR_NULL;
     if ((uintptr_t)scale & 3u) return GDN_ERR_LAYOUT;
     p.w = W.ptr;

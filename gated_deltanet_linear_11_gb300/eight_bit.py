@@ -111,7 +111,7 @@ def gdn_add_rmsnorm(x, weight, residual=None, eps=1e-6, weight_offset=0.0, eight
     a pair (int8 codes, fp32 scales of the rows) with ``eight_bit``.
 
     x, residual [T, D] bf16 or fp32 views; weight [D] bf16 or fp32; residual_out may be the
-    residual itself.
+    residual itself; eps at least 2^-126.
     """
     lib, _ = _entry("gdn_add_rmsnorm")
     _need_cuda(x, weight, residual, y, scale, residual_out)
@@ -140,7 +140,8 @@ def gdn_gated_rmsnorm(x, z, weight, eps=1e-6, eight_bit=False, y=None, scale=Non
     """The Gated DeltaNet layer's output norm: per head, x weight / sqrt(mean x^2 + eps) *
     silu(z).  Returns y [T, H D] of x's type, or (int8 codes, fp32 scales of the tokens).
 
-    x, z [T, H, D] bf16 or fp32 views (token-major); weight [D] bf16 or fp32.
+    x, z [T, H, D] bf16 or fp32 views (token-major); weight [D] bf16 or fp32; eps at least
+    2^-126.
     """
     lib, _ = _entry("gdn_gated_rmsnorm")
     _need_cuda(x, z, weight, y, scale)

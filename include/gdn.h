@@ -537,7 +537,8 @@ gdn_status_t gdn_quantize_rows(const gdn_matrix_t *x, const gdn_matrix_t *q, flo
  * The norm is that of the fp32 sum; residual_out is the sum rounded once.
  * x [T, D] bf16 or fp32; residual and residual_out likewise and of x's type, or both NULL
  * (h = x); weight [D] bf16 or fp32; y [T, D] of x's type, or int8 with scale fp32 [T] (NULL
- * otherwise).  eps is positive and finite.  D is at most GDN_MAX_ROW.
+ * otherwise).  eps is finite and at least 2^-126.  D is at most GDN_MAX_ROW.
+ * Nothing on the way to y leaves fp32's range unless y or h does.
  */
 gdn_status_t gdn_add_rmsnorm(const gdn_matrix_t *x, const gdn_matrix_t *residual,
                              const gdn_matrix_t *residual_out, const gdn_matrix_t *weight,
@@ -550,7 +551,9 @@ gdn_status_t gdn_add_rmsnorm(const gdn_matrix_t *x, const gdn_matrix_t *residual
  *     y = x weight / sqrt(mean_head x^2 + eps) * silu(z),   silu(z) = z / (1 + e^-z).
  * x, z [T, H, D] views as above, of one type, D a power of two from 16 to 256 and H D at most
  * GDN_MAX_ROW; weight [D] bf16 or fp32; y [T, H D] of x's type, or int8 with scale fp32 [T],
- * one for all heads of a token (NULL otherwise).  eps is positive and finite.
+ * one for all heads of a token (NULL otherwise).  eps is finite and at least 2^-126.
+ * The norm's product with the weight comes first, then that with silu(z), both in fp32; where
+ * silu(z) is under 2^-119 in size, it may be a zero.
  */
 gdn_status_t gdn_gated_rmsnorm(const gdn_tensor_t *x, const gdn_tensor_t *z,
                                const gdn_matrix_t *weight, float eps, const gdn_matrix_t *y,

@@ -190,3 +190,16 @@ def test_names_of_the_package():
     import gated_deltanet_linear_11_gb300 as gdn
     assert set(eight_bit.__all__) <= set(gdn.__all__)
     assert all(hasattr(gdn, name) for name in gdn.__all__)
+
+
+@no_gpu
+def test_smallest_eps(lib):
+    """Beside an eps under 2^-126 the squares of small rows would lack digits: 3e-22 squared is 64
+    of fp32's smallest steps."""
+    x, z, w, g = mat(4, 64), desc(4, 1, 64), mat(1, 64), mat(4, 64)
+    for eps in (1e-45, 1e-40, 1.17e-38):
+        assert lib.gdn_add_rmsnorm(ref(x), None, None, ref(w), 0.0, eps, ref(g), None, None) == 6
+        assert lib.gdn_gated_rmsnorm(ref(z), ref(z), ref(w), eps, ref(g), None, None) == 6
+    none = mat(0, 64, ptr=None)
+    assert lib.gdn_add_rmsnorm(ref(none), None, None, ref(w), 0.0, 2.0 ** -126, ref(none), None,
+                               None) == 0
