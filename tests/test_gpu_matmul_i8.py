@@ -356,3 +356,20 @@ def test_tiles_made_again_of_very_many():
     out[:, channels] = want[:, [c % 64 for c in channels]]
     for m in range(M):
         assert (out[m].view(-1, 64) == want[m]).all(), m
+
+
+@pytest.mark.parametrize("M,N", [(70, 2600), (70, 19456), (140, 2600), (140, 19456)])
+def test_longest_rows_of_pairs(M, N):
+    """K as long as it may be: sums and sums of squares up to 2^31, tiles in parts and whole."""
+    K = 131071
+    a, kinds = codes(1, M, K, pad=1), codes(2, 8, K)
+    a[0], a[1], a[M - 1] = -128, 127, -128
+    kinds[0], kinds[1], kinds[2, K // 2:] = -128, 127, -128
+    w = torch.empty(N, K + 1, dtype=torch.int8, device="cuda")
+    w.view(-1, 8, K + 1)[:, :, :K] = kinds
+    w = w[:, :K]
+    assert gdn.gdn_matmul_i8_workspace_size(a, w) > 0
+    sa, sw = scales(1, M), scales(2, 8)
+    out = gdn.gdn_matmul_i8(a, sa, w, sw.repeat(N // 8), dtype=F32)
+    want = ref.product(a, sa, kinds, sw, None, F32).cuda()
+    assert (out.view(M, -1, 8) == want[:, None]).all()
