@@ -9,9 +9,6 @@
 
 namespace gdn {
 
-// The sum of K products of codes stays within an int32 up to here: K * 128^2 < 2^31.
-constexpr int64_t kMatmulMaxK = 131071;
-
 struct I8Maps {
     CUtensorMap w, a;
 };

@@ -543,8 +543,8 @@ template <typename T, int MODE, bool OUT8>
 static gdn_status_t launch_rows_t(const RowParams &p, cudaStream_t st) {
     const int chunks = (p.D + 7) / 8;               // 8-element pieces of a row
     // two rows of every input have to fit, padded to whole warps (norms: 27136 elements of bf16)
-    const size_t inputs = MODE == kRowQuantize ? 1 : 2;
-    const bool vec = p.vec && 2 * inputs * ((size_t)p.D + 1024) * sizeof(T) <= (size_t)kRowSmem;
+    constexpr int fits = kRowSmem / (2 * (MODE == kRowQuantize ? 1 : 2) * (int)sizeof(T)) - 1024;
+    const bool vec = p.vec && p.D <= fits;
     if (chunks <= 32)
         return vec ? launch_rows_k<T, MODE, OUT8, 1, true, true>(p, 128, st)
                    : launch_rows_k<T, MODE, OUT8, 1, true, false>(p, 128, st);
@@ -562,8 +562,9 @@ static gdn_status_t launch_rows_t(const RowParams &p, cudaStream_t st) {
     if (nv == 2)
         return vec ? launch_rows_k<T, MODE, OUT8, 2, false, true>(p, threads, st)
                    : launch_rows_k<T, MODE, OUT8, 2, false, false>(p, threads, st);
-    return vec ? launch_rows_k<T, MODE, OUT8, 4, false, true>(p, threads, st)
-               : launch_rows_k<T, MODE, OUT8, 4, false, false>(p, threads, st);
+    if constexpr (fits > 2048 * 8)
+        if (vec) return launch_rows_k<T, MODE, OUT8, 4, false, true>(p, threads, st);
+    return launch_rows_k<T, MODE, OUT8, 4, false, false>(p, threads, st);
 }
 
 template <typename T>

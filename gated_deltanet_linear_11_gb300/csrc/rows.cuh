@@ -5,8 +5,6 @@
 
 namespace gdn {
 
-constexpr int kMaxRow = 32768;              // longest row of the row operators
-
 enum RowMode { kRowQuantize = 0, kRowAddNorm = 1, kRowGatedNorm = 2 };
 
 struct RowParams {
