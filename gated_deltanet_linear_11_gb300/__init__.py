@@ -58,9 +58,7 @@ __all__ = ["gdn_conv1d_fwd", "gdn_conv1d_update", "gdn_chunk_prefill",
            "gdn_layer_prefill", "gdn_layer_decode", "gdn_linear_prefill",
            "gdn_linear_prefill_workspace_size", "gdn_linear_decode", "gdn_kv_cache",
            "gdn_kv_append", "gdn_kv_read", "gdn_kv_attention",
-           "gdn_kv_attention_workspace_size", "gdn_quantize_rows", "gdn_add_rmsnorm",
-           "gdn_gated_rmsnorm", "gdn_matmul_i8", "gdn_matmul_i8_workspace_size", "GdnError",
-           "load"]
+           "gdn_kv_attention_workspace_size", "GdnError", "load"]
 
 _DT = {torch.bfloat16: _lib.GDN_BF16, torch.float32: _lib.GDN_F32}
 

@@ -185,13 +185,6 @@ def test_binding_refusals(lib, monkeypatch):
     assert e.value.code == 7
 
 
-def test_names_of_the_package():
-    """`from gated_deltanet_linear_11_gb300 import *` brings every entry."""
-    import gated_deltanet_linear_11_gb300 as gdn
-    assert set(eight_bit.__all__) <= set(gdn.__all__)
-    assert all(hasattr(gdn, name) for name in gdn.__all__)
-
-
 @no_gpu
 def test_smallest_eps(lib):
     """Beside an eps under 2^-126 the squares of small rows would lack digits: 3e-22 squared is 64
