@@ -200,9 +200,10 @@ template <int N> struct ExactSums {
 // by ranges of K.  Each sends its int32 sums to the CTA that adds them up, one of its share of
 // the channels (reading the others' memory between two barriers took 2 us longer at 64 tokens).
 // Tokens are converted into fp16 tiles in shared memory.
-// Measured, 16480 channels of 5120: 16 tokens 18.3 us, 64 tokens 23.8 us, where HBM takes 12.5:
+// Measured, 16480 channels of 5120: 16 tokens 18.3 us, 64 tokens 23.9 us, where HBM takes 12.5:
 // each step's chain (copy, codes out of shared memory, conversion, TMEM, products) is waited for
-// with two CTAs an SM; issue slots are 54% busy, the tensor pipe 16%.  More converting warps
+// with two CTAs an SM; issue slots are 54% busy, the tensor pipe 16%.  5120 channels of 6144 make
+// 160 CTAs, mostly one an SM, with 12 steps each: 16 tokens 11.7 us, 64 tokens 16.1 (HBM: 4.7).  More converting warps
 // shorten no chain and take the registers (16 of 56 registers took 3.6 us longer at 64 tokens).
 template <int NT>
 __global__ void __launch_bounds__(kI8Threads, I8Shape<NT>::CTAS)
@@ -466,9 +467,12 @@ matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__
 // int32 sums go to the workspace and are added up by a kernel after this one.  Warps 0-7 move
 // sums (a thread: one channel, half of the tokens), 8-11 convert, 12 copies, 13 issues products
 // (in the first CTA of a pair).
-// Measured, 16480 channels of 5120: 4096 tokens 344 us (2000 TFLOP/s, above a library bf16
-// product's rate), 1024 tokens 97 us (1770; the tensor pipe is 78% busy), 256 tokens 33 us, of
-// which some 11 are the tokens' kernel, the first copies and the sums' way out.
+// Measured, 16480 channels of 5120: 4096 tokens 344 us (2000 TFLOP/s) for a few calls and 371 to
+// 379 in a long run of them, where power limits the clock (1850; a library bf16 product's rate is
+// 1905), 1024 tokens 97 us (1770; the tensor pipe is 78% busy), 256 tokens 33 us, of which some 11
+// are the tokens' kernel, the first copies and the sums' way out.  Where the tiles are fewer than
+// the pairs and no cut pays, pairs stay idle: 500 tokens of 5120 channels of 6144, 37 us, are 40
+// tiles for 76 pairs.
 constexpr int kPairSumWarps = 8, kPairConvWarps = 4, kPairMaxStages = 4;
 constexpr int kPairThreads = 32 * (kPairSumWarps + kPairConvWarps + 4);  // two warps idle
 constexpr int kPairTokens = 256;                 // most tokens of a tile
@@ -998,9 +1002,9 @@ PairPlan pair_plan(int64_t M, int64_t N, int64_t K, int pairs) {
     return plan;
 }
 
-// Ranges of K of a tile of the cluster kernel: as many as keep every SM busy, of at least two
-// steps each; clusters of a power of two fit the device best (40 tiles: 13.7 us in fours, 17.1
-// in sevens).
+// Ranges of K of a tile of the cluster kernel: a power of two, up to eight, while all CTAs fit at
+// once and the ranges have two steps each (one of them may have a single one); clusters of such
+// sizes fit the device best (40 tiles: 13.7 us in fours, 17.1 in sevens).
 int64_t few_parts(int64_t tiles, int64_t steps, int64_t ctas) {
     int64_t parts = 1;
     while (parts < 8 && 2 * parts * tiles <= ctas && 4 * parts <= steps + 1) parts *= 2;

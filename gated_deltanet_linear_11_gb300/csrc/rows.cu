@@ -13,11 +13,13 @@
 // one pass through shared memory.  The split of a row depends on its length alone, so a row's
 // results are the same in any batch.
 //
-// Measured, 4096 bf16 rows: norm with residual of 5120 29.2 us (5.7 TB/s, 85% of a copy's rate),
-// to 8 bits 24.9 (87%); gated norm of 48 x 128 25.5 (87%), to 8 bits 29.1 (64%: the row's maximum
-// is one more barrier between its loads and its stores); 10240 rows of 5120 to 8 bits 29 (80%),
-// from fp32 43.4 (89%).  64 rows and fewer take 1.5 to 3 us, a launch and the row's way through
-// the SM.
+// Measured, 4096 bf16 rows: norm with residual of 5120 29.8 us (5.6 TB/s, 83% of a copy's rate),
+// to 8 bits 24.9 (87%); gated norm of 48 x 128 25.5 (87%), to 8 bits 29.1 (64%: gates and codes
+// together are 22% more instructions than the gates alone, which fill 73% of the issue slots);
+// 10240 rows of 5120 to 8 bits 29 to 30 (78%), from fp32 43 (90%).  fp32: 4096 norms of 5120 57.5
+// (86%), to 8 bits 44 (91%); 4096 gated norms of 48 x 128 52 (85%), to 8 bits 44 (76%).  64 rows and
+// fewer take 1.5 to 3 us, a launch and the row's way through the SM.  Rows too long for the ring
+// (1000 fp32 norms of 16384: 77 us, 50%) and rows off 16 bytes go element by element.
 #include <atomic>
 
 #include "bulk_ptx.cuh"
@@ -178,7 +180,10 @@ __device__ __forceinline__ void largest8(uint32_t &m, const float (&f)[8]) {
 constexpr float kToInteger = 12582912.f;
 
 // v silu(z).  For bf16, 1 / (1 + e^-z) from the hardware's base-2 exponential and reciprocal
-// (about 2^-22 each, far under the half step of 2^-9); e^-z past fp32 gives a zero.
+// (about 2^-22 each, and the exponent's rounding): far under bf16's half step of 2^-9, and for codes
+// up to 127 under 2^-13 of a step, where 2^-10 is allowed.  200 x 64 tokens of 48 x 128 had 43 codes
+// of 79 million beside the nearest, all within 2^-15 of a border; with an exact exponential and
+// division 41.  e^-z past 2^126 gives a zero.
 template <typename T>
 __device__ __forceinline__ void gate8(float (&v)[8], const float (&z)[8]) {
 #pragma unroll

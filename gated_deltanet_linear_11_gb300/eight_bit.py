@@ -157,7 +157,8 @@ def gdn_gated_rmsnorm(x, z, weight, eps=1e-6, eight_bit=False, y=None, scale=Non
 
 @_on_device
 def gdn_matmul_i8_workspace_size(a, w, simt=False):
-    """Workspace bytes of gdn_matmul_i8 (by the sizes and the alignment of a and w)."""
+    """Workspace bytes of gdn_matmul_i8 (by the sizes and the alignment of a and w and by their
+    device)."""
     return int(_lib.load().gdn_matmul_i8_workspace_size(
         _matrix("a", a, _I8), _matrix("w", w, _I8), GDN_PREFILL_SIMT if simt else 0))
 

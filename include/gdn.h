@@ -568,8 +568,10 @@ gdn_status_t gdn_gated_rmsnorm(const gdn_tensor_t *x, const gdn_tensor_t *z,
  * and so is each of the two products and the addition after it, in this order.  Every output
  * is the same bits whatever the other rows and channels, the layout and the kernel are.
  * Rows of a or w that do not start on 16 bytes are first copied to the workspace.
- * workspace: device scratch of gdn_matmul_i8_workspace_size() bytes (which looks at the sizes
- * and the alignment of a and w), 256-byte aligned (may be NULL when 0).
+ * workspace: device scratch of gdn_matmul_i8_workspace_size() bytes, 256-byte aligned (may be
+ * NULL when 0).  The size goes by the sizes and the alignment of a and w and by the SMs of the
+ * current device: ask with the device current that the product runs on.  It does not grow with
+ * every size (a product of more tokens may take a kernel that needs less).
  * flags: GDN_PREFILL_SIMT forces the CUDA-core kernel.
  */
 #define GDN_MATMUL_MAX_K 131071
