@@ -405,8 +405,10 @@ rows_kernel(const __grid_constant__ RowParams p) {
                 r = shrink;
             }
             // Products past fp32 or among its smallest numbers, though h r w may be neither: h r, at
-            // most sqrt(D), comes first then, as it does in rows of floating-point type.
-            if (!OUT8 || m >= kInfBits || m < kSmallBits) {
+            // most sqrt(D), comes first then, as it does in rows of floating-point type.  (Not where
+            // all are zero, as in rows of padding, and r is up to 2^22: with products of at most
+            // 2^-150 the row's codes are zeros.)
+            if (!OUT8 || (m - kSmallBits >= kInfBits - kSmallBits && (m != 0 || r > 4194304.f))) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) mul8(v[i], r);
                 if constexpr (OUT8) {

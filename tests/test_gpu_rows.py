@@ -253,7 +253,7 @@ def test_weights_and_rows_far_from_one(D, dtype):
     about 4, so results stay under 1e38."""
     sizes = [(30.0, 1e37, 1e-6), (100.0, 1e37, 1e-6), (1e3, 1e36, 1e-6), (3e37, 1e34, 1e-6),
              (3e37, 1e-38, 1e-6), (1e-10, 1e-35, 1e-6), (1e-18, 1e-24, 2.0 ** -126),
-             (1e-20, 1e-20, 2.0 ** -126)]
+             (1e-20, 1e-20, 2.0 ** -126), (1e-20, 1e-28, 2.0 ** -126)]
     for size, weight, eps in sizes:
         x = (rnd(D, 4, D, dtype=F32) * size).to(dtype)
         x[2] = 0
