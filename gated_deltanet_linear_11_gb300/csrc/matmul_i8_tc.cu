@@ -203,8 +203,9 @@ template <int N> struct ExactSums {
 // Measured, 16480 channels of 5120: 16 tokens 18.3 us, 64 tokens 23.9 us, where HBM takes 12.5:
 // each step's chain (copy, codes out of shared memory, conversion, TMEM, products) is waited for
 // with two CTAs an SM; issue slots are 54% busy, the tensor pipe 16%.  5120 channels of 6144 make
-// 160 CTAs, mostly one an SM, with 12 steps each: 16 tokens 11.7 us, 64 tokens 16.1 (HBM: 4.7).  More converting warps
-// shorten no chain and take the registers (16 of 56 registers took 3.6 us longer at 64 tokens).
+// 160 CTAs, mostly one an SM, with 12 steps each: 16 tokens 11.7 us, 64 tokens 16.1 (HBM: 4.7).
+// More converting warps shorten no chain and take the registers (16 of 56 registers took 3.6 us
+// longer at 64 tokens, 16480 channels).
 template <int NT>
 __global__ void __launch_bounds__(kI8Threads, I8Shape<NT>::CTAS)
 matmul_i8_tc_kernel(const __grid_constant__ I8Maps maps, const __grid_constant__ MatmulParams p, int tiles_m) {
